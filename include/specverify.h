@@ -16,6 +16,12 @@
  * by rotation), spec_future_gather (ConFu's future token),
  * spec_la_prefill_attn (prefill-form LA).
  *
+ * For serving: a KV cache in 8 bits with a scale per (page, KV head) --
+ * spec_verify_attn_kv8 attends over it, kv8_commit and kv8_append write it,
+ * spec_page_plan builds block tables and slot maps from request lengths --
+ * and spec_logits_adjust (penalties, biases and grammar masks ahead of the
+ * acceptance).  The pages have no counterpart of these.
+ *
  * Sources, cited by page title and section / equation:
  *   [LA]  "Lookahead Attention: Self-Speculative Verification via Parallel
  *         Token Proposals": sec. 2.1-2.4, sec. 3.1 (mask M_LA), sec. 3.2
@@ -94,7 +100,7 @@ typedef int spec_status_t;
 
 /* device status bits (spec_get_status) */
 #define SPEC_DEV_BAD_TREE     0x01  /* vparent not an earlier valid row */
-#define SPEC_DEV_BAD_PAGE     0x02  /* page id outside [0, n_pages) */
+#define SPEC_DEV_BAD_PAGE     0x02  /* page id (or slot) outside the cache */
 #define SPEC_DEV_SEQ_OVERFLOW 0x04  /* seq_len outside [0, cache capacity] */
 #define SPEC_DEV_CAPACITY     0x08  /* commit: cache or free list full */
 #define SPEC_DEV_BAD_INDEX    0x10  /* path / row_of / acc_len out of range */
@@ -135,6 +141,40 @@ typedef struct spec_kv_desc {
     int max_pages_per_seq;   /* paged: row length of page_table */
     int32_t *page_table;     /* paged */
 } spec_kv_desc;
+
+/*
+ * A KV cache in 8 bits, paged: e4m3 codes and one fp32 scale for the keys
+ * and one for the values of every (page, KV head); an element stands for
+ * code * scale.
+ *
+ *   kv     : uint8 [n_pages][n_kv_heads][page_size / 8][2][8][head_dim]:
+ *            token t of a page has its key at [t / 8][0][t % 8][:] and its
+ *            value at [t / 8][1][t % 8][:].  One (page, head) is one
+ *            contiguous tile, fetched by one tensor copy, in which both the
+ *            key groups and the value groups lie at a fixed stride.
+ *            16-byte aligned.
+ *   scales : fp32 [n_pages][n_kv_heads][2] (keys, values).
+ *   page_table as in spec_kv_desc.  page_size: a multiple of 16, <= 256.
+ *
+ * The writers (kv8_commit, kv8_append) give a block the scale 2^e with the
+ * smallest e, -60 <= e <= 60, for which every value is at most 448 * 2^e: a
+ * power of two costs e4m3 (a floating-point format) no precision, and makes
+ * the step to a larger scale exact but for e4m3's subnormals.  Larger values
+ * saturate.  A non-finite value makes the block's scale NaN, so the block
+ * reads as NaN until its page is begun again.  Readers take any finite scale;
+ * one below 2^-60 counts as 2^-60, one above 2^60 as 2^60.
+ */
+typedef struct spec_kv8_desc {
+    int n_kv_heads;
+    int head_dim;            /* 64 or 128 */
+    void *kv;
+    float *scales;
+    int batch;
+    int n_pages;
+    int page_size;
+    int max_pages_per_seq;
+    int32_t *page_table;     /* int32 [batch][max_pages_per_seq] */
+} spec_kv8_desc;
 
 /* Shape of one verify-attention call. */
 typedef struct spec_attn_desc {
@@ -218,6 +258,18 @@ typedef struct spec_rotate_desc {
     int gamma;          /* streams per node (<= 64) */
     float eps;          /* rotation angle per stream index, radians */
 } spec_rotate_desc;
+
+/* Shape of one logits adjustment call. */
+typedef struct spec_logits_desc {
+    int batch;          /* B */
+    int n_judge_rows;   /* Rj: logits rows per request */
+    int vocab;          /* V */
+    int logit_dtype;    /* SPEC_BF16 or SPEC_F32 */
+    int max_nodes;      /* N (<= 256): row length of tokens / tree_parent; 0 = no tree */
+    int hist_cap;       /* row length of history; 0 = none */
+    int n_bias;         /* row length of bias_ids / bias (<= 1024); 0 = none */
+    int n_masks;        /* grammar masks; 0 = none */
+} spec_logits_desc;
 
 /* Library version (SPECVERIFY_VERSION). */
 int spec_version(void);
@@ -576,6 +628,157 @@ spec_status_t kv_commit(const spec_kv_desc *cache, int batch, int n_rows,
                         const int32_t *path, const int32_t *acc_len,
                         int32_t *seq_len, const int32_t *free_pages,
                         int n_free, int32_t *free_head, void *stream);
+
+/* Bytes of workspace spec_verify_attn_kv8 needs for this shape and cache. */
+spec_status_t spec_verify_attn_kv8_workspace_size(const spec_attn_desc *attn,
+                                                  const spec_kv8_desc *cache,
+                                                  size_t *bytes);
+
+/*
+ * spec_verify_attn_kv8 -- spec_verify_attn over a committed prefix held in
+ * 8 bits.  The arguments are those of spec_verify_attn with a spec_kv8_desc
+ * cache: q, kb, vb, soft_k, soft_v and o keep attn->dtype (the block and the
+ * soft prompt are attended as they are, not as the cache would round them),
+ * and one row per request (n_rows = 1 with its own vis bit) is the
+ * single-token decoding form.
+ *
+ * Scores, softmax statistics and sums are held in fp32.  A row that sees a
+ * block whose scale is NaN gets o = lse = NaN.  Codes in slots past seq_len
+ * are never used.  A seq_len outside [0, capacity] is clamped and sets
+ * SPEC_DEV_SEQ_OVERFLOW; a page id outside [0, n_pages) is not read and sets
+ * SPEC_DEV_BAD_PAGE (the affected outputs are then unspecified).  q, kb, vb,
+ * soft_k, soft_v and o must be 16-byte aligned.
+ */
+spec_status_t spec_verify_attn_kv8(const spec_attn_desc *attn, const void *q,
+                                   const spec_kv8_desc *cache, const void *kb,
+                                   const void *vb, const void *soft_k,
+                                   const void *soft_v, const int32_t *seq_len,
+                                   const uint32_t *vis, const uint8_t *row_flags,
+                                   void *o, float *lse, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/*
+ * kv8_commit -- kv_commit into a cache held in 8 bits: arguments, page
+ * allocation, and what is skipped and reported are kv_commit's; `dtype` is
+ * the type of kb and vb (16-byte aligned).
+ *
+ * A block whose first new row is the page's first row takes its scale from
+ * the new rows alone.  In a partly used page the scale is the larger of its
+ * present one and that of the new rows; where it grows, the rows before the
+ * new ones are rounded to it again (nearest even).  Rows of the page behind
+ * the last new one are not touched.  An out-of-range path entry leaves its
+ * slot as it was (SPEC_DEV_BAD_INDEX).  Two launches.
+ */
+spec_status_t kv8_commit(const spec_kv8_desc *cache, int dtype, int batch, int n_rows,
+                         const void *kb, const void *vb, int path_cap,
+                         const int32_t *path, const int32_t *acc_len,
+                         int32_t *seq_len, const int32_t *free_pages,
+                         int n_free, int32_t *free_head, void *stream);
+
+/*
+ * kv8_append -- writes a packed batch of new tokens (a prompt or a chunk of
+ * one, of any number of requests) into the slots that spec_page_plan gave
+ * them.
+ *
+ *   k, v      (dtype) token i's row of KV head h begins at element
+ *             i * row_stride + h * head_dim; row_stride >= n_kv_heads *
+ *             head_dim (each of k and v may lie inside wider rows, such as a
+ *             joint projection's output); rows on 16-byte boundaries.
+ *   slot_map  int64 [n_tokens]: page * page_size + offset, or < 0 for a
+ *             token that is not written.  Tokens of one page follow one
+ *             another with rising slots, as spec_page_plan numbers them.
+ *
+ * Blocks take or raise their scales as in kv8_commit (a run of tokens that
+ * begins at offset 0 begins the page).  A page named by two separate runs of
+ * one call is unspecified.  A slot past the cache is skipped and sets
+ * SPEC_DEV_BAD_PAGE.  page_table, batch and max_pages_per_seq of the
+ * descriptor are not used.  One launch.
+ */
+spec_status_t kv8_append(const spec_kv8_desc *cache, int dtype, int n_tokens,
+                         const void *k, long long row_stride_k, const void *v,
+                         long long row_stride_v, const int64_t *slot_map,
+                         void *stream);
+
+/*
+ * spec_page_plan -- block tables and slot maps from request lengths: room
+ * for n_new[b] more tokens of every request, before they are computed.
+ *
+ *   seq_len    int32 [batch]: tokens each request holds.
+ *   n_new      int32 [batch]: tokens it is about to get (0 = none).
+ *   page_table int32 [batch][max_pages_per_seq], in/out: new entries.
+ *   free_pages int32 [n_free], free_head int32 [1] in/out, as in kv_commit.
+ *   cu_new     int32 [batch + 1] out: first packed token of each request
+ *              (the exclusive sums of n_new).
+ *   slot_map   int64 [n_slots] out: packed token cu_new[b] + i is token
+ *              seq_len[b] + i of request b and gets page * page_size +
+ *              offset; -1 behind the last token.
+ *   new_len    int32 [batch] out, or NULL: seq_len + n_new.
+ *
+ * Pages are taken as kv_commit takes them.  A request that would exceed its
+ * table is skipped (its slots are -1, new_len = seq_len; SPEC_DEV_CAPACITY),
+ * as is one whose seq_len is out of range (SPEC_DEV_SEQ_OVERFLOW) or whose
+ * n_new is negative (counted as 0; SPEC_DEV_BAD_INDEX).  If the free list
+ * cannot serve all requests no page is taken, every slot is -1 and
+ * SPEC_DEV_CAPACITY is set.  A page id outside [0, n_pages) gives slot -1 and
+ * SPEC_DEV_BAD_PAGE; more packed tokens than n_slots set SPEC_DEV_BAD_INDEX
+ * (pages are taken, the first n_slots slots written).  The new tokens of all
+ * requests number at most 2^31 - 1024 (else SPEC_DEV_BAD_INDEX and nothing is
+ * planned); seq_len itself is not changed.  One launch.
+ */
+spec_status_t spec_page_plan(int batch, int page_size, int n_pages,
+                             int max_pages_per_seq, const int32_t *seq_len,
+                             const int32_t *n_new, int32_t *page_table,
+                             const int32_t *free_pages, int n_free,
+                             int32_t *free_head, int32_t *cu_new,
+                             long long n_slots, int64_t *slot_map,
+                             int32_t *new_len, void *stream);
+
+/*
+ * spec_logits_adjust -- penalties for repeated tokens, biases and grammar
+ * masks on the judged rows, ahead of spec_vocab_reduce / spec_accept /
+ * spec_accept_soft.
+ *
+ *   logits, out  [batch][n_judge_rows][vocab] (logit_dtype); out may be
+ *                logits itself, and must not overlap it otherwise.
+ *   history      int32 [batch][hist_cap]: committed tokens, hist_len int32
+ *                [batch] of them, the first n_prompt[b] (n_prompt NULL: 0)
+ *                the prompt.  Negative entries are padding.
+ *   tokens, tree_parent  int32 [batch][max_nodes]: the draft, as in
+ *                spec_accept (a lookahead chain has tree_parent[i] = i - 1).
+ *   row_node     int32 [batch][n_judge_rows], or NULL (row j: node j): the
+ *                node that the row follows; -1: the row follows the history
+ *                alone.
+ *   repetition, presence, frequency  fp32 [batch], each NULL for none
+ *                (repetition > 0).
+ *   bias_ids, bias  int32 / fp32 [batch][n_bias]: added to those tokens;
+ *                negative ids are unused entries, equal ids add up.
+ *   mask_bits    uint32 [n_masks][ceil(vocab / 32)]: bit v % 32 of word v /
+ *                32 allows token v.  row_mask int32 [batch][n_judge_rows]:
+ *                the row's mask, negative for none.
+ *
+ * With n the number of times token v occurs in the history behind the prompt
+ * and on the row's path (its node and the node's ancestors), in fp32:
+ *   z = logits[v]
+ *   if v is in the history (prompt too) or on the path:
+ *       z = z > 0 ? z / repetition : z * repetition
+ *   z = z - frequency * n - (n > 0 ? presence : 0) + bias[v]
+ *   out[v] = allowed ? z, rounded to nearest : -inf
+ * A row whose mask allows nothing is -inf throughout.  A history, draft or
+ * bias token >= vocab, a row_node or row_mask out of range, or a hist_len
+ * outside [0, hist_cap] (clamped) is left out and sets SPEC_DEV_BAD_INDEX; a
+ * parent that does not precede its node ends the path there and sets
+ * SPEC_DEV_BAD_TREE (both for draft nodes only where a row's path meets
+ * them).  One launch.
+ */
+spec_status_t spec_logits_adjust(const spec_logits_desc *desc, const void *logits,
+                                 void *out, const int32_t *history,
+                                 const int32_t *hist_len, const int32_t *n_prompt,
+                                 const int32_t *tokens, const int32_t *tree_parent,
+                                 const int32_t *row_node, const float *repetition,
+                                 const float *presence, const float *frequency,
+                                 const int32_t *bias_ids, const float *bias,
+                                 const uint32_t *mask_bits, const int32_t *row_mask,
+                                 void *stream);
 
 /*
  * spec_set_wait_limit -- limit, in SM clock cycles, of the internal pipeline

@@ -21,3 +21,4 @@ from .specverify_oracle import (  # noqa: F401
     rotate_stream_values, future_gather,
     kv_commit_contiguous, kv_commit_paged,
 )
+from . import kv8_oracle as kv8  # noqa: F401,E402

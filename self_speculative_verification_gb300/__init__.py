@@ -11,7 +11,8 @@ __version__ = "0.1.0"
 
 _API = ("spec_mask_build", "spec_verify_attn", "spec_verify_attn_workspace_size",
         "spec_vocab_reduce", "spec_accept", "kv_commit", "spec_get_status",
-        "spec_version")
+        "spec_version", "spec_verify_attn_kv8", "spec_verify_attn_kv8_workspace_size",
+        "kv8_desc", "kv8_commit", "kv8_append", "spec_page_plan", "spec_logits_adjust")
 
 
 def __getattr__(name):

@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int, c_size_t, c_void_p
+from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_void_p
 
 import torch
 
@@ -45,7 +45,8 @@ EXPORTS = ("spec_version", "spec_status_string", "spec_mask_build",
            "spec_verify_attn_noalloc", "spec_vocab_reduce", "spec_accept", "kv_commit",
            "spec_get_status", "spec_la_prefill_attn", "spec_accept_soft", "spec_draft_tree",
            "spec_prune_tree", "spec_stream_rotate_values", "spec_future_gather",
-           "spec_set_wait_limit")
+           "spec_set_wait_limit", "spec_verify_attn_kv8_workspace_size", "spec_verify_attn_kv8",
+           "kv8_commit", "kv8_append", "spec_page_plan", "spec_logits_adjust")
 SPEC_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -104,6 +105,18 @@ class PrefillDesc(ctypes.Structure):
                 ("dtype", c_int), ("scale", c_float)]
 
 
+class Kv8Desc(ctypes.Structure):
+    _fields_ = [("n_kv_heads", c_int), ("head_dim", c_int), ("kv", c_void_p),
+                ("scales", c_void_p), ("batch", c_int), ("n_pages", c_int),
+                ("page_size", c_int), ("max_pages_per_seq", c_int), ("page_table", c_void_p)]
+
+
+class LogitsDesc(ctypes.Structure):
+    _fields_ = [("batch", c_int), ("n_judge_rows", c_int), ("vocab", c_int),
+                ("logit_dtype", c_int), ("max_nodes", c_int), ("hist_cap", c_int),
+                ("n_bias", c_int), ("n_masks", c_int)]
+
+
 _lib = None
 
 
@@ -145,6 +158,17 @@ def load_library():
         "spec_prune_tree": ([POINTER(PruneDesc)] + [vp] * 10, c_int),
         "spec_stream_rotate_values": ([POINTER(RotateDesc), vp, vp, vp], c_int),
         "spec_future_gather": ([c_int, c_int, c_int, c_int, vp, vp, c_int, vp, vp], c_int),
+        "spec_verify_attn_kv8_workspace_size": ([POINTER(AttnDesc), POINTER(Kv8Desc),
+                                                 POINTER(c_size_t)], c_int),
+        "spec_verify_attn_kv8": ([POINTER(AttnDesc), vp, POINTER(Kv8Desc)] + [vp] * 10 +
+                                 [c_size_t, vp], c_int),
+        "kv8_commit": ([POINTER(Kv8Desc), c_int, c_int, c_int, vp, vp, c_int, vp, vp, vp, vp, c_int,
+                        vp, vp], c_int),
+        "kv8_append": ([POINTER(Kv8Desc), c_int, c_int, vp, c_longlong, vp, c_longlong, vp, vp],
+                       c_int),
+        "spec_page_plan": ([c_int, c_int, c_int, c_int, vp, vp, vp, vp, c_int, vp, vp, c_longlong,
+                            vp, vp, vp], c_int),
+        "spec_logits_adjust": ([POINTER(LogitsDesc)] + [vp] * 16, c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -418,3 +442,195 @@ def spec_future_gather(o, last_node, row_offset, out, stream=None):
     _check("spec_future_gather", lib.spec_future_gather(
         B, R, row, spec_dtype(o), _ptr(o, name="o"), _ptr(last_node, torch.int32, "last_node"),
         row_offset, _ptr(out), _stream(stream)))
+
+
+# ------------------------------------------------ 8-bit cache, plans, logits
+
+def _on(t, dtype, shape, name, dev, optional=False):
+    """Device pointer of a contiguous tensor of this type and shape (None: any)
+    on device `dev`, the current one, where the library launches."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _cur(stream):
+    """Handle of a torch stream (None: the current one), which must belong to
+    the current device, and that device's index."""
+    dev = torch.cuda.current_device()
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{dev}")
+    return stream.cuda_stream, dev
+
+
+def kv8_desc(kv: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor = None) -> Kv8Desc:
+    """kv: float8_e4m3fn (or uint8) [n_pages][Hkv][page_size / 8][2][8][d];
+    scales fp32 [n_pages][Hkv][2]; page_table int32 [B][max_pages] (None for
+    kv8_append alone)."""
+    if kv.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"kv must be float8_e4m3fn or uint8, got {kv.dtype}")
+    if kv.dim() != 6 or kv.shape[3] != 2 or kv.shape[4] != 8:
+        raise ValueError("kv must be [n_pages][Hkv][page_size / 8][2][8][d]")
+    P, Hkv, groups, _, _, d = kv.shape
+    dev = kv.get_device()
+    _on(kv, None, None, "kv", dev)
+    _on(scales, torch.float32, (P, Hkv, 2), "scales", dev)
+    B = maxp = 0
+    pt = _on(page_table, torch.int32, None, "page_table", dev, optional=True)
+    if page_table is not None:
+        B, maxp = page_table.shape
+    desc = Kv8Desc(Hkv, d, kv.data_ptr(), scales.data_ptr(), B, P, groups * 8, maxp, pt)
+    desc.device = dev
+    return desc
+
+
+def _cache_on(cache, dev):
+    if getattr(cache, "device", dev) != dev:
+        raise ValueError(f"the cache is on cuda:{cache.device}, the current device is cuda:{dev}")
+
+
+def spec_verify_attn_kv8_workspace_size(attn: AttnDesc, cache: Kv8Desc) -> int:
+    n = c_size_t(0)
+    _check("spec_verify_attn_kv8_workspace_size",
+           load_library().spec_verify_attn_kv8_workspace_size(
+               ctypes.byref(attn), ctypes.byref(cache), ctypes.byref(n)))
+    return n.value
+
+
+def spec_verify_attn_kv8(attn: AttnDesc, q, cache: Kv8Desc, kb, vb, soft_k, soft_v, seq_len, vis,
+                         row_flags, o, lse, workspace, stream=None):
+    """spec_verify_attn over a prefix held in 8 bits."""
+    st, dev = _cur(stream)
+    B, R, Hq, Hkv, d, ns = (attn.batch, attn.n_rows, attn.n_q_heads, attn.n_kv_heads, attn.head_dim,
+                            attn.n_soft)
+    dt = torch.bfloat16 if attn.dtype == SPEC_BF16 else torch.float32
+    _cache_on(cache, dev)
+    soft = (Hkv, ns, d)
+    if ns == 0:
+        soft_k = soft_v = None
+    _check("spec_verify_attn_kv8", load_library().spec_verify_attn_kv8(
+        ctypes.byref(attn), _on(q, dt, (B, R, Hq, d), "q", dev), ctypes.byref(cache),
+        _on(kb, dt, (B, Hkv, R, d), "kb", dev), _on(vb, dt, (B, Hkv, R, d), "vb", dev),
+        _on(soft_k, dt, soft, "soft_k", dev, ns == 0), _on(soft_v, dt, soft, "soft_v", dev, ns == 0),
+        _on(seq_len, torch.int32, (B,), "seq_len", dev),
+        _on(vis, torch.int32, (B, R, (R + 31) // 32), "vis", dev),
+        _on(row_flags, torch.uint8, (B, R), "row_flags", dev),
+        _on(o, dt, (B, R, Hq, d), "o", dev), _on(lse, torch.float32, (B, Hq, R), "lse", dev),
+        _on(workspace, None, None, "workspace", dev), workspace.numel() * workspace.element_size(),
+        st))
+
+
+def kv8_commit(cache: Kv8Desc, kb, vb, path, acc_len, seq_len, free_pages, free_head, stream=None):
+    """kv_commit into a cache held in 8 bits."""
+    st, dev = _cur(stream)
+    _cache_on(cache, dev)
+    B, Hkv, R, d = kb.shape
+    if (Hkv, d) != (cache.n_kv_heads, cache.head_dim):
+        raise ValueError(f"kb must be [B][{cache.n_kv_heads}][R][{cache.head_dim}]")
+    i32 = torch.int32
+    cap = path.shape[1]
+    _check("kv8_commit", load_library().kv8_commit(
+        ctypes.byref(cache), spec_dtype(kb), B, R, _on(kb, None, None, "kb", dev),
+        _on(vb, kb.dtype, kb.shape, "vb", dev), cap, _on(path, i32, (B, cap), "path", dev),
+        _on(acc_len, i32, (B,), "acc_len", dev), _on(seq_len, i32, (B,), "seq_len", dev),
+        _on(free_pages, i32, None, "free_pages", dev), free_pages.numel(),
+        _on(free_head, i32, (1,), "free_head", dev), st))
+
+
+def _packed_rows(t, cache, n, name, dev):
+    """Pointer and row stride of [n][Hkv][d] rows that may lie in wider rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    Hkv, d = cache.n_kv_heads, cache.head_dim
+    if t.shape != (n, Hkv, d):
+        raise ValueError(f"{name} must be {[n, Hkv, d]}, got {list(t.shape)}")
+    if n and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.data_ptr(), t.stride(0) if n > 1 else Hkv * d
+
+
+def kv8_append(cache: Kv8Desc, k, v, slot_map, stream=None):
+    """Packed new tokens k, v [n][Hkv][d] (rows may be part of wider ones) into
+    the slots of slot_map int64 [n]."""
+    st, dev = _cur(stream)
+    _cache_on(cache, dev)
+    n = slot_map.numel()
+    pk, sk = _packed_rows(k, cache, n, "k", dev)
+    pv, sv = _packed_rows(v, cache, n, "v", dev)
+    if v.dtype != k.dtype:
+        raise TypeError(f"v must be {k.dtype}, got {v.dtype}")
+    _check("kv8_append", load_library().kv8_append(
+        ctypes.byref(cache), spec_dtype(k), n, pk, sk, pv, sv,
+        _on(slot_map, torch.int64, (n,), "slot_map", dev), st))
+
+
+def spec_page_plan(page_size, n_pages, seq_len, n_new, page_table, free_pages, free_head, cu_new,
+                   slot_map, new_len=None, stream=None):
+    """Block tables and slot maps for n_new[b] more tokens of each request."""
+    st, dev = _cur(stream)
+    B, maxp = page_table.shape
+    i32 = torch.int32
+    _check("spec_page_plan", load_library().spec_page_plan(
+        B, page_size, n_pages, maxp, _on(seq_len, i32, (B,), "seq_len", dev),
+        _on(n_new, i32, (B,), "n_new", dev), _on(page_table, i32, None, "page_table", dev),
+        _on(free_pages, i32, None, "free_pages", dev), free_pages.numel(),
+        _on(free_head, i32, (1,), "free_head", dev), _on(cu_new, i32, (B + 1,), "cu_new", dev),
+        slot_map.numel(), _on(slot_map, torch.int64, None, "slot_map", dev),
+        _on(new_len, i32, (B,), "new_len", dev, True), st))
+
+
+def logits_desc(batch, n_judge_rows, vocab, logit_dtype, max_nodes=0, hist_cap=0, n_bias=0,
+                n_masks=0) -> LogitsDesc:
+    return LogitsDesc(batch, n_judge_rows, vocab, logit_dtype, max_nodes, hist_cap, n_bias, n_masks)
+
+
+def spec_logits_adjust(desc: LogitsDesc, logits, out, history=None, hist_len=None, n_prompt=None,
+                       tokens=None, tree_parent=None, row_node=None, repetition=None,
+                       presence=None, frequency=None, bias_ids=None, bias=None, mask_bits=None,
+                       row_mask=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks on judged rows;
+    what the descriptor gives no room (0) is not passed."""
+    st, dev = _cur(stream)
+    B, Rj, V, N, H, nb, nm = (desc.batch, desc.n_judge_rows, desc.vocab, desc.max_nodes,
+                              desc.hist_cap, desc.n_bias, desc.n_masks)
+    dt = torch.bfloat16 if desc.logit_dtype == SPEC_BF16 else torch.float32
+    i32, f32 = torch.int32, torch.float32
+    if H == 0:
+        history = hist_len = n_prompt = None
+    if N == 0:
+        tokens = tree_parent = row_node = None
+    if nb == 0:
+        bias_ids = bias = None
+    if nm == 0:
+        mask_bits = row_mask = None
+    _check("spec_logits_adjust", load_library().spec_logits_adjust(
+        ctypes.byref(desc), _on(logits, dt, (B, Rj, V), "logits", dev),
+        _on(out, dt, (B, Rj, V), "out", dev), _on(history, i32, (B, H), "history", dev, H == 0),
+        _on(hist_len, i32, (B,), "hist_len", dev, H == 0),
+        _on(n_prompt, i32, (B,), "n_prompt", dev, True),
+        _on(tokens, i32, (B, N), "tokens", dev, N == 0),
+        _on(tree_parent, i32, (B, N), "tree_parent", dev, N == 0),
+        _on(row_node, i32, (B, Rj), "row_node", dev, True),
+        _on(repetition, f32, (B,), "repetition", dev, True),
+        _on(presence, f32, (B,), "presence", dev, True),
+        _on(frequency, f32, (B,), "frequency", dev, True),
+        _on(bias_ids, i32, (B, nb), "bias_ids", dev, nb == 0),
+        _on(bias, f32, (B, nb), "bias", dev, nb == 0),
+        _on(mask_bits, i32, (nm, (V + 31) // 32), "mask_bits", dev, nm == 0),
+        _on(row_mask, i32, (B, Rj), "row_mask", dev, nm == 0), st))

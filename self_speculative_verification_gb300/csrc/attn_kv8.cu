@@ -1,0 +1,383 @@
+// spec_verify_attn_kv8: masked attention of the speculative rows over
+// (committed prefix in 8 bits || soft prompt || block).
+//
+// O = softmax(q K^T * scale + mask) V and LSE = ln sum exp(q k * scale) with
+// K and V of the prefix read as code * scale(page, head).
+//
+// This file holds the host planning, the CUDA-core kernel (fp32 inputs, whose
+// products the tensor cores' 8- and 16-bit operands cannot hold) and its
+// combine kernel.
+#include <math.h>
+
+#include "attn_kv8.cuh"
+#include "kv8_common.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kRows = 16;    // packed rows per CTA (4 warps x 4 rows)
+constexpr int kCols = 32;    // columns per tile (one per lane)
+
+enum { kColPrefix = 0, kColSoft = 1, kColBlock = 2 };
+
+// CTA (split, KV head x row block, request): a running softmax over its
+// columns, 32 at a time through shared memory; lane = column for the scores
+// (four rows per warp share each key vector), lane = head dimension for O.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
+    pdl_wait();
+    const AttnParams &P = Q.a;
+    constexpr int KP = D + 4;        // key row pitch: a quarter-warp's 16-byte reads spread over the banks
+    __shared__ __align__(16) float sq[kRows][D];
+    __shared__ __align__(16) float sk[kCols][KP];
+    __shared__ __align__(16) float sv_[kCols][D];
+    __shared__ uint32_t svis[kRows][SPEC_MAX_ROWS / 32];
+    __shared__ uint8_t sflags[kRows];
+
+    const int split = blockIdx.x;
+    const int h = blockIdx.y / P.n_rb, rb = blockIdx.y % P.n_rb;
+    const int b = blockIdx.z;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    const int S = clamp_seq(P, b, split == 0 && blockIdx.y == 0 && tid == 0);
+    const int nsp = n_splits_of(P, S);
+    if (split >= nsp) return;
+    const int t0 = split * P.chunk, t1 = min(S, t0 + P.chunk);
+    const bool last = split == nsp - 1;
+    const int row0 = rb * kRows;
+
+    const T *q = static_cast<const T *>(P.q);
+    for (int i = tid; i < kRows * D; i += 128) {
+        const int p = row0 + i / D;
+        float x = 0.f;
+        if (p < P.M) {
+            const int r = p / P.G, hq = h * P.G + p % P.G;
+            x = load_f(q + (((size_t)b * P.R + r) * P.Hq + hq) * D + i % D) * P.scale_log2;
+        }
+        sq[i / D][i % D] = x;
+    }
+    for (int i = tid; i < kRows * P.W; i += 128) {
+        const int pr = i / P.W, w = i % P.W, p = row0 + pr;
+        svis[pr][w] = p < P.M ? P.vis[((size_t)b * P.R + p / P.G) * P.W + w] : 0u;
+    }
+    if (tid < kRows) {
+        const int p = row0 + tid;
+        sflags[tid] = p < P.M ? P.row_flags[(size_t)b * P.R + p / P.G] : 0;
+    }
+
+    float m[4], l[4], acc[4][D / 32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) acc[i][j] = 0.f;
+    }
+
+    const uint8_t *kv = static_cast<const uint8_t *>(P.kc);
+    const int n_prefix_tiles = ceil_div(t1 - t0, kCols);
+    const int n_soft_tiles = last ? ceil_div(P.n_soft, kCols) : 0;
+    const int n_block_tiles = last ? ceil_div(P.R, kCols) : 0;
+    const int n_tiles = n_prefix_tiles + n_soft_tiles + n_block_tiles;
+    bool bad_page = false;
+
+    for (int tile = 0; tile < n_tiles; ++tile) {
+        int kind, base, ncols;
+        if (tile < n_prefix_tiles) {
+            kind = kColPrefix;
+            base = t0 + tile * kCols;
+            ncols = min(kCols, t1 - base);
+        } else if (tile < n_prefix_tiles + n_soft_tiles) {
+            kind = kColSoft;
+            base = (tile - n_prefix_tiles) * kCols;
+            ncols = min(kCols, P.n_soft - base);
+        } else {
+            kind = kColBlock;
+            base = (tile - n_prefix_tiles - n_soft_tiles) * kCols;
+            ncols = min(kCols, P.R - base);
+        }
+        __syncthreads();             // previous tile consumed (and sq / svis ready)
+        if (kind == kColPrefix) {
+            // 16 codes a vector: K and V of the tile
+            constexpr int VPR = D / 16;
+            constexpr int kPer = 2 * kCols * VPR / 128;
+            uint4 w[kPer];
+            float sc[kPer];
+#pragma unroll
+            for (int it = 0; it < kPer; ++it) {
+                const int i = tid + it * 128, x = i / (kCols * VPR), j = (i / VPR) % kCols, c = i % VPR;
+                w[it] = make_uint4(0u, 0u, 0u, 0u);
+                sc[it] = 0.f;
+                if (j < ncols) {
+                    const int t = base + j;
+                    const int page = P.page_table[(size_t)b * P.max_pages + t / P.page_size];
+                    if (page < 0 || page >= P.n_pages) {
+                        bad_page = true;
+                    } else {
+                        w[it] = *reinterpret_cast<const uint4 *>(
+                            kv + kv8_block(page, h, P.Hkv, P.page_size, D) +
+                            kv8_row(t % P.page_size, x, D) + c * 16);
+                        sc[it] = kv8_read_scale(Q.scales[((size_t)page * P.Hkv + h) * 2 + x]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < kPer; ++it) {
+                const int i = tid + it * 128, x = i / (kCols * VPR), j = (i / VPR) % kCols, c = i % VPR;
+                float *dst = x ? &sv_[j][c * 16] : &sk[j][c * 16];
+                const uint32_t u[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 lo = from_e4m3x2(u[e] & 0xffffu), hi = from_e4m3x2(u[e] >> 16);
+                    *reinterpret_cast<float4 *>(dst + 4 * e) =
+                        make_float4(lo.x * sc[it], lo.y * sc[it], hi.x * sc[it], hi.y * sc[it]);
+                }
+            }
+        } else {
+            const size_t first = kind == kColSoft ? (size_t)h * P.n_soft
+                                                  : ((size_t)b * P.Hkv + h) * P.R;
+            const T *kp = static_cast<const T *>(kind == kColSoft ? P.soft_k : P.kb) + (first + base) * D;
+            const T *vp = static_cast<const T *>(kind == kColSoft ? P.soft_v : P.vb) + (first + base) * D;
+            for (int i = tid; i < kCols * D; i += 128) {
+                const int j = i / D, k = i % D;
+                sk[j][k] = j < ncols ? load_f(kp + i) : 0.f;
+                sv_[j][k] = j < ncols ? load_f(vp + i) : 0.f;
+            }
+        }
+        __syncthreads();
+
+        // scores: four rows of this warp against the lane's column
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int k = 0; k < D; k += 4) {
+            const float4 kk = *reinterpret_cast<const float4 *>(&sk[lane][k]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 qq = *reinterpret_cast<const float4 *>(&sq[warp * 4 + i][k]);
+                s[i] = fmaf(qq.x, kk.x, s[i]);
+                s[i] = fmaf(qq.y, kk.y, s[i]);
+                s[i] = fmaf(qq.z, kk.z, s[i]);
+                s[i] = fmaf(qq.w, kk.w, s[i]);
+            }
+        }
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int pr = warp * 4 + i;
+            const uint8_t fl = sflags[pr];
+            bool visible = false;
+            if (lane < ncols && (fl & SPEC_ROW_VALID)) {
+                if (kind == kColPrefix) visible = true;
+                else if (kind == kColSoft) visible = (fl & SPEC_ROW_SEES_SOFT) != 0;
+                else visible = (svis[pr][(base + lane) >> 5] >> ((base + lane) & 31)) & 1u;
+            }
+            const float mn = fmaxf(m[i], warp_max(visible ? s[i] : -INFINITY));
+            const float mr = mn == -INFINITY ? 0.f : mn;    // (nothing but masked, -inf or NaN scores)
+            const float alpha = exp2f(m[i] - mr);
+            p[i] = visible ? exp2f(s[i] - mr) : 0.f;
+            l[i] = l[i] * alpha + warp_sum(p[i]);
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) acc[i][j] *= alpha;
+            m[i] = mn;
+        }
+        // O: columns without weight in a row are left out (their values may
+        // be anything)
+        for (int jj = 0; jj < ncols; ++jj) {
+            float v[D / 32];
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) v[j] = sv_[jj][lane + 32 * j];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float pj = __shfl_sync(0xffffffffu, p[i], jj);
+                if (pj != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) acc[i][j] = fmaf(pj, v[j], acc[i][j]);
+                }
+            }
+        }
+    }
+    if (bad_page) raise_status(P.status, SPEC_DEV_BAD_PAGE);
+
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = row0 + warp * 4 + i;
+        if (p >= P.M) continue;
+        const size_t idx = part_index(P, b, h, split, p);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) P.part_o[idx * D + lane + 32 * j] = acc[i][j];
+        if (lane == 0) {
+            P.part_ml[idx * 2] = m[i];
+            P.part_ml[idx * 2 + 1] = l[i];
+        }
+    }
+}
+
+// Merge the splits of every packed row, one warp each.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) attn_kv8_combine_kernel(AttnParams P) {
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int p = blockIdx.x * 4 + warp;
+    const int h = blockIdx.y, b = blockIdx.z;
+    if (p >= P.M) return;
+    const int nsp = n_splits_of(P, clamp_seq(P, b, false));
+    float mstar = -INFINITY;
+    for (int s = 0; s < nsp; ++s) mstar = fmaxf(mstar, P.part_ml[part_index(P, b, h, s, p) * 2]);
+    const float mr = mstar == -INFINITY ? 0.f : mstar;
+    float out[D / 32], L = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) out[j] = 0.f;
+    for (int s = 0; s < nsp; ++s) {
+        const size_t idx = part_index(P, b, h, s, p);
+        // (a split without visible columns has sums 0, or NaN that must stay)
+        const float ms = P.part_ml[idx * 2];
+        const float w = ms == -INFINITY ? 1.f : exp2f(ms - mr);
+        L = fmaf(w, P.part_ml[idx * 2 + 1], L);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) out[j] = fmaf(w, P.part_o[idx * D + lane + 32 * j], out[j]);
+    }
+    const int r = p / P.G, hq = h * P.G + p % P.G;
+    T *o = static_cast<T *>(P.o) + (((size_t)b * P.R + r) * P.Hq + hq) * D;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) store_f(o + lane + 32 * j, out[j] * inv);
+    if (lane == 0)
+        P.lse[((size_t)b * P.Hq + hq) * P.R + r] = L == 0.f ? -INFINITY : (mr + log2f(L)) * kLn2;
+}
+
+// ---------------------------------------------------------------- planning
+
+struct Plan8 {
+    Kv8Params Q;
+    size_t off_ml;      // byte offset of part_ml in the workspace
+    size_t ws_bytes;
+};
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+spec_status_t make_plan8(const spec_attn_desc *a, const spec_kv8_desc *c, Plan8 *out) {
+    if (!a || !c) return SPEC_ERR_INVALID_ARG;
+    if (a->batch < 0 || a->n_rows <= 0 || a->n_q_heads <= 0 || a->n_kv_heads <= 0 ||
+        a->n_q_heads % a->n_kv_heads != 0 || a->n_soft < 0 || a->split_tokens < 0)
+        return SPEC_ERR_INVALID_ARG;
+    if (a->n_rows > SPEC_MAX_ROWS || a->n_soft > 64) return SPEC_ERR_UNSUPPORTED;
+    if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
+    const spec_status_t st = check_kv8(c);
+    if (st != SPEC_OK) return st;
+    if (c->n_kv_heads != a->n_kv_heads || c->head_dim != a->head_dim || c->batch < a->batch ||
+        c->max_pages_per_seq <= 0 || a->split_tokens % 64 != 0)
+        return SPEC_ERR_INVALID_ARG;
+    if (a->batch > 65535 || (long long)c->max_pages_per_seq * c->page_size > (1ll << 30))
+        return SPEC_ERR_UNSUPPORTED;
+    Plan8 plan{};
+    AttnParams &P = plan.Q.a;
+    P.B = a->batch;
+    P.R = a->n_rows;
+    P.Hq = a->n_q_heads;
+    P.Hkv = a->n_kv_heads;
+    P.G = a->n_q_heads / a->n_kv_heads;
+    P.d = a->head_dim;
+    if ((long long)P.R * P.G > (1 << 20)) return SPEC_ERR_UNSUPPORTED;
+    P.M = P.R * P.G;
+    P.W = ceil_div(P.R, 32);
+    P.n_soft = a->n_soft;
+    P.paged = 1;
+    P.page_size = c->page_size;
+    P.max_pages = c->max_pages_per_seq;
+    P.n_pages = c->n_pages;
+    P.capacity = c->max_pages_per_seq * c->page_size;
+    const float scale = a->scale != 0.f ? a->scale : 1.f / sqrtf((float)a->head_dim);
+    P.scale_log2 = scale * kLog2e;
+    P.rb_rows = kRows;
+    P.n_rb = ceil_div(P.M, P.rb_rows);
+    if ((long long)P.Hkv * P.n_rb > 65535) return SPEC_ERR_UNSUPPORTED;
+    if (a->split_tokens > 0) {
+        P.chunk = a->split_tokens;
+    } else {
+        // about eight CTAs per SM for prefixes at half the capacity
+        const long long units = (long long)P.B * P.Hkv * P.n_rb;
+        const long long half = P.capacity / 2 > 64 ? P.capacity / 2 : 64;
+        const long long target = 8ll * num_sms();
+        long long chunk = (units * half + target - 1) / target;
+        chunk = (chunk + 63) / 64 * 64;
+        if (chunk < 128) chunk = 128;
+        if (chunk > 16384) chunk = 16384;
+        P.chunk = (int)chunk;
+    }
+    P.max_splits = ceil_div(P.capacity, P.chunk);
+    const size_t nrow = (size_t)P.B * P.Hkv * P.max_splits * P.M;
+    plan.off_ml = align256(nrow * P.d * sizeof(float));
+    plan.ws_bytes = plan.off_ml + align256(nrow * 2 * sizeof(float));
+    *out = plan;
+    return SPEC_OK;
+}
+
+template <typename T, int D>
+spec_status_t launch_simt8(const Kv8Params &Q, cudaStream_t s) {
+    const AttnParams &P = Q.a;
+    spec_status_t st = launch(attn_kv8_simt_kernel<T, D>, dim3(P.max_splits, P.Hkv * P.n_rb, P.B),
+                              dim3(128), 0, s, Q);
+    if (st != SPEC_OK) return st;
+    st = launch(attn_kv8_combine_kernel<T, D>, dim3(ceil_div(P.M, 4), P.Hkv, P.B), dim3(128), 0, s, P);
+    return st != SPEC_OK ? st : launch_status();
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" spec_status_t spec_verify_attn_kv8_workspace_size(const spec_attn_desc *attn,
+                                                             const spec_kv8_desc *cache,
+                                                             size_t *bytes) {
+    if (!bytes) return SPEC_ERR_INVALID_ARG;
+    sv::Plan8 plan;
+    const spec_status_t st = sv::make_plan8(attn, cache, &plan);
+    if (st != SPEC_OK) return st;
+    *bytes = plan.ws_bytes;
+    return SPEC_OK;
+}
+
+extern "C" spec_status_t spec_verify_attn_kv8(const spec_attn_desc *attn, const void *q,
+                                              const spec_kv8_desc *cache, const void *kb,
+                                              const void *vb, const void *soft_k,
+                                              const void *soft_v, const int32_t *seq_len,
+                                              const uint32_t *vis, const uint8_t *row_flags,
+                                              void *o, float *lse, void *workspace,
+                                              size_t workspace_bytes, void *stream) {
+    using namespace sv;
+    Plan8 plan;
+    const spec_status_t st = make_plan8(attn, cache, &plan);
+    if (st != SPEC_OK) return st;
+    AttnParams &P = plan.Q.a;
+    if (P.B == 0) return SPEC_OK;
+    if (!q || !kb || !vb || !seq_len || !vis || !row_flags || !o || !lse || !workspace ||
+        !cache->kv || !cache->scales || !cache->page_table ||
+        (P.n_soft > 0 && (!soft_k || !soft_v)))
+        return SPEC_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kb) || !aligned16(vb) || !aligned16(o) ||
+        !aligned16(cache->kv) || (P.n_soft > 0 && (!aligned16(soft_k) || !aligned16(soft_v))) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
+        return SPEC_ERR_INVALID_ARG;
+    if (workspace_bytes < plan.ws_bytes) return SPEC_ERR_CAPACITY;
+    P.status = status_ptr();
+    if (!P.status) return SPEC_ERR_CUDA;
+    P.q = q;
+    P.kc = cache->kv;
+    P.page_table = cache->page_table;
+    P.kb = kb;
+    P.vb = vb;
+    P.soft_k = soft_k;
+    P.soft_v = soft_v;
+    P.seq_len = seq_len;
+    P.vis = vis;
+    P.row_flags = row_flags;
+    P.o = o;
+    P.lse = lse;
+    P.part_o = static_cast<float *>(workspace);
+    P.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.off_ml);
+    plan.Q.scales = cache->scales;
+    cudaStream_t s = as_stream(stream);
+    if (attn->dtype == SPEC_BF16)
+        return P.d == 128 ? launch_simt8<__nv_bfloat16, 128>(plan.Q, s)
+                          : launch_simt8<__nv_bfloat16, 64>(plan.Q, s);
+    return P.d == 128 ? launch_simt8<float, 128>(plan.Q, s) : launch_simt8<float, 64>(plan.Q, s);
+}
