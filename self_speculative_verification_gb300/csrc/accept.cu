@@ -99,7 +99,7 @@ vocab_reduce_kernel(const T *__restrict__ logits, int V, const int32_t *__restri
                 best.m = bm;
                 best.idx = bi;
             }
-            const float mb = best.m * c2;
+            const float mb = best_ref(best) * c2;
             float acc[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) acc[j] = 0.f;

@@ -26,11 +26,15 @@ __device__ __forceinline__ void best_push(Best &b, float z, int i, float inv_t) 
         b.s = b.s * __expf((b.m - z) * inv_t) + 1.f;
         b.m = z;
         b.idx = i;
-    } else {
+    } else if (z != -INFINITY) {      // (a masked logit adds nothing)
         b.s += __expf((z - b.m) * inv_t);
         if (z == b.m && i < b.idx) b.idx = i;
     }
 }
+
+// The reference a thread's exponents are taken against: its max, or 0 while
+// it has met masked (-inf) logits alone, whose terms are then 2^-inf = 0.
+__device__ __forceinline__ float best_ref(const Best &b) { return b.m == -INFINITY ? 0.f : b.m; }
 
 __device__ __forceinline__ Best best_merge(Best a, Best b, float inv_t) {
     if (b.m > a.m || (b.m == a.m && b.idx < a.idx)) {
@@ -84,7 +88,7 @@ __device__ __forceinline__ void push_bf16_batch(Best &best, const Bf16Batch &x, 
         best.idx = bi;
     }
     const uint64_t c22 = pair(c2, c2);
-    const float nmb = -best.m * c2;
+    const float nmb = -best_ref(best) * c2;
     const uint64_t nmb2 = pair(nmb, nmb);
     uint64_t acc[4] = {pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
@@ -216,7 +220,7 @@ __device__ bool bulk_row_scan(const __nv_bfloat16 *slice, int n_el, int v0, floa
                 best.m = bm;
                 best.idx = bi;
             }
-            const float mb = best.m * c2;
+            const float mb = best_ref(best) * c2;
             float acc[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] = 0.f;
