@@ -643,8 +643,8 @@ spec_status_t spec_verify_attn_kv8_workspace_size(const spec_attn_desc *attn,
  * single-token decoding form.
  *
  * Scores, softmax statistics and sums are held in fp32.  A row that sees a
- * block whose scale is NaN gets o = lse = NaN.  Codes in slots past seq_len
- * are never used.  A seq_len outside [0, capacity] is clamped and sets
+ * block whose key scale is NaN gets o = lse = NaN, one whose value scale is
+ * NaN o = NaN.  Codes in slots past seq_len are never used.  A seq_len outside [0, capacity] is clamped and sets
  * SPEC_DEV_SEQ_OVERFLOW; a page id outside [0, n_pages) is not read and sets
  * SPEC_DEV_BAD_PAGE (the affected outputs are then unspecified).  q, kb, vb,
  * soft_k, soft_v and o must be 16-byte aligned.
@@ -685,8 +685,9 @@ spec_status_t kv8_commit(const spec_kv8_desc *cache, int dtype, int batch, int n
  *             head_dim (each of k and v may lie inside wider rows, such as a
  *             joint projection's output); rows on 16-byte boundaries.
  *   slot_map  int64 [n_tokens]: page * page_size + offset, or < 0 for a
- *             token that is not written.  Tokens of one page follow one
- *             another with rising slots, as spec_page_plan numbers them.
+ *             token that is not written (its slot is left as it was).
+ *             Tokens of one page follow one another in consecutive slots,
+ *             as spec_page_plan numbers them.
  *
  * Blocks take or raise their scales as in kv8_commit (a run of tokens that
  * begins at offset 0 begins the page).  A page named by two separate runs of

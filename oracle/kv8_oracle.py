@@ -110,9 +110,11 @@ def append(codes, scales, k, v, slot_map, page_size):
             continue
         page, off = divmod(int(slot_map[i]), page_size)
         m = 1
-        while i + m < n and off + m < page_size and slot_map[i + m] == slot_map[i] + m:
+        while i + m < n and off + m < page_size and slot_map[i + m] in (-1, slot_map[i] + m):
             m += 1
-        write_rows(codes, scales, page, off, list(k[i:i + m]), list(v[i:i + m]))
+        keep = [slot_map[i + t] >= 0 for t in range(m)]
+        write_rows(codes, scales, page, off, [r if w else None for r, w in zip(k[i:i + m], keep)],
+                   [r if w else None for r, w in zip(v[i:i + m], keep)])
         i += m
     return codes, scales
 

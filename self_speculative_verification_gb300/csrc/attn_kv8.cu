@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
             }
         }
         float p[4];
+        unsigned seen[4];            // columns each row sees
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int pr = warp * 4 + i;
@@ -175,13 +176,14 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
             const float mr = mn == -INFINITY ? 0.f : mn;    // (nothing but masked, -inf or NaN scores)
             const float alpha = exp2f(m[i] - mr);
             p[i] = visible ? exp2f(s[i] - mr) : 0.f;
+            seen[i] = __ballot_sync(0xffffffffu, visible);
             l[i] = l[i] * alpha + warp_sum(p[i]);
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) acc[i][j] *= alpha;
             m[i] = mn;
         }
-        // O: columns without weight in a row are left out (their values may
-        // be anything)
+        // O: columns a row does not see are left out (their values may be
+        // anything)
         for (int jj = 0; jj < ncols; ++jj) {
             float v[D / 32];
 #pragma unroll
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float pj = __shfl_sync(0xffffffffu, p[i], jj);
-                if (pj != 0.f) {
+                if ((seen[i] >> jj) & 1u) {
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j) acc[i][j] = fmaf(pj, v[j], acc[i][j]);
                 }

@@ -195,8 +195,8 @@ struct Append8Params {
 constexpr int kAppendTokens = 64;
 
 // CTA (64 packed tokens, hpc heads): the runs that begin among its tokens (a
-// run: consecutive tokens in consecutive slots of one page), one warp per
-// (run, head, K / V).
+// run: consecutive tokens in consecutive slots of one page, tokens that are
+// not written in between), one warp per (run, head, K / V).
 template <typename T, int D>
 __global__ void __launch_bounds__(kWriteWarps * 32) kv8_append_kernel(Append8Params P) {
     pdl_wait();
@@ -213,7 +213,12 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv8_append_kernel(Append8Par
             if (s >= n_slots) {
                 if (blockIdx.y == 0) raise_status(P.status, SPEC_DEV_BAD_PAGE);
             } else if (s >= 0) {
-                start = i == 0 || s % P.ps == 0 || P.slots[i - 1] != s - 1;
+                // it goes on with a run when the nearest written token before
+                // it lies as far back as that one's slot
+                int m = 1;
+                const int off = (int)(s % P.ps);
+                while (m <= off && m <= i && P.slots[i - m] < 0) ++m;
+                start = m > off || m > i || P.slots[i - m] != s - m;
             }
         }
         const unsigned m = __ballot_sync(0xffffffffu, start);
@@ -230,10 +235,13 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv8_append_kernel(Append8Par
         const int page = (int)(slot / P.ps), first = (int)(slot % P.ps);
         // the run's length
         int n = 0;
+        bool gaps = false;
         for (int k = 0; first + k < P.ps; k += 32) {
-            const bool ok = first + k + lane < P.ps && k + lane < P.n - i &&
-                            P.slots[i + k + lane] == slot + k + lane;
-            const unsigned m = __ballot_sync(0xffffffffu, !ok);
+            const bool in = first + k + lane < P.ps && k + lane < P.n - i;
+            const long long s = in ? P.slots[i + k + lane] : 0;
+            gaps = gaps || s < 0;
+            const unsigned m =
+                __ballot_sync(0xffffffffu, !in || (s >= 0 && s != slot + k + lane));
             if (m) {
                 n = k + __ffs(m) - 1;
                 break;
@@ -243,7 +251,10 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv8_append_kernel(Append8Par
         const T *src = x ? static_cast<const T *>(P.v) + (size_t)i * P.stride_v + (size_t)h * D
                          : static_cast<const T *>(P.k) + (size_t)i * P.stride_k + (size_t)h * D;
         const long long stride = x ? P.stride_v : P.stride_k;
-        auto row = [&](int r) -> const T * { return src + (size_t)r * stride; };
+        gaps = __any_sync(0xffffffffu, gaps);
+        auto row = [&](int r) -> const T * {
+            return gaps && P.slots[i + r] < 0 ? nullptr : src + (size_t)r * stride;
+        };
         write_block<T, D>(P.kv + kv8_block(page, h, P.Hkv, P.ps, D),
                           P.scales + ((size_t)page * P.Hkv + h) * 2 + x, x, first, n, row);
     }
