@@ -253,6 +253,7 @@ struct Plan8 {
     Kv8Params Q;
     size_t off_ml;      // byte offset of part_ml in the workspace
     size_t ws_bytes;
+    bool use_tc;
 };
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -307,6 +308,12 @@ spec_status_t make_plan8(const spec_attn_desc *a, const spec_kv8_desc *c, Plan8 
         P.chunk = (int)chunk;
     }
     P.max_splits = ceil_div(P.capacity, P.chunk);
+    plan.use_tc = kv8_tc_supported(P, a->dtype);
+    if (plan.use_tc) {
+        plan.ws_bytes = kv8_tc_workspace_bytes(P);
+        *out = plan;
+        return SPEC_OK;
+    }
     const size_t nrow = (size_t)P.B * P.Hkv * P.max_splits * P.M;
     plan.off_ml = align256(nrow * P.d * sizeof(float));
     plan.ws_bytes = plan.off_ml + align256(nrow * 2 * sizeof(float));
@@ -378,6 +385,7 @@ extern "C" spec_status_t spec_verify_attn_kv8(const spec_attn_desc *attn, const 
     P.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.off_ml);
     plan.Q.scales = cache->scales;
     cudaStream_t s = as_stream(stream);
+    if (plan.use_tc) return launch_attn_kv8_tc(plan.Q, s);
     if (attn->dtype == SPEC_BF16)
         return P.d == 128 ? launch_simt8<__nv_bfloat16, 128>(plan.Q, s)
                           : launch_simt8<__nv_bfloat16, 64>(plan.Q, s);

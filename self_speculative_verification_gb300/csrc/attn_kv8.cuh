@@ -1,4 +1,5 @@
-// What the kernels of spec_verify_attn_kv8 share: the parameters of a call.
+// What the kernels of spec_verify_attn_kv8 share: the parameters of a call,
+// and the tensor-core path's workspace and launch.
 #pragma once
 
 #include "attn_common.cuh"
@@ -12,5 +13,12 @@ struct Kv8Params {
     AttnParams a;
     const float *scales;     // [n_pages][Hkv][2]
 };
+
+// The tensor-core path (bf16 rows): rows per unit, bytes of workspace, and a
+// call, whose workspace begins at Q.a.part_o.
+int kv8_tc_rows(const AttnParams &P);
+bool kv8_tc_supported(const AttnParams &P, int dtype);
+size_t kv8_tc_workspace_bytes(const AttnParams &P);
+spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s);
 
 }  // namespace sv

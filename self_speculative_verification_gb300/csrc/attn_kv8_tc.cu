@@ -1,0 +1,1009 @@
+// The tensor-core path of spec_verify_attn_kv8 (bf16 rows).
+//
+// The cache's codes go to the tensor cores as they are: a step takes 128
+// tokens of one (request, KV head) and computes, with kind::f8f6f4 (e4m3 x
+// e4m3 -> fp32),
+//   S^T [128 tokens x rows] = K (A, K-major) . Q^T (B),
+//   O^T [head dims x rows] += V^T (A, MN-major) . P^T (B, MN-major),
+// so the keys and values are the M = 128 operands whatever the number of
+// query rows, both read straight from the tile the tensor copy left in shared
+// memory (its eight-row key and value groups alternate, i.e. either lies at a
+// fixed stride), and a thread of the softmax owns one token: the block's two
+// scales are a scalar each to it.
+//
+// What is not 8 bits wide is made so without loss that counts: a bf16 value
+// has 8 significant bits, an e4m3 value 4, so a query (and a block or
+// soft-prompt key or value) is the sum of two e4m3 values under one
+// power-of-two scale per row, exact but for elements under 2^-9 of the row's
+// largest (there: half of e4m3's smallest step, 2^-17.8 of the largest).  P
+// is split the same way, its second part raised by 2^4 into columns of its
+// own: 2^-9 of p, as bf16 would give it, and 2^-21 of the largest p where p
+// is small.  The two parts of Q are 2 R columns of one product, the two parts
+// of P 2 R columns of the other.
+//
+// Softmax: p = 2^(s + log2(v_scale) - M), M per row, raised only when a value
+// would pass e4m3's 448; so the tile needs no maximum, only a vote (and
+// every row's sum is a register of each token's thread until the unit ends).
+// l adds p / v_scale.
+//
+// A persistent grid takes equal parts of the linear step space (attn_tc_sched):
+// a unit is a (request, KV head, block of R packed rows), its steps the prefix
+// in 128-token tiles, then the tail -- soft prompt and block, which a first
+// kernel has split into two e4m3 tiles -- in the same form, two ring slots a
+// step.  Units split between CTAs leave fp32 partials for a combine kernel.
+//
+// Bound by the cache's bytes up to 64 packed rows per KV head (12 MMAs of
+// about 50 cycles against ~1400 cycles to stream a tile at d = 128), by the
+// softmax beyond, where the row blocks of a head read the cache through L2.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include "attn_kv8.cuh"
+#include "attn_tc_sched.cuh"
+#include "kv8_common.cuh"
+
+namespace sv {
+namespace {
+
+using namespace tc5;
+
+constexpr int kStep = 128;                  // tokens a step
+constexpr int kTcThreads = 12 * 32;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kRecWarp = 10;
+constexpr float kTop = 8.75f;               // log2 of the largest P allowed (448 = 2^8.807)
+constexpr float kAim = 7.f;                 // log2 P of a row's maximum when M is raised
+constexpr float kNoRef = -1e30f;            // M of a row that has seen nothing
+constexpr float kLoUp = 16.f;               // factor of P's second part
+
+struct Tc8Params {
+    TcParams t;              // schedule, split, partials (t.a: the call)
+    const float *scales;     // the cache's
+    const float *q_scale;    // [units][RB]: softmax scale (log2) x the row's power of two
+    const float2 *tail_scale;    // [B][Hkv][tail_pad]: scales of the tail's tokens
+    int tail_len, tail_pad;  // n_soft + R, rounded up to 16
+    int n_tail;              // its 128-token tiles
+    int box_tokens;          // tokens per cache box
+};
+
+template <int D, int RB>
+struct Cfg {
+    static constexpr int HR = RB / 2;                   // rows of a softmax warpgroup
+    static constexpr int kSlot = 2 * kStep * D;         // K and V of a step
+    static constexpr int kQ = 2 * RB * D;               // a unit's queries, both parts
+    static constexpr int kP = kStep * 128;              // P^T, rows of 128 bytes
+    static constexpr int NS = D == 64 ? 8 : (RB == 64 ? 4 : 5);
+    static constexpr uint32_t kColS = 2 * RB;           // TMEM: O at 0, S buffer b at kColS (1 + b)
+    static constexpr int kCols = 6 * RB <= 64 ? 64 : 6 * RB <= 128 ? 128 : 6 * RB <= 256 ? 256 : 512;
+};
+
+template <int D, int RB>
+struct Shared8 {
+    using C = Cfg<D, RB>;
+    uint64_t full[C::NS], empty[C::NS];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2], o_upd[2];
+    uint64_t drain;
+    float2 scale[C::NS][8];              // key / value scale of each box of a slot
+    float2 row[2][C::HR];                // a row's q_scale and M
+    float fac[2][C::HR];
+    int rmax[2][4][C::HR];
+    float rsum[2][4][C::HR];
+    int out[2][C::HR];                   // (row * Hq + head) * 2 + valid, or -1
+    uint32_t tmem_base;
+};
+
+template <int D, int RB>
+constexpr size_t smem8() {
+    using C = Cfg<D, RB>;
+    return (size_t)C::NS * C::kSlot + 2 * C::kQ + 2 * C::kP + sizeof(Shared8<D, RB>) + 1024;
+}
+static_assert(smem8<128, 64>() <= 227 * 1024 && smem8<128, 32>() <= 227 * 1024 &&
+                  smem8<64, 64>() <= 227 * 1024,
+              "shared memory of the 8-bit attention kernel");
+
+// OR over the 128 threads of a warpgroup (named barrier `id`).
+__device__ __forceinline__ bool group_or(int id, bool x) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "barrier.cta.red.or.pred p, %1, 128, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((int)x)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_sync(int id) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+}
+
+// Floats as integers of the same order (NaN as -inf), and back.
+__device__ __forceinline__ int order_of(float x) {
+    const int i = __float_as_int(x == x ? x : -INFINITY);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float of_order(int i) {
+    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// Two values of P: the e4m3 pair nearest to them, and the pair nearest to 16
+// times what it leaves (through f16, whose 11 bits leave 2^-12 of p).
+__device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32_t &lo) {
+    uint32_t pf, hf, d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pf) : "f"(p1), "f"(p0));
+    hi = e4m3x2(p0, p1);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hf) : "h"((uint16_t)hi));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(pf), "r"(hf));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0x4c004c00u));   // 16, 16
+    uint16_t l;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(d));
+    lo = l;
+}
+
+// The cursor's step: prefix tile or tail tile, its first token, how many of
+// its 128 tokens there are.
+struct Step8 {
+    bool tail;
+    int tile, n;
+};
+__device__ __forceinline__ Step8 step_at(const Tc8Params &P, const Cursor &c) {
+    const int np = (c.S + kStep - 1) / kStep;
+    Step8 s;
+    s.tail = c.tile >= np;
+    s.tile = s.tail ? c.tile - np : c.tile;
+    s.n = min(kStep, (s.tail ? P.tail_len : c.S) - s.tile * kStep);
+    return s;
+}
+
+template <int D, int RB>
+__global__ void __launch_bounds__(kTcThreads, 1)
+attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ CUtensorMap m_kv,
+                   const __grid_constant__ CUtensorMap m_tail,
+                   const __grid_constant__ CUtensorMap m_q) {
+    pdl_wait();
+    using C = Cfg<D, RB>;
+    constexpr int HR = C::HR, NS = C::NS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *ring = smem;
+    uint8_t *qbuf = ring + NS * C::kSlot;
+    uint8_t *pbuf = qbuf + 2 * C::kQ;
+    auto &sh = *reinterpret_cast<Shared8<D, RB> *>(pbuf + 2 * C::kP);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const TcParams &T = P.t;
+    const AttnParams &A = T.a;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&sh.full[s], 2);           // the copies, the scales
+            mbar_init(&sh.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sh.q_full[b], 1);
+            mbar_init(&sh.q_empty[b], 1);
+            mbar_init(&sh.s_full[b], 1);
+            mbar_init(&sh.p_full[b], 8);
+            mbar_init(&sh.o_upd[b], 1);
+        }
+        mbar_init(&sh.drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sh.tmem_base)),
+                     "r"(C::kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sh.tmem_base;
+
+    const WarpSched ws = warp_sched(T);
+    const int cta = blockIdx.x;
+    const long long t_begin = sched_range_lo(T, ws, cta);
+    const long long t_end = sched_range_lo(T, ws, cta + 1);
+    if (threadIdx.x == 0) {
+        T.bounds[cta] = t_begin;
+        if (cta == T.n_ctas - 1) T.bounds[T.n_ctas] = ws.T;
+    }
+    auto unit_of = [&](const Cursor &c) { return (c.b * T.seg_h + c.h) * T.seg_rb + c.rb; };
+
+    if (warp == kRecWarp) {
+        const BoundaryRec rec = warp_boundary_record(T, ws, cta, t_begin, t_end);
+        if (lane == 0) T.recs[cta] = rec;
+    } else if (t_begin < t_end && warp == kProducerWarp) {
+        // ------------------------------------------------------- producer
+        // lane i owns box i of a step: box_tokens tokens (prefix) or 16 (tail)
+        const uint64_t keep = policy_evict_last();
+        const uint64_t stream = T.seg_rb == 1 ? policy_evict_first() : keep;
+        const int bt = P.box_tokens, boxes = kStep / bt;
+        Cursor c;
+        cursor_init(T, ws, t_begin, c);
+        // this lane's page of the cursor's step: -1 no box, -2 a bad page
+        auto page_of = [&](const Cursor &k) -> int {
+            const Step8 s = step_at(P, k);
+            const int tok = s.tile * kStep + lane * bt;
+            if (s.tail || lane >= boxes || tok >= k.S) return -1;
+            const int pg = A.page_table[(size_t)k.b * A.max_pages + tok / A.page_size];
+            return pg < 0 || pg >= A.n_pages ? -2 : pg;
+        };
+        auto scale_of = [&](const Cursor &k, int pg) {
+            if (pg < 0) return make_float2(1.f, 1.f);
+            return *reinterpret_cast<const float2 *>(P.scales + ((size_t)pg * A.Hkv + k.h) * 2);
+        };
+        int pg = page_of(c);
+        float2 sc = scale_of(c, pg);
+        int slot = 0, nq = 0;
+        long long used = 0;                  // ring slots taken so far
+        bool ok = true;
+        for (long long t = t_begin; t < t_end; ++t) {
+            const Step8 s = step_at(P, c);
+            bool got = true;
+            if (t == t_begin || c.tile == 0) {
+                // the unit's queries, once the unit two back is done with the
+                // buffer
+                const int qb = nq & 1;
+                if (lane == 0) {
+                    got = nq < 2 || mbar_wait(&sh.q_empty[qb], (uint32_t)(((nq >> 1) - 1) & 1), T.wait);
+                    if (got) {
+                        mbar_arrive_expect_tx(&sh.q_full[qb], C::kQ);
+                        tma_load_2d(qbuf + qb * C::kQ, &m_q, 0, unit_of(c) * (2 * RB), &sh.q_full[qb],
+                                    keep);
+                    }
+                }
+                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                    ok = false;
+                    break;
+                }
+                ++nq;
+            }
+            const int parts = s.tail ? 2 : 1;
+            for (int part = 0; part < parts; ++part) {
+                if (lane == 0)
+                    got = mbar_wait(&sh.empty[slot], (uint32_t)(((used / NS) & 1) ^ 1), T.wait);
+                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                    ok = false;
+                    break;
+                }
+                bool mine;
+                int rows;
+                if (s.tail) {
+                    mine = lane < 8 && lane * 16 < s.n;
+                    rows = 32;
+                } else {
+                    mine = pg >= 0;
+                    rows = 2 * bt;
+                    if (pg == -2) raise_status(A.status, SPEC_DEV_BAD_PAGE);
+                }
+                const uint32_t bytes =
+                    (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * (uint32_t)(rows * D);
+                if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
+                __syncwarp();
+                uint8_t *dst = ring + slot * C::kSlot + lane * rows * D;
+                if (mine) {
+                    if (s.tail)
+                        tma_load_2d(dst, &m_tail, 0,
+                                    ((c.b * A.Hkv + c.h) * 2 + part) * (2 * P.tail_pad) +
+                                        s.tile * (2 * kStep) + lane * 32,
+                                    &sh.full[slot], keep);
+                    else
+                        tma_load_3d(dst, &m_kv, 0, 2 * ((s.tile * kStep + lane * bt) % A.page_size),
+                                    pg * A.Hkv + c.h, &sh.full[slot], stream);
+                }
+                if (!s.tail && lane < boxes) sh.scale[slot][lane] = sc;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.full[slot]);
+                ++used;
+                slot = slot + 1 == NS ? 0 : slot + 1;
+            }
+            if (!ok) break;
+            cursor_next(T, c);
+            if (t + 1 < t_end) {
+                pg = page_of(c);
+                sc = scale_of(c, pg);
+            }
+        }
+        if (lane == 0) {
+            if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
+            // do not leave while copies into this CTA's shared memory are in
+            // flight (the default limit: these copies were issued and complete)
+            for (long long i = used - 1; i >= 0 && i >= used - NS; --i)
+                if (!mbar_wait(&sh.full[i % NS], (uint32_t)((i / NS) & 1))) {
+                    raise_status(A.status, SPEC_DEV_TIMEOUT);
+                    break;
+                }
+            for (int n = nq - 1; n >= 0 && n >= nq - 2; --n)
+                if (!mbar_wait(&sh.q_full[n & 1], (uint32_t)((n >> 1) & 1))) {
+                    raise_status(A.status, SPEC_DEV_TIMEOUT);
+                    break;
+                }
+        }
+    } else if (t_begin < t_end && warp == kMmaWarp) {
+        // ----------------------------------------------------- MMA issuer
+        Cursor c;
+        cursor_init(T, ws, t_begin, c);       // warp-collective
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_e4m3(kStep, 2 * RB, false, false);
+            constexpr uint32_t id_pv = idesc_e4m3(kStep, 2 * RB, true, true);
+            // slot: 8-token groups of 8 key rows, then 8 value rows, D bytes
+            // each.  K (K-major): groups 16 D apart, a step of 32 head
+            // dimensions 32 bytes on.  V (MN-major): the same groups, 8 D
+            // further; a step of 32 tokens is four groups.  At D = 64 the 128
+            // rows of M are the 64 dimensions twice (leading offset 0).
+            const uint64_t kd0 = smem_desc_sw<D>(smem_u32(ring), 16, 16 * D);
+            const uint64_t vd0 = smem_desc_sw<D>(smem_u32(ring) + 8 * D, 0, 16 * D);
+            const uint64_t qd0 = smem_desc_sw<D>(smem_u32(qbuf), 16, 8 * D);
+            const uint64_t pd0 = smem_desc(smem_u32(pbuf), 0, 1024);
+            int nq = 0, slot = 0, prev_slot = 0, prev_parts = 1;
+            bool ok = true, prev_first = true;
+            long long used = 0;
+            auto issue_pv = [&](long long j) -> bool {
+                const int b = (int)(j & 1);
+                if (!mbar_wait(&sh.p_full[b], (uint32_t)((j >> 1) & 1), T.wait)) return false;
+                fence_after();
+                int sl = prev_slot;
+                for (int part = 0; part < prev_parts; ++part) {
+                    const uint64_t vd = vd0 + (uint64_t)((sl * C::kSlot) >> 4);
+#pragma unroll
+                    for (int k = 0; k < kStep / 32; ++k)
+                        mma8_ss(tmem, vd + (uint64_t)((k * 4 * 16 * D) >> 4),
+                                pd0 + (uint64_t)((b * C::kP + k * 4 * 1024) >> 4), id_pv,
+                                (k > 0 || part > 0 || !prev_first) ? 1u : 0u);
+                    commit(&sh.empty[sl]);
+                    sl = sl + 1 == NS ? 0 : sl + 1;
+                }
+                commit(&sh.o_upd[b]);
+                return true;
+            };
+            long long k = 0;
+            for (long long t = t_begin; t < t_end; ++t, ++k) {
+                const Step8 s = step_at(P, c);
+                const bool new_unit = k == 0 || c.tile == 0;
+                const bool last = c.tile == c.n_tiles - 1 || t == t_end - 1;
+                if (new_unit) {
+                    if (!mbar_wait(&sh.q_full[nq & 1], (uint32_t)((nq >> 1) & 1), T.wait)) {
+                        ok = false;
+                        break;
+                    }
+                    ++nq;
+                }
+                const int qb = (nq - 1) & 1, first_slot = slot, parts = s.tail ? 2 : 1;
+                for (int part = 0; part < parts && ok; ++part) {
+                    if (!mbar_wait(&sh.full[slot], (uint32_t)((used / NS) & 1), T.wait)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint64_t kd = kd0 + (uint64_t)((slot * C::kSlot) >> 4);
+                    const uint64_t qd = qd0 + (uint64_t)((qb * C::kQ) >> 4);
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e)
+                        mma8_ss(tmem + C::kColS * (1 + (uint32_t)(k & 1)), kd + (uint64_t)(e * 32 >> 4),
+                                qd + (uint64_t)(e * 32 >> 4), id_s, (e > 0 || part > 0) ? 1u : 0u);
+                    ++used;
+                    slot = slot + 1 == NS ? 0 : slot + 1;
+                }
+                if (!ok) break;
+                commit(&sh.s_full[k & 1]);
+                if (last) commit(&sh.q_empty[qb]);
+                if (k > 0 && !(ok = issue_pv(k - 1))) break;
+                prev_slot = first_slot;
+                prev_parts = parts;
+                prev_first = new_unit;
+                cursor_next(T, c);
+            }
+            if (ok && k > 0) ok = issue_pv(k - 1);
+            if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
+            // every MMA issued above has completed before TMEM is released
+            // (the default limit)
+            commit(&sh.drain);
+            if (!mbar_wait(&sh.drain, 0)) raise_status(A.status, SPEC_DEV_TIMEOUT);
+        }
+    } else if (t_begin < t_end && warp < kProducerWarp) {
+        // -------------------------------------------------------- softmax
+        // warpgroup g: rows g HR .. of the unit; a thread: one token of the
+        // step (TMEM lane), later one head dimension of O
+        const int g = warp >> 2, wq = warp & 3, bar = 1 + g;
+        const int tok = wq * 32 + lane, gi = threadIdx.x & 127;
+        const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+        Cursor c;
+        cursor_init(T, ws, t_begin, c);
+        float l[HR];
+        bool ok = true, seg_whole = false;
+        int seg_b = 0, seg_h = 0, seg_id = 0, slot = 0;
+        long long used = 0, k = 0;
+
+        // end of this CTA's part of a unit, after PV(j): the row sums over the
+        // tokens' threads, then O / l and LSE, or the partials
+        auto epilogue = [&](long long j) -> bool {
+            const bool got = ok && mbar_wait_warp(&sh.o_upd[j & 1], (uint32_t)((j >> 1) & 1), T.wait);
+            float mine = 0.f;
+#pragma unroll
+            for (int i = 0; i < HR; ++i) {
+                const float s = warp_sum(l[i]);
+                if (lane == i) mine = s;
+            }
+            if (lane < HR) sh.rsum[g][wq][lane] = mine;
+            if (group_or(bar, !got)) return false;
+            fence_after();
+            uint32_t hi[HR], lo[HR];
+            const uint32_t to = tmem + lane_base + (uint32_t)(g * RB);
+            ldn<HR>(to, hi);
+            ldn<HR>(to + HR, lo);
+            wait_ldn<HR>(hi, lo);
+            const size_t prow = slot_row(T, seg_id, cta, 0, 1, g * HR);
+#pragma unroll
+            for (int i = 0; i < HR; ++i) {
+                const float L = (sh.rsum[g][0][i] + sh.rsum[g][1][i]) + (sh.rsum[g][2][i] + sh.rsum[g][3][i]);
+                const float o = fmaf(__uint_as_float(lo[i]), 1.f / kLoUp, __uint_as_float(hi[i]));
+                const int out = sh.out[g][i];
+                if (out < 0) continue;
+                const float M = sh.row[g][i].y;
+                if (seg_whole) {
+                    const size_t r = (size_t)seg_b * A.R * A.Hq + (size_t)(out >> 1);
+                    const bool none = !(out & 1) || L == 0.f;
+                    if (tok < D)
+                        static_cast<__nv_bfloat16 *>(A.o)[r * D + tok] =
+                            __float2bfloat16_rn(none ? 0.f : o / L);
+                    if (gi == i) {
+                        const int hq = (out >> 1) % A.Hq, rr = (out >> 1) / A.Hq;
+                        A.lse[((size_t)seg_b * A.Hq + hq) * A.R + rr] =
+                            none ? -INFINITY : (M + log2f(L)) * kLn2;
+                    }
+                } else {
+                    if (tok < D) A.part_o[(prow + i) * D + tok] = o;
+                    if (gi == i) {
+                        A.part_ml[(prow + i) * 2] = M;
+                        A.part_ml[(prow + i) * 2 + 1] = L;
+                    }
+                }
+            }
+            fence_before();
+            return true;
+        };
+
+        for (long long t = t_begin; t < t_end; ++t, ++k) {
+            const bool new_unit = k == 0 || c.tile == 0;
+            if (new_unit) {
+                if (k > 0 && !epilogue(k - 1)) {
+                    ok = false;
+                    break;
+                }
+                seg_b = c.b;
+                seg_h = c.h;
+                seg_id = unit_of(c);
+                const long long seg_lo = t - c.tile;
+                seg_whole = seg_lo >= t_begin && seg_lo + c.n_tiles <= t_end;
+                group_sync(bar);               // the last unit's rows are read
+                if (gi < HR) {
+                    const int r = g * HR + gi, p = c.rb * RB + r;
+                    int out = -1;
+                    if (p < A.M) {
+                        const int rr = p / A.G;
+                        const int valid = A.row_flags[(size_t)c.b * A.R + rr] & SPEC_ROW_VALID;
+                        out = (rr * A.Hq + c.h * A.G + p % A.G) * 2 + (valid ? 1 : 0);
+                    }
+                    sh.out[g][gi] = out;
+                    sh.row[g][gi] = make_float2(P.q_scale[(size_t)seg_id * RB + r], kNoRef);
+                }
+                group_sync(bar);
+#pragma unroll
+                for (int i = 0; i < HR; ++i) l[i] = 0.f;
+            }
+            const Step8 s = step_at(P, c);
+            const int slot0 = slot, parts = s.tail ? 2 : 1;
+            // rows' visibility of this warp's 32 tail tokens, lane i: row i
+            uint32_t seen = 0xffffffffu;
+            float2 sc = make_float2(1.f, 1.f);
+            const bool here = tok < s.n;
+            if (s.tail) {
+                const int tt0 = s.tile * kStep + wq * 32;
+                if (here)
+                    sc = P.tail_scale[((size_t)seg_b * A.Hkv + seg_h) * P.tail_pad + tt0 + lane];
+                seen = 0u;
+                const int p = c.rb * RB + g * HR + lane;
+                if (lane < HR && p < A.M) {
+                    const int rr = p / A.G;
+                    const uint8_t fl = A.row_flags[(size_t)seg_b * A.R + rr];
+                    if (fl & SPEC_ROW_VALID) {
+                        const int ns = A.n_soft - tt0;          // soft tokens from here on
+                        if (ns > 0 && (fl & SPEC_ROW_SEES_SOFT))
+                            seen |= ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
+                        // block columns c0 .. c0 + 31
+                        const int c0 = tt0 - A.n_soft;
+                        const uint32_t *vr = A.vis + ((size_t)seg_b * A.R + rr) * A.W;
+                        auto word = [&](int w) {
+                            if (w < 0 || w >= A.W) return 0u;
+                            const int left = A.R - w * 32;      // columns from the word's first
+                            return left >= 32 ? vr[w] : vr[w] & ((1u << left) - 1u);
+                        };
+                        const int w0 = c0 >> 5, sft = c0 & 31;  // (floor)
+                        uint32_t x = word(w0) >> sft;
+                        if (sft) x |= word(w0 + 1) << (32 - sft);
+                        seen |= x;
+                    }
+                }
+            }
+            if (ok) ok = mbar_wait_warp(&sh.s_full[k & 1], (uint32_t)((k >> 1) & 1), T.wait);
+            // the slots' own barriers: the scales, and the rows cleared below
+            for (int part = 0; part < parts; ++part) {
+                if (ok) ok = mbar_wait_warp(&sh.full[slot], (uint32_t)((used / NS) & 1), T.wait);
+                ++used;
+                slot = slot + 1 == NS ? 0 : slot + 1;
+            }
+            float v[HR], y[HR];
+            float lsv = 0.f, isv = 1.f;
+            bool v_nan = false, trig = false;
+            if (ok) {
+                fence_after();
+                if (!s.tail && here) {
+                    sc = sh.scale[slot0][tok / P.box_tokens];
+                    sc.x = kv8_read_scale(sc.x);
+                    sc.y = kv8_read_scale(sc.y);
+                }
+                v_nan = sc.y != sc.y;
+                if (v_nan) sc.y = 1.f;
+                lsv = log2f(sc.y);
+                isv = 1.f / sc.y;
+                uint32_t hi[HR], lo[HR];
+                const uint32_t ts = tmem + lane_base + C::kColS * (1 + (uint32_t)(k & 1)) + (uint32_t)(g * HR);
+                ldn<HR>(ts, hi);
+                ldn<HR>(ts + RB, lo);
+                wait_ldn<HR>(hi, lo);
+#pragma unroll
+                for (int i = 0; i < HR; ++i)
+                    v[i] = (__uint_as_float(hi[i]) + __uint_as_float(lo[i])) * sc.x;
+            }
+            auto visible = [&](int i) {           // (every lane takes part)
+                const uint32_t row = __shfl_sync(0xffffffffu, seen, i);
+                return here && ((row >> lane) & 1u);
+            };
+            // y = log2 P, -inf for what a row does not see
+            auto exponents = [&] {
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < HR; ++i) {
+                    const float2 rc = sh.row[g][i];
+                    y[i] = fmaf(v[i], rc.x, lsv - rc.y);
+                    if (s.tail) y[i] = visible(i) ? y[i] : -INFINITY;
+                }
+                if (!here) {
+#pragma unroll
+                    for (int i = 0; i < HR; ++i) y[i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < HR; ++i) top = fmaxf(top, y[i]);
+                return top;
+            };
+            if (ok) trig = exponents() > kTop;
+            if (group_or(bar, trig || !ok)) {
+                if (group_or(bar, !ok)) {
+                    ok = false;
+                    break;
+                }
+                // raise M of the rows whose maximum grew
+                int mine = order_of(-INFINITY);
+#pragma unroll
+                for (int i = 0; i < HR; ++i) {
+                    const float x = y[i] == -INFINITY ? -INFINITY : fmaf(v[i], sh.row[g][i].x, lsv);
+                    const int m = __reduce_max_sync(0xffffffffu, order_of(x));
+                    if (lane == i) mine = m;
+                }
+                if (lane < HR) sh.rmax[g][wq][lane] = mine;
+                group_sync(bar);
+                if (gi < HR) {
+                    const float m = of_order(max(max(sh.rmax[g][0][gi], sh.rmax[g][1][gi]),
+                                                 max(sh.rmax[g][2][gi], sh.rmax[g][3][gi])));
+                    const float was = sh.row[g][gi].y, now = fmaxf(was, m - kAim);
+                    sh.fac[g][gi] = was == now ? 1.f : exp2f(was - now);
+                    sh.row[g][gi].y = now;
+                }
+                group_sync(bar);
+#pragma unroll
+                for (int i = 0; i < HR; ++i) l[i] *= sh.fac[g][i];
+                if (!new_unit) {
+                    ok = mbar_wait_warp(&sh.o_upd[(k - 1) & 1], (uint32_t)(((k - 1) >> 1) & 1), T.wait);
+                    if (ok) {
+                        fence_after();
+                        uint32_t hi[HR], lo[HR];
+                        const uint32_t to = tmem + lane_base + (uint32_t)(g * RB);
+                        ldn<HR>(to, hi);
+                        ldn<HR>(to + HR, lo);
+                        wait_ldn<HR>(hi, lo);
+#pragma unroll
+                        for (int i = 0; i < HR; ++i) {
+                            const float f = sh.fac[g][i];
+                            hi[i] = __float_as_uint(__uint_as_float(hi[i]) * f);
+                            lo[i] = __float_as_uint(__uint_as_float(lo[i]) * f);
+                        }
+                        stn<HR>(to, hi);
+                        stn<HR>(to + HR, lo);
+                        wait_st();
+                    }
+                }
+                exponents();
+            }
+#pragma unroll
+            for (int i = 0; i < HR; ++i) {
+                y[i] = fast_exp2(y[i]);
+                l[i] = fmaf(y[i], isv, l[i]);
+            }
+            if (__any_sync(0xffffffffu, v_nan)) {
+#pragma unroll
+                for (int i = 0; i < HR; ++i) {
+                    const bool sees = s.tail ? visible(i) : here;
+                    if (v_nan && sees) y[i] = __uint_as_float(0x7fffffffu);
+                }
+            }
+            // P(k) into buffer k % 2, once PV(k - 2) has read it
+            if (ok && k >= 2)
+                ok = mbar_wait_warp(&sh.o_upd[k & 1], (uint32_t)(((k - 2) >> 1) & 1), T.wait);
+            if (ok) {
+                uint8_t *prow = pbuf + (int)(k & 1) * C::kP + tok * 128;
+                uint32_t w[RB / 4];                 // first parts, then second parts
+#pragma unroll
+                for (int i = 0; i < HR; i += 4) {
+                    uint32_t h0, l0, h1, l1;
+                    split_p(y[i], y[i + 1], h0, l0);
+                    split_p(y[i + 2], y[i + 3], h1, l1);
+                    w[i / 4] = h0 | (h1 << 16);
+                    w[HR / 4 + i / 4] = l0 | (l1 << 16);
+                }
+                if constexpr (RB == 8) {
+                    *reinterpret_cast<uint2 *>(prow + ((tok & 7) << 4) + g * 8) = make_uint2(w[0], w[1]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < RB / 16; ++q)
+                        *reinterpret_cast<uint4 *>(prow + (((g * (RB / 16) + q) ^ (tok & 7)) << 4)) =
+                            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                }
+                // V rows past the last token hold whatever the copy left: P is
+                // 0 there, but 0 x NaN is NaN
+                if (!here && g == 0) {
+                    int sl = slot0;
+                    for (int part = 0; part < parts; ++part) {
+                        uint4 *vr = reinterpret_cast<uint4 *>(ring + sl * C::kSlot + kv8_row(tok, 1, D));
+#pragma unroll
+                        for (int e = 0; e < D / 16; ++e) vr[e] = make_uint4(0u, 0u, 0u, 0u);
+                        sl = sl + 1 == NS ? 0 : sl + 1;
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[k & 1]);
+            }
+            cursor_next(T, c);
+        }
+        // (a warpgroup leaves the loop together or runs it to its end)
+        if (k > 0 && (ok || t_begin + k == t_end) && !epilogue(k - 1)) ok = false;
+        if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == kMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(C::kCols));
+}
+
+// Merge of the units split between CTAs: block (i, rows) takes four rows, a
+// warp each, of the unit whose first boundary lies between CTAs i and i + 1.
+template <int D>
+__global__ void __launch_bounds__(128) attn_kv8_tc_combine_kernel(const __grid_constant__ TcParams T) {
+    pdl_wait();
+    const AttnParams &A = T.a;
+    const BoundaryRec rec = T.recs[blockIdx.x + 1];
+    if (rec.seg < 0) return;
+    const int rb = rec.seg % T.seg_rb, h = (rec.seg / T.seg_rb) % T.seg_h;
+    const int b = rec.seg / (T.seg_rb * T.seg_h);
+    const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const int p = rb * A.rb_rows + r;
+    if (p >= A.M) return;
+    auto has_part = [&](int i) {
+        if (rec.last - rec.first < 32) return ((rec.parts >> (i - rec.first)) & 1u) != 0;
+        return max(T.bounds[i], rec.s0) < min(T.bounds[i + 1], rec.s1);
+    };
+    // lane i: part first + i, first + i + 32, ...
+    float m = kNoRef;
+    for (int i = rec.first + lane; i <= rec.last; i += 32)
+        if (has_part(i)) m = fmaxf(m, A.part_ml[slot_row(T, rec.seg, i, 0, 1, r) * 2]);
+    m = warp_max(m);
+    constexpr int E = D / 32;
+    float out[E], L = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = 0.f;
+    for (int i0 = rec.first; i0 <= rec.last; i0 += 32) {
+        const int i = i0 + lane;
+        float w = 0.f;
+        const bool part = i <= rec.last && has_part(i);
+        if (part) {
+            const size_t row = slot_row(T, rec.seg, i, 0, 1, r);
+            w = exp2f(A.part_ml[row * 2] - m);
+            L = fmaf(w, A.part_ml[row * 2 + 1], L);
+        }
+        unsigned todo = __ballot_sync(0xffffffffu, part);
+        while (todo) {
+            // four parts' rows in flight
+            float x[4][E], wj[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = todo ? __ffs(todo) - 1 : -1;
+                if (todo) todo &= todo - 1;
+                wj[u] = j >= 0 ? __shfl_sync(0xffffffffu, w, j) : 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    x[u][e] = j >= 0 ? A.part_o[slot_row(T, rec.seg, i0 + j, 0, 1, r) * D + lane + 32 * e]
+                                     : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < E; ++e) out[e] = fmaf(wj[u], x[u][e], out[e]);
+        }
+    }
+    L = warp_sum(L);
+    const int rr = p / A.G, hq = h * A.G + p % A.G;
+    const bool valid = (A.row_flags[(size_t)b * A.R + rr] & SPEC_ROW_VALID) != 0;
+    const bool none = !valid || L == 0.f;
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(A.o) + (((size_t)b * A.R + rr) * A.Hq + hq) * D;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[lane + 32 * e] = __float2bfloat16_rn(none ? 0.f : out[e] / L);
+    if (lane == 0)
+        A.lse[((size_t)b * A.Hq + hq) * A.R + rr] = none ? -INFINITY : (m + log2f(L)) * kLn2;
+}
+
+// ------------------------------------------------------------ preparation
+
+struct Prep8Params {
+    AttnParams a;
+    uint8_t *q8;             // [units][2][RB][D]
+    float *q_scale;          // [units][RB]
+    uint8_t *tail8;          // [B][Hkv][2][tail_pad / 8][2][8][D]
+    float2 *tail_scale;      // [B][Hkv][tail_pad]
+    int rb, seg_rb, tail_pad;
+    long long q_rows, t_rows;
+};
+
+// A row of D bf16 values (lane: D / 32 of them) as two e4m3 rows under one
+// power-of-two scale, which is returned (NaN for a row that is not finite,
+// whose codes are 0).
+template <int D>
+__device__ float split_row(const __nv_bfloat16 *src, uint8_t *hi, uint8_t *lo, bool zero_is_small) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    float x[E];
+    uint32_t amax = 0;
+    if (src) {
+        if constexpr (E == 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(src + lane * 4);
+            x[0] = __uint_as_float(v.x << 16);
+            x[1] = __uint_as_float(v.x & 0xffff0000u);
+            x[2] = __uint_as_float(v.y << 16);
+            x[3] = __uint_as_float(v.y & 0xffff0000u);
+        } else {
+            const uint32_t v = *reinterpret_cast<const uint32_t *>(src + lane * 2);
+            x[0] = __uint_as_float(v << 16);
+            x[1] = __uint_as_float(v & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    const bool bad = amax >= 0x7f800000u;
+    // 2^e: the largest value lies in (224, 448] of it
+    const int e = min(max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -110), 119);
+    const float r = exp2_int(-e);
+    uint32_t h = 0u, w = 0u;
+    if (!bad) {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const float a = x[i] * r, c = x[i + 1] * r;
+            const uint32_t p = e4m3x2(a, c);
+            const float2 f = from_e4m3x2(p);
+            h |= p << (8 * i);
+            w |= e4m3x2(a - f.x, c - f.y) << (8 * i);
+        }
+    }
+    if constexpr (E == 4) {
+        *reinterpret_cast<uint32_t *>(hi + lane * 4) = h;
+        *reinterpret_cast<uint32_t *>(lo + lane * 4) = w;
+    } else {
+        *reinterpret_cast<uint16_t *>(hi + lane * 2) = (uint16_t)h;
+        *reinterpret_cast<uint16_t *>(lo + lane * 2) = (uint16_t)w;
+    }
+    if (bad) return __uint_as_float(0x7fffffffu);
+    // (a value row of zeros must not raise its readers' references)
+    return amax == 0 && zero_is_small ? exp2_int(kKv8MinExp) : exp2_int(e);
+}
+
+// One warp a row: the query rows of every unit, then the tail's keys and
+// values (a token's two rows, soft prompt first, by one warp).
+template <int D>
+__global__ void __launch_bounds__(256) attn_kv8_prep_kernel(const __grid_constant__ Prep8Params P) {
+    pdl_wait();
+    const AttnParams &A = P.a;
+    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < A.B; b += 256) check_seq_len(A, b);
+    if (w < P.q_rows) {
+        const int r = (int)(w % P.rb);
+        const long long u = w / P.rb;
+        const int rb = (int)(u % P.seg_rb), h = (int)((u / P.seg_rb) % A.Hkv);
+        const int b = (int)(u / ((long long)P.seg_rb * A.Hkv)), p = rb * P.rb + r;
+        const __nv_bfloat16 *src = nullptr;
+        if (p < A.M)
+            src = static_cast<const __nv_bfloat16 *>(A.q) +
+                  (((size_t)b * A.R + p / A.G) * A.Hq + h * A.G + p % A.G) * D;
+        uint8_t *dst = P.q8 + ((size_t)u * 2 * P.rb + r) * D;
+        const float s = split_row<D>(src, dst, dst + (size_t)P.rb * D, false);
+        if (lane == 0) P.q_scale[w] = s * A.scale_log2;
+        return;
+    }
+    const long long t = w - P.q_rows;
+    if (t >= P.t_rows) return;
+    const int tt = (int)(t % P.tail_pad);
+    const long long bh = t / P.tail_pad;
+    const int h = (int)(bh % A.Hkv);
+    const __nv_bfloat16 *k = nullptr, *v = nullptr;
+    if (tt < A.n_soft) {
+        const size_t at = ((size_t)h * A.n_soft + tt) * D;
+        k = static_cast<const __nv_bfloat16 *>(A.soft_k) + at;
+        v = static_cast<const __nv_bfloat16 *>(A.soft_v) + at;
+    } else if (tt - A.n_soft < A.R) {
+        const size_t at = ((size_t)bh * A.R + tt - A.n_soft) * D;
+        k = static_cast<const __nv_bfloat16 *>(A.kb) + at;
+        v = static_cast<const __nv_bfloat16 *>(A.vb) + at;
+    }
+    uint8_t *hi = P.tail8 + (size_t)bh * 2 * (2 * P.tail_pad * D);
+    uint8_t *lo = hi + (size_t)2 * P.tail_pad * D;
+    const int ko = kv8_row(tt, 0, D), vo = kv8_row(tt, 1, D);
+    const float sk = split_row<D>(k, hi + ko, lo + ko, false);
+    const float sv_ = split_row<D>(v, hi + vo, lo + vo, true);
+    if (lane == 0) P.tail_scale[t] = make_float2(sk, sv_);
+}
+
+// ------------------------------------------------------------------ host
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Offsets of the workspace's parts.
+struct Ws8 {
+    size_t o, ml, bounds, recs, q8, q_scale, tail8, tail_scale, bytes;
+    int n_ctas, rb, seg_rb, tail_pad;
+    long long units;
+};
+
+Ws8 plan_ws(const AttnParams &A) {
+    Ws8 w{};
+    w.n_ctas = num_sms();
+    w.rb = kv8_tc_rows(A);
+    w.seg_rb = ceil_div(A.M, w.rb);
+    w.units = (long long)A.B * A.Hkv * w.seg_rb;
+    w.tail_pad = ceil_div(A.n_soft + A.R, 16) * 16;
+    const size_t rows = ((size_t)w.units + w.n_ctas) * w.rb;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += up256(bytes);
+        return o;
+    };
+    w.o = take(rows * A.d * sizeof(float));
+    w.ml = take(rows * 2 * sizeof(float));
+    w.bounds = take(((size_t)w.n_ctas + 1) * sizeof(long long));
+    w.recs = take((size_t)w.n_ctas * sizeof(BoundaryRec));
+    w.q8 = take((size_t)w.units * 2 * w.rb * A.d);
+    w.q_scale = take((size_t)w.units * w.rb * sizeof(float));
+    w.tail8 = take((size_t)A.B * A.Hkv * 4 * w.tail_pad * A.d);
+    w.tail_scale = take((size_t)A.B * A.Hkv * w.tail_pad * sizeof(float2));
+    w.bytes = at;
+    return w;
+}
+
+template <int D, int RB>
+spec_status_t launch_units(const Tc8Params &P, const CUtensorMap *m, cudaStream_t s) {
+    const spec_status_t st =
+        set_smem_limit(reinterpret_cast<const void *>(attn_kv8_tc_kernel<D, RB>), smem8<D, RB>());
+    if (st != SPEC_OK) return st;
+    return launch(attn_kv8_tc_kernel<D, RB>, dim3(P.t.n_ctas), dim3(kTcThreads), smem8<D, RB>(), s, P,
+                  m[0], m[1], m[2]);
+}
+
+template <int D>
+spec_status_t launch_rows(const Tc8Params &P, const Prep8Params &R, const CUtensorMap *m, int rb,
+                          cudaStream_t s) {
+    const long long prep = R.q_rows + R.t_rows;
+    spec_status_t st = launch(attn_kv8_prep_kernel<D>, dim3((unsigned)ceil_div_ll(prep, 8)), dim3(256),
+                              0, s, R);
+    if (st != SPEC_OK) return st;
+    st = rb == 8    ? launch_units<D, 8>(P, m, s)
+         : rb == 16 ? launch_units<D, 16>(P, m, s)
+         : rb == 32 ? launch_units<D, 32>(P, m, s)
+                    : launch_units<D, 64>(P, m, s);
+    if (st != SPEC_OK) return st;
+    if (P.t.n_ctas > 1)
+        st = launch(attn_kv8_tc_combine_kernel<D>, dim3(P.t.n_ctas - 1, ceil_div(rb, 4)), dim3(128), 0,
+                    s, P.t);
+    return st != SPEC_OK ? st : launch_status();
+}
+
+}  // namespace
+
+// Packed rows per unit: the fewest of 8, 16, 32 and 64 that hold a KV head's
+// rows (a step's MMAs and softmax grow with them), 64-row blocks beyond.
+int kv8_tc_rows(const AttnParams &P) { return P.M <= 8 ? 8 : P.M <= 16 ? 16 : P.M <= 32 ? 32 : 64; }
+
+// TMA coordinates and unit numbers are 32-bit.
+bool kv8_tc_supported(const AttnParams &P, int dtype) {
+    if (dtype != SPEC_BF16) return false;
+    const Ws8 w = plan_ws(P);
+    return w.units * 2 * w.rb < (1ll << 31) &&
+           (long long)P.B * P.Hkv * 4 * w.tail_pad < (1ll << 31) && (long long)P.R * P.Hq < (1ll << 30);
+}
+
+size_t kv8_tc_workspace_bytes(const AttnParams &P) { return plan_ws(P).bytes; }
+
+spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s) {
+    const Ws8 w = plan_ws(Q.a);
+    char *base = reinterpret_cast<char *>(Q.a.part_o);
+    Tc8Params P{};
+    TcParams &T = P.t;
+    T.a = Q.a;
+    T.a.rb_rows = w.rb;
+    T.a.n_rb = w.seg_rb;
+    T.a.part_ml = reinterpret_cast<float *>(base + w.ml);
+    T.n_ctas = w.n_ctas;
+    T.bounds = reinterpret_cast<long long *>(base + w.bounds);
+    T.recs = reinterpret_cast<BoundaryRec *>(base + w.recs);
+    T.wait = wait_limit();
+    T.seg_h = Q.a.Hkv;
+    T.seg_rb = w.seg_rb;
+    T.seg_cost = 2;
+    T.pair_steps = 1;                       // a step: two of the schedule's 64-token tiles
+    P.scales = Q.scales;
+    P.q_scale = reinterpret_cast<const float *>(base + w.q_scale);
+    P.tail_scale = reinterpret_cast<const float2 *>(base + w.tail_scale);
+    P.tail_len = Q.a.n_soft + Q.a.R;
+    P.tail_pad = w.tail_pad;
+    P.n_tail = ceil_div(P.tail_len, kStep);
+    T.tail = 2 * P.n_tail;
+    P.box_tokens = 16;
+    while (P.box_tokens < kStep && Q.a.page_size % (2 * P.box_tokens) == 0) P.box_tokens *= 2;
+    Prep8Params R{};
+    R.a = Q.a;
+    R.q8 = reinterpret_cast<uint8_t *>(base + w.q8);
+    R.q_scale = reinterpret_cast<float *>(base + w.q_scale);
+    R.tail8 = reinterpret_cast<uint8_t *>(base + w.tail8);
+    R.tail_scale = reinterpret_cast<float2 *>(base + w.tail_scale);
+    R.rb = w.rb;
+    R.seg_rb = w.seg_rb;
+    R.tail_pad = w.tail_pad;
+    R.q_rows = w.units * w.rb;
+    R.t_rows = (long long)Q.a.B * Q.a.Hkv * w.tail_pad;
+
+    const int D = Q.a.d, ps = Q.a.page_size;
+    CUtensorMap m[3];
+    // the cache as [page x head][rows: 8 keys, 8 values, ...][D]
+    const cuuint64_t d0[3] = {(cuuint64_t)D, (cuuint64_t)2 * ps, (cuuint64_t)Q.a.n_pages * Q.a.Hkv};
+    const cuuint64_t s0[2] = {(cuuint64_t)D, (cuuint64_t)2 * ps * D};
+    const cuuint32_t b0[3] = {(cuuint32_t)D, (cuuint32_t)(2 * P.box_tokens), 1u};
+    const cuuint64_t s1[1] = {(cuuint64_t)D};
+    const cuuint64_t d1[2] = {(cuuint64_t)D, (cuuint64_t)Q.a.B * Q.a.Hkv * 4 * w.tail_pad};
+    const cuuint32_t b1[2] = {(cuuint32_t)D, 32u};
+    const cuuint64_t d2[2] = {(cuuint64_t)D, (cuuint64_t)w.units * 2 * w.rb};
+    const cuuint32_t b2[2] = {(cuuint32_t)D, (cuuint32_t)(2 * w.rb)};
+    if (!encode_u8_map(&m[0], Q.a.kc, 3, d0, s0, b0) || !encode_u8_map(&m[1], R.tail8, 2, d1, s1, b1) ||
+        !encode_u8_map(&m[2], R.q8, 2, d2, s1, b2))
+        return SPEC_ERR_CUDA;
+    return D == 128 ? launch_rows<128>(P, R, m, w.rb, s) : launch_rows<64>(P, R, m, w.rb, s);
+}
+
+}  // namespace sv

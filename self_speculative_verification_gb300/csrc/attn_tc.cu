@@ -1855,11 +1855,11 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 namespace {
 
-// Arguments of one bf16 map encoding; zero-filled so that keys compare
-// bytewise.
+// Arguments of one map encoding; zero-filled so that keys compare bytewise.
 struct MapKey {
     const void *base;
     int rank;
+    int bytes;               // elements are bytes, else bf16
     cuuint64_t dims[5];
     cuuint64_t strides[4];
     cuuint32_t box[5];
@@ -1871,15 +1871,14 @@ MapKey g_map_keys[kMapCache];
 CUtensorMap g_map_vals[kMapCache];
 int g_map_used = 0, g_map_next = 0;
 
-}  // namespace
-
-bool encode_bf16_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
-                     const cuuint64_t *strides, const cuuint32_t *box) {
+bool encode_map(CUtensorMap *map, bool bytes, const void *base, int rank, const cuuint64_t *dims,
+                const cuuint64_t *strides, const cuuint32_t *box) {
     if (rank < 1 || rank > 5) return false;
     MapKey key;
     memset(&key, 0, sizeof(key));
     key.base = base;
     key.rank = rank;
+    key.bytes = bytes;
     for (int i = 0; i < rank; ++i) {
         key.dims[i] = dims[i];
         key.box[i] = box[i];
@@ -1896,8 +1895,11 @@ bool encode_bf16_map(CUtensorMap *map, const void *base, int rank, const cuuint6
     auto fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
-    if (fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base),
-           dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const CUtensorMapSwizzle swizzle =
+        bytes && box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+           (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;
     std::lock_guard<std::mutex> lk(g_map_mu);
@@ -1906,4 +1908,17 @@ bool encode_bf16_map(CUtensorMap *map, const void *base, int rank, const cuuint6
     g_map_vals[slot] = *map;
     return true;
 }
+
+}  // namespace
+
+bool encode_bf16_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+                     const cuuint64_t *strides, const cuuint32_t *box) {
+    return encode_map(map, false, base, rank, dims, strides, box);
+}
+
+bool encode_u8_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+                   const cuuint64_t *strides, const cuuint32_t *box) {
+    return encode_map(map, true, base, rank, dims, strides, box);
+}
+
 }  // namespace sv

@@ -96,6 +96,15 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 __device__ __forceinline__ uint64_t policy_evict_first() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -168,6 +177,9 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // false if the driver rejects the arguments.
 bool encode_bf16_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
                      const cuuint64_t *strides, const cuuint32_t *box);
+// The same for bytes, swizzled over rows of box[0] = 64 or 128 bytes.
+bool encode_u8_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+                   const cuuint64_t *strides, const cuuint32_t *box);
 
 // ------------------------------------------------------------- tcgen05
 namespace tc5 {
@@ -182,6 +194,14 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
     d |= (uint64_t)1 << 46;             // descriptor version of the sm_100 family
     d |= (uint64_t)2 << 61;             // 128-byte swizzle
     return d;
+}
+
+// The same for a tile swizzled over rows of ROW = 64 or 128 bytes.
+template <int ROW>
+__device__ __forceinline__ uint64_t smem_desc_sw(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    static_assert(ROW == 64 || ROW == 128, "swizzle span");
+    const uint64_t d = smem_desc(addr, lbo, sbo);
+    return ROW == 128 ? d : (d & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);   // 64-byte swizzle
 }
 
 // bf16 x bf16 -> fp32, M x N; a_mn / b_mn: operand stored MN-major.
@@ -205,6 +225,20 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, 
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(id), "r"(accumulate));
+}
+
+// e4m3 x e4m3 -> fp32, M x N (K = 32 an instruction)
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma8_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a), "l"(b), "r"(id), "r"(accumulate));
 }
 
@@ -256,6 +290,71 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31]));
 }
+
+// N columns of this warp's lanes (N = 4, 8, 16 or 32), loaded and waited for.
+#define SV_R4(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
+#define SV_O4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
+#define SV_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
+template <int N>
+__device__ __forceinline__ void ldn(uint32_t taddr, uint32_t (&r)[N]) {
+    static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
+    if constexpr (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : SV_O4(r, 0)
+                     : "r"(taddr));
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : SV_O4(r, 0), SV_O4(r, 4)
+                     : "r"(taddr));
+    else if constexpr (N == 16)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+            "%14,%15}, [%16];"
+            : SV_O4(r, 0), SV_O4(r, 4), SV_O4(r, 8), SV_O4(r, 12)
+            : "r"(taddr));
+    else
+        ld32(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void stn(uint32_t taddr, const uint32_t (&r)[N]) {
+    static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
+    if constexpr (N == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+                     SV_I4(r, 0));
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                         taddr),
+                     SV_I4(r, 0), SV_I4(r, 4));
+    else if constexpr (N == 16)
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+            "%13,%14,%15,%16};" ::"r"(taddr),
+            SV_I4(r, 0), SV_I4(r, 4), SV_I4(r, 8), SV_I4(r, 12));
+    else
+        st32(taddr, r);
+}
+// tcgen05.wait::ld that ties two loads' registers to the wait.
+template <int N>
+__device__ __forceinline__ void wait_ldn(uint32_t (&a)[N], uint32_t (&b)[N]) {
+    if constexpr (N == 4)
+        asm volatile("tcgen05.wait::ld.sync.aligned;" : SV_R4(a, 0), SV_R4(b, 0)::"memory");
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : SV_R4(a, 0), SV_R4(a, 4), SV_R4(b, 0), SV_R4(b, 4)::"memory");
+    else if constexpr (N == 16)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : SV_R4(a, 0), SV_R4(a, 4), SV_R4(a, 8), SV_R4(a, 12), SV_R4(b, 0),
+                       SV_R4(b, 4), SV_R4(b, 8), SV_R4(b, 12)::"memory");
+    else
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : SV_R4(a, 0), SV_R4(a, 4), SV_R4(a, 8), SV_R4(a, 12), SV_R4(a, 16),
+                       SV_R4(a, 20), SV_R4(a, 24), SV_R4(a, 28), SV_R4(b, 0), SV_R4(b, 4),
+                       SV_R4(b, 8), SV_R4(b, 12), SV_R4(b, 16), SV_R4(b, 20), SV_R4(b, 24),
+                       SV_R4(b, 28)::"memory");
+}
+#undef SV_R4
+#undef SV_O4
+#undef SV_I4
 
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 

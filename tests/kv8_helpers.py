@@ -152,14 +152,19 @@ class Attn:
         of 2^-24 each, ds = 2^-17 max|q| sum|k| scale at most.  Each moves p
         by a factor within e^(2 ds) and LSE by ds.  P (bf16 rows) is the sum
         of two e4m3 values as well: 2^-8 of it, or 2^-14 of the largest p
-        where it is far below that; block values 2^-8 likewise.  The output's
-        own rounding is 2^-8 (bf16) or 2^-24 (fp32) of it."""
+        where it is far below that.  A block or soft-prompt value (bf16 rows)
+        is one like a query: off by at most 2^-10 / 224 = 2^-17.8 of the
+        largest of its row, which the row's weights, whose sum is 1, pass on
+        at most whole.  The output's own rounding is 2^-8 (bf16) or 2^-24
+        (fp32) of it."""
         B, R, Hq, Hkv, d = self.shape
         scale = self.scale or 1 / math.sqrt(d)
         big = np.abs(self.q).max() * self.k_abs * scale
         if self.dtype == "bf16":
             ds = 2.0 ** -16.8 * big
-            return (2.0 ** -8 * np.abs(O) + (2.0 ** -7 + 2 * ds) * A + 1e-7, ds + 1e-5)
+            v = max([np.abs(self.vb).max()] + ([np.abs(self.soft_v).max()] if self.n_soft else []))
+            return (2.0 ** -8 * np.abs(O) + (2.0 ** -7 + 2 * ds) * A + 2.0 ** -17.8 * v + 1e-7,
+                    ds + 1e-5)
         ds = 2.0 ** -17 * big
         return 2.0 ** -22 * np.abs(O) + (2 * ds + 2.0 ** -18) * A + 1e-9, ds + 2e-6
 
@@ -174,7 +179,8 @@ class Attn:
         to, tl = self.tolerance(O, A)
         assert np.isfinite(got).all()
         over = np.abs(got - O) / to
-        assert over.max() <= 1, f"O off by {over.max()} of its bound at {np.unravel_index(over.argmax(), O.shape)}"
+        at = np.unravel_index(over.argmax(), O.shape)
+        assert over.max() <= 1, f"O {got[at]} for {O[at]} at {at}: {over.max()} of its bound"
         fin = np.isfinite(L)
         assert np.array_equal(np.isneginf(lse), ~fin)
         if fin.any():
