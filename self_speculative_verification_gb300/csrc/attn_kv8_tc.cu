@@ -59,11 +59,12 @@ constexpr float kLoUp = 16.f;               // factor of P's second part
 struct Tc8Params {
     TcParams t;              // schedule, split, partials (t.a: the call)
     const float *scales;     // the cache's
-    const float *q_scale;    // [units][RB]: softmax scale (log2) x the row's power of two
+    const float2 *q_meta;    // [units][RB]: softmax scale (log2) x the row's power of two;
+                             // output row and whether it is valid (see Prep8Params)
     const float2 *tail_scale;    // [B][Hkv][tail_pad]: scales of the tail's tokens
     int tail_len, tail_pad;  // n_soft + R, rounded up to 16
     int n_tail;              // its 128-token tiles
-    int box_tokens;          // tokens per cache box
+    int box_log2;            // log2 of the tokens per cache box
 };
 
 template <int D, int RB>
@@ -84,9 +85,10 @@ struct Shared8 {
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], o_upd[2];
     uint64_t drain;
-    float2 scale[C::NS][8];              // key / value scale of each box of a slot
-    float2 row[2][C::HR];                // a row's q_scale and M
-    float fac[2][C::HR];
+    float4 scale[C::NS][8];              // TokenScale of each box of a slot
+    alignas(16) float qs[2][C::HR];      // a row's q_scale
+    alignas(16) float neg_m[2][C::HR];   // and its -M
+    alignas(16) float fac[2][C::HR];     // slow path: what its sums are scaled by; end: 1 / l
     int rmax[2][4][C::HR];
     float rsum[2][4][C::HR];
     int out[2][C::HR];                   // (row * Hq + head) * 2 + valid, or -1
@@ -124,6 +126,41 @@ __device__ __forceinline__ int order_of(float x) {
 }
 __device__ __forceinline__ float of_order(int i) {
     return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// What a token's thread needs of its two scales: (key scale, log2 of the value
+// scale, 1 / value scale, NaN if the value scale is NaN else 0).
+__device__ __forceinline__ float4 token_scale(float k, float v) {
+    const bool bad = v != v;
+    v = bad ? 1.f : v;
+    return make_float4(k, log2f(v), 1.f / v, bad ? __uint_as_float(0x7fffffffu) : 0.f);
+}
+
+// Sums over the warp of HR values a lane: lane i * (32 / HR) holds the i-th
+// (each round halves the values a lane carries).
+template <int HR>
+__device__ __forceinline__ float warp_sums(const float (&x)[HR]) {
+    const int lane = threadIdx.x & 31;
+    float r[HR];
+#pragma unroll
+    for (int i = 0; i < HR; ++i) r[i] = x[i];
+    int n = HR;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int j = 0; j < HR / 2; ++j) {
+                if (j >= n) break;
+                const float send = up ? r[j] : r[j + n], keep = up ? r[j + n] : r[j];
+                r[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        } else {
+            r[0] += __shfl_xor_sync(0xffffffffu, r[0], o);
+        }
+    }
+    return r[0];
 }
 
 // Two values of P: the e4m3 pair nearest to them, and the pair nearest to 16
@@ -220,7 +257,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         // lane i owns box i of a step: box_tokens tokens (prefix) or 16 (tail)
         const uint64_t keep = policy_evict_last();
         const uint64_t stream = T.seg_rb == 1 ? policy_evict_first() : keep;
-        const int bt = P.box_tokens, boxes = kStep / bt;
+        const int bt = 1 << P.box_log2, boxes = kStep / bt;
         Cursor c;
         cursor_init(T, ws, t_begin, c);
         // this lane's page of the cursor's step: -1 no box, -2 a bad page
@@ -236,7 +273,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             return *reinterpret_cast<const float2 *>(P.scales + ((size_t)pg * A.Hkv + k.h) * 2);
         };
         int pg = page_of(c);
-        float2 sc = scale_of(c, pg);
+        float2 sc = scale_of(c, pg);         // a step ahead of its use
         int slot = 0, nq = 0;
         long long used = 0;                  // ring slots taken so far
         bool ok = true;
@@ -294,7 +331,8 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                         tma_load_3d(dst, &m_kv, 0, 2 * ((s.tile * kStep + lane * bt) % A.page_size),
                                     pg * A.Hkv + c.h, &sh.full[slot], stream);
                 }
-                if (!s.tail && lane < boxes) sh.scale[slot][lane] = sc;
+                if (!s.tail && lane < boxes)
+                    sh.scale[slot][lane] = token_scale(kv8_read_scale(sc.x), kv8_read_scale(sc.y));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.full[slot]);
                 ++used;
@@ -421,51 +459,57 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         // tokens' threads, then O / l and LSE, or the partials
         auto epilogue = [&](long long j) -> bool {
             const bool got = ok && mbar_wait_warp(&sh.o_upd[j & 1], (uint32_t)((j >> 1) & 1), T.wait);
-            float mine = 0.f;
-#pragma unroll
-            for (int i = 0; i < HR; ++i) {
-                const float s = warp_sum(l[i]);
-                if (lane == i) mine = s;
-            }
-            if (lane < HR) sh.rsum[g][wq][lane] = mine;
+            constexpr int kPer = 32 / HR;
+            const float sum = warp_sums<HR>(l);
+            if (lane % kPer == 0) sh.rsum[g][wq][lane / kPer] = sum;
             if (group_or(bar, !got)) return false;
             fence_after();
+            const size_t prow = slot_row(T, seg_id, cta, 0, 1, g * HR);
+            if (gi < HR) {
+                const float L = (sh.rsum[g][0][gi] + sh.rsum[g][1][gi]) +
+                                (sh.rsum[g][2][gi] + sh.rsum[g][3][gi]);
+                const float M = -sh.neg_m[g][gi];
+                const int out = sh.out[g][gi];
+                const bool none = !(out & 1) || L == 0.f;
+                sh.fac[g][gi] = none ? 0.f : 1.f / L;
+                if (seg_whole && out >= 0) {
+                    const int hq = (out >> 1) % A.Hq, rr = (out >> 1) / A.Hq;
+                    A.lse[((size_t)seg_b * A.Hq + hq) * A.R + rr] =
+                        none ? -INFINITY : (M + log2f(L)) * kLn2;
+                } else if (!seg_whole) {
+                    *reinterpret_cast<float2 *>(A.part_ml + (prow + gi) * 2) = make_float2(M, L);
+                }
+            }
+            group_sync(bar);
             uint32_t hi[HR], lo[HR];
             const uint32_t to = tmem + lane_base + (uint32_t)(g * RB);
             ldn<HR>(to, hi);
             ldn<HR>(to + HR, lo);
             wait_ldn<HR>(hi, lo);
-            const size_t prow = slot_row(T, seg_id, cta, 0, 1, g * HR);
-#pragma unroll
-            for (int i = 0; i < HR; ++i) {
-                const float L = (sh.rsum[g][0][i] + sh.rsum[g][1][i]) + (sh.rsum[g][2][i] + sh.rsum[g][3][i]);
-                const float o = fmaf(__uint_as_float(lo[i]), 1.f / kLoUp, __uint_as_float(hi[i]));
-                const int out = sh.out[g][i];
-                if (out < 0) continue;
-                const float M = sh.row[g][i].y;
+            if (tok < D) {
                 if (seg_whole) {
-                    const size_t r = (size_t)seg_b * A.R * A.Hq + (size_t)(out >> 1);
-                    const bool none = !(out & 1) || L == 0.f;
-                    if (tok < D)
-                        static_cast<__nv_bfloat16 *>(A.o)[r * D + tok] =
-                            __float2bfloat16_rn(none ? 0.f : o / L);
-                    if (gi == i) {
-                        const int hq = (out >> 1) % A.Hq, rr = (out >> 1) / A.Hq;
-                        A.lse[((size_t)seg_b * A.Hq + hq) * A.R + rr] =
-                            none ? -INFINITY : (M + log2f(L)) * kLn2;
+                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(A.o) + (size_t)seg_b * A.R * A.Hq * D + tok;
+#pragma unroll
+                    for (int i = 0; i < HR; ++i) {
+                        const int out = sh.out[g][i];
+                        if (out < 0) break;              // (rows past the last are at the end)
+                        const float inv = sh.fac[g][i];
+                        const float x = fmaf(__uint_as_float(lo[i]), 1.f / kLoUp, __uint_as_float(hi[i]));
+                        o[(size_t)(out >> 1) * D] = __float2bfloat16_rn(inv == 0.f ? 0.f : x * inv);
                     }
                 } else {
-                    if (tok < D) A.part_o[(prow + i) * D + tok] = o;
-                    if (gi == i) {
-                        A.part_ml[(prow + i) * 2] = M;
-                        A.part_ml[(prow + i) * 2 + 1] = L;
-                    }
+                    float *o = A.part_o + prow * D + tok;
+#pragma unroll
+                    for (int i = 0; i < HR; ++i)
+                        o[i * D] = fmaf(__uint_as_float(lo[i]), 1.f / kLoUp, __uint_as_float(hi[i]));
                 }
             }
             fence_before();
             return true;
         };
 
+        float2 meta = make_float2(0.f, 0.f);     // the next unit's row gi, loaded ahead
+        if (gi < HR) meta = P.q_meta[(size_t)unit_of(c) * RB + g * HR + gi];
         for (long long t = t_begin; t < t_end; ++t, ++k) {
             const bool new_unit = k == 0 || c.tile == 0;
             if (new_unit) {
@@ -480,52 +524,45 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 seg_whole = seg_lo >= t_begin && seg_lo + c.n_tiles <= t_end;
                 group_sync(bar);               // the last unit's rows are read
                 if (gi < HR) {
-                    const int r = g * HR + gi, p = c.rb * RB + r;
-                    int out = -1;
-                    if (p < A.M) {
-                        const int rr = p / A.G;
-                        const int valid = A.row_flags[(size_t)c.b * A.R + rr] & SPEC_ROW_VALID;
-                        out = (rr * A.Hq + c.h * A.G + p % A.G) * 2 + (valid ? 1 : 0);
-                    }
-                    sh.out[g][gi] = out;
-                    sh.row[g][gi] = make_float2(P.q_scale[(size_t)seg_id * RB + r], kNoRef);
+                    sh.out[g][gi] = __float_as_int(meta.y);
+                    sh.qs[g][gi] = meta.x;
+                    sh.neg_m[g][gi] = -kNoRef;
                 }
                 group_sync(bar);
 #pragma unroll
                 for (int i = 0; i < HR; ++i) l[i] = 0.f;
             }
             const Step8 s = step_at(P, c);
+            cursor_next(T, c);
+            if (c.tile == 0 && t + 1 < t_end && gi < HR)
+                meta = P.q_meta[(size_t)unit_of(c) * RB + g * HR + gi];
             const int slot0 = slot, parts = s.tail ? 2 : 1;
             // rows' visibility of this warp's 32 tail tokens, lane i: row i
-            uint32_t seen = 0xffffffffu;
-            float2 sc = make_float2(1.f, 1.f);
+            uint32_t seen = 0u;
+            float4 sc = make_float4(0.f, 0.f, 1.f, 0.f);
             const bool here = tok < s.n;
             if (s.tail) {
                 const int tt0 = s.tile * kStep + wq * 32;
-                if (here)
-                    sc = P.tail_scale[((size_t)seg_b * A.Hkv + seg_h) * P.tail_pad + tt0 + lane];
-                seen = 0u;
-                const int p = c.rb * RB + g * HR + lane;
-                if (lane < HR && p < A.M) {
-                    const int rr = p / A.G;
-                    const uint8_t fl = A.row_flags[(size_t)seg_b * A.R + rr];
-                    if (fl & SPEC_ROW_VALID) {
-                        const int ns = A.n_soft - tt0;          // soft tokens from here on
-                        if (ns > 0 && (fl & SPEC_ROW_SEES_SOFT))
-                            seen |= ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
-                        // block columns c0 .. c0 + 31
-                        const int c0 = tt0 - A.n_soft;
-                        const uint32_t *vr = A.vis + ((size_t)seg_b * A.R + rr) * A.W;
-                        auto word = [&](int w) {
-                            if (w < 0 || w >= A.W) return 0u;
-                            const int left = A.R - w * 32;      // columns from the word's first
-                            return left >= 32 ? vr[w] : vr[w] & ((1u << left) - 1u);
-                        };
-                        const int w0 = c0 >> 5, sft = c0 & 31;  // (floor)
-                        uint32_t x = word(w0) >> sft;
-                        if (sft) x |= word(w0 + 1) << (32 - sft);
-                        seen |= x;
-                    }
+                if (here) {
+                    const float2 x = P.tail_scale[((size_t)seg_b * A.Hkv + seg_h) * P.tail_pad + tt0 + lane];
+                    sc = token_scale(x.x, x.y);
+                }
+                const int out = lane < HR ? sh.out[g][lane] : -1;
+                if (out >= 0 && (out & 1)) {
+                    const int rr = (out >> 1) / A.Hq;
+                    const uint32_t *vr = A.vis + ((size_t)seg_b * A.R + rr) * A.W;
+                    auto word = [&](int w) {
+                        if (w < 0 || w >= A.W) return 0u;
+                        const int left = A.R - w * 32;          // columns from the word's first
+                        return left >= 32 ? vr[w] : vr[w] & ((1u << left) - 1u);
+                    };
+                    // block columns c0 .. c0 + 31
+                    const int c0 = tt0 - A.n_soft, sft = c0 & 31, w0 = c0 >> 5;     // (floor)
+                    seen = word(w0) >> sft;
+                    if (sft) seen |= word(w0 + 1) << (32 - sft);
+                    const int ns = A.n_soft - tt0;              // soft tokens from here on
+                    if (ns > 0 && (A.row_flags[(size_t)seg_b * A.R + rr] & SPEC_ROW_SEES_SOFT))
+                        seen |= ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
                 }
             }
             if (ok) ok = mbar_wait_warp(&sh.s_full[k & 1], (uint32_t)((k >> 1) & 1), T.wait);
@@ -535,62 +572,67 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 ++used;
                 slot = slot + 1 == NS ? 0 : slot + 1;
             }
-            float v[HR], y[HR];
-            float lsv = 0.f, isv = 1.f;
-            bool v_nan = false, trig = false;
-            if (ok) {
-                fence_after();
-                if (!s.tail && here) {
-                    sc = sh.scale[slot0][tok / P.box_tokens];
-                    sc.x = kv8_read_scale(sc.x);
-                    sc.y = kv8_read_scale(sc.y);
-                }
-                v_nan = sc.y != sc.y;
-                if (v_nan) sc.y = 1.f;
-                lsv = log2f(sc.y);
-                isv = 1.f / sc.y;
+            const uint32_t ts = tmem + lane_base + C::kColS * (1 + (uint32_t)(k & 1)) + (uint32_t)(g * HR);
+            float y[HR];
+            // y = s x (key scale, softmax scale) + log2(value scale) [- M]: the
+            // exponents of P, from the two parts of S
+            auto exponents = [&](bool less_m) {
                 uint32_t hi[HR], lo[HR];
-                const uint32_t ts = tmem + lane_base + C::kColS * (1 + (uint32_t)(k & 1)) + (uint32_t)(g * HR);
                 ldn<HR>(ts, hi);
                 ldn<HR>(ts + RB, lo);
                 wait_ldn<HR>(hi, lo);
+                const uint64_t sk2 = pair(sc.x, sc.x), lv2 = pair(sc.y, sc.y);
 #pragma unroll
-                for (int i = 0; i < HR; ++i)
-                    v[i] = (__uint_as_float(hi[i]) + __uint_as_float(lo[i])) * sc.x;
-            }
-            auto visible = [&](int i) {           // (every lane takes part)
-                const uint32_t row = __shfl_sync(0xffffffffu, seen, i);
-                return here && ((row >> lane) & 1u);
-            };
-            // y = log2 P, -inf for what a row does not see
-            auto exponents = [&] {
-                float top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < HR; ++i) {
-                    const float2 rc = sh.row[g][i];
-                    y[i] = fmaf(v[i], rc.x, lsv - rc.y);
-                    if (s.tail) y[i] = visible(i) ? y[i] : -INFINITY;
+                for (int i = 0; i < HR; i += 4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(&sh.qs[g][i]);
+                    float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (less_m) m = *reinterpret_cast<const float4 *>(&sh.neg_m[g][i]);
+                    const uint64_t z0 = pair(0.f, 0.f);
+                    uint64_t r0 = fma2(add2(pair(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
+                                            pair(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1]))),
+                                       fma2(pair(q.x, q.y), sk2, z0), add2(pair(m.x, m.y), lv2));
+                    uint64_t r1 =
+                        fma2(add2(pair(__uint_as_float(hi[i + 2]), __uint_as_float(hi[i + 3])),
+                                  pair(__uint_as_float(lo[i + 2]), __uint_as_float(lo[i + 3]))),
+                             fma2(pair(q.z, q.w), sk2, z0), add2(pair(m.z, m.w), lv2));
+                    unpair(r0, y[i], y[i + 1]);
+                    unpair(r1, y[i + 2], y[i + 3]);
                 }
-                if (!here) {
+            };
+            // -inf for what a row does not see
+            auto mask = [&] {
+                if (s.tail) {
+#pragma unroll
+                    for (int i = 0; i < HR; ++i) {
+                        const uint32_t row = __shfl_sync(0xffffffffu, seen, i);
+                        y[i] = here && ((row >> lane) & 1u) ? y[i] : -INFINITY;
+                    }
+                } else if (!here) {
 #pragma unroll
                     for (int i = 0; i < HR; ++i) y[i] = -INFINITY;
                 }
-#pragma unroll
-                for (int i = 0; i < HR; ++i) top = fmaxf(top, y[i]);
-                return top;
             };
-            if (ok) trig = exponents() > kTop;
-            if (group_or(bar, trig || !ok)) {
+            float top = -INFINITY;
+            if (ok) {
+                fence_after();
+                if (!s.tail && here) sc = sh.scale[slot0][tok >> P.box_log2];
+                exponents(true);
+                mask();
+#pragma unroll
+                for (int i = 0; i < HR; i += 2) top = max3(top, y[i], y[i + 1]);
+            }
+            if (group_or(bar, top > kTop || !ok)) {
                 if (group_or(bar, !ok)) {
                     ok = false;
                     break;
                 }
                 // raise M of the rows whose maximum grew
+                exponents(false);
+                mask();
                 int mine = order_of(-INFINITY);
 #pragma unroll
                 for (int i = 0; i < HR; ++i) {
-                    const float x = y[i] == -INFINITY ? -INFINITY : fmaf(v[i], sh.row[g][i].x, lsv);
-                    const int m = __reduce_max_sync(0xffffffffu, order_of(x));
+                    const int m = __reduce_max_sync(0xffffffffu, order_of(y[i]));
                     if (lane == i) mine = m;
                 }
                 if (lane < HR) sh.rmax[g][wq][lane] = mine;
@@ -598,45 +640,50 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 if (gi < HR) {
                     const float m = of_order(max(max(sh.rmax[g][0][gi], sh.rmax[g][1][gi]),
                                                  max(sh.rmax[g][2][gi], sh.rmax[g][3][gi])));
-                    const float was = sh.row[g][gi].y, now = fmaxf(was, m - kAim);
+                    const float was = -sh.neg_m[g][gi], now = fmaxf(was, m - kAim);
                     sh.fac[g][gi] = was == now ? 1.f : exp2f(was - now);
-                    sh.row[g][gi].y = now;
+                    sh.neg_m[g][gi] = -now;
                 }
                 group_sync(bar);
 #pragma unroll
-                for (int i = 0; i < HR; ++i) l[i] *= sh.fac[g][i];
+                for (int i = 0; i < HR; ++i) {
+                    l[i] *= sh.fac[g][i];
+                    y[i] += sh.neg_m[g][i];
+                }
                 if (!new_unit) {
                     ok = mbar_wait_warp(&sh.o_upd[(k - 1) & 1], (uint32_t)(((k - 1) >> 1) & 1), T.wait);
                     if (ok) {
                         fence_after();
-                        uint32_t hi[HR], lo[HR];
                         const uint32_t to = tmem + lane_base + (uint32_t)(g * RB);
-                        ldn<HR>(to, hi);
-                        ldn<HR>(to + HR, lo);
-                        wait_ldn<HR>(hi, lo);
+#pragma unroll 1
+                        for (int e = 0; e < RB; e += HR) {       // first parts, second parts
+                            uint32_t x[HR];
+                            ldn<HR>(to + e, x);
+                            wait_ldn<HR>(x);
 #pragma unroll
-                        for (int i = 0; i < HR; ++i) {
-                            const float f = sh.fac[g][i];
-                            hi[i] = __float_as_uint(__uint_as_float(hi[i]) * f);
-                            lo[i] = __float_as_uint(__uint_as_float(lo[i]) * f);
+                            for (int i = 0; i < HR; ++i)
+                                x[i] = __float_as_uint(__uint_as_float(x[i]) * sh.fac[g][i]);
+                            stn<HR>(to + e, x);
                         }
-                        stn<HR>(to, hi);
-                        stn<HR>(to + HR, lo);
                         wait_st();
                     }
                 }
-                exponents();
             }
+            {
+                const uint64_t is2 = pair(sc.z, sc.z);
 #pragma unroll
-            for (int i = 0; i < HR; ++i) {
-                y[i] = fast_exp2(y[i]);
-                l[i] = fmaf(y[i], isv, l[i]);
+                for (int i = 0; i < HR; i += 2) {
+                    y[i] = fast_exp2(y[i]);
+                    y[i + 1] = fast_exp2(y[i + 1]);
+                    unpair(fma2(pair(y[i], y[i + 1]), is2, pair(l[i], l[i + 1])), l[i], l[i + 1]);
+                }
             }
-            if (__any_sync(0xffffffffu, v_nan)) {
+            if (__any_sync(0xffffffffu, sc.w != sc.w)) {
+                // a NaN value scale: NaN in the rows that see the token
 #pragma unroll
                 for (int i = 0; i < HR; ++i) {
-                    const bool sees = s.tail ? visible(i) : here;
-                    if (v_nan && sees) y[i] = __uint_as_float(0x7fffffffu);
+                    const uint32_t row = __shfl_sync(0xffffffffu, seen, i);
+                    if (here && (!s.tail || ((row >> lane) & 1u))) y[i] += sc.w;
                 }
             }
             // P(k) into buffer k % 2, once PV(k - 2) has read it
@@ -677,10 +724,9 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p_full[k & 1]);
             }
-            cursor_next(T, c);
         }
         // (a warpgroup leaves the loop together or runs it to its end)
-        if (k > 0 && (ok || t_begin + k == t_end) && !epilogue(k - 1)) ok = false;
+        if (k > 0 && t_begin + k == t_end && !epilogue(k - 1)) ok = false;
         if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
     }
     fence_before();
@@ -762,7 +808,7 @@ __global__ void __launch_bounds__(128) attn_kv8_tc_combine_kernel(const __grid_c
 struct Prep8Params {
     AttnParams a;
     uint8_t *q8;             // [units][2][RB][D]
-    float *q_scale;          // [units][RB]
+    float2 *q_meta;          // [units][RB]: scale; (row * Hq + head) * 2 + valid, -1 past the last
     uint8_t *tail8;          // [B][Hkv][2][tail_pad / 8][2][8][D]
     float2 *tail_scale;      // [B][Hkv][tail_pad]
     int rb, seg_rb, tail_pad;
@@ -840,12 +886,15 @@ __global__ void __launch_bounds__(256) attn_kv8_prep_kernel(const __grid_constan
         const int rb = (int)(u % P.seg_rb), h = (int)((u / P.seg_rb) % A.Hkv);
         const int b = (int)(u / ((long long)P.seg_rb * A.Hkv)), p = rb * P.rb + r;
         const __nv_bfloat16 *src = nullptr;
-        if (p < A.M)
-            src = static_cast<const __nv_bfloat16 *>(A.q) +
-                  (((size_t)b * A.R + p / A.G) * A.Hq + h * A.G + p % A.G) * D;
+        int out = -1;
+        if (p < A.M) {
+            const int rr = p / A.G, at = rr * A.Hq + h * A.G + p % A.G;
+            src = static_cast<const __nv_bfloat16 *>(A.q) + ((size_t)b * A.R * A.Hq + at) * D;
+            out = 2 * at + (A.row_flags[(size_t)b * A.R + rr] & SPEC_ROW_VALID ? 1 : 0);
+        }
         uint8_t *dst = P.q8 + ((size_t)u * 2 * P.rb + r) * D;
         const float s = split_row<D>(src, dst, dst + (size_t)P.rb * D, false);
-        if (lane == 0) P.q_scale[w] = s * A.scale_log2;
+        if (lane == 0) P.q_meta[w] = make_float2(s * A.scale_log2, __int_as_float(out));
         return;
     }
     const long long t = w - P.q_rows;
@@ -877,7 +926,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Offsets of the workspace's parts.
 struct Ws8 {
-    size_t o, ml, bounds, recs, q8, q_scale, tail8, tail_scale, bytes;
+    size_t o, ml, bounds, recs, q8, q_meta, tail8, tail_scale, bytes;
     int n_ctas, rb, seg_rb, tail_pad;
     long long units;
 };
@@ -901,7 +950,7 @@ Ws8 plan_ws(const AttnParams &A) {
     w.bounds = take(((size_t)w.n_ctas + 1) * sizeof(long long));
     w.recs = take((size_t)w.n_ctas * sizeof(BoundaryRec));
     w.q8 = take((size_t)w.units * 2 * w.rb * A.d);
-    w.q_scale = take((size_t)w.units * w.rb * sizeof(float));
+    w.q_meta = take((size_t)w.units * w.rb * sizeof(float2));
     w.tail8 = take((size_t)A.B * A.Hkv * 4 * w.tail_pad * A.d);
     w.tail_scale = take((size_t)A.B * A.Hkv * w.tail_pad * sizeof(float2));
     w.bytes = at;
@@ -969,18 +1018,18 @@ spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s) {
     T.seg_cost = 2;
     T.pair_steps = 1;                       // a step: two of the schedule's 64-token tiles
     P.scales = Q.scales;
-    P.q_scale = reinterpret_cast<const float *>(base + w.q_scale);
+    P.q_meta = reinterpret_cast<const float2 *>(base + w.q_meta);
     P.tail_scale = reinterpret_cast<const float2 *>(base + w.tail_scale);
     P.tail_len = Q.a.n_soft + Q.a.R;
     P.tail_pad = w.tail_pad;
     P.n_tail = ceil_div(P.tail_len, kStep);
     T.tail = 2 * P.n_tail;
-    P.box_tokens = 16;
-    while (P.box_tokens < kStep && Q.a.page_size % (2 * P.box_tokens) == 0) P.box_tokens *= 2;
+    P.box_log2 = 4;
+    while ((1 << P.box_log2) < kStep && Q.a.page_size % (2 << P.box_log2) == 0) ++P.box_log2;
     Prep8Params R{};
     R.a = Q.a;
     R.q8 = reinterpret_cast<uint8_t *>(base + w.q8);
-    R.q_scale = reinterpret_cast<float *>(base + w.q_scale);
+    R.q_meta = reinterpret_cast<float2 *>(base + w.q_meta);
     R.tail8 = reinterpret_cast<uint8_t *>(base + w.tail8);
     R.tail_scale = reinterpret_cast<float2 *>(base + w.tail_scale);
     R.rb = w.rb;
@@ -994,7 +1043,7 @@ spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s) {
     // the cache as [page x head][rows: 8 keys, 8 values, ...][D]
     const cuuint64_t d0[3] = {(cuuint64_t)D, (cuuint64_t)2 * ps, (cuuint64_t)Q.a.n_pages * Q.a.Hkv};
     const cuuint64_t s0[2] = {(cuuint64_t)D, (cuuint64_t)2 * ps * D};
-    const cuuint32_t b0[3] = {(cuuint32_t)D, (cuuint32_t)(2 * P.box_tokens), 1u};
+    const cuuint32_t b0[3] = {(cuuint32_t)D, (cuuint32_t)(2 << P.box_log2), 1u};
     const cuuint64_t s1[1] = {(cuuint64_t)D};
     const cuuint64_t d1[2] = {(cuuint64_t)D, (cuuint64_t)Q.a.B * Q.a.Hkv * 4 * w.tail_pad};
     const cuuint32_t b1[2] = {(cuuint32_t)D, 32u};

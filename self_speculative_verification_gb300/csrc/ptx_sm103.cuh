@@ -352,6 +352,20 @@ __device__ __forceinline__ void wait_ldn(uint32_t (&a)[N], uint32_t (&b)[N]) {
                        SV_R4(b, 8), SV_R4(b, 12), SV_R4(b, 16), SV_R4(b, 20), SV_R4(b, 24),
                        SV_R4(b, 28)::"memory");
 }
+template <int N>
+__device__ __forceinline__ void wait_ldn(uint32_t (&a)[N]) {
+    if constexpr (N == 4)
+        asm volatile("tcgen05.wait::ld.sync.aligned;" : SV_R4(a, 0)::"memory");
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.wait::ld.sync.aligned;" : SV_R4(a, 0), SV_R4(a, 4)::"memory");
+    else if constexpr (N == 16)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : SV_R4(a, 0), SV_R4(a, 4), SV_R4(a, 8), SV_R4(a, 12)::"memory");
+    else
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : SV_R4(a, 0), SV_R4(a, 4), SV_R4(a, 8), SV_R4(a, 12), SV_R4(a, 16),
+                       SV_R4(a, 20), SV_R4(a, 24), SV_R4(a, 28)::"memory");
+}
 #undef SV_R4
 #undef SV_O4
 #undef SV_I4
