@@ -50,7 +50,7 @@ using namespace tc5;
 
 constexpr int kStep = 128;                  // tokens a step
 constexpr int kTcThreads = 12 * 32;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kRecWarp = 10;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kRecWarp = 10, kScaleWarp = 11;
 constexpr float kTop = 8.75f;               // log2 of the largest P allowed (448 = 2^8.807)
 constexpr float kAim = 7.f;                 // log2 P of a row's maximum when M is raised
 constexpr float kNoRef = -1e30f;            // M of a row that has seen nothing
@@ -65,6 +65,8 @@ struct Tc8Params {
     int tail_len, tail_pad;  // n_soft + R, rounded up to 16
     int n_tail;              // its 128-token tiles
     int box_log2;            // log2 of the tokens per cache box
+    int ps16;                // page_size / 16, and ceil(2^32 / it): a page index is a product
+    uint64_t ps16_inv;       // (exact for 26-bit token / 16: the error is under 16 * 2^26 / 2^32)
 };
 
 template <int D, int RB>
@@ -249,132 +251,159 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
     }
     auto unit_of = [&](const Cursor &c) { return (c.b * T.seg_h + c.h) * T.seg_rb + c.rb; };
 
+    const int n_steps = (int)(t_end - t_begin);
+
     if (warp == kRecWarp) {
         const BoundaryRec rec = warp_boundary_record(T, ws, cta, t_begin, t_end);
         if (lane == 0) T.recs[cta] = rec;
-    } else if (t_begin < t_end && warp == kProducerWarp) {
-        // ------------------------------------------------------- producer
-        // lane i owns box i of a step: box_tokens tokens (prefix) or 16 (tail)
+    } else if (n_steps > 0 && (warp == kProducerWarp || warp == kScaleWarp)) {
+        // ------------------------------------- producer: copies, and scales
+        // Both warps walk the range in groups of up to four prefix steps of a
+        // unit (or one tail step): lane 8 u + i owns box i of the group's step
+        // u, so a page id costs one load per lane and group, issued a group
+        // ahead of its use (and the scale warp's scales another group).
+        const bool copies = warp == kProducerWarp;
         const uint64_t keep = policy_evict_last();
         const uint64_t stream = T.seg_rb == 1 ? policy_evict_first() : keep;
-        const int bt = 1 << P.box_log2, boxes = kStep / bt;
-        Cursor c;
-        cursor_init(T, ws, t_begin, c);
-        // this lane's page of the cursor's step: -1 no box, -2 a bad page
-        auto page_of = [&](const Cursor &k) -> int {
-            const Step8 s = step_at(P, k);
-            const int tok = s.tile * kStep + lane * bt;
-            if (s.tail || lane >= boxes || tok >= k.S) return -1;
-            const int pg = A.page_table[(size_t)k.b * A.max_pages + tok / A.page_size];
-            return pg < 0 || pg >= A.n_pages ? -2 : pg;
+        const int bt = 1 << P.box_log2, boxes = kStep >> P.box_log2;
+        const int u = lane >> 3, box = lane & 7;
+        struct Group {
+            Cursor c;            // its first step
+            int k, n;            // that step's number, steps (0: past the range)
+            bool tail;
+            int pg, row;         // this lane's page (-1 no box, -2 a bad page), row of its tile
         };
-        auto scale_of = [&](int h, int pg) {
-            if (pg < 0) return make_float2(1.f, 1.f);
-            return *reinterpret_cast<const float2 *>(P.scales + ((size_t)pg * A.Hkv + h) * 2);
+        auto group_at = [&](const Cursor &c, int k) {
+            Group g;
+            g.c = c;
+            g.k = k;
+            g.n = 0;
+            g.tail = false;
+            g.pg = -1;
+            g.row = 0;
+            if (k >= n_steps) return g;
+            const int np = (c.S + kStep - 1) / kStep;
+            g.tail = c.tile >= np;
+            g.n = g.tail ? 1 : min(min(4, np - c.tile), n_steps - k);
+            const int tok = (c.tile + u) * kStep + (box << P.box_log2);
+            if (!g.tail && u < g.n && box < boxes && tok < c.S) {
+                const int w = tok >> 4, j = (int)((w * P.ps16_inv) >> 32);
+                g.row = (w - j * P.ps16) * 32;
+                const int pg = A.page_table[(size_t)c.b * A.max_pages + j];
+                g.pg = pg < 0 || pg >= A.n_pages ? -2 : pg;
+            }
+            return g;
         };
-        // page ids are loaded two steps ahead of their copies, scales one, so
-        // that neither load's latency is in the loop (attn_long 1066 -> 700 us)
-        Cursor ahead = c;
-        long long ta = t_begin;
-        auto next_page = [&]() -> int {      // of the step after `ahead`
-            if (++ta >= t_end) return -1;
-            cursor_next(T, ahead);
-            return page_of(ahead);
+        auto after = [&](const Group &g) {          // the group that follows
+            Cursor c = g.c;
+            if (g.n > 0 && g.k + g.n < n_steps) {
+                c.tile += g.n - 1;
+                cursor_next(T, c);
+            }
+            return group_at(c, g.n > 0 ? g.k + g.n : n_steps);
         };
-        int pg = page_of(c), pg1 = next_page();
-        int h1 = ahead.h;
-        float2 sc = scale_of(c.h, pg), sc1 = scale_of(h1, pg1);
-        int pg2 = next_page(), h2 = ahead.h;
-        int slot = 0, nq = 0;
-        long long used = 0;                  // ring slots taken so far
+        auto scale_of = [&](const Group &g) {
+            if (g.pg < 0) return make_float2(1.f, 1.f);
+            return *reinterpret_cast<const float2 *>(P.scales + ((size_t)g.pg * A.Hkv + g.c.h) * 2);
+        };
+        Cursor c0;
+        cursor_init(T, ws, t_begin, c0);
+        Group cur = group_at(c0, 0), next = after(cur);
+        float2 sc = make_float2(1.f, 1.f), sc1 = sc;
+        if (!copies) sc = scale_of(cur);
+        int slot = 0, phase = 0, nq = 0;
+        long long used = 0;                          // ring slots taken so far
         bool ok = true;
-        for (long long t = t_begin; t < t_end; ++t) {
-            const Step8 s = step_at(P, c);
-            bool got = true;
-            if (t == t_begin || c.tile == 0) {
-                // the unit's queries, once the unit two back is done with the
-                // buffer
-                const int qb = nq & 1;
-                if (lane == 0) {
-                    got = nq < 2 || mbar_wait(&sh.q_empty[qb], (uint32_t)(((nq >> 1) - 1) & 1), T.wait);
-                    if (got) {
-                        mbar_arrive_expect_tx(&sh.q_full[qb], C::kQ);
-                        tma_load_2d(qbuf + qb * C::kQ, &m_q, 0, unit_of(c) * (2 * RB), &sh.q_full[qb],
-                                    keep);
+        while (cur.n > 0 && ok) {
+            const Group far = after(next);
+            float4 ts;
+            if (copies) {
+                if (cur.pg == -2) raise_status(A.status, SPEC_DEV_BAD_PAGE);
+                if (cur.c.tile == 0 || cur.k == 0) {
+                    // the unit's queries, once the unit two back is done with
+                    // the buffer
+                    const int qb = nq & 1;
+                    bool got = true;
+                    if (lane == 0) {
+                        got = nq < 2 ||
+                              mbar_wait(&sh.q_empty[qb], (uint32_t)(((nq >> 1) - 1) & 1), T.wait);
+                        if (got) {
+                            mbar_arrive_expect_tx(&sh.q_full[qb], C::kQ);
+                            tma_load_2d(qbuf + qb * C::kQ, &m_q, 0, unit_of(cur.c) * (2 * RB),
+                                        &sh.q_full[qb], keep);
+                        }
                     }
+                    if (!__shfl_sync(0xffffffffu, got, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    ++nq;
                 }
-                if (!__shfl_sync(0xffffffffu, got, 0)) {
-                    ok = false;
-                    break;
-                }
-                ++nq;
+            } else {
+                sc1 = scale_of(next);
+                ts = token_scale(kv8_read_scale(sc.x), kv8_read_scale(sc.y));
             }
-            const int parts = s.tail ? 2 : 1;
-            for (int part = 0; part < parts; ++part) {
-                if (lane == 0)
-                    got = mbar_wait(&sh.empty[slot], (uint32_t)(((used / NS) & 1) ^ 1), T.wait);
+            const unsigned boxed = __ballot_sync(0xffffffffu, cur.pg >= 0);
+            const int np = (cur.c.S + kStep - 1) / kStep, tile0 = cur.c.tile - np;   // (tail)
+            const int slots = cur.tail ? 2 : cur.n;
+            for (int i = 0; i < slots; ++i) {
+                bool got = true;
+                if (lane == 0) got = mbar_wait(&sh.empty[slot], (uint32_t)(phase ^ 1), T.wait);
                 if (!__shfl_sync(0xffffffffu, got, 0)) {
                     ok = false;
                     break;
                 }
-                bool mine;
-                int rows;
-                if (s.tail) {
-                    mine = lane < 8 && lane * 16 < s.n;
-                    rows = 32;
-                } else {
-                    mine = pg >= 0;
-                    rows = 2 * bt;
-                    if (pg == -2) raise_status(A.status, SPEC_DEV_BAD_PAGE);
-                }
-                const uint32_t bytes =
-                    (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * (uint32_t)(rows * D);
-                if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
-                __syncwarp();
-                uint8_t *dst = ring + slot * C::kSlot + lane * rows * D;
-                if (mine) {
-                    if (s.tail)
-                        tma_load_2d(dst, &m_tail, 0,
-                                    ((c.b * A.Hkv + c.h) * 2 + part) * (2 * P.tail_pad) +
-                                        s.tile * (2 * kStep) + lane * 32,
+                uint8_t *dst = ring + slot * C::kSlot;
+                if (!copies) {
+                    if (!cur.tail && u == i && box < boxes) sh.scale[slot][box] = ts;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.full[slot]);
+                } else if (cur.tail) {
+                    // part i of the tail tile: boxes of 16 tokens
+                    const int n = min(kStep, P.tail_len - tile0 * kStep), nb = (n + 15) >> 4;
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], (uint32_t)(nb * 32 * D));
+                    __syncwarp();
+                    if (lane < nb)
+                        tma_load_2d(dst + lane * 32 * D, &m_tail, 0,
+                                    ((cur.c.b * A.Hkv + cur.c.h) * 2 + i) * (2 * P.tail_pad) +
+                                        tile0 * (2 * kStep) + lane * 32,
                                     &sh.full[slot], keep);
-                    else
-                        tma_load_3d(dst, &m_kv, 0, 2 * ((s.tile * kStep + lane * bt) % A.page_size),
-                                    pg * A.Hkv + c.h, &sh.full[slot], stream);
+                } else {
+                    const uint32_t bytes = (uint32_t)__popc((boxed >> (8 * i)) & 0xffu) * (uint32_t)(2 * bt * D);
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
+                    __syncwarp();
+                    if (u == i && cur.pg >= 0)
+                        tma_load_3d(dst + box * (2 * bt * D), &m_kv, 0, cur.row, cur.pg * A.Hkv + cur.c.h,
+                                    &sh.full[slot], stream);
                 }
-                if (!s.tail && lane < boxes)
-                    sh.scale[slot][lane] = token_scale(kv8_read_scale(sc.x), kv8_read_scale(sc.y));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.full[slot]);
                 ++used;
-                slot = slot + 1 == NS ? 0 : slot + 1;
+                if (++slot == NS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
-            if (!ok) break;
-            cursor_next(T, c);
-            pg = pg1;
+            cur = next;
+            next = far;
             sc = sc1;
-            pg1 = pg2;
-            h1 = h2;
-            sc1 = scale_of(h1, pg1);
-            pg2 = next_page();
-            h2 = ahead.h;
         }
         if (lane == 0) {
             if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
             // do not leave while copies into this CTA's shared memory are in
             // flight (the default limit: these copies were issued and complete)
-            for (long long i = used - 1; i >= 0 && i >= used - NS; --i)
-                if (!mbar_wait(&sh.full[i % NS], (uint32_t)((i / NS) & 1))) {
-                    raise_status(A.status, SPEC_DEV_TIMEOUT);
-                    break;
-                }
-            for (int n = nq - 1; n >= 0 && n >= nq - 2; --n)
-                if (!mbar_wait(&sh.q_full[n & 1], (uint32_t)((n >> 1) & 1))) {
-                    raise_status(A.status, SPEC_DEV_TIMEOUT);
-                    break;
-                }
+            if (copies) {
+                for (long long i = used - 1; i >= 0 && i >= used - NS; --i)
+                    if (!mbar_wait(&sh.full[i % NS], (uint32_t)((i / NS) & 1))) {
+                        raise_status(A.status, SPEC_DEV_TIMEOUT);
+                        break;
+                    }
+                for (int n = nq - 1; n >= 0 && n >= nq - 2; --n)
+                    if (!mbar_wait(&sh.q_full[n & 1], (uint32_t)((n >> 1) & 1))) {
+                        raise_status(A.status, SPEC_DEV_TIMEOUT);
+                        break;
+                    }
+            }
         }
-    } else if (t_begin < t_end && warp == kMmaWarp) {
+    } else if (n_steps > 0 && warp == kMmaWarp) {
         // ----------------------------------------------------- MMA issuer
         Cursor c;
         cursor_init(T, ws, t_begin, c);       // warp-collective
@@ -390,20 +419,20 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             const uint64_t vd0 = smem_desc_sw<D>(smem_u32(ring) + 8 * D, 0, 16 * D);
             const uint64_t qd0 = smem_desc_sw<D>(smem_u32(qbuf), 16, 8 * D);
             const uint64_t pd0 = smem_desc(smem_u32(pbuf), 0, 1024);
-            int nq = 0, slot = 0, prev_slot = 0, prev_parts = 1;
+            int nq = 0, slot = 0, phase = 0, prev_slot = 0, prev_parts = 1;
             bool ok = true, prev_first = true;
-            long long used = 0;
-            auto issue_pv = [&](long long j) -> bool {
-                const int b = (int)(j & 1);
+            auto issue_pv = [&](int j) -> bool {
+                const int b = j & 1;
                 if (!mbar_wait(&sh.p_full[b], (uint32_t)((j >> 1) & 1), T.wait)) return false;
                 fence_after();
+                const uint64_t pd = pd0 + (uint64_t)((b * C::kP) >> 4);
                 int sl = prev_slot;
                 for (int part = 0; part < prev_parts; ++part) {
                     const uint64_t vd = vd0 + (uint64_t)((sl * C::kSlot) >> 4);
 #pragma unroll
                     for (int k = 0; k < kStep / 32; ++k)
                         mma8_ss(tmem, vd + (uint64_t)((k * 4 * 16 * D) >> 4),
-                                pd0 + (uint64_t)((b * C::kP + k * 4 * 1024) >> 4), id_pv,
+                                pd + (uint64_t)((k * 4 * 1024) >> 4), id_pv,
                                 (k > 0 || part > 0 || !prev_first) ? 1u : 0u);
                     commit(&sh.empty[sl]);
                     sl = sl + 1 == NS ? 0 : sl + 1;
@@ -411,11 +440,10 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 commit(&sh.o_upd[b]);
                 return true;
             };
-            long long k = 0;
-            for (long long t = t_begin; t < t_end; ++t, ++k) {
-                const Step8 s = step_at(P, c);
+            for (int k = 0; k < n_steps; ++k) {
+                const bool tail = c.tile * kStep >= c.S;
                 const bool new_unit = k == 0 || c.tile == 0;
-                const bool last = c.tile == c.n_tiles - 1 || t == t_end - 1;
+                const bool last = c.tile == c.n_tiles - 1 || k == n_steps - 1;
                 if (new_unit) {
                     if (!mbar_wait(&sh.q_full[nq & 1], (uint32_t)((nq >> 1) & 1), T.wait)) {
                         ok = false;
@@ -423,39 +451,42 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     }
                     ++nq;
                 }
-                const int qb = (nq - 1) & 1, first_slot = slot, parts = s.tail ? 2 : 1;
-                for (int part = 0; part < parts && ok; ++part) {
-                    if (!mbar_wait(&sh.full[slot], (uint32_t)((used / NS) & 1), T.wait)) {
+                const int qb = (nq - 1) & 1, first_slot = slot, parts = tail ? 2 : 1;
+                const uint64_t qd = qd0 + (uint64_t)((qb * C::kQ) >> 4);
+                const uint32_t ts = tmem + C::kColS * (1 + (uint32_t)(k & 1));
+                for (int part = 0; part < parts; ++part) {
+                    if (!mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait)) {
                         ok = false;
                         break;
                     }
                     fence_after();
                     const uint64_t kd = kd0 + (uint64_t)((slot * C::kSlot) >> 4);
-                    const uint64_t qd = qd0 + (uint64_t)((qb * C::kQ) >> 4);
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e)
-                        mma8_ss(tmem + C::kColS * (1 + (uint32_t)(k & 1)), kd + (uint64_t)(e * 32 >> 4),
-                                qd + (uint64_t)(e * 32 >> 4), id_s, (e > 0 || part > 0) ? 1u : 0u);
-                    ++used;
-                    slot = slot + 1 == NS ? 0 : slot + 1;
+                        mma8_ss(ts, kd + (uint64_t)(e * 32 >> 4), qd + (uint64_t)(e * 32 >> 4), id_s,
+                                (e > 0 || part > 0) ? 1u : 0u);
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                 }
                 if (!ok) break;
                 commit(&sh.s_full[k & 1]);
                 if (last) commit(&sh.q_empty[qb]);
+                cursor_next(T, c);
                 if (k > 0 && !(ok = issue_pv(k - 1))) break;
                 prev_slot = first_slot;
                 prev_parts = parts;
                 prev_first = new_unit;
-                cursor_next(T, c);
             }
-            if (ok && k > 0) ok = issue_pv(k - 1);
+            if (ok && n_steps > 0) ok = issue_pv(n_steps - 1);
             if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
             // every MMA issued above has completed before TMEM is released
             // (the default limit)
             commit(&sh.drain);
             if (!mbar_wait(&sh.drain, 0)) raise_status(A.status, SPEC_DEV_TIMEOUT);
         }
-    } else if (t_begin < t_end && warp < kProducerWarp) {
+    } else if (n_steps > 0 && warp < kProducerWarp) {
         // -------------------------------------------------------- softmax
         // warpgroup g: rows g HR .. of the unit; a thread: one token of the
         // step (TMEM lane), later one head dimension of O
@@ -466,12 +497,11 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         cursor_init(T, ws, t_begin, c);
         float l[HR];
         bool ok = true, seg_whole = false;
-        int seg_b = 0, seg_h = 0, seg_id = 0, slot = 0;
-        long long used = 0, k = 0;
+        int seg_b = 0, seg_h = 0, seg_id = 0, slot = 0, phase = 0, k = 0;
 
         // end of this CTA's part of a unit, after PV(j): the row sums over the
         // tokens' threads, then O / l and LSE, or the partials
-        auto epilogue = [&](long long j) -> bool {
+        auto epilogue = [&](int j) -> bool {
             const bool got = ok && mbar_wait_warp(&sh.o_upd[j & 1], (uint32_t)((j >> 1) & 1), T.wait);
             constexpr int kPer = 32 / HR;
             const float sum = warp_sums<HR>(l);
@@ -524,7 +554,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
 
         float2 meta = make_float2(0.f, 0.f);     // the next unit's row gi, loaded ahead
         if (gi < HR) meta = P.q_meta[(size_t)unit_of(c) * RB + g * HR + gi];
-        for (long long t = t_begin; t < t_end; ++t, ++k) {
+        for (; k < n_steps; ++k) {
             const bool new_unit = k == 0 || c.tile == 0;
             if (new_unit) {
                 if (k > 0 && !epilogue(k - 1)) {
@@ -534,8 +564,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 seg_b = c.b;
                 seg_h = c.h;
                 seg_id = unit_of(c);
-                const long long seg_lo = t - c.tile;
-                seg_whole = seg_lo >= t_begin && seg_lo + c.n_tiles <= t_end;
+                seg_whole = c.tile == 0 && k + c.n_tiles <= n_steps;
                 group_sync(bar);               // the last unit's rows are read
                 if (gi < HR) {
                     sh.out[g][gi] = __float_as_int(meta.y);
@@ -548,7 +577,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             }
             const Step8 s = step_at(P, c);
             cursor_next(T, c);
-            if (c.tile == 0 && t + 1 < t_end && gi < HR)
+            if (c.tile == 0 && k + 1 < n_steps && gi < HR)
                 meta = P.q_meta[(size_t)unit_of(c) * RB + g * HR + gi];
             const int slot0 = slot, parts = s.tail ? 2 : 1;
             // rows' visibility of this warp's 32 tail tokens, lane i: row i
@@ -579,12 +608,19 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                         seen |= ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
                 }
             }
-            if (ok) ok = mbar_wait_warp(&sh.s_full[k & 1], (uint32_t)((k >> 1) & 1), T.wait);
-            // the slots' own barriers: the scales, and the rows cleared below
-            for (int part = 0; part < parts; ++part) {
-                if (ok) ok = mbar_wait_warp(&sh.full[slot], (uint32_t)((used / NS) & 1), T.wait);
-                ++used;
-                slot = slot + 1 == NS ? 0 : slot + 1;
+            if (ok) {
+                // S, and the slots' own barriers for the scales and for the
+                // rows cleared below.  S(k) was issued behind PV(k - 2), so its
+                // barrier also frees the P buffer written below.
+                ok = mbar_wait(&sh.s_full[k & 1], (uint32_t)((k >> 1) & 1), T.wait);
+                for (int part = 0; part < parts; ++part) {
+                    ok = ok && mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait);
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
             }
             const uint32_t ts = tmem + lane_base + C::kColS * (1 + (uint32_t)(k & 1)) + (uint32_t)(g * HR);
             float y[HR];
@@ -700,11 +736,8 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     if (here && (!s.tail || ((row >> lane) & 1u))) y[i] += sc.w;
                 }
             }
-            // P(k) into buffer k % 2, once PV(k - 2) has read it
-            if (ok && k >= 2)
-                ok = mbar_wait_warp(&sh.o_upd[k & 1], (uint32_t)(((k - 2) >> 1) & 1), T.wait);
             if (ok) {
-                uint8_t *prow = pbuf + (int)(k & 1) * C::kP + tok * 128;
+                uint8_t *prow = pbuf + (k & 1) * C::kP + tok * 128;
                 uint32_t w[RB / 4];                 // first parts, then second parts
 #pragma unroll
                 for (int i = 0; i < HR; i += 4) {
@@ -740,7 +773,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             }
         }
         // (a warpgroup leaves the loop together or runs it to its end)
-        if (k > 0 && t_begin + k == t_end && !epilogue(k - 1)) ok = false;
+        if (k == n_steps && !epilogue(k - 1)) ok = false;
         if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
     }
     fence_before();
@@ -1040,6 +1073,8 @@ spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s) {
     T.tail = 2 * P.n_tail;
     P.box_log2 = 4;
     while ((1 << P.box_log2) < kStep && Q.a.page_size % (2 << P.box_log2) == 0) ++P.box_log2;
+    P.ps16 = Q.a.page_size / 16;
+    P.ps16_inv = ((1ull << 32) + P.ps16 - 1) / P.ps16;
     Prep8Params R{};
     R.a = Q.a;
     R.q8 = reinterpret_cast<uint8_t *>(base + w.q8);
