@@ -69,15 +69,25 @@ struct Tc8Params {
     uint64_t ps16_inv;       // (exact for 26-bit token / 16: the error is under 16 * 2^26 / 2^32)
 };
 
+// Two softmax warpgroups.  Up to 32 rows they take alternate steps, each with
+// all of the unit's rows and a running softmax (M, l, O) of its own, merged at
+// the unit's end: a step's chain (wait, tensor memory, vote, exponentials, P,
+// arrive: ~2000 cycles, most of it latency) then costs half.  With 64 rows, whose arithmetic
+// is the larger part, they take half of the rows of every step.
 template <int D, int RB>
 struct Cfg {
-    static constexpr int HR = RB / 2;                   // rows of a softmax warpgroup
+    static constexpr bool kAlt = RB <= 32;
+    static constexpr int RW = kAlt ? RB : RB / 2;       // rows of a warpgroup
+    static constexpr int CH = RW < 16 ? RW : 16;        // rows taken from tensor memory at a time
     static constexpr int kSlot = 2 * kStep * D;         // K and V of a step
     static constexpr int kQ = 2 * RB * D;               // a unit's queries, both parts
     static constexpr int kP = kStep * 128;              // P^T, rows of 128 bytes
     static constexpr int NS = D == 64 ? 8 : (RB == 64 ? 4 : 5);
-    static constexpr uint32_t kColS = 2 * RB;           // TMEM: O at 0, S buffer b at kColS (1 + b)
-    static constexpr int kCols = 6 * RB <= 64 ? 64 : 6 * RB <= 128 ? 128 : 6 * RB <= 256 ? 256 : 512;
+    // TMEM: O of warpgroup g at 2 RW g (first parts, then second parts), S
+    // buffer b at kColS + 2 RB b
+    static constexpr uint32_t kColS = 4 * RW;
+    static constexpr int kUsed = 4 * RW + 4 * RB;
+    static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
 };
 
 template <int D, int RB>
@@ -87,13 +97,13 @@ struct Shared8 {
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], o_upd[2];
     uint64_t drain;
-    float4 scale[C::NS][8];              // TokenScale of each box of a slot
-    alignas(16) float qs[2][C::HR];      // a row's q_scale
-    alignas(16) float neg_m[2][C::HR];   // and its -M
-    alignas(16) float fac[2][C::HR];     // slow path: what its sums are scaled by; end: 1 / l
-    int rmax[2][4][C::HR];
-    float rsum[2][4][C::HR];
-    int out[2][C::HR];                   // (row * Hq + head) * 2 + valid, or -1
+    float4 scale[C::NS][8];              // token_scale of each box of a slot
+    alignas(16) float qs[2][C::RW];      // a row's q_scale
+    alignas(16) float neg_m[2][C::RW];   // and its -M
+    alignas(16) float fac[2][C::RW];     // what its O is scaled by
+    int rmax[2][4][C::RW];
+    float rsum[2][4][C::RW];
+    int out[2][C::RW];                   // (row * Hq + head) * 2 + valid, or -1
     uint32_t tmem_base;
 };
 
@@ -106,19 +116,21 @@ static_assert(smem8<128, 64>() <= 227 * 1024 && smem8<128, 32>() <= 227 * 1024 &
                   smem8<64, 64>() <= 227 * 1024,
               "shared memory of the 8-bit attention kernel");
 
-// OR over the 128 threads of a warpgroup (named barrier `id`).
+// OR over the N threads at named barrier `id` (1 + g: a warpgroup; 3: both).
+template <int N>
 __device__ __forceinline__ bool group_or(int id, bool x) {
     int r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "barrier.cta.red.or.pred p, %1, 128, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+        "barrier.cta.red.or.pred p, %1, %3, q;\n\tselp.b32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"(id), "r"((int)x)
+        : "r"(id), "r"((int)x), "n"(N)
         : "memory");
     return r != 0;
 }
+template <int N>
 __device__ __forceinline__ void group_sync(int id) {
-    asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
 }
 
 // Floats as integers of the same order (NaN as -inf), and back.
@@ -179,21 +191,6 @@ __device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32
     lo = l;
 }
 
-// The cursor's step: prefix tile or tail tile, its first token, how many of
-// its 128 tokens there are.
-struct Step8 {
-    bool tail;
-    int tile, n;
-};
-__device__ __forceinline__ Step8 step_at(const Tc8Params &P, const Cursor &c) {
-    const int np = (c.S + kStep - 1) / kStep;
-    Step8 s;
-    s.tail = c.tile >= np;
-    s.tile = s.tail ? c.tile - np : c.tile;
-    s.n = min(kStep, (s.tail ? P.tail_len : c.S) - s.tile * kStep);
-    return s;
-}
-
 template <int D, int RB>
 __global__ void __launch_bounds__(kTcThreads, 1)
 attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ CUtensorMap m_kv,
@@ -201,7 +198,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                    const __grid_constant__ CUtensorMap m_q) {
     pdl_wait();
     using C = Cfg<D, RB>;
-    constexpr int HR = C::HR, NS = C::NS;
+    constexpr int RW = C::RW, NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -223,7 +220,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             mbar_init(&sh.q_full[b], 1);
             mbar_init(&sh.q_empty[b], 1);
             mbar_init(&sh.s_full[b], 1);
-            mbar_init(&sh.p_full[b], 8);
+            mbar_init(&sh.p_full[b], C::kAlt ? 4 : 8);
             mbar_init(&sh.o_upd[b], 1);
         }
         mbar_init(&sh.drain, 1);
@@ -419,65 +416,68 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             const uint64_t vd0 = smem_desc_sw<D>(smem_u32(ring) + 8 * D, 0, 16 * D);
             const uint64_t qd0 = smem_desc_sw<D>(smem_u32(qbuf), 16, 8 * D);
             const uint64_t pd0 = smem_desc(smem_u32(pbuf), 0, 1024);
-            int nq = 0, slot = 0, phase = 0, prev_slot = 0, prev_parts = 1;
+            int nq = 0, slot = 0, phase = 0, prev_slot = 0, prev_parts = 1, k = 0;
             bool ok = true, prev_first = true;
             auto issue_pv = [&](int j) -> bool {
                 const int b = j & 1;
                 if (!mbar_wait(&sh.p_full[b], (uint32_t)((j >> 1) & 1), T.wait)) return false;
                 fence_after();
                 const uint64_t pd = pd0 + (uint64_t)((b * C::kP) >> 4);
+                const uint32_t to = tmem + (C::kAlt ? (uint32_t)(b * 2 * RW) : 0u);
                 int sl = prev_slot;
                 for (int part = 0; part < prev_parts; ++part) {
                     const uint64_t vd = vd0 + (uint64_t)((sl * C::kSlot) >> 4);
 #pragma unroll
-                    for (int k = 0; k < kStep / 32; ++k)
-                        mma8_ss(tmem, vd + (uint64_t)((k * 4 * 16 * D) >> 4),
-                                pd + (uint64_t)((k * 4 * 1024) >> 4), id_pv,
-                                (k > 0 || part > 0 || !prev_first) ? 1u : 0u);
+                    for (int e = 0; e < kStep / 32; ++e)
+                        mma8_ss(to, vd + (uint64_t)((e * 4 * 16 * D) >> 4),
+                                pd + (uint64_t)((e * 4 * 1024) >> 4), id_pv,
+                                (e > 0 || part > 0 || !prev_first) ? 1u : 0u);
                     commit(&sh.empty[sl]);
                     sl = sl + 1 == NS ? 0 : sl + 1;
                 }
                 commit(&sh.o_upd[b]);
                 return true;
             };
-            for (int k = 0; k < n_steps; ++k) {
-                const bool tail = c.tile * kStep >= c.S;
-                const bool new_unit = k == 0 || c.tile == 0;
-                const bool last = c.tile == c.n_tiles - 1 || k == n_steps - 1;
-                if (new_unit) {
-                    if (!mbar_wait(&sh.q_full[nq & 1], (uint32_t)((nq >> 1) & 1), T.wait)) {
-                        ok = false;
-                        break;
-                    }
-                    ++nq;
+            while (ok && k < n_steps) {
+                // a unit's steps of this range
+                const int k0 = k, n = min(n_steps - k, c.n_tiles - c.tile);
+                const int n_prefix = (c.S + kStep - 1) / kStep - c.tile;     // of them prefix steps
+                const int qb = nq & 1;
+                if (!mbar_wait(&sh.q_full[qb], (uint32_t)((nq >> 1) & 1), T.wait)) {
+                    ok = false;
+                    break;
                 }
-                const int qb = (nq - 1) & 1, first_slot = slot, parts = tail ? 2 : 1;
+                ++nq;
                 const uint64_t qd = qd0 + (uint64_t)((qb * C::kQ) >> 4);
-                const uint32_t ts = tmem + C::kColS * (1 + (uint32_t)(k & 1));
-                for (int part = 0; part < parts; ++part) {
-                    if (!mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait)) {
-                        ok = false;
-                        break;
-                    }
-                    fence_after();
-                    const uint64_t kd = kd0 + (uint64_t)((slot * C::kSlot) >> 4);
+                for (int i = 0; i < n; ++i, ++k) {
+                    const int first_slot = slot, parts = i >= n_prefix ? 2 : 1;
+                    const uint32_t ts = tmem + C::kColS + (uint32_t)((k & 1) * 2 * RB);
+                    for (int part = 0; part < parts; ++part) {
+                        if (!mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_after();
+                        const uint64_t kd = kd0 + (uint64_t)((slot * C::kSlot) >> 4);
 #pragma unroll
-                    for (int e = 0; e < D / 32; ++e)
-                        mma8_ss(ts, kd + (uint64_t)(e * 32 >> 4), qd + (uint64_t)(e * 32 >> 4), id_s,
-                                (e > 0 || part > 0) ? 1u : 0u);
-                    if (++slot == NS) {
-                        slot = 0;
-                        phase ^= 1;
+                        for (int e = 0; e < D / 32; ++e)
+                            mma8_ss(ts, kd + (uint64_t)(e * 32 >> 4), qd + (uint64_t)(e * 32 >> 4),
+                                    id_s, (e > 0 || part > 0) ? 1u : 0u);
+                        if (++slot == NS) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
                     }
+                    if (!ok) break;
+                    commit(&sh.s_full[k & 1]);
+                    if (i == n - 1) commit(&sh.q_empty[qb]);
+                    if (k > 0 && !(ok = issue_pv(k - 1))) break;
+                    prev_slot = first_slot;
+                    prev_parts = parts;
+                    prev_first = k - k0 < (C::kAlt ? 2 : 1);     // the first into its O
                 }
-                if (!ok) break;
-                commit(&sh.s_full[k & 1]);
-                if (last) commit(&sh.q_empty[qb]);
+                c.tile += n - 1;
                 cursor_next(T, c);
-                if (k > 0 && !(ok = issue_pv(k - 1))) break;
-                prev_slot = first_slot;
-                prev_parts = parts;
-                prev_first = new_unit;
             }
             if (ok && n_steps > 0) ok = issue_pv(n_steps - 1);
             if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
@@ -488,292 +488,333 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         }
     } else if (n_steps > 0 && warp < kProducerWarp) {
         // -------------------------------------------------------- softmax
-        // warpgroup g: rows g HR .. of the unit; a thread: one token of the
-        // step (TMEM lane), later one head dimension of O
+        // warpgroup g: the steps k = g (mod 2), or rows RW g .. of every step;
+        // a thread: one token of the step (TMEM lane), later one dimension of O
+        constexpr bool kAlt = C::kAlt;
+        constexpr int CH = C::CH;
         const int g = warp >> 2, wq = warp & 3, bar = 1 + g;
         const int tok = wq * 32 + lane, gi = threadIdx.x & 127;
+        const int row0 = kAlt ? 0 : g * RW;
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+        const uint32_t to = tmem + lane_base;          // O of both warpgroups
         Cursor c;
         cursor_init(T, ws, t_begin, c);
-        float l[HR];
-        bool ok = true, seg_whole = false;
-        int seg_b = 0, seg_h = 0, seg_id = 0, slot = 0, phase = 0, k = 0;
+        float l[RW];
+        // ok: this warp's waits were met; dead: the warpgroup has stopped (it
+        // still meets the others at the units' barriers)
+        bool ok = true, dead = false;
+        int slot = 0, phase = 0, k = 0;
 
-        // end of this CTA's part of a unit, after PV(j): the row sums over the
-        // tokens' threads, then O / l and LSE, or the partials
-        auto epilogue = [&](int j) -> bool {
-            const bool got = ok && mbar_wait_warp(&sh.o_upd[j & 1], (uint32_t)((j >> 1) & 1), T.wait);
-            constexpr int kPer = 32 / HR;
-            const float sum = warp_sums<HR>(l);
+        float2 meta = make_float2(0.f, 0.f);     // the unit's row gi, loaded a unit ahead
+        if (gi < RW) meta = P.q_meta[(size_t)unit_of(c) * RB + row0 + gi];
+        while (k < n_steps) {
+            // --- a unit's steps of this range
+            const int k0 = k, tile0 = c.tile, n = min(n_steps - k, c.n_tiles - c.tile), S = c.S;
+            const int np = (S + kStep - 1) / kStep, seg_b = c.b, seg_h = c.h, seg_id = unit_of(c);
+            const bool seg_whole = tile0 == 0 && n == c.n_tiles;
+            if (gi < RW) {
+                sh.out[g][gi] = __float_as_int(meta.y);
+                sh.qs[g][gi] = meta.x;
+                sh.neg_m[g][gi] = -kNoRef;
+            }
+            c.tile += n - 1;
+            cursor_next(T, c);
+            if (gi < RW && k + n < n_steps) meta = P.q_meta[(size_t)unit_of(c) * RB + row0 + gi];
+#pragma unroll
+            for (int i = 0; i < RW; ++i) l[i] = 0.f;
+            group_sync<128>(bar);
+
+            for (; k < k0 + n; ++k) {
+                const int tile = tile0 + k - k0;
+                const bool tail = tile >= np;
+                const int slot0 = slot, phase0 = phase;
+                slot += tail ? 2 : 1;
+                if (slot >= NS) {
+                    slot -= NS;
+                    phase ^= 1;
+                }
+                if (dead || (kAlt && (k & 1) != g)) continue;
+                const int left = tail ? P.tail_len - (tile - np) * kStep : S - tile * kStep;
+                const bool here = tok < left;
+                // rows' visibility of this warp's 32 tail tokens, lane i: row i
+                uint32_t seen = 0u;
+                float4 sc = make_float4(0.f, 0.f, 1.f, 0.f);
+                if (tail) {
+                    const int tt0 = (tile - np) * kStep + wq * 32;
+                    if (here) {
+                        const float2 x =
+                            P.tail_scale[((size_t)seg_b * A.Hkv + seg_h) * P.tail_pad + tt0 + lane];
+                        sc = token_scale(x.x, x.y);
+                    }
+                    const int out = lane < RW ? sh.out[g][lane] : -1;
+                    if (out >= 0 && (out & 1)) {
+                        const int rr = (out >> 1) / A.Hq;
+                        const uint32_t *vr = A.vis + ((size_t)seg_b * A.R + rr) * A.W;
+                        auto word = [&](int w) {
+                            if (w < 0 || w >= A.W) return 0u;
+                            const int cols = A.R - w * 32;      // from the word's first
+                            return cols >= 32 ? vr[w] : vr[w] & ((1u << cols) - 1u);
+                        };
+                        // block columns c0 .. c0 + 31
+                        const int c0 = tt0 - A.n_soft, sft = c0 & 31, w0 = c0 >> 5;     // (floor)
+                        seen = word(w0) >> sft;
+                        if (sft) seen |= word(w0 + 1) << (32 - sft);
+                        const int ns = A.n_soft - tt0;          // soft tokens from here on
+                        if (ns > 0 && (A.row_flags[(size_t)seg_b * A.R + rr] & SPEC_ROW_SEES_SOFT))
+                            seen |= ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
+                    }
+                }
+                if (ok) {
+                    // S, and the slots' own barriers for the scales and for the
+                    // rows cleared below.  S(k) was issued behind PV(k - 2), so
+                    // its barrier also frees the P buffer written below and,
+                    // where the warpgroups alternate, their O.
+                    ok = mbar_wait(&sh.s_full[k & 1], (uint32_t)((k >> 1) & 1), T.wait) &&
+                         mbar_wait(&sh.full[slot0], (uint32_t)phase0, T.wait);
+                    if (tail) {
+                        const int s1 = slot0 + 1 == NS ? 0 : slot0 + 1;
+                        ok = ok && mbar_wait(&sh.full[s1], (uint32_t)(s1 ? phase0 : phase0 ^ 1), T.wait);
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                }
+                const uint32_t ts = to + C::kColS + (uint32_t)((k & 1) * 2 * RB + row0);
+                float y[RW];
+                // y = s x (key scale, softmax scale) + log2(value scale) [- M]:
+                // the exponents of P, from the two parts of S
+                auto exponents = [&](bool less_m) {
+                    const uint64_t sk2 = pair(sc.x, sc.x), lv2 = pair(sc.y, sc.y), z = pair(0.f, 0.f);
+#pragma unroll
+                    for (int i0 = 0; i0 < RW; i0 += CH) {
+                        uint32_t hi[CH], lo[CH];
+                        ldn<CH>(ts + i0, hi);
+                        ldn<CH>(ts + RB + i0, lo);
+                        wait_ldn<CH>(hi, lo);
+#pragma unroll
+                        for (int i = 0; i < CH; i += 4) {
+                            const float4 q = *reinterpret_cast<const float4 *>(&sh.qs[g][i0 + i]);
+                            float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (less_m) m = *reinterpret_cast<const float4 *>(&sh.neg_m[g][i0 + i]);
+                            unpair(fma2(add2(pair(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
+                                             pair(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1]))),
+                                        fma2(pair(q.x, q.y), sk2, z), add2(pair(m.x, m.y), lv2)),
+                                   y[i0 + i], y[i0 + i + 1]);
+                            unpair(
+                                fma2(add2(pair(__uint_as_float(hi[i + 2]), __uint_as_float(hi[i + 3])),
+                                          pair(__uint_as_float(lo[i + 2]), __uint_as_float(lo[i + 3]))),
+                                     fma2(pair(q.z, q.w), sk2, z), add2(pair(m.z, m.w), lv2)),
+                                y[i0 + i + 2], y[i0 + i + 3]);
+                        }
+                    }
+                };
+                // -inf for what a row does not see
+                auto mask = [&] {
+                    if (tail) {
+#pragma unroll
+                        for (int i = 0; i < RW; ++i) {
+                            const uint32_t row = __shfl_sync(0xffffffffu, seen, i);
+                            y[i] = here && ((row >> lane) & 1u) ? y[i] : -INFINITY;
+                        }
+                    } else if (!here) {
+#pragma unroll
+                        for (int i = 0; i < RW; ++i) y[i] = -INFINITY;
+                    }
+                };
+                float top = -INFINITY;
+                if (ok) {
+                    fence_after();
+                    if (!tail && here) sc = sh.scale[slot0][tok >> P.box_log2];
+                    exponents(true);
+                    mask();
+#pragma unroll
+                    for (int i = 0; i < RW; i += 2) top = max3(top, y[i], y[i + 1]);
+                }
+                if (group_or<128>(bar, top > kTop || !ok)) {
+                    if (group_or<128>(bar, !ok)) {
+                        dead = true;
+                        continue;
+                    }
+                    // raise M of the rows whose maximum grew
+                    exponents(false);
+                    mask();
+                    int mine = order_of(-INFINITY);
+#pragma unroll
+                    for (int i = 0; i < RW; ++i) {
+                        const int m = __reduce_max_sync(0xffffffffu, order_of(y[i]));
+                        if (lane == i) mine = m;
+                    }
+                    if (lane < RW) sh.rmax[g][wq][lane] = mine;
+                    group_sync<128>(bar);
+                    if (gi < RW) {
+                        const float m = of_order(max(max(sh.rmax[g][0][gi], sh.rmax[g][1][gi]),
+                                                     max(sh.rmax[g][2][gi], sh.rmax[g][3][gi])));
+                        const float was = -sh.neg_m[g][gi], now = fmaxf(was, m - kAim);
+                        sh.fac[g][gi] = was == now ? 1.f : exp2f(was - now);
+                        sh.neg_m[g][gi] = -now;
+                    }
+                    group_sync<128>(bar);
+#pragma unroll
+                    for (int i = 0; i < RW; ++i) {
+                        l[i] *= sh.fac[g][i];
+                        y[i] += sh.neg_m[g][i];
+                    }
+                    if (k - k0 >= (kAlt ? 2 : 1)) {        // O holds earlier steps
+                        if (!kAlt)
+                            ok = mbar_wait_warp(&sh.o_upd[(k - 1) & 1], (uint32_t)(((k - 1) >> 1) & 1),
+                                                T.wait);
+                        if (ok) {
+                            fence_after();
+#pragma unroll 1
+                            for (int e = 0; e < 2 * RW; e += CH) {
+                                uint32_t x[CH];
+                                const uint32_t at = to + (uint32_t)(g * 2 * RW + e);
+                                ldn<CH>(at, x);
+                                wait_ldn<CH>(x);
+#pragma unroll
+                                for (int i = 0; i < CH; ++i)
+                                    x[i] = __float_as_uint(__uint_as_float(x[i]) *
+                                                           sh.fac[g][(e & (RW - 1)) + i]);
+                                stn<CH>(at, x);
+                            }
+                            wait_st();
+                        }
+                    }
+                }
+                {
+                    const uint64_t is2 = pair(sc.z, sc.z);
+#pragma unroll
+                    for (int i = 0; i < RW; i += 2) {
+                        y[i] = fast_exp2(y[i]);
+                        y[i + 1] = fast_exp2(y[i + 1]);
+                        unpair(fma2(pair(y[i], y[i + 1]), is2, pair(l[i], l[i + 1])), l[i], l[i + 1]);
+                    }
+                }
+                if (__any_sync(0xffffffffu, sc.w != sc.w)) {
+                    // a NaN value scale: NaN in the rows that see the token
+#pragma unroll
+                    for (int i = 0; i < RW; ++i) {
+                        const uint32_t row = __shfl_sync(0xffffffffu, seen, i);
+                        if (here && (!tail || ((row >> lane) & 1u))) y[i] += sc.w;
+                    }
+                }
+                if (ok) {
+                    uint8_t *prow = pbuf + (k & 1) * C::kP + tok * 128;
+                    uint32_t w[RW / 2];                 // first parts, then second parts
+#pragma unroll
+                    for (int i = 0; i < RW; i += 4) {
+                        uint32_t h0, l0, h1, l1;
+                        split_p(y[i], y[i + 1], h0, l0);
+                        split_p(y[i + 2], y[i + 3], h1, l1);
+                        w[i / 4] = h0 | (h1 << 16);
+                        w[RW / 4 + i / 4] = l0 | (l1 << 16);
+                    }
+                    const int q0 = kAlt ? 0 : g * (RW / 8);
+#pragma unroll
+                    for (int q = 0; q < RW / 8; ++q)
+                        *reinterpret_cast<uint4 *>(prow + (((q0 + q) ^ (tok & 7)) << 4)) =
+                            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                    // V rows past the last token hold whatever the copy left: P
+                    // is 0 there, but 0 x NaN is NaN
+                    if (!here && (kAlt || g == 0)) {
+                        for (int part = 0; part < (tail ? 2 : 1); ++part) {
+                            const int sl = slot0 + part >= NS ? slot0 + part - NS : slot0 + part;
+                            uint4 *vr = reinterpret_cast<uint4 *>(ring + sl * C::kSlot + kv8_row(tok, 1, D));
+#pragma unroll
+                            for (int e = 0; e < D / 16; ++e) vr[e] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_full[k & 1]);
+                }
+            }
+
+            // --- the unit's end in this range: PV(k - 1) and all before it, the
+            // row sums over the tokens' threads, then O / l and LSE, or the
+            // partials (two running softmaxes merged where the groups alternate)
+            const int j = k - 1;
+            // (alternating groups: step j's waits, the other follows by the barrier)
+            const bool got = !dead && ok &&
+                             ((kAlt && (j & 1) != g) ||
+                              mbar_wait_warp(&sh.o_upd[j & 1], (uint32_t)((j >> 1) & 1), T.wait));
+            constexpr int kPer = 32 / RW;
+            const float sum = warp_sums<RW>(l);
             if (lane % kPer == 0) sh.rsum[g][wq][lane / kPer] = sum;
-            if (group_or(bar, !got)) return false;
+            if (group_or<256>(3, !got)) {
+                ok = false;
+                break;
+            }
             fence_after();
-            const size_t prow = slot_row(T, seg_id, cta, 0, 1, g * HR);
-            if (gi < HR) {
-                const float L = (sh.rsum[g][0][gi] + sh.rsum[g][1][gi]) +
-                                (sh.rsum[g][2][gi] + sh.rsum[g][3][gi]);
-                const float M = -sh.neg_m[g][gi];
-                const int out = sh.out[g][gi];
+            const size_t prow = slot_row(T, seg_id, cta, 0, 1, 0);
+            if (threadIdx.x < RB) {
+                const int r = threadIdx.x, rg = kAlt ? 0 : r / RW, ri = kAlt ? r : r % RW;
+                auto row_sum = [&](int q) {
+                    return (sh.rsum[q][0][ri] + sh.rsum[q][1][ri]) + (sh.rsum[q][2][ri] + sh.rsum[q][3][ri]);
+                };
+                float M = -sh.neg_m[rg][ri], L = row_sum(rg), f0 = 1.f, f1 = 0.f;
+                if (kAlt) {
+                    const float m0 = M, m1 = -sh.neg_m[1][ri];
+                    M = fmaxf(m0, m1);
+                    f0 = exp2f(m0 - M);
+                    f1 = exp2f(m1 - M);
+                    L = f0 * L + f1 * row_sum(1);
+                }
+                const int out = sh.out[rg][ri];
                 const bool none = !(out & 1) || L == 0.f;
-                sh.fac[g][gi] = none ? 0.f : 1.f / L;
+                const float inv = !seg_whole ? 1.f : none ? 0.f : 1.f / L;
+                sh.fac[rg][ri] = f0 * inv;
+                if (kAlt) sh.fac[1][ri] = f1 * inv;
                 if (seg_whole && out >= 0) {
                     const int hq = (out >> 1) % A.Hq, rr = (out >> 1) / A.Hq;
                     A.lse[((size_t)seg_b * A.Hq + hq) * A.R + rr] =
                         none ? -INFINITY : (M + log2f(L)) * kLn2;
                 } else if (!seg_whole) {
-                    *reinterpret_cast<float2 *>(A.part_ml + (prow + gi) * 2) = make_float2(M, L);
+                    *reinterpret_cast<float2 *>(A.part_ml + (prow + r) * 2) = make_float2(M, L);
                 }
             }
-            group_sync(bar);
-            uint32_t hi[HR], lo[HR];
-            const uint32_t to = tmem + lane_base + (uint32_t)(g * RB);
-            ldn<HR>(to, hi);
-            ldn<HR>(to + HR, lo);
-            wait_ldn<HR>(hi, lo);
-            if (tok < D) {
-                if (seg_whole) {
+            group_sync<256>(3);
+            // warpgroup g writes rows (RB / 2) g ..
+            constexpr int HB = RB / 2, CE = HB < 16 ? HB : 16;
+#pragma unroll 1
+            for (int i0 = g * HB; i0 < (g + 1) * HB; i0 += CE) {
+                uint32_t a0[CE], b0[CE], a1[CE], b1[CE];
+                const int og = kAlt ? 0 : g, oi = kAlt ? i0 : i0 - g * RW;
+                ldn<CE>(to + (uint32_t)(og * 2 * RW + oi), a0);
+                ldn<CE>(to + (uint32_t)(og * 2 * RW + RW + oi), b0);
+                wait_ldn<CE>(a0, b0);
+                if constexpr (kAlt) {
+                    ldn<CE>(to + (uint32_t)(2 * RW + oi), a1);
+                    ldn<CE>(to + (uint32_t)(3 * RW + oi), b1);
+                    wait_ldn<CE>(a1, b1);
+                }
+                if (tok < D) {
                     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(A.o) + (size_t)seg_b * A.R * A.Hq * D + tok;
+                    float *po = A.part_o + (prow + i0) * D + tok;
 #pragma unroll
-                    for (int i = 0; i < HR; ++i) {
-                        const int out = sh.out[g][i];
-                        if (out < 0) break;              // (rows past the last are at the end)
-                        const float inv = sh.fac[g][i];
-                        const float x = fmaf(__uint_as_float(lo[i]), 1.f / kLoUp, __uint_as_float(hi[i]));
-                        o[(size_t)(out >> 1) * D] = __float2bfloat16_rn(inv == 0.f ? 0.f : x * inv);
+                    for (int i = 0; i < CE; ++i) {
+                        const float f0 = sh.fac[og][oi + i];
+                        // (a factor of 0: nothing seen, and O may hold anything)
+                        float x = f0 == 0.f ? 0.f
+                                            : f0 * fmaf(__uint_as_float(b0[i]), 1.f / kLoUp,
+                                                        __uint_as_float(a0[i]));
+                        if constexpr (kAlt) {
+                            const float f1 = sh.fac[1][oi + i];
+                            if (f1 != 0.f)
+                                x = fmaf(f1, fmaf(__uint_as_float(b1[i]), 1.f / kLoUp,
+                                                  __uint_as_float(a1[i])), x);
+                        }
+                        if (seg_whole) {
+                            const int out = sh.out[og][oi + i];
+                            if (out >= 0) o[(size_t)(out >> 1) * D] = __float2bfloat16_rn(x);
+                        } else {
+                            po[i * D] = x;
+                        }
                     }
-                } else {
-                    float *o = A.part_o + prow * D + tok;
-#pragma unroll
-                    for (int i = 0; i < HR; ++i)
-                        o[i * D] = fmaf(__uint_as_float(lo[i]), 1.f / kLoUp, __uint_as_float(hi[i]));
                 }
             }
             fence_before();
-            return true;
-        };
-
-        float2 meta = make_float2(0.f, 0.f);     // the next unit's row gi, loaded ahead
-        if (gi < HR) meta = P.q_meta[(size_t)unit_of(c) * RB + g * HR + gi];
-        for (; k < n_steps; ++k) {
-            const bool new_unit = k == 0 || c.tile == 0;
-            if (new_unit) {
-                if (k > 0 && !epilogue(k - 1)) {
-                    ok = false;
-                    break;
-                }
-                seg_b = c.b;
-                seg_h = c.h;
-                seg_id = unit_of(c);
-                seg_whole = c.tile == 0 && k + c.n_tiles <= n_steps;
-                group_sync(bar);               // the last unit's rows are read
-                if (gi < HR) {
-                    sh.out[g][gi] = __float_as_int(meta.y);
-                    sh.qs[g][gi] = meta.x;
-                    sh.neg_m[g][gi] = -kNoRef;
-                }
-                group_sync(bar);
-#pragma unroll
-                for (int i = 0; i < HR; ++i) l[i] = 0.f;
-            }
-            const Step8 s = step_at(P, c);
-            cursor_next(T, c);
-            if (c.tile == 0 && k + 1 < n_steps && gi < HR)
-                meta = P.q_meta[(size_t)unit_of(c) * RB + g * HR + gi];
-            const int slot0 = slot, parts = s.tail ? 2 : 1;
-            // rows' visibility of this warp's 32 tail tokens, lane i: row i
-            uint32_t seen = 0u;
-            float4 sc = make_float4(0.f, 0.f, 1.f, 0.f);
-            const bool here = tok < s.n;
-            if (s.tail) {
-                const int tt0 = s.tile * kStep + wq * 32;
-                if (here) {
-                    const float2 x = P.tail_scale[((size_t)seg_b * A.Hkv + seg_h) * P.tail_pad + tt0 + lane];
-                    sc = token_scale(x.x, x.y);
-                }
-                const int out = lane < HR ? sh.out[g][lane] : -1;
-                if (out >= 0 && (out & 1)) {
-                    const int rr = (out >> 1) / A.Hq;
-                    const uint32_t *vr = A.vis + ((size_t)seg_b * A.R + rr) * A.W;
-                    auto word = [&](int w) {
-                        if (w < 0 || w >= A.W) return 0u;
-                        const int left = A.R - w * 32;          // columns from the word's first
-                        return left >= 32 ? vr[w] : vr[w] & ((1u << left) - 1u);
-                    };
-                    // block columns c0 .. c0 + 31
-                    const int c0 = tt0 - A.n_soft, sft = c0 & 31, w0 = c0 >> 5;     // (floor)
-                    seen = word(w0) >> sft;
-                    if (sft) seen |= word(w0 + 1) << (32 - sft);
-                    const int ns = A.n_soft - tt0;              // soft tokens from here on
-                    if (ns > 0 && (A.row_flags[(size_t)seg_b * A.R + rr] & SPEC_ROW_SEES_SOFT))
-                        seen |= ns >= 32 ? 0xffffffffu : (1u << ns) - 1u;
-                }
-            }
-            if (ok) {
-                // S, and the slots' own barriers for the scales and for the
-                // rows cleared below.  S(k) was issued behind PV(k - 2), so its
-                // barrier also frees the P buffer written below.
-                ok = mbar_wait(&sh.s_full[k & 1], (uint32_t)((k >> 1) & 1), T.wait);
-                for (int part = 0; part < parts; ++part) {
-                    ok = ok && mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait);
-                    if (++slot == NS) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
-                }
-                ok = __all_sync(0xffffffffu, ok);
-            }
-            const uint32_t ts = tmem + lane_base + C::kColS * (1 + (uint32_t)(k & 1)) + (uint32_t)(g * HR);
-            float y[HR];
-            // y = s x (key scale, softmax scale) + log2(value scale) [- M]: the
-            // exponents of P, from the two parts of S
-            auto exponents = [&](bool less_m) {
-                uint32_t hi[HR], lo[HR];
-                ldn<HR>(ts, hi);
-                ldn<HR>(ts + RB, lo);
-                wait_ldn<HR>(hi, lo);
-                const uint64_t sk2 = pair(sc.x, sc.x), lv2 = pair(sc.y, sc.y);
-#pragma unroll
-                for (int i = 0; i < HR; i += 4) {
-                    const float4 q = *reinterpret_cast<const float4 *>(&sh.qs[g][i]);
-                    float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (less_m) m = *reinterpret_cast<const float4 *>(&sh.neg_m[g][i]);
-                    const uint64_t z0 = pair(0.f, 0.f);
-                    uint64_t r0 = fma2(add2(pair(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
-                                            pair(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1]))),
-                                       fma2(pair(q.x, q.y), sk2, z0), add2(pair(m.x, m.y), lv2));
-                    uint64_t r1 =
-                        fma2(add2(pair(__uint_as_float(hi[i + 2]), __uint_as_float(hi[i + 3])),
-                                  pair(__uint_as_float(lo[i + 2]), __uint_as_float(lo[i + 3]))),
-                             fma2(pair(q.z, q.w), sk2, z0), add2(pair(m.z, m.w), lv2));
-                    unpair(r0, y[i], y[i + 1]);
-                    unpair(r1, y[i + 2], y[i + 3]);
-                }
-            };
-            // -inf for what a row does not see
-            auto mask = [&] {
-                if (s.tail) {
-#pragma unroll
-                    for (int i = 0; i < HR; ++i) {
-                        const uint32_t row = __shfl_sync(0xffffffffu, seen, i);
-                        y[i] = here && ((row >> lane) & 1u) ? y[i] : -INFINITY;
-                    }
-                } else if (!here) {
-#pragma unroll
-                    for (int i = 0; i < HR; ++i) y[i] = -INFINITY;
-                }
-            };
-            float top = -INFINITY;
-            if (ok) {
-                fence_after();
-                if (!s.tail && here) sc = sh.scale[slot0][tok >> P.box_log2];
-                exponents(true);
-                mask();
-#pragma unroll
-                for (int i = 0; i < HR; i += 2) top = max3(top, y[i], y[i + 1]);
-            }
-            if (group_or(bar, top > kTop || !ok)) {
-                if (group_or(bar, !ok)) {
-                    ok = false;
-                    break;
-                }
-                // raise M of the rows whose maximum grew
-                exponents(false);
-                mask();
-                int mine = order_of(-INFINITY);
-#pragma unroll
-                for (int i = 0; i < HR; ++i) {
-                    const int m = __reduce_max_sync(0xffffffffu, order_of(y[i]));
-                    if (lane == i) mine = m;
-                }
-                if (lane < HR) sh.rmax[g][wq][lane] = mine;
-                group_sync(bar);
-                if (gi < HR) {
-                    const float m = of_order(max(max(sh.rmax[g][0][gi], sh.rmax[g][1][gi]),
-                                                 max(sh.rmax[g][2][gi], sh.rmax[g][3][gi])));
-                    const float was = -sh.neg_m[g][gi], now = fmaxf(was, m - kAim);
-                    sh.fac[g][gi] = was == now ? 1.f : exp2f(was - now);
-                    sh.neg_m[g][gi] = -now;
-                }
-                group_sync(bar);
-#pragma unroll
-                for (int i = 0; i < HR; ++i) {
-                    l[i] *= sh.fac[g][i];
-                    y[i] += sh.neg_m[g][i];
-                }
-                if (!new_unit) {
-                    ok = mbar_wait_warp(&sh.o_upd[(k - 1) & 1], (uint32_t)(((k - 1) >> 1) & 1), T.wait);
-                    if (ok) {
-                        fence_after();
-                        const uint32_t to = tmem + lane_base + (uint32_t)(g * RB);
-#pragma unroll 1
-                        for (int e = 0; e < RB; e += HR) {       // first parts, second parts
-                            uint32_t x[HR];
-                            ldn<HR>(to + e, x);
-                            wait_ldn<HR>(x);
-#pragma unroll
-                            for (int i = 0; i < HR; ++i)
-                                x[i] = __float_as_uint(__uint_as_float(x[i]) * sh.fac[g][i]);
-                            stn<HR>(to + e, x);
-                        }
-                        wait_st();
-                    }
-                }
-            }
-            {
-                const uint64_t is2 = pair(sc.z, sc.z);
-#pragma unroll
-                for (int i = 0; i < HR; i += 2) {
-                    y[i] = fast_exp2(y[i]);
-                    y[i + 1] = fast_exp2(y[i + 1]);
-                    unpair(fma2(pair(y[i], y[i + 1]), is2, pair(l[i], l[i + 1])), l[i], l[i + 1]);
-                }
-            }
-            if (__any_sync(0xffffffffu, sc.w != sc.w)) {
-                // a NaN value scale: NaN in the rows that see the token
-#pragma unroll
-                for (int i = 0; i < HR; ++i) {
-                    const uint32_t row = __shfl_sync(0xffffffffu, seen, i);
-                    if (here && (!s.tail || ((row >> lane) & 1u))) y[i] += sc.w;
-                }
-            }
-            if (ok) {
-                uint8_t *prow = pbuf + (k & 1) * C::kP + tok * 128;
-                uint32_t w[RB / 4];                 // first parts, then second parts
-#pragma unroll
-                for (int i = 0; i < HR; i += 4) {
-                    uint32_t h0, l0, h1, l1;
-                    split_p(y[i], y[i + 1], h0, l0);
-                    split_p(y[i + 2], y[i + 3], h1, l1);
-                    w[i / 4] = h0 | (h1 << 16);
-                    w[HR / 4 + i / 4] = l0 | (l1 << 16);
-                }
-                if constexpr (RB == 8) {
-                    *reinterpret_cast<uint2 *>(prow + ((tok & 7) << 4) + g * 8) = make_uint2(w[0], w[1]);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < RB / 16; ++q)
-                        *reinterpret_cast<uint4 *>(prow + (((g * (RB / 16) + q) ^ (tok & 7)) << 4)) =
-                            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-                }
-                // V rows past the last token hold whatever the copy left: P is
-                // 0 there, but 0 x NaN is NaN
-                if (!here && g == 0) {
-                    int sl = slot0;
-                    for (int part = 0; part < parts; ++part) {
-                        uint4 *vr = reinterpret_cast<uint4 *>(ring + sl * C::kSlot + kv8_row(tok, 1, D));
-#pragma unroll
-                        for (int e = 0; e < D / 16; ++e) vr[e] = make_uint4(0u, 0u, 0u, 0u);
-                        sl = sl + 1 == NS ? 0 : sl + 1;
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[k & 1]);
-            }
+            group_sync<256>(3);              // O, M and l may be written again
         }
-        // (a warpgroup leaves the loop together or runs it to its end)
-        if (k == n_steps && !epilogue(k - 1)) ok = false;
         if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
     }
     fence_before();
