@@ -50,7 +50,7 @@ using namespace tc5;
 
 constexpr int kStep = 128;                  // tokens a step
 constexpr int kTcThreads = 12 * 32;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kRecWarp = 10, kScaleWarp = 11;
+constexpr int kProducerWarp = 8, kScoreWarp = 9, kValueWarp = 10, kProducerWarp2 = 11;
 constexpr float kTop = 8.75f;               // log2 of the largest P allowed (448 = 2^8.807)
 constexpr float kAim = 7.f;                 // log2 P of a row's maximum when M is raised
 constexpr float kNoRef = -1e30f;            // M of a row that has seen nothing
@@ -96,7 +96,7 @@ struct Shared8 {
     uint64_t full[C::NS], empty[C::NS];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], o_upd[2];
-    uint64_t drain;
+    uint64_t drain[2];
     float4 scale[C::NS][8];              // token_scale of each box of a slot
     alignas(16) float qs[2][C::RW];      // a row's q_scale
     alignas(16) float neg_m[2][C::RW];   // and its -M
@@ -213,7 +213,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&sh.full[s], 2);           // the copies, the scales
+            mbar_init(&sh.full[s], 2);           // the two producers
             mbar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -223,11 +223,12 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             mbar_init(&sh.p_full[b], C::kAlt ? 4 : 8);
             mbar_init(&sh.o_upd[b], 1);
         }
-        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.drain[0], 1);
+        mbar_init(&sh.drain[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sh.tmem_base)),
                      "r"(C::kCols));
@@ -250,20 +251,25 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
 
     const int n_steps = (int)(t_end - t_begin);
 
-    if (warp == kRecWarp) {
+    // (by the warp whose first work comes last)
+    if (warp == kValueWarp) {
         const BoundaryRec rec = warp_boundary_record(T, ws, cta, t_begin, t_end);
         if (lane == 0) T.recs[cta] = rec;
-    } else if (n_steps > 0 && (warp == kProducerWarp || warp == kScaleWarp)) {
-        // ------------------------------------- producer: copies, and scales
-        // Both warps walk the range in groups of up to four prefix steps of a
-        // unit (or one tail step): lane 8 u + i owns box i of the group's step
-        // u, so a page id costs one load per lane and group, issued a group
-        // ahead of its use (and the scale warp's scales another group).
-        const bool copies = warp == kProducerWarp;
+    }
+
+    if (n_steps > 0 && (warp == kProducerWarp || warp == kProducerWarp2)) {
+        // ------------------------------------------------------ producers
+        // Two warps, each with every other box of a step (a copy costs its
+        // issuing warp about 100 cycles): the box's copy and its scales.
+        // They walk the range in groups of up to eight prefix steps of a unit
+        // (or one tail step): lane 4 u + i owns box 2 i + w of the group's
+        // step u, so a page id costs one load per lane and group, issued two
+        // groups ahead of its copy, and a scale one, issued a group ahead.
+        const int w = warp == kProducerWarp ? 0 : 1;
         const uint64_t keep = policy_evict_last();
         const uint64_t stream = T.seg_rb == 1 ? policy_evict_first() : keep;
         const int bt = 1 << P.box_log2, boxes = kStep >> P.box_log2;
-        const int u = lane >> 3, box = lane & 7;
+        const int u = lane >> 2, box = 2 * (lane & 3) + w;
         struct Group {
             Cursor c;            // its first step
             int k, n;            // that step's number, steps (0: past the range)
@@ -281,11 +287,11 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             if (k >= n_steps) return g;
             const int np = (c.S + kStep - 1) / kStep;
             g.tail = c.tile >= np;
-            g.n = g.tail ? 1 : min(min(4, np - c.tile), n_steps - k);
+            g.n = g.tail ? 1 : min(min(8, np - c.tile), n_steps - k);
             const int tok = (c.tile + u) * kStep + (box << P.box_log2);
             if (!g.tail && u < g.n && box < boxes && tok < c.S) {
-                const int w = tok >> 4, j = (int)((w * P.ps16_inv) >> 32);
-                g.row = (w - j * P.ps16) * 32;
+                const int t16 = tok >> 4, j = (int)((t16 * P.ps16_inv) >> 32);
+                g.row = (t16 - j * P.ps16) * 32;
                 const int pg = A.page_table[(size_t)c.b * A.max_pages + j];
                 g.pg = pg < 0 || pg >= A.n_pages ? -2 : pg;
             }
@@ -306,42 +312,38 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         Cursor c0;
         cursor_init(T, ws, t_begin, c0);
         Group cur = group_at(c0, 0), next = after(cur);
-        float2 sc = make_float2(1.f, 1.f), sc1 = sc;
-        if (!copies) sc = scale_of(cur);
+        float2 sc = scale_of(cur);
         int slot = 0, phase = 0, nq = 0;
         long long used = 0;                          // ring slots taken so far
         bool ok = true;
         while (cur.n > 0 && ok) {
             const Group far = after(next);
-            float4 ts;
-            if (copies) {
-                if (cur.pg == -2) raise_status(A.status, SPEC_DEV_BAD_PAGE);
-                if (cur.c.tile == 0 || cur.k == 0) {
-                    // the unit's queries, once the unit two back is done with
-                    // the buffer
-                    const int qb = nq & 1;
-                    bool got = true;
-                    if (lane == 0) {
-                        got = nq < 2 ||
-                              mbar_wait(&sh.q_empty[qb], (uint32_t)(((nq >> 1) - 1) & 1), T.wait);
-                        if (got) {
-                            mbar_arrive_expect_tx(&sh.q_full[qb], C::kQ);
-                            tma_load_2d(qbuf + qb * C::kQ, &m_q, 0, unit_of(cur.c) * (2 * RB),
-                                        &sh.q_full[qb], keep);
-                        }
+            const float2 sc1 = scale_of(next);
+            const float4 ts = token_scale(kv8_read_scale(sc.x), kv8_read_scale(sc.y));
+            if (cur.pg == -2) raise_status(A.status, SPEC_DEV_BAD_PAGE);
+            if (w == 0 && (cur.c.tile == 0 || cur.k == 0)) {
+                // the unit's queries, once the unit two back is done with the
+                // buffer
+                const int qb = nq & 1;
+                bool got = true;
+                if (lane == 0) {
+                    got = nq < 2 || mbar_wait(&sh.q_empty[qb], (uint32_t)(((nq >> 1) - 1) & 1), T.wait);
+                    if (got) {
+                        mbar_arrive_expect_tx(&sh.q_full[qb], C::kQ);
+                        tma_load_2d(qbuf + qb * C::kQ, &m_q, 0, unit_of(cur.c) * (2 * RB), &sh.q_full[qb],
+                                    keep);
                     }
-                    if (!__shfl_sync(0xffffffffu, got, 0)) {
-                        ok = false;
-                        break;
-                    }
-                    ++nq;
                 }
-            } else {
-                sc1 = scale_of(next);
-                ts = token_scale(kv8_read_scale(sc.x), kv8_read_scale(sc.y));
+                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                    ok = false;
+                    break;
+                }
+                ++nq;
             }
             const unsigned boxed = __ballot_sync(0xffffffffu, cur.pg >= 0);
             const int np = (cur.c.S + kStep - 1) / kStep, tile0 = cur.c.tile - np;   // (tail)
+            // tail tiles: boxes of 16 tokens, nb of them, this warp's nw
+            const int nb = (min(kStep, P.tail_len - tile0 * kStep) + 15) >> 4, nw = (nb + 1 - w) >> 1;
             const int slots = cur.tail ? 2 : cur.n;
             for (int i = 0; i < slots; ++i) {
                 bool got = true;
@@ -351,27 +353,24 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     break;
                 }
                 uint8_t *dst = ring + slot * C::kSlot;
-                if (!copies) {
-                    if (!cur.tail && u == i && box < boxes) sh.scale[slot][box] = ts;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.full[slot]);
-                } else if (cur.tail) {
-                    // part i of the tail tile: boxes of 16 tokens
-                    const int n = min(kStep, P.tail_len - tile0 * kStep), nb = (n + 15) >> 4;
-                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], (uint32_t)(nb * 32 * D));
-                    __syncwarp();
-                    if (lane < nb)
-                        tma_load_2d(dst + lane * 32 * D, &m_tail, 0,
+                const bool mine = u == i && box < boxes && !cur.tail;
+                if (mine) sh.scale[slot][box] = ts;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&sh.full[slot],
+                                          cur.tail ? (uint32_t)(nw * 32 * D)
+                                                   : (uint32_t)__popc((boxed >> (4 * i)) & 0xfu) *
+                                                         (uint32_t)(2 * bt * D));
+                __syncwarp();
+                if (cur.tail) {
+                    if (u == 0 && box < nb)
+                        tma_load_2d(dst + box * 32 * D, &m_tail, 0,
                                     ((cur.c.b * A.Hkv + cur.c.h) * 2 + i) * (2 * P.tail_pad) +
-                                        tile0 * (2 * kStep) + lane * 32,
+                                        tile0 * (2 * kStep) + box * 32,
                                     &sh.full[slot], keep);
-                } else {
-                    const uint32_t bytes = (uint32_t)__popc((boxed >> (8 * i)) & 0xffu) * (uint32_t)(2 * bt * D);
-                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
-                    __syncwarp();
-                    if (u == i && cur.pg >= 0)
-                        tma_load_3d(dst + box * (2 * bt * D), &m_kv, 0, cur.row, cur.pg * A.Hkv + cur.c.h,
-                                    &sh.full[slot], stream);
+                } else if (mine && cur.pg >= 0) {
+                    tma_load_3d(dst + box * (2 * bt * D), &m_kv, 0, cur.row, cur.pg * A.Hkv + cur.c.h,
+                                &sh.full[slot], stream);
                 }
                 ++used;
                 if (++slot == NS) {
@@ -387,104 +386,117 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
             // do not leave while copies into this CTA's shared memory are in
             // flight (the default limit: these copies were issued and complete)
-            if (copies) {
-                for (long long i = used - 1; i >= 0 && i >= used - NS; --i)
-                    if (!mbar_wait(&sh.full[i % NS], (uint32_t)((i / NS) & 1))) {
-                        raise_status(A.status, SPEC_DEV_TIMEOUT);
-                        break;
-                    }
-                for (int n = nq - 1; n >= 0 && n >= nq - 2; --n)
-                    if (!mbar_wait(&sh.q_full[n & 1], (uint32_t)((n >> 1) & 1))) {
-                        raise_status(A.status, SPEC_DEV_TIMEOUT);
-                        break;
-                    }
-            }
+            for (long long i = used - 1; i >= 0 && i >= used - NS; --i)
+                if (!mbar_wait(&sh.full[i % NS], (uint32_t)((i / NS) & 1))) {
+                    raise_status(A.status, SPEC_DEV_TIMEOUT);
+                    break;
+                }
+            for (int n = nq - 1; n >= 0 && n >= nq - 2; --n)
+                if (!mbar_wait(&sh.q_full[n & 1], (uint32_t)((n >> 1) & 1))) {
+                    raise_status(A.status, SPEC_DEV_TIMEOUT);
+                    break;
+                }
         }
-    } else if (n_steps > 0 && warp == kMmaWarp) {
-        // ----------------------------------------------------- MMA issuer
+    } else if (n_steps > 0 && (warp == kScoreWarp || warp == kValueWarp)) {
+        // ---------------------------------------------------- MMA issuers
+        // One thread issues S, another PV (one alone took ~2000 cycles a step,
+        // more than the tile takes to stream).  Slot: 8-token groups of 8 key
+        // rows, then 8 value rows, D bytes each.  K (K-major): groups 16 D
+        // apart, a step of 32 head dimensions 32 bytes on.  V (MN-major): the
+        // same groups, 8 D further; a step of 32 tokens is four groups.  At
+        // D = 64 the 128 rows of M are the 64 dimensions twice (leading
+        // offset 0).
+        const bool scores = warp == kScoreWarp;
         Cursor c;
         cursor_init(T, ws, t_begin, c);       // warp-collective
         if (lane == 0) {
             constexpr uint32_t id_s = idesc_e4m3(kStep, 2 * RB, false, false);
             constexpr uint32_t id_pv = idesc_e4m3(kStep, 2 * RB, true, true);
-            // slot: 8-token groups of 8 key rows, then 8 value rows, D bytes
-            // each.  K (K-major): groups 16 D apart, a step of 32 head
-            // dimensions 32 bytes on.  V (MN-major): the same groups, 8 D
-            // further; a step of 32 tokens is four groups.  At D = 64 the 128
-            // rows of M are the 64 dimensions twice (leading offset 0).
             const uint64_t kd0 = smem_desc_sw<D>(smem_u32(ring), 16, 16 * D);
             const uint64_t vd0 = smem_desc_sw<D>(smem_u32(ring) + 8 * D, 0, 16 * D);
             const uint64_t qd0 = smem_desc_sw<D>(smem_u32(qbuf), 16, 8 * D);
             const uint64_t pd0 = smem_desc(smem_u32(pbuf), 0, 1024);
-            int nq = 0, slot = 0, phase = 0, prev_slot = 0, prev_parts = 1, k = 0;
-            bool ok = true, prev_first = true;
-            auto issue_pv = [&](int j) -> bool {
-                const int b = j & 1;
-                if (!mbar_wait(&sh.p_full[b], (uint32_t)((j >> 1) & 1), T.wait)) return false;
-                fence_after();
-                const uint64_t pd = pd0 + (uint64_t)((b * C::kP) >> 4);
-                const uint32_t to = tmem + (C::kAlt ? (uint32_t)(b * 2 * RW) : 0u);
-                int sl = prev_slot;
-                for (int part = 0; part < prev_parts; ++part) {
-                    const uint64_t vd = vd0 + (uint64_t)((sl * C::kSlot) >> 4);
-#pragma unroll
-                    for (int e = 0; e < kStep / 32; ++e)
-                        mma8_ss(to, vd + (uint64_t)((e * 4 * 16 * D) >> 4),
-                                pd + (uint64_t)((e * 4 * 1024) >> 4), id_pv,
-                                (e > 0 || part > 0 || !prev_first) ? 1u : 0u);
-                    commit(&sh.empty[sl]);
-                    sl = sl + 1 == NS ? 0 : sl + 1;
-                }
-                commit(&sh.o_upd[b]);
-                return true;
-            };
+            int nq = 0, slot = 0, phase = 0, k = 0;
+            bool ok = true;
             while (ok && k < n_steps) {
                 // a unit's steps of this range
                 const int k0 = k, n = min(n_steps - k, c.n_tiles - c.tile);
                 const int n_prefix = (c.S + kStep - 1) / kStep - c.tile;     // of them prefix steps
                 const int qb = nq & 1;
-                if (!mbar_wait(&sh.q_full[qb], (uint32_t)((nq >> 1) & 1), T.wait)) {
+                if (scores && !mbar_wait(&sh.q_full[qb], (uint32_t)((nq >> 1) & 1), T.wait)) {
                     ok = false;
                     break;
                 }
                 ++nq;
                 const uint64_t qd = qd0 + (uint64_t)((qb * C::kQ) >> 4);
                 for (int i = 0; i < n; ++i, ++k) {
-                    const int first_slot = slot, parts = i >= n_prefix ? 2 : 1;
-                    const uint32_t ts = tmem + C::kColS + (uint32_t)((k & 1) * 2 * RB);
-                    for (int part = 0; part < parts; ++part) {
-                        if (!mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait)) {
+                    const int parts = i >= n_prefix ? 2 : 1, b = k & 1;
+                    if (scores) {
+                        // S buffer b has been read when P(k - 2) is there
+                        if (k >= 2 && !mbar_wait(&sh.p_full[b], (uint32_t)(((k - 2) >> 1) & 1), T.wait)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t ts = tmem + C::kColS + (uint32_t)(b * 2 * RB);
+                        for (int part = 0; part < parts; ++part) {
+                            if (!mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait)) {
+                                ok = false;
+                                break;
+                            }
+                            fence_after();
+                            const uint64_t kd = kd0 + (uint64_t)((slot * C::kSlot) >> 4);
+#pragma unroll
+                            for (int e = 0; e < D / 32; ++e)
+                                mma8_ss(ts, kd + (uint64_t)(e * 32 >> 4), qd + (uint64_t)(e * 32 >> 4),
+                                        id_s, (e > 0 || part > 0) ? 1u : 0u);
+                            if (++slot == NS) {
+                                slot = 0;
+                                phase ^= 1;
+                            }
+                        }
+                        if (!ok) break;
+                        commit(&sh.s_full[b]);
+                        if (i == n - 1) commit(&sh.q_empty[qb]);
+                    } else {
+                        if (!mbar_wait(&sh.p_full[b], (uint32_t)((k >> 1) & 1), T.wait)) {
                             ok = false;
                             break;
                         }
                         fence_after();
-                        const uint64_t kd = kd0 + (uint64_t)((slot * C::kSlot) >> 4);
+                        const uint64_t pd = pd0 + (uint64_t)((b * C::kP) >> 4);
+                        const uint32_t to = tmem + (C::kAlt ? (uint32_t)(b * 2 * RW) : 0u);
+                        const bool first = k - k0 < (C::kAlt ? 2 : 1);       // into its O
+                        for (int part = 0; part < parts; ++part) {
+                            // (met: S(k) has read the slot)
+                            if (!mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait)) {
+                                ok = false;
+                                break;
+                            }
+                            const uint64_t vd = vd0 + (uint64_t)((slot * C::kSlot) >> 4);
 #pragma unroll
-                        for (int e = 0; e < D / 32; ++e)
-                            mma8_ss(ts, kd + (uint64_t)(e * 32 >> 4), qd + (uint64_t)(e * 32 >> 4),
-                                    id_s, (e > 0 || part > 0) ? 1u : 0u);
-                        if (++slot == NS) {
-                            slot = 0;
-                            phase ^= 1;
+                            for (int e = 0; e < kStep / 32; ++e)
+                                mma8_ss(to, vd + (uint64_t)((e * 4 * 16 * D) >> 4),
+                                        pd + (uint64_t)((e * 4 * 1024) >> 4), id_pv,
+                                        (e > 0 || part > 0 || !first) ? 1u : 0u);
+                            commit(&sh.empty[slot]);
+                            if (++slot == NS) {
+                                slot = 0;
+                                phase ^= 1;
+                            }
                         }
+                        if (!ok) break;
+                        commit(&sh.o_upd[b]);
                     }
-                    if (!ok) break;
-                    commit(&sh.s_full[k & 1]);
-                    if (i == n - 1) commit(&sh.q_empty[qb]);
-                    if (k > 0 && !(ok = issue_pv(k - 1))) break;
-                    prev_slot = first_slot;
-                    prev_parts = parts;
-                    prev_first = k - k0 < (C::kAlt ? 2 : 1);     // the first into its O
                 }
                 c.tile += n - 1;
                 cursor_next(T, c);
             }
-            if (ok && n_steps > 0) ok = issue_pv(n_steps - 1);
             if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
             // every MMA issued above has completed before TMEM is released
             // (the default limit)
-            commit(&sh.drain);
-            if (!mbar_wait(&sh.drain, 0)) raise_status(A.status, SPEC_DEV_TIMEOUT);
+            uint64_t *drain = &sh.drain[scores ? 0 : 1];
+            commit(drain);
+            if (!mbar_wait(drain, 0)) raise_status(A.status, SPEC_DEV_TIMEOUT);
         }
     } else if (n_steps > 0 && warp < kProducerWarp) {
         // -------------------------------------------------------- softmax
@@ -565,12 +577,12 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     }
                 }
                 if (ok) {
-                    // S, and the slots' own barriers for the scales and for the
-                    // rows cleared below.  S(k) was issued behind PV(k - 2), so
-                    // its barrier also frees the P buffer written below and,
-                    // where the warpgroups alternate, their O.
-                    ok = mbar_wait(&sh.s_full[k & 1], (uint32_t)((k >> 1) & 1), T.wait) &&
-                         mbar_wait(&sh.full[slot0], (uint32_t)phase0, T.wait);
+                    // PV(k - 2) has read the P buffer written below (and, where
+                    // the warpgroups alternate, is in their O); the slots' own
+                    // barriers for the scales and for the rows cleared below; S
+                    ok = (k < 2 || mbar_wait(&sh.o_upd[k & 1], (uint32_t)(((k - 2) >> 1) & 1), T.wait)) &&
+                         mbar_wait(&sh.full[slot0], (uint32_t)phase0, T.wait) &&
+                         mbar_wait(&sh.s_full[k & 1], (uint32_t)((k >> 1) & 1), T.wait);
                     if (tail) {
                         const int s1 = slot0 + 1 == NS ? 0 : slot0 + 1;
                         ok = ok && mbar_wait(&sh.full[s1], (uint32_t)(s1 ? phase0 : phase0 ^ 1), T.wait);
@@ -820,7 +832,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == kMmaWarp)
+    if (warp == kScoreWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(C::kCols));
 }
