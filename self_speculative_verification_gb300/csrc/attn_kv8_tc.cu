@@ -78,7 +78,8 @@ template <int D, int RB>
 struct Cfg {
     static constexpr bool kAlt = RB <= 32;
     static constexpr int RW = kAlt ? RB : RB / 2;       // rows of a warpgroup
-    static constexpr int CH = RW < 16 ? RW : 16;        // rows taken from tensor memory at a time
+    static constexpr int CH = kAlt ? RW : 16;           // rows taken from tensor memory at a time
+    static constexpr int NB = kAlt ? 4 : 3;             // S buffers: S runs ahead of the softmax
     static constexpr int kSlot = 2 * kStep * D;         // K and V of a step
     static constexpr int kQ = 2 * RB * D;               // a unit's queries, both parts
     static constexpr int kP = kStep * 128;              // P^T, rows of 128 bytes
@@ -86,7 +87,7 @@ struct Cfg {
     // TMEM: O of warpgroup g at 2 RW g (first parts, then second parts), S
     // buffer b at kColS + 2 RB b
     static constexpr uint32_t kColS = 4 * RW;
-    static constexpr int kUsed = 4 * RW + 4 * RB;
+    static constexpr int kUsed = 4 * RW + NB * 2 * RB;
     static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
 };
 
@@ -95,7 +96,8 @@ struct Shared8 {
     using C = Cfg<D, RB>;
     uint64_t full[C::NS], empty[C::NS];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], o_upd[2];
+    uint64_t s_full[C::NB], s_free[C::NB];
+    uint64_t p_full[2], o_upd[2];
     uint64_t drain[2];
     float4 scale[C::NS][8];              // token_scale of each box of a slot
     alignas(16) float qs[2][C::RW];      // a row's q_scale
@@ -219,9 +221,12 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.q_full[b], 1);
             mbar_init(&sh.q_empty[b], 1);
-            mbar_init(&sh.s_full[b], 1);
             mbar_init(&sh.p_full[b], C::kAlt ? 4 : 8);
             mbar_init(&sh.o_upd[b], 1);
+        }
+        for (int b = 0; b < C::NB; ++b) {
+            mbar_init(&sh.s_full[b], 1);
+            mbar_init(&sh.s_free[b], C::kAlt ? 4 : 8);
         }
         mbar_init(&sh.drain[0], 1);
         mbar_init(&sh.drain[1], 1);
@@ -416,7 +421,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             const uint64_t vd0 = smem_desc_sw<D>(smem_u32(ring) + 8 * D, 0, 16 * D);
             const uint64_t qd0 = smem_desc_sw<D>(smem_u32(qbuf), 16, 8 * D);
             const uint64_t pd0 = smem_desc(smem_u32(pbuf), 0, 1024);
-            int nq = 0, slot = 0, phase = 0, k = 0;
+            int nq = 0, slot = 0, phase = 0, k = 0, sb = 0, sphase = 0;
             bool ok = true;
             while (ok && k < n_steps) {
                 // a unit's steps of this range
@@ -432,12 +437,11 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 for (int i = 0; i < n; ++i, ++k) {
                     const int parts = i >= n_prefix ? 2 : 1, b = k & 1;
                     if (scores) {
-                        // S buffer b has been read when P(k - 2) is there
-                        if (k >= 2 && !mbar_wait(&sh.p_full[b], (uint32_t)(((k - 2) >> 1) & 1), T.wait)) {
+                        if (!mbar_wait(&sh.s_free[sb], (uint32_t)(sphase ^ 1), T.wait)) {
                             ok = false;
                             break;
                         }
-                        const uint32_t ts = tmem + C::kColS + (uint32_t)(b * 2 * RB);
+                        const uint32_t ts = tmem + C::kColS + (uint32_t)(sb * 2 * RB);
                         for (int part = 0; part < parts; ++part) {
                             if (!mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait)) {
                                 ok = false;
@@ -455,8 +459,12 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                             }
                         }
                         if (!ok) break;
-                        commit(&sh.s_full[b]);
+                        commit(&sh.s_full[sb]);
                         if (i == n - 1) commit(&sh.q_empty[qb]);
+                        if (++sb == C::NB) {
+                            sb = 0;
+                            sphase ^= 1;
+                        }
                     } else {
                         if (!mbar_wait(&sh.p_full[b], (uint32_t)((k >> 1) & 1), T.wait)) {
                             ok = false;
@@ -515,7 +523,8 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         // ok: this warp's waits were met; dead: the warpgroup has stopped (it
         // still meets the others at the units' barriers)
         bool ok = true, dead = false;
-        int slot = 0, phase = 0, k = 0;
+        int k = 0;
+        uint32_t taken = 0;                      // ring slots before the unit
 
         float2 meta = make_float2(0.f, 0.f);     // the unit's row gi, loaded a unit ahead
         if (gi < RW) meta = P.q_meta[(size_t)unit_of(c) * RB + row0 + gi];
@@ -536,16 +545,15 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             for (int i = 0; i < RW; ++i) l[i] = 0.f;
             group_sync<128>(bar);
 
-            for (; k < k0 + n; ++k) {
+            k = k0 + (kAlt ? (k0 ^ g) & 1 : 0);
+            for (; k < k0 + n; k += kAlt ? 2 : 1) {
+                if (dead) continue;
                 const int tile = tile0 + k - k0;
                 const bool tail = tile >= np;
-                const int slot0 = slot, phase0 = phase;
-                slot += tail ? 2 : 1;
-                if (slot >= NS) {
-                    slot -= NS;
-                    phase ^= 1;
-                }
-                if (dead || (kAlt && (k & 1) != g)) continue;
+                // (a tail step takes two slots)
+                const uint32_t at = taken + (uint32_t)(k - k0 + max(0, tile - max(np, tile0)));
+                const int slot0 = (int)(at % NS), phase0 = (int)((at / NS) & 1u);
+                const int sb = k % C::NB;
                 const int left = tail ? P.tail_len - (tile - np) * kStep : S - tile * kStep;
                 const bool here = tok < left;
                 // rows' visibility of this warp's 32 tail tokens, lane i: row i
@@ -577,19 +585,23 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     }
                 }
                 if (ok) {
-                    // PV(k - 2) has read the P buffer written below (and, where
-                    // the warpgroups alternate, is in their O); the slots' own
-                    // barriers for the scales and for the rows cleared below; S
-                    ok = (k < 2 || mbar_wait(&sh.o_upd[k & 1], (uint32_t)(((k - 2) >> 1) & 1), T.wait)) &&
-                         mbar_wait(&sh.full[slot0], (uint32_t)phase0, T.wait) &&
-                         mbar_wait(&sh.s_full[k & 1], (uint32_t)((k >> 1) & 1), T.wait);
+                    // S; the slots' own barriers for the scales and for the rows
+                    // cleared below; PV(k - 2) has read the P buffer written
+                    // below (and, where the warpgroups alternate, is in their O)
+                    uint64_t *const bs = &sh.s_full[sb], *const bf = &sh.full[slot0], *const bo = &sh.o_upd[k & 1];
+                    const uint32_t ps = (uint32_t)((k / C::NB) & 1), po = (uint32_t)(((k >> 1) - 1) & 1);
+                    const bool s_in = mbar_test_wait(bs, ps), f_in = mbar_test_wait(bf, (uint32_t)phase0),
+                               o_in = k < 2 || mbar_test_wait(bo, po);
+                    ok = (s_in || mbar_wait(bs, ps, T.wait)) &&
+                         (f_in || mbar_wait(bf, (uint32_t)phase0, T.wait)) &&
+                         (o_in || mbar_wait(bo, po, T.wait));
                     if (tail) {
                         const int s1 = slot0 + 1 == NS ? 0 : slot0 + 1;
                         ok = ok && mbar_wait(&sh.full[s1], (uint32_t)(s1 ? phase0 : phase0 ^ 1), T.wait);
                     }
                     ok = __all_sync(0xffffffffu, ok);
                 }
-                const uint32_t ts = to + C::kColS + (uint32_t)((k & 1) * 2 * RB + row0);
+                const uint32_t ts = to + C::kColS + (uint32_t)(sb * 2 * RB + row0);
                 float y[RW];
                 // y = s x (key scale, softmax scale) + log2(value scale) [- M]:
                 // the exponents of P, from the two parts of S
@@ -691,6 +703,10 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                         }
                     }
                 }
+                // (the scores are in registers for good)
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.s_free[sb]);
                 {
                     const uint64_t is2 = pair(sc.z, sc.z);
 #pragma unroll
@@ -744,6 +760,8 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             // --- the unit's end in this range: PV(k - 1) and all before it, the
             // row sums over the tokens' threads, then O / l and LSE, or the
             // partials (two running softmaxes merged where the groups alternate)
+            k = k0 + n;
+            taken += (uint32_t)(n + max(0, tile0 + n - max(np, tile0)));
             const int j = k - 1;
             // (alternating groups: step j's waits, the other follows by the barrier)
             const bool got = !dead && ok &&
