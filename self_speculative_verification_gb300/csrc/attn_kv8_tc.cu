@@ -82,8 +82,9 @@ struct Cfg {
     static constexpr int NB = kAlt ? 4 : 3;             // S buffers: S runs ahead of the softmax
     static constexpr int kSlot = 2 * kStep * D;         // K and V of a step
     static constexpr int kQ = 2 * RB * D;               // a unit's queries, both parts
-    static constexpr int kP = kStep * 128;              // P^T, rows of 128 bytes
-    static constexpr int NS = D == 64 ? 8 : (RB == 64 ? 4 : 5);
+    static constexpr int PW = kAlt ? 64 : 128;          // bytes of a token's row of P^T
+    static constexpr int kP = kStep * PW;
+    static constexpr int NS = (kAlt ? 6 : 4) * (128 / D);   // ring slots
     // TMEM: O of warpgroup g at 2 RW g (first parts, then second parts), S
     // buffer b at kColS + 2 RB b
     static constexpr uint32_t kColS = 4 * RW;
@@ -103,8 +104,7 @@ struct Shared8 {
     alignas(16) float qs[2][C::RW];      // a row's q_scale
     alignas(16) float neg_m[2][C::RW];   // and its -M
     alignas(16) float fac[2][C::RW];     // what its O is scaled by
-    int rmax[2][4][C::RW];
-    float rsum[2][4][C::RW];
+    int red[2][4][C::RW];                // the warps' maxima (ordered), or sums
     int out[2][C::RW];                   // (row * Hq + head) * 2 + valid, or -1
     uint32_t tmem_base;
 };
@@ -112,7 +112,7 @@ struct Shared8 {
 template <int D, int RB>
 constexpr size_t smem8() {
     using C = Cfg<D, RB>;
-    return (size_t)C::NS * C::kSlot + 2 * C::kQ + 2 * C::kP + sizeof(Shared8<D, RB>) + 1024;
+    return (size_t)C::NS * C::kSlot + 2 * C::kQ + 2 * C::kP + sizeof(Shared8<D, RB>);
 }
 static_assert(smem8<128, 64>() <= 227 * 1024 && smem8<128, 32>() <= 227 * 1024 &&
                   smem8<64, 64>() <= 227 * 1024,
@@ -201,15 +201,16 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
     pdl_wait();
     using C = Cfg<D, RB>;
     constexpr int RW = C::RW, NS = C::NS;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem;
     uint8_t *qbuf = ring + NS * C::kSlot;
     uint8_t *pbuf = qbuf + 2 * C::kQ;
     auto &sh = *reinterpret_cast<Shared8<D, RB> *>(pbuf + 2 * C::kP);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (warp numbers and step counts are broadcast: the compiler then keeps what
+    // follows from them, the descriptors of copies and MMAs among it, in uniform
+    // registers)
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const TcParams &T = P.t;
     const AttnParams &A = T.a;
 
@@ -254,7 +255,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
     }
     auto unit_of = [&](const Cursor &c) { return (c.b * T.seg_h + c.h) * T.seg_rb + c.rb; };
 
-    const int n_steps = (int)(t_end - t_begin);
+    const int n_steps = __shfl_sync(0xffffffffu, (int)(t_end - t_begin), 0);
 
     // (by the warp whose first work comes last)
     if (warp == kValueWarp) {
@@ -346,36 +347,41 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 ++nq;
             }
             const unsigned boxed = __ballot_sync(0xffffffffu, cur.pg >= 0);
-            const int np = (cur.c.S + kStep - 1) / kStep, tile0 = cur.c.tile - np;   // (tail)
+            const int np = (cur.c.S + kStep - 1) / kStep;
+            const bool tail = __shfl_sync(0xffffffffu, (int)cur.tail, 0) != 0;
+            const int tile0 = __shfl_sync(0xffffffffu, cur.c.tile - np, 0);          // (tail)
+            const int bh = __shfl_sync(0xffffffffu, cur.c.b * A.Hkv + cur.c.h, 0);
             // tail tiles: boxes of 16 tokens, nb of them, this warp's nw
             const int nb = (min(kStep, P.tail_len - tile0 * kStep) + 15) >> 4, nw = (nb + 1 - w) >> 1;
-            const int slots = cur.tail ? 2 : cur.n;
+            const int slots = __shfl_sync(0xffffffffu, cur.tail ? 2 : cur.n, 0);
+            const int tile_of = cur.pg * A.Hkv + cur.c.h;
             for (int i = 0; i < slots; ++i) {
-                bool got = true;
-                if (lane == 0) got = mbar_wait(&sh.empty[slot], (uint32_t)(phase ^ 1), T.wait);
-                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[slot], (uint32_t)(phase ^ 1), T.wait))) {
                     ok = false;
                     break;
                 }
                 uint8_t *dst = ring + slot * C::kSlot;
-                const bool mine = u == i && box < boxes && !cur.tail;
-                if (mine) sh.scale[slot][box] = ts;
+                if (u == i && box < boxes && !tail) sh.scale[slot][box] = ts;
                 __syncwarp();
+                const unsigned mine = (boxed >> (4 * i)) & 0xfu;
                 if (lane == 0)
-                    mbar_arrive_expect_tx(&sh.full[slot],
-                                          cur.tail ? (uint32_t)(nw * 32 * D)
-                                                   : (uint32_t)__popc((boxed >> (4 * i)) & 0xfu) *
-                                                         (uint32_t)(2 * bt * D));
+                    mbar_arrive_expect_tx(&sh.full[slot], tail ? (uint32_t)(nw * 32 * D)
+                                                               : (uint32_t)__popc(mine) * (uint32_t)(2 * bt * D));
                 __syncwarp();
-                if (cur.tail) {
-                    if (u == 0 && box < nb)
-                        tma_load_2d(dst + box * 32 * D, &m_tail, 0,
-                                    ((cur.c.b * A.Hkv + cur.c.h) * 2 + i) * (2 * P.tail_pad) +
-                                        tile0 * (2 * kStep) + box * 32,
-                                    &sh.full[slot], keep);
-                } else if (mine && cur.pg >= 0) {
-                    tma_load_3d(dst + box * (2 * bt * D), &m_kv, 0, cur.row, cur.pg * A.Hkv + cur.c.h,
-                                &sh.full[slot], stream);
+                if (tail) {
+                    const int row = (bh * 2 + i) * (2 * P.tail_pad) + tile0 * (2 * kStep);
+                    for (int x = w; x < nb; x += 2)
+                        if (lane == 0)
+                            tma_load_2d(dst + x * 32 * D, &m_tail, 0, row + x * 32, &sh.full[slot], keep);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int z = __shfl_sync(0xffffffffu, tile_of, (4 * i + x) & 31);
+                        const int row = __shfl_sync(0xffffffffu, cur.row, (4 * i + x) & 31);
+                        if (((mine >> x) & 1u) && lane == 0)
+                            tma_load_3d(dst + (2 * x + w) * (2 * bt * D), &m_kv, 0, row, z,
+                                        &sh.full[slot], stream);
+                    }
                 }
                 ++used;
                 if (++slot == NS) {
@@ -414,91 +420,103 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         const bool scores = warp == kScoreWarp;
         Cursor c;
         cursor_init(T, ws, t_begin, c);       // warp-collective
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_e4m3(kStep, 2 * RB, false, false);
-            constexpr uint32_t id_pv = idesc_e4m3(kStep, 2 * RB, true, true);
-            const uint64_t kd0 = smem_desc_sw<D>(smem_u32(ring), 16, 16 * D);
-            const uint64_t vd0 = smem_desc_sw<D>(smem_u32(ring) + 8 * D, 0, 16 * D);
-            const uint64_t qd0 = smem_desc_sw<D>(smem_u32(qbuf), 16, 8 * D);
-            const uint64_t pd0 = smem_desc(smem_u32(pbuf), 0, 1024);
-            int nq = 0, slot = 0, phase = 0, k = 0, sb = 0, sphase = 0;
-            bool ok = true;
-            while (ok && k < n_steps) {
-                // a unit's steps of this range
-                const int k0 = k, n = min(n_steps - k, c.n_tiles - c.tile);
-                const int n_prefix = (c.S + kStep - 1) / kStep - c.tile;     // of them prefix steps
-                const int qb = nq & 1;
-                if (scores && !mbar_wait(&sh.q_full[qb], (uint32_t)((nq >> 1) & 1), T.wait)) {
-                    ok = false;
-                    break;
-                }
-                ++nq;
-                const uint64_t qd = qd0 + (uint64_t)((qb * C::kQ) >> 4);
-                for (int i = 0; i < n; ++i, ++k) {
-                    const int parts = i >= n_prefix ? 2 : 1, b = k & 1;
-                    if (scores) {
-                        if (!mbar_wait(&sh.s_free[sb], (uint32_t)(sphase ^ 1), T.wait)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t ts = tmem + C::kColS + (uint32_t)(sb * 2 * RB);
-                        for (int part = 0; part < parts; ++part) {
-                            if (!mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait)) {
-                                ok = false;
-                                break;
-                            }
-                            fence_after();
-                            const uint64_t kd = kd0 + (uint64_t)((slot * C::kSlot) >> 4);
-#pragma unroll
-                            for (int e = 0; e < D / 32; ++e)
-                                mma8_ss(ts, kd + (uint64_t)(e * 32 >> 4), qd + (uint64_t)(e * 32 >> 4),
-                                        id_s, (e > 0 || part > 0) ? 1u : 0u);
-                            if (++slot == NS) {
-                                slot = 0;
-                                phase ^= 1;
-                            }
-                        }
-                        if (!ok) break;
-                        commit(&sh.s_full[sb]);
-                        if (i == n - 1) commit(&sh.q_empty[qb]);
-                        if (++sb == C::NB) {
-                            sb = 0;
-                            sphase ^= 1;
-                        }
-                    } else {
-                        if (!mbar_wait(&sh.p_full[b], (uint32_t)((k >> 1) & 1), T.wait)) {
+        constexpr uint32_t id_s = idesc_e4m3(kStep, 2 * RB, false, false);
+        constexpr uint32_t id_pv = idesc_e4m3(kStep, 2 * RB, true, true);
+        const uint64_t kd0 = smem_desc_sw<D>(smem_u32(ring), 16, 16 * D);
+        const uint64_t vd0 = smem_desc_sw<D>(smem_u32(ring) + 8 * D, 0, 16 * D);
+        const uint64_t qd0 = smem_desc_sw<D>(smem_u32(qbuf), 16, 8 * D);
+        const uint64_t pd0 = smem_desc_sw<C::PW>(smem_u32(pbuf), 0, 8 * C::PW);
+        int nq = 0, slot = 0, phase = 0, k = 0, sb = 0, sphase = 0;
+        // every lane waits and counts, lane 0 issues
+        auto wait = [&](uint64_t *bar, int parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)parity, T.wait)) != 0;
+        };
+        bool ok = true;
+        while (ok && k < n_steps) {
+            // a unit's steps of this range
+            const int k0 = k;
+            const int n = __shfl_sync(0xffffffffu, min(n_steps - k, c.n_tiles - c.tile), 0);
+            const int n_prefix =              // of them prefix steps
+                __shfl_sync(0xffffffffu, (c.S + kStep - 1) / kStep - c.tile, 0);
+            const int qb = nq & 1;
+            if (scores && !wait(&sh.q_full[qb], (nq >> 1) & 1)) {
+                ok = false;
+                break;
+            }
+            ++nq;
+            const uint64_t qd = qd0 + (uint64_t)((qb * C::kQ) >> 4);
+            for (int i = 0; i < n && ok; ++i, ++k) {
+                const int parts = i >= n_prefix ? 2 : 1, b = k & 1;
+                if (scores) {
+                    if (!wait(&sh.s_free[sb], sphase ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t ts = tmem + C::kColS + (uint32_t)(sb * 2 * RB);
+                    for (int part = 0; part < parts; ++part) {
+                        if (!wait(&sh.full[slot], phase)) {
                             ok = false;
                             break;
                         }
                         fence_after();
-                        const uint64_t pd = pd0 + (uint64_t)((b * C::kP) >> 4);
-                        const uint32_t to = tmem + (C::kAlt ? (uint32_t)(b * 2 * RW) : 0u);
-                        const bool first = k - k0 < (C::kAlt ? 2 : 1);       // into its O
-                        for (int part = 0; part < parts; ++part) {
-                            // (met: S(k) has read the slot)
-                            if (!mbar_wait(&sh.full[slot], (uint32_t)phase, T.wait)) {
-                                ok = false;
-                                break;
-                            }
-                            const uint64_t vd = vd0 + (uint64_t)((slot * C::kSlot) >> 4);
+                        const uint64_t kd = kd0 + (uint64_t)((slot * C::kSlot) >> 4);
+                        if (lane == 0) {
+#pragma unroll
+                            for (int e = 0; e < D / 32; ++e)
+                                mma8_ss(ts, kd + (uint64_t)(e * 32 >> 4), qd + (uint64_t)(e * 32 >> 4),
+                                        id_s, (e > 0 || part > 0) ? 1u : 0u);
+                        }
+                        if (++slot == NS) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (!ok) break;
+                    if (lane == 0) {
+                        commit(&sh.s_full[sb]);
+                        if (i == n - 1) commit(&sh.q_empty[qb]);
+                    }
+                    if (++sb == C::NB) {
+                        sb = 0;
+                        sphase ^= 1;
+                    }
+                } else {
+                    if (!wait(&sh.p_full[b], (k >> 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint64_t pd = pd0 + (uint64_t)((b * C::kP) >> 4);
+                    const uint32_t to = tmem + (C::kAlt ? (uint32_t)(b * 2 * RW) : 0u);
+                    const bool first = k - k0 < (C::kAlt ? 2 : 1);       // into its O
+                    for (int part = 0; part < parts; ++part) {
+                        // (met: S(k) has read the slot)
+                        if (!wait(&sh.full[slot], phase)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_after();
+                        const uint64_t vd = vd0 + (uint64_t)((slot * C::kSlot) >> 4);
+                        if (lane == 0) {
 #pragma unroll
                             for (int e = 0; e < kStep / 32; ++e)
                                 mma8_ss(to, vd + (uint64_t)((e * 4 * 16 * D) >> 4),
-                                        pd + (uint64_t)((e * 4 * 1024) >> 4), id_pv,
+                                        pd + (uint64_t)((e * 32 * C::PW) >> 4), id_pv,
                                         (e > 0 || part > 0 || !first) ? 1u : 0u);
                             commit(&sh.empty[slot]);
-                            if (++slot == NS) {
-                                slot = 0;
-                                phase ^= 1;
-                            }
                         }
-                        if (!ok) break;
-                        commit(&sh.o_upd[b]);
+                        if (++slot == NS) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
                     }
+                    if (!ok) break;
+                    if (lane == 0) commit(&sh.o_upd[b]);
                 }
-                c.tile += n - 1;
-                cursor_next(T, c);
             }
+            c.tile += n - 1;
+            cursor_next(T, c);
+        }
+        if (lane == 0) {
             if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
             // every MMA issued above has completed before TMEM is released
             // (the default limit)
@@ -666,11 +684,11 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                         const int m = __reduce_max_sync(0xffffffffu, order_of(y[i]));
                         if (lane == i) mine = m;
                     }
-                    if (lane < RW) sh.rmax[g][wq][lane] = mine;
+                    if (lane < RW) sh.red[g][wq][lane] = mine;
                     group_sync<128>(bar);
                     if (gi < RW) {
-                        const float m = of_order(max(max(sh.rmax[g][0][gi], sh.rmax[g][1][gi]),
-                                                     max(sh.rmax[g][2][gi], sh.rmax[g][3][gi])));
+                        const float m = of_order(max(max(sh.red[g][0][gi], sh.red[g][1][gi]),
+                                                     max(sh.red[g][2][gi], sh.red[g][3][gi])));
                         const float was = -sh.neg_m[g][gi], now = fmaxf(was, m - kAim);
                         sh.fac[g][gi] = was == now ? 1.f : exp2f(was - now);
                         sh.neg_m[g][gi] = -now;
@@ -725,7 +743,8 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     }
                 }
                 if (ok) {
-                    uint8_t *prow = pbuf + (k & 1) * C::kP + tok * 128;
+                    uint8_t *prow = pbuf + (k & 1) * C::kP + tok * C::PW;
+                    const int swz = C::PW == 128 ? tok & 7 : (tok >> 1) & 3;
                     uint32_t w[RW / 2];                 // first parts, then second parts
 #pragma unroll
                     for (int i = 0; i < RW; i += 4) {
@@ -738,7 +757,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     const int q0 = kAlt ? 0 : g * (RW / 8);
 #pragma unroll
                     for (int q = 0; q < RW / 8; ++q)
-                        *reinterpret_cast<uint4 *>(prow + (((q0 + q) ^ (tok & 7)) << 4)) =
+                        *reinterpret_cast<uint4 *>(prow + (((q0 + q) ^ swz) << 4)) =
                             make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
                     // V rows past the last token hold whatever the copy left: P
                     // is 0 there, but 0 x NaN is NaN
@@ -769,7 +788,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                               mbar_wait_warp(&sh.o_upd[j & 1], (uint32_t)((j >> 1) & 1), T.wait));
             constexpr int kPer = 32 / RW;
             const float sum = warp_sums<RW>(l);
-            if (lane % kPer == 0) sh.rsum[g][wq][lane / kPer] = sum;
+            if (lane % kPer == 0) sh.red[g][wq][lane / kPer] = __float_as_int(sum);
             if (group_or<256>(3, !got)) {
                 ok = false;
                 break;
@@ -779,7 +798,8 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             if (threadIdx.x < RB) {
                 const int r = threadIdx.x, rg = kAlt ? 0 : r / RW, ri = kAlt ? r : r % RW;
                 auto row_sum = [&](int q) {
-                    return (sh.rsum[q][0][ri] + sh.rsum[q][1][ri]) + (sh.rsum[q][2][ri] + sh.rsum[q][3][ri]);
+                    auto part = [&](int w) { return __int_as_float(sh.red[q][w][ri]); };
+                    return (part(0) + part(1)) + (part(2) + part(3));
                 };
                 float M = -sh.neg_m[rg][ri], L = row_sum(rg), f0 = 1.f, f1 = 0.f;
                 if (kAlt) {
