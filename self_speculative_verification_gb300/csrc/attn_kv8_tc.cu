@@ -56,11 +56,16 @@ constexpr float kAim = 7.f;                 // log2 P of a row's maximum when M 
 constexpr float kNoRef = -1e30f;            // M of a row that has seen nothing
 constexpr float kLoUp = 16.f;               // factor of P's second part
 
+// A unit's row, as the preparing kernel leaves it.
+struct alignas(8) RowMeta {
+    float scale;             // softmax scale (log2) x the row's power of two
+    int out;                 // (row * Hq + head) * 2 + valid, within the request; -1 past the last
+};
+
 struct Tc8Params {
     TcParams t;              // schedule, split, partials (t.a: the call)
     const float *scales;     // the cache's
-    const float2 *q_meta;    // [units][RB]: softmax scale (log2) x the row's power of two;
-                             // output row and whether it is valid (see Prep8Params)
+    const RowMeta *q_meta;   // [units][RB]
     const float2 *tail_scale;    // [B][Hkv][tail_pad]: scales of the tail's tokens
     int tail_len, tail_pad;  // n_soft + R, rounded up to 16
     int n_tail;              // its 128-token tiles
@@ -104,8 +109,8 @@ struct Shared8 {
     alignas(16) float qs[2][C::RW];      // a row's q_scale
     alignas(16) float neg_m[2][C::RW];   // and its -M
     alignas(16) float fac[2][C::RW];     // what its O is scaled by
-    int red[2][4][C::RW];                // the warps' maxima (ordered), or sums
-    int out[2][C::RW];                   // (row * Hq + head) * 2 + valid, or -1
+    alignas(16) int red[2][4][C::RW];    // the warps' maxima (ordered), or sums; what M is raised by
+    int out[2][C::RW];                   // RowMeta::out
     uint32_t tmem_base;
 };
 
@@ -198,7 +203,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ CUtensorMap m_kv,
                    const __grid_constant__ CUtensorMap m_tail,
                    const __grid_constant__ CUtensorMap m_q) {
-    pdl_wait();
     using C = Cfg<D, RB>;
     constexpr int RW = C::RW, NS = C::NS;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -249,6 +253,10 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
     const int cta = blockIdx.x;
     const long long t_begin = sched_range_lo(T, ws, cta);
     const long long t_end = sched_range_lo(T, ws, cta + 1);
+    // (the preparing kernel has begun, so every kernel before it has ended and
+    // the schedule's inputs are there; its own rows and the workspace's parts
+    // that a kernel before it may still be reading are waited for here)
+    pdl_wait();
     if (threadIdx.x == 0) {
         T.bounds[cta] = t_begin;
         if (cta == T.n_ctas - 1) T.bounds[T.n_ctas] = ws.T;
@@ -544,7 +552,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         int k = 0;
         uint32_t taken = 0;                      // ring slots before the unit
 
-        float2 meta = make_float2(0.f, 0.f);     // the unit's row gi, loaded a unit ahead
+        RowMeta meta{0.f, -1};             // the unit's row gi, loaded a unit ahead
         if (gi < RW) meta = P.q_meta[(size_t)unit_of(c) * RB + row0 + gi];
         while (k < n_steps) {
             // --- a unit's steps of this range
@@ -552,10 +560,11 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             const int np = (S + kStep - 1) / kStep, seg_b = c.b, seg_h = c.h, seg_id = unit_of(c);
             const bool seg_whole = tile0 == 0 && n == c.n_tiles;
             if (gi < RW) {
-                sh.out[g][gi] = __float_as_int(meta.y);
-                sh.qs[g][gi] = meta.x;
-                sh.neg_m[g][gi] = -kNoRef;
+                sh.out[g][gi] = meta.out;
+                sh.qs[g][gi] = meta.scale;
+                sh.neg_m[g][gi] = 0.f;
             }
+            bool unset = true;           // rows without a reference: M (0) is still to be set
             c.tile += n - 1;
             cursor_next(T, c);
             if (gi < RW && k + n < n_steps) meta = P.q_meta[(size_t)unit_of(c) * RB + row0 + gi];
@@ -621,9 +630,9 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 }
                 const uint32_t ts = to + C::kColS + (uint32_t)(sb * 2 * RB + row0);
                 float y[RW];
-                // y = s x (key scale, softmax scale) + log2(value scale) [- M]:
-                // the exponents of P, from the two parts of S
-                auto exponents = [&](bool less_m) {
+                // y = s x (key scale, softmax scale) + log2(value scale) - M: the
+                // exponents of P, from the two parts of S
+                auto exponents = [&] {
                     const uint64_t sk2 = pair(sc.x, sc.x), lv2 = pair(sc.y, sc.y), z = pair(0.f, 0.f);
 #pragma unroll
                     for (int i0 = 0; i0 < RW; i0 += CH) {
@@ -634,8 +643,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
 #pragma unroll
                         for (int i = 0; i < CH; i += 4) {
                             const float4 q = *reinterpret_cast<const float4 *>(&sh.qs[g][i0 + i]);
-                            float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (less_m) m = *reinterpret_cast<const float4 *>(&sh.neg_m[g][i0 + i]);
+                            const float4 m = *reinterpret_cast<const float4 *>(&sh.neg_m[g][i0 + i]);
                             unpair(fma2(add2(pair(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
                                              pair(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1]))),
                                         fma2(pair(q.x, q.y), sk2, z), add2(pair(m.x, m.y), lv2)),
@@ -665,19 +673,17 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 if (ok) {
                     fence_after();
                     if (!tail && here) sc = sh.scale[slot0][tok >> P.box_log2];
-                    exponents(true);
+                    exponents();
                     mask();
 #pragma unroll
                     for (int i = 0; i < RW; i += 2) top = max3(top, y[i], y[i + 1]);
                 }
-                if (group_or<128>(bar, top > kTop || !ok)) {
+                if (group_or<128>(bar, unset || top > kTop || !ok)) {
                     if (group_or<128>(bar, !ok)) {
                         dead = true;
                         continue;
                     }
-                    // raise M of the rows whose maximum grew
-                    exponents(false);
-                    mask();
+                    // set M, or raise it where a row's maximum grew
                     int mine = order_of(-INFINITY);
 #pragma unroll
                     for (int i = 0; i < RW; ++i) {
@@ -686,18 +692,23 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     }
                     if (lane < RW) sh.red[g][wq][lane] = mine;
                     group_sync<128>(bar);
+                    bool none = false;
                     if (gi < RW) {
                         const float m = of_order(max(max(sh.red[g][0][gi], sh.red[g][1][gi]),
                                                      max(sh.red[g][2][gi], sh.red[g][3][gi])));
-                        const float was = -sh.neg_m[g][gi], now = fmaxf(was, m - kAim);
-                        sh.fac[g][gi] = was == now ? 1.f : exp2f(was - now);
-                        sh.neg_m[g][gi] = -now;
+                        // (a row without a reference has M = 0 and no sums yet)
+                        const float was = sh.neg_m[g][gi];
+                        none = m == -INFINITY && was == 0.f;
+                        const float up = m == -INFINITY ? 0.f : was == 0.f ? m - kAim : fmaxf(0.f, m - kAim);
+                        sh.red[g][0][gi] = __float_as_int(up);
+                        sh.fac[g][gi] = was == 0.f ? 0.f : exp2f(-up);
+                        sh.neg_m[g][gi] = was - up == 0.f && !none ? -1e-30f : was - up;
                     }
-                    group_sync<128>(bar);
+                    unset = group_or<128>(bar, none);
 #pragma unroll
                     for (int i = 0; i < RW; ++i) {
                         l[i] *= sh.fac[g][i];
-                        y[i] += sh.neg_m[g][i];
+                        y[i] -= __int_as_float(sh.red[g][0][i]);
                     }
                     if (k - k0 >= (kAlt ? 2 : 1)) {        // O holds earlier steps
                         if (!kAlt)
@@ -705,17 +716,18 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                                                 T.wait);
                         if (ok) {
                             fence_after();
+                            constexpr int CO = RW < 16 ? RW : 16;
 #pragma unroll 1
-                            for (int e = 0; e < 2 * RW; e += CH) {
-                                uint32_t x[CH];
+                            for (int e = 0; e < 2 * RW; e += CO) {
+                                uint32_t x[CO];
                                 const uint32_t at = to + (uint32_t)(g * 2 * RW + e);
-                                ldn<CH>(at, x);
-                                wait_ldn<CH>(x);
+                                ldn<CO>(at, x);
+                                wait_ldn<CO>(x);
 #pragma unroll
-                                for (int i = 0; i < CH; ++i)
+                                for (int i = 0; i < CO; ++i)
                                     x[i] = __float_as_uint(__uint_as_float(x[i]) *
                                                            sh.fac[g][(e & (RW - 1)) + i]);
-                                stn<CH>(at, x);
+                                stn<CO>(at, x);
                             }
                             wait_st();
                         }
@@ -782,10 +794,11 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             k = k0 + n;
             taken += (uint32_t)(n + max(0, tile0 + n - max(np, tile0)));
             const int j = k - 1;
-            // (alternating groups: step j's waits, the other follows by the barrier)
+            // (each group waits for its own last PV, behind the last use of sh.red
+            // by any of its warps)
+            const int jw = kAlt && (j & 1) != g ? j - 1 : j;
             const bool got = !dead && ok &&
-                             ((kAlt && (j & 1) != g) ||
-                              mbar_wait_warp(&sh.o_upd[j & 1], (uint32_t)((j >> 1) & 1), T.wait));
+                             (jw < k0 || mbar_wait_warp(&sh.o_upd[jw & 1], (uint32_t)((jw >> 1) & 1), T.wait));
             constexpr int kPer = 32 / RW;
             const float sum = warp_sums<RW>(l);
             if (lane % kPer == 0) sh.red[g][wq][lane / kPer] = __float_as_int(sum);
@@ -801,9 +814,11 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     auto part = [&](int w) { return __int_as_float(sh.red[q][w][ri]); };
                     return (part(0) + part(1)) + (part(2) + part(3));
                 };
-                float M = -sh.neg_m[rg][ri], L = row_sum(rg), f0 = 1.f, f1 = 0.f;
+                // (-M of 0: the row has seen nothing)
+                auto ref = [&](int q) { return sh.neg_m[q][ri] == 0.f ? kNoRef : -sh.neg_m[q][ri]; };
+                float M = ref(rg), L = row_sum(rg), f0 = 1.f, f1 = 0.f;
                 if (kAlt) {
-                    const float m0 = M, m1 = -sh.neg_m[1][ri];
+                    const float m0 = M, m1 = ref(1);
                     M = fmaxf(m0, m1);
                     f0 = exp2f(m0 - M);
                     f1 = exp2f(m1 - M);
@@ -815,7 +830,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 sh.fac[rg][ri] = f0 * inv;
                 if (kAlt) sh.fac[1][ri] = f1 * inv;
                 if (seg_whole && out >= 0) {
-                    const int hq = (out >> 1) % A.Hq, rr = (out >> 1) / A.Hq;
+                    const int rr = (out >> 1) / A.Hq, hq = (out >> 1) - rr * A.Hq;
                     A.lse[((size_t)seg_b * A.Hq + hq) * A.R + rr] =
                         none ? -INFINITY : (M + log2f(L)) * kLn2;
                 } else if (!seg_whole) {
@@ -946,97 +961,95 @@ __global__ void __launch_bounds__(128) attn_kv8_tc_combine_kernel(const __grid_c
 struct Prep8Params {
     AttnParams a;
     uint8_t *q8;             // [units][2][RB][D]
-    float2 *q_meta;          // [units][RB]: scale; (row * Hq + head) * 2 + valid, -1 past the last
+    RowMeta *q_meta;         // [units][RB]
     uint8_t *tail8;          // [B][Hkv][2][tail_pad / 8][2][8][D]
     float2 *tail_scale;      // [B][Hkv][tail_pad]
     int rb, seg_rb, tail_pad;
     long long q_rows, t_rows;
 };
 
-// A row of D bf16 values (lane: D / 32 of them) as two e4m3 rows under one
+// A row of D bf16 values (src NULL: zeros) as two e4m3 rows under one
 // power-of-two scale, which is returned (NaN for a row that is not finite,
-// whose codes are 0).
+// whose codes are 0): eight lanes a row, D / 8 values each.
 template <int D>
 __device__ float split_row(const __nv_bfloat16 *src, uint8_t *hi, uint8_t *lo, bool zero_is_small) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
+    constexpr int E = D / 8;
+    const int sub = threadIdx.x & 7;
     float x[E];
     uint32_t amax = 0;
-    if (src) {
-        if constexpr (E == 4) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(src + lane * 4);
-            x[0] = __uint_as_float(v.x << 16);
-            x[1] = __uint_as_float(v.x & 0xffff0000u);
-            x[2] = __uint_as_float(v.y << 16);
-            x[3] = __uint_as_float(v.y & 0xffff0000u);
-        } else {
-            const uint32_t v = *reinterpret_cast<const uint32_t *>(src + lane * 2);
-            x[0] = __uint_as_float(v << 16);
-            x[1] = __uint_as_float(v & 0xffff0000u);
-        }
-    } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = 0.f;
+    for (int e = 0; e < E; e += 8) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (src) v = *reinterpret_cast<const uint4 *>(src + sub * E + e);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[e + 2 * i] = __uint_as_float(w[i] << 16);
+            x[e + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            amax = max(amax, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+        }
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
-    amax = __reduce_max_sync(0xffffffffu, amax);
+    for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const bool bad = amax >= 0x7f800000u;
     // 2^e: the largest value lies in (224, 448] of it
     const int e = min(max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -110), 119);
-    const float r = exp2_int(-e);
-    uint32_t h = 0u, w = 0u;
-    if (!bad) {
+    const float r = bad ? 0.f : exp2_int(-e);
+    uint32_t h[E / 4], w[E / 4];
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-            const float a = x[i] * r, c = x[i + 1] * r;
-            const uint32_t p = e4m3x2(a, c);
-            const float2 f = from_e4m3x2(p);
-            h |= p << (8 * i);
-            w |= e4m3x2(a - f.x, c - f.y) << (8 * i);
-        }
+    for (int i = 0; i < E; i += 4) {
+        const float a = bad ? 0.f : x[i] * r, b = bad ? 0.f : x[i + 1] * r;
+        const float c = bad ? 0.f : x[i + 2] * r, d = bad ? 0.f : x[i + 3] * r;
+        const uint32_t p = e4m3x2(a, b), q = e4m3x2(c, d);
+        const float2 f = from_e4m3x2(p), g = from_e4m3x2(q);
+        h[i / 4] = p | (q << 16);
+        w[i / 4] = e4m3x2(a - f.x, b - f.y) | (e4m3x2(c - g.x, d - g.y) << 16);
     }
-    if constexpr (E == 4) {
-        *reinterpret_cast<uint32_t *>(hi + lane * 4) = h;
-        *reinterpret_cast<uint32_t *>(lo + lane * 4) = w;
+    if constexpr (E == 16) {
+        *reinterpret_cast<uint4 *>(hi + sub * E) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(lo + sub * E) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-        *reinterpret_cast<uint16_t *>(hi + lane * 2) = (uint16_t)h;
-        *reinterpret_cast<uint16_t *>(lo + lane * 2) = (uint16_t)w;
+        *reinterpret_cast<uint2 *>(hi + sub * E) = make_uint2(h[0], h[1]);
+        *reinterpret_cast<uint2 *>(lo + sub * E) = make_uint2(w[0], w[1]);
     }
     if (bad) return __uint_as_float(0x7fffffffu);
     // (a value row of zeros must not raise its readers' references)
     return amax == 0 && zero_is_small ? exp2_int(kKv8MinExp) : exp2_int(e);
 }
 
-// One warp a row: the query rows of every unit, then the tail's keys and
-// values (a token's two rows, soft prompt first, by one warp).
+// Eight lanes a row: the query rows of every unit, then the tail's tokens
+// (soft prompt first), a key row and a value row each.  It lets the attention
+// kernel start at once: that one waits for it only where it reads these rows.
 template <int D>
 __global__ void __launch_bounds__(256) attn_kv8_prep_kernel(const __grid_constant__ Prep8Params P) {
     pdl_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const AttnParams &A = P.a;
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < A.B; b += 256) check_seq_len(A, b);
-    if (w < P.q_rows) {
-        const int r = (int)(w % P.rb);
-        const long long u = w / P.rb;
+    const long long w = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);
+    const int sub = threadIdx.x & 7;
+    const long long q_pad = (P.q_rows + 3) & ~3ll;        // (a warp's four rows are of one kind)
+    if (w < q_pad) {
+        const bool real = w < P.q_rows;
+        const long long at = real ? w : P.q_rows - 1;
+        const int r = (int)(at % P.rb);
+        const long long u = at / P.rb;
         const int rb = (int)(u % P.seg_rb), h = (int)((u / P.seg_rb) % A.Hkv);
         const int b = (int)(u / ((long long)P.seg_rb * A.Hkv)), p = rb * P.rb + r;
         const __nv_bfloat16 *src = nullptr;
-        int out = -1;
+        RowMeta m{0.f, -1};
         if (p < A.M) {
-            const int rr = p / A.G, at = rr * A.Hq + h * A.G + p % A.G;
-            src = static_cast<const __nv_bfloat16 *>(A.q) + ((size_t)b * A.R * A.Hq + at) * D;
-            out = 2 * at + (A.row_flags[(size_t)b * A.R + rr] & SPEC_ROW_VALID ? 1 : 0);
+            const int rr = p / A.G, hq = h * A.G + p % A.G, row = rr * A.Hq + hq;
+            src = static_cast<const __nv_bfloat16 *>(A.q) + ((size_t)b * A.R * A.Hq + row) * D;
+            m.out = 2 * row + (A.row_flags[(size_t)b * A.R + rr] & SPEC_ROW_VALID ? 1 : 0);
         }
         uint8_t *dst = P.q8 + ((size_t)u * 2 * P.rb + r) * D;
-        const float s = split_row<D>(src, dst, dst + (size_t)P.rb * D, false);
-        if (lane == 0) P.q_meta[w] = make_float2(s * A.scale_log2, __int_as_float(out));
+        m.scale = split_row<D>(src, dst, dst + (size_t)P.rb * D, false) * A.scale_log2;
+        if (sub == 0 && real) P.q_meta[at] = m;
         return;
     }
-    const long long t = w - P.q_rows;
-    if (t >= P.t_rows) return;
+    const long long t0 = w - q_pad, t = t0 < P.t_rows ? t0 : P.t_rows - 1;
     const int tt = (int)(t % P.tail_pad);
     const long long bh = t / P.tail_pad;
     const int h = (int)(bh % A.Hkv);
@@ -1055,7 +1068,7 @@ __global__ void __launch_bounds__(256) attn_kv8_prep_kernel(const __grid_constan
     const int ko = kv8_row(tt, 0, D), vo = kv8_row(tt, 1, D);
     const float sk = split_row<D>(k, hi + ko, lo + ko, false);
     const float sv_ = split_row<D>(v, hi + vo, lo + vo, true);
-    if (lane == 0) P.tail_scale[t] = make_float2(sk, sv_);
+    if (sub == 0) P.tail_scale[t] = make_float2(sk, sv_);
 }
 
 // ------------------------------------------------------------------ host
@@ -1088,7 +1101,7 @@ Ws8 plan_ws(const AttnParams &A) {
     w.bounds = take(((size_t)w.n_ctas + 1) * sizeof(long long));
     w.recs = take((size_t)w.n_ctas * sizeof(BoundaryRec));
     w.q8 = take((size_t)w.units * 2 * w.rb * A.d);
-    w.q_meta = take((size_t)w.units * w.rb * sizeof(float2));
+    w.q_meta = take((size_t)w.units * w.rb * sizeof(RowMeta));
     w.tail8 = take((size_t)A.B * A.Hkv * 4 * w.tail_pad * A.d);
     w.tail_scale = take((size_t)A.B * A.Hkv * w.tail_pad * sizeof(float2));
     w.bytes = at;
@@ -1107,8 +1120,8 @@ spec_status_t launch_units(const Tc8Params &P, const CUtensorMap *m, cudaStream_
 template <int D>
 spec_status_t launch_rows(const Tc8Params &P, const Prep8Params &R, const CUtensorMap *m, int rb,
                           cudaStream_t s) {
-    const long long prep = R.q_rows + R.t_rows;
-    spec_status_t st = launch(attn_kv8_prep_kernel<D>, dim3((unsigned)ceil_div_ll(prep, 8)), dim3(256),
+    const long long prep = ((R.q_rows + 3) & ~3ll) + R.t_rows;
+    spec_status_t st = launch(attn_kv8_prep_kernel<D>, dim3((unsigned)ceil_div_ll(prep, 32)), dim3(256),
                               0, s, R);
     if (st != SPEC_OK) return st;
     st = rb == 8    ? launch_units<D, 8>(P, m, s)
@@ -1156,7 +1169,7 @@ spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s) {
     T.seg_cost = 2;
     T.pair_steps = 1;                       // a step: two of the schedule's 64-token tiles
     P.scales = Q.scales;
-    P.q_meta = reinterpret_cast<const float2 *>(base + w.q_meta);
+    P.q_meta = reinterpret_cast<const RowMeta *>(base + w.q_meta);
     P.tail_scale = reinterpret_cast<const float2 *>(base + w.tail_scale);
     P.tail_len = Q.a.n_soft + Q.a.R;
     P.tail_pad = w.tail_pad;
@@ -1169,7 +1182,7 @@ spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s) {
     Prep8Params R{};
     R.a = Q.a;
     R.q8 = reinterpret_cast<uint8_t *>(base + w.q8);
-    R.q_meta = reinterpret_cast<float2 *>(base + w.q_meta);
+    R.q_meta = reinterpret_cast<RowMeta *>(base + w.q_meta);
     R.tail8 = reinterpret_cast<uint8_t *>(base + w.tail8);
     R.tail_scale = reinterpret_cast<float2 *>(base + w.tail_scale);
     R.rb = w.rb;
