@@ -109,8 +109,8 @@ struct Shared8 {
     alignas(16) float qs[2][C::RW];      // a row's q_scale
     alignas(16) float neg_m[2][C::RW];   // and its -M
     alignas(16) float fac[2][C::RW];     // what its O is scaled by
-    alignas(16) int red[2][4][C::RW];    // the warps' maxima (ordered), or sums; what M is raised by
-    int out[2][C::RW];                   // RowMeta::out
+    alignas(16) float red[2][4][C::RW];  // the warps' maxima, or sums; what M is raised by
+    alignas(16) int out[2][C::RW];       // RowMeta::out
     uint32_t tmem_base;
 };
 
@@ -140,13 +140,11 @@ __device__ __forceinline__ void group_sync(int id) {
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
 }
 
-// Floats as integers of the same order (NaN as -inf), and back.
-__device__ __forceinline__ int order_of(float x) {
-    const int i = __float_as_int(x == x ? x : -INFINITY);
-    return i ^ ((i >> 31) & 0x7fffffff);
-}
-__device__ __forceinline__ float of_order(int i) {
-    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+// Largest of the warp's values (a NaN counts only where all are).
+__device__ __forceinline__ float warp_redux_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // What a token's thread needs of its two scales: (key scale, log2 of the value
@@ -220,7 +218,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&sh.full[s], 2);           // the two producers
+            mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -273,28 +271,32 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
 
     if (n_steps > 0 && (warp == kProducerWarp || warp == kProducerWarp2)) {
         // ------------------------------------------------------ producers
-        // Two warps, each with every other box of a step (a copy costs its
-        // issuing warp about 100 cycles): the box's copy and its scales.
-        // They walk the range in groups of up to eight prefix steps of a unit
-        // (or one tail step): lane 4 u + i owns box 2 i + w of the group's
-        // step u, so a page id costs one load per lane and group, issued two
-        // groups ahead of its copy, and a scale one, issued a group ahead.
+        // Two warps take alternate ring slots (a slot's copies keep their
+        // issuing warp for most of the time the tile takes to stream, and
+        // the other warp gets its next slot ready meanwhile): its copies and
+        // its scales.  They walk the range in groups of up to eight prefix
+        // steps of a unit (or one tail step, two slots): lane 8 u + i owns
+        // box i of the warp's u-th step of the group, so a page id costs one
+        // load per lane, issued two groups ahead of its copy, and a scale
+        // one, issued a group ahead.
         const int w = warp == kProducerWarp ? 0 : 1;
         const uint64_t keep = policy_evict_last();
         const uint64_t stream = T.seg_rb == 1 ? policy_evict_first() : keep;
         const int bt = 1 << P.box_log2, boxes = kStep >> P.box_log2;
-        const int u = lane >> 2, box = 2 * (lane & 3) + w;
+        const int u = lane >> 3, box = lane & 7;
         struct Group {
             Cursor c;            // its first step
             int k, n;            // that step's number, steps (0: past the range)
+            int at;              // its first slot, counted from the range's first
             bool tail;
             int pg, row;         // this lane's page (-1 no box, -2 a bad page), row of its tile
         };
-        auto group_at = [&](const Cursor &c, int k) {
+        auto group_at = [&](const Cursor &c, int k, int at) {
             Group g;
             g.c = c;
             g.k = k;
             g.n = 0;
+            g.at = at;
             g.tail = false;
             g.pg = -1;
             g.row = 0;
@@ -302,8 +304,9 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             const int np = (c.S + kStep - 1) / kStep;
             g.tail = c.tile >= np;
             g.n = g.tail ? 1 : min(min(8, np - c.tile), n_steps - k);
-            const int tok = (c.tile + u) * kStep + (box << P.box_log2);
-            if (!g.tail && u < g.n && box < boxes && tok < c.S) {
+            const int i = 2 * u + ((at ^ w) & 1);            // this lane's step of the group
+            const int tok = (c.tile + i) * kStep + (box << P.box_log2);
+            if (!g.tail && i < g.n && box < boxes && tok < c.S) {
                 const int t16 = tok >> 4, j = (int)((t16 * P.ps16_inv) >> 32);
                 g.row = (t16 - j * P.ps16) * 32;
                 const int pg = A.page_table[(size_t)c.b * A.max_pages + j];
@@ -317,7 +320,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 c.tile += g.n - 1;
                 cursor_next(T, c);
             }
-            return group_at(c, g.n > 0 ? g.k + g.n : n_steps);
+            return group_at(c, g.n > 0 ? g.k + g.n : n_steps, g.at + (g.tail ? 2 : g.n));
         };
         auto scale_of = [&](const Group &g) {
             if (g.pg < 0) return make_float2(1.f, 1.f);
@@ -325,10 +328,10 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         };
         Cursor c0;
         cursor_init(T, ws, t_begin, c0);
-        Group cur = group_at(c0, 0), next = after(cur);
+        Group cur = group_at(c0, 0, 0), next = after(cur);
         float2 sc = scale_of(cur);
-        int slot = 0, phase = 0, nq = 0;
-        long long used = 0;                          // ring slots taken so far
+        int slot = w, phase = 0, nq = 0, used = 0;   // used: slots filled by this warp
+        static_assert(NS % 2 == 0, "a warp's slots have one parity");
         bool ok = true;
         while (cur.n > 0 && ok) {
             const Group far = after(next);
@@ -339,61 +342,58 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 // the unit's queries, once the unit two back is done with the
                 // buffer
                 const int qb = nq & 1;
-                bool got = true;
-                if (lane == 0) {
-                    got = nq < 2 || mbar_wait(&sh.q_empty[qb], (uint32_t)(((nq >> 1) - 1) & 1), T.wait);
-                    if (got) {
-                        mbar_arrive_expect_tx(&sh.q_full[qb], C::kQ);
-                        tma_load_2d(qbuf + qb * C::kQ, &m_q, 0, unit_of(cur.c) * (2 * RB), &sh.q_full[qb],
-                                    keep);
-                    }
-                }
-                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                if (nq >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sh.q_empty[qb],
+                                                                  (uint32_t)(((nq >> 1) - 1) & 1), T.wait))) {
                     ok = false;
                     break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh.q_full[qb], C::kQ);
+                    tma_load_2d(qbuf + qb * C::kQ, &m_q, 0, unit_of(cur.c) * (2 * RB), &sh.q_full[qb], keep);
                 }
                 ++nq;
             }
             const unsigned boxed = __ballot_sync(0xffffffffu, cur.pg >= 0);
-            const int np = (cur.c.S + kStep - 1) / kStep;
             const bool tail = __shfl_sync(0xffffffffu, (int)cur.tail, 0) != 0;
-            const int tile0 = __shfl_sync(0xffffffffu, cur.c.tile - np, 0);          // (tail)
+            // (tail) its tile and its boxes of 16 tokens
+            const int tile0 = __shfl_sync(0xffffffffu, cur.c.tile - (cur.c.S + kStep - 1) / kStep, 0);
             const int bh = __shfl_sync(0xffffffffu, cur.c.b * A.Hkv + cur.c.h, 0);
-            // tail tiles: boxes of 16 tokens, nb of them, this warp's nw
-            const int nb = (min(kStep, P.tail_len - tile0 * kStep) + 15) >> 4, nw = (nb + 1 - w) >> 1;
+            const int nb = (min(kStep, P.tail_len - tile0 * kStep) + 15) >> 4;
+            const int first = (__shfl_sync(0xffffffffu, cur.at, 0) ^ w) & 1;
             const int slots = __shfl_sync(0xffffffffu, cur.tail ? 2 : cur.n, 0);
             const int tile_of = cur.pg * A.Hkv + cur.c.h;
-            for (int i = 0; i < slots; ++i) {
+            for (int i = first, v = 0; i < slots; i += 2, ++v) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[slot], (uint32_t)(phase ^ 1), T.wait))) {
                     ok = false;
                     break;
                 }
                 uint8_t *dst = ring + slot * C::kSlot;
-                if (u == i && box < boxes && !tail) sh.scale[slot][box] = ts;
+                if (u == v && box < boxes && !tail) sh.scale[slot][box] = ts;
                 __syncwarp();
-                const unsigned mine = (boxed >> (4 * i)) & 0xfu;
+                const unsigned mine = (boxed >> (8 * v)) & 0xffu;
                 if (lane == 0)
-                    mbar_arrive_expect_tx(&sh.full[slot], tail ? (uint32_t)(nw * 32 * D)
+                    mbar_arrive_expect_tx(&sh.full[slot], tail ? (uint32_t)(nb * 32 * D)
                                                                : (uint32_t)__popc(mine) * (uint32_t)(2 * bt * D));
                 __syncwarp();
                 if (tail) {
                     const int row = (bh * 2 + i) * (2 * P.tail_pad) + tile0 * (2 * kStep);
-                    for (int x = w; x < nb; x += 2)
+                    for (int x = 0; x < nb; ++x)
                         if (lane == 0)
                             tma_load_2d(dst + x * 32 * D, &m_tail, 0, row + x * 32, &sh.full[slot], keep);
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int z = __shfl_sync(0xffffffffu, tile_of, (4 * i + x) & 31);
-                        const int row = __shfl_sync(0xffffffffu, cur.row, (4 * i + x) & 31);
+                    for (int x = 0; x < 8; ++x) {
+                        if (x >= boxes) break;
+                        const int z = __shfl_sync(0xffffffffu, tile_of, (8 * v + x) & 31);
+                        const int row = __shfl_sync(0xffffffffu, cur.row, (8 * v + x) & 31);
                         if (((mine >> x) & 1u) && lane == 0)
-                            tma_load_3d(dst + (2 * x + w) * (2 * bt * D), &m_kv, 0, row, z,
-                                        &sh.full[slot], stream);
+                            tma_load_3d(dst + x * (2 * bt * D), &m_kv, 0, row, z, &sh.full[slot], stream);
                     }
                 }
                 ++used;
-                if (++slot == NS) {
-                    slot = 0;
+                slot += 2;
+                if (slot >= NS) {
+                    slot -= NS;
                     phase ^= 1;
                 }
             }
@@ -405,8 +405,8 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
             // do not leave while copies into this CTA's shared memory are in
             // flight (the default limit: these copies were issued and complete)
-            for (long long i = used - 1; i >= 0 && i >= used - NS; --i)
-                if (!mbar_wait(&sh.full[i % NS], (uint32_t)((i / NS) & 1))) {
+            for (int i = used - 1; i >= 0 && i >= used - NS / 2; --i)
+                if (!mbar_wait(&sh.full[w + 2 * (i % (NS / 2))], (uint32_t)((i / (NS / 2)) & 1))) {
                     raise_status(A.status, SPEC_DEV_TIMEOUT);
                     break;
                 }
@@ -684,31 +684,40 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                         continue;
                     }
                     // set M, or raise it where a row's maximum grew
-                    int mine = order_of(-INFINITY);
+                    float mine = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < RW; ++i) {
-                        const int m = __reduce_max_sync(0xffffffffu, order_of(y[i]));
-                        if (lane == i) mine = m;
+                        const float m = warp_redux_max(y[i]);
+                        mine = lane == i ? m : mine;
                     }
                     if (lane < RW) sh.red[g][wq][lane] = mine;
                     group_sync<128>(bar);
                     bool none = false;
                     if (gi < RW) {
-                        const float m = of_order(max(max(sh.red[g][0][gi], sh.red[g][1][gi]),
-                                                     max(sh.red[g][2][gi], sh.red[g][3][gi])));
+                        // (fmaxf leaves out a NaN: a row of NaN alone counts as unseen)
+                        const float m = fmaxf(fmaxf(fmaxf(sh.red[g][0][gi], sh.red[g][1][gi]),
+                                                    fmaxf(sh.red[g][2][gi], sh.red[g][3][gi])), -INFINITY);
                         // (a row without a reference has M = 0 and no sums yet)
                         const float was = sh.neg_m[g][gi];
                         none = m == -INFINITY && was == 0.f;
                         const float up = m == -INFINITY ? 0.f : was == 0.f ? m - kAim : fmaxf(0.f, m - kAim);
-                        sh.red[g][0][gi] = __float_as_int(up);
+                        sh.red[g][0][gi] = up;
                         sh.fac[g][gi] = was == 0.f ? 0.f : exp2f(-up);
                         sh.neg_m[g][gi] = was - up == 0.f && !none ? -1e-30f : was - up;
                     }
                     unset = group_or<128>(bar, none);
 #pragma unroll
-                    for (int i = 0; i < RW; ++i) {
-                        l[i] *= sh.fac[g][i];
-                        y[i] -= __int_as_float(sh.red[g][0][i]);
+                    for (int i = 0; i < RW; i += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&sh.fac[g][i]);
+                        const float4 d = *reinterpret_cast<const float4 *>(&sh.red[g][0][i]);
+                        l[i] *= f.x;
+                        l[i + 1] *= f.y;
+                        l[i + 2] *= f.z;
+                        l[i + 3] *= f.w;
+                        y[i] -= d.x;
+                        y[i + 1] -= d.y;
+                        y[i + 2] -= d.z;
+                        y[i + 3] -= d.w;
                     }
                     if (k - k0 >= (kAlt ? 2 : 1)) {        // O holds earlier steps
                         if (!kAlt)
@@ -724,9 +733,14 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                                 ldn<CO>(at, x);
                                 wait_ldn<CO>(x);
 #pragma unroll
-                                for (int i = 0; i < CO; ++i)
-                                    x[i] = __float_as_uint(__uint_as_float(x[i]) *
-                                                           sh.fac[g][(e & (RW - 1)) + i]);
+                                for (int i = 0; i < CO; i += 4) {
+                                    const float4 f =
+                                        *reinterpret_cast<const float4 *>(&sh.fac[g][(e & (RW - 1)) + i]);
+                                    x[i] = __float_as_uint(__uint_as_float(x[i]) * f.x);
+                                    x[i + 1] = __float_as_uint(__uint_as_float(x[i + 1]) * f.y);
+                                    x[i + 2] = __float_as_uint(__uint_as_float(x[i + 2]) * f.z);
+                                    x[i + 3] = __float_as_uint(__uint_as_float(x[i + 3]) * f.w);
+                                }
                                 stn<CO>(at, x);
                             }
                             wait_st();
@@ -794,14 +808,14 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             k = k0 + n;
             taken += (uint32_t)(n + max(0, tile0 + n - max(np, tile0)));
             const int j = k - 1;
+            constexpr int kPer = 32 / RW;
+            const float sum = warp_sums<RW>(l);
             // (each group waits for its own last PV, behind the last use of sh.red
             // by any of its warps)
             const int jw = kAlt && (j & 1) != g ? j - 1 : j;
             const bool got = !dead && ok &&
                              (jw < k0 || mbar_wait_warp(&sh.o_upd[jw & 1], (uint32_t)((jw >> 1) & 1), T.wait));
-            constexpr int kPer = 32 / RW;
-            const float sum = warp_sums<RW>(l);
-            if (lane % kPer == 0) sh.red[g][wq][lane / kPer] = __float_as_int(sum);
+            if (lane % kPer == 0) sh.red[g][wq][lane / kPer] = sum;
             if (group_or<256>(3, !got)) {
                 ok = false;
                 break;
@@ -811,8 +825,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             if (threadIdx.x < RB) {
                 const int r = threadIdx.x, rg = kAlt ? 0 : r / RW, ri = kAlt ? r : r % RW;
                 auto row_sum = [&](int q) {
-                    auto part = [&](int w) { return __int_as_float(sh.red[q][w][ri]); };
-                    return (part(0) + part(1)) + (part(2) + part(3));
+                    return (sh.red[q][0][ri] + sh.red[q][1][ri]) + (sh.red[q][2][ri] + sh.red[q][3][ri]);
                 };
                 // (-M of 0: the row has seen nothing)
                 auto ref = [&](int q) { return sh.neg_m[q][ri] == 0.f ? kNoRef : -sh.neg_m[q][ri]; };
@@ -855,25 +868,34 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 if (tok < D) {
                     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(A.o) + (size_t)seg_b * A.R * A.Hq * D + tok;
                     float *po = A.part_o + (prow + i0) * D + tok;
+                    float f0[CE], f1[CE], x[CE];
+                    int out[CE];
+                    // (read ahead of the stores, which the compiler keeps them behind)
+#pragma unroll
+                    for (int i = 0; i < CE; i += 4) {
+                        *reinterpret_cast<float4 *>(&f0[i]) = *reinterpret_cast<const float4 *>(&sh.fac[og][oi + i]);
+                        if constexpr (kAlt)
+                            *reinterpret_cast<float4 *>(&f1[i]) = *reinterpret_cast<const float4 *>(&sh.fac[1][oi + i]);
+                        *reinterpret_cast<int4 *>(&out[i]) = *reinterpret_cast<const int4 *>(&sh.out[og][oi + i]);
+                    }
 #pragma unroll
                     for (int i = 0; i < CE; ++i) {
-                        const float f0 = sh.fac[og][oi + i];
                         // (a factor of 0: nothing seen, and O may hold anything)
-                        float x = f0 == 0.f ? 0.f
-                                            : f0 * fmaf(__uint_as_float(b0[i]), 1.f / kLoUp,
-                                                        __uint_as_float(a0[i]));
-                        if constexpr (kAlt) {
-                            const float f1 = sh.fac[1][oi + i];
-                            if (f1 != 0.f)
-                                x = fmaf(f1, fmaf(__uint_as_float(b1[i]), 1.f / kLoUp,
-                                                  __uint_as_float(a1[i])), x);
-                        }
-                        if (seg_whole) {
-                            const int out = sh.out[og][oi + i];
-                            if (out >= 0) o[(size_t)(out >> 1) * D] = __float2bfloat16_rn(x);
-                        } else {
-                            po[i * D] = x;
-                        }
+                        x[i] = f0[i] == 0.f ? 0.f
+                                            : f0[i] * fmaf(__uint_as_float(b0[i]), 1.f / kLoUp,
+                                                           __uint_as_float(a0[i]));
+                        if constexpr (kAlt)
+                            if (f1[i] != 0.f)
+                                x[i] = fmaf(f1[i], fmaf(__uint_as_float(b1[i]), 1.f / kLoUp,
+                                                        __uint_as_float(a1[i])), x[i]);
+                    }
+                    if (seg_whole) {
+#pragma unroll
+                        for (int i = 0; i < CE; ++i)
+                            if (out[i] >= 0) o[(size_t)(out[i] >> 1) * D] = __float2bfloat16_rn(x[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < CE; ++i) po[i * D] = x[i];
                     }
                 }
             }
