@@ -724,7 +724,8 @@ spec_status_t kv8_append(const spec_kv8_desc *cache, int dtype, int n_tokens,
  * SPEC_DEV_BAD_PAGE; more packed tokens than n_slots set SPEC_DEV_BAD_INDEX
  * (pages are taken, the first n_slots slots written).  The new tokens of all
  * requests number at most 2^31 - 1024 (else SPEC_DEV_BAD_INDEX and nothing is
- * planned); seq_len itself is not changed.  One launch.
+ * planned); seq_len itself is not changed.  One launch, two for more than
+ * 4096 slots.
  */
 spec_status_t spec_page_plan(int batch, int page_size, int n_pages,
                              int max_pages_per_seq, const int32_t *seq_len,

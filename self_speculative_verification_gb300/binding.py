@@ -449,10 +449,8 @@ def spec_future_gather(o, last_node, row_offset, out, stream=None):
 def _on(t, dtype, shape, name, dev, optional=False):
     """Device pointer of a contiguous tensor of this type and shape (None: any)
     on device `dev`, the current one, where the library launches."""
-    if t is None:
-        if optional:
-            return None
-        raise TypeError(f"{name} must be a CUDA tensor")
+    if t is None and optional:
+        return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
@@ -471,8 +469,9 @@ def _cur(stream):
     the current device, and that device's index."""
     dev = torch.cuda.current_device()
     if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream.device.index != dev:
+        # (the handle alone: building a Stream object takes ten times as long)
+        return torch._C._cuda_getCurrentRawStream(dev), dev
+    if stream.device.index != dev:
         raise ValueError(f"stream is on {stream.device}, the current device is cuda:{dev}")
     return stream.cuda_stream, dev
 

@@ -9,9 +9,8 @@
 //
 // One warp writes one block: its rows come in as 16-byte vectors (a bf16 row
 // of 128 is half a warp's), the maximum is a bit-pattern maximum over the
-// warp, the rows are read a second time (from L1 / L2: a block's new rows are
-// at most 128 KB) and stored as 8- or 4-byte groups of codes.  Bound by the
-// rows' bytes for prompts and by launch latency for a commit of a few rows.
+// warp, and they leave as 8- or 4-byte groups of codes.  Bound by the rows'
+// bytes for prompts and by launch latency for a commit of a few rows.
 #include "commit_common.cuh"
 #include "kv8.cuh"
 #include "kv8_common.cuh"
@@ -23,15 +22,14 @@ namespace {
 template <typename T> struct RowVec;
 template <> struct RowVec<float> {
     static constexpr int N = 4;
-    __device__ static void load(const float *p, float (&x)[4]) {
-        const float4 v = *reinterpret_cast<const float4 *>(p);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    __device__ static void get(const uint4 &v, float (&x)[4]) {
+        x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
     }
 };
 template <> struct RowVec<__nv_bfloat16> {
     static constexpr int N = 8;
-    __device__ static void load(const __nv_bfloat16 *p, float (&x)[8]) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    __device__ static void get(const uint4 &v, float (&x)[8]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -61,21 +59,36 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const float (&x)[N], f
 
 // One warp: rows `n` of one block, at offsets first .. first + n - 1 of its
 // page; row(i) is the i-th row's first element or nullptr (not written).
+// Sixteen rows pass through registers at a time; a block of more is read
+// twice, the second time from L1 / L2 (at most 128 KB).
 template <typename T, int D, typename Row>
 __device__ void write_block(uint8_t *tile, float *scale, int x, int first, int n, const Row &row) {
     constexpr int N = RowVec<T>::N, LPR = D / N;     // lanes per row
-    constexpr int RPI = 32 / LPR;                    // rows per round
+    constexpr int RPI = 32 / LPR, kHeld = 16 / RPI;  // rows per round, rounds held
     const int lane = threadIdx.x & 31, sub = lane / LPR, col = (lane % LPR) * N;
+    uint4 held[kHeld];
     uint32_t amax = 0;       // bits of the largest finite |x| (they order as the values do)
     bool bad = false, any = false;
-    for (int i0 = 0; i0 < n; i0 += 4 * RPI) {
+    uint32_t have = 0;       // rounds of `held` that hold a row
+    auto fetch = [&](int i0) {
+        have = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kHeld; ++u) {
             const int i = i0 + u * RPI + sub;
             const T *p = i < n ? row(i) : nullptr;
             if (!p) continue;
+            have |= 1u << u;
+            held[u] = *reinterpret_cast<const uint4 *>(p + col);
+        }
+    };
+    const int last = (n - 1) / 16 * 16;
+    for (int i0 = 0; i0 <= last; i0 += 16) {
+        fetch(i0);
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) {
+            if (!((have >> u) & 1u)) continue;
             float v[N];
-            RowVec<T>::load(p + col, v);
+            RowVec<T>::get(held[u], v);
             any = true;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
@@ -110,15 +123,14 @@ __device__ void write_block(uint8_t *tile, float *scale, int x, int first, int n
         }
     }
     const float r = 1.f / s;                         // exact for a power of two
-    for (int i0 = 0; i0 < n; i0 += 4 * RPI) {
+    for (int i0 = last; i0 >= 0; i0 -= 16) {         // (the last rows are still held)
+        if (i0 != last) fetch(i0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * RPI + sub;
-            const T *p = i < n ? row(i) : nullptr;
-            if (!p) continue;
+        for (int u = 0; u < kHeld; ++u) {
+            if (!((have >> u) & 1u)) continue;
             float v[N];
-            RowVec<T>::load(p + col, v);
-            store_codes<N>(tile + kv8_row(first + i, x, D) + col, v, r);
+            RowVec<T>::get(held[u], v);
+            store_codes<N>(tile + kv8_row(first + i0 + u * RPI + sub, x, D) + col, v, r);
         }
     }
     __syncwarp();
@@ -200,7 +212,8 @@ constexpr int kAppendTokens = 64;
 template <typename T, int D>
 __global__ void __launch_bounds__(kWriteWarps * 32) kv8_append_kernel(Append8Params P) {
     pdl_wait();
-    __shared__ int s_start[kAppendTokens];
+    __shared__ int s_start[kAppendTokens], s_len[kAppendTokens];    // len < 0: with gaps
+    __shared__ int s_page[kAppendTokens], s_first[kAppendTokens];
     __shared__ int s_runs[kAppendTokens / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int base = blockIdx.x * kAppendTokens, h0 = blockIdx.y * P.hpc;
@@ -208,8 +221,9 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv8_append_kernel(Append8Par
     if (threadIdx.x < kAppendTokens) {
         const int i = base + threadIdx.x;
         bool start = false;
+        long long s = -1;
         if (i < P.n) {
-            const long long s = P.slots[i];
+            s = P.slots[i];
             if (s >= n_slots) {
                 if (blockIdx.y == 0) raise_status(P.status, SPEC_DEV_BAD_PAGE);
             } else if (s >= 0) {
@@ -223,40 +237,46 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv8_append_kernel(Append8Par
         }
         const unsigned m = __ballot_sync(0xffffffffu, start);
         if (lane == 0) s_runs[warp] = __popc(m);
-        if (start) s_start[warp * 32 + __popc(m & ((1u << lane) - 1u))] = i;
+        if (start) {
+            const int at = warp * 32 + __popc(m & ((1u << lane) - 1u));
+            s_start[at] = i;
+            s_page[at] = (int)(s / P.ps);
+            s_first[at] = (int)(s % P.ps);
+        }
     }
     __syncthreads();
     const int n0 = s_runs[0], n_runs = n0 + s_runs[1];
-    const int heads = min(P.hpc, P.Hkv - h0);
-    for (int u = warp; u < n_runs * heads * 2; u += kWriteWarps) {
-        const int ri = u / (heads * 2), h = h0 + (u >> 1) % heads, x = u & 1;
-        const int i = ri < n0 ? s_start[ri] : s_start[32 + ri - n0];
-        const long long slot = P.slots[i];
-        const int page = (int)(slot / P.ps), first = (int)(slot % P.ps);
-        // the run's length
+    // the runs' lengths, one warp each
+    for (int r = warp; r < n_runs; r += kWriteWarps) {
+        const int at = r < n0 ? r : 32 + r - n0, i = s_start[at], first = s_first[at];
+        const long long slot = (long long)s_page[at] * P.ps + first;
         int n = 0;
         bool gaps = false;
         for (int k = 0; first + k < P.ps; k += 32) {
             const bool in = first + k + lane < P.ps && k + lane < P.n - i;
             const long long s = in ? P.slots[i + k + lane] : 0;
-            gaps = gaps || s < 0;
-            const unsigned m =
-                __ballot_sync(0xffffffffu, !in || (s >= 0 && s != slot + k + lane));
-            if (m) {
-                n = k + __ffs(m) - 1;
-                break;
-            }
-            n = k + 32;
+            const unsigned end = __ballot_sync(0xffffffffu, !in || (s >= 0 && s != slot + k + lane));
+            const int here = end ? __ffs(end) - 1 : 32;
+            gaps = gaps || __any_sync(0xffffffffu, lane < here && s < 0);
+            n = k + here;
+            if (end) break;
         }
+        if (lane == 0) s_len[at] = gaps ? -n : n;
+    }
+    __syncthreads();
+    const int heads = min(P.hpc, P.Hkv - h0);
+    for (int u = warp; u < n_runs * heads * 2; u += kWriteWarps) {
+        const int r = u / (heads * 2), h = h0 + (u >> 1) % heads, x = u & 1;
+        const int at = r < n0 ? r : 32 + r - n0;
+        const int i = s_start[at], page = s_page[at], first = s_first[at], len = s_len[at];
         const T *src = x ? static_cast<const T *>(P.v) + (size_t)i * P.stride_v + (size_t)h * D
                          : static_cast<const T *>(P.k) + (size_t)i * P.stride_k + (size_t)h * D;
         const long long stride = x ? P.stride_v : P.stride_k;
-        gaps = __any_sync(0xffffffffu, gaps);
-        auto row = [&](int r) -> const T * {
-            return gaps && P.slots[i + r] < 0 ? nullptr : src + (size_t)r * stride;
+        auto row = [&](int t) -> const T * {
+            return len < 0 && P.slots[i + t] < 0 ? nullptr : src + (size_t)t * stride;
         };
         write_block<T, D>(P.kv + kv8_block(page, h, P.Hkv, P.ps, D),
-                          P.scales + ((size_t)page * P.Hkv + h) * 2 + x, x, first, n, row);
+                          P.scales + ((size_t)page * P.Hkv + h) * 2 + x, x, first, abs(len), row);
     }
 }
 
@@ -365,10 +385,10 @@ extern "C" spec_status_t kv8_append(const spec_kv8_desc *cache, int dtype, int n
     P.n_pages = cache->n_pages;
     P.status = status_ptr();
     if (!P.status) return SPEC_ERR_CUDA;
-    // heads split over CTAs until every SM has a few
+    // heads split over CTAs until every SM has sixteen
     const int gx = (int)ceil_div_ll(n_tokens, kAppendTokens);
     int split = 1;
-    while (split < P.Hkv && split < 32768 && (long long)gx * split < 4ll * num_sms()) split *= 2;
+    while (split < P.Hkv && split < 32768 && (long long)gx * split < 16ll * num_sms()) split *= 2;
     P.hpc = ceil_div(P.Hkv, split);
     const int gy = ceil_div(P.Hkv, P.hpc);
     if (gy > 65535) return SPEC_ERR_UNSUPPORTED;

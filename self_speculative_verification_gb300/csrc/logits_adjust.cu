@@ -2,19 +2,19 @@
 // on the judged rows.
 //
 // A row's logits change at few tokens (those of the history, of the row's
-// path in the draft tree, and those with a bias) but for its mask, so a CTA
-// takes one request and one slice of the vocabulary for a group of its rows
-// and works in two steps:
-//   1. the rows' slices are copied in 16-byte vectors, tokens the mask does
-//      not allow as -inf;
-//   2. the slice's list of touched tokens -- counted once in shared memory,
-//      the same for all of the request's rows -- is applied to every row from
-//      the row's own logit, with the occurrences on that row's path found
-//      from the ancestor bits of its node.
+// path in the draft tree, and those with a bias) but for its mask.  A CTA
+// takes one request, one slice of the vocabulary and a group of the request's
+// rows:
+//   1. the slice's tokens are counted once in shared memory, the same for all
+//      of the rows, and a bit set for every touched one;
+//   2. the rows' slices pass through registers in 16-byte vectors, several in
+//      flight a thread; a vector without a touched token is copied, the
+//      others' tokens take their penalties and biases, with the occurrences
+//      on that row's path found from the ancestor bits of its node; tokens
+//      that the row's mask does not allow become -inf.
 // Counts are integers and a token's biases are added in index order, so
 // results do not depend on the order of the threads.  Bound by the rows'
-// bytes, read and written once; one pass over the history per slice comes
-// from L2.
+// bytes, read and written once; the history is read once per CTA, from L2.
 #include <math.h>
 
 #include "common.cuh"
@@ -24,6 +24,8 @@ namespace {
 
 constexpr int kAdjThreads = 256;
 constexpr int kAdjSlice = 2048;              // vocabulary tokens a CTA takes
+constexpr int kAdjRows = 64;                 // most rows a CTA takes
+constexpr int kAdjFlight = 4;                // vectors in flight a thread
 constexpr int kAdjMaxNodes = SPEC_MAX_ROWS;
 constexpr int kAdjMaxBias = 1024;
 constexpr uint32_t kAdjSeen = 0x80000000u;   // in the history (prompt or not)
@@ -38,79 +40,36 @@ struct AdjParams {
     const uint32_t *mask_bits;
     const int32_t *row_mask;
     int B, Rj, V, N, H, n_bias, n_masks;
-    int slice, rows;                         // tokens and rows a CTA takes
+    int rows;                                // rows a CTA takes
     int *status;
 };
 
-// Copies n elements, element i allowed iff bit v0 + i of mask (mask NULL: all
-// are); others become -inf.
-template <typename T>
-__device__ void copy_masked(T *dst, const T *src, int n, const uint32_t *mask, int v0) {
-    constexpr int N = 16 / (int)sizeof(T);
-    constexpr uint32_t kNegInf = sizeof(T) == 2 ? 0xff80u : 0xff800000u;
-    const int tid = threadIdx.x;
-    auto one = [&](int i) {
-        T x = src[i];
-        if (mask && !((mask[(v0 + i) >> 5] >> ((v0 + i) & 31)) & 1u)) store_f(&x, -INFINITY);
-        dst[i] = x;
-    };
-    if (((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(src)) & 15) != 0) {
-        for (int i = tid; i < n; i += kAdjThreads) one(i);
-        return;
-    }
-    // up to the first 16-byte boundary, vectors, the rest
-    const int off = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
-    const int lead = min(n, off ? N - off : 0);
-    if (tid < lead) one(tid);
-    const int nv = (n - lead) / N;
-    const uint4 *sp = reinterpret_cast<const uint4 *>(src + lead);
-    uint4 *dp = reinterpret_cast<uint4 *>(dst + lead);
-    for (int i = tid; i < nv; i += kAdjThreads) {
-        uint4 x = sp[i];
-        if (mask) {
-            // the vector's N mask bits, which may lie in two words
-            const int v = v0 + lead + i * N;
-            const int w = v >> 5, s = v & 31;
-            uint64_t m = mask[w];
-            if (s + N > 32) m |= (uint64_t)mask[w + 1] << 32;
-            const uint32_t ok = (uint32_t)(m >> s);
-            uint32_t e[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (N == 8) {
-                    if (!((ok >> (2 * j)) & 1u)) e[j] = (e[j] & 0xffff0000u) | kNegInf;
-                    if (!((ok >> (2 * j + 1)) & 1u)) e[j] = (e[j] & 0xffffu) | (kNegInf << 16);
-                } else {
-                    if (!((ok >> j) & 1u)) e[j] = kNegInf;
-                }
-            }
-            x = make_uint4(e[0], e[1], e[2], e[3]);
-        }
-        dp[i] = x;
-    }
-    const int t0 = lead + nv * N;
-    if (t0 + tid < n) one(t0 + tid);         // fewer than N <= kAdjThreads are left
+// Bits [at, at + 8) of a bit string.
+__device__ __forceinline__ uint32_t bits8(const uint32_t *w, int at) {
+    const int s = at & 31;
+    uint64_t m = w[at >> 5];
+    if (s > 24) m |= (uint64_t)w[(at >> 5) + 1] << 32;
+    return (uint32_t)(m >> s) & 0xffu;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P) {
     pdl_wait();
+    constexpr int N = 16 / (int)sizeof(T);           // logits a vector
     __shared__ uint32_t s_cnt[kAdjSlice];            // occurrences behind the prompt | kAdjSeen
     __shared__ float s_bias[kAdjSlice];
     __shared__ int16_t s_node[kAdjSlice];            // first node with the token, -1
-    __shared__ uint16_t s_list[kAdjSlice];           // the touched tokens
+    __shared__ uint32_t s_hit[kAdjSlice / 32 + 1];   // touched tokens
     __shared__ uint32_t s_anc[kAdjMaxNodes][kAdjMaxNodes / 32];   // path of each node
     __shared__ int16_t s_par[kAdjMaxNodes], s_next[kAdjMaxNodes];
     __shared__ int s_tok[kAdjMaxNodes];
-    __shared__ int s_n;
+    __shared__ int s_mask[kAdjRows], s_follow[kAdjRows];          // mask and node of each row
     const int tid = threadIdx.x, lane = tid & 31;
-    const int b = blockIdx.y, v0 = blockIdx.x * P.slice, nv = min(P.slice, P.V - v0);
-    const int j0 = blockIdx.z * P.rows, j1 = min(P.Rj, j0 + P.rows);
+    const int b = blockIdx.y, v0 = blockIdx.x * kAdjSlice, nv = min(kAdjSlice, P.V - v0);
+    const int j0 = blockIdx.z * P.rows, rows = min(P.Rj - j0, P.rows);
     int bits = 0;
-    const T *in = static_cast<const T *>(P.logits) + (size_t)b * P.Rj * P.V + v0;
-    T *out = static_cast<T *>(P.out) + (size_t)b * P.Rj * P.V + v0;
 
-    for (int i = tid; i < nv; i += kAdjThreads) {
+    for (int i = tid; i < kAdjSlice; i += kAdjThreads) {
         s_cnt[i] = 0u;
         s_bias[i] = 0.f;
         s_node[i] = -1;
@@ -123,7 +82,22 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
         s_par[x] = (int16_t)((p >= x || p < -1) ? -2 : p);
         s_tok[x] = P.tokens[(size_t)b * P.N + x];
     }
-    if (tid == 0) s_n = 0;
+    for (int j = tid; j < rows; j += kAdjThreads) {
+        const size_t at = (size_t)b * P.Rj + j0 + j;
+        int m = P.n_masks > 0 ? P.row_mask[at] : -1;
+        if (P.n_masks > 0 && m >= P.n_masks) {
+            bits |= SPEC_DEV_BAD_INDEX;
+            m = -1;
+        }
+        s_mask[j] = m;
+        int node = -1;
+        if (P.N > 0) node = P.row_node ? P.row_node[at] : j0 + j;
+        if (node >= P.N || node < -1) {
+            bits |= SPEC_DEV_BAD_INDEX;
+            node = -1;
+        }
+        s_follow[j] = node;
+    }
     __syncthreads();
 
     // the history's tokens of this slice
@@ -134,15 +108,15 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
     }
     const int np = P.n_prompt ? P.n_prompt[b] : 0;
     const int32_t *hist = P.history + (size_t)b * P.H;
-    for (int i0 = tid; i0 < hl; i0 += 4 * kAdjThreads) {
-        int t[4];
+    for (int i0 = tid; i0 < hl; i0 += 8 * kAdjThreads) {
+        int t[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
             const int i = i0 + u * kAdjThreads;
             t[u] = i < hl ? hist[i] : -1;
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
             if (t[u] >= P.V) bits |= SPEC_DEV_BAD_INDEX;
             const int v = t[u] - v0;
             if (t[u] < 0 || v < 0 || v >= nv) continue;
@@ -187,65 +161,119 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
             if (leads) s_node[v] = (int16_t)x;
         }
     }
-    // step 1, which touches none of the above
-    for (int j = j0; j < j1; ++j) {
-        int m = P.n_masks > 0 ? P.row_mask[(size_t)b * P.Rj + j] : -1;
-        if (m >= P.n_masks && P.n_masks > 0) {
-            bits |= SPEC_DEV_BAD_INDEX;
-            m = -1;
-        }
-        const uint32_t *mask = m >= 0 ? P.mask_bits + (size_t)m * ((P.V + 31) / 32) : nullptr;
-        if (mask || in != out)
-            copy_masked(out + (size_t)j * P.V, in + (size_t)j * P.V, nv, mask, v0);
-    }
-    __syncthreads();
-
-    // the touched tokens
-    for (int i = tid; i < kAdjSlice; i += kAdjThreads) {
-        const bool on = i < nv && (s_cnt[i] != 0u || s_node[i] >= 0 || s_bias[i] != 0.f);
-        const unsigned m = __ballot_sync(0xffffffffu, on);
-        int at = 0;
-        if (lane == 0 && m) at = atomicAdd(&s_n, __popc(m));
-        at = __shfl_sync(0xffffffffu, at, 0);
-        if (on) s_list[at + __popc(m & ((1u << lane) - 1u))] = (uint16_t)i;
-    }
-    __syncthreads();
-    const int n = s_n;
-    const float rep = P.repetition ? P.repetition[b] : 1.f;
-    const float pres = P.presence ? P.presence[b] : 0.f;
-    const float freq = P.frequency ? P.frequency[b] : 0.f;
-    for (int j = j0 + (tid >> 5); j < j1; j += kAdjThreads / 32) {
-        int node = -1;
-        if (P.N > 0) node = P.row_node ? P.row_node[(size_t)b * P.Rj + j] : j;
-        if (node >= P.N || node < -1) {
-            bits |= SPEC_DEV_BAD_INDEX;
-            node = -1;
-        }
-        if (blockIdx.x == 0) {            // this row's path: reported once
-            for (int y = node; y != -1; y = s_par[y]) {
+    if (blockIdx.x == 0)                     // the rows' paths: reported once
+        for (int j = tid; j < rows; j += kAdjThreads)
+            for (int y = s_follow[j]; y != -1; y = s_par[y]) {
                 if (y == -2) {
                     bits |= SPEC_DEV_BAD_TREE;
                     break;
                 }
                 if (s_tok[y] >= P.V) bits |= SPEC_DEV_BAD_INDEX;
             }
+    __syncthreads();
+    for (int i = tid; i < kAdjSlice; i += kAdjThreads) {
+        const unsigned m =
+            __ballot_sync(0xffffffffu, s_cnt[i] != 0u || s_node[i] >= 0 || s_bias[i] != 0.f);
+        if (lane == 0) s_hit[i >> 5] = m;
+    }
+    if (tid == 0) s_hit[kAdjSlice / 32] = 0u;
+    __syncthreads();
+
+    const float rep = P.repetition ? P.repetition[b] : 1.f;
+    const float pres = P.presence ? P.presence[b] : 0.f;
+    const float freq = P.frequency ? P.frequency[b] : 0.f;
+    const int words = (P.V + 31) / 32;
+    // a touched token's logit, in the row that follows `node`
+    auto adjust = [&](float z, int v, int node) {
+        const uint32_t c = s_cnt[v];
+        int k = (int)(c & ~kAdjSeen);
+        if (node >= 0)
+            for (int y = s_node[v]; y >= 0; y = s_next[y]) k += (s_anc[node][y >> 5] >> (y & 31)) & 1u;
+        if (k > 0 || (c & kAdjSeen)) z = z > 0.f ? z / rep : z * rep;
+        return z - freq * (float)k - (k > 0 ? pres : 0.f) + s_bias[v];
+    };
+    const T *in = static_cast<const T *>(P.logits) + ((size_t)b * P.Rj + j0) * P.V + v0;
+    T *out = static_cast<T *>(P.out) + ((size_t)b * P.Rj + j0) * P.V + v0;
+    // one logit at a time: `n` of row j from `first`
+    auto singles = [&](int j, int first, int n) {
+        for (int i = first; i < first + n; ++i) {
+            const T *src = in + (size_t)j * P.V + i;
+            T x = *src;
+            if ((s_hit[i >> 5] >> (i & 31)) & 1u) store_f(&x, adjust(load_f(src), i, s_follow[j]));
+            if (s_mask[j] >= 0 &&
+                !((P.mask_bits[(size_t)s_mask[j] * words + ((v0 + i) >> 5)] >> ((v0 + i) & 31)) & 1u))
+                store_f(&x, -INFINITY);
+            out[(size_t)j * P.V + i] = x;
         }
-        const int m = P.n_masks > 0 ? P.row_mask[(size_t)b * P.Rj + j] : -1;
-        const uint32_t *mask =
-            m >= 0 && m < P.n_masks ? P.mask_bits + (size_t)m * ((P.V + 31) / 32) : nullptr;
-        for (int i = lane; i < n; i += 32) {
-            const int v = s_list[i];
-            if (mask && !((mask[(v0 + v) >> 5] >> ((v0 + v) & 31)) & 1u)) continue;
-            const uint32_t c = s_cnt[v];
-            int k = (int)(c & ~kAdjSeen);
-            if (node >= 0)
-                for (int y = s_node[v]; y >= 0; y = s_next[y])
-                    k += (s_anc[node][y >> 5] >> (y & 31)) & 1u;
-            float z = load_f(in + (size_t)j * P.V + v);
-            if (k > 0 || (c & kAdjSeen)) z = z > 0.f ? z / rep : z * rep;
-            z = z - freq * (float)k - (k > 0 ? pres : 0.f) + s_bias[v];
-            store_f(out + (size_t)j * P.V + v, z);
+    };
+    if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
+        for (int i = tid; i < rows * nv; i += kAdjThreads) singles(i / nv, i % nv, 1);
+        if (bits) raise_status(P.status, bits);
+        return;
+    }
+    // row j's logits up to its first 16-byte boundary, and its vectors
+    auto lead_of = [&](int j) {
+        const int off = (int)((reinterpret_cast<uintptr_t>(in + (size_t)j * P.V) & 15) / sizeof(T));
+        return min(nv, off ? N - off : 0);
+    };
+    constexpr int kVecs = kAdjSlice / N;             // at most, a row
+    for (int i0 = tid; i0 < rows * kVecs; i0 += kAdjFlight * kAdjThreads) {
+        uint4 x[kAdjFlight];
+        int row[kAdjFlight], at[kAdjFlight];         // at: within the slice, -1 none
+        uint32_t ok[kAdjFlight];
+#pragma unroll
+        for (int f = 0; f < kAdjFlight; ++f) {
+            const int i = i0 + f * kAdjThreads, j = i / kVecs, e = i % kVecs;
+            at[f] = -1;
+            row[f] = j;
+            ok[f] = 0xffu;
+            if (j >= rows) continue;
+            const int lead = lead_of(j);
+            if (e >= (nv - lead) / N) continue;
+            at[f] = lead + e * N;
+            x[f] = *reinterpret_cast<const uint4 *>(in + (size_t)j * P.V + at[f]);
+            if (s_mask[j] >= 0) {
+                const int v = v0 + at[f], w = v >> 5, sft = v & 31;
+                const uint32_t *mw = P.mask_bits + (size_t)s_mask[j] * words;
+                uint64_t m = mw[w];
+                if (sft + N > 32) m |= (uint64_t)mw[w + 1] << 32;
+                ok[f] = (uint32_t)(m >> sft);
+            }
         }
+#pragma unroll
+        for (int f = 0; f < kAdjFlight; ++f) {
+            if (at[f] < 0) continue;
+            constexpr uint32_t kAll = (1u << N) - 1u;
+            const uint32_t hit = bits8(s_hit, at[f]) & kAll;
+            uint32_t e[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+            if (hit | (~ok[f] & kAll)) {
+                const int node = s_follow[row[f]];
+#pragma unroll
+                for (int q = 0; q < N; ++q) {
+                    const bool touched = (hit >> q) & 1u, masked = !((ok[f] >> q) & 1u);
+                    if (!touched && !masked) continue;
+                    if constexpr (N == 8) {
+                        const uint32_t h = (e[q >> 1] >> (16 * (q & 1))) & 0xffffu;
+                        uint32_t r = 0xff80u;            // -inf
+                        if (!masked) {
+                            const float z = adjust(__uint_as_float(h << 16), at[f] + q, node);
+                            r = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(z));
+                        }
+                        e[q >> 1] = (e[q >> 1] & (0xffffu << (16 * (1 - (q & 1))))) | (r << (16 * (q & 1)));
+                    } else {
+                        e[q] = masked ? 0xff800000u
+                                      : __float_as_uint(adjust(__uint_as_float(e[q]), at[f] + q, node));
+                    }
+                }
+            }
+            *reinterpret_cast<uint4 *>(out + (size_t)row[f] * P.V + at[f]) = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+    }
+    // the rows' ends outside the vectors: fewer than N logits each
+    for (int i = tid; i < 2 * rows; i += kAdjThreads) {
+        const int j = i >> 1, lead = lead_of(j), tail = (nv - lead) % N;
+        if (i & 1) singles(j, nv - tail, tail);
+        else singles(j, 0, lead);
     }
     if (bits) raise_status(P.status, bits);
 }
@@ -296,11 +324,15 @@ extern "C" spec_status_t spec_logits_adjust(
     P.n_masks = d->n_masks;
     P.status = status_ptr();
     if (!P.status) return SPEC_ERR_CUDA;
-    P.slice = kAdjSlice;
-    P.rows = P.Rj;
-    const int slices = ceil_div(P.V, P.slice);
-    // rows split until every SM has two CTAs
-    while (P.rows > 1 && (long long)slices * P.B * ceil_div(P.Rj, P.rows) < 2ll * num_sms())
+    // Rows a CTA: enough for its rows' bytes to outweigh the history it reads
+    // (4 bytes a token against two times its logits' size), fewer until every
+    // SM has four CTAs
+    const int slices = ceil_div(P.V, kAdjSlice);
+    const int es = d->logit_dtype == SPEC_BF16 ? 2 : 4;
+    const long long even = 4ll * P.H / (2ll * es * kAdjSlice);
+    P.rows = (int)(even < 8 ? 8 : even > kAdjRows ? kAdjRows : even);
+    if (P.rows > P.Rj) P.rows = P.Rj;
+    while (P.rows > 1 && (long long)slices * P.B * ceil_div(P.Rj, P.rows) < 4ll * num_sms())
         P.rows = ceil_div(P.rows, 2);
     const dim3 grid(slices, P.B, ceil_div(P.Rj, P.rows));
     if (grid.z > 65535) return SPEC_ERR_UNSUPPORTED;

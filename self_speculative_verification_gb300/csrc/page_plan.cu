@@ -1,26 +1,22 @@
 // spec_page_plan: block tables and slot maps from request lengths.
 //
-// One launch of one thread-block cluster (one CTA for small batches, up to
-// eight): every CTA scans the requests by itself -- pages and tokens before
-// each, kept in shared memory a chunk of requests at a time -- and then takes
-// its share of the packed tokens, 128 to a warp; a token that opens a new page
-// also records it in the page table.  The cluster barrier at the end orders
-// the update of free_head behind every CTA's read of it, so no second launch
-// is needed.  Bound by launch and scan latency; the slots are 8 bytes each.
-#include <cooperative_groups.h>
-
+// Every CTA scans the requests by itself -- pages and tokens before each, kept
+// in shared memory a chunk of requests at a time -- and then takes its share
+// of the packed tokens, 256 to a warp; a token that opens a new page also
+// records it in the page table.  A small batch is one CTA and one launch; a
+// larger one is spread over the SMs, and a second launch moves free_head,
+// which every CTA of the first has to have read.  Bound by launch and scan
+// latency; the slots are 8 bytes each.
 #include "common.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace sv {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 constexpr int kPlanChunk = 2048;                     // requests scanned at a time
 constexpr int kPlanItems = kPlanChunk / kPlanThreads;
-constexpr int kPlanTokens = 128;                     // packed tokens a warp takes at a time
-constexpr int kPlanMaxCtas = 8;
+constexpr int kPlanTokens = 256;                     // packed tokens a warp takes at a time
+constexpr int kPlanAlone = 4096;                     // slots that one CTA takes alone
 
 struct PlanParams {
     const int32_t *seq_len, *n_new, *free_pages;
@@ -28,6 +24,10 @@ struct PlanParams {
     int64_t *slot_map;
     long long n_slots;
     int B, ps, n_pages, max_pages, n_free, capacity;
+    // pos / ps as (pos ps_mul) >> ps_shift: with L = ceil(log2 ps), ps_mul =
+    // ceil(2^(31 + L) / ps) and ps_shift = 31 + L, exact for pos < 2^31
+    uint64_t ps_mul;
+    int ps_shift;
     int *status;
 };
 
@@ -62,7 +62,8 @@ __device__ __forceinline__ PlanReq plan_request(const PlanParams &P, int b, int 
 // Exclusive sums over the block of two values a thread.
 __device__ void block_scan2(long long a, long long p, long long *ex_a, long long *ex_p,
                             long long *tot_a, long long *tot_p) {
-    __shared__ long long sa[32], sp[32];
+    constexpr int kWarps = kPlanThreads / 32;
+    __shared__ long long sa[kWarps], sp[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto scan = [&](long long x) {
 #pragma unroll
@@ -78,7 +79,7 @@ __device__ void block_scan2(long long a, long long p, long long *ex_a, long long
         sp[warp] = ip;
     }
     __syncthreads();
-    const long long wa = scan(sa[lane]), wp = scan(sp[lane]);
+    const long long wa = scan(lane < kWarps ? sa[lane] : 0), wp = scan(lane < kWarps ? sp[lane] : 0);
     *tot_a = __shfl_sync(0xffffffffu, wa, 31);
     *tot_p = __shfl_sync(0xffffffffu, wp, 31);
     const long long ba = __shfl_sync(0xffffffffu, wa, warp > 0 ? warp - 1 : 0);
@@ -88,10 +89,9 @@ __device__ void block_scan2(long long a, long long p, long long *ex_a, long long
     __syncthreads();          // sa / sp may be written again
 }
 
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams P) {
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams P, bool move_head) {
     pdl_wait();
-    cg::cluster_group cluster = cg::this_cluster();
-    const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int nc = (int)gridDim.x, rank = (int)blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31;
     __shared__ int s_cu[kPlanChunk + 1];      // first packed token, within the chunk
     __shared__ int s_S[kPlanChunk];
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams P) {
     block_scan2(tok, pages, &d0, &d1, &tot_tok, &tot_pages);
     const int head = *P.free_head;
     bool serve = head >= 0 && (long long)head + tot_pages <= P.n_free;
-    if (!serve) bits |= SPEC_DEV_CAPACITY;
+    if (!serve) bits |= SPEC_DEV_CAPACITY;       // (every CTA finds the same)
     const bool fits = tot_tok <= (1ll << 31) - 1024;
     if (!fits || tot_tok > P.n_slots) bits |= SPEC_DEV_BAD_INDEX;
     serve = serve && fits;
@@ -159,25 +159,38 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams P) {
                 else hi = mid - 1;
             }
             int k = lo;
-#pragma unroll 4
-            for (int i = 0; i < kPlanTokens; i += 32) {
-                const int t = (int)t0 + i + lane;
-                if (t >= n_tok) break;
+            // every token's page first, so that their loads are in flight at once
+            constexpr int kPer = kPlanTokens / 32;
+            int page[kPer], off[kPer];
+            int32_t *entry[kPer];            // where a page it opens is recorded
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int t = (int)t0 + i * 32 + lane;
+                page[i] = -2;                // no slot
+                off[i] = 0;
+                entry[i] = nullptr;
+                if (t >= n_tok) continue;
                 while (t >= s_cu[k + 1]) ++k;
+                if (!s_ok[k]) continue;
+                const int S = s_S[k], pos = S + t - s_cu[k];
+                const int j = (int)(((uint64_t)pos * P.ps_mul) >> P.ps_shift);
+                off[i] = pos - j * P.ps;
+                int32_t *at = P.page_table + (size_t)(b0 + k) * P.max_pages + j;
+                const bool fresh = j * P.ps >= S;            // a page it takes now
+                page[i] = fresh ? P.free_pages[s_pg[k] + j] : *at;
+                if (fresh && off[i] == 0) entry[i] = at;
+                if (page[i] < 0) page[i] = -1;
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int t = (int)t0 + i * 32 + lane;
+                if (t >= n_tok) continue;
                 long long slot = -1;
-                if (s_ok[k]) {
-                    const int S = s_S[k], pos = S + t - s_cu[k];
-                    const int j = pos / P.ps, off = pos - j * P.ps;
-                    const bool fresh = j * P.ps >= S;        // a page it takes now
-                    const int page = fresh ? P.free_pages[s_pg[k] + j]
-                                           : P.page_table[(size_t)(b0 + k) * P.max_pages + j];
-                    if (page >= 0 && page < P.n_pages) {
-                        slot = (long long)page * P.ps + off;
-                        if (fresh && off == 0)
-                            P.page_table[(size_t)(b0 + k) * P.max_pages + j] = page;
-                    } else {
-                        bits |= SPEC_DEV_BAD_PAGE;
-                    }
+                if (page[i] >= 0 && page[i] < P.n_pages) {
+                    slot = (long long)page[i] * P.ps + off[i];
+                    if (entry[i]) *entry[i] = page[i];
+                } else if (page[i] != -2) {
+                    bits |= SPEC_DEV_BAD_PAGE;
                 }
                 if (tok0 + t < P.n_slots) P.slot_map[tok0 + t] = slot;
             }
@@ -197,8 +210,28 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams P) {
         }
     if (rank == 0 && tid == 0) P.cu_new[P.B] = fits ? (int32_t)tot_tok : 0;
     if (bits) raise_status(P.status, bits);
-    cluster.sync();               // every CTA has read free_head
-    if (rank == 0 && tid == 0 && serve) *P.free_head = head + (int)tot_pages;
+    if (move_head) {                          // (one CTA, whose threads have all read it)
+        __syncthreads();
+        if (tid == 0 && serve) *P.free_head = head + (int)tot_pages;
+    }
+}
+
+// free_head, behind a plan of several CTAs (which has reported what is wrong).
+__global__ void __launch_bounds__(kPlanThreads) page_plan_head_kernel(PlanParams P) {
+    pdl_wait();
+    int bits = 0;
+    long long tok = 0, pages = 0, tot_tok, tot_pages, d0, d1;
+    for (int b = threadIdx.x; b < P.B; b += kPlanThreads) {
+        const PlanReq r = plan_request(P, b, &bits);
+        tok += r.n;
+        pages += r.take;
+    }
+    block_scan2(tok, pages, &d0, &d1, &tot_tok, &tot_pages);
+    const int head = *P.free_head;
+    __syncthreads();
+    if (threadIdx.x == 0 && head >= 0 && (long long)head + tot_pages <= P.n_free &&
+        tot_tok <= (1ll << 31) - 1024)
+        *P.free_head = head + (int)tot_pages;
 }
 
 }  // namespace
@@ -237,22 +270,18 @@ extern "C" spec_status_t spec_page_plan(int batch, int page_size, int n_pages,
     P.capacity = max_pages_per_seq * page_size;
     P.status = status_ptr();
     if (!P.status) return SPEC_ERR_CUDA;
-    // one CTA per 8192 slots (8 for each thread), up to a portable cluster
+    int log = 0;
+    while ((1ll << log) < page_size) ++log;
+    P.ps_shift = 31 + log;
+    P.ps_mul = ((1ull << P.ps_shift) + page_size - 1) / page_size;
+    cudaStream_t s = as_stream(stream);
+    // a plan of few slots is one CTA's; others: 8 warps' pieces a CTA
     int nc = 1;
-    while (nc < kPlanMaxCtas && n_slots > 8192ll * nc) nc *= 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(nc);
-    cfg.blockDim = dim3(kPlanThreads);
-    cfg.stream = as_stream(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = nc;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, page_plan_kernel, P) != cudaSuccess) return SPEC_ERR_CUDA;
-    return launch_status();
+    if (n_slots > kPlanAlone) {
+        const long long want = (n_slots + 8 * kPlanTokens - 1) / (8 * kPlanTokens);
+        nc = (int)(want < num_sms() ? want : num_sms());
+    }
+    spec_status_t st = launch(page_plan_kernel, dim3(nc), dim3(kPlanThreads), 0, s, P, nc == 1);
+    if (st == SPEC_OK && nc > 1) st = launch(page_plan_head_kernel, dim3(1), dim3(kPlanThreads), 0, s, P);
+    return st != SPEC_OK ? st : launch_status();
 }
