@@ -765,6 +765,7 @@ spec_status_t spec_page_plan(int batch, int page_size, int n_pages,
  *       z = z > 0 ? z / repetition : z * repetition
  *   z = z - frequency * n - (n > 0 ? presence : 0) + bias[v]
  *   out[v] = allowed ? z, rounded to nearest : -inf
+ * (computed as z * factor + sum, the factor and the sum rounded to fp32).
  * A row whose mask allows nothing is -inf throughout.  A history, draft or
  * bias token >= vocab, a row_node or row_mask out of range, or a hist_len
  * outside [0, hist_cap] (clamped) is left out and sets SPEC_DEV_BAD_INDEX; a

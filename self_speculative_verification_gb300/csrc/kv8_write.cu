@@ -18,13 +18,17 @@
 namespace sv {
 namespace {
 
-// One 16-byte vector of new values as floats.
+// One 16-byte vector of new values: its floats, and the largest |x| of it as
+// fp32 bits (which order as the values do; a non-finite one is the largest).
 template <typename T> struct RowVec;
 template <> struct RowVec<float> {
     static constexpr int N = 4;
     __device__ static void get(const uint4 &v, float (&x)[4]) {
         x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
         x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+    }
+    __device__ static uint32_t amax(const uint4 &v) {
+        return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
     }
 };
 template <> struct RowVec<__nv_bfloat16> {
@@ -37,22 +41,28 @@ template <> struct RowVec<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    __device__ static uint32_t amax(const uint4 &v) {
+        auto max2 = [](uint32_t a, uint32_t b) {
+            uint32_t r;
+            asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+            return r;
+        };
+        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+        return max(m << 16, m & 0xffff0000u);
+    }
 };
 
-// N values as codes: x * r, a non-finite x as NaN.
+// N values as codes, x * r; `odd`: among non-finite ones, which become NaN.
 template <int N>
-__device__ __forceinline__ void store_codes(uint8_t *dst, const float (&x)[N], float r) {
+__device__ __forceinline__ void store_codes(uint8_t *dst, float (&x)[N], float r, bool odd) {
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = fabsf(x[i]) < INFINITY ? x[i] : __uint_as_float(0x7fffffffu);
+    }
     uint32_t w[N / 4];
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-        float y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float v = x[4 * i + j];
-            y[j] = fabsf(v) < INFINITY ? v * r : __uint_as_float(0x7fffffffu);
-        }
-        w[i] = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
-    }
+    for (int i = 0; i < N / 4; ++i)
+        w[i] = e4m3x2(x[4 * i] * r, x[4 * i + 1] * r) | (e4m3x2(x[4 * i + 2] * r, x[4 * i + 3] * r) << 16);
     if constexpr (N == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t *>(dst) = w[0];
 }
@@ -67,8 +77,6 @@ __device__ void write_block(uint8_t *tile, float *scale, int x, int first, int n
     constexpr int RPI = 32 / LPR, kHeld = 16 / RPI;  // rows per round, rounds held
     const int lane = threadIdx.x & 31, sub = lane / LPR, col = (lane % LPR) * N;
     uint4 held[kHeld];
-    uint32_t amax = 0;       // bits of the largest finite |x| (they order as the values do)
-    bool bad = false, any = false;
     uint32_t have = 0;       // rounds of `held` that hold a row
     auto fetch = [&](int i0) {
         have = 0;
@@ -76,32 +84,41 @@ __device__ void write_block(uint8_t *tile, float *scale, int x, int first, int n
         for (int u = 0; u < kHeld; ++u) {
             const int i = i0 + u * RPI + sub;
             const T *p = i < n ? row(i) : nullptr;
+            held[u] = make_uint4(0u, 0u, 0u, 0u);
             if (!p) continue;
             have |= 1u << u;
             held[u] = *reinterpret_cast<const uint4 *>(p + col);
         }
     };
+    constexpr uint32_t kInf = 0x7f800000u;
     const int last = (n - 1) / 16 * 16;
+    uint32_t amax = 0, any = 0;
     for (int i0 = 0; i0 <= last; i0 += 16) {
         fetch(i0);
+        any |= have;
 #pragma unroll
-        for (int u = 0; u < kHeld; ++u) {
-            if (!((have >> u) & 1u)) continue;
-            float v[N];
-            RowVec<T>::get(held[u], v);
-            any = true;
+        for (int u = 0; u < kHeld; ++u) amax = max(amax, RowVec<T>::amax(held[u]));
+    }
+    if (!__any_sync(0xffffffffu, any != 0u)) return;
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    const bool bad = amax >= kInf;
+    if (bad) {               // the largest finite one, value by value
+        amax = 0;
+        for (int i0 = 0; i0 <= last; i0 += 16) {
+            if (last > 0) fetch(i0);
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const uint32_t a = __float_as_uint(v[j]) & 0x7fffffffu;
-                if (a >= 0x7f800000u) bad = true;
-                else amax = max(amax, a);
+            for (int u = 0; u < kHeld; ++u) {
+                float v[N];
+                RowVec<T>::get(held[u], v);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const uint32_t a = __float_as_uint(v[j]) & 0x7fffffffu;
+                    if (a < kInf) amax = max(amax, a);
+                }
             }
         }
+        amax = __reduce_max_sync(0xffffffffu, amax);
     }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    bad = __any_sync(0xffffffffu, bad);
-    any = __any_sync(0xffffffffu, any);
-    if (!any) return;
     const float need = exp2_int(kv8_exponent(__uint_as_float(amax)));
     const float was = first > 0 ? *scale : 0.f;
     // a partly used block keeps the larger scale; NaN stays NaN
@@ -130,7 +147,7 @@ __device__ void write_block(uint8_t *tile, float *scale, int x, int first, int n
             if (!((have >> u) & 1u)) continue;
             float v[N];
             RowVec<T>::get(held[u], v);
-            store_codes<N>(tile + kv8_row(first + i0 + u * RPI + sub, x, D) + col, v, r);
+            store_codes<N>(tile + kv8_row(first + i0 + u * RPI + sub, x, D) + col, v, r, bad);
         }
     }
     __syncwarp();
@@ -210,7 +227,7 @@ constexpr int kAppendTokens = 64;
 // run: consecutive tokens in consecutive slots of one page, tokens that are
 // not written in between), one warp per (run, head, K / V).
 template <typename T, int D>
-__global__ void __launch_bounds__(kWriteWarps * 32) kv8_append_kernel(Append8Params P) {
+__global__ void __launch_bounds__(kWriteWarps * 32, 4) kv8_append_kernel(Append8Params P) {
     pdl_wait();
     __shared__ int s_start[kAppendTokens], s_len[kAppendTokens];    // len < 0: with gaps
     __shared__ int s_page[kAppendTokens], s_first[kAppendTokens];

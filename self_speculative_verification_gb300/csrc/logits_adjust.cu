@@ -57,7 +57,8 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
     pdl_wait();
     constexpr int N = 16 / (int)sizeof(T);           // logits a vector
     __shared__ uint32_t s_cnt[kAdjSlice];            // occurrences behind the prompt | kAdjSeen
-    __shared__ float s_bias[kAdjSlice];
+    __shared__ float s_add[kAdjSlice];               // the biases, then what a row without the
+                                                     // token on its path adds
     __shared__ int16_t s_node[kAdjSlice];            // first node with the token, -1
     __shared__ uint32_t s_hit[kAdjSlice / 32 + 1];   // touched tokens
     __shared__ uint32_t s_anc[kAdjMaxNodes][kAdjMaxNodes / 32];   // path of each node
@@ -71,7 +72,7 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
 
     for (int i = tid; i < kAdjSlice; i += kAdjThreads) {
         s_cnt[i] = 0u;
-        s_bias[i] = 0.f;
+        s_add[i] = 0.f;
         s_node[i] = -1;
     }
     for (int x = tid; x < P.N; x += kAdjThreads) {
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
         float x = bias[i];
         for (int k = i + 1; k < P.n_bias; ++k)
             if (ids[k] == t) x += bias[k];
-        s_bias[v] = x;
+        s_add[v] = x;
     }
     // the draft's paths, and its tokens of this slice
     for (int x = tid; x < P.N; x += kAdjThreads) {
@@ -171,26 +172,34 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
                 if (s_tok[y] >= P.V) bits |= SPEC_DEV_BAD_INDEX;
             }
     __syncthreads();
+    const float rep = P.repetition ? P.repetition[b] : 1.f, inv_rep = 1.f / rep;
+    const float pres = P.presence ? P.presence[b] : 0.f;
+    const float freq = P.frequency ? P.frequency[b] : 0.f;
     for (int i = tid; i < kAdjSlice; i += kAdjThreads) {
-        const unsigned m =
-            __ballot_sync(0xffffffffu, s_cnt[i] != 0u || s_node[i] >= 0 || s_bias[i] != 0.f);
+        const uint32_t c = s_cnt[i];
+        const unsigned m = __ballot_sync(0xffffffffu, c != 0u || s_node[i] >= 0 || s_add[i] != 0.f);
         if (lane == 0) s_hit[i >> 5] = m;
+        const int k = (int)(c & ~kAdjSeen);
+        if (k > 0) s_add[i] -= fmaf(freq, (float)k, pres);
     }
     if (tid == 0) s_hit[kAdjSlice / 32] = 0u;
     __syncthreads();
-
-    const float rep = P.repetition ? P.repetition[b] : 1.f;
-    const float pres = P.presence ? P.presence[b] : 0.f;
-    const float freq = P.frequency ? P.frequency[b] : 0.f;
     const int words = (P.V + 31) / 32;
     // a touched token's logit, in the row that follows `node`
     auto adjust = [&](float z, int v, int node) {
         const uint32_t c = s_cnt[v];
-        int k = (int)(c & ~kAdjSeen);
-        if (node >= 0)
-            for (int y = s_node[v]; y >= 0; y = s_next[y]) k += (s_anc[node][y >> 5] >> (y & 31)) & 1u;
-        if (k > 0 || (c & kAdjSeen)) z = z > 0.f ? z / rep : z * rep;
-        return z - freq * (float)k - (k > 0 ? pres : 0.f) + s_bias[v];
+        float add = s_add[v];
+        bool seen = (c & kAdjSeen) != 0u;
+        int y = s_node[v];
+        if (y >= 0 && node >= 0) {
+            int k = 0;                               // occurrences on the path
+            for (; y >= 0; y = s_next[y]) k += (s_anc[node][y >> 5] >> (y & 31)) & 1u;
+            if (k > 0) {
+                seen = true;
+                add -= freq * (float)k + ((c & ~kAdjSeen) == 0u ? pres : 0.f);
+            }
+        }
+        return fmaf(z, !seen ? 1.f : z > 0.f ? inv_rep : rep, add);
     };
     const T *in = static_cast<const T *>(P.logits) + ((size_t)b * P.Rj + j0) * P.V + v0;
     T *out = static_cast<T *>(P.out) + ((size_t)b * P.Rj + j0) * P.V + v0;
@@ -244,29 +253,43 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
         for (int f = 0; f < kAdjFlight; ++f) {
             if (at[f] < 0) continue;
             constexpr uint32_t kAll = (1u << N) - 1u;
-            const uint32_t hit = bits8(s_hit, at[f]) & kAll;
+            uint32_t hit = bits8(s_hit, at[f]) & ok[f] & kAll;
             uint32_t e[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
-            if (hit | (~ok[f] & kAll)) {
-                const int node = s_follow[row[f]];
+            T *dst = out + (size_t)row[f] * P.V + at[f];
+            if (~ok[f] & kAll) {
 #pragma unroll
-                for (int q = 0; q < N; ++q) {
-                    const bool touched = (hit >> q) & 1u, masked = !((ok[f] >> q) & 1u);
-                    if (!touched && !masked) continue;
+                for (int q = 0; q < 4; ++q) {
                     if constexpr (N == 8) {
-                        const uint32_t h = (e[q >> 1] >> (16 * (q & 1))) & 0xffffu;
-                        uint32_t r = 0xff80u;            // -inf
-                        if (!masked) {
-                            const float z = adjust(__uint_as_float(h << 16), at[f] + q, node);
-                            r = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(z));
-                        }
-                        e[q >> 1] = (e[q >> 1] & (0xffffu << (16 * (1 - (q & 1))))) | (r << (16 * (q & 1)));
+                        const uint32_t keep = ((ok[f] >> (2 * q)) & 1u) * 0xffffu |
+                                              ((ok[f] >> (2 * q + 1)) & 1u) * 0xffff0000u;
+                        e[q] = (e[q] & keep) | (0xff80ff80u & ~keep);
                     } else {
-                        e[q] = masked ? 0xff800000u
-                                      : __float_as_uint(adjust(__uint_as_float(e[q]), at[f] + q, node));
+                        e[q] = (ok[f] >> q) & 1u ? e[q] : 0xff800000u;
                     }
                 }
             }
-            *reinterpret_cast<uint4 *>(out + (size_t)row[f] * P.V + at[f]) = make_uint4(e[0], e[1], e[2], e[3]);
+            // the touched tokens, one after the other
+            const int node = hit ? s_follow[row[f]] : -1;
+            while (hit) {
+                const int q = __ffs(hit) - 1;
+                hit &= hit - 1;
+                const int h = N == 8 ? q >> 1 : q;
+                const uint32_t word = h < 2 ? (h == 0 ? e[0] : e[1]) : (h == 2 ? e[2] : e[3]);
+                uint32_t r;
+                if constexpr (N == 8) {
+                    const float z =
+                        adjust(__uint_as_float(q & 1 ? word & 0xffff0000u : word << 16), at[f] + q, node);
+                    const uint32_t t = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(z));
+                    r = q & 1 ? (word & 0xffffu) | (t << 16) : (word & 0xffff0000u) | t;
+                } else {
+                    r = __float_as_uint(adjust(__uint_as_float(word), at[f] + q, node));
+                }
+                if (h == 0) e[0] = r;
+                else if (h == 1) e[1] = r;
+                else if (h == 2) e[2] = r;
+                else e[3] = r;
+            }
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(e[0], e[1], e[2], e[3]);
         }
     }
     // the rows' ends outside the vectors: fewer than N logits each
@@ -324,16 +347,12 @@ extern "C" spec_status_t spec_logits_adjust(
     P.n_masks = d->n_masks;
     P.status = status_ptr();
     if (!P.status) return SPEC_ERR_CUDA;
-    // Rows a CTA: enough for its rows' bytes to outweigh the history it reads
-    // (4 bytes a token against two times its logits' size), fewer until every
-    // SM has four CTAs
+    // Rows a CTA: as many as leave six CTAs (about what is resident) for every
+    // SM, since each counts the request's history anew
     const int slices = ceil_div(P.V, kAdjSlice);
-    const int es = d->logit_dtype == SPEC_BF16 ? 2 : 4;
-    const long long even = 4ll * P.H / (2ll * es * kAdjSlice);
-    P.rows = (int)(even < 8 ? 8 : even > kAdjRows ? kAdjRows : even);
-    if (P.rows > P.Rj) P.rows = P.Rj;
-    while (P.rows > 1 && (long long)slices * P.B * ceil_div(P.Rj, P.rows) < 4ll * num_sms())
-        P.rows = ceil_div(P.rows, 2);
+    const long long parts = 6ll * num_sms() / ((long long)slices * P.B);
+    P.rows = ceil_div(P.Rj, (int)(parts < 1 ? 1 : parts > P.Rj ? P.Rj : parts));
+    if (P.rows > kAdjRows) P.rows = kAdjRows;
     const dim3 grid(slices, P.B, ceil_div(P.Rj, P.rows));
     if (grid.z > 65535) return SPEC_ERR_UNSUPPORTED;
     cudaStream_t s = as_stream(stream);
