@@ -62,8 +62,11 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
     __shared__ int16_t s_node[kAdjSlice];            // first node with the token, -1
     __shared__ uint32_t s_hit[kAdjSlice / 32 + 1];   // touched tokens
     __shared__ uint32_t s_anc[kAdjMaxNodes][kAdjMaxNodes / 32];   // path of each node
-    __shared__ int16_t s_par[kAdjMaxNodes], s_next[kAdjMaxNodes];
-    __shared__ int s_tok[kAdjMaxNodes];
+    __shared__ int16_t s_up[kAdjMaxNodes], s_next[kAdjMaxNodes];
+    __shared__ uint8_t s_bad[kAdjMaxNodes];          // status bits of each node's path
+    __shared__ int s_draft[kAdjMaxNodes];            // the slice's nodes and biases, in order:
+    __shared__ int s_given[kAdjMaxBias];             // token within the slice << 16 | index
+    __shared__ int n_draft, n_given;
     __shared__ int s_mask[kAdjRows], s_follow[kAdjRows];          // mask and node of each row
     const int tid = threadIdx.x, lane = tid & 31;
     const int b = blockIdx.y, v0 = blockIdx.x * kAdjSlice, nv = min(kAdjSlice, P.V - v0);
@@ -75,14 +78,30 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
         s_add[i] = 0.f;
         s_node[i] = -1;
     }
-    for (int x = tid; x < P.N; x += kAdjThreads) {
-        const int p = P.tree_parent[(size_t)b * P.N + x];
-        // -2: the path ends here for a bad parent (a node past the tree's end
-        // may hold anything, so it is reported only where a row's path meets
-        // it)
-        s_par[x] = (int16_t)((p >= x || p < -1) ? -2 : p);
-        s_tok[x] = P.tokens[(size_t)b * P.N + x];
-    }
+    // the entries of `ids` within the slice, in index order (one warp)
+    auto gather = [&](const int32_t *ids, int n, int *list, int *count, bool report) {
+        int m = 0;
+        for (int i0 = 0; i0 < n; i0 += 128) {
+            int t[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u + lane;
+                t[u] = i < n ? ids[i] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (report && t[u] >= P.V) bits |= SPEC_DEV_BAD_INDEX;
+                const int v = t[u] - v0;
+                const bool mine = t[u] >= 0 && v >= 0 && v < nv;
+                const unsigned w = __ballot_sync(0xffffffffu, mine);
+                if (mine) list[m + __popc(w & ((1u << lane) - 1u))] = v << 16 | (i0 + 32 * u + lane);
+                m += __popc(w);
+            }
+        }
+        if (lane == 0) *count = m;
+    };
+    if (tid < 32) gather(P.tokens + (size_t)b * P.N, P.N, s_draft, &n_draft, false);
+    else if (tid < 64) gather(P.bias_ids + (size_t)b * P.n_bias, P.n_bias, s_given, &n_given, true);
     for (int j = tid; j < rows; j += kAdjThreads) {
         const size_t at = (size_t)b * P.Rj + j0 + j;
         int m = P.n_masks > 0 ? P.row_mask[at] : -1;
@@ -126,51 +145,71 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
         }
     }
     // the biases: the first entry of a token adds up all of them, in order
-    const int32_t *ids = P.bias_ids + (size_t)b * P.n_bias;
     const float *bias = P.bias + (size_t)b * P.n_bias;
-    for (int i = tid; i < P.n_bias; i += kAdjThreads) {
-        const int t = ids[i], v = t - v0;
-        if (t >= P.V) bits |= SPEC_DEV_BAD_INDEX;
-        if (t < 0 || v < 0 || v >= nv) continue;
+    for (int i = tid; i < n_given; i += kAdjThreads) {
+        const int v = s_given[i] >> 16;
         bool leads = true;
-        for (int k = 0; k < i && leads; ++k) leads = ids[k] != t;
+        for (int k = 0; k < i && leads; ++k) leads = (s_given[k] >> 16) != v;
         if (!leads) continue;
-        float x = bias[i];
-        for (int k = i + 1; k < P.n_bias; ++k)
-            if (ids[k] == t) x += bias[k];
+        float x = bias[s_given[i] & 0xffff];
+        for (int k = i + 1; k < n_given; ++k)
+            if ((s_given[k] >> 16) == v) x += bias[s_given[k] & 0xffff];
         s_add[v] = x;
     }
-    // the draft's paths, and its tokens of this slice
-    for (int x = tid; x < P.N; x += kAdjThreads) {
-        uint32_t w[kAdjMaxNodes / 32];
-#pragma unroll
-        for (int k = 0; k < kAdjMaxNodes / 32; ++k) w[k] = 0u;
-        for (int y = x; y >= 0; y = s_par[y])
-#pragma unroll
-            for (int k = 0; k < kAdjMaxNodes / 32; ++k)
-                if (k == (y >> 5)) w[k] |= 1u << (y & 31);
-#pragma unroll
-        for (int k = 0; k < kAdjMaxNodes / 32; ++k) s_anc[x][k] = w[k];
-        const int t = s_tok[x], v = t - v0;
-        if (t >= 0 && t < P.V && v >= 0 && v < nv) {
-            int next = -1;
-            for (int y = x + 1; y < P.N && next < 0; ++y)
-                if (s_tok[y] == t) next = y;
-            s_next[x] = (int16_t)next;
-            bool leads = true;
-            for (int y = 0; y < x && leads; ++y) leads = s_tok[y] != t;
-            if (leads) s_node[v] = (int16_t)x;
-        }
+    // the draft's tokens of this slice
+    for (int i = tid; i < n_draft; i += kAdjThreads) {
+        const int v = s_draft[i] >> 16, x = s_draft[i] & 0xffff;
+        int next = -1;
+        for (int k = i + 1; k < n_draft && next < 0; ++k)
+            if ((s_draft[k] >> 16) == v) next = s_draft[k] & 0xffff;
+        s_next[x] = (int16_t)next;
+        bool leads = true;
+        for (int k = 0; k < i && leads; ++k) leads = (s_draft[k] >> 16) != v;
+        if (leads) s_node[v] = (int16_t)x;
     }
-    if (blockIdx.x == 0)                     // the rows' paths: reported once
-        for (int j = tid; j < rows; j += kAdjThreads)
-            for (int y = s_follow[j]; y != -1; y = s_par[y]) {
-                if (y == -2) {
-                    bits |= SPEC_DEV_BAD_TREE;
-                    break;
-                }
-                if (s_tok[y] >= P.V) bits |= SPEC_DEV_BAD_INDEX;
+    // its paths, where one is looked at (and reported, by the first slice):
+    // each node takes on what its ancestor knows, 1, 2, 4, ... levels up
+    if (P.N > 0 && (n_draft > 0 || blockIdx.x == 0)) {
+        const int x = tid;
+        static_assert(kAdjMaxNodes <= kAdjThreads, "one node a thread");
+        constexpr int kWords = kAdjMaxNodes / 32;
+        uint32_t w[kWords];
+        int up = -1;
+        uint8_t bad = 0;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) w[k] = k == (x >> 5) ? 1u << (x & 31) : 0u;
+        if (x < P.N) {
+            const int p = P.tree_parent[(size_t)b * P.N + x];
+            // a node past the tree's end may hold anything, so a bad one is
+            // reported only where a row's path meets it, and ends that path
+            if (p >= x || p < -1) bad |= SPEC_DEV_BAD_TREE;
+            else up = p;
+            if (P.tokens[(size_t)b * P.N + x] >= P.V) bad |= SPEC_DEV_BAD_INDEX;
+        }
+        bool changed;
+        do {
+            changed = false;
+            if (x < P.N) {
+                s_up[x] = (int16_t)up;
+                s_bad[x] = bad;
+#pragma unroll
+                for (int k = 0; k < kWords; ++k)
+                    if (32 * k < P.N) s_anc[x][k] = w[k];
             }
+            __syncthreads();
+            if (up >= 0) {
+#pragma unroll
+                for (int k = 0; k < kWords; ++k)
+                    if (32 * k < P.N) w[k] |= s_anc[up][k];
+                bad |= s_bad[up];
+                up = s_up[up];
+                changed = true;
+            }
+        } while (__syncthreads_or(changed));
+        if (blockIdx.x == 0)
+            for (int j = tid; j < rows; j += kAdjThreads)
+                if (s_follow[j] >= 0) bits |= s_bad[s_follow[j]];
+    }
     __syncthreads();
     const float rep = P.repetition ? P.repetition[b] : 1.f, inv_rep = 1.f / rep;
     const float pres = P.presence ? P.presence[b] : 0.f;
