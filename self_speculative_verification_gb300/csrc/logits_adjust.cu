@@ -24,7 +24,8 @@ namespace {
 
 constexpr int kAdjThreads = 256;
 constexpr int kAdjSlice = 2048;              // vocabulary tokens a CTA takes
-constexpr int kAdjRows = 64;                 // most rows a CTA takes
+constexpr int kAdjRows = 16;                 // most rows a CTA takes
+constexpr int kAdjResident = 4;              // CTAs an SM holds
 constexpr int kAdjFlight = 4;                // vectors in flight a thread
 constexpr int kAdjMaxNodes = SPEC_MAX_ROWS;
 constexpr int kAdjMaxBias = 1024;
@@ -53,14 +54,16 @@ __device__ __forceinline__ uint32_t bits8(const uint32_t *w, int at) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P) {
+__global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kernel(AdjParams P) {
     pdl_wait();
     constexpr int N = 16 / (int)sizeof(T);           // logits a vector
     __shared__ uint32_t s_cnt[kAdjSlice];            // occurrences behind the prompt | kAdjSeen
-    __shared__ float s_add[kAdjSlice];               // the biases, then what a row without the
+    __shared__ __align__(16) float s_add[kAdjSlice]; // the biases, then what a row without the
                                                      // token on its path adds
     __shared__ int16_t s_node[kAdjSlice];            // first node with the token, -1
-    __shared__ uint32_t s_hit[kAdjSlice / 32 + 1];   // touched tokens
+    __shared__ uint32_t s_hit[kAdjSlice / 32 + 1];   // touched tokens,
+    __shared__ uint32_t s_old[kAdjSlice / 32 + 1];   // those in the history,
+    __shared__ uint32_t s_new[kAdjSlice / 32 + 1];   // and those of the draft
     __shared__ uint32_t s_anc[kAdjMaxNodes][kAdjMaxNodes / 32];   // path of each node
     __shared__ int16_t s_up[kAdjMaxNodes], s_next[kAdjMaxNodes];
     __shared__ uint8_t s_bad[kAdjMaxNodes];          // status bits of each node's path
@@ -69,13 +72,13 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
     __shared__ int n_draft, n_given;
     __shared__ int s_mask[kAdjRows], s_follow[kAdjRows];          // mask and node of each row
     const int tid = threadIdx.x, lane = tid & 31;
-    const int b = blockIdx.y, v0 = blockIdx.x * kAdjSlice, nv = min(kAdjSlice, P.V - v0);
-    const int j0 = blockIdx.z * P.rows, rows = min(P.Rj - j0, P.rows);
+    const int b = blockIdx.y, v0 = blockIdx.z * kAdjSlice, nv = min(kAdjSlice, P.V - v0);
+    const int j0 = blockIdx.x * P.rows, rows = min(P.Rj - j0, P.rows);
     int bits = 0;
 
     for (int i = tid; i < kAdjSlice; i += kAdjThreads) {
         s_cnt[i] = 0u;
-        s_add[i] = 0.f;
+        s_add[i] = -0.f;                             // leaves every x as it is, -0 too
         s_node[i] = -1;
     }
     // the entries of `ids` within the slice, in index order (one warp)
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
     }
     // its paths, where one is looked at (and reported, by the first slice):
     // each node takes on what its ancestor knows, 1, 2, 4, ... levels up
-    if (P.N > 0 && (n_draft > 0 || blockIdx.x == 0)) {
+    if (P.N > 0 && (n_draft > 0 || blockIdx.z == 0)) {
         const int x = tid;
         static_assert(kAdjMaxNodes <= kAdjThreads, "one node a thread");
         constexpr int kWords = kAdjMaxNodes / 32;
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
                 changed = true;
             }
         } while (__syncthreads_or(changed));
-        if (blockIdx.x == 0)
+        if (blockIdx.z == 0)
             for (int j = tid; j < rows; j += kAdjThreads)
                 if (s_follow[j] >= 0) bits |= s_bad[s_follow[j]];
     }
@@ -216,12 +219,18 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
     const float freq = P.frequency ? P.frequency[b] : 0.f;
     for (int i = tid; i < kAdjSlice; i += kAdjThreads) {
         const uint32_t c = s_cnt[i];
-        const unsigned m = __ballot_sync(0xffffffffu, c != 0u || s_node[i] >= 0 || s_add[i] != 0.f);
-        if (lane == 0) s_hit[i >> 5] = m;
+        const unsigned old = __ballot_sync(0xffffffffu, c != 0u);
+        const unsigned fresh = __ballot_sync(0xffffffffu, s_node[i] >= 0);
+        const unsigned any = __ballot_sync(0xffffffffu, s_add[i] != 0.f) | old | fresh;
+        if (lane == 0) {
+            s_old[i >> 5] = old;
+            s_new[i >> 5] = fresh;
+            s_hit[i >> 5] = any;
+        }
         const int k = (int)(c & ~kAdjSeen);
         if (k > 0) s_add[i] -= fmaf(freq, (float)k, pres);
     }
-    if (tid == 0) s_hit[kAdjSlice / 32] = 0u;
+    if (tid == 0) s_hit[kAdjSlice / 32] = s_old[kAdjSlice / 32] = s_new[kAdjSlice / 32] = 0u;
     __syncthreads();
     const int words = (P.V + 31) / 32;
     // a touched token's logit, in the row that follows `node`
@@ -292,9 +301,56 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
         for (int f = 0; f < kAdjFlight; ++f) {
             if (at[f] < 0) continue;
             constexpr uint32_t kAll = (1u << N) - 1u;
-            uint32_t hit = bits8(s_hit, at[f]) & ok[f] & kAll;
             uint32_t e[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
             T *dst = out + (size_t)row[f] * P.V + at[f];
+            if (bits8(s_hit, at[f]) & ok[f] & kAll) {
+                const uint32_t old = bits8(s_old, at[f]);
+                float add[N];
+                if ((at[f] & 3) == 0) {
+#pragma unroll
+                    for (int q = 0; q < N; q += 4) {
+                        const float4 t = *reinterpret_cast<const float4 *>(s_add + at[f] + q);
+                        add[q] = t.x; add[q + 1] = t.y; add[q + 2] = t.z; add[q + 3] = t.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < N; ++q) add[q] = s_add[at[f] + q];
+                }
+                auto known = [&](float z, int q) {
+                    return fmaf(z, !((old >> q) & 1u) ? 1.f : z > 0.f ? inv_rep : rep, add[q]);
+                };
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if constexpr (N == 8) {
+                        const __nv_bfloat162 r = __floats2bfloat162_rn(
+                            known(__uint_as_float(e[q] << 16), 2 * q),
+                            known(__uint_as_float(e[q] & 0xffff0000u), 2 * q + 1));
+                        e[q] = *reinterpret_cast<const uint32_t *>(&r);
+                    } else {
+                        e[q] = __float_as_uint(known(__uint_as_float(e[q]), q));
+                    }
+                }
+                // the draft's tokens anew, for this row's path
+                const uint32_t fresh = bits8(s_new, at[f]) & kAll;
+                if (fresh) {
+                    const int node = s_follow[row[f]];
+#pragma unroll
+                    for (int q = 0; q < N; ++q) {
+                        if (!((fresh >> q) & 1u)) continue;
+                        const uint32_t word = q * 4 / N == 0 ? x[f].x : q * 4 / N == 1 ? x[f].y
+                                            : q * 4 / N == 2 ? x[f].z : x[f].w;
+                        if constexpr (N == 8) {
+                            const float z = adjust(
+                                __uint_as_float(q & 1 ? word & 0xffff0000u : word << 16), at[f] + q, node);
+                            const uint32_t t = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(z));
+                            e[q / 2] = q & 1 ? (e[q / 2] & 0xffffu) | (t << 16)
+                                             : (e[q / 2] & 0xffff0000u) | t;
+                        } else {
+                            e[q] = __float_as_uint(adjust(__uint_as_float(word), at[f] + q, node));
+                        }
+                    }
+                }
+            }
             if (~ok[f] & kAll) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -306,27 +362,6 @@ __global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(AdjParams P)
                         e[q] = (ok[f] >> q) & 1u ? e[q] : 0xff800000u;
                     }
                 }
-            }
-            // the touched tokens, one after the other
-            const int node = hit ? s_follow[row[f]] : -1;
-            while (hit) {
-                const int q = __ffs(hit) - 1;
-                hit &= hit - 1;
-                const int h = N == 8 ? q >> 1 : q;
-                const uint32_t word = h < 2 ? (h == 0 ? e[0] : e[1]) : (h == 2 ? e[2] : e[3]);
-                uint32_t r;
-                if constexpr (N == 8) {
-                    const float z =
-                        adjust(__uint_as_float(q & 1 ? word & 0xffff0000u : word << 16), at[f] + q, node);
-                    const uint32_t t = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(z));
-                    r = q & 1 ? (word & 0xffffu) | (t << 16) : (word & 0xffff0000u) | t;
-                } else {
-                    r = __float_as_uint(adjust(__uint_as_float(word), at[f] + q, node));
-                }
-                if (h == 0) e[0] = r;
-                else if (h == 1) e[1] = r;
-                else if (h == 2) e[2] = r;
-                else e[3] = r;
             }
             *reinterpret_cast<uint4 *>(dst) = make_uint4(e[0], e[1], e[2], e[3]);
         }
@@ -386,14 +421,16 @@ extern "C" spec_status_t spec_logits_adjust(
     P.n_masks = d->n_masks;
     P.status = status_ptr();
     if (!P.status) return SPEC_ERR_CUDA;
-    // Rows a CTA: as many as leave six CTAs (about what is resident) for every
-    // SM, since each counts the request's history anew
+    // Rows a CTA: as many as leave one CTA for every place on the SMs, since
+    // each counts the request's history anew, but no more than 16: slices with
+    // many touched tokens (often the first: low ids are the common tokens) take
+    // longer, so they start first and further CTAs even them out
     const int slices = ceil_div(P.V, kAdjSlice);
-    const long long parts = 6ll * num_sms() / ((long long)slices * P.B);
+    const long long parts = (long long)kAdjResident * num_sms() / ((long long)slices * P.B);
     P.rows = ceil_div(P.Rj, (int)(parts < 1 ? 1 : parts > P.Rj ? P.Rj : parts));
     if (P.rows > kAdjRows) P.rows = kAdjRows;
-    const dim3 grid(slices, P.B, ceil_div(P.Rj, P.rows));
-    if (grid.z > 65535) return SPEC_ERR_UNSUPPORTED;
+    const dim3 grid(ceil_div(P.Rj, P.rows), P.B, slices);
+    if (slices > 65535) return SPEC_ERR_UNSUPPORTED;
     cudaStream_t s = as_stream(stream);
     const spec_status_t st =
         d->logit_dtype == SPEC_BF16
