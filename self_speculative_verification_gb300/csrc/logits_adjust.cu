@@ -29,7 +29,6 @@ constexpr int kAdjResident = 4;              // CTAs an SM holds
 constexpr int kAdjFlight = 4;                // vectors in flight a thread
 constexpr int kAdjMaxNodes = SPEC_MAX_ROWS;
 constexpr int kAdjMaxBias = 1024;
-constexpr uint32_t kAdjSeen = 0x80000000u;   // in the history (prompt or not)
 
 struct AdjParams {
     const void *logits;
@@ -45,22 +44,20 @@ struct AdjParams {
     int *status;
 };
 
-// Bits [at, at + 8) of a bit string.
+// Bits [at, at + 8) of a bit string that has a byte behind its last.
 __device__ __forceinline__ uint32_t bits8(const uint32_t *w, int at) {
-    const int s = at & 31;
-    uint64_t m = w[at >> 5];
-    if (s > 24) m |= (uint64_t)w[(at >> 5) + 1] << 32;
-    return (uint32_t)(m >> s) & 0xffu;
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(w) + (at >> 3);
+    return ((p[0] | (uint32_t)p[1] << 8) >> (at & 7)) & 0xffu;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kernel(AdjParams P) {
     pdl_wait();
     constexpr int N = 16 / (int)sizeof(T);           // logits a vector
-    __shared__ uint32_t s_cnt[kAdjSlice];            // occurrences behind the prompt | kAdjSeen
+    __shared__ __align__(16) uint32_t s_cnt[kAdjSlice];   // occurrences behind the prompt
     __shared__ __align__(16) float s_add[kAdjSlice]; // the biases, then what a row without the
                                                      // token on its path adds
-    __shared__ int16_t s_node[kAdjSlice];            // first node with the token, -1
+    __shared__ __align__(16) int16_t s_node[kAdjSlice];            // first node with the token, -1
     __shared__ uint32_t s_hit[kAdjSlice / 32 + 1];   // touched tokens,
     __shared__ uint32_t s_old[kAdjSlice / 32 + 1];   // those in the history,
     __shared__ uint32_t s_new[kAdjSlice / 32 + 1];   // and those of the draft
@@ -76,11 +73,35 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
     const int j0 = blockIdx.x * P.rows, rows = min(P.Rj - j0, P.rows);
     int bits = 0;
 
-    for (int i = tid; i < kAdjSlice; i += kAdjThreads) {
-        s_cnt[i] = 0u;
-        s_add[i] = -0.f;                             // leaves every x as it is, -0 too
-        s_node[i] = -1;
+    // what every thread reads, asked for at once: its node, the request's
+    // factors, and the first part of the history (whose entries past its
+    // length are there, but unused)
+    constexpr int kHist = 8;                         // entries in flight a thread
+    const int32_t *hist = P.history + (size_t)b * P.H;
+    int t[kHist];
+#pragma unroll
+    for (int u = 0; u < kHist; ++u) {
+        const int i = tid + u * kAdjThreads;
+        t[u] = i < P.H ? hist[i] : -1;
     }
+    int hl = P.H > 0 ? P.hist_len[b] : 0;
+    const int np = P.n_prompt ? P.n_prompt[b] : 0;
+    const float rep = P.repetition ? P.repetition[b] : 1.f, inv_rep = 1.f / rep;
+    const float pres = P.presence ? P.presence[b] : 0.f;
+    const float freq = P.frequency ? P.frequency[b] : 0.f;
+    int parent = -1, token = -1;
+    static_assert(kAdjMaxNodes <= kAdjThreads, "one node a thread");
+    if (tid < P.N) {
+        parent = P.tree_parent[(size_t)b * P.N + tid];
+        token = P.tokens[(size_t)b * P.N + tid];
+    }
+    constexpr uint32_t kNone = 0x80000000u;          // -0 leaves every x as it is, -0 too
+    for (int i = tid; i < kAdjSlice / 4; i += kAdjThreads) {
+        reinterpret_cast<uint4 *>(s_cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+        reinterpret_cast<uint4 *>(s_add)[i] = make_uint4(kNone, kNone, kNone, kNone);
+        reinterpret_cast<uint2 *>(s_node)[i] = make_uint2(~0u, ~0u);
+    }
+    if (tid <= kAdjSlice / 32) s_hit[tid] = s_old[tid] = s_new[tid] = 0u;
     // the entries of `ids` within the slice, in index order (one warp)
     auto gather = [&](const int32_t *ids, int n, int *list, int *count, bool report) {
         int m = 0;
@@ -124,27 +145,26 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
     __syncthreads();
 
     // the history's tokens of this slice
-    int hl = P.H > 0 ? P.hist_len[b] : 0;
     if (hl < 0 || hl > P.H) {
         bits |= SPEC_DEV_BAD_INDEX;
         hl = hl < 0 ? 0 : P.H;
     }
-    const int np = P.n_prompt ? P.n_prompt[b] : 0;
-    const int32_t *hist = P.history + (size_t)b * P.H;
-    for (int i0 = tid; i0 < hl; i0 += 8 * kAdjThreads) {
-        int t[8];
+    for (int i0 = tid;;) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kHist; ++u) {
+            const int i = i0 + u * kAdjThreads, v = t[u] - v0;
+            if (i >= hl) continue;
+            if (t[u] >= P.V) bits |= SPEC_DEV_BAD_INDEX;
+            if (t[u] < 0 || v < 0 || v >= nv) continue;
+            atomicOr(&s_old[v >> 5], 1u << (v & 31));
+            if (i >= np) atomicAdd(&s_cnt[v], 1u);
+        }
+        i0 += kHist * kAdjThreads;
+        if (i0 >= hl) break;
+#pragma unroll
+        for (int u = 0; u < kHist; ++u) {
             const int i = i0 + u * kAdjThreads;
             t[u] = i < hl ? hist[i] : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (t[u] >= P.V) bits |= SPEC_DEV_BAD_INDEX;
-            const int v = t[u] - v0;
-            if (t[u] < 0 || v < 0 || v >= nv) continue;
-            atomicOr(&s_cnt[v], kAdjSeen);
-            if (i0 + u * kAdjThreads >= np) atomicAdd(&s_cnt[v], 1u);
         }
     }
     // the biases: the first entry of a token adds up all of them, in order
@@ -158,6 +178,7 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
         for (int k = i + 1; k < n_given; ++k)
             if ((s_given[k] >> 16) == v) x += bias[s_given[k] & 0xffff];
         s_add[v] = x;
+        atomicOr(&s_hit[v >> 5], 1u << (v & 31));
     }
     // the draft's tokens of this slice
     for (int i = tid; i < n_draft; i += kAdjThreads) {
@@ -168,13 +189,14 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
         s_next[x] = (int16_t)next;
         bool leads = true;
         for (int k = 0; k < i && leads; ++k) leads = (s_draft[k] >> 16) != v;
-        if (leads) s_node[v] = (int16_t)x;
+        if (!leads) continue;
+        s_node[v] = (int16_t)x;
+        atomicOr(&s_new[v >> 5], 1u << (v & 31));
     }
     // its paths, where one is looked at (and reported, by the first slice):
     // each node takes on what its ancestor knows, 1, 2, 4, ... levels up
     if (P.N > 0 && (n_draft > 0 || blockIdx.z == 0)) {
         const int x = tid;
-        static_assert(kAdjMaxNodes <= kAdjThreads, "one node a thread");
         constexpr int kWords = kAdjMaxNodes / 32;
         uint32_t w[kWords];
         int up = -1;
@@ -182,12 +204,11 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
 #pragma unroll
         for (int k = 0; k < kWords; ++k) w[k] = k == (x >> 5) ? 1u << (x & 31) : 0u;
         if (x < P.N) {
-            const int p = P.tree_parent[(size_t)b * P.N + x];
             // a node past the tree's end may hold anything, so a bad one is
             // reported only where a row's path meets it, and ends that path
-            if (p >= x || p < -1) bad |= SPEC_DEV_BAD_TREE;
-            else up = p;
-            if (P.tokens[(size_t)b * P.N + x] >= P.V) bad |= SPEC_DEV_BAD_INDEX;
+            if (parent >= x || parent < -1) bad |= SPEC_DEV_BAD_TREE;
+            else up = parent;
+            if (token >= P.V) bad |= SPEC_DEV_BAD_INDEX;
         }
         bool changed;
         do {
@@ -214,37 +235,26 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
                 if (s_follow[j] >= 0) bits |= s_bad[s_follow[j]];
     }
     __syncthreads();
-    const float rep = P.repetition ? P.repetition[b] : 1.f, inv_rep = 1.f / rep;
-    const float pres = P.presence ? P.presence[b] : 0.f;
-    const float freq = P.frequency ? P.frequency[b] : 0.f;
-    for (int i = tid; i < kAdjSlice; i += kAdjThreads) {
-        const uint32_t c = s_cnt[i];
-        const unsigned old = __ballot_sync(0xffffffffu, c != 0u);
-        const unsigned fresh = __ballot_sync(0xffffffffu, s_node[i] >= 0);
-        const unsigned any = __ballot_sync(0xffffffffu, s_add[i] != 0.f) | old | fresh;
-        if (lane == 0) {
-            s_old[i >> 5] = old;
-            s_new[i >> 5] = fresh;
-            s_hit[i >> 5] = any;
-        }
-        const int k = (int)(c & ~kAdjSeen);
-        if (k > 0) s_add[i] -= fmaf(freq, (float)k, pres);
+    // what the history's tokens add, and the touched ones
+    static_assert(kAdjSlice == 8 * kAdjThreads && kAdjSlice / 32 < kAdjThreads, "eight tokens a thread");
+    for (uint32_t m = bits8(s_old, 8 * tid); m; m &= m - 1) {
+        const int v = 8 * tid + __ffs(m) - 1;
+        if (s_cnt[v]) s_add[v] -= fmaf(freq, (float)s_cnt[v], pres);
     }
-    if (tid == 0) s_hit[kAdjSlice / 32] = s_old[kAdjSlice / 32] = s_new[kAdjSlice / 32] = 0u;
+    if (tid < kAdjSlice / 32) s_hit[tid] |= s_old[tid] | s_new[tid];
     __syncthreads();
     const int words = (P.V + 31) / 32;
     // a touched token's logit, in the row that follows `node`
     auto adjust = [&](float z, int v, int node) {
-        const uint32_t c = s_cnt[v];
         float add = s_add[v];
-        bool seen = (c & kAdjSeen) != 0u;
+        bool seen = (s_old[v >> 5] >> (v & 31)) & 1u;
         int y = s_node[v];
         if (y >= 0 && node >= 0) {
             int k = 0;                               // occurrences on the path
             for (; y >= 0; y = s_next[y]) k += (s_anc[node][y >> 5] >> (y & 31)) & 1u;
             if (k > 0) {
                 seen = true;
-                add -= freq * (float)k + ((c & ~kAdjSeen) == 0u ? pres : 0.f);
+                add -= freq * (float)k + (s_cnt[v] == 0u ? pres : 0.f);
             }
         }
         return fmaf(z, !seen ? 1.f : z > 0.f ? inv_rep : rep, add);
@@ -253,6 +263,7 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
     T *out = static_cast<T *>(P.out) + ((size_t)b * P.Rj + j0) * P.V + v0;
     // one logit at a time: `n` of row j from `first`
     auto singles = [&](int j, int first, int n) {
+#pragma unroll 1
         for (int i = first; i < first + n; ++i) {
             const T *src = in + (size_t)j * P.V + i;
             T x = *src;
@@ -273,97 +284,101 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
         const int off = (int)((reinterpret_cast<uintptr_t>(in + (size_t)j * P.V) & 15) / sizeof(T));
         return min(nv, off ? N - off : 0);
     };
+    // A thread takes the same vectors in every row; where the rows begin alike
+    // (their length a multiple of 16 bytes) these are the same tokens, and what
+    // it knows of them stays in registers.
     constexpr int kVecs = kAdjSlice / N;             // at most, a row
-    for (int i0 = tid; i0 < rows * kVecs; i0 += kAdjFlight * kAdjThreads) {
-        uint4 x[kAdjFlight];
-        int row[kAdjFlight], at[kAdjFlight];         // at: within the slice, -1 none
-        uint32_t ok[kAdjFlight];
+    constexpr uint32_t kAll = (1u << N) - 1u;
+    for (int e0 = tid; e0 < kVecs; e0 += kAdjThreads) {
+        int known_at = -1;
+        uint32_t hit = 0, old = 0, fresh = 0;
+        float add[N];
+        for (int r0 = 0; r0 < rows; r0 += kAdjFlight) {
+            uint4 x[kAdjFlight];
+            int at[kAdjFlight];                      // within the slice, -1 none
+            uint32_t ok[kAdjFlight];
 #pragma unroll
-        for (int f = 0; f < kAdjFlight; ++f) {
-            const int i = i0 + f * kAdjThreads, j = i / kVecs, e = i % kVecs;
-            at[f] = -1;
-            row[f] = j;
-            ok[f] = 0xffu;
-            if (j >= rows) continue;
-            const int lead = lead_of(j);
-            if (e >= (nv - lead) / N) continue;
-            at[f] = lead + e * N;
-            x[f] = *reinterpret_cast<const uint4 *>(in + (size_t)j * P.V + at[f]);
-            if (s_mask[j] >= 0) {
-                const int v = v0 + at[f], w = v >> 5, sft = v & 31;
-                const uint32_t *mw = P.mask_bits + (size_t)s_mask[j] * words;
-                uint64_t m = mw[w];
-                if (sft + N > 32) m |= (uint64_t)mw[w + 1] << 32;
-                ok[f] = (uint32_t)(m >> sft);
+            for (int f = 0; f < kAdjFlight; ++f) {
+                const int j = r0 + f;
+                at[f] = -1;
+                ok[f] = kAll;
+                if (j >= rows) continue;
+                const int first = lead_of(j) + e0 * N;
+                if (first + N > nv) continue;
+                at[f] = first;
+                x[f] = *reinterpret_cast<const uint4 *>(in + (size_t)j * P.V + first);
+                if (s_mask[j] >= 0) {
+                    const int v = v0 + first, w = v >> 5, sft = v & 31;
+                    const uint32_t *mw = P.mask_bits + (size_t)s_mask[j] * words;
+                    uint64_t m = mw[w];
+                    if (sft + N > 32) m |= (uint64_t)mw[w + 1] << 32;
+                    ok[f] = (uint32_t)(m >> sft) & kAll;
+                }
             }
-        }
 #pragma unroll
-        for (int f = 0; f < kAdjFlight; ++f) {
-            if (at[f] < 0) continue;
-            constexpr uint32_t kAll = (1u << N) - 1u;
-            uint32_t e[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
-            T *dst = out + (size_t)row[f] * P.V + at[f];
-            if (bits8(s_hit, at[f]) & ok[f] & kAll) {
-                const uint32_t old = bits8(s_old, at[f]);
-                float add[N];
-                if ((at[f] & 3) == 0) {
+            for (int f = 0; f < kAdjFlight; ++f) {
+                if (at[f] < 0) continue;
+                if (at[f] != known_at) {
+                    known_at = at[f];
+                    hit = bits8(s_hit, known_at) & kAll;
+                    if (hit) {
+                        old = bits8(s_old, known_at);
+                        fresh = bits8(s_new, known_at) & kAll;
 #pragma unroll
-                    for (int q = 0; q < N; q += 4) {
-                        const float4 t = *reinterpret_cast<const float4 *>(s_add + at[f] + q);
-                        add[q] = t.x; add[q + 1] = t.y; add[q + 2] = t.z; add[q + 3] = t.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < N; ++q) add[q] = s_add[at[f] + q];
-                }
-                auto known = [&](float z, int q) {
-                    return fmaf(z, !((old >> q) & 1u) ? 1.f : z > 0.f ? inv_rep : rep, add[q]);
-                };
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if constexpr (N == 8) {
-                        const __nv_bfloat162 r = __floats2bfloat162_rn(
-                            known(__uint_as_float(e[q] << 16), 2 * q),
-                            known(__uint_as_float(e[q] & 0xffff0000u), 2 * q + 1));
-                        e[q] = *reinterpret_cast<const uint32_t *>(&r);
-                    } else {
-                        e[q] = __float_as_uint(known(__uint_as_float(e[q]), q));
+                        for (int q = 0; q < N; ++q) add[q] = s_add[known_at + q];
                     }
                 }
-                // the draft's tokens anew, for this row's path
-                const uint32_t fresh = bits8(s_new, at[f]) & kAll;
-                if (fresh) {
-                    const int node = s_follow[row[f]];
+                uint32_t e[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+                if (hit & ok[f]) {
+                    auto known = [&](float z, int q) {
+                        return fmaf(z, !((old >> q) & 1u) ? 1.f : z > 0.f ? inv_rep : rep, add[q]);
+                    };
 #pragma unroll
-                    for (int q = 0; q < N; ++q) {
-                        if (!((fresh >> q) & 1u)) continue;
-                        const uint32_t word = q * 4 / N == 0 ? x[f].x : q * 4 / N == 1 ? x[f].y
-                                            : q * 4 / N == 2 ? x[f].z : x[f].w;
+                    for (int q = 0; q < 4; ++q) {
                         if constexpr (N == 8) {
-                            const float z = adjust(
-                                __uint_as_float(q & 1 ? word & 0xffff0000u : word << 16), at[f] + q, node);
-                            const uint32_t t = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(z));
-                            e[q / 2] = q & 1 ? (e[q / 2] & 0xffffu) | (t << 16)
-                                             : (e[q / 2] & 0xffff0000u) | t;
+                            const __nv_bfloat162 r = __floats2bfloat162_rn(
+                                known(__uint_as_float(e[q] << 16), 2 * q),
+                                known(__uint_as_float(e[q] & 0xffff0000u), 2 * q + 1));
+                            e[q] = *reinterpret_cast<const uint32_t *>(&r);
                         } else {
-                            e[q] = __float_as_uint(adjust(__uint_as_float(word), at[f] + q, node));
+                            e[q] = __float_as_uint(known(__uint_as_float(e[q]), q));
+                        }
+                    }
+                    // the draft's tokens anew, for this row's path
+                    for (uint32_t m = fresh; m; m &= m - 1) {
+                        const int q = __ffs(m) - 1, h = q * 4 / N;
+                        const uint32_t word = h < 2 ? (h == 0 ? x[f].x : x[f].y) : (h == 2 ? x[f].z : x[f].w);
+                        uint32_t keep = 0, z = word;
+                        if constexpr (N == 8) {
+                            keep = q & 1 ? 0xffffu : 0xffff0000u;
+                            z = q & 1 ? word & 0xffff0000u : word << 16;
+                        }
+                        const float y = adjust(__uint_as_float(z), at[f] + q, s_follow[r0 + f]);
+                        z = __float_as_uint(y);
+                        if constexpr (N == 8) {
+                            z = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y));
+                            z = q & 1 ? z << 16 : z;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k == h) e[k] = (e[k] & keep) | z;
+                    }
+                }
+                if (ok[f] != kAll) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if constexpr (N == 8) {
+                            const uint32_t keep = ((ok[f] >> (2 * q)) & 1u) * 0xffffu |
+                                                  ((ok[f] >> (2 * q + 1)) & 1u) * 0xffff0000u;
+                            e[q] = (e[q] & keep) | (0xff80ff80u & ~keep);
+                        } else {
+                            e[q] = (ok[f] >> q) & 1u ? e[q] : 0xff800000u;
                         }
                     }
                 }
+                *reinterpret_cast<uint4 *>(out + (size_t)(r0 + f) * P.V + at[f]) =
+                    make_uint4(e[0], e[1], e[2], e[3]);
             }
-            if (~ok[f] & kAll) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if constexpr (N == 8) {
-                        const uint32_t keep = ((ok[f] >> (2 * q)) & 1u) * 0xffffu |
-                                              ((ok[f] >> (2 * q + 1)) & 1u) * 0xffff0000u;
-                        e[q] = (e[q] & keep) | (0xff80ff80u & ~keep);
-                    } else {
-                        e[q] = (ok[f] >> q) & 1u ? e[q] : 0xff800000u;
-                    }
-                }
-            }
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(e[0], e[1], e[2], e[3]);
         }
     }
     // the rows' ends outside the vectors: fewer than N logits each
