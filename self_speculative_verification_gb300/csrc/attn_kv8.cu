@@ -23,7 +23,7 @@ enum { kColPrefix = 0, kColSoft = 1, kColBlock = 2 };
 // CTA (split, KV head x row block, request): a running softmax over its
 // columns, 32 at a time through shared memory; lane = column for the scores
 // (four rows per warp share each key vector), lane = head dimension for O.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
     pdl_wait();
     const AttnParams &P = Q.a;
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
     const bool last = split == nsp - 1;
     const int row0 = rb * kRows;
 
-    const T *q = static_cast<const T *>(P.q);
+    const float *q = static_cast<const float *>(P.q);
     for (int i = tid; i < kRows * D; i += 128) {
         const int p = row0 + i / D;
         float x = 0.f;
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
         } else {
             const size_t first = kind == kColSoft ? (size_t)h * P.n_soft
                                                   : ((size_t)b * P.Hkv + h) * P.R;
-            const T *kp = static_cast<const T *>(kind == kColSoft ? P.soft_k : P.kb) + (first + base) * D;
-            const T *vp = static_cast<const T *>(kind == kColSoft ? P.soft_v : P.vb) + (first + base) * D;
+            const float *kp = static_cast<const float *>(kind == kColSoft ? P.soft_k : P.kb) + (first + base) * D;
+            const float *vp = static_cast<const float *>(kind == kColSoft ? P.soft_v : P.vb) + (first + base) * D;
             for (int i = tid; i < kCols * D; i += 128) {
                 const int j = i / D, k = i % D;
                 sk[j][k] = j < ncols ? load_f(kp + i) : 0.f;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
 }
 
 // Merge the splits of every packed row, one warp each.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128) attn_kv8_combine_kernel(AttnParams P) {
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(128) attn_kv8_combine_kernel(AttnParams P) {
         for (int j = 0; j < D / 32; ++j) out[j] = fmaf(w, P.part_o[idx * D + lane + 32 * j], out[j]);
     }
     const int r = p / P.G, hq = h * P.G + p % P.G;
-    T *o = static_cast<T *>(P.o) + (((size_t)b * P.R + r) * P.Hq + hq) * D;
+    float *o = static_cast<float *>(P.o) + (((size_t)b * P.R + r) * P.Hq + hq) * D;
     const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) store_f(o + lane + 32 * j, out[j] * inv);
@@ -308,8 +308,9 @@ spec_status_t make_plan8(const spec_attn_desc *a, const spec_kv8_desc *c, Plan8 
         P.chunk = (int)chunk;
     }
     P.max_splits = ceil_div(P.capacity, P.chunk);
-    plan.use_tc = kv8_tc_supported(P, a->dtype);
+    plan.use_tc = a->dtype == SPEC_BF16;
     if (plan.use_tc) {
+        if (!kv8_tc_supported(P)) return SPEC_ERR_UNSUPPORTED;
         plan.ws_bytes = kv8_tc_workspace_bytes(P);
         *out = plan;
         return SPEC_OK;
@@ -321,13 +322,13 @@ spec_status_t make_plan8(const spec_attn_desc *a, const spec_kv8_desc *c, Plan8 
     return SPEC_OK;
 }
 
-template <typename T, int D>
+template <int D>
 spec_status_t launch_simt8(const Kv8Params &Q, cudaStream_t s) {
     const AttnParams &P = Q.a;
-    spec_status_t st = launch(attn_kv8_simt_kernel<T, D>, dim3(P.max_splits, P.Hkv * P.n_rb, P.B),
+    spec_status_t st = launch(attn_kv8_simt_kernel<D>, dim3(P.max_splits, P.Hkv * P.n_rb, P.B),
                               dim3(128), 0, s, Q);
     if (st != SPEC_OK) return st;
-    st = launch(attn_kv8_combine_kernel<T, D>, dim3(ceil_div(P.M, 4), P.Hkv, P.B), dim3(128), 0, s, P);
+    st = launch(attn_kv8_combine_kernel<D>, dim3(ceil_div(P.M, 4), P.Hkv, P.B), dim3(128), 0, s, P);
     return st != SPEC_OK ? st : launch_status();
 }
 
@@ -386,8 +387,5 @@ extern "C" spec_status_t spec_verify_attn_kv8(const spec_attn_desc *attn, const 
     plan.Q.scales = cache->scales;
     cudaStream_t s = as_stream(stream);
     if (plan.use_tc) return launch_attn_kv8_tc(plan.Q, s);
-    if (attn->dtype == SPEC_BF16)
-        return P.d == 128 ? launch_simt8<__nv_bfloat16, 128>(plan.Q, s)
-                          : launch_simt8<__nv_bfloat16, 64>(plan.Q, s);
-    return P.d == 128 ? launch_simt8<float, 128>(plan.Q, s) : launch_simt8<float, 64>(plan.Q, s);
+    return P.d == 128 ? launch_simt8<128>(plan.Q, s) : launch_simt8<64>(plan.Q, s);
 }

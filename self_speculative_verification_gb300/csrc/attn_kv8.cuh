@@ -17,7 +17,7 @@ struct Kv8Params {
 // The tensor-core path (bf16 rows): rows per unit, bytes of workspace, and a
 // call, whose workspace begins at Q.a.part_o.
 int kv8_tc_rows(const AttnParams &P);
-bool kv8_tc_supported(const AttnParams &P, int dtype);
+bool kv8_tc_supported(const AttnParams &P);
 size_t kv8_tc_workspace_bytes(const AttnParams &P);
 spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s);
 

@@ -1164,8 +1164,7 @@ spec_status_t launch_rows(const Tc8Params &P, const Prep8Params &R, const CUtens
 int kv8_tc_rows(const AttnParams &P) { return P.M <= 8 ? 8 : P.M <= 16 ? 16 : P.M <= 32 ? 32 : 64; }
 
 // TMA coordinates and unit numbers are 32-bit.
-bool kv8_tc_supported(const AttnParams &P, int dtype) {
-    if (dtype != SPEC_BF16) return false;
+bool kv8_tc_supported(const AttnParams &P) {
     const Ws8 w = plan_ws(P);
     return w.units * 2 * w.rb < (1ll << 31) &&
            (long long)P.B * P.Hkv * 4 * w.tail_pad < (1ll << 31) && (long long)P.R * P.Hq < (1ll << 30);
