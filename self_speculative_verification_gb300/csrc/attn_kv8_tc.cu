@@ -49,10 +49,10 @@ namespace {
 using namespace tc5;
 
 constexpr int kStep = 128;                  // tokens a step
-constexpr int kTcThreads = 12 * 32;
-constexpr int kProducerWarp = 8, kScoreWarp = 9, kValueWarp = 10, kProducerWarp2 = 11;
 constexpr float kTop = 8.75f;               // log2 of the largest P allowed (448 = 2^8.807)
-constexpr float kAim = 7.f;                 // log2 P of a row's maximum when M is raised
+constexpr float kAim = 3.f;                 // log2 P of a row's maximum when M is raised: 2^5.75 of
+                                            // room before the next raise (a step with one takes
+                                            // twice as long), and P of 2^-17 of it is still held
 constexpr float kNoRef = -1e30f;            // M of a row that has seen nothing
 constexpr float kLoUp = 16.f;               // factor of P's second part
 
@@ -82,7 +82,11 @@ struct Tc8Params {
 template <int D, int RB>
 struct Cfg {
     static constexpr bool kAlt = RB <= 32;
-    static constexpr int RW = kAlt ? RB : RB / 2;       // rows of a warpgroup
+    static constexpr int NA = kAlt ? 2 : 1;             // steps in the softmax at a time
+    static constexpr int NR = RB <= 32 ? 1 : 2;         // warpgroups that share a step's rows
+    static constexpr int NG = NA * NR;                  // softmax warpgroups
+    static constexpr int RW = RB / NR;                  // rows of a warpgroup
+    static constexpr int kThreads = NG * 128 + 128;
     static constexpr int CH = kAlt ? RW : 16;           // rows taken from tensor memory at a time
     static constexpr int NB = kAlt ? 4 : 3;             // S buffers: S runs ahead of the softmax
     static constexpr int kSlot = 2 * kStep * D;         // K and V of a step
@@ -92,8 +96,8 @@ struct Cfg {
     static constexpr int NS = (kAlt ? 6 : 4) * (128 / D);   // ring slots
     // TMEM: O of warpgroup g at 2 RW g (first parts, then second parts), S
     // buffer b at kColS + 2 RB b
-    static constexpr uint32_t kColS = 4 * RW;
-    static constexpr int kUsed = 4 * RW + NB * 2 * RB;
+    static constexpr uint32_t kColS = 2 * NG * RW;
+    static constexpr int kUsed = (int)kColS + NB * 2 * RB;
     static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
 };
 
@@ -106,11 +110,11 @@ struct Shared8 {
     uint64_t p_full[2], o_upd[2];
     uint64_t drain[2];
     float4 scale[C::NS][8];              // token_scale of each box of a slot
-    alignas(16) float qs[2][C::RW];      // a row's q_scale
-    alignas(16) float neg_m[2][C::RW];   // and its -M
-    alignas(16) float fac[2][C::RW];     // what its O is scaled by
-    alignas(16) float red[2][4][C::RW];  // the warps' maxima, or sums; what M is raised by
-    alignas(16) int out[2][C::RW];       // RowMeta::out
+    alignas(16) float qs[C::NG][C::RW];      // a row's q_scale
+    alignas(16) float neg_m[C::NG][C::RW];   // and its -M
+    alignas(16) float fac[C::NG][C::RW];     // what its O is scaled by
+    alignas(16) float red[C::NG][4][C::RW];  // the warps' maxima, or sums; what M is raised by
+    alignas(16) int out[C::NG][C::RW];       // RowMeta::out
     uint32_t tmem_base;
 };
 
@@ -123,7 +127,9 @@ static_assert(smem8<128, 64>() <= 227 * 1024 && smem8<128, 32>() <= 227 * 1024 &
                   smem8<64, 64>() <= 227 * 1024,
               "shared memory of the 8-bit attention kernel");
 
-// OR over the N threads at named barrier `id` (1 + g: a warpgroup; 3: both).
+constexpr int kAllBar = 8;               // all softmax warpgroups
+
+// OR over the N threads at named barrier `id` (1 + g: a warpgroup).
 template <int N>
 __device__ __forceinline__ bool group_or(int id, bool x) {
     int r;
@@ -197,12 +203,15 @@ __device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32
 }
 
 template <int D, int RB>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__((Cfg<D, RB>::kThreads), 1)
 attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ CUtensorMap m_kv,
                    const __grid_constant__ CUtensorMap m_tail,
                    const __grid_constant__ CUtensorMap m_q) {
     using C = Cfg<D, RB>;
-    constexpr int RW = C::RW, NS = C::NS;
+    constexpr int RW = C::RW, NS = C::NS, NG = C::NG, NR = C::NR;
+    // warps: the softmax's, then the producers and the two that issue MMAs
+    constexpr int kProducerWarp = 4 * NG, kScoreWarp = 4 * NG + 1, kValueWarp = 4 * NG + 2,
+                  kProducerWarp2 = 4 * NG + 3;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem;
     uint8_t *qbuf = ring + NS * C::kSlot;
@@ -224,12 +233,12 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.q_full[b], 1);
             mbar_init(&sh.q_empty[b], 1);
-            mbar_init(&sh.p_full[b], C::kAlt ? 4 : 8);
+            mbar_init(&sh.p_full[b], 4 * NR);
             mbar_init(&sh.o_upd[b], 1);
         }
         for (int b = 0; b < C::NB; ++b) {
             mbar_init(&sh.s_full[b], 1);
-            mbar_init(&sh.s_free[b], C::kAlt ? 4 : 8);
+            mbar_init(&sh.s_free[b], 4 * NR);
         }
         mbar_init(&sh.drain[0], 1);
         mbar_init(&sh.drain[1], 1);
@@ -494,7 +503,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                         break;
                     }
                     const uint64_t pd = pd0 + (uint64_t)((b * C::kP) >> 4);
-                    const uint32_t to = tmem + (C::kAlt ? (uint32_t)(b * 2 * RW) : 0u);
+                    const uint32_t to = tmem + (C::kAlt ? (uint32_t)(b * 2 * RB) : 0u);
                     const bool first = k - k0 < (C::kAlt ? 2 : 1);       // into its O
                     for (int part = 0; part < parts; ++part) {
                         // (met: S(k) has read the slot)
@@ -540,7 +549,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         constexpr int CH = C::CH;
         const int g = warp >> 2, wq = warp & 3, bar = 1 + g;
         const int tok = wq * 32 + lane, gi = threadIdx.x & 127;
-        const int row0 = kAlt ? 0 : g * RW;
+        const int ga = g / NR, row0 = g % NR * RW;
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
         const uint32_t to = tmem + lane_base;          // O of both warpgroups
         Cursor c;
@@ -572,7 +581,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             for (int i = 0; i < RW; ++i) l[i] = 0.f;
             group_sync<128>(bar);
 
-            k = k0 + (kAlt ? (k0 ^ g) & 1 : 0);
+            k = k0 + (kAlt ? (k0 ^ ga) & 1 : 0);
             for (; k < k0 + n; k += kAlt ? 2 : 1) {
                 if (dead) continue;
                 const int tile = tile0 + k - k0;
@@ -780,14 +789,14 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                         w[i / 4] = h0 | (h1 << 16);
                         w[RW / 4 + i / 4] = l0 | (l1 << 16);
                     }
-                    const int q0 = kAlt ? 0 : g * (RW / 8);
+                    const int q0 = g % NR * (RW / 8);
 #pragma unroll
                     for (int q = 0; q < RW / 8; ++q)
                         *reinterpret_cast<uint4 *>(prow + (((q0 + q) ^ swz) << 4)) =
                             make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
                     // V rows past the last token hold whatever the copy left: P
                     // is 0 there, but 0 x NaN is NaN
-                    if (!here && (kAlt || g == 0)) {
+                    if (!here && row0 == 0) {
                         for (int part = 0; part < (tail ? 2 : 1); ++part) {
                             const int sl = slot0 + part >= NS ? slot0 + part - NS : slot0 + part;
                             uint4 *vr = reinterpret_cast<uint4 *>(ring + sl * C::kSlot + kv8_row(tok, 1, D));
@@ -812,18 +821,18 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             const float sum = warp_sums<RW>(l);
             // (each group waits for its own last PV, behind the last use of sh.red
             // by any of its warps)
-            const int jw = kAlt && (j & 1) != g ? j - 1 : j;
+            const int jw = kAlt && (j & 1) != ga ? j - 1 : j;
             const bool got = !dead && ok &&
                              (jw < k0 || mbar_wait_warp(&sh.o_upd[jw & 1], (uint32_t)((jw >> 1) & 1), T.wait));
             if (lane % kPer == 0) sh.red[g][wq][lane / kPer] = sum;
-            if (group_or<256>(3, !got)) {
+            if (group_or<NG * 128>(kAllBar, !got)) {
                 ok = false;
                 break;
             }
             fence_after();
             const size_t prow = slot_row(T, seg_id, cta, 0, 1, 0);
             if (threadIdx.x < RB) {
-                const int r = threadIdx.x, rg = kAlt ? 0 : r / RW, ri = kAlt ? r : r % RW;
+                const int r = threadIdx.x, rg = r / RW, ri = r % RW;
                 auto row_sum = [&](int q) {
                     return (sh.red[q][0][ri] + sh.red[q][1][ri]) + (sh.red[q][2][ri] + sh.red[q][3][ri]);
                 };
@@ -831,17 +840,17 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 auto ref = [&](int q) { return sh.neg_m[q][ri] == 0.f ? kNoRef : -sh.neg_m[q][ri]; };
                 float M = ref(rg), L = row_sum(rg), f0 = 1.f, f1 = 0.f;
                 if (kAlt) {
-                    const float m0 = M, m1 = ref(1);
+                    const float m0 = M, m1 = ref(NR + rg);
                     M = fmaxf(m0, m1);
                     f0 = exp2f(m0 - M);
                     f1 = exp2f(m1 - M);
-                    L = f0 * L + f1 * row_sum(1);
+                    L = f0 * L + f1 * row_sum(NR + rg);
                 }
                 const int out = sh.out[rg][ri];
                 const bool none = !(out & 1) || L == 0.f;
                 const float inv = !seg_whole ? 1.f : none ? 0.f : 1.f / L;
                 sh.fac[rg][ri] = f0 * inv;
-                if (kAlt) sh.fac[1][ri] = f1 * inv;
+                if (kAlt) sh.fac[(NG - 1) / NR * NR + rg][ri] = f1 * inv;
                 if (seg_whole && out >= 0) {
                     const int rr = (out >> 1) / A.Hq, hq = (out >> 1) - rr * A.Hq;
                     A.lse[((size_t)seg_b * A.Hq + hq) * A.R + rr] =
@@ -850,19 +859,19 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     *reinterpret_cast<float2 *>(A.part_ml + (prow + r) * 2) = make_float2(M, L);
                 }
             }
-            group_sync<256>(3);
-            // warpgroup g writes rows (RB / 2) g ..
-            constexpr int HB = RB / 2, CE = HB < 16 ? HB : 16;
+            group_sync<NG * 128>(kAllBar);
+            // warpgroup g writes rows (RB / NG) g ..
+            constexpr int HB = RB / NG, CE = HB < 16 ? HB : 16;
 #pragma unroll 1
             for (int i0 = g * HB; i0 < (g + 1) * HB; i0 += CE) {
                 uint32_t a0[CE], b0[CE], a1[CE], b1[CE];
-                const int og = kAlt ? 0 : g, oi = kAlt ? i0 : i0 - g * RW;
+                const int og = i0 / RW, oi = i0 % RW;
                 ldn<CE>(to + (uint32_t)(og * 2 * RW + oi), a0);
                 ldn<CE>(to + (uint32_t)(og * 2 * RW + RW + oi), b0);
                 wait_ldn<CE>(a0, b0);
                 if constexpr (kAlt) {
-                    ldn<CE>(to + (uint32_t)(2 * RW + oi), a1);
-                    ldn<CE>(to + (uint32_t)(3 * RW + oi), b1);
+                    ldn<CE>(to + (uint32_t)(2 * RB + og * 2 * RW + oi), a1);
+                    ldn<CE>(to + (uint32_t)(2 * RB + og * 2 * RW + RW + oi), b1);
                     wait_ldn<CE>(a1, b1);
                 }
                 if (tok < D) {
@@ -875,7 +884,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     for (int i = 0; i < CE; i += 4) {
                         *reinterpret_cast<float4 *>(&f0[i]) = *reinterpret_cast<const float4 *>(&sh.fac[og][oi + i]);
                         if constexpr (kAlt)
-                            *reinterpret_cast<float4 *>(&f1[i]) = *reinterpret_cast<const float4 *>(&sh.fac[1][oi + i]);
+                            *reinterpret_cast<float4 *>(&f1[i]) = *reinterpret_cast<const float4 *>(&sh.fac[(NG - 1) / NR * NR + og][oi + i]);
                         *reinterpret_cast<int4 *>(&out[i]) = *reinterpret_cast<const int4 *>(&sh.out[og][oi + i]);
                     }
 #pragma unroll
@@ -900,7 +909,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 }
             }
             fence_before();
-            group_sync<256>(3);              // O, M and l may be written again
+            group_sync<NG * 128>(kAllBar);              // O, M and l may be written again
         }
         if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
     }
@@ -1135,7 +1144,7 @@ spec_status_t launch_units(const Tc8Params &P, const CUtensorMap *m, cudaStream_
     const spec_status_t st =
         set_smem_limit(reinterpret_cast<const void *>(attn_kv8_tc_kernel<D, RB>), smem8<D, RB>());
     if (st != SPEC_OK) return st;
-    return launch(attn_kv8_tc_kernel<D, RB>, dim3(P.t.n_ctas), dim3(kTcThreads), smem8<D, RB>(), s, P,
+    return launch(attn_kv8_tc_kernel<D, RB>, dim3(P.t.n_ctas), dim3(Cfg<D, RB>::kThreads), smem8<D, RB>(), s, P,
                   m[0], m[1], m[2]);
 }
 
