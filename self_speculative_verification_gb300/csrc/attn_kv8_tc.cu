@@ -372,6 +372,14 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             const int slots = __shfl_sync(0xffffffffu, cur.tail ? 2 : cur.n, 0);
             const int tile_of = cur.pg * A.Hkv + cur.c.h;
             for (int i = first, v = 0; i < slots; i += 2, ++v) {
+                // (everything a copy needs, before its slot is waited for)
+                int z[8], row[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    z[x] = __shfl_sync(0xffffffffu, tile_of, (8 * v + x) & 31);
+                    row[x] = __shfl_sync(0xffffffffu, cur.row, (8 * v + x) & 31);
+                }
+                const unsigned mine = (boxed >> (8 * v)) & 0xffu;
                 if (!__all_sync(0xffffffffu, mbar_wait(&sh.empty[slot], (uint32_t)(phase ^ 1), T.wait))) {
                     ok = false;
                     break;
@@ -379,24 +387,26 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 uint8_t *dst = ring + slot * C::kSlot;
                 if (u == v && box < boxes && !tail) sh.scale[slot][box] = ts;
                 __syncwarp();
-                const unsigned mine = (boxed >> (8 * v)) & 0xffu;
                 if (lane == 0)
                     mbar_arrive_expect_tx(&sh.full[slot], tail ? (uint32_t)(nb * 32 * D)
                                                                : (uint32_t)__popc(mine) * (uint32_t)(2 * bt * D));
                 __syncwarp();
                 if (tail) {
-                    const int row = (bh * 2 + i) * (2 * P.tail_pad) + tile0 * (2 * kStep);
+                    const int r0 = (bh * 2 + i) * (2 * P.tail_pad) + tile0 * (2 * kStep);
                     for (int x = 0; x < nb; ++x)
                         if (lane == 0)
-                            tma_load_2d(dst + x * 32 * D, &m_tail, 0, row + x * 32, &sh.full[slot], keep);
+                            tma_load_2d(dst + x * 32 * D, &m_tail, 0, r0 + x * 32, &sh.full[slot], keep);
+                } else if (mine == 0xffu) {
+                    if (lane == 0) {
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            tma_load_3d(dst + x * (32 * D), &m_kv, 0, row[x], z[x], &sh.full[slot], stream);
+                    }
                 } else {
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        if (x >= boxes) break;
-                        const int z = __shfl_sync(0xffffffffu, tile_of, (8 * v + x) & 31);
-                        const int row = __shfl_sync(0xffffffffu, cur.row, (8 * v + x) & 31);
                         if (((mine >> x) & 1u) && lane == 0)
-                            tma_load_3d(dst + x * (2 * bt * D), &m_kv, 0, row, z, &sh.full[slot], stream);
+                            tma_load_3d(dst + x * (2 * bt * D), &m_kv, 0, row[x], z[x], &sh.full[slot], stream);
                     }
                 }
                 ++used;
