@@ -62,8 +62,16 @@ struct alignas(8) RowMeta {
     int out;                 // (row * Hq + head) * 2 + valid, within the request; -1 past the last
 };
 
+// A CTA's range of the schedule, as the preparing kernel leaves it: its steps,
+// and where the first one is.
+struct alignas(16) CtaPlan {
+    int n_steps, b, h, rb;
+    int S, n_tiles, tile, unused;
+};
+
 struct Tc8Params {
     TcParams t;              // schedule, split, partials (t.a: the call)
+    const CtaPlan *plan;     // [n_ctas]
     const float *scales;     // the cache's
     const RowMeta *q_meta;   // [units][RB]
     const float2 *tail_scale;    // [B][Hkv][tail_pad]: scales of the tail's tokens
@@ -255,28 +263,26 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
     __syncthreads();
     fence_after();
     const uint32_t tmem = sh.tmem_base;
-
-    const WarpSched ws = warp_sched(T);
-    const int cta = blockIdx.x;
-    const long long t_begin = sched_range_lo(T, ws, cta);
-    const long long t_end = sched_range_lo(T, ws, cta + 1);
-    // (the preparing kernel has begun, so every kernel before it has ended and
-    // the schedule's inputs are there; its own rows and the workspace's parts
-    // that a kernel before it may still be reading are waited for here)
+    // (the preparing kernel's range, queries and tail; it began after every
+    // kernel before it had ended)
     pdl_wait();
-    if (threadIdx.x == 0) {
-        T.bounds[cta] = t_begin;
-        if (cta == T.n_ctas - 1) T.bounds[T.n_ctas] = ws.T;
-    }
+    const int cta = blockIdx.x;
+    const int4 r0 = __ldcg(reinterpret_cast<const int4 *>(P.plan + cta));
+    const int4 r1 = __ldcg(reinterpret_cast<const int4 *>(P.plan + cta) + 1);
     auto unit_of = [&](const Cursor &c) { return (c.b * T.seg_h + c.h) * T.seg_rb + c.rb; };
 
-    const int n_steps = __shfl_sync(0xffffffffu, (int)(t_end - t_begin), 0);
-
-    // (by the warp whose first work comes last)
-    if (warp == kValueWarp) {
-        const BoundaryRec rec = warp_boundary_record(T, ws, cta, t_begin, t_end);
-        if (lane == 0) T.recs[cta] = rec;
-    }
+    const int n_steps = __shfl_sync(0xffffffffu, r0.x, 0);
+    auto range_begin = [&] {
+        Cursor c;
+        c.b = r0.y;
+        c.h = r0.z;
+        c.rb = r0.w;
+        c.S = r1.x;
+        c.n_prefix = ceil_div(c.S, kTile);
+        c.n_tiles = r1.y;
+        c.tile = r1.z;
+        return c;
+    };
 
     if (n_steps > 0 && (warp == kProducerWarp || warp == kProducerWarp2)) {
         // ------------------------------------------------------ producers
@@ -335,9 +341,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             if (g.pg < 0) return make_float2(1.f, 1.f);
             return *reinterpret_cast<const float2 *>(P.scales + ((size_t)g.pg * A.Hkv + g.c.h) * 2);
         };
-        Cursor c0;
-        cursor_init(T, ws, t_begin, c0);
-        Group cur = group_at(c0, 0, 0), next = after(cur);
+        Group cur = group_at(range_begin(), 0, 0), next = after(cur);
         float2 sc = scale_of(cur);
         int slot = w, phase = 0, nq = 0, used = 0;   // used: slots filled by this warp
         static_assert(NS % 2 == 0, "a warp's slots have one parity");
@@ -347,20 +351,22 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             const float2 sc1 = scale_of(next);
             const float4 ts = token_scale(kv8_read_scale(sc.x), kv8_read_scale(sc.y));
             if (cur.pg == -2) raise_status(A.status, SPEC_DEV_BAD_PAGE);
-            if (w == 0 && (cur.c.tile == 0 || cur.k == 0)) {
-                // the unit's queries, once the unit two back is done with the
-                // buffer
+            // the unit's queries, once the unit two back is done with the buffer
+            auto queries = [&] {
                 const int qb = nq & 1;
                 if (nq >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sh.q_empty[qb],
-                                                                  (uint32_t)(((nq >> 1) - 1) & 1), T.wait))) {
-                    ok = false;
-                    break;
-                }
+                                                                  (uint32_t)(((nq >> 1) - 1) & 1), T.wait)))
+                    return false;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&sh.q_full[qb], C::kQ);
                     tma_load_2d(qbuf + qb * C::kQ, &m_q, 0, unit_of(cur.c) * (2 * RB), &sh.q_full[qb], keep);
                 }
                 ++nq;
+                return true;
+            };
+            if (w == 0 && (cur.c.tile == 0 || cur.k == 0) && !queries()) {
+                ok = false;
+                break;
             }
             const unsigned boxed = __ballot_sync(0xffffffffu, cur.pg >= 0);
             const bool tail = __shfl_sync(0xffffffffu, (int)cur.tail, 0) != 0;
@@ -445,8 +451,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         // D = 64 the 128 rows of M are the 64 dimensions twice (leading
         // offset 0).
         const bool scores = warp == kScoreWarp;
-        Cursor c;
-        cursor_init(T, ws, t_begin, c);       // warp-collective
+        Cursor c = range_begin();
         constexpr uint32_t id_s = idesc_e4m3(kStep, 2 * RB, false, false);
         constexpr uint32_t id_pv = idesc_e4m3(kStep, 2 * RB, true, true);
         const uint64_t kd0 = smem_desc_sw<D>(smem_u32(ring), 16, 16 * D);
@@ -562,8 +567,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         const int ga = g / NR, row0 = g % NR * RW;
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
         const uint32_t to = tmem + lane_base;          // O of both warpgroups
-        Cursor c;
-        cursor_init(T, ws, t_begin, c);
+        Cursor c = range_begin();
         float l[RW];
         // ok: this warp's waits were met; dead: the warpgroup has stopped (it
         // still meets the others at the units' barriers)
@@ -1000,13 +1004,15 @@ __global__ void __launch_bounds__(128) attn_kv8_tc_combine_kernel(const __grid_c
 // ------------------------------------------------------------ preparation
 
 struct Prep8Params {
-    AttnParams a;
+    TcParams t;              // (t.a: the call)
+    CtaPlan *plan;
+    int plan_ctas;           // blocks that lay out the schedule
     uint8_t *q8;             // [units][2][RB][D]
     RowMeta *q_meta;         // [units][RB]
     uint8_t *tail8;          // [B][Hkv][2][tail_pad / 8][2][8][D]
     float2 *tail_scale;      // [B][Hkv][tail_pad]
     int rb, seg_rb, tail_pad;
-    long long q_rows, t_rows;
+    int q_rows, t_rows;
 };
 
 // A row of D bf16 values (src NULL: zeros) as two e4m3 rows under one
@@ -1065,19 +1071,54 @@ template <int D>
 __global__ void __launch_bounds__(256) attn_kv8_prep_kernel(const __grid_constant__ Prep8Params P) {
     pdl_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const AttnParams &A = P.a;
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < A.B; b += 256) check_seq_len(A, b);
-    const long long w = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);
+    const AttnParams &A = P.t.a;
+    if ((int)blockIdx.x < P.plan_ctas) {
+        // a warp each: a CTA's range, and its record for the merge
+        const TcParams &T = P.t;
+        const int cta = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+        if (cta < T.n_ctas) {
+            const WarpSched ws = warp_sched(T);
+            // its last position first, then its first (as sched_range_lo, which
+            // does not say in which unit that is)
+            int b = 0, S = 0, nt = 0, seg = 0, tile = 0;
+            long long lo = ws.T, hi = ws.T, t0, c0 = 0;
+#pragma unroll 1
+            for (int i = cta + 1 == T.n_ctas ? cta : cta + 1; i >= cta; --i) {
+                hi = lo;
+                const long long x = div_nn(ws.C * i, T.n_ctas);
+                sched_locate(T, ws, x, true, b, t0, c0, S);
+                nt = seg_tiles(T, S);
+                seg = (int)div_nn(x - c0, nt + T.seg_cost);
+                const long long off = x - c0 - (long long)seg * (nt + T.seg_cost);
+                tile = off > T.seg_cost ? (int)off - T.seg_cost : 0;
+                lo = t0 + (long long)seg * nt + tile;
+            }
+            const int h = seg / T.seg_rb, rb = seg - h * T.seg_rb;
+            if (lane < 2)
+                reinterpret_cast<int4 *>(P.plan + cta)[lane] =
+                    lane == 0 ? make_int4((int)(hi - lo), b, h, rb) : make_int4(S, nt, tile, 0);
+            if (lane == 0) {
+                T.bounds[cta] = lo;
+                if (cta == T.n_ctas - 1) T.bounds[cta + 1] = ws.T;
+            }
+            const BoundaryRec rec =
+                boundary_record(T, ws, cta, lo, hi, (b * T.seg_h + h) * T.seg_rb + rb, tile, nt,
+                                c0 + (long long)seg * (nt + T.seg_cost));
+            if (lane == 0) T.recs[cta] = rec;
+        }
+        if (blockIdx.x == 0)
+            for (int b = threadIdx.x; b < A.B; b += 256) check_seq_len(A, b);
+        return;
+    }
+    const int w = ((int)blockIdx.x - P.plan_ctas) * 32 + (threadIdx.x >> 3);
     const int sub = threadIdx.x & 7;
-    const long long q_pad = (P.q_rows + 3) & ~3ll;        // (a warp's four rows are of one kind)
+    const int q_pad = (P.q_rows + 3) & ~3;                // (a warp's four rows are of one kind)
     if (w < q_pad) {
         const bool real = w < P.q_rows;
-        const long long at = real ? w : P.q_rows - 1;
-        const int r = (int)(at % P.rb);
-        const long long u = at / P.rb;
-        const int rb = (int)(u % P.seg_rb), h = (int)((u / P.seg_rb) % A.Hkv);
-        const int b = (int)(u / ((long long)P.seg_rb * A.Hkv)), p = rb * P.rb + r;
+        const unsigned at = real ? w : P.q_rows - 1, u = at / P.rb, r = at % P.rb;
+        const unsigned bh = u / P.seg_rb;
+        const int rb = (int)(u % P.seg_rb), h = (int)(bh % A.Hkv), b = (int)(bh / A.Hkv);
+        const int p = rb * P.rb + (int)r;
         const __nv_bfloat16 *src = nullptr;
         RowMeta m{0.f, -1};
         if (p < A.M) {
@@ -1090,10 +1131,8 @@ __global__ void __launch_bounds__(256) attn_kv8_prep_kernel(const __grid_constan
         if (sub == 0 && real) P.q_meta[at] = m;
         return;
     }
-    const long long t0 = w - q_pad, t = t0 < P.t_rows ? t0 : P.t_rows - 1;
-    const int tt = (int)(t % P.tail_pad);
-    const long long bh = t / P.tail_pad;
-    const int h = (int)(bh % A.Hkv);
+    const unsigned t = min(w - q_pad, P.t_rows - 1), bh = t / P.tail_pad;
+    const int tt = (int)(t % P.tail_pad), h = (int)(bh % A.Hkv);
     const __nv_bfloat16 *k = nullptr, *v = nullptr;
     if (tt < A.n_soft) {
         const size_t at = ((size_t)h * A.n_soft + tt) * D;
@@ -1118,7 +1157,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Offsets of the workspace's parts.
 struct Ws8 {
-    size_t o, ml, bounds, recs, q8, q_meta, tail8, tail_scale, bytes;
+    size_t o, ml, bounds, recs, plan, q8, q_meta, tail8, tail_scale, bytes;
     int n_ctas, rb, seg_rb, tail_pad;
     long long units;
 };
@@ -1141,6 +1180,7 @@ Ws8 plan_ws(const AttnParams &A) {
     w.ml = take(rows * 2 * sizeof(float));
     w.bounds = take(((size_t)w.n_ctas + 1) * sizeof(long long));
     w.recs = take((size_t)w.n_ctas * sizeof(BoundaryRec));
+    w.plan = take((size_t)w.n_ctas * sizeof(CtaPlan));
     w.q8 = take((size_t)w.units * 2 * w.rb * A.d);
     w.q_meta = take((size_t)w.units * w.rb * sizeof(RowMeta));
     w.tail8 = take((size_t)A.B * A.Hkv * 4 * w.tail_pad * A.d);
@@ -1161,9 +1201,9 @@ spec_status_t launch_units(const Tc8Params &P, const CUtensorMap *m, cudaStream_
 template <int D>
 spec_status_t launch_rows(const Tc8Params &P, const Prep8Params &R, const CUtensorMap *m, int rb,
                           cudaStream_t s) {
-    const long long prep = ((R.q_rows + 3) & ~3ll) + R.t_rows;
-    spec_status_t st = launch(attn_kv8_prep_kernel<D>, dim3((unsigned)ceil_div_ll(prep, 32)), dim3(256),
-                              0, s, R);
+    const long long prep = ((R.q_rows + 3ll) & ~3ll) + R.t_rows;
+    spec_status_t st = launch(attn_kv8_prep_kernel<D>, dim3((unsigned)(R.plan_ctas + ceil_div_ll(prep, 32))),
+                              dim3(256), 0, s, R);
     if (st != SPEC_OK) return st;
     st = rb == 8    ? launch_units<D, 8>(P, m, s)
          : rb == 16 ? launch_units<D, 16>(P, m, s)
@@ -1206,7 +1246,7 @@ spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s) {
     T.wait = wait_limit();
     T.seg_h = Q.a.Hkv;
     T.seg_rb = w.seg_rb;
-    T.seg_cost = 2;
+    T.seg_cost = 5;
     T.pair_steps = 1;                       // a step: two of the schedule's 64-token tiles
     P.scales = Q.scales;
     P.q_meta = reinterpret_cast<const RowMeta *>(base + w.q_meta);
@@ -1220,7 +1260,10 @@ spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s) {
     P.ps16 = Q.a.page_size / 16;
     P.ps16_inv = ((1ull << 32) + P.ps16 - 1) / P.ps16;
     Prep8Params R{};
-    R.a = Q.a;
+    R.plan = reinterpret_cast<CtaPlan *>(base + w.plan);
+    R.plan_ctas = ceil_div(w.n_ctas, 8);
+    P.plan = R.plan;
+    R.t = T;
     R.q8 = reinterpret_cast<uint8_t *>(base + w.q8);
     R.q_meta = reinterpret_cast<RowMeta *>(base + w.q_meta);
     R.tail8 = reinterpret_cast<uint8_t *>(base + w.tail8);
@@ -1228,8 +1271,8 @@ spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s) {
     R.rb = w.rb;
     R.seg_rb = w.seg_rb;
     R.tail_pad = w.tail_pad;
-    R.q_rows = w.units * w.rb;
-    R.t_rows = (long long)Q.a.B * Q.a.Hkv * w.tail_pad;
+    R.q_rows = (int)(w.units * w.rb);
+    R.t_rows = Q.a.B * Q.a.Hkv * w.tail_pad;
 
     const int D = Q.a.d, ps = Q.a.page_size;
     CUtensorMap m[3];

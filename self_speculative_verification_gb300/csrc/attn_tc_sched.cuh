@@ -169,18 +169,26 @@ __device__ void sched_request(const TcParams &P, const WarpSched &w, int b, int 
     }
 }
 
+// a / b and a % b of values >= 0, b > 0: in 32 bits where both fit (a 64-bit
+// division takes several times as long, and the ones below wait for each
+// other at a kernel's start).
+__device__ __forceinline__ long long div_nn(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 // First tile of CTA i's range (warp-collective).
 __device__ long long sched_range_lo(const TcParams &P, const WarpSched &w, int i) {
     if (i <= 0) return 0;
     if (i >= P.n_ctas) return w.T;
-    if (P.seg_cost == 0) return w.T * i / P.n_ctas;    // plain tile split
-    const long long c = w.C * i / P.n_ctas;
+    if (P.seg_cost == 0) return div_nn(w.T * i, P.n_ctas);    // plain tile split
+    const long long c = div_nn(w.C * i, P.n_ctas);
     int b, S;
     long long t0, c0;
     sched_locate(P, w, c, true, b, t0, c0, S);
     const int nt = seg_tiles(P, S);
     const long long u = nt + P.seg_cost;
-    const long long seg = (c - c0) / u, off = (c - c0) % u;
+    const long long seg = div_nn(c - c0, u), off = c - c0 - seg * u;
     return t0 + seg * nt + (off > P.seg_cost ? off - P.seg_cost : 0);
 }
 
@@ -189,7 +197,7 @@ __device__ long long sched_range_lo(const TcParams &P, const WarpSched &w, int i
 // C i / n maps to, so it is the last i with C i / n <= x.  For tile j of a
 // segment whose costs start at cs, x = cs + seg_cost + j.
 __device__ __forceinline__ int cost_split_cta(long long C, int n, long long x) {
-    const long long i = ((long long)n * (x + 1) + C - 1) / C - 1;
+    const long long i = div_nn((long long)n * (x + 1) + C - 1, C) - 1;
     return (int)(i < 0 ? 0 : (i >= n ? n - 1 : i));
 }
 
@@ -219,8 +227,8 @@ __device__ void cursor_init(const TcParams &P, const WarpSched &w, long long t, 
     c.n_prefix = ceil_div(c.S, kTile);
     c.n_tiles = seg_tiles(P, c.S);
     const long long local = t - start;
-    const int seg = (int)(local / c.n_tiles);
-    c.tile = (int)(local % c.n_tiles);
+    const int seg = (int)div_nn(local, c.n_tiles);
+    c.tile = (int)(local - (long long)seg * c.n_tiles);
     c.h = seg / P.seg_rb;
     c.rb = seg % P.seg_rb;
 }
@@ -282,40 +290,49 @@ __device__ __forceinline__ void check_seq_len(const AttnParams &A, int b) {
     if (S_raw < 0 || S_raw > A.capacity) raise_status(A.status, SPEC_DEV_SEQ_OVERFLOW);
 }
 
-// The record this CTA writes for the combine (warp-collective): when its
-// range starts inside a unit and the ranges between the unit's first CTA
-// and this one are empty (this is the unit's first boundary), the unit and
-// the CTAs sharing it; otherwise seg = -1.
-__device__ BoundaryRec warp_boundary_record(const TcParams &P, const WarpSched &w, int cta,
-                                            long long t_begin, long long t_end) {
+// The record a CTA writes for the combine (warp-collective): when its range
+// [t_begin, t_end) starts inside a unit and the ranges between the unit's
+// first CTA and this one are empty (this is the unit's first boundary), the
+// unit and the CTAs sharing it; otherwise seg = -1.  The range starts at step
+// `tile` of unit `seg`, which has nt steps and starts at the cost position cs.
+__device__ BoundaryRec boundary_record(const TcParams &P, const WarpSched &w, int cta, long long t_begin,
+                                       long long t_end, int seg, int tile, int nt, long long cs) {
     BoundaryRec rec{0, 0, -1, 0, 0, 0};
-    if (t_begin >= t_end) return rec;
-    Cursor c;
-    cursor_init(P, w, t_begin, c);
-    if (c.tile == 0) return rec;
-    rec.s0 = t_begin - c.tile;
-    rec.s1 = rec.s0 + c.n_tiles;
-    bool first_boundary = true;
-    int f = cta - 1, l = cta;
-    for (;; --f) {
-        const long long lo = sched_range_lo(P, w, f);
-        if (lo <= rec.s0 || f == 0) break;
-        if (lo < t_begin) first_boundary = false;   // a part starts in between
-    }
-    while (l + 1 < P.n_ctas && sched_range_lo(P, w, l + 1) < rec.s1) ++l;
-    if (!first_boundary) return rec;
-    rec.seg = (c.b * P.seg_h + c.h) * P.seg_rb + c.rb;
+    if (t_begin >= t_end || tile == 0) return rec;
+    rec.s0 = t_begin - tile;
+    rec.s1 = rec.s0 + nt;
+    // CTA i's range starts at the cost position C i / n; a unit's first
+    // seg_cost + 1 positions map to its first tile
+    const int f = cost_split_cta(w.C, P.n_ctas, cs + P.seg_cost);
+    const int l = cost_split_cta(w.C, P.n_ctas, cs + P.seg_cost + nt - 1);
+    if (f + 1 < cta && sched_range_lo(P, w, f + 1) < t_begin) return rec;   // a part starts in between
+    rec.seg = seg;
     rec.first = f;
     rec.last = l;
     if (l - f < 32) {
-        long long lo = sched_range_lo(P, w, f);
-        for (int j = f; j <= l; ++j) {
-            const long long hi = sched_range_lo(P, w, j + 1);
-            if (max(lo, rec.s0) < min(hi, rec.s1)) rec.parts |= 1u << (j - f);
-            lo = hi;
-        }
+        auto lo = [&](int i) {           // of CTA i's range, within the unit
+            if (i <= f) return rec.s0;
+            if (i > l) return rec.s1;
+            const long long at = div_nn(w.C * i, P.n_ctas) - cs - P.seg_cost;
+            return rec.s0 + (at > 0 ? at : 0);
+        };
+        const int i = f + (threadIdx.x & 31);
+        rec.parts = __ballot_sync(0xffffffffu, i <= l && lo(i) < lo(i + 1));
     }
     return rec;
+}
+
+__device__ BoundaryRec warp_boundary_record(const TcParams &P, const WarpSched &w, int cta,
+                                            long long t_begin, long long t_end) {
+    if (t_begin >= t_end) return BoundaryRec{0, 0, -1, 0, 0, 0};
+    Cursor c;
+    cursor_init(P, w, t_begin, c);
+    int S;
+    long long t0, c0;
+    sched_request(P, w, c.b, S, t0, c0);
+    const long long cs = c0 + div_nn(t_begin - c.tile - t0, c.n_tiles) * (c.n_tiles + P.seg_cost);
+    return boundary_record(P, w, cta, t_begin, t_end, (c.b * P.seg_h + c.h) * P.seg_rb + c.rb, c.tile,
+                           c.n_tiles, cs);
 }
 
 // ------------------------------------------------ tcgen05 kernels' steps
