@@ -227,7 +227,8 @@ constexpr int kAppendTokens = 64;
 // run: consecutive tokens in consecutive slots of one page, tokens that are
 // not written in between), one warp per (run, head, K / V).
 template <typename T, int D>
-__global__ void __launch_bounds__(kWriteWarps * 32, 4) kv8_append_kernel(Append8Params P) {
+__global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 2 ? 4 : 2)
+kv8_append_kernel(Append8Params P) {
     pdl_wait();
     __shared__ int s_start[kAppendTokens], s_len[kAppendTokens];    // len < 0: with gaps
     __shared__ int s_page[kAppendTokens], s_first[kAppendTokens];
@@ -289,11 +290,14 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 4) kv8_append_kernel(Append8
         const T *src = x ? static_cast<const T *>(P.v) + (size_t)i * P.stride_v + (size_t)h * D
                          : static_cast<const T *>(P.k) + (size_t)i * P.stride_k + (size_t)h * D;
         const long long stride = x ? P.stride_v : P.stride_k;
-        auto row = [&](int t) -> const T * {
-            return len < 0 && P.slots[i + t] < 0 ? nullptr : src + (size_t)t * stride;
-        };
-        write_block<T, D>(P.kv + kv8_block(page, h, P.Hkv, P.ps, D),
-                          P.scales + ((size_t)page * P.Hkv + h) * 2 + x, x, first, abs(len), row);
+        uint8_t *tile = P.kv + kv8_block(page, h, P.Hkv, P.ps, D);
+        float *scale = P.scales + ((size_t)page * P.Hkv + h) * 2 + x;
+        if (len > 0)
+            write_block<T, D>(tile, scale, x, first, len, [&](int t) { return src + (size_t)t * stride; });
+        else
+            write_block<T, D>(tile, scale, x, first, -len, [&](int t) -> const T * {
+                return P.slots[i + t] < 0 ? nullptr : src + (size_t)t * stride;
+            });
     }
 }
 
@@ -402,10 +406,11 @@ extern "C" spec_status_t kv8_append(const spec_kv8_desc *cache, int dtype, int n
     P.n_pages = cache->n_pages;
     P.status = status_ptr();
     if (!P.status) return SPEC_ERR_CUDA;
-    // heads split over CTAs until every SM has sixteen
+    // heads split over CTAs until every SM has eight: each finds the runs anew
+    // (sixteen: 54 us instead of 48 on 36 K tokens of 8 heads)
     const int gx = (int)ceil_div_ll(n_tokens, kAppendTokens);
     int split = 1;
-    while (split < P.Hkv && split < 32768 && (long long)gx * split < 16ll * num_sms()) split *= 2;
+    while (split < P.Hkv && split < 32768 && (long long)gx * split < 8ll * num_sms()) split *= 2;
     P.hpc = ceil_div(P.Hkv, split);
     const int gy = ceil_div(P.Hkv, P.hpc);
     if (gy > 65535) return SPEC_ERR_UNSUPPORTED;
