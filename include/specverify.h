@@ -644,8 +644,12 @@ spec_status_t spec_verify_attn_kv8_workspace_size(const spec_attn_desc *attn,
  *
  * Scores, softmax statistics and sums are held in fp32.  A row that sees a
  * block whose key scale is NaN gets o = lse = NaN, one whose value scale is
- * NaN o = NaN.  Codes in slots past seq_len are never used.  A seq_len outside [0, capacity] is clamped and sets
- * SPEC_DEV_SEQ_OVERFLOW; a page id outside [0, n_pages) is not read and sets
+ * NaN o = NaN; so does a row that sees a block or soft-prompt row with a
+ * non-finite key.  A non-finite value among those makes its seeing rows' o
+ * NaN in that dimension, and leaves their other dimensions unspecified.
+ * Rows that do not see such a place are not affected, and codes in slots
+ * past seq_len are never used.  A seq_len outside [0, capacity] is clamped
+ * and sets SPEC_DEV_SEQ_OVERFLOW; a page id outside [0, n_pages) is not read and sets
  * SPEC_DEV_BAD_PAGE (the affected outputs are then unspecified).  q, kb, vb,
  * soft_k, soft_v and o must be 16-byte aligned.
  */
@@ -713,7 +717,8 @@ spec_status_t kv8_append(const spec_kv8_desc *cache, int dtype, int n_tokens,
  *   slot_map   int64 [n_slots] out: packed token cu_new[b] + i is token
  *              seq_len[b] + i of request b and gets page * page_size +
  *              offset; -1 behind the last token.
- *   new_len    int32 [batch] out, or NULL: seq_len + n_new.
+ *   new_len    int32 [batch] out, or NULL: seq_len + n_new (not seq_len's
+ *              own array, which other threads still read).
  *
  * Pages are taken as kv_commit takes them.  A request that would exceed its
  * table is skipped (its slots are -1, new_len = seq_len; SPEC_DEV_CAPACITY),
@@ -785,8 +790,9 @@ spec_status_t spec_logits_adjust(const spec_logits_desc *desc, const void *logit
 
 /*
  * spec_set_wait_limit -- limit, in SM clock cycles, of the internal pipeline
- * waits of the kernels launched from now on (verify attention, prefill
- * attention, and the bulk row stream of the vocabulary reduction),
+ * waits of the kernels launched from now on (verify attention over either
+ * cache, prefill attention, and the bulk row stream of the vocabulary
+ * reduction),
  * process-wide.  The pages have no counterpart: this is the
  * library's guard against a hang.  A wait that runs out sets
  * SPEC_DEV_TIMEOUT; the kernel then stops issuing work, waits (with the

@@ -451,7 +451,12 @@ def _on(t, dtype, shape, name, dev, optional=False):
     on device `dev`, the current one, where the library launches."""
     if t is None and optional:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if (t.get_device() == dev and (dtype is None or t.dtype is dtype) and
+            (shape is None or t.shape == shape) and t.is_contiguous()):
+        return t.data_ptr()
+    if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
@@ -459,9 +464,7 @@ def _on(t, dtype, shape, name, dev, optional=False):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _cur(stream):
@@ -479,12 +482,14 @@ def _cur(stream):
 def kv8_desc(kv: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor = None) -> Kv8Desc:
     """kv: float8_e4m3fn (or uint8) [n_pages][Hkv][page_size / 8][2][8][d];
     scales fp32 [n_pages][Hkv][2]; page_table int32 [B][max_pages] (None for
-    kv8_append alone)."""
+    kv8_append alone).  The descriptor keeps the tensors alive."""
     if kv.dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise TypeError(f"kv must be float8_e4m3fn or uint8, got {kv.dtype}")
     if kv.dim() != 6 or kv.shape[3] != 2 or kv.shape[4] != 8:
         raise ValueError("kv must be [n_pages][Hkv][page_size / 8][2][8][d]")
     P, Hkv, groups, _, _, d = kv.shape
+    if not kv.is_cuda:
+        raise TypeError("kv must be a CUDA tensor")
     dev = kv.get_device()
     _on(kv, None, None, "kv", dev)
     _on(scales, torch.float32, (P, Hkv, 2), "scales", dev)
@@ -494,6 +499,7 @@ def kv8_desc(kv: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor = 
         B, maxp = page_table.shape
     desc = Kv8Desc(Hkv, d, kv.data_ptr(), scales.data_ptr(), B, P, groups * 8, maxp, pt)
     desc.device = dev
+    desc.tensors = (kv, scales, page_table)     # (alive as long as the descriptor)
     return desc
 
 

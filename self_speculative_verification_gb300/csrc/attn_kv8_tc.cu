@@ -17,7 +17,7 @@
 // power-of-two scale per row, exact but for elements under 2^-9 of the row's
 // largest (there: half of e4m3's smallest step, 2^-17.8 of the largest).  P
 // is split the same way, its second part raised by 2^4 into columns of its
-// own: 2^-9 of p, as bf16 would give it, and 2^-21 of the largest p where p
+// own: 2^-9 of p, as bf16 would give it, and 2^-17 of the largest p where p
 // is small.  The two parts of Q are 2 R columns of one product, the two parts
 // of P 2 R columns of the other.
 //

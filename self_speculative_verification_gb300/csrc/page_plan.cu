@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams P, b
         }
         if (tid == 0) s_cu[nb] = (int)ta;
         __syncthreads();
-        // this CTA's 128-token pieces of the chunk
+        // this CTA's pieces of the chunk
         const int n_tok = (int)ta;
         const int warps = kPlanThreads / 32 * nc, w = rank * (kPlanThreads / 32) + (tid >> 5);
         for (long long t0 = (long long)w * kPlanTokens; t0 < n_tok; t0 += (long long)warps * kPlanTokens) {
@@ -249,6 +249,7 @@ extern "C" spec_status_t spec_page_plan(int batch, int page_size, int n_pages,
         return SPEC_ERR_INVALID_ARG;
     if ((long long)max_pages_per_seq * page_size > (1ll << 30)) return SPEC_ERR_UNSUPPORTED;
     if (n_slots > 0 && !slot_map) return SPEC_ERR_INVALID_ARG;
+    if (new_len && new_len == seq_len) return SPEC_ERR_INVALID_ARG;
     if (!free_head || (batch > 0 && (!seq_len || !n_new || !page_table)) ||
         (n_free > 0 && !free_pages))
         return SPEC_ERR_INVALID_ARG;

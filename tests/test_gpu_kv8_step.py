@@ -302,3 +302,58 @@ def test_what_the_python_entry_points_refuse():
     with pytest.raises(ValueError, match="cu_new"):
         bn.spec_page_plan(16, 8, c.d_S, c.d_S, c.d_table, i32(4), i32(1), i32(2), slots)
     assert bn.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("x", [float("nan"), float("inf"), float("-inf")])
+def test_non_finite_rows_that_no_row_sees(dtype, x):
+    """Padding rows of the block (and the soft prompt, where no row sees it)
+    may hold anything: every output keeps its bits."""
+    a, b = (Attn(33, B=3, R=20, S=(100, 0, 260), n_soft=5, mask="tree", dtype=dtype) for _ in range(2))
+    b.d_flags.copy_(b.d_flags & 1)
+    a.d_flags.copy_(a.d_flags & 1)
+    off = torch.from_numpy(~b.valid).cuda()
+    assert off.any()
+    b.d_q[off] = x
+    at = off[:, None].expand(3, 2, 20)
+    b.d_kb[at] = x
+    b.d_vb[at] = x
+    b.d_sk.fill_(x)
+    b.d_sv.fill_(x)
+    a.run()
+    b.run()
+    assert torch.equal(a.o, b.o) and torch.equal(a.lse, b.lse)
+    assert bn.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_writers_at_the_end_of_a_cache_of_many_gigabytes(dtype):
+    """Offsets past 2^32 bytes: pages at the end of a 6 GB cache."""
+    rng = np.random.default_rng(34)
+    H, d, ps, n_pages, R = 8, 128, 64, 48000, 5
+    kv = torch.empty((n_pages, H, ps // 8, 2, 8, d), dtype=torch.uint8, device="cuda")
+    sc = torch.ones((n_pages, H, 2), device="cuda")
+    assert kv.numel() > 1 << 32
+    last = np.array([n_pages - 1, n_pages - 3], dtype=np.int32)
+    tail = kv[-4:]
+    tail.zero_()
+    codes, scales = np.zeros((4, H, 2, ps, d)), np.ones((4, H, 2))
+    dt = torch_dt(dtype)
+    k, v = (to_storage(rng.standard_normal((ps + 7, H, d)), dtype) for _ in range(2))
+    at = np.concatenate([np.arange(ps) + 3 * ps, np.arange(7) + ps])         # within the last four pages
+    slots = at + (n_pages - 4) * ps
+    cache = bn.kv8_desc(kv, sc, dev(last.reshape(2, 1)))
+    bn.kv8_append(cache, dev(k).to(dt), dev(v).to(dt), dev(slots))
+    codes, scales = kv8.append(codes, scales, k, v, at, ps)
+    kb, vb = (to_storage(rng.standard_normal((2, H, R, d)) * 3, dtype) for _ in range(2))
+    seq, table = np.array([0, 7], dtype=np.int32), np.array([[3], [1]], dtype=np.int32)
+    d_seq, head = dev(seq), i32(1)
+    # the first request's page is a new one: the last of the cache once more
+    bn.kv8_commit(cache, dev(kb).to(dt), dev(vb).to(dt), dev(np.tile(np.arange(R, dtype=np.int32), (2, 1))),
+                  dev(np.array([R, R], dtype=np.int32)), d_seq, dev(last[:1]), head)
+    assert bn.spec_get_status() == 0
+    codes, scales, table, seq, h = kv8.commit(codes, scales, table, seq, np.array([3], dtype=np.int32), 0, kb,
+                                              vb, [list(range(R))] * 2, ps)
+    assert np.array_equal(TABLE[unpack(tail)], codes)
+    assert np.array_equal(sc[-4:].double().cpu().numpy(), scales)
+    assert d_seq.tolist() == [R, 7 + R] and int(head) == h == 1

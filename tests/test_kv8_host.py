@@ -167,7 +167,7 @@ def test_append_refusals(lib):
 
 
 def plan(lib, B=2, ps=16, pages=8, maxp=4, n_free=8, n_slots=4, **ptrs):
-    p = dict(seq_len=P, n_new=P, table=P, free_pages=P, free_head=P, cu=P, slots=P, new_len=P)
+    p = dict(seq_len=P, n_new=P, table=P, free_pages=P, free_head=P, cu=P, slots=P, new_len=2 * P)
     p.update(ptrs)
     return lib.spec_page_plan(B, ps, pages, maxp, p["seq_len"], p["n_new"], p["table"], p["free_pages"],
                               n_free, p["free_head"], p["cu"], n_slots, p["slots"], p["new_len"], None)
@@ -178,7 +178,7 @@ def test_plan_refusals(lib):
                      (dict(maxp=0), INVALID), (dict(n_free=-1), INVALID), (dict(n_slots=-1), INVALID),
                      (dict(cu=None), INVALID), (dict(slots=None), INVALID), (dict(free_head=None), INVALID),
                      (dict(seq_len=None), INVALID), (dict(n_new=None), INVALID), (dict(table=None), INVALID),
-                     (dict(free_pages=None), INVALID),
+                     (dict(free_pages=None), INVALID), (dict(seq_len=P, new_len=P), INVALID),
                      (dict(ps=1 << 16, maxp=(1 << 14) + 1), UNSUPPORTED)]:
         assert plan(lib, **kw) == want, kw
 
