@@ -81,6 +81,40 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
     const int n_tiles = n_prefix_tiles + n_soft_tiles + n_block_tiles;
     bool bad_page = false;
 
+    // a prefix tile's K and V, 16 codes a vector, and their scales, in
+    // registers a tile ahead
+    constexpr int VPR = D / 16;
+    constexpr int kPer = 2 * kCols * VPR / 128;
+    uint4 w[kPer];
+    float sc[kPer];
+    auto fetch = [&](int tile) {
+        if (tile >= n_prefix_tiles) return;
+        const int base = t0 + tile * kCols, ncols = min(kCols, t1 - base);
+        // (a thread's vectors are K's, then V's, of one token or a few)
+        int page[kPer];
+#pragma unroll
+        for (int it = 0; it < kPer; ++it) {
+            const int j = ((tid + it * 128) / VPR) % kCols, t = base + j;
+            page[it] = j < ncols ? P.page_table[(size_t)b * P.max_pages + t / P.page_size] : 0;
+        }
+#pragma unroll
+        for (int it = 0; it < kPer; ++it) {
+            const int i = tid + it * 128, x = i / (kCols * VPR), j = (i / VPR) % kCols, c = i % VPR;
+            w[it] = make_uint4(0u, 0u, 0u, 0u);
+            sc[it] = 0.f;
+            if (j >= ncols) continue;
+            if (page[it] < 0 || page[it] >= P.n_pages) {
+                bad_page = true;
+                continue;
+            }
+            w[it] = *reinterpret_cast<const uint4 *>(
+                kv + kv8_block(page[it], h, P.Hkv, P.page_size, D) +
+                kv8_row((base + j) % P.page_size, x, D) + c * 16);
+            sc[it] = Q.scales[((size_t)page[it] * P.Hkv + h) * 2 + x];
+        }
+    };
+    fetch(0);
+
     for (int tile = 0; tile < n_tiles; ++tile) {
         int kind, base, ncols;
         if (tile < n_prefix_tiles) {
@@ -98,39 +132,17 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
         }
         __syncthreads();             // previous tile consumed (and sq / svis ready)
         if (kind == kColPrefix) {
-            // 16 codes a vector: K and V of the tile
-            constexpr int VPR = D / 16;
-            constexpr int kPer = 2 * kCols * VPR / 128;
-            uint4 w[kPer];
-            float sc[kPer];
-#pragma unroll
-            for (int it = 0; it < kPer; ++it) {
-                const int i = tid + it * 128, x = i / (kCols * VPR), j = (i / VPR) % kCols, c = i % VPR;
-                w[it] = make_uint4(0u, 0u, 0u, 0u);
-                sc[it] = 0.f;
-                if (j < ncols) {
-                    const int t = base + j;
-                    const int page = P.page_table[(size_t)b * P.max_pages + t / P.page_size];
-                    if (page < 0 || page >= P.n_pages) {
-                        bad_page = true;
-                    } else {
-                        w[it] = *reinterpret_cast<const uint4 *>(
-                            kv + kv8_block(page, h, P.Hkv, P.page_size, D) +
-                            kv8_row(t % P.page_size, x, D) + c * 16);
-                        sc[it] = kv8_read_scale(Q.scales[((size_t)page * P.Hkv + h) * 2 + x]);
-                    }
-                }
-            }
 #pragma unroll
             for (int it = 0; it < kPer; ++it) {
                 const int i = tid + it * 128, x = i / (kCols * VPR), j = (i / VPR) % kCols, c = i % VPR;
                 float *dst = x ? &sv_[j][c * 16] : &sk[j][c * 16];
                 const uint32_t u[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
+                const float f = kv8_read_scale(sc[it]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 lo = from_e4m3x2(u[e] & 0xffffu), hi = from_e4m3x2(u[e] >> 16);
                     *reinterpret_cast<float4 *>(dst + 4 * e) =
-                        make_float4(lo.x * sc[it], lo.y * sc[it], hi.x * sc[it], hi.y * sc[it]);
+                        make_float4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
                 }
             }
         } else {
@@ -145,6 +157,7 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
             }
         }
         __syncthreads();
+        fetch(tile + 1);
 
         // scores: four rows of this warp against the lane's column
         float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -303,7 +316,7 @@ spec_status_t make_plan8(const spec_attn_desc *a, const spec_kv8_desc *c, Plan8 
         const long long target = 8ll * num_sms();
         long long chunk = (units * half + target - 1) / target;
         chunk = (chunk + 63) / 64 * 64;
-        if (chunk < 128) chunk = 128;
+        if (chunk < 64) chunk = 64;
         if (chunk > 16384) chunk = 16384;
         P.chunk = (int)chunk;
     }
