@@ -8,14 +8,23 @@
 //   1. the slice's tokens are counted once in shared memory, the same for all
 //      of the rows, and a bit set for every touched one;
 //   2. the rows' slices pass through registers in 16-byte vectors, several in
-//      flight a thread; a vector without a touched token is copied, the
-//      others' tokens take their penalties and biases, with the occurrences
-//      on that row's path found from the ancestor bits of its node; tokens
-//      that the row's mask does not allow become -inf.
+//      flight a thread; tokens that the row's mask does not allow become -inf;
+//   3. the touched tokens take their penalties and biases, with the
+//      occurrences on that row's path found from the ancestor bits of its
+//      node.  Up to 256 of them are listed, and their logits written over
+//      those of step 2, a thread a (token, row): done with the vectors, each
+//      warp would run the adjustment for the one lane that needs it (70 us
+//      against 63 on 480 rows of 128256 logits).  In slices with more (the
+//      first ones: low ids are the common tokens) it is done with the vectors
+//      (11.5 us against 16 on 128 rows of 32000 logits).
 // Counts are integers and a token's biases are added in index order, so
 // results do not depend on the order of the threads.  Bound by the rows'
-// bytes, read and written once; the history is read once per CTA, from L2.
+// bytes, read and written once (63 us: 3.9 TB/s; without masks 51 us), then
+// by the instructions of a vector (~50 a warp) and a CTA's counting; the
+// history is read once per CTA, from L2.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -29,6 +38,7 @@ constexpr int kAdjResident = 4;              // CTAs an SM holds
 constexpr int kAdjFlight = 4;                // vectors in flight a thread
 constexpr int kAdjMaxNodes = SPEC_MAX_ROWS;
 constexpr int kAdjMaxBias = 1024;
+constexpr int kAdjListed = 256;              // touched tokens a slice lists
 
 struct AdjParams {
     const void *logits;
@@ -50,6 +60,15 @@ __device__ __forceinline__ uint32_t bits8(const uint32_t *w, int at) {
     return ((p[0] | (uint32_t)p[1] << 8) >> (at & 7)) & 0xffu;
 }
 
+// The bytes of x that kSel's digits name (8 + the byte), each replaced by its
+// sign (prmt's sign form, which __byte_perm leaves out).
+template <uint32_t kSel>
+__device__ __forceinline__ uint32_t byte_signs(uint32_t x) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(r) : "r"(x), "n"(kSel));
+    return r;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kernel(AdjParams P) {
     pdl_wait();
@@ -61,6 +80,9 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
     __shared__ uint32_t s_hit[kAdjSlice / 32 + 1];   // touched tokens,
     __shared__ uint32_t s_old[kAdjSlice / 32 + 1];   // those in the history,
     __shared__ uint32_t s_new[kAdjSlice / 32 + 1];   // and those of the draft
+    __shared__ uint16_t s_list[kAdjListed];          // the touched ones one after the other,
+                                                     // where there are few
+    __shared__ int n_list;
     __shared__ uint32_t s_anc[kAdjMaxNodes][kAdjMaxNodes / 32];   // path of each node
     __shared__ int16_t s_up[kAdjMaxNodes], s_next[kAdjMaxNodes];
     __shared__ uint8_t s_bad[kAdjMaxNodes];          // status bits of each node's path
@@ -235,14 +257,32 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
                 if (s_follow[j] >= 0) bits |= s_bad[s_follow[j]];
     }
     __syncthreads();
-    // what the history's tokens add, and the touched ones
-    static_assert(kAdjSlice == 8 * kAdjThreads && kAdjSlice / 32 < kAdjThreads, "eight tokens a thread");
-    for (uint32_t m = bits8(s_old, 8 * tid); m; m &= m - 1) {
+    // what the history's tokens add; the touched ones, listed by one warp
+    static_assert(kAdjSlice == 8 * kAdjThreads && kAdjSlice == 64 * 32, "eight tokens a thread, two words a lane");
+    for (uint32_t m = reinterpret_cast<const uint8_t *>(s_old)[tid]; m; m &= m - 1) {
         const int v = 8 * tid + __ffs(m) - 1;
         if (s_cnt[v]) s_add[v] -= fmaf(freq, (float)s_cnt[v], pres);
     }
-    if (tid < kAdjSlice / 32) s_hit[tid] |= s_old[tid] | s_new[tid];
+    if (tid < 32) {
+        const uint32_t m0 = s_hit[2 * lane] | s_old[2 * lane] | s_new[2 * lane];
+        const uint32_t m1 = s_hit[2 * lane + 1] | s_old[2 * lane + 1] | s_new[2 * lane + 1];
+        s_hit[2 * lane] = m0;
+        s_hit[2 * lane + 1] = m1;
+        uint64_t m = (uint64_t)m1 << 32 | m0;
+        const int n = __popcll(m);
+        int at = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += x;
+        }
+        const int total = __shfl_sync(0xffffffffu, at, 31);
+        if (lane == 0) n_list = total;
+        if (total <= kAdjListed)
+            for (at -= n; m; m &= m - 1) s_list[at++] = (uint16_t)(64 * lane + __ffsll(m) - 1);
+    }
     __syncthreads();
+    const bool listed = n_list <= kAdjListed;
     const int words = (P.V + 31) / 32;
     // a touched token's logit, in the row that follows `node`
     auto adjust = [&](float z, int v, int node) {
@@ -261,132 +301,170 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
     };
     const T *in = static_cast<const T *>(P.logits) + ((size_t)b * P.Rj + j0) * P.V + v0;
     T *out = static_cast<T *>(P.out) + ((size_t)b * P.Rj + j0) * P.V + v0;
-    // one logit at a time: `n` of row j from `first`
+    auto allowed = [&](int j, int i) {
+        return s_mask[j] < 0 ||
+               ((P.mask_bits[(size_t)s_mask[j] * words + ((v0 + i) >> 5)] >> ((v0 + i) & 31)) & 1u);
+    };
+    // one logit at a time: `n` of row j from `first`; listed tokens are
+    // adjusted later
     auto singles = [&](int j, int first, int n) {
 #pragma unroll 1
         for (int i = first; i < first + n; ++i) {
-            const T *src = in + (size_t)j * P.V + i;
-            T x = *src;
-            if ((s_hit[i >> 5] >> (i & 31)) & 1u) store_f(&x, adjust(load_f(src), i, s_follow[j]));
-            if (s_mask[j] >= 0 &&
-                !((P.mask_bits[(size_t)s_mask[j] * words + ((v0 + i) >> 5)] >> ((v0 + i) & 31)) & 1u))
-                store_f(&x, -INFINITY);
+            T x = in[(size_t)j * P.V + i];
+            if (!allowed(j, i)) store_f(&x, -INFINITY);
+            else if (!listed && ((s_hit[i >> 5] >> (i & 31)) & 1u))
+                store_f(&x, adjust(load_f(&x), i, s_follow[j]));
             out[(size_t)j * P.V + i] = x;
         }
     };
-    if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
-        for (int i = tid; i < rows * nv; i += kAdjThreads) singles(i / nv, i % nv, 1);
-        if (bits) raise_status(P.status, bits);
-        return;
-    }
     // row j's logits up to its first 16-byte boundary, and its vectors
     auto lead_of = [&](int j) {
         const int off = (int)((reinterpret_cast<uintptr_t>(in + (size_t)j * P.V) & 15) / sizeof(T));
         return min(nv, off ? N - off : 0);
     };
+    const bool vectors = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    if (!vectors)
+        for (int i = tid; i < rows * nv; i += kAdjThreads) singles(i / nv, i % nv, 1);
     // A thread takes the same vectors in every row; where the rows begin alike
     // (their length a multiple of 16 bytes) these are the same tokens, and what
     // it knows of them stays in registers.
     constexpr int kVecs = kAdjSlice / N;             // at most, a row
     constexpr uint32_t kAll = (1u << N) - 1u;
-    for (int e0 = tid; e0 < kVecs; e0 += kAdjThreads) {
-        int known_at = -1;
-        uint32_t hit = 0, old = 0, fresh = 0;
-        float add[N];
-        for (int r0 = 0; r0 < rows; r0 += kAdjFlight) {
-            uint4 x[kAdjFlight];
-            int at[kAdjFlight];                      // within the slice, -1 none
-            uint32_t ok[kAdjFlight];
-#pragma unroll
-            for (int f = 0; f < kAdjFlight; ++f) {
-                const int j = r0 + f;
-                at[f] = -1;
-                ok[f] = kAll;
-                if (j >= rows) continue;
-                const int first = lead_of(j) + e0 * N;
-                if (first + N > nv) continue;
-                at[f] = first;
-                x[f] = *reinterpret_cast<const uint4 *>(in + (size_t)j * P.V + first);
-                if (s_mask[j] >= 0) {
-                    const int v = v0 + first, w = v >> 5, sft = v & 31;
-                    const uint32_t *mw = P.mask_bits + (size_t)s_mask[j] * words;
-                    uint64_t m = mw[w];
-                    if (sft + N > 32) m |= (uint64_t)mw[w + 1] << 32;
-                    ok[f] = (uint32_t)(m >> sft) & kAll;
-                }
-            }
-#pragma unroll
-            for (int f = 0; f < kAdjFlight; ++f) {
-                if (at[f] < 0) continue;
-                if (at[f] != known_at) {
-                    known_at = at[f];
-                    hit = bits8(s_hit, known_at) & kAll;
-                    if (hit) {
-                        old = bits8(s_old, known_at);
-                        fresh = bits8(s_new, known_at) & kAll;
-#pragma unroll
-                        for (int q = 0; q < N; ++q) add[q] = s_add[known_at + q];
+    auto pass = [&](auto lists) {
+        constexpr bool kLists = decltype(lists)::value;
+        for (int e0 = tid; e0 < kVecs && vectors; e0 += kAdjThreads) {
+            int known_at = -1;
+            uint32_t hit = 0, old = 0, fresh = 0;
+            float add[N];
+            for (int r0 = 0; r0 < rows; r0 += kAdjFlight) {
+                uint4 x[kAdjFlight];
+                int at[kAdjFlight];                      // within the slice, -1 none
+                uint32_t ok[kAdjFlight];
+    #pragma unroll
+                for (int f = 0; f < kAdjFlight; ++f) {
+                    const int j = r0 + f;
+                    at[f] = -1;
+                    ok[f] = kAll;
+                    if (j >= rows) continue;
+                    const int first = lead_of(j) + e0 * N;
+                    if (first + N > nv) continue;
+                    at[f] = first;
+                    x[f] = *reinterpret_cast<const uint4 *>(in + (size_t)j * P.V + first);
+                    if (s_mask[j] >= 0) {
+                        const int v = v0 + first, w = v >> 5, sft = v & 31;
+                        const uint32_t *mw = P.mask_bits + (size_t)s_mask[j] * words;
+                        uint64_t m = mw[w];
+                        if (sft + N > 32) m |= (uint64_t)mw[w + 1] << 32;
+                        ok[f] = (uint32_t)(m >> sft) & kAll;
                     }
                 }
-                uint32_t e[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
-                if (hit & ok[f]) {
-                    auto known = [&](float z, int q) {
-                        return fmaf(z, !((old >> q) & 1u) ? 1.f : z > 0.f ? inv_rep : rep, add[q]);
-                    };
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+    #pragma unroll
+                for (int f = 0; f < kAdjFlight; ++f) {
+                    if (at[f] < 0) continue;
+                    if (!kLists && at[f] != known_at) {
+                        known_at = at[f];
+                        hit = bits8(s_hit, known_at) & kAll;
+                        if (hit) {
+                            old = bits8(s_old, known_at);
+                            fresh = bits8(s_new, known_at) & kAll;
+    #pragma unroll
+                            for (int q = 0; q < N; ++q) add[q] = s_add[known_at + q];
+                        }
+                    }
+                    uint32_t e[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+                    if (!kLists && (hit & ok[f])) {
+                        auto known = [&](float z, int q) {
+                            return fmaf(z, !((old >> q) & 1u) ? 1.f : z > 0.f ? inv_rep : rep, add[q]);
+                        };
+    #pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if constexpr (N == 8) {
+                                const __nv_bfloat162 r = __floats2bfloat162_rn(
+                                    known(__uint_as_float(e[q] << 16), 2 * q),
+                                    known(__uint_as_float(e[q] & 0xffff0000u), 2 * q + 1));
+                                e[q] = *reinterpret_cast<const uint32_t *>(&r);
+                            } else {
+                                e[q] = __float_as_uint(known(__uint_as_float(e[q]), q));
+                            }
+                        }
+                        // the draft's tokens anew, for this row's path
+                        for (uint32_t m = fresh; m; m &= m - 1) {
+                            const int q = __ffs(m) - 1, h = q * 4 / N;
+                            const uint32_t word = h < 2 ? (h == 0 ? x[f].x : x[f].y) : (h == 2 ? x[f].z : x[f].w);
+                            uint32_t keep = 0, z = word;
+                            if constexpr (N == 8) {
+                                keep = q & 1 ? 0xffffu : 0xffff0000u;
+                                z = q & 1 ? word & 0xffff0000u : word << 16;
+                            }
+                            const float y = adjust(__uint_as_float(z), at[f] + q, s_follow[r0 + f]);
+                            z = __float_as_uint(y);
+                            if constexpr (N == 8) {
+                                z = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y));
+                                z = q & 1 ? z << 16 : z;
+                            }
+    #pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k == h) e[k] = (e[k] & keep) | z;
+                        }
+                    }
+                    if (ok[f] != kAll) {
                         if constexpr (N == 8) {
-                            const __nv_bfloat162 r = __floats2bfloat162_rn(
-                                known(__uint_as_float(e[q] << 16), 2 * q),
-                                known(__uint_as_float(e[q] & 0xffff0000u), 2 * q + 1));
-                            e[q] = *reinterpret_cast<const uint32_t *>(&r);
+#pragma unroll
+                            for (int q = 0; q < 4; q += 2) {
+                                // four bits, each at a byte's top, whose sign fills a logit's halves
+                                const uint32_t t = (((ok[f] >> 2 * q) & 15u) * 0x00204081u & 0x01010101u) << 7;
+                                const uint32_t k0 = byte_signs<0x9988>(t), k1 = byte_signs<0xbbaa>(t);
+                                e[q] = (e[q] & k0) | (0xff80ff80u & ~k0);
+                                e[q + 1] = (e[q + 1] & k1) | (0xff80ff80u & ~k1);
+                            }
                         } else {
-                            e[q] = __float_as_uint(known(__uint_as_float(e[q]), q));
-                        }
-                    }
-                    // the draft's tokens anew, for this row's path
-                    for (uint32_t m = fresh; m; m &= m - 1) {
-                        const int q = __ffs(m) - 1, h = q * 4 / N;
-                        const uint32_t word = h < 2 ? (h == 0 ? x[f].x : x[f].y) : (h == 2 ? x[f].z : x[f].w);
-                        uint32_t keep = 0, z = word;
-                        if constexpr (N == 8) {
-                            keep = q & 1 ? 0xffffu : 0xffff0000u;
-                            z = q & 1 ? word & 0xffff0000u : word << 16;
-                        }
-                        const float y = adjust(__uint_as_float(z), at[f] + q, s_follow[r0 + f]);
-                        z = __float_as_uint(y);
-                        if constexpr (N == 8) {
-                            z = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y));
-                            z = q & 1 ? z << 16 : z;
-                        }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (k == h) e[k] = (e[k] & keep) | z;
-                    }
-                }
-                if (ok[f] != kAll) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if constexpr (N == 8) {
-                            const uint32_t keep = ((ok[f] >> (2 * q)) & 1u) * 0xffffu |
-                                                  ((ok[f] >> (2 * q + 1)) & 1u) * 0xffff0000u;
-                            e[q] = (e[q] & keep) | (0xff80ff80u & ~keep);
-                        } else {
-                            e[q] = (ok[f] >> q) & 1u ? e[q] : 0xff800000u;
+                            for (int q = 0; q < 4; ++q) e[q] = (ok[f] >> q) & 1u ? e[q] : 0xff800000u;
                         }
                     }
+                    *reinterpret_cast<uint4 *>(out + (size_t)(r0 + f) * P.V + at[f]) =
+                        make_uint4(e[0], e[1], e[2], e[3]);
                 }
-                *reinterpret_cast<uint4 *>(out + (size_t)(r0 + f) * P.V + at[f]) =
-                    make_uint4(e[0], e[1], e[2], e[3]);
             }
         }
-    }
-    // the rows' ends outside the vectors: fewer than N logits each
-    for (int i = tid; i < 2 * rows; i += kAdjThreads) {
+    };
+    if (listed) pass(std::true_type{});
+    else pass(std::false_type{});
+    // (the rows' ends outside the vectors: fewer than N logits each)
+    for (int i = tid; i < 2 * rows && vectors; i += kAdjThreads) {
         const int j = i >> 1, lead = lead_of(j), tail = (nv - lead) % N;
         if (i & 1) singles(j, nv - tail, tail);
         else singles(j, 0, lead);
     }
+    if (!listed) {
+        if (bits) raise_status(P.status, bits);
+        return;
+    }
+    __syncthreads();
+    // the listed tokens that the row allows, over what was written there
+    // (in place, an allowed token's logit is still as it was given)
+    int shift = 0;
+    while ((1 << shift) < rows) ++shift;
+    const int j = tid & ((1 << shift) - 1);
+    if (j < rows)
+        for (int i0 = tid >> shift; i0 < n_list; i0 += kAdjFlight * (kAdjThreads >> shift)) {
+            int v[kAdjFlight];
+            float z[kAdjFlight];
+            uint32_t w[kAdjFlight];
+#pragma unroll
+            for (int f = 0; f < kAdjFlight; ++f) {
+                const int i = i0 + f * (kAdjThreads >> shift);
+                v[f] = i < n_list ? s_list[i] : -1;
+                w[f] = ~0u;
+                if (v[f] < 0) continue;
+                z[f] = load_f(in + (size_t)j * P.V + v[f]);
+                if (s_mask[j] >= 0) w[f] = P.mask_bits[(size_t)s_mask[j] * words + ((v0 + v[f]) >> 5)];
+            }
+#pragma unroll
+            for (int f = 0; f < kAdjFlight; ++f)
+                if (v[f] >= 0 && ((w[f] >> ((v0 + v[f]) & 31)) & 1u))
+                    store_f(out + (size_t)j * P.V + v[f], adjust(z[f], v[f], s_follow[j]));
+        }
     if (bits) raise_status(P.status, bits);
 }
 
