@@ -26,15 +26,22 @@
 // every row's sum is a register of each token's thread until the unit ends).
 // l adds p / v_scale.
 //
-// A persistent grid takes equal parts of the linear step space (attn_tc_sched):
+// A persistent grid takes equal parts of the linear step space (attn_tc_sched;
+// a unit's start counted as five steps: 4600-8000 cycles by a fit over the
+// CTAs, tree 104 -> 93 us against two):
 // a unit is a (request, KV head, block of R packed rows), its steps the prefix
 // in 128-token tiles, then the tail -- soft prompt and block, which a first
 // kernel has split into two e4m3 tiles -- in the same form, two ring slots a
 // step.  Units split between CTAs leave fp32 partials for a combine kernel.
 //
-// Bound by the cache's bytes up to 64 packed rows per KV head (12 MMAs of
-// about 50 cycles against ~1400 cycles to stream a tile at d = 128), by the
-// softmax beyond, where the row blocks of a head read the cache through L2.
+// Bound by the cache's bytes up to 32 packed rows per KV head (8 MMAs of
+// about 50 cycles against ~1400 cycles to stream a tile at d = 128): 64
+// requests of 16-32 K tokens, 8 KV heads, 32 rows take 503 us, 6.4 TB/s.  By
+// the softmax's chain from 64 rows on (~2600 cycles a step), where the row
+// blocks of a head read the cache through L2: 8 requests of 256-2048 tokens
+// with 120-node trees, 480 rows a head, take 89 us, 207 TFLOP/s.  Small calls
+// wait for the preparing kernel and the first copies, then for the combine:
+// one token over 32 K takes 26 us, over 300 tokens 17 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -82,16 +89,17 @@ struct Tc8Params {
     uint64_t ps16_inv;       // (exact for 26-bit token / 16: the error is under 16 * 2^26 / 2^32)
 };
 
-// Two softmax warpgroups.  Up to 32 rows they take alternate steps, each with
+// The softmax's warpgroups.  Up to 32 rows two take alternate steps, each with
 // all of the unit's rows and a running softmax (M, l, O) of its own, merged at
 // the unit's end: a step's chain (wait, tensor memory, vote, exponentials, P,
-// arrive: ~2000 cycles, most of it latency) then costs half.  With 64 rows, whose arithmetic
-// is the larger part, they take half of the rows of every step.
+// arrive: ~2000 cycles, most of it latency) then costs half.  With 64 rows, whose
+// arithmetic is the larger part, they take half of the rows of every step (four
+// with a quarter each repeat what a step costs a thread: tree 105 -> 111 us).
 template <int D, int RB>
 struct Cfg {
     static constexpr bool kAlt = RB <= 32;
     static constexpr int NA = kAlt ? 2 : 1;             // steps in the softmax at a time
-    static constexpr int NR = RB <= 32 ? 1 : 2;         // warpgroups that share a step's rows
+    static constexpr int NR = kAlt ? 1 : 2;             // warpgroups that share a step's rows
     static constexpr int NG = NA * NR;                  // softmax warpgroups
     static constexpr int RW = RB / NR;                  // rows of a warpgroup
     static constexpr int kThreads = NG * 128 + 128;
