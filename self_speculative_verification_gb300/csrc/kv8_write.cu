@@ -29,9 +29,11 @@ template <> struct RowVec<float> {
         x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
         x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
     }
-    __device__ static uint32_t amax(const uint4 &v) {
-        return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+    // the running maximum m of |x|, and its value's bits
+    __device__ static uint32_t amax(uint32_t m, const uint4 &v) {
+        return max(max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu)), m);
     }
+    __device__ static uint32_t bits(uint32_t m) { return m; }
 };
 template <> struct RowVec<__nv_bfloat16> {
     static constexpr int N = 8;
@@ -43,15 +45,17 @@ template <> struct RowVec<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
-    __device__ static uint32_t amax(const uint4 &v) {
-        auto max2 = [](uint32_t a, uint32_t b) {
-            uint32_t r;
-            asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
-            return r;
-        };
-        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
-        return max(m << 16, m & 0xffff0000u);
+    __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
     }
+    // the running maxima m of the even and the odd values' |x|, and the larger one's bits
+    __device__ static uint32_t amax(uint32_t m, const uint4 &v) {
+        m = max2(max2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), m);
+        return max2(max2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu), m);
+    }
+    __device__ static uint32_t bits(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
 };
 
 // N values as codes, x * r; `odd`: among non-finite ones, which become NaN.
@@ -70,10 +74,11 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, float (&x)[N], float r
 }
 
 // One warp: rows `n` of one block, at offsets first .. first + n - 1 of its
-// page; row(i) is the i-th row's first element or nullptr (not written).
+// page; row(i) is the i-th row's first element or, unless kDense, nullptr
+// (not written).
 // Sixteen rows pass through registers at a time; a block of more is read
 // twice, the second time from L1 / L2 (at most 128 KB).
-template <typename T, int D, typename Row>
+template <typename T, int D, bool kDense, typename Row>
 __device__ void write_block(uint8_t *tile, float *scale, int x, int first, int n, const Row &row) {
     constexpr int N = RowVec<T>::N, LPR = D / N;     // lanes per row
     constexpr int RPI = 32 / LPR, kHeld = 16 / RPI;  // rows per round, rounds held
@@ -85,9 +90,10 @@ __device__ void write_block(uint8_t *tile, float *scale, int x, int first, int n
 #pragma unroll
         for (int u = 0; u < kHeld; ++u) {
             const int i = i0 + u * RPI + sub;
-            const T *p = i < n ? row(i) : nullptr;
             held[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (!p) continue;
+            if (i >= n) continue;
+            const T *p = row(i);
+            if (!kDense && !p) continue;
             have |= 1u << u;
             held[u] = *reinterpret_cast<const uint4 *>(p + col);
         }
@@ -99,10 +105,10 @@ __device__ void write_block(uint8_t *tile, float *scale, int x, int first, int n
         fetch(i0);
         any |= have;
 #pragma unroll
-        for (int u = 0; u < kHeld; ++u) amax = max(amax, RowVec<T>::amax(held[u]));
+        for (int u = 0; u < kHeld; ++u) amax = RowVec<T>::amax(amax, held[u]);
     }
-    if (!__any_sync(0xffffffffu, any != 0u)) return;
-    amax = __reduce_max_sync(0xffffffffu, amax);
+    if (!kDense && !__any_sync(0xffffffffu, any != 0u)) return;
+    amax = __reduce_max_sync(0xffffffffu, RowVec<T>::bits(amax));
     const bool bad = amax >= kInf;
     if (bad) {               // the largest finite one, value by value
         amax = 0;
@@ -144,12 +150,16 @@ __device__ void write_block(uint8_t *tile, float *scale, int x, int first, int n
     const float r = 1.f / s;                         // exact for a power of two
     for (int i0 = last; i0 >= 0; i0 -= 16) {         // (the last rows are still held)
         if (i0 != last) fetch(i0);
+        // (from a multiple of eight on, the rows' places are constants apart)
+        const bool even = ((first + i0) & 7) == 0;
+        uint8_t *at = tile + kv8_row(first + i0, x, D) + sub * D + col;
 #pragma unroll
         for (int u = 0; u < kHeld; ++u) {
-            if (!((have >> u) & 1u)) continue;
+            if (kDense ? i0 + u * RPI + sub >= n : !((have >> u) & 1u)) continue;
             float v[N];
             RowVec<T>::get(held[u], v);
-            store_codes<N>(tile + kv8_row(first + i0 + u * RPI + sub, x, D) + col, v, r, bad);
+            store_codes<N>(even ? at + kv8_row(u * RPI, 0, D)
+                                : tile + kv8_row(first + i0 + u * RPI + sub, x, D) + col, v, r, bad);
         }
     }
     __syncwarp();
@@ -207,7 +217,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv8_commit_kernel(Commit8Par
         }
         return src + (size_t)r * D;
     };
-    write_block<T, D>(Q.kv + kv8_block(page, h, P.Hkv, ps, D),
+    write_block<T, D, false>(Q.kv + kv8_block(page, h, P.Hkv, ps, D),
                       Q.scales + ((size_t)page * P.Hkv + h) * 2 + x, x, t0 - j * ps, t1 - t0, row);
     if (bad_row) raise_status(P.status, SPEC_DEV_BAD_INDEX);
 }
@@ -295,9 +305,9 @@ kv8_append_kernel(Append8Params P) {
         uint8_t *tile = P.kv + kv8_block(page, h, P.Hkv, P.ps, D);
         float *scale = P.scales + ((size_t)page * P.Hkv + h) * 2 + x;
         if (len > 0)
-            write_block<T, D>(tile, scale, x, first, len, [&](int t) { return src + (size_t)t * stride; });
+            write_block<T, D, true>(tile, scale, x, first, len, [&](int t) { return src + (size_t)t * stride; });
         else
-            write_block<T, D>(tile, scale, x, first, -len, [&](int t) -> const T * {
+            write_block<T, D, false>(tile, scale, x, first, -len, [&](int t) -> const T * {
                 return P.slots[i + t] < 0 ? nullptr : src + (size_t)t * stride;
             });
     }
