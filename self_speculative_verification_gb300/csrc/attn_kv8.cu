@@ -12,70 +12,92 @@
 // combine kernel.
 #include <math.h>
 
+#include <type_traits>
+
 #include "attn_kv8.cuh"
 #include "kv8_common.cuh"
 
 namespace sv {
 namespace {
 
-constexpr int kRows = 16;    // packed rows per CTA (4 warps x 4 rows)
-constexpr int kCols = 32;    // columns per tile (one per lane)
+constexpr int kCols = 64;    // columns per tile
 
 enum { kColPrefix = 0, kColSoft = 1, kColBlock = 2 };
 
+// Shared memory of a CTA of RB packed rows.
+template <int D, int RB>
+struct SimtShared {
+    // (row pitches: eight rows' 16-byte reads, or eight columns' P, spread over the banks)
+    alignas(16) float q[RB][D + 4];
+    alignas(16) float k[kCols][D + 4];
+    alignas(16) float v[kCols][D];
+    alignas(16) float p[kCols][RB + 4];    // a row's -0: the column is not seen
+    float alpha[RB];                       // what the rows' O is scaled by
+    uint32_t vis[RB][SPEC_MAX_ROWS / 32];
+    uint8_t flags[RB];
+};
+
 // CTA (split, KV head x row block, request): a running softmax over its
-// columns, 32 at a time through shared memory; lane = column for the scores
-// (four rows per warp share each key vector), lane = head dimension for O.
-template <int D>
+// columns, 64 at a time through shared memory.  Scores: a thread takes RB / 8
+// rows and every 16th column; O: RB / 4 (d = 128) or RB / 8 (d = 64) rows and
+// four head dimensions.  With 32 rows either product makes 5.3 fused
+// multiply-adds a thread of every shared-memory wavefront of its warp.
+template <int D, int RB>
 __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
     pdl_wait();
     const AttnParams &P = Q.a;
-    constexpr int KP = D + 4;        // key row pitch: a quarter-warp's 16-byte reads spread over the banks
-    __shared__ __align__(16) float sq[kRows][D];
-    __shared__ __align__(16) float sk[kCols][KP];
-    __shared__ __align__(16) float sv_[kCols][D];
-    __shared__ uint32_t svis[kRows][SPEC_MAX_ROWS / 32];
-    __shared__ uint8_t sflags[kRows];
+    extern __shared__ __align__(16) uint8_t smem[];
+    auto &sh = *reinterpret_cast<SimtShared<D, RB> *>(smem);
+    constexpr int RT = RB / 8, CT = kCols / 16;          // scores: rows and columns a thread
+    constexpr int DG = D / 4, RP = RB * DG / 128;        // O: groups of dimensions, rows a thread
 
     const int split = blockIdx.x;
     const int h = blockIdx.y / P.n_rb, rb = blockIdx.y % P.n_rb;
     const int b = blockIdx.z;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
+    const int rg = tid / 16, cg = tid % 16;              // scores: rows rg RT .., columns cg + 16 c
+    const int pg = tid / DG, dg = tid % DG;              // O: rows pg RP .., dimensions 4 dg ..
 
     const int S = clamp_seq(P, b, split == 0 && blockIdx.y == 0 && tid == 0);
     const int nsp = n_splits_of(P, S);
     if (split >= nsp) return;
     const int t0 = split * P.chunk, t1 = min(S, t0 + P.chunk);
     const bool last = split == nsp - 1;
-    const int row0 = rb * kRows;
+    const int row0 = rb * RB;
 
     const float *q = static_cast<const float *>(P.q);
-    for (int i = tid; i < kRows * D; i += 128) {
-        const int p = row0 + i / D;
-        float x = 0.f;
+    for (int i = tid; i < RB * DG; i += 128) {
+        const int p = row0 + i / DG, c = i % DG * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p < P.M) {
             const int r = p / P.G, hq = h * P.G + p % P.G;
-            x = load_f(q + (((size_t)b * P.R + r) * P.Hq + hq) * D + i % D) * P.scale_log2;
+            x = *reinterpret_cast<const float4 *>(q + (((size_t)b * P.R + r) * P.Hq + hq) * D + c);
+            x.x *= P.scale_log2;
+            x.y *= P.scale_log2;
+            x.z *= P.scale_log2;
+            x.w *= P.scale_log2;
         }
-        sq[i / D][i % D] = x;
+        *reinterpret_cast<float4 *>(&sh.q[i / DG][c]) = x;
     }
-    for (int i = tid; i < kRows * P.W; i += 128) {
+    for (int i = tid; i < RB * P.W; i += 128) {
         const int pr = i / P.W, w = i % P.W, p = row0 + pr;
-        svis[pr][w] = p < P.M ? P.vis[((size_t)b * P.R + p / P.G) * P.W + w] : 0u;
+        sh.vis[pr][w] = p < P.M ? P.vis[((size_t)b * P.R + p / P.G) * P.W + w] : 0u;
     }
-    if (tid < kRows) {
+    if (tid < RB) {
         const int p = row0 + tid;
-        sflags[tid] = p < P.M ? P.row_flags[(size_t)b * P.R + p / P.G] : 0;
+        sh.flags[tid] = p < P.M ? P.row_flags[(size_t)b * P.R + p / P.G] : 0;
     }
 
-    float m[4], l[4], acc[4][D / 32];
+    float m[RT], l[RT], acc[RP][4];                      // (l: of this thread's columns)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RT; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) acc[i][j] = 0.f;
     }
+#pragma unroll
+    for (int i = 0; i < RP; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 
     const uint8_t *kv = static_cast<const uint8_t *>(P.kc);
     const int n_prefix_tiles = ceil_div(t1 - t0, kCols);
@@ -93,7 +115,6 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
     auto fetch = [&](int tile) {
         if (tile >= n_prefix_tiles) return;
         const int base = t0 + tile * kCols, ncols = min(kCols, t1 - base);
-        // (a thread's vectors are K's, then V's, of one token or a few)
         int page[kPer];
 #pragma unroll
         for (int it = 0; it < kPer; ++it) {
@@ -133,12 +154,12 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
             base = (tile - n_prefix_tiles - n_soft_tiles) * kCols;
             ncols = min(kCols, P.R - base);
         }
-        __syncthreads();             // previous tile consumed (and sq / svis ready)
+        __syncthreads();             // previous tile consumed (and q, vis, flags ready)
         if (kind == kColPrefix) {
 #pragma unroll
             for (int it = 0; it < kPer; ++it) {
                 const int i = tid + it * 128, x = i / (kCols * VPR), j = (i / VPR) % kCols, c = i % VPR;
-                float *dst = x ? &sv_[j][c * 16] : &sk[j][c * 16];
+                float *dst = x ? &sh.v[j][c * 16] : &sh.k[j][c * 16];
                 const uint32_t u[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
                 const float f = kv8_read_scale(sc[it]);
 #pragma unroll
@@ -153,80 +174,141 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
                                                   : ((size_t)b * P.Hkv + h) * P.R;
             const float *kp = static_cast<const float *>(kind == kColSoft ? P.soft_k : P.kb) + (first + base) * D;
             const float *vp = static_cast<const float *>(kind == kColSoft ? P.soft_v : P.vb) + (first + base) * D;
-            for (int i = tid; i < kCols * D; i += 128) {
-                const int j = i / D, k = i % D;
-                sk[j][k] = j < ncols ? load_f(kp + i) : 0.f;
-                sv_[j][k] = j < ncols ? load_f(vp + i) : 0.f;
+            for (int i = tid; i < kCols * DG; i += 128) {
+                const int j = i / DG, c = i % DG * 4;
+                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4 *>(&sh.k[j][c]) =
+                    j < ncols ? *reinterpret_cast<const float4 *>(kp + 4 * i) : z;
+                *reinterpret_cast<float4 *>(&sh.v[j][c]) =
+                    j < ncols ? *reinterpret_cast<const float4 *>(vp + 4 * i) : z;
             }
         }
         __syncthreads();
         fetch(tile + 1);
 
-        // scores: four rows of this warp against the lane's column
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
+        float s[RT][CT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) s[i][c] = 0.f;
+#pragma unroll 4
         for (int k = 0; k < D; k += 4) {
-            const float4 kk = *reinterpret_cast<const float4 *>(&sk[lane][k]);
+            float4 kk[CT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 qq = *reinterpret_cast<const float4 *>(&sq[warp * 4 + i][k]);
-                s[i] = fmaf(qq.x, kk.x, s[i]);
-                s[i] = fmaf(qq.y, kk.y, s[i]);
-                s[i] = fmaf(qq.z, kk.z, s[i]);
-                s[i] = fmaf(qq.w, kk.w, s[i]);
-            }
-        }
-        float p[4];
-        unsigned seen[4];            // columns each row sees
+            for (int c = 0; c < CT; ++c) kk[c] = *reinterpret_cast<const float4 *>(&sh.k[cg + 16 * c][k]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int pr = warp * 4 + i;
-            const uint8_t fl = sflags[pr];
-            bool visible = false;
-            if (lane < ncols && (fl & SPEC_ROW_VALID)) {
-                if (kind == kColPrefix) visible = true;
-                else if (kind == kColSoft) visible = (fl & SPEC_ROW_SEES_SOFT) != 0;
-                else visible = (svis[pr][(base + lane) >> 5] >> ((base + lane) & 31)) & 1u;
-            }
-            const float mn = fmaxf(m[i], warp_max(visible ? s[i] : -INFINITY));
-            const float mr = mn == -INFINITY ? 0.f : mn;    // (nothing but masked, -inf or NaN scores)
-            const float alpha = exp2f(m[i] - mr);
-            p[i] = visible ? exp2f(s[i] - mr) : 0.f;
-            seen[i] = __ballot_sync(0xffffffffu, visible);
-            l[i] = l[i] * alpha + warp_sum(p[i]);
+            for (int i = 0; i < RT; ++i) {
+                const float4 qq = *reinterpret_cast<const float4 *>(&sh.q[rg * RT + i][k]);
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) acc[i][j] *= alpha;
-            m[i] = mn;
-        }
-        // O: columns a row does not see are left out (their values may be
-        // anything)
-        for (int jj = 0; jj < ncols; ++jj) {
-            float v[D / 32];
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) v[j] = sv_[jj][lane + 32 * j];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float pj = __shfl_sync(0xffffffffu, p[i], jj);
-                if ((seen[i] >> jj) & 1u) {
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) acc[i][j] = fmaf(pj, v[j], acc[i][j]);
+                for (int c = 0; c < CT; ++c) {
+                    s[i][c] = fmaf(qq.x, kk[c].x, s[i][c]);
+                    s[i][c] = fmaf(qq.y, kk[c].y, s[i][c]);
+                    s[i][c] = fmaf(qq.z, kk[c].z, s[i][c]);
+                    s[i][c] = fmaf(qq.w, kk[c].w, s[i][c]);
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int pr = rg * RT + i;
+            const uint8_t fl = sh.flags[pr];
+            unsigned seen = 0;
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                const int j = cg + 16 * c;
+                bool visible = false;
+                if (j < ncols && (fl & SPEC_ROW_VALID)) {
+                    if (kind == kColPrefix) visible = true;
+                    else if (kind == kColSoft) visible = (fl & SPEC_ROW_SEES_SOFT) != 0;
+                    else visible = (sh.vis[pr][(base + j) >> 5] >> ((base + j) & 31)) & 1u;
+                }
+                seen |= (unsigned)visible << c;
+                if (visible) top = fmaxf(top, s[i][c]);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float mn = fmaxf(m[i], top);
+            const float mr = mn == -INFINITY ? 0.f : mn;    // (nothing but masked, -inf or NaN scores)
+            const float alpha = exp2f(m[i] - mr);
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                const float p = (seen >> c) & 1u ? exp2f(s[i][c] - mr) : -0.f;
+                sum += p;
+                s[i][c] = p;
+            }
+            l[i] = fmaf(l[i], alpha, sum);
+            m[i] = mn;
+            if (cg == 0) sh.alpha[pr] = alpha;
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            float *dst = &sh.p[cg + 16 * c][rg * RT];
+            if constexpr (RT == 4) *reinterpret_cast<float4 *>(dst) = make_float4(s[0][c], s[1][c], s[2][c], s[3][c]);
+            else dst[0] = s[0][c];
+        }
+        __syncthreads();
+
+#pragma unroll
+        for (int i = 0; i < RP; ++i) {
+            const float f = sh.alpha[pg * RP + i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] *= f;
+        }
+        // O.  Outside the prefix, columns that a row does not see are left out:
+        // their values may be anything.
+        auto add = [&](auto all) {
+            constexpr bool kAll = decltype(all)::value;
+#pragma unroll 4
+            for (int j = 0; j < ncols; ++j) {
+                const float4 v = *reinterpret_cast<const float4 *>(&sh.v[j][4 * dg]);
+                float pj[RP];
+                if constexpr (RP % 4 == 0) {
+#pragma unroll
+                    for (int i = 0; i < RP; i += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(&sh.p[j][pg * RP + i]);
+                        pj[i] = x.x;
+                        pj[i + 1] = x.y;
+                        pj[i + 2] = x.z;
+                        pj[i + 3] = x.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < RP; ++i) pj[i] = sh.p[j][pg * RP + i];
+                }
+#pragma unroll
+                for (int i = 0; i < RP; ++i) {
+                    if (!kAll && __float_as_int(pj[i]) == (int)0x80000000u) continue;
+                    acc[i][0] = fmaf(pj[i], v.x, acc[i][0]);
+                    acc[i][1] = fmaf(pj[i], v.y, acc[i][1]);
+                    acc[i][2] = fmaf(pj[i], v.z, acc[i][2]);
+                    acc[i][3] = fmaf(pj[i], v.w, acc[i][3]);
+                }
+            }
+        };
+        if (kind == kColPrefix) add(std::true_type{});
+        else add(std::false_type{});
     }
     if (bad_page) raise_status(P.status, SPEC_DEV_BAD_PAGE);
 
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int p = row0 + warp * 4 + i;
+    for (int i = 0; i < RP; ++i) {
+        const int pr = pg * RP + i, p = row0 + pr;
         if (p >= P.M) continue;
-        const size_t idx = part_index(P, b, h, split, p);
+        // (a row that is not valid sees nothing, but its O may have met a NaN)
+        const bool valid = (sh.flags[pr] & SPEC_ROW_VALID) != 0;
+        *reinterpret_cast<float4 *>(P.part_o + part_index(P, b, h, split, p) * D + 4 * dg) =
+            valid ? make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) P.part_o[idx * D + lane + 32 * j] = acc[i][j];
-        if (lane == 0) {
-            P.part_ml[idx * 2] = m[i];
-            P.part_ml[idx * 2 + 1] = l[i];
-        }
+    for (int i = 0; i < RT; ++i) {
+        const int p = row0 + rg * RT + i;
+        float sum = l[i];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (cg == 0 && p < P.M)
+            *reinterpret_cast<float2 *>(P.part_ml + part_index(P, b, h, split, p) * 2) = make_float2(m[i], sum);
     }
 }
 
@@ -307,7 +389,7 @@ spec_status_t make_plan8(const spec_attn_desc *a, const spec_kv8_desc *c, Plan8 
     P.capacity = c->max_pages_per_seq * c->page_size;
     const float scale = a->scale != 0.f ? a->scale : 1.f / sqrtf((float)a->head_dim);
     P.scale_log2 = scale * kLog2e;
-    P.rb_rows = kRows;
+    P.rb_rows = P.M <= 8 ? 8 : 32;
     P.n_rb = ceil_div(P.M, P.rb_rows);
     if ((long long)P.Hkv * P.n_rb > 65535) return SPEC_ERR_UNSUPPORTED;
     if (a->split_tokens > 0) {
@@ -338,11 +420,13 @@ spec_status_t make_plan8(const spec_attn_desc *a, const spec_kv8_desc *c, Plan8 
     return SPEC_OK;
 }
 
-template <int D>
+template <int D, int RB>
 spec_status_t launch_simt8(const Kv8Params &Q, cudaStream_t s) {
     const AttnParams &P = Q.a;
-    spec_status_t st = launch(attn_kv8_simt_kernel<D>, dim3(P.max_splits, P.Hkv * P.n_rb, P.B),
-                              dim3(128), 0, s, Q);
+    constexpr size_t kSmem = sizeof(SimtShared<D, RB>);
+    spec_status_t st = set_smem_limit((const void *)attn_kv8_simt_kernel<D, RB>, kSmem);
+    if (st != SPEC_OK) return st;
+    st = launch(attn_kv8_simt_kernel<D, RB>, dim3(P.max_splits, P.Hkv * P.n_rb, P.B), dim3(128), kSmem, s, Q);
     if (st != SPEC_OK) return st;
     st = launch(attn_kv8_combine_kernel<D>, dim3(ceil_div(P.M, 4), P.Hkv, P.B), dim3(128), 0, s, P);
     return st != SPEC_OK ? st : launch_status();
@@ -403,5 +487,6 @@ extern "C" spec_status_t spec_verify_attn_kv8(const spec_attn_desc *attn, const 
     plan.Q.scales = cache->scales;
     cudaStream_t s = as_stream(stream);
     if (plan.use_tc) return launch_attn_kv8_tc(plan.Q, s);
-    return P.d == 128 ? launch_simt8<128>(plan.Q, s) : launch_simt8<64>(plan.Q, s);
+    if (P.rb_rows == 8) return P.d == 128 ? launch_simt8<128, 8>(plan.Q, s) : launch_simt8<64, 8>(plan.Q, s);
+    return P.d == 128 ? launch_simt8<128, 32>(plan.Q, s) : launch_simt8<64, 32>(plan.Q, s);
 }
