@@ -4,7 +4,7 @@
 // O = softmax(q K^T * scale + mask) V and LSE = ln sum exp(q k * scale) with
 // K and V of the prefix read as code * scale(page, head).
 //
-// The smallest calls (two requests of 128-200 tokens) take 14 us, two
+// The smallest calls (two requests of 128-200 tokens) take 10 us, two
 // launches whose reads wait for each other (page, codes and scale, sums).
 //
 // This file holds the host planning, the CUDA-core kernel (fp32 inputs, whose
@@ -16,11 +16,12 @@
 
 #include "attn_kv8.cuh"
 #include "kv8_common.cuh"
+#include "ptx_sm103.cuh"
 
 namespace sv {
 namespace {
 
-constexpr int kCols = 64;    // columns per tile
+constexpr int kCols = 32;    // columns per tile
 
 enum { kColPrefix = 0, kColSoft = 1, kColBlock = 2 };
 
@@ -38,12 +39,15 @@ struct SimtShared {
 };
 
 // CTA (split, KV head x row block, request): a running softmax over its
-// columns, 64 at a time through shared memory.  Scores: a thread takes RB / 8
-// rows and every 16th column; O: RB / 4 (d = 128) or RB / 8 (d = 64) rows and
-// four head dimensions.  With 32 rows either product makes 5.3 fused
-// multiply-adds a thread of every shared-memory wavefront of its warp.
+// columns, 32 at a time through shared memory.  Scores: a thread takes RB / 8
+// rows and every 16th column, two dimensions to a packed fma; O: RB / 4
+// (d = 128) or RB / 8 (d = 64) rows and four head dimensions.  With 32 rows and
+// d = 128 a warp's shared-memory wavefront feeds four (scores) and five (O)
+// fused multiply-adds a thread, about what the SM does in its time; 28 rows
+// over 30 K tokens, 16 heads, take 755 us, 27 TFLOP/s (64 columns at a time,
+// half of the CTAs an SM: 15 % slower).
 template <int D, int RB>
-__global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
+__global__ void __launch_bounds__(128, (D == 128 && RB == 32 ? 4 : 1)) attn_kv8_simt_kernel(Kv8Params Q) {
     pdl_wait();
     const AttnParams &P = Q.a;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -88,16 +92,15 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
         sh.flags[tid] = p < P.M ? P.row_flags[(size_t)b * P.R + p / P.G] : 0;
     }
 
-    float m[RT], l[RT], acc[RP][4];                      // (l: of this thread's columns)
+    float m[RT], l[RT];                                  // (l: of this thread's columns)
+    uint64_t acc[RP][2];                                 // dimensions 0, 1 and 2, 3
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < RP; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+    for (int i = 0; i < RP; ++i) acc[i][0] = acc[i][1] = 0ull;
 
     const uint8_t *kv = static_cast<const uint8_t *>(P.kc);
     const int n_prefix_tiles = ceil_div(t1 - t0, kCols);
@@ -160,12 +163,17 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
             for (int it = 0; it < kPer; ++it) {
                 const int i = tid + it * 128, x = i / (kCols * VPR), j = (i / VPR) % kCols, c = i % VPR;
                 float *dst = x ? &sh.v[j][c * 16] : &sh.k[j][c * 16];
-                const uint32_t u[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
+                // its four groups from the (c / 2)-th on, so that a row's eight
+                // threads write to different banks
+                const bool r1 = (c >> 1) & 1, r2 = (c >> 2) & 1;
+                const uint32_t a0 = r1 ? w[it].y : w[it].x, a1 = r1 ? w[it].z : w[it].y;
+                const uint32_t a2 = r1 ? w[it].w : w[it].z, a3 = r1 ? w[it].x : w[it].w;
+                const uint32_t u[4] = {r2 ? a2 : a0, r2 ? a3 : a1, r2 ? a0 : a2, r2 ? a1 : a3};
                 const float f = kv8_read_scale(sc[it]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 lo = from_e4m3x2(u[e] & 0xffffu), hi = from_e4m3x2(u[e] >> 16);
-                    *reinterpret_cast<float4 *>(dst + 4 * e) =
+                    *reinterpret_cast<float4 *>(dst + 4 * ((e + (c >> 1)) & 3)) =
                         make_float4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
                 }
             }
@@ -186,28 +194,33 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
         __syncthreads();
         fetch(tile + 1);
 
+        // (sums of the even and of the odd dimensions, side by side)
+        uint64_t s2[RT][CT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) s2[i][c] = 0ull;
+#pragma unroll 4
+        for (int k = 0; k < D; k += 4) {
+            ulonglong2 kk[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) kk[c] = *reinterpret_cast<const ulonglong2 *>(&sh.k[cg + 16 * c][k]);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const ulonglong2 qq = *reinterpret_cast<const ulonglong2 *>(&sh.q[rg * RT + i][k]);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) s2[i][c] = fma2(qq.y, kk[c].y, fma2(qq.x, kk[c].x, s2[i][c]));
+            }
+        }
         float s[RT][CT];
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int c = 0; c < CT; ++c) s[i][c] = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < D; k += 4) {
-            float4 kk[CT];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) kk[c] = *reinterpret_cast<const float4 *>(&sh.k[cg + 16 * c][k]);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const float4 qq = *reinterpret_cast<const float4 *>(&sh.q[rg * RT + i][k]);
-#pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    s[i][c] = fmaf(qq.x, kk[c].x, s[i][c]);
-                    s[i][c] = fmaf(qq.y, kk[c].y, s[i][c]);
-                    s[i][c] = fmaf(qq.z, kk[c].z, s[i][c]);
-                    s[i][c] = fmaf(qq.w, kk[c].w, s[i][c]);
-                }
+            for (int c = 0; c < CT; ++c) {
+                float x, y;
+                unpair(s2[i][c], x, y);
+                s[i][c] = x + y;
             }
-        }
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const int pr = rg * RT + i;
@@ -253,8 +266,9 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
 #pragma unroll
         for (int i = 0; i < RP; ++i) {
             const float f = sh.alpha[pg * RP + i];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] *= f;
+            const uint64_t ff = pair(f, f), z = pair(-0.f, -0.f);
+            acc[i][0] = fma2(acc[i][0], ff, z);
+            acc[i][1] = fma2(acc[i][1], ff, z);
         }
         // O.  Outside the prefix, columns that a row does not see are left out:
         // their values may be anything.
@@ -262,7 +276,7 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
             constexpr bool kAll = decltype(all)::value;
 #pragma unroll 4
             for (int j = 0; j < ncols; ++j) {
-                const float4 v = *reinterpret_cast<const float4 *>(&sh.v[j][4 * dg]);
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&sh.v[j][4 * dg]);
                 float pj[RP];
                 if constexpr (RP % 4 == 0) {
 #pragma unroll
@@ -280,10 +294,9 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
 #pragma unroll
                 for (int i = 0; i < RP; ++i) {
                     if (!kAll && __float_as_int(pj[i]) == (int)0x80000000u) continue;
-                    acc[i][0] = fmaf(pj[i], v.x, acc[i][0]);
-                    acc[i][1] = fmaf(pj[i], v.y, acc[i][1]);
-                    acc[i][2] = fmaf(pj[i], v.z, acc[i][2]);
-                    acc[i][3] = fmaf(pj[i], v.w, acc[i][3]);
+                    const uint64_t pp = pair(pj[i], pj[i]);
+                    acc[i][0] = fma2(pp, v.x, acc[i][0]);
+                    acc[i][1] = fma2(pp, v.y, acc[i][1]);
                 }
             }
         };
@@ -298,8 +311,8 @@ __global__ void __launch_bounds__(128) attn_kv8_simt_kernel(Kv8Params Q) {
         if (p >= P.M) continue;
         // (a row that is not valid sees nothing, but its O may have met a NaN)
         const bool valid = (sh.flags[pr] & SPEC_ROW_VALID) != 0;
-        *reinterpret_cast<float4 *>(P.part_o + part_index(P, b, h, split, p) * D + 4 * dg) =
-            valid ? make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<ulonglong2 *>(P.part_o + part_index(P, b, h, split, p) * D + 4 * dg) =
+            valid ? make_ulonglong2(acc[i][0], acc[i][1]) : make_ulonglong2(0ull, 0ull);
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
