@@ -35,8 +35,13 @@ struct SimtShared {
     alignas(16) float p[kCols][RB + 4];    // a row's -0: the column is not seen
     float alpha[RB];                       // what the rows' O is scaled by
     uint32_t vis[RB][SPEC_MAX_ROWS / 32];
+    uint32_t any[SPEC_MAX_ROWS / 32];      // block columns that one of the rows sees
     uint8_t flags[RB];
 };
+
+// CTAs that share an SM (fewer registers a thread than the compiler takes
+// when not asked: single token 130 -> 113 us, 300 rows a head 226 -> 153 us).
+constexpr int simt_ctas(int d, int rb) { return d == 128 ? (rb == 32 ? 4 : 5) : (rb == 32 ? 5 : 8); }
 
 // CTA (split, KV head x row block, request): a running softmax over its
 // columns, 32 at a time through shared memory.  Scores: a thread takes RB / 8
@@ -47,7 +52,8 @@ struct SimtShared {
 // over 30 K tokens, 16 heads, take 755 us, 27 TFLOP/s (64 columns at a time,
 // half of the CTAs an SM: 15 % slower).
 template <int D, int RB>
-__global__ void __launch_bounds__(128, (D == 128 && RB == 32 ? 4 : 1)) attn_kv8_simt_kernel(Kv8Params Q) {
+__global__ void __launch_bounds__(128, simt_ctas(D, RB))
+attn_kv8_simt_kernel(Kv8Params Q) {
     pdl_wait();
     const AttnParams &P = Q.a;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -83,9 +89,16 @@ __global__ void __launch_bounds__(128, (D == 128 && RB == 32 ? 4 : 1)) attn_kv8_
         }
         *reinterpret_cast<float4 *>(&sh.q[i / DG][c]) = x;
     }
-    for (int i = tid; i < RB * P.W; i += 128) {
-        const int pr = i / P.W, w = i % P.W, p = row0 + pr;
-        sh.vis[pr][w] = p < P.M ? P.vis[((size_t)b * P.R + p / P.G) * P.W + w] : 0u;
+    if (last) {
+        if (tid < SPEC_MAX_ROWS / 32) sh.any[tid] = 0u;
+        __syncthreads();
+        for (int i = tid; i < RB * P.W; i += 128) {
+            const int pr = i / P.W, w = i % P.W, p = row0 + pr;
+            const uint32_t x = p < P.M ? P.vis[((size_t)b * P.R + p / P.G) * P.W + w] : 0u;
+            sh.vis[pr][w] = x;
+            if (x) atomicOr(&sh.any[w], x);
+        }
+        __syncthreads();
     }
     if (tid < RB) {
         const int p = row0 + tid;
@@ -156,6 +169,8 @@ __global__ void __launch_bounds__(128, (D == 128 && RB == 32 ? 4 : 1)) attn_kv8_
             kind = kColBlock;
             base = (tile - n_prefix_tiles - n_soft_tiles) * kCols;
             ncols = min(kCols, P.R - base);
+            static_assert(kCols == 32, "a tile's columns are a word of vis");
+            if (sh.any[base / 32] == 0u) continue;
         }
         __syncthreads();             // previous tile consumed (and q, vis, flags ready)
         if (kind == kColPrefix) {
