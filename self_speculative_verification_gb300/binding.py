@@ -449,14 +449,15 @@ def spec_future_gather(o, last_node, row_offset, out, stream=None):
 def _on(t, dtype, shape, name, dev, optional=False):
     """Device pointer of a contiguous tensor of this type and shape (None: any)
     on device `dev`, the current one, where the library launches."""
+    try:
+        if (t.get_device() == dev and (dtype is None or t.dtype is dtype) and
+                (shape is None or t.shape == shape) and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:          # not a tensor
+        pass
     if t is None and optional:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if (t.get_device() == dev and (dtype is None or t.dtype is dtype) and
-            (shape is None or t.shape == shape) and t.is_contiguous()):
-        return t.data_ptr()
-    if not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
@@ -470,9 +471,10 @@ def _on(t, dtype, shape, name, dev, optional=False):
 def _cur(stream):
     """Handle of a torch stream (None: the current one), which must belong to
     the current device, and that device's index."""
-    dev = torch.cuda.current_device()
+    # (the bare queries: torch.cuda's own take several times as long, and a
+    # Stream object ten times)
+    dev = torch._C._cuda_getDevice()
     if stream is None:
-        # (the handle alone: building a Stream object takes ten times as long)
         return torch._C._cuda_getCurrentRawStream(dev), dev
     if stream.device.index != dev:
         raise ValueError(f"stream is on {stream.device}, the current device is cuda:{dev}")
