@@ -95,6 +95,31 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
     const int j0 = blockIdx.x * P.rows, rows = min(P.Rj - j0, P.rows);
     int bits = 0;
 
+    const T *in = static_cast<const T *>(P.logits) + ((size_t)b * P.Rj + j0) * P.V + v0;
+    T *out = static_cast<T *>(P.out) + ((size_t)b * P.Rj + j0) * P.V + v0;
+    // row j's logits up to its first 16-byte boundary, and its vectors
+    auto lead_of = [&](int j) {
+        const int off = (int)((reinterpret_cast<uintptr_t>(in + (size_t)j * P.V) & 15) / sizeof(T));
+        return min(nv, off ? N - off : 0);
+    };
+    const bool vectors = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    // vector e0 of rows r0 .., the first ones ahead of everything else
+    uint4 x[kAdjFlight];
+    int at[kAdjFlight];                              // within the slice, -1 none
+    auto load = [&](int e0, int r0) {
+#pragma unroll
+        for (int f = 0; f < kAdjFlight; ++f) {
+            const int j = r0 + f;
+            at[f] = -1;
+            if (j >= rows || !vectors) continue;
+            const int first = lead_of(j) + e0 * N;
+            if (first + N > nv) continue;
+            at[f] = first;
+            x[f] = *reinterpret_cast<const uint4 *>(in + (size_t)j * P.V + first);
+        }
+    };
+    load(tid, 0);
+
     // what every thread reads, asked for at once: its node, the request's
     // factors, and the first part of the history (whose entries past its
     // length are there, but unused)
@@ -299,8 +324,6 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
         }
         return fmaf(z, !seen ? 1.f : z > 0.f ? inv_rep : rep, add);
     };
-    const T *in = static_cast<const T *>(P.logits) + ((size_t)b * P.Rj + j0) * P.V + v0;
-    T *out = static_cast<T *>(P.out) + ((size_t)b * P.Rj + j0) * P.V + v0;
     auto allowed = [&](int j, int i) {
         return s_mask[j] < 0 ||
                ((P.mask_bits[(size_t)s_mask[j] * words + ((v0 + i) >> 5)] >> ((v0 + i) & 31)) & 1u);
@@ -317,12 +340,6 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
             out[(size_t)j * P.V + i] = x;
         }
     };
-    // row j's logits up to its first 16-byte boundary, and its vectors
-    auto lead_of = [&](int j) {
-        const int off = (int)((reinterpret_cast<uintptr_t>(in + (size_t)j * P.V) & 15) / sizeof(T));
-        return min(nv, off ? N - off : 0);
-    };
-    const bool vectors = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
     if (!vectors)
         for (int i = tid; i < rows * nv; i += kAdjThreads) singles(i / nv, i % nv, 1);
     // A thread takes the same vectors in every row; where the rows begin alike
@@ -337,28 +354,22 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
             uint32_t hit = 0, old = 0, fresh = 0;
             float add[N];
             for (int r0 = 0; r0 < rows; r0 += kAdjFlight) {
-                uint4 x[kAdjFlight];
-                int at[kAdjFlight];                      // within the slice, -1 none
+                if (r0 > 0 || e0 != tid) load(e0, r0);
                 uint32_t ok[kAdjFlight];
-    #pragma unroll
+#pragma unroll
                 for (int f = 0; f < kAdjFlight; ++f) {
                     const int j = r0 + f;
-                    at[f] = -1;
                     ok[f] = kAll;
-                    if (j >= rows) continue;
-                    const int first = lead_of(j) + e0 * N;
-                    if (first + N > nv) continue;
-                    at[f] = first;
-                    x[f] = *reinterpret_cast<const uint4 *>(in + (size_t)j * P.V + first);
+                    if (at[f] < 0) continue;
                     if (s_mask[j] >= 0) {
-                        const int v = v0 + first, w = v >> 5, sft = v & 31;
+                        const int v = v0 + at[f], w = v >> 5, sft = v & 31;
                         const uint32_t *mw = P.mask_bits + (size_t)s_mask[j] * words;
                         uint64_t m = mw[w];
                         if (sft + N > 32) m |= (uint64_t)mw[w + 1] << 32;
                         ok[f] = (uint32_t)(m >> sft) & kAll;
                     }
                 }
-    #pragma unroll
+#pragma unroll
                 for (int f = 0; f < kAdjFlight; ++f) {
                     if (at[f] < 0) continue;
                     if (!kLists && at[f] != known_at) {
@@ -367,7 +378,7 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
                         if (hit) {
                             old = bits8(s_old, known_at);
                             fresh = bits8(s_new, known_at) & kAll;
-    #pragma unroll
+#pragma unroll
                             for (int q = 0; q < N; ++q) add[q] = s_add[known_at + q];
                         }
                     }
@@ -376,7 +387,7 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
                         auto known = [&](float z, int q) {
                             return fmaf(z, !((old >> q) & 1u) ? 1.f : z > 0.f ? inv_rep : rep, add[q]);
                         };
-    #pragma unroll
+#pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             if constexpr (N == 8) {
                                 const __nv_bfloat162 r = __floats2bfloat162_rn(
@@ -402,7 +413,7 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
                                 z = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y));
                                 z = q & 1 ? z << 16 : z;
                             }
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 if (k == h) e[k] = (e[k] & keep) | z;
                         }
