@@ -10,9 +10,9 @@
 // One warp writes one block: its rows come in as 16-byte vectors (a bf16 row
 // of 128 is half a warp's), the maximum is a bit-pattern maximum over the
 // warp, and they leave as 8- or 4-byte groups of codes.  Prompts of 36 K
-// tokens (8 heads of 128, bf16) take 43 us, 4.9 TB/s, bound by the ALU (57 %:
-// unpacking, maxima, run search); a commit of a few rows by its two launches
-// (5 us of GPU time).
+// tokens (8 heads of 128, bf16) take 41.6 us, 5.1 TB/s, then bound by the
+// search for runs ahead of the rows' reads and by the ALU (51 %: unpacking,
+// maxima); a commit of a few rows by its two launches (5 us of GPU time).
 #include "commit_common.cuh"
 #include "kv8.cuh"
 #include "kv8_common.cuh"

@@ -13,15 +13,16 @@
 //      occurrences on that row's path found from the ancestor bits of its
 //      node.  Up to 256 of them are listed, and their logits written over
 //      those of step 2, a thread a (token, row): done with the vectors, each
-//      warp would run the adjustment for the one lane that needs it (70 us
-//      against 63 on 480 rows of 128256 logits).  In slices with more (the
+//      warp would run the adjustment for the one lane that needs it (7 us more
+//      on 480 rows of 128256 logits).  In slices with more (the
 //      first ones: low ids are the common tokens) it is done with the vectors
 //      (11.5 us against 16 on 128 rows of 32000 logits).
 // Counts are integers and a token's biases are added in index order, so
 // results do not depend on the order of the threads.  Bound by the rows'
-// bytes, read and written once (63 us: 3.9 TB/s; without masks 51 us), then
-// by the instructions of a vector (~50 a warp) and a CTA's counting; the
-// history is read once per CTA, from L2.
+// bytes, read and written once (480 rows of 128256 logits: 57.5 us, 4.3 TB/s;
+// without masks 52 us), and by the waits of a CTA's counting, ahead of which
+// it asks for its first vectors (63 us without); the history is read once per
+// CTA, from L2.
 #include <math.h>
 
 #include <type_traits>
