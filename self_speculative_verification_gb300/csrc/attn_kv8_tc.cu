@@ -17,7 +17,7 @@
 // power-of-two scale per row, exact but for elements under 2^-9 of the row's
 // largest (there: half of e4m3's smallest step, 2^-17.8 of the largest).  P
 // is split the same way, its second part raised by 2^4 into columns of its
-// own: 2^-9 of p, as bf16 would give it, and 2^-17 of the largest p where p
+// own: 2^-9 of p, as bf16 would give it, and 2^-19 of the largest p where p
 // is small.  The two parts of Q are 2 R columns of one product, the two parts
 // of P 2 R columns of the other.
 //
@@ -57,9 +57,10 @@ using namespace tc5;
 
 constexpr int kStep = 128;                  // tokens a step
 constexpr float kTop = 8.75f;               // log2 of the largest P allowed (448 = 2^8.807)
-constexpr float kAim = 3.f;                 // log2 P of a row's maximum when M is raised: 2^5.75 of
-                                            // room before the next raise (a step with one takes
-                                            // twice as long), and P of 2^-17 of it is still held
+constexpr float kAim = 5.f;                 // log2 P of a row's maximum when M is raised: 2^3.75 of
+                                            // room before the next raise, which takes a step twice
+                                            // as long (2^1.75: tree 90 -> 98 us; 2^5.75 gains
+                                            // nothing more), and P to 2^-19 of it
 constexpr float kNoRef = -1e30f;            // M of a row that has seen nothing
 constexpr float kLoUp = 16.f;               // factor of P's second part
 

@@ -136,12 +136,17 @@ class Attn:
         args["soft_v"] = None if self.soft_v is None else np.abs(self.soft_v)
         A, _ = oracle.verify_attention(self.q, pk, [np.abs(v) for v in pv], self.kb,
                                        np.abs(self.vb), self.vis, self.valid, self.sees, **args)
+        # sum |v| over each request's columns, for every query head [B][1][Hq][d]
+        v = np.stack([np.abs(x).sum(1) for x in pv]) + np.abs(self.vb).sum(2)
+        if self.n_soft:
+            v = v + np.abs(self.soft_v).sum(1)
+        self.v_sum = np.repeat(v, self.q.shape[2] // v.shape[1], axis=1)[:, None]
         self.k_abs = max([np.abs(k).sum(-1).max() for k in pk if k.size] +
                          [np.abs(self.kb).sum(-1).max()] +
                          ([np.abs(self.soft_k).sum(-1).max()] if self.n_soft else []))
         return O, L, A
 
-    def tolerance(self, O, A):
+    def tolerance(self, O, A, v_sum):
         """Elementwise bounds on |dO| and |dLSE|.
 
         Scores: bf16 rows reach the tensor cores as the sum of two e4m3
@@ -151,11 +156,15 @@ class Attn:
         is ds = 2^-16.8 max|q| sum|k| scale.  fp32 rows: 128 products and sums
         of 2^-24 each, ds = 2^-17 max|q| sum|k| scale at most.  Each moves p
         by a factor within e^(2 ds) and LSE by ds.  P (bf16 rows) is the sum
-        of two e4m3 values as well: 2^-8 of it, or 2^-14 of the largest p
-        where it is far below that.  A block or soft-prompt value (bf16 rows)
-        is one like a query: off by at most 2^-10 / 224 = 2^-17.8 of the
-        largest of its row, which the row's weights, whose sum is 1, pass on
-        at most whole.  The output's own rounding is 2^-8 (bf16) or 2^-24
+        of two e4m3 values as well, the second raised by 2^4: it is off by
+        2^-8 of itself, or where it is small by half of the raised one's
+        smallest step, 2^-14 (or by all of itself, if that is less), under a
+        scale that keeps the row's largest P at 2^5 at least.  So a small p is
+        off by 2^-19 of the largest, which is at most the sum of all: together
+        by 2^-19 sum |v| in O, and by no more than A.  A block or soft-prompt
+        value (bf16 rows) is one like a query: off by at most 2^-10 / 224 =
+        2^-17.8 of the largest of its row, which the row's weights, whose sum
+        is 1, pass on at most whole.  The output's own rounding is 2^-8 (bf16) or 2^-24
         (fp32) of it."""
         B, R, Hq, Hkv, d = self.shape
         scale = self.scale or 1 / math.sqrt(d)
@@ -163,7 +172,8 @@ class Attn:
         if self.dtype == "bf16":
             ds = 2.0 ** -16.8 * big
             v = max([np.abs(self.vb).max()] + ([np.abs(self.soft_v).max()] if self.n_soft else []))
-            return (2.0 ** -8 * np.abs(O) + (2.0 ** -7 + 2 * ds) * A + 2.0 ** -17.8 * v + 1e-7,
+            small = np.minimum(A, 2.0 ** -19 * v_sum)
+            return (2.0 ** -8 * np.abs(O) + (2.0 ** -7 + 2 * ds) * A + small + 2.0 ** -17.8 * v + 1e-7,
                     ds + 1e-5)
         ds = 2.0 ** -17 * big
         return 2.0 ** -22 * np.abs(O) + (2 * ds + 2.0 ** -18) * A + 1e-9, ds + 2e-6
@@ -176,7 +186,7 @@ class Attn:
         got = self.o.double().cpu().numpy()[bs][:, :, hs]
         lse = self.lse.double().cpu().numpy()[bs][:, hs]
         O, A, L = O[bs][:, :, hs], A[bs][:, :, hs], L[bs][:, hs]
-        to, tl = self.tolerance(O, A)
+        to, tl = self.tolerance(O, A, self.v_sum[bs][:, :, hs])
         assert np.isfinite(got).all()
         over = np.abs(got - O) / to
         at = np.unravel_index(over.argmax(), O.shape)
