@@ -824,7 +824,8 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                             const int sl = slot0 + part >= NS ? slot0 + part - NS : slot0 + part;
                             uint4 *vr = reinterpret_cast<uint4 *>(ring + sl * C::kSlot + kv8_row(tok, 1, D));
 #pragma unroll
-                            for (int e = 0; e < D / 16; ++e) vr[e] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int e = 0; e < D / 16; ++e)        // (eight rows, eight bank groups)
+                                vr[(e + (D == 128 ? tok : tok >> 1)) & (D / 16 - 1)] = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
