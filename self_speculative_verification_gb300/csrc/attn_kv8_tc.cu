@@ -27,8 +27,8 @@
 // l adds p / v_scale.
 //
 // A persistent grid takes equal parts of the linear step space (attn_tc_sched;
-// a unit's start counted as five steps: 4600-8000 cycles by a fit over the
-// CTAs, tree 104 -> 93 us against two):
+// a unit's start counted as four steps: 2700-6800 cycles by a fit over the
+// CTAs, tree 99 -> 86 us against two):
 // a unit is a (request, KV head, block of R packed rows), its steps the prefix
 // in 128-token tiles, then the tail -- soft prompt and block, which a first
 // kernel has split into two e4m3 tiles -- in the same form, two ring slots a
@@ -1256,7 +1256,7 @@ spec_status_t launch_attn_kv8_tc(const Kv8Params &Q, cudaStream_t s) {
     T.wait = wait_limit();
     T.seg_h = Q.a.Hkv;
     T.seg_rb = w.seg_rb;
-    T.seg_cost = 5;
+    T.seg_cost = 4;
     T.pair_steps = 1;                       // a step: two of the schedule's 64-token tiles
     P.scales = Q.scales;
     P.q_meta = reinterpret_cast<const RowMeta *>(base + w.q_meta);
