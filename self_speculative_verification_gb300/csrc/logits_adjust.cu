@@ -33,7 +33,6 @@ namespace sv {
 namespace {
 
 constexpr int kAdjThreads = 256;
-constexpr int kAdjSlice = 2048;              // vocabulary tokens a CTA takes
 constexpr int kAdjRows = 16;                 // most rows a CTA takes
 constexpr int kAdjResident = 4;              // CTAs an SM holds
 constexpr int kAdjFlight = 4;                // vectors in flight a thread
@@ -55,6 +54,25 @@ struct AdjParams {
     int *status;
 };
 
+template <int kAdjSlice>
+struct AdjShared {
+    alignas(16) uint32_t cnt[kAdjSlice];     // occurrences behind the prompt
+    alignas(16) float add[kAdjSlice];        // the biases, then what a row without the token on
+                                             // its path adds
+    alignas(16) int16_t node[kAdjSlice];     // first node with the token, -1
+    uint32_t hit[kAdjSlice / 32 + 1];        // touched tokens,
+    uint32_t old[kAdjSlice / 32 + 1];        // those in the history,
+    uint32_t fresh[kAdjSlice / 32 + 1];      // and those of the draft
+    uint32_t anc[kAdjMaxNodes][kAdjMaxNodes / 32];   // path of each node
+    int draft[kAdjMaxNodes];                 // the slice's nodes in order: token within it << 16 | node
+    int mask[kAdjRows], follow[kAdjRows];    // mask and node of each row
+    float given[32];                         // biases on their way
+    int n_draft, n_list;
+    uint16_t list[kAdjListed];               // the touched tokens one after the other, where few
+    int16_t up[kAdjMaxNodes], next[kAdjMaxNodes];
+    uint8_t bad[kAdjMaxNodes];               // status bits of each node's path
+};
+
 // Bits [at, at + 8) of a bit string that has a byte behind its last.
 __device__ __forceinline__ uint32_t bits8(const uint32_t *w, int at) {
     const uint8_t *p = reinterpret_cast<const uint8_t *>(w) + (at >> 3);
@@ -70,27 +88,27 @@ __device__ __forceinline__ uint32_t byte_signs(uint32_t x) {
     return r;
 }
 
-template <typename T>
+template <typename T, int kAdjSlice>             // kAdjSlice: vocabulary tokens a CTA takes
 __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kernel(AdjParams P) {
     pdl_wait();
     constexpr int N = 16 / (int)sizeof(T);           // logits a vector
-    __shared__ __align__(16) uint32_t s_cnt[kAdjSlice];   // occurrences behind the prompt
-    __shared__ __align__(16) float s_add[kAdjSlice]; // the biases, then what a row without the
-                                                     // token on its path adds
-    __shared__ __align__(16) int16_t s_node[kAdjSlice];            // first node with the token, -1
-    __shared__ uint32_t s_hit[kAdjSlice / 32 + 1];   // touched tokens,
-    __shared__ uint32_t s_old[kAdjSlice / 32 + 1];   // those in the history,
-    __shared__ uint32_t s_new[kAdjSlice / 32 + 1];   // and those of the draft
-    __shared__ uint16_t s_list[kAdjListed];          // the touched ones one after the other,
-                                                     // where there are few
-    __shared__ int n_list;
-    __shared__ uint32_t s_anc[kAdjMaxNodes][kAdjMaxNodes / 32];   // path of each node
-    __shared__ int16_t s_up[kAdjMaxNodes], s_next[kAdjMaxNodes];
-    __shared__ uint8_t s_bad[kAdjMaxNodes];          // status bits of each node's path
-    __shared__ int s_draft[kAdjMaxNodes];            // the slice's nodes and biases, in order:
-    __shared__ int s_given[kAdjMaxBias];             // token within the slice << 16 | index
-    __shared__ int n_draft, n_given;
-    __shared__ int s_mask[kAdjRows], s_follow[kAdjRows];          // mask and node of each row
+    extern __shared__ __align__(16) uint8_t smem[];
+    auto &sh = *reinterpret_cast<AdjShared<kAdjSlice> *>(smem);
+    auto &s_cnt = sh.cnt;
+    auto &s_add = sh.add;
+    auto &s_node = sh.node;
+    auto &s_hit = sh.hit;
+    auto &s_old = sh.old;
+    auto &s_new = sh.fresh;
+    auto &s_list = sh.list;
+    auto &s_anc = sh.anc;
+    auto &s_up = sh.up;
+    auto &s_next = sh.next;
+    auto &s_bad = sh.bad;
+    auto &s_draft = sh.draft;
+    auto &s_mask = sh.mask;
+    auto &s_follow = sh.follow;
+    int &n_list = sh.n_list, &n_draft = sh.n_draft;
     const int tid = threadIdx.x, lane = tid & 31;
     const int b = blockIdx.y, v0 = blockIdx.z * kAdjSlice, nv = min(kAdjSlice, P.V - v0);
     const int j0 = blockIdx.x * P.rows, rows = min(P.Rj - j0, P.rows);
@@ -150,30 +168,28 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
         reinterpret_cast<uint2 *>(s_node)[i] = make_uint2(~0u, ~0u);
     }
     if (tid <= kAdjSlice / 32) s_hit[tid] = s_old[tid] = s_new[tid] = 0u;
-    // the entries of `ids` within the slice, in index order (one warp)
-    auto gather = [&](const int32_t *ids, int n, int *list, int *count, bool report) {
+    // the draft's tokens within the slice, in index order
+    if (tid < 32) {
+        const int32_t *ids = P.tokens + (size_t)b * P.N;
         int m = 0;
-        for (int i0 = 0; i0 < n; i0 += 128) {
-            int t[4];
+        for (int i0 = 0; i0 < P.N; i0 += 128) {
+            int x[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int i = i0 + 32 * u + lane;
-                t[u] = i < n ? ids[i] : -1;
+                x[u] = i < P.N ? ids[i] : -1;
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (report && t[u] >= P.V) bits |= SPEC_DEV_BAD_INDEX;
-                const int v = t[u] - v0;
-                const bool mine = t[u] >= 0 && v >= 0 && v < nv;
+                const int v = x[u] - v0;
+                const bool mine = x[u] >= 0 && v >= 0 && v < nv;
                 const unsigned w = __ballot_sync(0xffffffffu, mine);
-                if (mine) list[m + __popc(w & ((1u << lane) - 1u))] = v << 16 | (i0 + 32 * u + lane);
+                if (mine) s_draft[m + __popc(w & ((1u << lane) - 1u))] = v << 16 | (i0 + 32 * u + lane);
                 m += __popc(w);
             }
         }
-        if (lane == 0) *count = m;
-    };
-    if (tid < 32) gather(P.tokens + (size_t)b * P.N, P.N, s_draft, &n_draft, false);
-    else if (tid < 64) gather(P.bias_ids + (size_t)b * P.n_bias, P.n_bias, s_given, &n_given, true);
+        if (lane == 0) n_draft = m;
+    }
     for (int j = tid; j < rows; j += kAdjThreads) {
         const size_t at = (size_t)b * P.Rj + j0 + j;
         int m = P.n_masks > 0 ? P.row_mask[at] : -1;
@@ -215,18 +231,38 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
             t[u] = i < hl ? hist[i] : -1;
         }
     }
-    // the biases: the first entry of a token adds up all of them, in order
-    const float *bias = P.bias + (size_t)b * P.n_bias;
-    for (int i = tid; i < n_given; i += kAdjThreads) {
-        const int v = s_given[i] >> 16;
-        bool leads = true;
-        for (int k = 0; k < i && leads; ++k) leads = (s_given[k] >> 16) != v;
-        if (!leads) continue;
-        float x = bias[s_given[i] & 0xffff];
-        for (int k = i + 1; k < n_given; ++k)
-            if ((s_given[k] >> 16) == v) x += bias[s_given[k] & 0xffff];
-        s_add[v] = x;
-        atomicOr(&s_hit[v >> 5], 1u << (v & 31));
+    // the biases, by one warp: 32 entries after the other, the first lane of
+    // those with one token adds them up in index order
+    if (tid >= 32 && tid < 64) {
+        const int32_t *ids = P.bias_ids + (size_t)b * P.n_bias;
+        const float *bias = P.bias + (size_t)b * P.n_bias;
+        for (int i0 = 0; i0 < P.n_bias; i0 += 128) {
+            int x[4];
+            float y[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u + lane;
+                x[u] = i < P.n_bias ? ids[i] : -1;
+                y[u] = i < P.n_bias ? bias[i] : 0.f;
+                if (x[u] >= P.V) bits |= SPEC_DEV_BAD_INDEX;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int v = x[u] - v0;
+                const bool mine = x[u] >= 0 && v >= 0 && v < nv;
+                if (!__any_sync(0xffffffffu, mine)) continue;
+                sh.given[lane] = y[u];
+                unsigned peers = __match_any_sync(0xffffffffu, mine ? v : -1 - lane);
+                __syncwarp();
+                if (mine && lane == __ffs(peers) - 1) {
+                    float sum = s_add[v];
+                    for (; peers; peers &= peers - 1) sum += sh.given[__ffs(peers) - 1];
+                    s_add[v] = sum;
+                    atomicOr(&s_hit[v >> 5], 1u << (v & 31));
+                }
+                __syncwarp();
+            }
+        }
     }
     // the draft's tokens of this slice
     for (int i = tid; i < n_draft; i += kAdjThreads) {
@@ -284,18 +320,23 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
     }
     __syncthreads();
     // what the history's tokens add; the touched ones, listed by one warp
-    static_assert(kAdjSlice == 8 * kAdjThreads && kAdjSlice == 64 * 32, "eight tokens a thread, two words a lane");
-    for (uint32_t m = reinterpret_cast<const uint8_t *>(s_old)[tid]; m; m &= m - 1) {
-        const int v = 8 * tid + __ffs(m) - 1;
+    constexpr int kOwn = kAdjSlice / kAdjThreads, kWords = kAdjSlice / 1024;    // tokens a thread, words a lane
+    static_assert(kOwn == 8 || kOwn == 16, "a byte or two of s_old a thread");
+    for (uint32_t m = kOwn == 8 ? reinterpret_cast<const uint8_t *>(s_old)[tid]
+                                : reinterpret_cast<const uint16_t *>(s_old)[tid]; m; m &= m - 1) {
+        const int v = kOwn * tid + __ffs(m) - 1;
         if (s_cnt[v]) s_add[v] -= fmaf(freq, (float)s_cnt[v], pres);
     }
     if (tid < 32) {
-        const uint32_t m0 = s_hit[2 * lane] | s_old[2 * lane] | s_new[2 * lane];
-        const uint32_t m1 = s_hit[2 * lane + 1] | s_old[2 * lane + 1] | s_new[2 * lane + 1];
-        s_hit[2 * lane] = m0;
-        s_hit[2 * lane + 1] = m1;
-        uint64_t m = (uint64_t)m1 << 32 | m0;
-        const int n = __popcll(m);
+        uint32_t m[kWords];
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < kWords; ++q) {
+            const int w = kWords * lane + q;
+            m[q] = s_hit[w] | s_old[w] | s_new[w];
+            s_hit[w] = m[q];
+            n += __popc(m[q]);
+        }
         int at = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -304,8 +345,13 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
         }
         const int total = __shfl_sync(0xffffffffu, at, 31);
         if (lane == 0) n_list = total;
-        if (total <= kAdjListed)
-            for (at -= n; m; m &= m - 1) s_list[at++] = (uint16_t)(64 * lane + __ffsll(m) - 1);
+        if (total <= kAdjListed) {
+            at -= n;
+#pragma unroll
+            for (int q = 0; q < kWords; ++q)
+                for (; m[q]; m[q] &= m[q] - 1)
+                    s_list[at++] = (uint16_t)(32 * (kWords * lane + q) + __ffs(m[q]) - 1);
+        }
     }
     __syncthreads();
     const bool listed = n_list <= kAdjListed;
@@ -480,6 +526,14 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjResident) logits_adjust_kerne
     if (bits) raise_status(P.status, bits);
 }
 
+template <typename T, int kAdjSlice>
+spec_status_t launch_adjust(const AdjParams &P, dim3 grid, cudaStream_t s) {
+    constexpr size_t kSmem = sizeof(AdjShared<kAdjSlice>);
+    const spec_status_t st = set_smem_limit((const void *)logits_adjust_kernel<T, kAdjSlice>, kSmem);
+    if (st != SPEC_OK) return st;
+    return launch(logits_adjust_kernel<T, kAdjSlice>, grid, dim3(kAdjThreads), kSmem, s, P);
+}
+
 }  // namespace
 }  // namespace sv
 
@@ -526,21 +580,28 @@ extern "C" spec_status_t spec_logits_adjust(
     P.n_masks = d->n_masks;
     P.status = status_ptr();
     if (!P.status) return SPEC_ERR_CUDA;
-    // Rows a CTA: as many as leave one CTA for every place on the SMs, since
-    // each counts the request's history anew, but no more than 16: slices with
-    // many touched tokens (often the first: low ids are the common tokens) take
-    // longer, so they start first and further CTAs even them out
-    const int slices = ceil_div(P.V, kAdjSlice);
-    const long long parts = (long long)kAdjResident * num_sms() / ((long long)slices * P.B);
+    // Slices of 2048 tokens, or of 4096 for a few rows a request in more CTAs
+    // than there are places on the SMs: then the counting is the larger part
+    // (199 rows of 73557 logits: 59 us with 2048, 39 with 4096; 17 rows of
+    // 28523: 12.7 and 14.1; 60 rows a request: 58 and 69).
+    const long long places = (long long)kAdjResident * num_sms();
+    const bool wide = P.Rj <= 4 && (long long)ceil_div(P.V, 2048) * P.B > places;
+    // Rows a CTA: as many as leave one CTA for every place, since each counts
+    // the request's history anew, but no more than 16: slices with many touched
+    // tokens (often the first: low ids are the common tokens) take longer, so
+    // they start first and further CTAs even them out
+    const int slices = ceil_div(P.V, wide ? 4096 : 2048);
+    const long long parts = places / ((long long)slices * P.B);
     P.rows = ceil_div(P.Rj, (int)(parts < 1 ? 1 : parts > P.Rj ? P.Rj : parts));
     if (P.rows > kAdjRows) P.rows = kAdjRows;
     const dim3 grid(ceil_div(P.Rj, P.rows), P.B, slices);
     if (slices > 65535) return SPEC_ERR_UNSUPPORTED;
     cudaStream_t s = as_stream(stream);
-    const spec_status_t st =
-        d->logit_dtype == SPEC_BF16
-            ? launch(logits_adjust_kernel<__nv_bfloat16>, grid, dim3(kAdjThreads), 0, s, P)
-            : launch(logits_adjust_kernel<float>, grid, dim3(kAdjThreads), 0, s, P);
+    const bool bf16 = d->logit_dtype == SPEC_BF16;
+    const spec_status_t st = wide ? (bf16 ? launch_adjust<__nv_bfloat16, 4096>(P, grid, s)
+                                          : launch_adjust<float, 4096>(P, grid, s))
+                                  : (bf16 ? launch_adjust<__nv_bfloat16, 2048>(P, grid, s)
+                                          : launch_adjust<float, 2048>(P, grid, s));
     if (st != SPEC_OK) return st;
     return launch_status();
 }

@@ -245,3 +245,15 @@ def test_graph_replay():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o2, want) and bn.spec_get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kw", [dict(B=70, Rj=1, V=20000, H=600, N=2, vocab_used=900),
+                                dict(B=90, Rj=3, V=16001, H=900, N=4, nb=300, vocab_used=5000),
+                                dict(B=160, Rj=1, V=8197, H=20, N=0, nb=0, nm=1)])
+def test_few_rows_of_many_requests(kw, dtype):
+    """Decoding batches, whose calls take wider slices of the vocabulary."""
+    c = Case(seed=7, dtype=dtype, **kw)
+    c.check(c.run())
+    c.check(c.run(in_place=True))
+    assert bn.spec_get_status() == 0
