@@ -36,12 +36,13 @@
 //
 // Bound by the cache's bytes up to 32 packed rows per KV head (8 MMAs of
 // about 50 cycles against ~1400 cycles to stream a tile at d = 128): 64
-// requests of 16-32 K tokens, 8 KV heads, 32 rows take 503 us, 6.4 TB/s.  By
+// requests of 16-32 K tokens, 8 KV heads, 32 rows take 505 us, 6.4 TB/s.  By
 // the softmax's chain from 64 rows on (~2600 cycles a step), where the row
 // blocks of a head read the cache through L2: 8 requests of 256-2048 tokens
-// with 120-node trees, 480 rows a head, take 89 us, 207 TFLOP/s.  Small calls
+// with 120-node trees, 480 rows a head, take 85 us, 217 TFLOP/s.  Small calls
 // wait for the preparing kernel and the first copies, then for the combine:
-// one token over 32 K takes 26 us, over 300 tokens 17 us.
+// one token over 32 K takes 25 us, over 300 tokens 13 us; many short prefixes
+// pay a unit's chain each (1200 units of two steps: 37 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
