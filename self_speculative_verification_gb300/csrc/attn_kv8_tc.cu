@@ -36,7 +36,7 @@
 //
 // Bound by the cache's bytes up to 32 packed rows per KV head (8 MMAs of
 // about 50 cycles against ~1400 cycles to stream a tile at d = 128): 64
-// requests of 16-32 K tokens, 8 KV heads, 32 rows take 505 us, 6.4 TB/s.  By
+// requests of 16-32 K tokens, 8 KV heads, 32 rows take 497 us, 6.5 TB/s.  By
 // the softmax's chain from 64 rows on (~2600 cycles a step), where the row
 // blocks of a head read the cache through L2: 8 requests of 256-2048 tokens
 // with 120-node trees, 480 rows a head, take 85 us, 217 TFLOP/s.  Small calls
@@ -218,6 +218,16 @@ __device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32
     uint16_t l;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(d));
     lo = l;
+}
+
+// Clears token tok's value row of a slot (a function of its own: inlined it
+// costs the softmax's loop registers, 503 us instead of 497).  A row's groups are taken from the
+// (tok)-th on, so that eight rows' writes go to different banks.
+template <int D>
+__device__ __noinline__ void clear_row(uint8_t *slot, int tok) {
+    uint4 *row = reinterpret_cast<uint4 *>(slot + kv8_row(tok, 1, D));
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) row[(e + (D == 128 ? tok : tok >> 1)) & (D / 16 - 1)] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 template <int D, int RB>
@@ -821,13 +831,9 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     // V rows past the last token hold whatever the copy left: P
                     // is 0 there, but 0 x NaN is NaN
                     if (!here && row0 == 0) {
-                        for (int part = 0; part < (tail ? 2 : 1); ++part) {
-                            const int sl = slot0 + part >= NS ? slot0 + part - NS : slot0 + part;
-                            uint4 *vr = reinterpret_cast<uint4 *>(ring + sl * C::kSlot + kv8_row(tok, 1, D));
-#pragma unroll
-                            for (int e = 0; e < D / 16; ++e)        // (eight rows, eight bank groups)
-                                vr[(e + (D == 128 ? tok : tok >> 1)) & (D / 16 - 1)] = make_uint4(0u, 0u, 0u, 0u);
-                        }
+                        const int s1 = slot0 + 1 == NS ? 0 : slot0 + 1;
+                        clear_row<D>(ring + slot0 * C::kSlot, tok);
+                        if (tail) clear_row<D>(ring + s1 * C::kSlot, tok);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     fence_before();
