@@ -642,14 +642,20 @@ spec_status_t spec_verify_attn_kv8_workspace_size(const spec_attn_desc *attn,
  * and one row per request (n_rows = 1 with its own vis bit) is the
  * single-token decoding form.
  *
- * Scores, softmax statistics and sums are held in fp32.  A row that sees a
+ * Scores, softmax statistics and sums are held in fp32.  For fp32 rows so is
+ * everything else.  bf16 rows reach the tensor cores in 8-bit parts: a query,
+ * and a key or value of the block or the soft prompt, is held to 2^-17.8 of
+ * its row's largest element (values also to no less than 2^-110); a weight
+ * times its block's value scale to 2^-9 of itself, or to 2^-35 of the row's
+ * largest such product where it is below 2^-26 of it.  lse takes every weight
+ * in fp32, but for products below 2^-138 of the largest.  A row that sees a
  * block whose key scale is NaN gets o = lse = NaN, one whose value scale is
- * NaN o = NaN; so does a row that sees a block or soft-prompt row with a
- * non-finite key.  A non-finite value among those makes its seeing rows' o
- * NaN in that dimension, and leaves their other dimensions unspecified.
- * Rows that do not see such a place are not affected, and codes in slots
- * past seq_len are never used.  A seq_len outside [0, capacity] is clamped
- * and sets SPEC_DEV_SEQ_OVERFLOW; a page id outside [0, n_pages) is not read and sets
+ * NaN o = NaN; so does a row that sees a block or soft-prompt row with a non-
+ * finite key.  A non-finite value among those makes its seeing rows' o NaN in
+ * that dimension, and leaves their other dimensions unspecified.  Rows that
+ * do not see such a place are not affected, and codes in slots past seq_len
+ * are never used.  A seq_len outside [0, capacity] is clamped and sets
+ * SPEC_DEV_SEQ_OVERFLOW; a page id outside [0, n_pages) is not read and sets
  * SPEC_DEV_BAD_PAGE (the affected outputs are then unspecified).  q, kb, vb,
  * soft_k, soft_v and o must be 16-byte aligned.
  */

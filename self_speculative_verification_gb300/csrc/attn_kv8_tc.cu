@@ -11,18 +11,21 @@
 // fixed stride), and a thread of the softmax owns one token: the block's two
 // scales are a scalar each to it.
 //
-// What is not 8 bits wide is made so without loss that counts: a bf16 value
-// has 8 significant bits, an e4m3 value 4, so a query (and a block or
-// soft-prompt key or value) is the sum of two e4m3 values under one
-// power-of-two scale per row, exact but for elements under 2^-9 of the row's
-// largest (there: half of e4m3's smallest step, 2^-17.8 of the largest).  P
-// is split the same way, its second part raised by 2^4 into columns of its
-// own: 2^-9 of p, as bf16 would give it, and 2^-19 of the largest p where p
-// is small.  The two parts of Q are 2 R columns of one product, the two parts
-// of P 2 R columns of the other.
+// What is not 8 bits wide is made so.  A bf16 value has 8 significant bits, an
+// e4m3 value 4: a query (and a block or soft-prompt key or value) is the sum
+// of two e4m3 values under one power-of-two scale per row, exact but for
+// elements under 2^-9 of the row's largest (there: half of e4m3's smallest
+// step, 2^-17.8 of the largest).  P needs range more than bits, for a long
+// prefix of small weights beside a large one adds up: it is the sum of three
+// e5m2 values (3 significant bits, 30 binades of normal numbers; kind::f8f6f4
+// takes e4m3 x e5m2), the second raised by 2^3 and the third by 2^6, so that
+// what is left of a p lies in their range wherever p does.  That is p to 2^-9
+// of itself (bf16: 2^-8) down to 2^-26 of the row's largest, and to 2^-35 of
+// the largest below.  The parts of Q are columns of one product (or, at 64
+// rows, summed in it), the parts of P columns of the other.
 //
 // Softmax: p = 2^(s + log2(v_scale) - M), M per row, raised only when a value
-// would pass e4m3's 448; so the tile needs no maximum, only a vote (and
+// would pass e5m2's 57344; so the tile needs no maximum, only a vote (and
 // every row's sum is a register of each token's thread until the unit ends).
 // l adds p / v_scale.
 //
@@ -36,10 +39,10 @@
 //
 // Bound by the cache's bytes up to 32 packed rows per KV head (8 MMAs of
 // about 50 cycles against ~1400 cycles to stream a tile at d = 128): 64
-// requests of 16-32 K tokens, 8 KV heads, 32 rows take 497 us, 6.5 TB/s.  By
+// requests of 16-32 K tokens, 8 KV heads, 32 rows take 507 us, 6.4 TB/s.  By
 // the softmax's chain from 64 rows on (~2600 cycles a step), where the row
 // blocks of a head read the cache through L2: 8 requests of 256-2048 tokens
-// with 120-node trees, 480 rows a head, take 85 us, 217 TFLOP/s.  Small calls
+// with 120-node trees, 480 rows a head, take 95 us, 195 TFLOP/s.  Small calls
 // wait for the preparing kernel and the first copies, then for the combine:
 // one token over 32 K takes 25 us, over 300 tokens 13 us; many short prefixes
 // pay a unit's chain each (1200 units of two steps: 37 us).
@@ -57,13 +60,14 @@ namespace {
 using namespace tc5;
 
 constexpr int kStep = 128;                  // tokens a step
-constexpr float kTop = 8.75f;               // log2 of the largest P allowed (448 = 2^8.807)
-constexpr float kAim = 5.f;                 // log2 P of a row's maximum when M is raised: 2^3.75 of
+constexpr float kTop = 15.75f;              // log2 of the largest P allowed (57344 = 2^15.807)
+constexpr float kAim = 12.f;                // log2 P of a row's maximum when M is raised: 2^3.75 of
                                             // room before the next raise, which takes a step twice
                                             // as long (2^1.75: tree 90 -> 98 us; 2^5.75 gains
-                                            // nothing more), and P to 2^-19 of it
+                                            // nothing more), and 2^26 of P's normal range below it
 constexpr float kNoRef = -1e30f;            // M of a row that has seen nothing
-constexpr float kLoUp = 16.f;               // factor of P's second part
+constexpr int kParts = 3;                   // e5m2 values that P is the sum of,
+constexpr float kPartUp = 8.f;              // each raised by this over the one before
 
 // A unit's row, as the preparing kernel leaves it.
 struct alignas(8) RowMeta {
@@ -109,21 +113,32 @@ struct Cfg {
     static constexpr int NB = kAlt ? 4 : 3;             // S buffers: S runs ahead of the softmax
     static constexpr int kSlot = 2 * kStep * D;         // K and V of a step
     static constexpr int kQ = 2 * RB * D;               // a unit's queries, both parts
-    static constexpr int PW = kAlt ? 64 : 128;          // bytes of a token's row of P^T
-    static constexpr int kP = kStep * PW;
+    static constexpr int QB = RB == 32 ? 1 : 2;         // query buffers (32 rows: no room for two)
+    // P^T: tiles of PW columns, tokens PW bytes apart; the parts follow one
+    // another, RB columns each (up to 16 rows all of them in one tile)
+    static constexpr int PW = RB == 32 ? 32 : 64;
+    static constexpr int kPTile = kStep * PW;
+    static constexpr int kP = (RB <= 16 ? 1 : kParts) * kPTile;
+    static constexpr int PN = RB == 8 ? 32 : kParts * RB;   // columns of the product (8 rows: 24 and 8 idle)
     static constexpr int NS = (kAlt ? 6 : 4) * (128 / D);   // ring slots
-    // TMEM: O of warpgroup g at 2 RW g (first parts, then second parts), S
-    // buffer b at kColS + 2 RB b
-    static constexpr uint32_t kColS = 2 * NG * RW;
-    static constexpr int kUsed = (int)kColS + NB * 2 * RB;
-    static constexpr int kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    // the two parts of Q in columns of their own, or (64 rows, for which
+    // tensor memory has no room) as two products into the same ones
+    static constexpr bool kSumQ = RB == 64;
+    static constexpr int SN = kSumQ ? RB : 2 * RB;
+    // TMEM: part q of warpgroup g's O at O(g) + QS q, S buffer b at kColS + SN b
+    static constexpr int QS = RB;                       // (RB = RW where the groups alternate)
+    static constexpr int kOStep = kAlt ? (PN + RB) / (2 * RB) * (2 * RB) : RW;
+    static constexpr uint32_t kColS = kAlt ? 2 * kOStep : 256;
+    static constexpr int kUsed = (int)kColS + NB * SN;
+    static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    static_assert(kUsed <= 512 && kOStep >= (kAlt ? PN : RW) && PN % 16 == 0 && PN <= 256, "tensor memory");
 };
 
 template <int D, int RB>
 struct Shared8 {
     using C = Cfg<D, RB>;
     uint64_t full[C::NS], empty[C::NS];
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full[C::QB], q_empty[C::QB];
     uint64_t s_full[C::NB], s_free[C::NB];
     uint64_t p_full[2], o_upd[2];
     uint64_t drain[2];
@@ -139,10 +154,10 @@ struct Shared8 {
 template <int D, int RB>
 constexpr size_t smem8() {
     using C = Cfg<D, RB>;
-    return (size_t)C::NS * C::kSlot + 2 * C::kQ + 2 * C::kP + sizeof(Shared8<D, RB>);
+    return (size_t)C::NS * C::kSlot + C::QB * C::kQ + 2 * C::kP + sizeof(Shared8<D, RB>);
 }
 static_assert(smem8<128, 64>() <= 227 * 1024 && smem8<128, 32>() <= 227 * 1024 &&
-                  smem8<64, 64>() <= 227 * 1024,
+                  smem8<64, 64>() <= 227 * 1024 && smem8<64, 32>() <= 227 * 1024,
               "shared memory of the 8-bit attention kernel");
 
 constexpr int kAllBar = 8;               // all softmax warpgroups
@@ -206,18 +221,21 @@ __device__ __forceinline__ float warp_sums(const float (&x)[HR]) {
     return r[0];
 }
 
-// Two values of P: the e4m3 pair nearest to them, and the pair nearest to 16
-// times what it leaves (through f16, whose 11 bits leave 2^-12 of p).
-__device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32_t &lo) {
-    uint32_t pf, hf, d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pf) : "f"(p1), "f"(p0));
-    hi = e4m3x2(p0, p1);
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hf) : "h"((uint16_t)hi));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(pf), "r"(hf));
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0x4c004c00u));   // 16, 16
-    uint16_t l;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(d));
-    lo = l;
+// Two values of P as three e5m2 pairs (by way of f16, of which e5m2 is the upper
+// byte): the nearest, and the ones nearest to 8 and 64 times what is left.
+__device__ __forceinline__ void split_p(float p0, float p1, uint32_t (&part)[kParts]) {
+    uint32_t x;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(p1), "f"(p0));
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        uint16_t e;
+        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e) : "r"(x));
+        part[i] = e;
+        if (i + 1 == kParts) break;
+        // exact, both: what is left has fewer bits, and 8 times it is in range
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(__byte_perm(part[i], 0u, 0x1404)));
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0x48004800u));   // 8, 8
+    }
 }
 
 // Clears token tok's value row of a slot (a function of its own: inlined it
@@ -243,7 +261,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem;
     uint8_t *qbuf = ring + NS * C::kSlot;
-    uint8_t *pbuf = qbuf + 2 * C::kQ;
+    uint8_t *pbuf = qbuf + C::QB * C::kQ;
     auto &sh = *reinterpret_cast<Shared8<D, RB> *>(pbuf + 2 * C::kP);
 
     // (warp numbers and step counts are broadcast: the compiler then keeps what
@@ -258,9 +276,11 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < C::QB; ++b) {
             mbar_init(&sh.q_full[b], 1);
             mbar_init(&sh.q_empty[b], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.p_full[b], 4 * NR);
             mbar_init(&sh.o_upd[b], 1);
         }
@@ -363,7 +383,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         };
         Group cur = group_at(range_begin(), 0, 0), next = after(cur);
         float2 sc = scale_of(cur);
-        int slot = w, phase = 0, nq = 0, used = 0;   // used: slots filled by this warp
+        int slot = w, phase = 0, used = 0;   // used: slots filled by this warp
         static_assert(NS % 2 == 0, "a warp's slots have one parity");
         bool ok = true;
         while (cur.n > 0 && ok) {
@@ -371,23 +391,6 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             const float2 sc1 = scale_of(next);
             const float4 ts = token_scale(kv8_read_scale(sc.x), kv8_read_scale(sc.y));
             if (cur.pg == -2) raise_status(A.status, SPEC_DEV_BAD_PAGE);
-            // the unit's queries, once the unit two back is done with the buffer
-            auto queries = [&] {
-                const int qb = nq & 1;
-                if (nq >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sh.q_empty[qb],
-                                                                  (uint32_t)(((nq >> 1) - 1) & 1), T.wait)))
-                    return false;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sh.q_full[qb], C::kQ);
-                    tma_load_2d(qbuf + qb * C::kQ, &m_q, 0, unit_of(cur.c) * (2 * RB), &sh.q_full[qb], keep);
-                }
-                ++nq;
-                return true;
-            };
-            if (w == 0 && (cur.c.tile == 0 || cur.k == 0) && !queries()) {
-                ok = false;
-                break;
-            }
             const unsigned boxed = __ballot_sync(0xffffffffu, cur.pg >= 0);
             const bool tail = __shfl_sync(0xffffffffu, (int)cur.tail, 0) != 0;
             // (tail) its tile and its boxes of 16 tokens
@@ -455,11 +458,6 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     raise_status(A.status, SPEC_DEV_TIMEOUT);
                     break;
                 }
-            for (int n = nq - 1; n >= 0 && n >= nq - 2; --n)
-                if (!mbar_wait(&sh.q_full[n & 1], (uint32_t)((n >> 1) & 1))) {
-                    raise_status(A.status, SPEC_DEV_TIMEOUT);
-                    break;
-                }
         }
     } else if (n_steps > 0 && (warp == kScoreWarp || warp == kValueWarp)) {
         // ---------------------------------------------------- MMA issuers
@@ -469,29 +467,48 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         // apart, a step of 32 head dimensions 32 bytes on.  V (MN-major): the
         // same groups, 8 D further; a step of 32 tokens is four groups.  At
         // D = 64 the 128 rows of M are the 64 dimensions twice (leading
-        // offset 0).
+        // offset 0).  The first also fetches the units' queries, the next
+        // unit's while this one's first scores are computed or, with one
+        // buffer, once its last ones are.
         const bool scores = warp == kScoreWarp;
         Cursor c = range_begin();
-        constexpr uint32_t id_s = idesc_e4m3(kStep, 2 * RB, false, false);
-        constexpr uint32_t id_pv = idesc_e4m3(kStep, 2 * RB, true, true);
+        constexpr uint32_t id_s = idesc_e4m3(kStep, C::SN, false, false, false);
+        constexpr uint32_t id_pv = idesc_e4m3(kStep, C::PN, true, true, true);
         const uint64_t kd0 = smem_desc_sw<D>(smem_u32(ring), 16, 16 * D);
         const uint64_t vd0 = smem_desc_sw<D>(smem_u32(ring) + 8 * D, 0, 16 * D);
         const uint64_t qd0 = smem_desc_sw<D>(smem_u32(qbuf), 16, 8 * D);
-        const uint64_t pd0 = smem_desc_sw<C::PW>(smem_u32(pbuf), 0, 8 * C::PW);
+        const uint64_t pd0 = smem_desc_sw<C::PW>(smem_u32(pbuf), C::kPTile, 8 * C::PW);
         int nq = 0, slot = 0, phase = 0, k = 0, sb = 0, sphase = 0;
         // every lane waits and counts, lane 0 issues
         auto wait = [&](uint64_t *bar, int parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)parity, T.wait)) != 0;
         };
         bool ok = true;
+        // the queries of the unit at `at`, once the buffer's unit is done with it
+        int asked = 0;
+        auto queries = [&](const Cursor &at) {
+            const int qb = asked % C::QB, turn = asked / C::QB;
+            if (turn > 0 && !wait(&sh.q_empty[qb], (turn - 1) & 1)) return false;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sh.q_full[qb], C::kQ);
+                tma_load_2d(qbuf + qb * C::kQ, &m_q, 0, unit_of(at) * (2 * RB), &sh.q_full[qb],
+                            policy_evict_last());
+            }
+            ++asked;
+            return true;
+        };
+        if (scores) ok = queries(c);
         while (ok && k < n_steps) {
             // a unit's steps of this range
             const int k0 = k;
             const int n = __shfl_sync(0xffffffffu, min(n_steps - k, c.n_tiles - c.tile), 0);
             const int n_prefix =              // of them prefix steps
                 __shfl_sync(0xffffffffu, (c.S + kStep - 1) / kStep - c.tile, 0);
-            const int qb = nq & 1;
-            if (scores && !wait(&sh.q_full[qb], (nq >> 1) & 1)) {
+            Cursor c1 = c;                   // the next unit
+            c1.tile += n - 1;
+            cursor_next(T, c1);
+            const int qb = nq % C::QB;
+            if (scores && !wait(&sh.q_full[qb], (nq / C::QB) & 1)) {
                 ok = false;
                 break;
             }
@@ -504,7 +521,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                         ok = false;
                         break;
                     }
-                    const uint32_t ts = tmem + C::kColS + (uint32_t)(sb * 2 * RB);
+                    const uint32_t ts = tmem + C::kColS + (uint32_t)(sb * C::SN);
                     for (int part = 0; part < parts; ++part) {
                         if (!wait(&sh.full[slot], phase)) {
                             ok = false;
@@ -517,6 +534,12 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                             for (int e = 0; e < D / 32; ++e)
                                 mma8_ss(ts, kd + (uint64_t)(e * 32 >> 4), qd + (uint64_t)(e * 32 >> 4),
                                         id_s, (e > 0 || part > 0) ? 1u : 0u);
+                            if constexpr (C::kSumQ) {
+#pragma unroll
+                                for (int e = 0; e < D / 32; ++e)
+                                    mma8_ss(ts, kd + (uint64_t)(e * 32 >> 4),
+                                            qd + (uint64_t)((RB * D + e * 32) >> 4), id_s, 1u);
+                            }
                         }
                         if (++slot == NS) {
                             slot = 0;
@@ -532,13 +555,17 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                         sb = 0;
                         sphase ^= 1;
                     }
+                    if (i == (C::QB > 1 ? 0 : n - 1) && k0 + n < n_steps && !queries(c1)) {
+                        ok = false;
+                        break;
+                    }
                 } else {
                     if (!wait(&sh.p_full[b], (k >> 1) & 1)) {
                         ok = false;
                         break;
                     }
                     const uint64_t pd = pd0 + (uint64_t)((b * C::kP) >> 4);
-                    const uint32_t to = tmem + (C::kAlt ? (uint32_t)(b * 2 * RB) : 0u);
+                    const uint32_t to = tmem + (C::kAlt ? (uint32_t)(b * C::kOStep) : 0u);
                     const bool first = k - k0 < (C::kAlt ? 2 : 1);       // into its O
                     for (int part = 0; part < parts; ++part) {
                         // (met: S(k) has read the slot)
@@ -565,13 +592,15 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     if (lane == 0) commit(&sh.o_upd[b]);
                 }
             }
-            c.tile += n - 1;
-            cursor_next(T, c);
+            c = c1;
         }
         if (lane == 0) {
             if (!ok) raise_status(A.status, SPEC_DEV_TIMEOUT);
-            // every MMA issued above has completed before TMEM is released
+            // the queries asked for have landed, and every MMA issued above has completed before TMEM is released
             // (the default limit)
+            for (int q = asked - 1; q >= 0 && q >= asked - C::QB; --q)
+                if (!mbar_wait(&sh.q_full[q % C::QB], (uint32_t)((q / C::QB) & 1)))
+                    raise_status(A.status, SPEC_DEV_TIMEOUT);
             uint64_t *drain = &sh.drain[scores ? 0 : 1];
             commit(drain);
             if (!mbar_wait(drain, 0)) raise_status(A.status, SPEC_DEV_TIMEOUT);
@@ -587,6 +616,7 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         const int ga = g / NR, row0 = g % NR * RW;
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
         const uint32_t to = tmem + lane_base;          // O of both warpgroups
+        const uint32_t og = to + (uint32_t)(g * C::kOStep);    // and of this one
         Cursor c = range_begin();
         float l[RW];
         // ok: this warp's waits were met; dead: the warpgroup has stopped (it
@@ -671,31 +701,35 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     }
                     ok = __all_sync(0xffffffffu, ok);
                 }
-                const uint32_t ts = to + C::kColS + (uint32_t)(sb * 2 * RB + row0);
+                const uint32_t ts = to + C::kColS + (uint32_t)(sb * C::SN + row0);
                 float y[RW];
                 // y = s x (key scale, softmax scale) + log2(value scale) - M: the
-                // exponents of P, from the two parts of S
+                // exponents of P, from S or the two parts of it
                 auto exponents = [&] {
                     const uint64_t sk2 = pair(sc.x, sc.x), lv2 = pair(sc.y, sc.y), z = pair(0.f, 0.f);
 #pragma unroll
                     for (int i0 = 0; i0 < RW; i0 += CH) {
                         uint32_t hi[CH], lo[CH];
                         ldn<CH>(ts + i0, hi);
-                        ldn<CH>(ts + RB + i0, lo);
-                        wait_ldn<CH>(hi, lo);
+                        if constexpr (C::kSumQ) {
+                            wait_ldn<CH>(hi);
+                        } else {
+                            ldn<CH>(ts + RB + i0, lo);
+                            wait_ldn<CH>(hi, lo);
+                        }
+                        auto score = [&](int i) {
+                            const uint64_t x = pair(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1]));
+                            if constexpr (C::kSumQ) return x;
+                            else return add2(x, pair(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
+                        };
 #pragma unroll
                         for (int i = 0; i < CH; i += 4) {
                             const float4 q = *reinterpret_cast<const float4 *>(&sh.qs[g][i0 + i]);
                             const float4 m = *reinterpret_cast<const float4 *>(&sh.neg_m[g][i0 + i]);
-                            unpair(fma2(add2(pair(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
-                                             pair(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1]))),
-                                        fma2(pair(q.x, q.y), sk2, z), add2(pair(m.x, m.y), lv2)),
+                            unpair(fma2(score(i), fma2(pair(q.x, q.y), sk2, z), add2(pair(m.x, m.y), lv2)),
                                    y[i0 + i], y[i0 + i + 1]);
-                            unpair(
-                                fma2(add2(pair(__uint_as_float(hi[i + 2]), __uint_as_float(hi[i + 3])),
-                                          pair(__uint_as_float(lo[i + 2]), __uint_as_float(lo[i + 3]))),
-                                     fma2(pair(q.z, q.w), sk2, z), add2(pair(m.z, m.w), lv2)),
-                                y[i0 + i + 2], y[i0 + i + 3]);
+                            unpair(fma2(score(i + 2), fma2(pair(q.z, q.w), sk2, z), add2(pair(m.z, m.w), lv2)),
+                                   y[i0 + i + 2], y[i0 + i + 3]);
                         }
                     }
                 };
@@ -770,9 +804,9 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                             fence_after();
                             constexpr int CO = RW < 16 ? RW : 16;
 #pragma unroll 1
-                            for (int e = 0; e < 2 * RW; e += CO) {
+                            for (int e = 0; e < kParts * RW; e += CO) {
                                 uint32_t x[CO];
-                                const uint32_t at = to + (uint32_t)(g * 2 * RW + e);
+                                const uint32_t at = og + (uint32_t)(e / RW * C::QS + (e & (RW - 1)));
                                 ldn<CO>(at, x);
                                 wait_ldn<CO>(x);
 #pragma unroll
@@ -812,22 +846,36 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                     }
                 }
                 if (ok) {
-                    uint8_t *prow = pbuf + (k & 1) * C::kP + tok * C::PW;
-                    const int swz = C::PW == 128 ? tok & 7 : (tok >> 1) & 3;
-                    uint32_t w[RW / 2];                 // first parts, then second parts
+                    // 16 bytes of part q, rows 16 j ..: PW / 16 of them a tile's row,
+                    // in the order of the swizzle
+                    uint8_t *const prow = pbuf + (k & 1) * C::kP + tok * C::PW;
+                    const int swz = C::PW == 64 ? (tok >> 1) & 3 : (tok >> 2) & 1;
+                    constexpr int RJ = RW < 16 ? RW : 16;   // rows at a time
 #pragma unroll
-                    for (int i = 0; i < RW; i += 4) {
-                        uint32_t h0, l0, h1, l1;
-                        split_p(y[i], y[i + 1], h0, l0);
-                        split_p(y[i + 2], y[i + 3], h1, l1);
-                        w[i / 4] = h0 | (h1 << 16);
-                        w[RW / 4 + i / 4] = l0 | (l1 << 16);
+                    for (int j = 0; j < RW; j += RJ) {
+                        uint32_t w[kParts][RJ / 4];
+#pragma unroll
+                        for (int i = 0; i < RJ; i += 4) {
+                            uint32_t a[kParts], b[kParts];
+                            split_p(y[j + i], y[j + i + 1], a);
+                            split_p(y[j + i + 2], y[j + i + 3], b);
+#pragma unroll
+                            for (int q = 0; q < kParts; ++q) w[q][i / 4] = a[q] | (b[q] << 16);
+                        }
+                        auto at = [&](int q, int byte) {    // (byte: a multiple of 16 within the part)
+                            const int col = RB <= 16 ? q * RB + byte : byte;
+                            return prow + (RB <= 16 ? 0 : q * C::kPTile) + (((col >> 4) ^ swz) << 4);
+                        };
+                        if constexpr (RW == 8) {
+                            *reinterpret_cast<uint4 *>(at(0, 0)) = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
+                            *reinterpret_cast<uint2 *>(at(2, 0)) = make_uint2(w[2][0], w[2][1]);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < kParts; ++q)
+                                *reinterpret_cast<uint4 *>(at(q, row0 + j)) =
+                                    make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+                        }
                     }
-                    const int q0 = g % NR * (RW / 8);
-#pragma unroll
-                    for (int q = 0; q < RW / 8; ++q)
-                        *reinterpret_cast<uint4 *>(prow + (((q0 + q) ^ swz) << 4)) =
-                            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
                     // V rows past the last token hold whatever the copy left: P
                     // is 0 there, but 0 x NaN is NaN
                     if (!here && row0 == 0) {
@@ -892,42 +940,46 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
             }
             group_sync<NG * 128>(kAllBar);
             // warpgroup g writes rows (RB / NG) g ..
-            constexpr int HB = RB / NG, CE = HB < 16 ? HB : 16;
+            constexpr int HB = RB / NG, CE = HB < 8 ? HB : 8;
 #pragma unroll 1
             for (int i0 = g * HB; i0 < (g + 1) * HB; i0 += CE) {
-                uint32_t a0[CE], b0[CE], a1[CE], b1[CE];
-                const int og = i0 / RW, oi = i0 % RW;
-                ldn<CE>(to + (uint32_t)(og * 2 * RW + oi), a0);
-                ldn<CE>(to + (uint32_t)(og * 2 * RW + RW + oi), b0);
-                wait_ldn<CE>(a0, b0);
-                if constexpr (kAlt) {
-                    ldn<CE>(to + (uint32_t)(2 * RB + og * 2 * RW + oi), a1);
-                    ldn<CE>(to + (uint32_t)(2 * RB + og * 2 * RW + RW + oi), b1);
-                    wait_ldn<CE>(a1, b1);
-                }
+                const int rg = i0 / RW, oi = i0 % RW;
+                // O of rows i0 .., its parts summed
+                auto o_sum = [&](uint32_t at, float (&x)[CE]) {
+                    uint32_t a[CE], b[CE], c2[CE];
+                    ldn<CE>(at, a);
+                    ldn<CE>(at + C::QS, b);
+                    ldn<CE>(at + 2 * C::QS, c2);
+                    wait_ldn<CE>(a, b);
+                    wait_ldn<CE>(c2);
+#pragma unroll
+                    for (int i = 0; i < CE; ++i)
+                        x[i] = fmaf(fmaf(__uint_as_float(c2[i]), 1.f / kPartUp, __uint_as_float(b[i])),
+                                    1.f / kPartUp, __uint_as_float(a[i]));
+                };
+                float x[CE], x1[CE];
+                o_sum(to + (uint32_t)(kAlt ? oi : rg * C::kOStep + oi), x);
+                if constexpr (kAlt) o_sum(to + (uint32_t)(C::kOStep + oi), x1);
                 if (tok < D) {
                     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(A.o) + (size_t)seg_b * A.R * A.Hq * D + tok;
                     float *po = A.part_o + (prow + i0) * D + tok;
-                    float f0[CE], f1[CE], x[CE];
                     int out[CE];
                     // (read ahead of the stores, which the compiler keeps them behind)
 #pragma unroll
                     for (int i = 0; i < CE; i += 4) {
-                        *reinterpret_cast<float4 *>(&f0[i]) = *reinterpret_cast<const float4 *>(&sh.fac[og][oi + i]);
+                        float f0[4], f1[4];
+                        *reinterpret_cast<float4 *>(f0) = *reinterpret_cast<const float4 *>(&sh.fac[rg][oi + i]);
                         if constexpr (kAlt)
-                            *reinterpret_cast<float4 *>(&f1[i]) = *reinterpret_cast<const float4 *>(&sh.fac[(NG - 1) / NR * NR + og][oi + i]);
-                        *reinterpret_cast<int4 *>(&out[i]) = *reinterpret_cast<const int4 *>(&sh.out[og][oi + i]);
-                    }
+                            *reinterpret_cast<float4 *>(f1) =
+                                *reinterpret_cast<const float4 *>(&sh.fac[(NG - 1) / NR * NR + rg][oi + i]);
+                        *reinterpret_cast<int4 *>(&out[i]) = *reinterpret_cast<const int4 *>(&sh.out[rg][oi + i]);
 #pragma unroll
-                    for (int i = 0; i < CE; ++i) {
-                        // (a factor of 0: nothing seen, and O may hold anything)
-                        x[i] = f0[i] == 0.f ? 0.f
-                                            : f0[i] * fmaf(__uint_as_float(b0[i]), 1.f / kLoUp,
-                                                           __uint_as_float(a0[i]));
-                        if constexpr (kAlt)
-                            if (f1[i] != 0.f)
-                                x[i] = fmaf(f1[i], fmaf(__uint_as_float(b1[i]), 1.f / kLoUp,
-                                                        __uint_as_float(a1[i])), x[i]);
+                        for (int e = 0; e < 4; ++e) {
+                            // (a factor of 0: nothing seen, and O may hold anything)
+                            x[i + e] = f0[e] == 0.f ? 0.f : f0[e] * x[i + e];
+                            if constexpr (kAlt)
+                                if (f1[e] != 0.f) x[i + e] = fmaf(f1[e], x1[i + e], x[i + e]);
+                        }
                     }
                     if (seg_whole) {
 #pragma unroll
@@ -1036,7 +1088,7 @@ struct Prep8Params {
 // power-of-two scale, which is returned (NaN for a row that is not finite,
 // whose codes are 0): eight lanes a row, D / 8 values each.
 template <int D>
-__device__ float split_row(const __nv_bfloat16 *src, uint8_t *hi, uint8_t *lo, bool zero_is_small) {
+__device__ float split_row(const __nv_bfloat16 *src, uint8_t *hi, uint8_t *lo, bool value) {
     constexpr int E = D / 8;
     const int sub = threadIdx.x & 7;
     float x[E];
@@ -1056,8 +1108,10 @@ __device__ float split_row(const __nv_bfloat16 *src, uint8_t *hi, uint8_t *lo, b
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const bool bad = amax >= 0x7f800000u;
-    // 2^e: the largest value lies in (224, 448] of it
-    const int e = min(max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -110), 119);
+    // 2^e: the largest value lies in (224, 448] of it (or below: 1 / 2^e times P
+    // adds up to a row's sum, which has to stay finite)
+    const int e = min(max((int)(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0),
+                          value ? -100 : -110), 119);
     const float r = bad ? 0.f : exp2_int(-e);
     uint32_t h[E / 4], w[E / 4];
 #pragma unroll
@@ -1078,7 +1132,7 @@ __device__ float split_row(const __nv_bfloat16 *src, uint8_t *hi, uint8_t *lo, b
     }
     if (bad) return __uint_as_float(0x7fffffffu);
     // (a value row of zeros must not raise its readers' references)
-    return amax == 0 && zero_is_small ? exp2_int(kKv8MinExp) : exp2_int(e);
+    return amax == 0 && value ? exp2_int(kKv8MinExp) : exp2_int(e);
 }
 
 // Eight lanes a row: the query rows of every unit, then the tail's tokens

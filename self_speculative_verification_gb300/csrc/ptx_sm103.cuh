@@ -196,12 +196,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
     return d;
 }
 
-// The same for a tile swizzled over rows of ROW = 64 or 128 bytes.
+// The same for a tile swizzled over rows of ROW = 32, 64 or 128 bytes.
 template <int ROW>
 __device__ __forceinline__ uint64_t smem_desc_sw(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    static_assert(ROW == 64 || ROW == 128, "swizzle span");
+    static_assert(ROW == 32 || ROW == 64 || ROW == 128, "swizzle span");
     const uint64_t d = smem_desc(addr, lbo, sbo);
-    return ROW == 128 ? d : (d & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);   // 64-byte swizzle
+    constexpr uint64_t kMode = ROW == 32 ? 6 : ROW == 64 ? 4 : 2;
+    return (d & ~((uint64_t)7 << 61)) | (kMode << 61);
 }
 
 // bf16 x bf16 -> fp32, M x N; a_mn / b_mn: operand stored MN-major.
@@ -228,9 +229,9 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, 
         "l"(a), "l"(b), "r"(id), "r"(accumulate));
 }
 
-// e4m3 x e4m3 -> fp32, M x N (K = 32 an instruction)
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
-    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+// e4m3 x e4m3, or e4m3 x e5m2, -> fp32, M x N (K = 32 an instruction)
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn, bool b_e5m2) {
+    return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
