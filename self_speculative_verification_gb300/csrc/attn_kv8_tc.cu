@@ -917,12 +917,15 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 };
                 // (-M of 0: the row has seen nothing)
                 auto ref = [&](int q) { return sh.neg_m[q][ri] == 0.f ? kNoRef : -sh.neg_m[q][ri]; };
-                float M = ref(rg), L = row_sum(rg), f0 = 1.f, f1 = 0.f;
+                // What has seen nothing counts with 0 and its O is left out: a
+                // warpgroup without a step in the range has not written its own.
+                auto none_in = [&](int q) { return sh.neg_m[q][ri] == 0.f && row_sum(q) == 0.f; };
+                float M = ref(rg), L = row_sum(rg), f0 = none_in(rg) ? 0.f : 1.f, f1 = 0.f;
                 if (kAlt) {
                     const float m0 = M, m1 = ref(NR + rg);
                     M = fmaxf(m0, m1);
-                    f0 = exp2f(m0 - M);
-                    f1 = exp2f(m1 - M);
+                    f0 = none_in(rg) ? 0.f : exp2f(m0 - M);
+                    f1 = none_in(NR + rg) ? 0.f : exp2f(m1 - M);
                     L = f0 * L + f1 * row_sum(NR + rg);
                 }
                 const int out = sh.out[rg][ri];
