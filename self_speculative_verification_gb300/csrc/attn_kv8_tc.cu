@@ -917,22 +917,27 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
                 };
                 // (-M of 0: the row has seen nothing)
                 auto ref = [&](int q) { return sh.neg_m[q][ri] == 0.f ? kNoRef : -sh.neg_m[q][ri]; };
-                // What has seen nothing counts with 0 and its O is left out: a
-                // warpgroup without a step in the range has not written its own.
+                // What has seen nothing is left out: a warpgroup without a step in
+                // the range has not written its O.
                 auto none_in = [&](int q) { return sh.neg_m[q][ri] == 0.f && row_sum(q) == 0.f; };
-                float M = ref(rg), L = row_sum(rg), f0 = none_in(rg) ? 0.f : 1.f, f1 = 0.f;
+                float M = ref(rg), L = row_sum(rg), f0 = 1.f, f1 = 0.f;
                 if (kAlt) {
                     const float m0 = M, m1 = ref(NR + rg);
                     M = fmaxf(m0, m1);
-                    f0 = none_in(rg) ? 0.f : exp2f(m0 - M);
-                    f1 = none_in(NR + rg) ? 0.f : exp2f(m1 - M);
+                    f0 = exp2f(m0 - M);
+                    f1 = exp2f(m1 - M);
                     L = f0 * L + f1 * row_sum(NR + rg);
                 }
                 const int out = sh.out[rg][ri];
                 const bool none = !(out & 1) || L == 0.f;
                 const float inv = !seg_whole ? 1.f : none ? 0.f : 1.f / L;
-                sh.fac[rg][ri] = f0 * inv;
-                if (kAlt) sh.fac[(NG - 1) / NR * NR + rg][ri] = f1 * inv;
+                // (a factor that underflows still passes on a NaN: 2^-149, not 0,
+                // which leaves the O out)
+                auto factor = [&](float f, int q) {
+                    return (none && seg_whole) || none_in(q) ? 0.f : f * inv == 0.f ? 1.4e-45f : f * inv;
+                };
+                sh.fac[rg][ri] = factor(f0, rg);
+                if (kAlt) sh.fac[(NG - 1) / NR * NR + rg][ri] = factor(f1, NR + rg);
                 if (seg_whole && out >= 0) {
                     const int rr = (out >> 1) / A.Hq, hq = (out >> 1) - rr * A.Hq;
                     A.lse[((size_t)seg_b * A.Hq + hq) * A.R + rr] =

@@ -144,3 +144,19 @@ def test_block_values_of_any_size(R, G, size):
     o = a.o.double().cpu().numpy()
     assert np.all(np.abs(o - O) <= bound(a, O / size, A / size, np.abs(a.vb).max() / size) * size + 2.0 ** -110)
     assert np.abs(a.lse.double().cpu().numpy() - L).max() <= 2.0 ** -9 + 2.0 ** -12
+
+
+@pytest.mark.parametrize("R,G", ROWS)
+@pytest.mark.parametrize("B", [1, 160])
+def test_a_nan_value_scale_beside_a_far_larger_score(R, G, B):
+    """The block whose value scale is NaN has weights that underflow fp32
+    beside the first step's: 0 x NaN is NaN all the same, in a unit that one
+    CTA takes whole and in one that is cut."""
+    a = sink_call(R, 384, R, G, 128, 160.0, 0, ps=128)
+    for page in (1, 2):                      # the second step, and the third
+        keep = float(a.d_scales[int(a.table[0, page]), 0, 1])
+        a.d_scales[int(a.table[0, page]), 0, 1] = float("nan")
+        o, lse = outputs(a, B)
+        assert np.isnan(o).all() and np.isfinite(lse).all()
+        a.d_scales[int(a.table[0, page]), 0, 1] = keep
+    assert np.isfinite(outputs(a, B)[0]).all()
