@@ -370,7 +370,8 @@ spec_status_t spec_verify_attn(const spec_attn_desc *attn, const void *q,
  * child_draft_row; the first accepted child becomes the current node.  When
  * none is accepted, next_token is drawn from max(0, p - q) normalised (from
  * p when the node has no draft row or p <= q everywhere): the smallest v
- * whose cumulative mass exceeds u_sample[b] times the total (fp32 sums).
+ * whose cumulative mass exceeds u_sample[b] times the total (fp32 sums); it
+ * is -1 where that judge row's logits are all -inf.
  * max_nodes <= SPEC_MAX_ROWS (else SPEC_ERR_UNSUPPORTED).  A malformed index
  * anywhere in the tree (parent, token, judge or draft row) or a path longer
  * than path_cap sets SPEC_DEV_BAD_INDEX; the malformed node is never
@@ -556,7 +557,8 @@ spec_status_t spec_verify_attn_noalloc(const spec_attn_desc *attn, const void *q
  *
  *   logits    [n_rows][vocab] (dtype)
  *   proposal  int32 [n_rows] or NULL
- *   argmax    out int32 [n_rows]: index of the maximum, lowest on ties
+ *   argmax    out int32 [n_rows]: index of the maximum, lowest on ties; -1
+ *             for a row without a logit above -inf (its mask allows nothing)
  *   lse       out fp32 [n_rows]: ln sum_j exp(z_j)
  *   zprop     out fp32 [n_rows] (may be NULL iff proposal is NULL):
  *             z[proposal[i]]; NaN if the proposal is outside [0, vocab).
@@ -593,6 +595,8 @@ spec_status_t spec_vocab_reduce(const void *logits, int dtype, int n_rows,
  *   path = those nodes, next_token = argmax at the last node (the
  *   correction token), last_node = last node on the path.  Tree mode takes
  *   max_nodes <= SPEC_MAX_ROWS (else SPEC_ERR_UNSUPPORTED).
+ * A judge row whose argmax is -1 (no token is allowed there) accepts nothing:
+ *   the walk ends at its node or proposal, and next_token is -1.
  * path entries past acc_len are set to -1.  A path longer than path_cap or
  * an index out of range stops the walk and sets SPEC_DEV_BAD_INDEX.
  */
@@ -777,12 +781,13 @@ spec_status_t spec_page_plan(int batch, int page_size, int n_pages,
  *   z = z - frequency * n - (n > 0 ? presence : 0) + bias[v]
  *   out[v] = allowed ? z, rounded to nearest : -inf
  * (computed as z * factor + sum, the factor and the sum rounded to fp32).
- * A row whose mask allows nothing is -inf throughout.  A history, draft or
- * bias token >= vocab, a row_node or row_mask out of range, or a hist_len
- * outside [0, hist_cap] (clamped) is left out and sets SPEC_DEV_BAD_INDEX; a
- * parent that does not precede its node ends the path there and sets
- * SPEC_DEV_BAD_TREE (both for draft nodes only where a row's path meets
- * them).  One launch.
+ * A row whose mask allows nothing is -inf throughout (spec_vocab_reduce then
+ * names no token for it, and no acceptance takes one there).  A history,
+ * draft or bias token >= vocab, a row_node or row_mask out of range, or a
+ * hist_len outside [0, hist_cap] (clamped) is left out and sets
+ * SPEC_DEV_BAD_INDEX; a parent that does not precede its node ends the path
+ * there and sets SPEC_DEV_BAD_TREE (both for draft nodes only where a row's
+ * path meets them).  One launch.
  */
 spec_status_t spec_logits_adjust(const spec_logits_desc *desc, const void *logits,
                                  void *out, const int32_t *history,

@@ -144,7 +144,7 @@ vocab_reduce_kernel(const T *__restrict__ logits, int V, const int32_t *__restri
         Best r = cta_best;
         for (int i = 1; i < nc; ++i)
             r = best_merge(r, *cluster.map_shared_rank(&cta_best, i), inv_t);
-        if (argmax) argmax[row] = r.idx == INT_MAX ? 0 : r.idx;
+        if (argmax) argmax[row] = r.idx == INT_MAX ? -1 : r.idx;     // (no logit above -inf)
         lse[row] = r.m * inv_t + logf(r.s);
         if (proposal && zprop) {
             const int pidx = proposal[row];
@@ -216,7 +216,7 @@ vocab_reduce_bulk_kernel(const __nv_bfloat16 *__restrict__ logits, int V,
         Best r = cta_best;
         for (int i = 1; i < nc; ++i)
             r = best_merge(r, *cluster.map_shared_rank(&cta_best, i), inv_t);
-        if (argmax) argmax[row] = r.idx == INT_MAX ? 0 : r.idx;
+        if (argmax) argmax[row] = r.idx == INT_MAX ? -1 : r.idx;     // (no logit above -inf)
         lse[row] = r.m * inv_t + logf(r.s);
         if (proposal && zprop) {
             const int pidx = proposal[row];
@@ -279,13 +279,13 @@ __global__ void __launch_bounds__(128) accept_kernel(AcceptParams P) {
         // Node c's parent, token and judge row's argmax live in lane c % 32,
         // slot c / 32; the walk is then shuffles and ballots only.
         constexpr int kSlots = SPEC_MAX_ROWS / 32;
-        int par[kSlots], tok[kSlots], am[kSlots];   // am = -1: judge row out of range
+        int par[kSlots], tok[kSlots], am[kSlots];   // am = -1: no token, -2: judge row out of range
 #pragma unroll
         for (int k = 0; k < kSlots; ++k) {
             const int c = k * 32 + lane;
             par[k] = -3;
             tok[k] = 0;
-            am[k] = -1;
+            am[k] = -2;
             if (c < n) {
                 par[k] = P.tree_parent[(size_t)b * P.N + c];
                 tok[k] = P.tokens[(size_t)b * P.N + c];
@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(128) accept_kernel(AcceptParams P) {
 #pragma unroll
                 for (int k = 0; k < kSlots; ++k)
                     if (k == (cur >> 5)) want = __shfl_sync(0xffffffffu, am[k], cur & 31);
-                if (want < 0) {           // judge row out of range
-                    if (lane == 0) raise_status(P.status, SPEC_DEV_BAD_INDEX);
+                if (want < 0) {
+                    if (lane == 0 && want < -1) raise_status(P.status, SPEC_DEV_BAD_INDEX);
                     next = -1;
                     break;
                 }
@@ -570,7 +570,8 @@ __global__ void __launch_bounds__(kSoftThreads) soft_accept_kernel(SoftParams P)
     }
     __syncthreads();
     const int row = s_row;
-    if (row < 0) {
+    // no row, or one whose mask allows nothing: no token
+    if (row < 0 || P.lse_t[(size_t)b * P.Rj + row] == -INFINITY) {
         if (threadIdx.x == 0) P.next_token[b] = -1;
         return;
     }
