@@ -704,10 +704,13 @@ spec_status_t kv8_commit(const spec_kv8_desc *cache, int dtype, int batch, int n
  *             as spec_page_plan numbers them.
  *
  * Blocks take or raise their scales as in kv8_commit (a run of tokens that
- * begins at offset 0 begins the page).  A page named by two separate runs of
- * one call is unspecified.  A slot past the cache is skipped and sets
- * SPEC_DEV_BAD_PAGE.  page_table, batch and max_pages_per_seq of the
- * descriptor are not used.  One launch.
+ * begins at offset 0 begins the page).  So the token at offset 0 of a page
+ * that is new to its request has to be written: a run that begins behind it
+ * goes on with the scales that the page's former owner left (a larger scale
+ * stays, NaN stays NaN).  A page named by two separate runs of one call is
+ * unspecified.  A slot past the cache is skipped and sets SPEC_DEV_BAD_PAGE.
+ * page_table, batch and max_pages_per_seq of the descriptor are not used.
+ * One launch.
  */
 spec_status_t kv8_append(const spec_kv8_desc *cache, int dtype, int n_tokens,
                          const void *k, long long row_stride_k, const void *v,

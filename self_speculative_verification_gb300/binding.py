@@ -574,7 +574,8 @@ def _packed_rows(t, cache, n, name, dev):
 
 def kv8_append(cache: Kv8Desc, k, v, slot_map, stream=None):
     """Packed new tokens k, v [n][Hkv][d] (rows may be part of wider ones) into
-    the slots of slot_map int64 [n]."""
+    the slots of slot_map int64 [n] (negative: not written, which the token at
+    offset 0 of a new page has to be)."""
     st, dev = _cur(stream)
     _cache_on(cache, dev)
     n = slot_map.numel()
