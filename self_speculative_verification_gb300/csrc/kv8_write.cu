@@ -128,8 +128,9 @@ __device__ void write_block(uint8_t *tile, float *scale, int x, int first, int n
         amax = __reduce_max_sync(0xffffffffu, amax);
     }
     const float need = exp2_int(kv8_exponent(__uint_as_float(amax)));
-    const float was = first > 0 ? *scale : 0.f;
-    // a partly used block keeps the larger scale; NaN stays NaN
+    // a partly used block keeps the larger scale (the present one as readers
+    // take it, for its codes mean that); NaN stays NaN
+    const float was = first > 0 ? kv8_read_scale(*scale) : 0.f;
     const bool was_nan = was != was;
     const float s = fmaxf(was, need);                // (fmaxf drops a NaN)
     if (first > 0 && !was_nan && s > was) {

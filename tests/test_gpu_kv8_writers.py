@@ -50,3 +50,35 @@ def test_a_recycled_page_is_begun_by_its_first_token(dtype, was):
             assert np.all(gs[1] <= 2.0 ** -6)
             assert np.all(np.abs(got[1, :, 0, :14] * gs[1, :, 0, None, None] - x[6:].transpose(1, 0, 2))
                           <= 2.0 ** -4 * np.abs(x[6:].transpose(1, 0, 2)) + gs[1].max() * 2.0 ** -10)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("writer", ["append", "commit"])
+def test_scales_outside_the_readers_range(writer, d, dtype):
+    """Scales that the writers did not give count for them as for the reader:
+    below 2^-60 (0 and negative ones too) as 2^-60, above 2^60 as 2^60."""
+    rng = np.random.default_rng(4)
+    H, ps, n = 3, 32, 5
+    odd = np.array([0.0, -1.0, 2.0 ** -70, 2.0 ** 70, 2.0 ** -100, 3e38], dtype=np.float32)
+    codes, scales = random_cache(rng, len(odd), H, ps, d)
+    scales[:] = odd[:, None, None]
+    size = np.float32(2.0) ** rng.choice([-64, -60, -55, -3, 4, 50], size=(len(odd) * n, H, 1))
+    x = to_storage(rng.standard_normal((len(odd) * n, H, d)) * size, dtype)
+    at = np.concatenate([p * ps + 9 + np.arange(n) for p in range(len(odd))]).astype(np.int64)
+    kv, sc, dx = pack(codes), dev(scales), dev(x).to(torch_dt(dtype))
+    as_read = np.clip(scales.astype(np.float64), 2.0 ** -60, 2.0 ** 60)
+    if writer == "append":
+        bn.kv8_append(bn.kv8_desc(kv, sc), dx, dx, dev(at))
+    else:                                                   # every page a request with nine tokens
+        table = dev(np.arange(len(odd), dtype=np.int32)[:, None])
+        kb = dx.view(len(odd), n, H, d).transpose(1, 2).contiguous()
+        i32 = dict(dtype=torch.int32, device="cuda")
+        path = torch.arange(n, **i32).repeat(len(odd), 1)
+        seq = torch.full((len(odd),), 9, **i32)
+        bn.kv8_commit(bn.kv8_desc(kv, sc, table), kb, kb, path, torch.full_like(seq, n), seq,
+                      torch.zeros(1, **i32), torch.zeros(1, **i32))
+        assert seq.tolist() == [9 + n] * len(odd)
+    assert bn.spec_get_status() == 0
+    c, s = kv8.append(TABLE[codes], as_read, x, x, at, ps)
+    assert np.array_equal(TABLE[unpack(kv)], c) and np.array_equal(sc.double().cpu().numpy(), s)
