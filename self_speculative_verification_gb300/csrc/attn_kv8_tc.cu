@@ -379,7 +379,8 @@ attn_kv8_tc_kernel(const __grid_constant__ Tc8Params P, const __grid_constant__ 
         };
         auto scale_of = [&](const Group &g) {
             if (g.pg < 0) return make_float2(1.f, 1.f);
-            return *reinterpret_cast<const float2 *>(P.scales + ((size_t)g.pg * A.Hkv + g.c.h) * 2);
+            const float *at = P.scales + ((size_t)g.pg * A.Hkv + g.c.h) * 2;   // (4-byte aligned)
+            return make_float2(at[0], at[1]);
         };
         Group cur = group_at(range_begin(), 0, 0), next = after(cur);
         float2 sc = scale_of(cur);
