@@ -730,8 +730,10 @@ spec_status_t kv8_append(const spec_kv8_desc *cache, int dtype, int n_tokens,
  *   slot_map   int64 [n_slots] out: packed token cu_new[b] + i is token
  *              seq_len[b] + i of request b and gets page * page_size +
  *              offset; -1 behind the last token.
- *   new_len    int32 [batch] out, or NULL: seq_len + n_new (not seq_len's
- *              own array, which other threads still read).
+ *   new_len    int32 [batch] out, or NULL: seq_len + n_new.
+ *
+ * cu_new, slot_map and new_len overlap none of the other arrays, which other
+ * threads still read when they are written (else SPEC_ERR_INVALID_ARG).
  *
  * Pages are taken as kv_commit takes them.  A request that would exceed its
  * table is skipped (its slots are -1, new_len = seq_len; SPEC_DEV_CAPACITY),

@@ -235,6 +235,16 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_head_kernel(PlanParams
         *P.free_head = head + (int)tot_pages;
 }
 
+struct PlanArray {
+    const void *at;
+    size_t bytes;
+};
+
+bool overlap(const PlanArray &a, const PlanArray &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return a.bytes && b.bytes && a.at && b.at && x < y + b.bytes && y < x + a.bytes;
+}
+
 }  // namespace
 }  // namespace sv
 
@@ -250,10 +260,17 @@ extern "C" spec_status_t spec_page_plan(int batch, int page_size, int n_pages,
         return SPEC_ERR_INVALID_ARG;
     if ((long long)max_pages_per_seq * page_size > (1ll << 30)) return SPEC_ERR_UNSUPPORTED;
     if (n_slots > 0 && !slot_map) return SPEC_ERR_INVALID_ARG;
-    if (new_len && new_len == seq_len) return SPEC_ERR_INVALID_ARG;
     if (!free_head || (batch > 0 && (!seq_len || !n_new || !page_table)) ||
         (n_free > 0 && !free_pages))
         return SPEC_ERR_INVALID_ARG;
+    // outputs are written while other threads still read the inputs
+    const size_t b4 = (size_t)batch * 4;
+    const PlanArray arrays[] = {{cu_new, b4 + 4}, {slot_map, (size_t)n_slots * 8}, {new_len, b4},
+                                {seq_len, b4}, {n_new, b4}, {page_table, b4 * max_pages_per_seq},
+                                {free_pages, (size_t)n_free * 4}, {free_head, 4}};
+    for (int o = 0; o < 3; ++o)
+        for (int i = o + 1; i < (int)(sizeof(arrays) / sizeof(arrays[0])); ++i)
+            if (overlap(arrays[o], arrays[i])) return SPEC_ERR_INVALID_ARG;
     PlanParams P{};
     P.seq_len = seq_len;
     P.n_new = n_new;

@@ -1,0 +1,40 @@
+"""Host-side refusals of the page planner, the 8-bit attention and the logits
+adjustment at the ends of their arguments' ranges, without a GPU (the pointers
+are never dereferenced, and every call below is refused)."""
+
+import ctypes
+
+import pytest
+
+from self_speculative_verification_gb300 import binding as bn
+
+OK, INVALID, UNSUPPORTED, CAPACITY, CUDA = 0, 1, 2, 4, 5
+REF = ctypes.byref
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return bn.load_library()
+
+
+# arrays of a plan of 100 requests and 10000 slots, 1 MB apart
+B, SLOTS = 100, 10000
+ARRAYS = {n: 0x100000 * (i + 1) for i, n in enumerate(("seq_len", "n_new", "table", "free_pages", "free_head",
+                                                       "cu", "slots", "new_len"))}
+BYTES = dict(seq_len=4 * B, n_new=4 * B, table=4 * B * 8, free_pages=4 * 50, free_head=4, cu=4 * (B + 1),
+             slots=8 * SLOTS, new_len=4 * B)
+
+
+def plan(lib, **ptrs):
+    p = dict(ARRAYS, **ptrs)
+    return lib.spec_page_plan(B, 16, 64, 8, p["seq_len"], p["n_new"], p["table"], p["free_pages"], 50,
+                              p["free_head"], p["cu"], SLOTS, p["slots"], p["new_len"], None)
+
+
+@pytest.mark.parametrize("out,other", [(o, x) for o in ("cu", "slots", "new_len") for x in ARRAYS if x != o])
+def test_a_plan_whose_outputs_overlap_another_array(lib, out, other):
+    """Other threads still read the inputs when outputs are written."""
+    at = ARRAYS[other]
+    assert plan(lib, **{out: at}) == INVALID
+    assert plan(lib, **{out: at + BYTES[other] - 4}) == INVALID          # its last element
+    assert plan(lib, **{out: at - BYTES[out] + 4}) == INVALID            # its first one
