@@ -39,6 +39,7 @@ constexpr int kAdjFlight = 4;                // vectors in flight a thread
 constexpr int kAdjMaxNodes = SPEC_MAX_ROWS;
 constexpr int kAdjMaxBias = 1024;
 constexpr int kAdjListed = 256;              // touched tokens a slice lists
+constexpr int kAdjMaxSlices = 65535;         // (the grid's limit)
 
 struct AdjParams {
     const void *logits;
@@ -548,7 +549,8 @@ extern "C" spec_status_t spec_logits_adjust(
         d->hist_cap < 0 || d->n_bias < 0 || d->n_masks < 0)
         return SPEC_ERR_INVALID_ARG;
     if (d->logit_dtype != SPEC_F32 && d->logit_dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
-    if (d->max_nodes > kAdjMaxNodes || d->n_bias > kAdjMaxBias || d->batch > 65535)
+    if (d->max_nodes > kAdjMaxNodes || d->n_bias > kAdjMaxBias || d->batch > 65535 ||
+        d->vocab > kAdjMaxSlices * 4096)
         return SPEC_ERR_UNSUPPORTED;
     if (d->batch == 0) return SPEC_OK;
     if (!logits || !out || (d->hist_cap > 0 && (!history || !hist_len)) ||
@@ -585,17 +587,17 @@ extern "C" spec_status_t spec_logits_adjust(
     // (199 rows of 73557 logits: 59 us with 2048, 39 with 4096; 17 rows of
     // 28523: 12.7 and 14.1; 60 rows a request: 58 and 69).
     const long long places = (long long)kAdjResident * num_sms();
-    const bool wide = P.Rj <= 4 && (long long)ceil_div(P.V, 2048) * P.B > places;
+    const bool wide = P.Rj <= 4 && ceil_div_ll(P.V, 2048) * P.B > places;
     // Rows a CTA: as many as leave one CTA for every place, since each counts
     // the request's history anew, but no more than 16: slices with many touched
     // tokens (often the first: low ids are the common tokens) take longer, so
     // they start first and further CTAs even them out
-    const int slices = ceil_div(P.V, wide ? 4096 : 2048);
-    const long long parts = places / ((long long)slices * P.B);
-    P.rows = ceil_div(P.Rj, (int)(parts < 1 ? 1 : parts > P.Rj ? P.Rj : parts));
-    if (P.rows > kAdjRows) P.rows = kAdjRows;
-    const dim3 grid(ceil_div(P.Rj, P.rows), P.B, slices);
-    if (slices > 65535) return SPEC_ERR_UNSUPPORTED;
+    const long long slices = ceil_div_ll(P.V, wide ? 4096 : 2048);
+    if (slices > kAdjMaxSlices) return SPEC_ERR_UNSUPPORTED;
+    const long long parts = places / (slices * P.B);
+    const long long rows = ceil_div_ll(P.Rj, parts < 1 ? 1 : parts > P.Rj ? P.Rj : parts);
+    P.rows = (int)(rows > kAdjRows ? kAdjRows : rows);
+    const dim3 grid((unsigned)ceil_div_ll(P.Rj, P.rows), P.B, (unsigned)slices);
     cudaStream_t s = as_stream(stream);
     const bool bf16 = d->logit_dtype == SPEC_BF16;
     const spec_status_t st = wide ? (bf16 ? launch_adjust<__nv_bfloat16, 4096>(P, grid, s)

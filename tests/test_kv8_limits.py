@@ -38,3 +38,10 @@ def test_a_plan_whose_outputs_overlap_another_array(lib, out, other):
     assert plan(lib, **{out: at}) == INVALID
     assert plan(lib, **{out: at + BYTES[other] - 4}) == INVALID          # its last element
     assert plan(lib, **{out: at - BYTES[out] + 4}) == INVALID            # its first one
+
+
+@pytest.mark.parametrize("V", [65535 * 4096 + 1, (1 << 31) - 2048, (1 << 31) - 1])
+@pytest.mark.parametrize("Rj,batch", [(1, 1), (1, 4000), (1 << 30, 1)])
+def test_vocabularies_past_the_grid(lib, V, Rj, batch):
+    d = bn.logits_desc(batch, Rj, V, bn.SPEC_BF16)
+    assert lib.spec_logits_adjust(REF(d), 0x1000, 0x1000, *[None] * 14) == UNSUPPORTED
