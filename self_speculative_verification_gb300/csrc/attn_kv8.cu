@@ -421,7 +421,9 @@ spec_status_t make_plan8(const spec_attn_desc *a, const spec_kv8_desc *c, Plan8 
     P.n_rb = ceil_div(P.M, P.rb_rows);
     if ((long long)P.Hkv * P.n_rb > 65535) return SPEC_ERR_UNSUPPORTED;
     if (a->split_tokens > 0) {
-        P.chunk = a->split_tokens;
+        // (no longer than the longest prefix, rounded up to a tile)
+        const int most = (P.capacity + 63) / 64 * 64;
+        P.chunk = a->split_tokens < most ? a->split_tokens : most;
     } else {
         // about eight CTAs per SM for prefixes at half the capacity
         const long long units = (long long)P.B * P.Hkv * P.n_rb;

@@ -45,3 +45,18 @@ def test_a_plan_whose_outputs_overlap_another_array(lib, out, other):
 def test_vocabularies_past_the_grid(lib, V, Rj, batch):
     d = bn.logits_desc(batch, Rj, V, bn.SPEC_BF16)
     assert lib.spec_logits_adjust(REF(d), 0x1000, 0x1000, *[None] * 14) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("split", [1 << 30, (1 << 31) - 64])
+@pytest.mark.parametrize("pages", [4, 1 << 22])
+def test_splits_longer_than_the_cache(lib, split, pages):
+    """A split that holds every prefix is one split, whatever its length."""
+    c = bn.Kv8Desc(2, 128, 0x1000, 0x1000, 2, 1 << 23, 256, pages, 0x1000)
+
+    def size(tokens):
+        a = bn.attn_desc(2, 4, 4, 2, 128, bn.SPEC_F32, 0, split_tokens=tokens)
+        n = ctypes.c_size_t(0)
+        return lib.spec_verify_attn_kv8_workspace_size(REF(a), REF(c), REF(n)), n.value
+
+    assert size(split) == size(pages * 256)
+    assert size(split)[0] == OK and size(split)[1] > 0
