@@ -652,16 +652,21 @@ spec_status_t spec_verify_attn_kv8_workspace_size(const spec_attn_desc *attn,
  * its row's largest element (values also to no less than 2^-110); a weight
  * times its block's value scale to 2^-9 of itself, or to 2^-35 of the row's
  * largest such product where it is below 2^-26 of it.  lse takes every weight
- * in fp32, but for products below 2^-138 of the largest.  A row that sees a
- * block whose key scale is NaN gets o = lse = NaN, one whose value scale is
- * NaN o = NaN; so does a row that sees a block or soft-prompt row with a non-
- * finite key.  A non-finite value among those makes its seeing rows' o NaN in
- * that dimension, and leaves their other dimensions unspecified.  Rows that
- * do not see such a place are not affected, and codes in slots past seq_len
- * are never used.  A seq_len outside [0, capacity] is clamped and sets
- * SPEC_DEV_SEQ_OVERFLOW; a page id outside [0, n_pages) is not read and sets
- * SPEC_DEV_BAD_PAGE (the affected outputs are then unspecified).  q, kb, vb,
- * soft_k, soft_v and o must be 16-byte aligned.
+ * in fp32, but for products below 2^-138 of the largest.
+ *
+ * A row that sees a block whose key scale is NaN gets o = lse = NaN, one
+ * whose value scale is NaN o = NaN.  For bf16 rows a non-finite query gives o
+ * = lse = NaN, and so does a visible block or soft-prompt row with a
+ * non-finite key; one with a non-finite value gives o = NaN.  For fp32 rows
+ * these are what the arithmetic gives: a score of +inf or NaN makes o = lse =
+ * NaN, one of -inf has weight 0, a non-finite value reaches its own dimension
+ * of o.  Rows that do not see such a place are not affected, and codes in
+ * slots past seq_len are never used.
+ *
+ * A seq_len outside [0, capacity] is clamped and sets SPEC_DEV_SEQ_OVERFLOW;
+ * a page id outside [0, n_pages) is not read and sets SPEC_DEV_BAD_PAGE (the
+ * affected outputs are then unspecified).  q, kb, vb, soft_k, soft_v and o
+ * must be 16-byte aligned.
  */
 spec_status_t spec_verify_attn_kv8(const spec_attn_desc *attn, const void *q,
                                    const spec_kv8_desc *cache, const void *kb,
