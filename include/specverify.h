@@ -666,7 +666,8 @@ spec_status_t spec_verify_attn_kv8_workspace_size(const spec_attn_desc *attn,
  * A seq_len outside [0, capacity] is clamped and sets SPEC_DEV_SEQ_OVERFLOW;
  * a page id outside [0, n_pages) is not read and sets SPEC_DEV_BAD_PAGE (the
  * affected outputs are then unspecified).  q, kb, vb, soft_k, soft_v and o
- * must be 16-byte aligned.
+ * must be 16-byte aligned.  Calls that can overlap on the GPU (captured ones
+ * too) take workspaces of their own.
  */
 spec_status_t spec_verify_attn_kv8(const spec_attn_desc *attn, const void *q,
                                    const spec_kv8_desc *cache, const void *kb,

@@ -49,7 +49,7 @@ constexpr int simt_ctas(int d, int rb) { return d == 128 ? (rb == 32 ? 4 : 5) : 
 // (d = 128) or RB / 8 (d = 64) rows and four head dimensions.  With 32 rows and
 // d = 128 a warp's shared-memory wavefront feeds four (scores) and five (O)
 // fused multiply-adds a thread, about what the SM does in its time; 28 rows
-// over 30 K tokens, 16 heads, take 755 us, 27 TFLOP/s (64 columns at a time,
+// over 30 K tokens, 16 heads, take 762 us, 27 TFLOP/s (64 columns at a time,
 // half of the CTAs an SM: 15 % slower).
 template <int D, int RB>
 __global__ void __launch_bounds__(128, simt_ctas(D, RB))

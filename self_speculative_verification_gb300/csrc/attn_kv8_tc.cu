@@ -2,7 +2,7 @@
 //
 // The cache's codes go to the tensor cores as they are: a step takes 128
 // tokens of one (request, KV head) and computes, with kind::f8f6f4 (e4m3 x
-// e4m3 -> fp32),
+// e4m3 and e4m3 x e5m2, fp32 sums),
 //   S^T [128 tokens x rows] = K (A, K-major) . Q^T (B),
 //   O^T [head dims x rows] += V^T (A, MN-major) . P^T (B, MN-major),
 // so the keys and values are the M = 128 operands whatever the number of
@@ -30,8 +30,8 @@
 // l adds p / v_scale.
 //
 // A persistent grid takes equal parts of the linear step space (attn_tc_sched;
-// a unit's start counted as four steps: 2700-6800 cycles by a fit over the
-// CTAs, tree 99 -> 86 us against two):
+// a unit's start counted as four steps, 2700-6800 cycles by a fit over the
+// CTAs: tree 96 us, 100 with two and 98 with six):
 // a unit is a (request, KV head, block of R packed rows), its steps the prefix
 // in 128-token tiles, then the tail -- soft prompt and block, which a first
 // kernel has split into two e4m3 tiles -- in the same form, two ring slots a
@@ -39,12 +39,12 @@
 //
 // Bound by the cache's bytes up to 32 packed rows per KV head (8 MMAs of
 // about 50 cycles against ~1400 cycles to stream a tile at d = 128): 64
-// requests of 16-32 K tokens, 8 KV heads, 32 rows take 507 us, 6.4 TB/s.  By
-// the softmax's chain from 64 rows on (~2600 cycles a step), where the row
+// requests of 16-32 K tokens, 8 KV heads, 32 rows take 508 us, 6.4 TB/s.  By
+// the softmax's chain from 64 rows on (~2900 cycles a step), where the row
 // blocks of a head read the cache through L2: 8 requests of 256-2048 tokens
 // with 120-node trees, 480 rows a head, take 95 us, 195 TFLOP/s.  Small calls
 // wait for the preparing kernel and the first copies, then for the combine:
-// one token over 32 K takes 25 us, over 300 tokens 13 us; many short prefixes
+// one token over 32 K takes 21 us, over 300 tokens 12 us; many short prefixes
 // pay a unit's chain each (1200 units of two steps: 37 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -63,8 +63,8 @@ constexpr int kStep = 128;                  // tokens a step
 constexpr float kTop = 15.75f;              // log2 of the largest P allowed (57344 = 2^15.807)
 constexpr float kAim = 12.f;                // log2 P of a row's maximum when M is raised: 2^3.75 of
                                             // room before the next raise, which takes a step twice
-                                            // as long (2^1.75: tree 90 -> 98 us; 2^5.75 gains
-                                            // nothing more), and 2^26 of P's normal range below it
+                                            // as long (2^1.75: tree 96 -> 109 us; 2^5.75 gains
+                                            // nothing), and 2^26 of P's normal range below it
 constexpr float kNoRef = -1e30f;            // M of a row that has seen nothing
 constexpr int kParts = 3;                   // e5m2 values that P is the sum of,
 constexpr float kPartUp = 8.f;              // each raised by this over the one before
@@ -100,7 +100,8 @@ struct Tc8Params {
 // the unit's end: a step's chain (wait, tensor memory, vote, exponentials, P,
 // arrive: ~2000 cycles, most of it latency) then costs half.  With 64 rows, whose
 // arithmetic is the larger part, they take half of the rows of every step (four
-// with a quarter each repeat what a step costs a thread: tree 105 -> 111 us).
+// with a quarter each repeat what a step costs a thread: tree 105 -> 111 us,
+// with P in two parts).
 template <int D, int RB>
 struct Cfg {
     static constexpr bool kAlt = RB <= 32;
@@ -238,9 +239,9 @@ __device__ __forceinline__ void split_p(float p0, float p1, uint32_t (&part)[kPa
     }
 }
 
-// Clears token tok's value row of a slot (a function of its own: inlined it
-// costs the softmax's loop registers, 503 us instead of 497).  A row's groups are taken from the
-// (tok)-th on, so that eight rows' writes go to different banks.
+// Clears token tok's value row of a slot (a function of its own: inlined, tree
+// 96.3 -> 97.6 us, short prefixes 39.1 -> 38.3).  A row's groups are taken from
+// the (tok)-th on, so that eight rows' writes go to different banks.
 template <int D>
 __device__ __noinline__ void clear_row(uint8_t *slot, int tok) {
     uint4 *row = reinterpret_cast<uint4 *>(slot + kv8_row(tok, 1, D));

@@ -10,9 +10,11 @@
 // One warp writes one block: its rows come in as 16-byte vectors (a bf16 row
 // of 128 is half a warp's), the maximum is a bit-pattern maximum over the
 // warp, and they leave as 8- or 4-byte groups of codes.  Prompts of 36 K
-// tokens (8 heads of 128, bf16) take 41.6 us, 5.1 TB/s, then bound by the
-// search for runs ahead of the rows' reads and by the ALU (51 %: unpacking,
-// maxima); a commit of a few rows by its two launches (5 us of GPU time).
+// tokens (8 heads of 128) take 41.5 us in bf16, 5.1 TB/s, and 74.6 in fp32, 4.7
+// TB/s, bound by the search for runs ahead of the rows' reads and by the ALU
+// (bf16: 51 %, unpacking and maxima); a commit is bound by its two launches and
+// their dependent reads (8 rows of 16 requests, 32 heads: 6.7 us of GPU time;
+// up to 24 fp32 rows of 64 requests, 8 heads: 11.8, bf16 9.0).
 #include "commit_common.cuh"
 #include "kv8.cuh"
 #include "kv8_common.cuh"

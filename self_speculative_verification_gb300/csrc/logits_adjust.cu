@@ -19,8 +19,8 @@
 //      (11.5 us against 16 on 128 rows of 32000 logits).
 // Counts are integers and a token's biases are added in index order, so
 // results do not depend on the order of the threads.  Bound by the rows'
-// bytes, read and written once (480 rows of 128256 logits: 57 us, 4.3 TB/s;
-// without masks 52 us), and by the waits of a CTA's counting, ahead of which
+// bytes, read and written once (480 rows of 128256 logits: 57 us in bf16, 4.3
+// TB/s, without masks 52; 99 us in fp32, 5.0 TB/s), and by the waits of a CTA's counting, ahead of which
 // it asks for its first vectors (63 us without); the history is read once per
 // CTA, from L2.
 #include <math.h>
