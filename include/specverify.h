@@ -20,7 +20,10 @@
  * spec_verify_attn_kv8 attends over it, kv8_commit and kv8_append write it,
  * spec_page_plan builds block tables and slot maps from request lengths --
  * and spec_logits_adjust (penalties, biases and grammar masks ahead of the
- * acceptance).  The pages have no counterpart of these.
+ * acceptance).  A prompt, or a chunk of one, passes through spec_page_plan,
+ * spec_rope (rotary positions), kv_append or kv8_append (its keys and values
+ * into either cache) and spec_chunk_attn or spec_chunk_attn_kv8 (its attention
+ * over what the cache then holds).  The pages have no counterpart of these.
  *
  * Sources, cited by page title and section / equation:
  *   [LA]  "Lookahead Attention: Self-Speculative Verification via Parallel
@@ -270,6 +273,38 @@ typedef struct spec_logits_desc {
     int n_bias;         /* row length of bias_ids / bias (<= 1024); 0 = none */
     int n_masks;        /* grammar masks; 0 = none */
 } spec_logits_desc;
+
+/* Shape of one chunk attention call: a packed batch of new tokens. */
+typedef struct spec_chunk_desc {
+    int batch;         /* B: requests */
+    int n_tokens;      /* rows of q, o and lse; the requests' new tokens fill the first */
+    int n_q_heads;     /* Hq (multiple of n_kv_heads, at most 128 times as many) */
+    int n_kv_heads;    /* Hkv */
+    int head_dim;      /* d: 64 or 128 */
+    int dtype;         /* SPEC_BF16 or SPEC_F32, for q, o and a cache of rows */
+    float scale;       /* softmax scale; 0 -> 1/sqrt(head_dim) */
+} spec_chunk_desc;
+
+/* rotary layouts: which elements of a head make pair i */
+#define SPEC_ROPE_PAIRS  0  /* 2i and 2i + 1 */
+#define SPEC_ROPE_HALVES 1  /* i and i + rot_dim / 2 */
+
+/* rotary frequencies (spec_rope_freqs) */
+#define SPEC_ROPE_PLAIN  0
+#define SPEC_ROPE_LINEAR 1
+#define SPEC_ROPE_RAMP   2
+
+/* Shape of one rotary position call. */
+typedef struct spec_rope_desc {
+    int n_tokens;      /* rows of q and k */
+    int n_q_heads;     /* query heads; 0 = none */
+    int n_k_heads;     /* key heads; 0 = none */
+    int head_dim;      /* d: a multiple of 8, <= 256 */
+    int rot_dim;       /* even, <= head_dim: the first elements of a head, which turn */
+    int layout;        /* SPEC_ROPE_PAIRS or SPEC_ROPE_HALVES */
+    int dtype;         /* SPEC_BF16 or SPEC_F32 */
+    float attention;   /* factor on what turns; 0 -> 1 */
+} spec_rope_desc;
 
 /* Library version (SPECVERIFY_VERSION). */
 int spec_version(void);
@@ -809,6 +844,144 @@ spec_status_t spec_logits_adjust(const spec_logits_desc *desc, const void *logit
                                  const int32_t *bias_ids, const float *bias,
                                  const uint32_t *mask_bits, const int32_t *row_mask,
                                  void *stream);
+
+/*
+ * spec_rope_freqs -- rotary frequencies, in radians a position, for spec_rope:
+ * freqs (HOST, double [rot_dim / 2]), f_i = base^(-2i / rot_dim), and
+ *   SPEC_ROPE_PLAIN   f_i;
+ *   SPEC_ROPE_LINEAR  f_i / factor (factor > 0);
+ *   SPEC_ROPE_RAMP    f_i (w + (1 - w) / factor), w = (t - low) / (high - low)
+ *                     within [0, 1], t = trained_len f_i / 2 pi the turns that
+ *                     pair i makes over the trained length: fast pairs stay,
+ *                     slow ones are stretched (trained_len > 0, low < high).
+ * rot_dim is even, <= 256; arguments that a kind does not name are not looked
+ * at.  Runs on the host.
+ */
+spec_status_t spec_rope_freqs(int rot_dim, double base, int scaling, double factor,
+                              double trained_len, double low, double high, double *freqs);
+
+/*
+ * spec_rope -- rotary positions of queries and keys, ahead of kv_append /
+ * kv8_append and the attention calls, which take rows that have them.
+ *
+ *   freqs     HOST double [rot_dim / 2], radians a position, finite (from
+ *             spec_rope_freqs, or any other); read before the call returns.
+ *   q, q_out  (dtype) token i's row of query head h begins at element i *
+ *             row_stride + h * head_dim; rows of a stride >= n_q_heads *
+ *             head_dim (they may lie inside wider ones, such as a joint
+ *             projection's output), on 16-byte boundaries.  q_out may be q
+ *             itself, with its stride.  k, k_out likewise.
+ *   positions int32 [n_tokens]: each row's position; a row with a negative one
+ *             is left as it is (its output not written).  Or NULL, and
+ *   seq_len   int32 [batch], cu_new int32 [batch + 1], as in spec_page_plan:
+ *             packed token cu_new[b] + i has position seq_len[b] + i; rows that
+ *             belong to no request are left as they are.
+ *
+ * Pair i of a head, (x, y), becomes attention * (x cos t - y sin t, y cos t + x
+ * sin t), t = position * freqs[i]; elements from rot_dim on are copied.  The
+ * angle is held to 2^-24 of a half turn at any position (a frequency to 2^-53
+ * of itself), products and sums are fp32, rounded once to dtype.  What a call
+ * writes must not meet anything else that it reads or writes
+ * (SPEC_ERR_INVALID_ARG; rows of unlike strides are told apart by the spans of
+ * memory that they reach over).  A cu_new that decreases or leaves [0,
+ * n_tokens] sets SPEC_DEV_BAD_INDEX (which rows are turned is then
+ * unspecified), a negative seq_len SPEC_DEV_SEQ_OVERFLOW (its rows are left as
+ * they are).  One launch.
+ */
+spec_status_t spec_rope(const spec_rope_desc *desc, const double *freqs, const void *q,
+                        long long row_stride_q, void *q_out, long long row_stride_q_out,
+                        const void *k, long long row_stride_k, void *k_out,
+                        long long row_stride_k_out, const int32_t *positions, int batch,
+                        const int32_t *seq_len, const int32_t *cu_new, void *stream);
+
+/*
+ * kv_append -- kv8_append for a cache of rows: writes a packed batch of new
+ * tokens into their slots.
+ *
+ *   k, v      (the cache's dtype) token i's row of KV head h begins at element
+ *             i * row_stride + h * head_dim; row_stride >= n_kv_heads *
+ *             head_dim; rows on 16-byte boundaries, as is the cache.
+ *   slot_map  int64 [n_tokens]: page * page_size + offset (from
+ *             spec_page_plan), or request * max_seq + token for a contiguous
+ *             cache; < 0 for a token that is not written.
+ *
+ * A slot past the cache is skipped and sets SPEC_DEV_BAD_PAGE; of tokens with
+ * the same slot, which one is kept is unspecified, element by element.  k and
+ * v must not overlap the cache.  page_table and max_pages_per_seq of the
+ * descriptor are not used.  One launch.
+ */
+spec_status_t kv_append(const spec_kv_desc *cache, int n_tokens, const void *k,
+                        long long row_stride_k, const void *v, long long row_stride_v,
+                        const int64_t *slot_map, void *stream);
+
+/* Bytes of workspace spec_chunk_attn needs for this shape and cache; they do
+ * not depend on n_tokens or on the cache's size. */
+spec_status_t spec_chunk_attn_workspace_size(const spec_chunk_desc *desc,
+                                             const spec_kv_desc *cache, size_t *bytes);
+
+/*
+ * spec_chunk_attn -- attention of new tokens that the cache already holds
+ * (kv_append): each sees its request's tokens up to itself.  Prompts, chunks of
+ * prompts and single tokens, in one call.
+ *
+ *   q         (dtype) token i's row of query head h begins at element i *
+ *             row_stride_q + h * head_dim; row_stride_q >= n_q_heads *
+ *             head_dim; rows on 16-byte boundaries.
+ *   cache     of the same dtype, paged or contiguous.
+ *   seq_len   int32 [batch]: tokens each request held before the new ones.
+ *   cu_new    int32 [batch + 1]: first packed token of each request, as
+ *             spec_page_plan writes it: request b's new tokens are rows
+ *             cu_new[b] .. cu_new[b + 1] - 1 (none, if equal).
+ *   o         out (dtype) [n_tokens][n_q_heads][head_dim], 16-byte aligned; it
+ *             must not overlap q.
+ *   lse       out fp32 [n_tokens][n_q_heads]: natural-log log-sum-exp of the
+ *             row's scaled scores.
+ *   workspace device scratch of >= spec_chunk_attn_workspace_size bytes,
+ *             256-byte aligned; its contents on entry are ignored.
+ *
+ * New token i of request b sees cache tokens 0 .. seq_len[b] + i; for query
+ * head h the K/V head is h / (n_q_heads / n_kv_heads); scores are (q . k) *
+ * scale.  Scores, softmax statistics and sums are held in fp32; for bf16 rows a
+ * weight is rounded to bf16 (half a step: 2^-8 of itself) before its product
+ * with the value.  Rows of o and lse that belong to no request are left as they were.
+ *
+ * A row that sees a non-finite key or has a non-finite query gets o = lse =
+ * NaN where a score is +inf or NaN (-inf has weight 0; a row with no other
+ * score gets o = 0, lse = -inf); one that sees a non-finite value gets o
+ * non-finite in the value's dimension, and may in all.  Rows that do not see
+ * such a place are not affected, and slots past a request's last new token are
+ * never used.
+ *
+ * A request whose cu_new decreases or leaves [0, n_tokens] is skipped and sets
+ * SPEC_DEV_BAD_INDEX, one whose seq_len is negative or whose last new token
+ * lies past the capacity SPEC_DEV_SEQ_OVERFLOW (their rows are left as they
+ * were); a page id outside [0, n_pages) is not read and sets SPEC_DEV_BAD_PAGE
+ * (the affected outputs are then unspecified).  Calls that can overlap on the
+ * GPU (captured ones too) take workspaces of their own.  Two launches.
+ */
+spec_status_t spec_chunk_attn(const spec_chunk_desc *desc, const void *q,
+                              long long row_stride_q, const spec_kv_desc *cache,
+                              const int32_t *seq_len, const int32_t *cu_new, void *o,
+                              float *lse, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/* Bytes of workspace spec_chunk_attn_kv8 needs for this shape and cache. */
+spec_status_t spec_chunk_attn_kv8_workspace_size(const spec_chunk_desc *desc,
+                                                 const spec_kv8_desc *cache, size_t *bytes);
+
+/*
+ * spec_chunk_attn_kv8 -- spec_chunk_attn over a cache held in 8 bits
+ * (kv8_append): the new tokens too are attended as the cache holds them.  q and
+ * o have desc->dtype.  For bf16 rows an element counts as code * scale rounded
+ * to bf16, which is exact for the powers of two that the writers give.  A row
+ * that sees a block whose key scale is NaN gets o = lse = NaN, one whose value
+ * scale is NaN o = NaN.
+ */
+spec_status_t spec_chunk_attn_kv8(const spec_chunk_desc *desc, const void *q,
+                                  long long row_stride_q, const spec_kv8_desc *cache,
+                                  const int32_t *seq_len, const int32_t *cu_new, void *o,
+                                  float *lse, void *workspace, size_t workspace_bytes,
+                                  void *stream);
 
 /*
  * spec_set_wait_limit -- limit, in SM clock cycles, of the internal pipeline

@@ -22,3 +22,4 @@ from .specverify_oracle import (  # noqa: F401
     kv_commit_contiguous, kv_commit_paged,
 )
 from . import kv8_oracle as kv8  # noqa: F401,E402
+from . import chunk_oracle as chunk  # noqa: F401,E402

@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int, c_longlong, c_size_t, c_void_p
 
 import torch
 
@@ -33,6 +33,11 @@ SPEC_ACCEPT_THRESH_CHAIN = 0
 SPEC_ACCEPT_GREEDY_TREE = 1
 SPEC_ROW_VALID = 1
 SPEC_ROW_SEES_SOFT = 2
+SPEC_ROPE_PAIRS = 0
+SPEC_ROPE_HALVES = 1
+SPEC_ROPE_PLAIN = 0
+SPEC_ROPE_LINEAR = 1
+SPEC_ROPE_RAMP = 2
 SPEC_DEV_BAD_TREE = 0x01
 SPEC_DEV_BAD_PAGE = 0x02
 SPEC_DEV_SEQ_OVERFLOW = 0x04
@@ -46,7 +51,9 @@ EXPORTS = ("spec_version", "spec_status_string", "spec_mask_build",
            "spec_get_status", "spec_la_prefill_attn", "spec_accept_soft", "spec_draft_tree",
            "spec_prune_tree", "spec_stream_rotate_values", "spec_future_gather",
            "spec_set_wait_limit", "spec_verify_attn_kv8_workspace_size", "spec_verify_attn_kv8",
-           "kv8_commit", "kv8_append", "spec_page_plan", "spec_logits_adjust")
+           "kv8_commit", "kv8_append", "spec_page_plan", "spec_logits_adjust", "spec_rope_freqs",
+           "spec_rope", "kv_append", "spec_chunk_attn_workspace_size", "spec_chunk_attn",
+           "spec_chunk_attn_kv8_workspace_size", "spec_chunk_attn_kv8")
 SPEC_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -117,6 +124,17 @@ class LogitsDesc(ctypes.Structure):
                 ("n_bias", c_int), ("n_masks", c_int)]
 
 
+class ChunkDesc(ctypes.Structure):
+    _fields_ = [("batch", c_int), ("n_tokens", c_int), ("n_q_heads", c_int),
+                ("n_kv_heads", c_int), ("head_dim", c_int), ("dtype", c_int), ("scale", c_float)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("n_tokens", c_int), ("n_q_heads", c_int), ("n_k_heads", c_int),
+                ("head_dim", c_int), ("rot_dim", c_int), ("layout", c_int), ("dtype", c_int),
+                ("attention", c_float)]
+
+
 _lib = None
 
 
@@ -169,6 +187,18 @@ def load_library():
         "spec_page_plan": ([c_int, c_int, c_int, c_int, vp, vp, vp, vp, c_int, vp, vp, c_longlong,
                             vp, vp, vp], c_int),
         "spec_logits_adjust": ([POINTER(LogitsDesc)] + [vp] * 16, c_int),
+        "spec_rope_freqs": ([c_int, c_double, c_int] + [c_double] * 4 + [POINTER(c_double)], c_int),
+        "spec_rope": ([POINTER(RopeDesc), POINTER(c_double)] + [vp, c_longlong] * 4 +
+                      [vp, c_int, vp, vp, vp], c_int),
+        "kv_append": ([POINTER(KvDesc), c_int, vp, c_longlong, vp, c_longlong, vp, vp], c_int),
+        "spec_chunk_attn_workspace_size": ([POINTER(ChunkDesc), POINTER(KvDesc),
+                                            POINTER(c_size_t)], c_int),
+        "spec_chunk_attn": ([POINTER(ChunkDesc), vp, c_longlong, POINTER(KvDesc)] + [vp] * 5 +
+                            [c_size_t, vp], c_int),
+        "spec_chunk_attn_kv8_workspace_size": ([POINTER(ChunkDesc), POINTER(Kv8Desc),
+                                                POINTER(c_size_t)], c_int),
+        "spec_chunk_attn_kv8": ([POINTER(ChunkDesc), vp, c_longlong, POINTER(Kv8Desc)] + [vp] * 5 +
+                                [c_size_t, vp], c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -560,16 +590,20 @@ def kv8_commit(cache: Kv8Desc, kb, vb, path, acc_len, seq_len, free_pages, free_
 
 def _packed_rows(t, cache, n, name, dev):
     """Pointer and row stride of [n][Hkv][d] rows that may lie in wider rows."""
+    return _rows(t, n, cache.n_kv_heads, cache.head_dim, name, dev)
+
+
+def _rows(t, n, H, d, name, dev):
+    """Pointer and row stride of [n][H][d] rows that may lie in wider rows."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    Hkv, d = cache.n_kv_heads, cache.head_dim
-    if t.shape != (n, Hkv, d):
-        raise ValueError(f"{name} must be {[n, Hkv, d]}, got {list(t.shape)}")
-    if n and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != d)):
+    if t.shape != (n, H, d):
+        raise ValueError(f"{name} must be {[n, H, d]}, got {list(t.shape)}")
+    if n and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.data_ptr(), t.stride(0) if n > 1 else Hkv * d
+    return t.data_ptr(), t.stride(0) if n > 1 else H * d
 
 
 def kv8_append(cache: Kv8Desc, k, v, slot_map, stream=None):
@@ -642,3 +676,113 @@ def spec_logits_adjust(desc: LogitsDesc, logits, out, history=None, hist_len=Non
         _on(bias, f32, (B, nb), "bias", dev, nb == 0),
         _on(mask_bits, i32, (nm, (V + 31) // 32), "mask_bits", dev, nm == 0),
         _on(row_mask, i32, (B, Rj), "row_mask", dev, nm == 0), st))
+
+
+# ------------------------------------- a prompt's chunk: positions, cache, attention
+
+def rope_desc(n_tokens, n_q_heads, n_k_heads, head_dim, rot_dim, layout, dtype,
+              attention=1.0) -> RopeDesc:
+    return RopeDesc(n_tokens, n_q_heads, n_k_heads, head_dim, rot_dim, layout, dtype, attention)
+
+
+def spec_rope_freqs(rot_dim, base=10000.0, scaling=SPEC_ROPE_PLAIN, factor=1.0, trained_len=0.0,
+                    low=0.0, high=0.0):
+    """Rotary frequencies (radians a position) for spec_rope: a ctypes array of
+    rot_dim / 2 doubles, on the host."""
+    freqs = (c_double * max(1, rot_dim // 2))()
+    _check("spec_rope_freqs", load_library().spec_rope_freqs(
+        rot_dim, base, scaling, factor, trained_len, low, high, freqs))
+    return freqs
+
+
+def spec_rope(desc: RopeDesc, freqs, q, q_out, k=None, k_out=None, positions=None, seq_len=None,
+              cu_new=None, stream=None):
+    """Rotary positions of q [n][Hq][d] and k [n][Hk][d] (rows may be part of
+    wider ones) into q_out and k_out, which may be q and k themselves.  Positions
+    are given (int32 [n], negative: row left as it is), or follow from seq_len
+    int32 [B] and cu_new int32 [B + 1].  freqs: from spec_rope_freqs, or any
+    sequence of rot_dim / 2 numbers."""
+    st, dev = _cur(stream)
+    n, Hq, Hk, d = desc.n_tokens, desc.n_q_heads, desc.n_k_heads, desc.head_dim
+    half = max(1, desc.rot_dim // 2)
+    if len(freqs) != half:
+        raise ValueError(f"freqs must have {half} entries, got {len(freqs)}")
+    if not isinstance(freqs, ctypes.Array) or freqs._type_ is not c_double:
+        freqs = (c_double * half)(*(float(f) for f in freqs))
+    dt = torch.bfloat16 if desc.dtype == SPEC_BF16 else torch.float32
+    ptrs = []
+    for name, t, H in (("q", q, Hq), ("q_out", q_out, Hq), ("k", k, Hk), ("k_out", k_out, Hk)):
+        if H == 0:
+            ptrs += [None, 0]
+            continue
+        ptrs += _rows(t, n, H, d, name, dev)
+        if t.dtype != dt:
+            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    i32, B = torch.int32, 0
+    if positions is not None:
+        pos, sl, cu = _on(positions, i32, (n,), "positions", dev), None, None
+    else:
+        sl = _on(seq_len, i32, None, "seq_len", dev)
+        B, pos = seq_len.numel(), None
+        cu = _on(cu_new, i32, (B + 1,), "cu_new", dev)
+    _check("spec_rope", load_library().spec_rope(ctypes.byref(desc), freqs, *ptrs, pos, B, sl, cu, st))
+
+
+def kv_append(cache: KvDesc, k, v, slot_map, stream=None):
+    """Packed new tokens k, v [n][Hkv][d] (rows may be part of wider ones) into
+    the slots of slot_map int64 [n] (negative: not written) of a cache of rows."""
+    st, dev = _cur(stream)
+    n = slot_map.numel()
+    pk, sk = _packed_rows(k, cache, n, "k", dev)
+    pv, sv = _packed_rows(v, cache, n, "v", dev)
+    for name, t in (("k", k), ("v", v)):
+        if spec_dtype(t) != cache.dtype:
+            raise TypeError(f"{name} must have the cache's dtype, got {t.dtype}")
+    _check("kv_append", load_library().kv_append(
+        ctypes.byref(cache), n, pk, sk, pv, sv, _on(slot_map, torch.int64, (n,), "slot_map", dev), st))
+
+
+def chunk_desc(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, dtype, scale=0.0) -> ChunkDesc:
+    return ChunkDesc(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, dtype, scale)
+
+
+def _chunk_size(fn, desc, cache):
+    n = c_size_t(0)
+    _check(fn, getattr(load_library(), fn)(ctypes.byref(desc), ctypes.byref(cache), ctypes.byref(n)))
+    return n.value
+
+
+def _chunk(fn, desc, q, cache, seq_len, cu_new, o, lse, workspace, stream):
+    st, dev = _cur(stream)
+    _cache_on(cache, dev)
+    B, n, Hq, d = desc.batch, desc.n_tokens, desc.n_q_heads, desc.head_dim
+    dt = torch.bfloat16 if desc.dtype == SPEC_BF16 else torch.float32
+    pq, sq = _rows(q, n, Hq, d, "q", dev)
+    if q.dtype != dt:
+        raise TypeError(f"q must be {dt}, got {q.dtype}")
+    _check(fn, getattr(load_library(), fn)(
+        ctypes.byref(desc), pq, sq, ctypes.byref(cache), _on(seq_len, torch.int32, (B,), "seq_len", dev),
+        _on(cu_new, torch.int32, (B + 1,), "cu_new", dev), _on(o, dt, (n, Hq, d), "o", dev),
+        _on(lse, torch.float32, (n, Hq), "lse", dev), _on(workspace, None, None, "workspace", dev),
+        workspace.numel() * workspace.element_size(), st))
+
+
+def spec_chunk_attn_workspace_size(desc: ChunkDesc, cache: KvDesc) -> int:
+    return _chunk_size("spec_chunk_attn_workspace_size", desc, cache)
+
+
+def spec_chunk_attn(desc: ChunkDesc, q, cache: KvDesc, seq_len, cu_new, o, lse, workspace, stream=None):
+    """Attention of packed new tokens q [n][Hq][d] (rows may be part of wider
+    ones), which the cache of rows already holds, each over its request's tokens
+    up to itself; o [n][Hq][d], lse [n][Hq]."""
+    _chunk("spec_chunk_attn", desc, q, cache, seq_len, cu_new, o, lse, workspace, stream)
+
+
+def spec_chunk_attn_kv8_workspace_size(desc: ChunkDesc, cache: Kv8Desc) -> int:
+    return _chunk_size("spec_chunk_attn_kv8_workspace_size", desc, cache)
+
+
+def spec_chunk_attn_kv8(desc: ChunkDesc, q, cache: Kv8Desc, seq_len, cu_new, o, lse, workspace,
+                        stream=None):
+    """spec_chunk_attn over a cache held in 8 bits."""
+    _chunk("spec_chunk_attn_kv8", desc, q, cache, seq_len, cu_new, o, lse, workspace, stream)

@@ -1,0 +1,549 @@
+// spec_chunk_attn and spec_chunk_attn_kv8: attention of new tokens that the
+// cache already holds, each over everything up to itself.
+//
+//   o_i = sum_t exp(q_i . k_t scale - lse_i) v_t,  lse_i = ln sum_t exp(q_i . k_t scale),
+//   t = 0 .. seq_len + i
+//
+// This file holds the entry points, the CUDA-core kernel (fp32 rows) and the
+// kernel that merges the parts of units that several CTAs shared.
+#include <math.h>
+
+#include "chunk_attn.cuh"
+#include "kv8_common.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kRows = 32;        // packed rows of a CUDA-core unit
+constexpr int kKeys = 64;        // keys of a step
+constexpr int kSimtThreads = 128;
+constexpr int kSimtPerSm = 2;
+
+enum { kCacheRows = 0, kCache8 = 1 };
+
+template <int D>
+struct ChunkSimtShared {
+    float q[kRows][D];
+    float k[kKeys][D + 4];       // (a quarter warp's rows start in different banks)
+    float v[kKeys][D];
+    float p[kRows][kKeys + 4];
+    ChunkShare share;
+};
+
+// Four elements of token t of (request b, head h): from element c on, of its
+// key (x = 0) or value (x = 1) row; zeros and SPEC_DEV_BAD_PAGE for a page id
+// outside the cache.
+template <typename T, int D, int kCache>
+__device__ __forceinline__ float4 chunk_load4(const ChunkParams &P, int b, int h, int t, int x, int c) {
+    if (kCache == kCacheRows && !P.paged) {
+        const T *p = static_cast<const T *>(x ? P.vc : P.kc) + (((size_t)b * P.Hkv + h) * P.capacity + t) * D + c;
+        return make_float4(load_f(p), load_f(p + 1), load_f(p + 2), load_f(p + 3));
+    }
+    const int page = __ldg(P.page_table + (size_t)b * P.max_pages + t / P.ps), off = t % P.ps;
+    if (page < 0 || page >= P.n_pages) {
+        raise_status(P.status, SPEC_DEV_BAD_PAGE);
+        return make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (kCache == kCache8) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(
+            static_cast<const uint8_t *>(P.kc) + kv8_block(page, h, P.Hkv, P.ps, D) + kv8_row(off, x, D) + c);
+        const float s = kv8_read_scale(P.scales[((size_t)page * P.Hkv + h) * 2 + x]);
+        const float2 lo = from_e4m3x2(w & 0xffffu), hi = from_e4m3x2(w >> 16);
+        return make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s);
+    }
+    const T *p = static_cast<const T *>(x ? P.vc : P.kc) +
+                 ((((size_t)page * P.Hkv + h) * (D / 64) + c / 64) * P.ps + off) * 64 + c % 64;
+    return make_float4(load_f(p), load_f(p + 1), load_f(p + 2), load_f(p + 3));
+}
+
+// The CUDA-core kernel, everything in fp32.  128 threads: thread (ty, tx) has
+// the scores of rows 4 ty .. + 3 and keys tx + 16 i, and the outputs of the
+// same rows and dimensions 4 tx + 64 i .. + 3.
+template <typename T, int D, int kCache>
+__global__ void __launch_bounds__(kSimtThreads, kSimtPerSm) chunk_simt_kernel(ChunkParams P) {
+    pdl_wait();
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    ChunkSimtShared<D> &sh = *reinterpret_cast<ChunkSimtShared<D> *>(smem_raw);
+    constexpr int NC = D / 64;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    chunk_share<kSimtThreads>(P, sh.share);
+    ChunkWalk walk(P, sh.share);
+    ChunkPart u;
+    while (walk.next(P, u)) {
+        const long long rows = (long long)u.n * P.G, r0 = (long long)u.j * kRows;
+        const int nr = (int)min((long long)kRows, rows - r0);
+        __syncthreads();
+        for (int i = tid; i < kRows * (D / 4); i += kSimtThreads) {
+            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < nr) {
+                const long long p = r0 + r;
+                const T *src = static_cast<const T *>(P.q) + (u.first + p / P.G) * P.stride_q +
+                               ((long long)u.h * P.G + p % P.G) * D + c;
+                x = make_float4(load_f(src), load_f(src + 1), load_f(src + 2), load_f(src + 3));
+            }
+            *reinterpret_cast<float4 *>(&sh.q[r][c]) = x;
+        }
+        int seen[4];                                     // tokens this thread's rows see
+        float m[4], l[4], acc[4][NC][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i;
+            seen[i] = r < nr ? u.S + (int)((r0 + r) / P.G) + 1 : 0;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.f;
+        }
+        const int last = u.S + (int)((r0 + nr - 1) / P.G) + 1;
+        for (int s = u.s0; s < u.s1; ++s) {
+            const int t0 = s * kKeys, nk = min(kKeys, last - t0);
+            __syncthreads();
+            bool odd = false;                            // a non-finite value among them
+            for (int i = tid; i < kKeys * (D / 4); i += kSimtThreads) {
+                const int t = i / (D / 4), c = (i % (D / 4)) * 4;
+                float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+                if (t < nk) {
+                    k = chunk_load4<T, D, kCache>(P, u.b, u.h, t0 + t, 0, c);
+                    v = chunk_load4<T, D, kCache>(P, u.b, u.h, t0 + t, 1, c);
+                    odd = odd || !(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY &&
+                                   fabsf(v.w) < INFINITY);
+                }
+                *reinterpret_cast<float4 *>(&sh.k[t][c]) = k;
+                *reinterpret_cast<float4 *>(&sh.v[t][c]) = v;
+            }
+            odd = __syncthreads_or(odd);
+            float x[4][4] = {};
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                float4 a[4], k[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(&sh.q[ty * 4 + i][c]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const float4 *>(&sh.k[tx + 16 * i][c]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[i][j] = fmaf(a[i].w, k[j].w, fmaf(a[i].z, k[j].z, fmaf(a[i].y, k[j].y, fmaf(a[i].x, k[j].x, x[i][j]))));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float top = m[i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[i][j] = t0 + tx + 16 * j < seen[i] ? x[i][j] * P.scale_log2 : -INFINITY;
+                    top = fmaxf(top, x[i][j]);
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float base = top == -INFINITY ? 0.f : top;
+                const float alpha = m[i] == -INFINITY ? (l[i] == 0.f ? 0.f : 1.f) : exp2f(m[i] - base);
+                m[i] = top;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = t0 + tx + 16 * j < seen[i] ? exp2f(x[i][j] - base) : 0.f;
+                    sum += p;
+                    sh.p[ty * 4 + i][tx + 16 * j] = p;
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                l[i] = l[i] * alpha + sum;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][c][e] *= alpha;
+            }
+            __syncwarp();
+            if (!odd) {
+#pragma unroll 2
+                for (int t = 0; t < kKeys; t += 4) {
+                    float4 p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(&sh.p[ty * 4 + i][t]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {
+                            const float4 v = *reinterpret_cast<const float4 *>(&sh.v[t + k][tx * 4 + 64 * c]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float w = k == 0 ? p[i].x : k == 1 ? p[i].y : k == 2 ? p[i].z : p[i].w;
+                                acc[i][c][0] = fmaf(w, v.x, acc[i][c][0]);
+                                acc[i][c][1] = fmaf(w, v.y, acc[i][c][1]);
+                                acc[i][c][2] = fmaf(w, v.z, acc[i][c][2]);
+                                acc[i][c][3] = fmaf(w, v.w, acc[i][c][3]);
+                            }
+                        }
+                }
+            } else {                                     // (0 * NaN: only what a row sees)
+                for (int t = 0; t < kKeys; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (t0 + t >= seen[i]) continue;
+                        const float w = sh.p[ty * 4 + i][t];
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                acc[i][c][e] = fmaf(w, sh.v[t][tx * 4 + 64 * c + e], acc[i][c][e]);
+                    }
+            }
+        }
+        const bool whole = u.s0 == 0 && u.s1 == u.steps;
+        const int slot = chunk_slot(u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i;
+            if (r >= nr) continue;
+            if (whole) {
+                const long long p = r0 + r, row = u.first + p / P.G, hq = (long long)u.h * P.G + p % P.G;
+                T *o = static_cast<T *>(P.o) + (row * P.Hq + hq) * D;
+                const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) store_f(o + tx * 4 + 64 * c + e, acc[i][c][e] * inv);
+                if (tx == 0)
+                    P.lse[row * P.Hq + hq] = l[i] == 0.f ? -INFINITY
+                                             : l[i] != l[i] ? l[i]
+                                                            : (m[i] + log2f(l[i])) * kLn2;
+            } else {
+                float *o = P.part_o + ((size_t)slot * kRows + r) * D;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    *reinterpret_cast<float4 *>(o + tx * 4 + 64 * c) =
+                        make_float4(acc[i][c][0], acc[i][c][1], acc[i][c][2], acc[i][c][3]);
+                if (tx == 0) P.part_ml[(size_t)slot * kRows + r] = make_float2(m[i], l[i]);
+            }
+        }
+    }
+}
+
+constexpr int kMergeWarps = 8;
+
+// Merges the parts of the unit that is first cut where CTA blockIdx.x + 1
+// begins; a warp a row, in the parts' order.
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(ChunkParams P, int n_cta) {
+    pdl_wait();
+    const int i = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 c = P.records[i];
+    if (c.x >= P.B || c.w == 0) return;
+    const int4 a = P.records[i - 1];
+    if (a.x == c.x && a.y == c.y && a.z == c.z && a.w > 0) return;     // cut earlier
+    const ChunkReq r = chunk_request(P, c.x, nullptr);
+    const int steps = chunk_steps(P, r, c.z);
+    __shared__ int s_slot[1024];
+    __shared__ int s_n;
+    // the unit's parts: the one that begins it, then every CTA's that begins
+    // inside it and has a step of it
+    if (warp == 0) {
+        if (lane == 0) s_slot[0] = 2 * (i - 1) + 1;
+        int n = 1;
+        for (int k0 = i; k0 < n_cta; k0 += 32) {
+            const int k = k0 + lane;
+            const int4 x = k < n_cta ? P.records[k] : make_int4(P.B, 0, 0, 0);
+            const bool in = x.x == c.x && x.y == c.y && x.z == c.z && x.w > 0;
+            bool some = false;
+            if (in) {
+                const int4 y = P.records[k + 1];
+                const int end = y.x == c.x && y.y == c.y && y.z == c.z ? y.w : steps;
+                some = x.w < end;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, some);
+            if (some) s_slot[n + __popc(m & ((1u << lane) - 1u))] = 2 * k;
+            n += __popc(m);
+            if (!__all_sync(0xffffffffu, in)) break;
+        }
+        if (lane == 0) s_n = n;
+    }
+    __syncthreads();
+    const int n = s_n;
+    const long long r0 = (long long)c.z * P.ru;
+    const int nr = (int)min((long long)P.ru, (long long)r.n * P.G - r0);
+    constexpr int E = D / 32;
+    for (int row = blockIdx.y * kMergeWarps + warp; row < nr; row += gridDim.y * kMergeWarps) {
+        // the largest maximum, a part a lane
+        float top = -INFINITY;
+        for (int k = lane; k < n; k += 32) top = fmaxf(top, P.part_ml[(size_t)s_slot[k] * P.ru + row].x);
+        top = warp_max(top);
+        float l = 0.f, acc[E] = {};
+        constexpr int U = 4;                             // parts in flight
+        for (int k0 = 0; k0 < n; k0 += U) {
+            float2 ml[U];
+            float x[U][E];
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                ml[v] = make_float2(-INFINITY, 0.f);
+                if (k0 + v >= n) continue;
+                const size_t at = (size_t)s_slot[k0 + v] * P.ru + row;
+                ml[v] = P.part_ml[at];
+                const float *o = P.part_o + at * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(o);
+                    x[v][0] = f.x; x[v][1] = f.y; x[v][2] = f.z; x[v][3] = f.w;
+                } else {
+                    const float2 f = *reinterpret_cast<const float2 *>(o);
+                    x[v][0] = f.x; x[v][1] = f.y;
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                // (a part without weight may hold nothing; one of NaN has its
+                // maximum from the other scores, or none)
+                if (ml[v].y == 0.f) continue;
+                const float w = ml[v].x == -INFINITY ? 1.f : exp2f(ml[v].x - top);
+                l = fmaf(w, ml[v].y, l);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[v][e], acc[e]);
+            }
+        }
+        const long long p = r0 + row, tok = r.first + p / P.G, hq = (long long)c.y * P.G + p % P.G;
+        T *o = static_cast<T *>(P.o) + (tok * P.Hq + hq) * D + lane * E;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if constexpr (sizeof(T) == 2) {
+            uint32_t w[E / 2];
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+                w[e] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            if constexpr (E == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t *>(o) = w[0];
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) store_f(o + e, acc[e] * inv);
+        }
+        if (lane == 0)
+            P.lse[tok * P.Hq + hq] = l == 0.f ? -INFINITY : l != l ? l : (top + log2f(l)) * kLn2;
+    }
+}
+
+// ------------------------------------------------------------- host side
+
+ChunkPlan simt_plan() {
+    return ChunkPlan{kRows, kKeys, 2 * kKeys, 2 * kKeys, kSimtPerSm * num_sms()};
+}
+
+ChunkPlan plan_of(const ChunkParams &P, int dtype, bool kv8) {
+    (void)dtype;
+    (void)kv8;
+    (void)P;
+    return simt_plan();
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// What the workspace holds, in this order.
+struct ChunkSpace {
+    size_t o, ml, rec, bytes;
+};
+ChunkSpace space_of(const ChunkPlan &pl, int d) {
+    ChunkSpace w{};
+    const size_t rows = 2 * (size_t)pl.n_cta * pl.ru;
+    w.ml = round256(rows * d * sizeof(float));
+    w.rec = w.ml + round256(rows * sizeof(float2));
+    w.bytes = w.rec + round256((size_t)(pl.n_cta + 1) * sizeof(int4));
+    return w;
+}
+
+// Checks a call's shape, and fills in what follows from it.
+spec_status_t chunk_shape(const spec_chunk_desc *a, int n_kv_heads, int head_dim, int batch,
+                          long long capacity, ChunkParams &P) {
+    if (a->batch < 0 || a->n_tokens < 0 || a->n_q_heads <= 0 || a->n_kv_heads <= 0 ||
+        a->n_q_heads % a->n_kv_heads != 0 || !(a->scale >= 0.f) || !(a->scale < INFINITY))
+        return SPEC_ERR_INVALID_ARG;
+    if (a->dtype != SPEC_BF16 && a->dtype != SPEC_F32) return SPEC_ERR_UNSUPPORTED;
+    if (a->head_dim != 64 && a->head_dim != 128) return SPEC_ERR_UNSUPPORTED;
+    if (n_kv_heads != a->n_kv_heads || head_dim != a->head_dim || batch < a->batch || capacity <= 0)
+        return SPEC_ERR_INVALID_ARG;
+    if (capacity > (1ll << 30) || a->n_q_heads / a->n_kv_heads > 128) return SPEC_ERR_UNSUPPORTED;
+    P.B = a->batch;
+    P.n_tokens = a->n_tokens;
+    P.Hq = a->n_q_heads;
+    P.Hkv = a->n_kv_heads;
+    P.G = P.Hq / P.Hkv;
+    P.d = a->head_dim;
+    P.capacity = (int)capacity;
+    const float scale = a->scale > 0.f ? a->scale : 1.f / sqrtf((float)P.d);
+    P.scale_log2 = scale * kLog2e;
+    return SPEC_OK;
+}
+
+spec_status_t chunk_cache(const spec_chunk_desc *a, const spec_kv_desc *c, ChunkParams &P) {
+    if (!a || !c) return SPEC_ERR_INVALID_ARG;
+    P.paged = c->kind == SPEC_KV_PAGED;
+    if (!P.paged && c->kind != SPEC_KV_CONTIGUOUS) return SPEC_ERR_INVALID_ARG;
+    long long capacity = c->max_seq;
+    if (P.paged) {
+        if (c->n_pages <= 0 || c->page_size <= 0 || c->max_pages_per_seq <= 0) return SPEC_ERR_INVALID_ARG;
+        if (c->page_size % 16 != 0) return SPEC_ERR_UNSUPPORTED;
+        capacity = (long long)c->max_pages_per_seq * c->page_size;
+        P.ps = c->page_size;
+        P.max_pages = c->max_pages_per_seq;
+        P.n_pages = c->n_pages;
+    }
+    const spec_status_t st = chunk_shape(a, c->n_kv_heads, c->head_dim, c->batch, capacity, P);
+    if (st != SPEC_OK) return st;
+    if (c->dtype != a->dtype) return SPEC_ERR_INVALID_ARG;
+    // (tensor copies count rows of 64 elements, and heads, in 32 bits)
+    const long long tiles = P.paged ? (long long)c->n_pages * P.Hkv * (P.d / 64) : (long long)c->batch * P.Hkv;
+    if (tiles > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
+    P.kc = c->k;
+    P.vc = c->v;
+    P.page_table = c->page_table;
+    return SPEC_OK;
+}
+
+spec_status_t chunk_cache8(const spec_chunk_desc *a, const spec_kv8_desc *c, ChunkParams &P) {
+    if (!a || !c) return SPEC_ERR_INVALID_ARG;
+    spec_status_t st = check_kv8(c);
+    if (st != SPEC_OK) return st;
+    if (c->max_pages_per_seq <= 0) return SPEC_ERR_INVALID_ARG;
+    st = chunk_shape(a, c->n_kv_heads, c->head_dim, c->batch, (long long)c->max_pages_per_seq * c->page_size, P);
+    if (st != SPEC_OK) return st;
+    P.paged = 1;
+    P.ps = c->page_size;
+    P.max_pages = c->max_pages_per_seq;
+    P.n_pages = c->n_pages;
+    P.kc = c->kv;
+    P.vc = c->kv;
+    P.scales = c->scales;
+    P.page_table = c->page_table;
+    return SPEC_OK;
+}
+
+// Fills in the plan; the whole call's cost has to be countable in 64 bits.
+spec_status_t chunk_plan(const ChunkParams &P, int dtype, bool kv8, ChunkPlan &pl) {
+    pl = plan_of(P, dtype, kv8);
+    const double units = (double)P.n_tokens * P.G / pl.ru + P.B;
+    if (units * P.Hkv > 2147483647.0 ||
+        units * P.Hkv * P.G * ((double)pl.fixed_cost + P.capacity + pl.ru) > 1e18)
+        return SPEC_ERR_UNSUPPORTED;
+    return SPEC_OK;
+}
+
+template <typename T, int kCache>
+spec_status_t launch_simt(const ChunkParams &P, int n_cta, cudaStream_t s) {
+    const bool wide = P.d == 128;
+    const size_t smem = wide ? sizeof(ChunkSimtShared<128>) : sizeof(ChunkSimtShared<64>);
+    auto *f = wide ? chunk_simt_kernel<T, 128, kCache> : chunk_simt_kernel<T, 64, kCache>;
+    if (set_smem_limit(reinterpret_cast<const void *>(f), smem) != SPEC_OK) return SPEC_ERR_CUDA;
+    return launch(f, dim3(n_cta), dim3(kSimtThreads), smem, s, P);
+}
+
+spec_status_t run_chunk(ChunkParams &P, int dtype, bool kv8, const void *q, long long stride_q,
+                        const int32_t *seq_len, const int32_t *cu_new, void *o, float *lse,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+    ChunkPlan pl;
+    spec_status_t st = chunk_plan(P, dtype, kv8, pl);
+    if (st != SPEC_OK) return st;
+    const long long width = (long long)P.Hq * P.d;
+    if (stride_q < width) return SPEC_ERR_INVALID_ARG;
+    if (P.B == 0 || P.n_tokens == 0) return SPEC_OK;
+    if (!q || !P.kc || !P.vc || !seq_len || !cu_new || !o || !lse || !workspace ||
+        (P.paged && !P.page_table) || (kv8 && !P.scales))
+        return SPEC_ERR_INVALID_ARG;
+    const int es = dtype == SPEC_BF16 ? 2 : 4;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(P.kc) || !aligned16(P.vc) || stride_q * es % 16 != 0 ||
+        reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+        return SPEC_ERR_INVALID_ARG;
+    // (rows of q are read while others' results are written)
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+    const uintptr_t q1 = q0 + (uintptr_t)((P.n_tokens - 1ll) * stride_q + width) * es;
+    const uintptr_t o1 = o0 + (uintptr_t)(P.n_tokens * width) * es;
+    if (q0 < o1 && o0 < q1) return SPEC_ERR_INVALID_ARG;
+    const ChunkSpace w = space_of(pl, P.d);
+    if (workspace_bytes < w.bytes) return SPEC_ERR_CAPACITY;
+    P.q = q;
+    P.stride_q = stride_q;
+    P.seq_len = seq_len;
+    P.cu_new = cu_new;
+    P.o = o;
+    P.lse = lse;
+    uint8_t *base = static_cast<uint8_t *>(workspace);
+    P.part_o = reinterpret_cast<float *>(base + w.o);
+    P.part_ml = reinterpret_cast<float2 *>(base + w.ml);
+    P.records = reinterpret_cast<int4 *>(base + w.rec);
+    P.ru = pl.ru;
+    P.ks = pl.ks;
+    P.fixed_cost = pl.fixed_cost;
+    P.min_share = pl.min_share;
+    P.wait = wait_limit();
+    P.status = status_ptr();
+    if (!P.status) return SPEC_ERR_CUDA;
+    cudaStream_t s = as_stream(stream);
+    if (dtype == SPEC_BF16)
+        st = kv8 ? launch_simt<__nv_bfloat16, kCache8>(P, pl.n_cta, s)
+                 : launch_simt<__nv_bfloat16, kCacheRows>(P, pl.n_cta, s);
+    else
+        st = kv8 ? launch_simt<float, kCache8>(P, pl.n_cta, s) : launch_simt<float, kCacheRows>(P, pl.n_cta, s);
+    if (st != SPEC_OK) return st;
+    const dim3 grid(pl.n_cta - 1, ceil_div(pl.ru, 4 * kMergeWarps)), block(kMergeWarps * 32);
+    if (dtype == SPEC_BF16)
+        st = P.d == 128 ? launch(chunk_merge_kernel<__nv_bfloat16, 128>, grid, block, 0, s, P, pl.n_cta)
+                        : launch(chunk_merge_kernel<__nv_bfloat16, 64>, grid, block, 0, s, P, pl.n_cta);
+    else
+        st = P.d == 128 ? launch(chunk_merge_kernel<float, 128>, grid, block, 0, s, P, pl.n_cta)
+                        : launch(chunk_merge_kernel<float, 64>, grid, block, 0, s, P, pl.n_cta);
+    if (st != SPEC_OK) return st;
+    return launch_status();
+}
+
+spec_status_t size_of(const ChunkParams &P, int dtype, bool kv8, size_t *bytes) {
+    ChunkPlan pl;
+    const spec_status_t st = chunk_plan(P, dtype, kv8, pl);
+    if (st != SPEC_OK) return st;
+    *bytes = space_of(pl, P.d).bytes;
+    return SPEC_OK;
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" spec_status_t spec_chunk_attn_workspace_size(const spec_chunk_desc *desc,
+                                                        const spec_kv_desc *cache, size_t *bytes) {
+    using namespace sv;
+    if (!bytes) return SPEC_ERR_INVALID_ARG;
+    ChunkParams P{};
+    const spec_status_t st = chunk_cache(desc, cache, P);
+    return st == SPEC_OK ? size_of(P, desc->dtype, false, bytes) : st;
+}
+
+extern "C" spec_status_t spec_chunk_attn(const spec_chunk_desc *desc, const void *q, long long row_stride_q,
+                                         const spec_kv_desc *cache, const int32_t *seq_len,
+                                         const int32_t *cu_new, void *o, float *lse, void *workspace,
+                                         size_t workspace_bytes, void *stream) {
+    using namespace sv;
+    ChunkParams P{};
+    const spec_status_t st = chunk_cache(desc, cache, P);
+    if (st != SPEC_OK) return st;
+    return run_chunk(P, desc->dtype, false, q, row_stride_q, seq_len, cu_new, o, lse, workspace,
+                     workspace_bytes, stream);
+}
+
+extern "C" spec_status_t spec_chunk_attn_kv8_workspace_size(const spec_chunk_desc *desc,
+                                                            const spec_kv8_desc *cache, size_t *bytes) {
+    using namespace sv;
+    if (!bytes) return SPEC_ERR_INVALID_ARG;
+    ChunkParams P{};
+    const spec_status_t st = chunk_cache8(desc, cache, P);
+    return st == SPEC_OK ? size_of(P, desc->dtype, true, bytes) : st;
+}
+
+extern "C" spec_status_t spec_chunk_attn_kv8(const spec_chunk_desc *desc, const void *q,
+                                             long long row_stride_q, const spec_kv8_desc *cache,
+                                             const int32_t *seq_len, const int32_t *cu_new, void *o,
+                                             float *lse, void *workspace, size_t workspace_bytes,
+                                             void *stream) {
+    using namespace sv;
+    ChunkParams P{};
+    const spec_status_t st = chunk_cache8(desc, cache, P);
+    if (st != SPEC_OK) return st;
+    return run_chunk(P, desc->dtype, true, q, row_stride_q, seq_len, cu_new, o, lse, workspace,
+                     workspace_bytes, stream);
+}

@@ -1,0 +1,251 @@
+// Work decomposition shared by the chunk-attention kernels: attention of a
+// packed batch of new tokens over a KV cache that already holds them.
+//
+// Packed rows: for KV head h, the G = Hq / Hkv query heads h*G .. h*G+G-1 of
+// new token i of a request are its packed rows i*G .. i*G+G-1; row p sees the
+// cache's tokens 0 .. S + p / G (S: tokens held before), itself the last one.
+//
+// Unit: `ru` consecutive packed rows of one (request, KV head), cut along the
+// keys into steps of `ks` tokens up to the last one its last row sees.  Units
+// are numbered request by request, head by head, rows ascending.
+//
+// Ranges: every unit has a cost in closed form -- a fixed one, and the tokens
+// its last row sees -- so the sum over any number of units is closed too, and
+// a CTA finds its equal share of the whole call's cost from one scan of the
+// requests and two searches, whatever the lengths.  A share that begins or
+// ends inside a unit begins or ends at a step of it: the CTA then writes the
+// rows' running maximum, sum and unnormalised output (fp32) to one of its two
+// slots, and the merging kernel puts the parts together in order.
+#pragma once
+
+#include "common.cuh"
+#include "kv8.cuh"
+
+namespace sv {
+
+struct ChunkParams {
+    const void *q;
+    long long stride_q;      // elements between two tokens' rows of q
+    const void *kc, *vc;     // cache; 8 bits: kc the tiles
+    const float *scales;     // 8 bits: [n_pages][Hkv][2]
+    const int32_t *page_table, *seq_len, *cu_new;
+    void *o;
+    float *lse;
+    float *part_o;           // [2 n_cta][ru][d]
+    float2 *part_ml;         // [2 n_cta][ru] (log2 domain)
+    int4 *records;           // [n_cta + 1] where each CTA's share begins
+    int *status;
+    int B, n_tokens, Hq, Hkv, G, d;
+    int paged, ps, max_pages, n_pages;
+    int capacity;            // tokens per request
+    int ru, ks;              // rows of a unit, keys of a step
+    int fixed_cost;          // of a unit, in keys
+    int min_share;           // least cost (keys) worth a CTA
+    float scale_log2;        // softmax scale * log2(e)
+    long long wait;          // limit of every pipeline wait, in SM cycles
+};
+
+// The tensor-core path: rows and CTAs of a call, its kernel's launch.
+struct ChunkPlan {
+    int ru, ks, fixed_cost, min_share, n_cta;
+};
+ChunkPlan chunk_tc_plan(const ChunkParams &P, bool kv8);
+spec_status_t launch_chunk_tc(const ChunkParams &P, bool kv8, int n_cta, cudaStream_t s);
+
+namespace {
+
+// A request's new tokens: n of them, packed from row `first` on, S held
+// before; n = 0 for one without any, or with lengths out of range.
+struct ChunkReq {
+    int first, n, S;
+};
+
+__device__ __forceinline__ ChunkReq chunk_request(const ChunkParams &P, int b, int *bits) {
+    ChunkReq r{__ldg(P.cu_new + b), 0, 0};
+    const int end = __ldg(P.cu_new + b + 1);
+    if (r.first < 0 || end < r.first || end > P.n_tokens) {
+        if (bits) *bits |= SPEC_DEV_BAD_INDEX;
+        return r;
+    }
+    if (end == r.first) return r;
+    r.S = __ldg(P.seq_len + b);
+    if (r.S < 0 || r.S > P.capacity - (end - r.first)) {
+        if (bits) *bits |= SPEC_DEV_SEQ_OVERFLOW;
+        r.S = 0;
+        return r;
+    }
+    r.n = end - r.first;
+    return r;
+}
+
+__device__ __forceinline__ int chunk_units(const ChunkParams &P, const ChunkReq &r) {
+    return (int)(((long long)r.n * P.G + P.ru - 1) / P.ru);
+}
+
+// Cost of a head's first j units (in keys * G): unit i costs G (fixed + S) +
+// (i + 1) ru.
+__device__ __forceinline__ long long chunk_cost(const ChunkParams &P, const ChunkReq &r, long long j) {
+    return j * P.G * ((long long)P.fixed_cost + r.S) + P.ru * (j * (j + 1) / 2);
+}
+
+// A place in the call's work: unit j of head h of request b, from step s on.
+struct ChunkPos {
+    int b, h, j, s;
+};
+
+// Steps of unit j: up to the last token its last row sees.
+__device__ __forceinline__ int chunk_steps(const ChunkParams &P, const ChunkReq &r, int j) {
+    const long long rows = (long long)r.n * P.G;
+    const long long last = min(rows, (long long)(j + 1) * P.ru) - 1;
+    return (int)((r.S + last / P.G + P.ks) / P.ks);      // (S + last / G + 1 tokens)
+}
+
+__device__ __forceinline__ ChunkPos chunk_find(const ChunkParams &P, int b, const ChunkReq &r,
+                                               long long at) {
+    const int nu = chunk_units(P, r);
+    const long long head = chunk_cost(P, r, nu);
+    ChunkPos p{b, (int)(at / head), 0, 0};
+    at %= head;
+    int lo = 0, hi = nu - 1;                              // the last j with cost(j) <= at
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (chunk_cost(P, r, mid) <= at) lo = mid;
+        else hi = mid - 1;
+    }
+    p.j = lo;
+    const long long f = at - chunk_cost(P, r, lo), w = chunk_cost(P, r, lo + 1) - chunk_cost(P, r, lo);
+    p.s = (int)((double)f / (double)w * chunk_steps(P, r, lo));
+    p.s = min(p.s, chunk_steps(P, r, lo) - 1);
+    return p;
+}
+
+struct ChunkShare {
+    long long warp_sum[32];
+    ChunkPos begin, end;     // begin.b == B: nothing to do
+};
+
+// The share of CTA blockIdx.x, by all T threads of the CTA; records where it
+// begins.  Ends with a barrier.
+template <int T>
+__device__ void chunk_share(const ChunkParams &P, ChunkShare &sh) {
+    static_assert(T % 32 == 0 && T <= 1024, "threads");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (P.B + T - 1) / T, b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
+    if (tid == 0) sh.begin = sh.end = ChunkPos{P.B, 0, 0, 0};
+    long long mine = 0;
+    int bits = 0;
+    ChunkReq r{0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+        r = chunk_request(P, b, &bits);
+        mine += P.Hkv * chunk_cost(P, r, chunk_units(P, r));
+    }
+    if (bits && blockIdx.x == 0) raise_status(P.status, bits);
+    long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+    }
+    if (lane == 31) sh.warp_sum[warp] = sum;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < T / 32; ++w) {
+        const long long x = sh.warp_sum[w];
+        before += w < warp ? x : 0;
+        total += x;
+    }
+    before += sum - mine;
+    long long n = total / ((long long)P.min_share * P.G);
+    n = n < 1 ? 1 : n > gridDim.x ? gridDim.x : n;
+    for (int e = 0; e < 2; ++e) {
+        const long long i = (long long)blockIdx.x + e;
+        if (i >= n) break;
+        const long long at = total / n * i + total % n * i / n;
+        if (at < before || at >= before + mine) continue;
+        long long c = before;
+        for (int b = b0; b < b1; ++b) {
+            if (per > 1) r = chunk_request(P, b, nullptr);
+            const long long w = P.Hkv * chunk_cost(P, r, chunk_units(P, r));
+            if (at < c + w) {
+                (e ? sh.end : sh.begin) = chunk_find(P, b, r, at - c);
+                break;
+            }
+            c += w;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        const ChunkPos p = sh.begin;
+        P.records[blockIdx.x] = make_int4(p.b, p.h, p.j, p.s);
+        if (blockIdx.x == gridDim.x - 1) P.records[gridDim.x] = make_int4(P.B, 0, 0, 0);
+    }
+}
+
+// What a CTA does of one unit: steps s0 .. s1 - 1 of `steps`.
+struct ChunkPart {
+    int b, h, j;
+    int first, S;            // request: its first packed token, tokens held before
+    int n;                   // request: new tokens
+    int steps, s0, s1;
+};
+
+// Walks a CTA's share part by part.
+struct ChunkWalk {
+    ChunkPos at, end;
+    ChunkReq r;
+    int nu;
+    bool fresh;
+
+    __device__ __forceinline__ ChunkWalk(const ChunkParams &P, const ChunkShare &sh)
+        : at(sh.begin), end(sh.end), r{0, 0, 0}, nu(0), fresh(true) {}
+
+    __device__ __forceinline__ bool next(const ChunkParams &P, ChunkPart &u) {
+        while (at.b < P.B) {
+            if (fresh) {
+                r = chunk_request(P, at.b, nullptr);
+                nu = chunk_units(P, r);
+                fresh = false;
+            }
+            if (at.b > end.b) return false;
+            if (r.n == 0) {
+                at = ChunkPos{at.b + 1, 0, 0, 0};
+                fresh = true;
+                continue;
+            }
+            const bool last = at.b == end.b && at.h == end.h && at.j == end.j;
+            u.b = at.b;
+            u.h = at.h;
+            u.j = at.j;
+            u.first = r.first;
+            u.S = r.S;
+            u.n = r.n;
+            u.steps = chunk_steps(P, r, at.j);
+            u.s0 = at.s;
+            u.s1 = last ? end.s : u.steps;
+            if (last) {
+                at.b = P.B;
+            } else {
+                at.s = 0;
+                if (++at.j == nu) {
+                    at.j = 0;
+                    if (++at.h == P.Hkv) {
+                        at.h = 0;
+                        ++at.b;
+                        fresh = true;
+                    }
+                }
+            }
+            if (u.s0 < u.s1) return true;
+        }
+        return false;
+    }
+};
+
+// The slot of a part that is not a whole unit: a CTA has at most one that
+// begins inside its unit and one that begins with it.
+__device__ __forceinline__ int chunk_slot(const ChunkPart &u) {
+    return 2 * (int)blockIdx.x + (u.s0 > 0 ? 0 : 1);
+}
+
+}  // namespace
+}  // namespace sv
