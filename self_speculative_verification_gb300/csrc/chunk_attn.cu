@@ -33,11 +33,11 @@ struct ChunkSimtShared {
 // Four elements of token t of (request b, head h): from element c on, of its
 // key (x = 0) or value (x = 1) row; zeros and SPEC_DEV_BAD_PAGE for a page id
 // outside the cache.
-template <typename T, int D, int kCache>
+template <int D, int kCache>
 __device__ __forceinline__ float4 chunk_load4(const ChunkParams &P, int b, int h, int t, int x, int c) {
     if (kCache == kCacheRows && !P.paged) {
-        const T *p = static_cast<const T *>(x ? P.vc : P.kc) + (((size_t)b * P.Hkv + h) * P.capacity + t) * D + c;
-        return make_float4(load_f(p), load_f(p + 1), load_f(p + 2), load_f(p + 3));
+        const float *p = static_cast<const float *>(x ? P.vc : P.kc) + (((size_t)b * P.Hkv + h) * P.capacity + t) * D + c;
+        return *reinterpret_cast<const float4 *>(p);
     }
     const int page = __ldg(P.page_table + (size_t)b * P.max_pages + t / P.ps), off = t % P.ps;
     if (page < 0 || page >= P.n_pages) {
@@ -51,15 +51,15 @@ __device__ __forceinline__ float4 chunk_load4(const ChunkParams &P, int b, int h
         const float2 lo = from_e4m3x2(w & 0xffffu), hi = from_e4m3x2(w >> 16);
         return make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s);
     }
-    const T *p = static_cast<const T *>(x ? P.vc : P.kc) +
+    const float *p = static_cast<const float *>(x ? P.vc : P.kc) +
                  ((((size_t)page * P.Hkv + h) * (D / 64) + c / 64) * P.ps + off) * 64 + c % 64;
-    return make_float4(load_f(p), load_f(p + 1), load_f(p + 2), load_f(p + 3));
+    return *reinterpret_cast<const float4 *>(p);
 }
 
 // The CUDA-core kernel, everything in fp32.  128 threads: thread (ty, tx) has
 // the scores of rows 4 ty .. + 3 and keys tx + 16 i, and the outputs of the
 // same rows and dimensions 4 tx + 64 i .. + 3.
-template <typename T, int D, int kCache>
+template <int D, int kCache>
 __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm) chunk_simt_kernel(ChunkParams P) {
     pdl_wait();
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -78,9 +78,9 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm) chunk_simt_kernel(Ch
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < nr) {
                 const long long p = r0 + r;
-                const T *src = static_cast<const T *>(P.q) + (u.first + p / P.G) * P.stride_q +
+                const float *src = static_cast<const float *>(P.q) + (u.first + p / P.G) * P.stride_q +
                                ((long long)u.h * P.G + p % P.G) * D + c;
-                x = make_float4(load_f(src), load_f(src + 1), load_f(src + 2), load_f(src + 3));
+                x = *reinterpret_cast<const float4 *>(src);
             }
             *reinterpret_cast<float4 *>(&sh.q[r][c]) = x;
         }
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm) chunk_simt_kernel(Ch
                 const int t = i / (D / 4), c = (i % (D / 4)) * 4;
                 float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
                 if (t < nk) {
-                    k = chunk_load4<T, D, kCache>(P, u.b, u.h, t0 + t, 0, c);
-                    v = chunk_load4<T, D, kCache>(P, u.b, u.h, t0 + t, 1, c);
+                    k = chunk_load4<D, kCache>(P, u.b, u.h, t0 + t, 0, c);
+                    v = chunk_load4<D, kCache>(P, u.b, u.h, t0 + t, 1, c);
                     odd = odd || !(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY &&
                                    fabsf(v.w) < INFINITY);
                 }
@@ -201,12 +201,12 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm) chunk_simt_kernel(Ch
             if (r >= nr) continue;
             if (whole) {
                 const long long p = r0 + r, row = u.first + p / P.G, hq = (long long)u.h * P.G + p % P.G;
-                T *o = static_cast<T *>(P.o) + (row * P.Hq + hq) * D;
+                float *o = static_cast<float *>(P.o) + (row * P.Hq + hq) * D;
                 const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) store_f(o + tx * 4 + 64 * c + e, acc[i][c][e] * inv);
+                    *reinterpret_cast<float4 *>(o + tx * 4 + 64 * c) =
+                        make_float4(acc[i][c][0] * inv, acc[i][c][1] * inv, acc[i][c][2] * inv, acc[i][c][3] * inv);
                 if (tx == 0)
                     P.lse[row * P.Hq + hq] = l[i] == 0.f ? -INFINITY
                                              : l[i] != l[i] ? l[i]
@@ -330,10 +330,7 @@ ChunkPlan simt_plan() {
 }
 
 ChunkPlan plan_of(const ChunkParams &P, int dtype, bool kv8) {
-    (void)dtype;
-    (void)kv8;
-    (void)P;
-    return simt_plan();
+    return dtype == SPEC_BF16 ? chunk_tc_plan(P, kv8) : simt_plan();
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -393,6 +390,7 @@ spec_status_t chunk_cache(const spec_chunk_desc *a, const spec_kv_desc *c, Chunk
     // (tensor copies count rows of 64 elements, and heads, in 32 bits)
     const long long tiles = P.paged ? (long long)c->n_pages * P.Hkv * (P.d / 64) : (long long)c->batch * P.Hkv;
     if (tiles > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
+    P.cache_heads = tiles;
     P.kc = c->k;
     P.vc = c->v;
     P.page_table = c->page_table;
@@ -427,11 +425,11 @@ spec_status_t chunk_plan(const ChunkParams &P, int dtype, bool kv8, ChunkPlan &p
     return SPEC_OK;
 }
 
-template <typename T, int kCache>
+template <int kCache>
 spec_status_t launch_simt(const ChunkParams &P, int n_cta, cudaStream_t s) {
     const bool wide = P.d == 128;
     const size_t smem = wide ? sizeof(ChunkSimtShared<128>) : sizeof(ChunkSimtShared<64>);
-    auto *f = wide ? chunk_simt_kernel<T, 128, kCache> : chunk_simt_kernel<T, 64, kCache>;
+    auto *f = wide ? chunk_simt_kernel<128, kCache> : chunk_simt_kernel<64, kCache>;
     if (set_smem_limit(reinterpret_cast<const void *>(f), smem) != SPEC_OK) return SPEC_ERR_CUDA;
     return launch(f, dim3(n_cta), dim3(kSimtThreads), smem, s, P);
 }
@@ -477,11 +475,8 @@ spec_status_t run_chunk(ChunkParams &P, int dtype, bool kv8, const void *q, long
     P.status = status_ptr();
     if (!P.status) return SPEC_ERR_CUDA;
     cudaStream_t s = as_stream(stream);
-    if (dtype == SPEC_BF16)
-        st = kv8 ? launch_simt<__nv_bfloat16, kCache8>(P, pl.n_cta, s)
-                 : launch_simt<__nv_bfloat16, kCacheRows>(P, pl.n_cta, s);
-    else
-        st = kv8 ? launch_simt<float, kCache8>(P, pl.n_cta, s) : launch_simt<float, kCacheRows>(P, pl.n_cta, s);
+    if (dtype == SPEC_BF16) st = launch_chunk_tc(P, kv8, pl.n_cta, s);
+    else st = kv8 ? launch_simt<kCache8>(P, pl.n_cta, s) : launch_simt<kCacheRows>(P, pl.n_cta, s);
     if (st != SPEC_OK) return st;
     const dim3 grid(pl.n_cta - 1, ceil_div(pl.ru, 4 * kMergeWarps)), block(kMergeWarps * 32);
     if (dtype == SPEC_BF16)

@@ -38,6 +38,7 @@ struct ChunkParams {
     int B, n_tokens, Hq, Hkv, G, d;
     int paged, ps, max_pages, n_pages;
     int capacity;            // tokens per request
+    long long cache_heads;   // contiguous: requests * heads of the cache
     int ru, ks;              // rows of a unit, keys of a step
     int fixed_cost;          // of a unit, in keys
     int min_share;           // least cost (keys) worth a CTA

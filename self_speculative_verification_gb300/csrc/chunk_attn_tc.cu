@@ -1,0 +1,879 @@
+// Tensor-core chunk attention (bf16 rows), over a bf16 cache or one in 8 bits.
+//
+// Design (GB300, tcgen05):
+// * A unit is 2 TB consecutive new tokens of one (request, KV head), TB =
+//   128 / G: two query tiles A and B of up to 128 packed rows (row t G + g:
+//   token t, query head g of the group), which share every K/V tile.  The
+//   persistent grid, one CTA per SM, takes equal shares of the call's cost, cut
+//   at 128-key steps (chunk_attn.cuh), so single tokens behind long histories
+//   and long prompts fill the GPU alike.
+// * Warps 0-3 run the softmax of tile A and 4-7 that of tile B, one row a
+//   thread; warp 8 copies the unit's queries and the cache's tiles, warp 9
+//   issues the MMAs from one thread.  The MMA thread interleaves the tiles --
+//   PV_A(j), S_A(j+1), PV_B(j), S_B(j+1) -- so the tensor core works on one
+//   while the other's softmax runs.
+// * bf16 cache: K and V tiles come by tensor copies, one a page and 64 elements,
+//   into a ring of 128-byte-swizzled slots.  Warps 10 and 11 look through the
+//   value tiles that not every row sees whole (the last ones of a unit): rows
+//   past the unit's last token become zeros, and non-finite values too, whose
+//   first place they note, for a hidden value's weight of zero would not keep
+//   it out of the sum.
+// * 8-bit cache: 16 tokens' codes, keys and values, are one run of memory, which
+//   a bulk copy brings into a stage; warps 12-15 turn them into the slots' bf16
+//   tiles (code * scale, exact for a power of two) and do what warps 10 and 11
+//   do on the way.
+// * Softmax and TMEM as in the prefill kernel: O (fp32) and S of a tile side by
+//   side, P (bf16) over the first half of S, the running maximum raised only
+//   when it grows by more than 2^8.
+// * Every wait is bounded; on expiry the kernel sets SPEC_DEV_TIMEOUT, stops
+//   issuing work, waits (bounded) for its own copies and MMAs, frees its TMEM
+//   and returns.
+#include "chunk_attn.cuh"
+#include "kv8_common.cuh"
+#include "ptx_sm103.cuh"
+
+namespace sv {
+namespace {
+
+namespace ctc {
+
+constexpr int kM = 128;                  // rows of a query tile
+constexpr int kN = 128;                  // keys of a step
+constexpr int kHalf = 128 * 128;         // 128 rows x 64 bf16
+constexpr int kGroupWarps = 4;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kFixWarp = 10;             // bf16 cache: 10 and 11
+constexpr int kConvWarp = 12;            // 8-bit cache: 12 .. 15
+constexpr int kTmemCols = 512;
+constexpr int kBadRing = 8;
+__host__ __device__ constexpr uint32_t col_o(int x) { return 256u * (uint32_t)x; }
+__host__ __device__ constexpr uint32_t col_s(int x) { return 256u * (uint32_t)x + 128u; }
+constexpr float kRescale = 8.f;          // log2 growth allowed before rescaling
+constexpr int kMaxSlots = 12, kMaxStages = 4;
+
+// Sizes by head_dim and cache.  Registers: the launch gives every thread
+// kLaunchRegs, the softmax warpgroups raise theirs and the others lower; the
+// sum must fit the launch's, or the raise would wait forever.
+template <int D, bool K8>
+struct Cfg {
+    static constexpr int NH = D / 64;
+    static constexpr int kTile = NH * kHalf;             // a Q, K or V tile
+    static constexpr int kSlots = D == 128 ? (K8 ? 3 : 5) : 8;
+    static constexpr int kStages = K8 ? (D == 128 ? 2 : 4) : 0;
+    static constexpr int kStage = 2 * kN * D;            // codes of a step, K and V
+    static constexpr int kWarps = K8 ? 16 : 12;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kLaunchRegs = K8 ? 128 : 168;
+    static constexpr int kSoftmaxRegs = K8 ? 176 : 184;
+    static constexpr int kOtherRegs = K8 ? 80 : 128;
+    static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
+                  "register split exceeds the launch allocation");
+};
+
+struct Params {
+    ChunkParams c;
+    int tb;                  // tokens of a query tile
+    int box;                 // tokens of a tensor copy (paged: of one page)
+    uint32_t ps_mul;         // t / ps = (t ps_mul) >> 31 + ps_shift, t < 2^30
+    int ps_shift;
+};
+
+struct Shared {
+    uint64_t q_full, q_empty;
+    uint64_t full[kMaxSlots], empty[kMaxSlots], fixed[kMaxSlots];
+    uint64_t st_full[kMaxStages], st_empty[kMaxStages];
+    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int bad[kBadRing][4];    // by unit and looking warp: first token with a non-finite value
+    ChunkShare share;
+};
+
+template <int D, bool K8>
+constexpr size_t smem_bytes() {
+    using C = Cfg<D, K8>;
+    return (size_t)(2 + C::kSlots) * C::kTile + (size_t)C::kStages * C::kStage + sizeof(Shared) + 1024;
+}
+
+// A CTA's part of a unit, by query tiles.
+struct Tiles {
+    int tok[2];              // first token (within the request)
+    int nt[2];               // tokens
+    int steps[2];            // steps of the part that the tile takes
+    int seen0;               // tokens that the unit's first row sees
+    int lim;                 // tokens that its last row sees
+};
+
+__device__ __forceinline__ Tiles tiles_of(const Params &P, const ChunkPart &u) {
+    Tiles t;
+    t.tok[0] = u.j * 2 * P.tb;
+    t.tok[1] = t.tok[0] + P.tb;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        t.nt[x] = max(0, min(P.tb, u.n - t.tok[x]));
+        const int end = (u.S + t.tok[x] + t.nt[x] + kN - 1) / kN;      // its last row's steps
+        t.steps[x] = t.nt[x] > 0 ? max(0, min(u.s1, end) - u.s0) : 0;
+    }
+    t.seen0 = u.S + t.tok[0] + 1;
+    t.lim = u.S + t.tok[0] + t.nt[0] + t.nt[1];
+    return t;
+}
+
+// Whether step s holds tokens that some row of the unit does not see.
+__device__ __forceinline__ bool ragged(const Tiles &t, int s) { return (s + 1) * kN > t.seen0; }
+
+__device__ __forceinline__ int page_of(const Params &P, int t) {
+    return (int)(((uint64_t)(uint32_t)t * P.ps_mul) >> P.ps_shift);
+}
+
+// 16 bytes of eight bf16: whether one of them is not finite.
+__device__ __forceinline__ bool odd8(const uint4 &v) {
+    const uint32_t m = 0x7f807f80u, one = 0x00800080u;
+    return ((((v.x & m) + one) | ((v.y & m) + one) | ((v.z & m) + one) | ((v.w & m) + one)) & 0x80008000u) != 0;
+}
+
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// global -> shared bulk copy; both 16-byte aligned, bytes a multiple of 16
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Four e4m3 codes as bf16 times 2^-120: sign, and exponent and mantissa in the
+// low bits of bf16's (subnormal codes become subnormal).  NaN codes are not
+// told apart.
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+    return make_uint2((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u));
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// 16 codes times their scale as bf16.  `pow2`: the scale is 2^e, given as the
+// bf16 pairs 2^64 and 2^(56 + e); their products are exact.
+__device__ __forceinline__ void widen16(const uint4 &codes, float scale, bool pow2, uint32_t m1, uint32_t m2, uint4 &lo,
+                                        uint4 &hi) {
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t nan = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+    uint32_t out[8];
+    if (pow2 && !(nan & 0x80808080u)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint2 x = widen4(w[i]);
+            out[2 * i] = mul2(mul2(x.x, m1), m2);
+            out[2 * i + 1] = mul2(mul2(x.y, m1), m2);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = from_e4m3x2(w[i] & 0xffffu), b = from_e4m3x2(w[i] >> 16);
+            out[2 * i] = pack_bf16(a.x * scale, a.y * scale);
+            out[2 * i + 1] = pack_bf16(b.x * scale, b.y * scale);
+        }
+    }
+    lo = make_uint4(out[0], out[1], out[2], out[3]);
+    hi = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+}  // namespace ctc
+
+template <int D, bool K8>
+__global__ void __launch_bounds__(ctc::Cfg<D, K8>::kThreads, 1)
+chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ CUtensorMap mq,
+                const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using namespace ctc;
+    using namespace tc5;
+    using C = Cfg<D, K8>;
+    constexpr int NH = C::NH, kTile = C::kTile, kSlots = C::kSlots;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *qbuf = smem;                                // query tiles A and B
+    uint8_t *ring = smem + 2 * kTile;                    // kSlots K / V tiles
+    uint8_t *stages = ring + kSlots * kTile;             // 8 bits: codes
+    Shared &sh = *reinterpret_cast<Shared *>(stages + C::kStages * C::kStage);
+    const ChunkParams &A = P.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == kProducerWarp * 32) {
+        const CUtensorMap *maps[3] = {&mq, &mk, &mv};
+        for (int i = 0; i < (K8 ? 1 : 3); ++i)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i]))
+                         : "memory");
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_empty, 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&sh.s_full[x], 1);
+            mbar_init(&sh.p_full[x], kGroupWarps);
+            mbar_init(&sh.o_done[x], 1);
+            mbar_init(&sh.o_free[x], kGroupWarps);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&sh.full[s], K8 ? 4 : 1);
+            mbar_init(&sh.empty[s], K8 ? 1 : 3);
+            mbar_init(&sh.fixed[s], 2);
+        }
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&sh.st_full[s], 1);
+            mbar_init(&sh.st_empty[s], 4);
+        }
+        mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // the rows of the query tiles that hold no query (128 is not a multiple of G)
+    const int rows = P.tb * A.G;
+    for (int i = threadIdx.x; i < (kM - rows) * 2 * NH * 8; i += C::kThreads) {
+        const int r = rows + i / (2 * NH * 8), c = i % (2 * NH * 8);
+        *reinterpret_cast<uint4 *>(qbuf + (c / 8) * kHalf + r * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_async();
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sh.tmem_base)),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_wait();
+    fence_before();
+    chunk_share<C::kThreads>(A, sh.share);
+    fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    volatile int *abort = &sh.abort;
+    const long long wait = A.wait;
+    ChunkWalk walk(A, sh.share);
+    ChunkPart u;
+
+    if (warp >= kProducerWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+        if (warp == kProducerWarp) {
+            // ------------------------------------------------------ producer
+            // The whole warp walks; lane i issues copy i of a tile.
+            const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
+            const int per = kN / P.box;                  // copies a tile, by tokens
+            const int hh = lane % NH, bx = lane / NH;    // rows cache: this lane's copy
+            int slot = 0, nu = 0;                        // next slot (8 bits: stage); units
+            uint32_t ph = 1;                             // parity of its release
+            long long ld = 0;                            // fills issued
+            bool ok = true;
+            while (ok && walk.next(A, u)) {
+                const Tiles t = tiles_of(P, u);
+                const int tiles = t.steps[1] > 0 ? 2 : 1;
+                if (!mbar_wait_warp(&sh.q_empty, (uint32_t)((nu & 1) ^ 1), wait)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(tiles * NH * rows * 128));
+                __syncwarp();
+                if (lane < tiles * NH)
+                    tma_load_3d(qbuf + lane * kHalf, &mq, (lane % NH) * 64, u.h * A.G, u.first + t.tok[lane / NH],
+                                &sh.q_full, pol_q);
+                ++nu;
+                const int32_t *table = A.paged ? A.page_table + (size_t)u.b * A.max_pages : nullptr;
+                // the page of this lane's copy, loaded a step ahead of its use
+                const int at = K8 ? lane * 16 : bx * P.box;
+                const bool mine = K8 ? lane < kN / 16 : bx < per;
+                auto page_id = [&](int s) -> int {
+                    const int tok = s * kN + at;
+                    return A.paged && mine && s < u.s1 && tok < t.lim ? __ldg(table + page_of(P, tok)) : -1;
+                };
+                int next_id = page_id(u.s0);
+                for (int s = u.s0; s < u.s1 && ok; ++s) {
+                    const int id = next_id, tok = s * kN + at;
+                    next_id = page_id(s + 1);
+                    bool in = mine && tok < t.lim;
+                    if (in && A.paged && (id < 0 || id >= A.n_pages)) {
+                        in = false;
+                        raise_status(A.status, SPEC_DEV_BAD_PAGE);
+                    }
+                    const int off = A.paged ? tok - page_of(P, tok) * A.ps : tok;
+                    const uint32_t n_in = (uint32_t)__popc(__ballot_sync(0xffffffffu, in));
+                    if constexpr (K8) {
+                        if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.st_empty[slot], ph, wait)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&sh.st_full[slot], n_in * (32 * D));
+                        __syncwarp();
+                        if (in)
+                            bulk_load(stages + slot * C::kStage + lane * (32 * D),
+                                      static_cast<const uint8_t *>(A.kc) + kv8_block(id, u.h, A.Hkv, A.ps, D) +
+                                          (size_t)off * (2 * D),
+                                      32 * D, &sh.st_full[slot]);
+                        ++ld;
+                        if (++slot == C::kStages) {
+                            slot = 0;
+                            ph ^= 1u;
+                        }
+                    } else {
+                        for (int kv = 0; kv < 2; ++kv) {
+                            if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.empty[slot], ph, wait)) {
+                                ok = false;
+                                break;
+                            }
+                            if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], n_in * (uint32_t)(P.box * 128));
+                            __syncwarp();
+                            uint8_t *dst = ring + slot * kTile + hh * kHalf + bx * P.box * 128;
+                            if (in && A.paged)
+                                tma_load_3d(dst, kv ? &mv : &mk, 0, off, (id * A.Hkv + u.h) * NH + hh, &sh.full[slot],
+                                            pol_kv);
+                            else if (in)
+                                tma_load_3d(dst, kv ? &mv : &mk, hh * 64, tok, u.b * A.Hkv + u.h, &sh.full[slot],
+                                            pol_kv);
+                            ++ld;
+                            if (++slot == kSlots) {
+                                slot = 0;
+                                ph ^= 1u;
+                            }
+                        }
+                    }
+                }
+            }
+            if (lane == 0) {
+                if (!ok) {
+                    raise_status(A.status, SPEC_DEV_TIMEOUT);
+                    *abort = 1;
+                }
+                // do not leave while copies into this CTA's shared memory are in
+                // flight (earlier ones were consumed, hence complete)
+                constexpr int kFills = K8 ? C::kStages : kSlots;
+                uint64_t *bars = K8 ? sh.st_full : sh.full;
+                for (long long i = ld - 1; i >= 0 && i >= ld - kFills; --i)
+                    if (!mbar_wait(&bars[i % kFills], (uint32_t)((i / kFills) & 1))) {
+                        raise_status(A.status, SPEC_DEV_TIMEOUT);
+                        break;
+                    }
+                if (nu > 0 && !mbar_wait(&sh.q_full, (uint32_t)((nu - 1) & 1)))
+                    raise_status(A.status, SPEC_DEV_TIMEOUT);
+            }
+        } else if (warp == kMmaWarp) {
+            // --------------------------------------------------- MMA issuer
+            if (lane == 0) {
+                const uint32_t id_s = idesc(kM, kN, false, false);
+                const uint32_t id_pv = idesc(kM, D, false, true);
+                int slot = 0;                            // ring slot of the next K / V tile
+                uint32_t ph = 0, fix_ph = 0;             // parity of its fill; of the fixes, a bit a slot
+                int nu = 0;                              // parts started
+                int np[2] = {0, 0};                      // P hand-offs taken, per tile
+                int nact[2] = {0, 0};                    // parts in which the tile took part
+                bool ok = true;
+                const uint64_t qd[2] = {smem_desc(smem_u32(qbuf), 16, 1024),
+                                        smem_desc(smem_u32(qbuf + kTile), 16, 1024)};
+                // descriptors of slot 0 (K: K-major, V: MN-major); a slot is kTile
+                // further, i.e. kTile >> 4 in the address field
+                const uint64_t kd0 = smem_desc(smem_u32(ring), 16, 1024);
+                const uint64_t vd0 = smem_desc(smem_u32(ring), kHalf, 1024);
+                auto advance = [&]() {
+                    if (++slot == kSlots) {
+                        slot = 0;
+                        ph ^= 1u;
+                    }
+                };
+                auto issue_s = [&](int x, int k_slot) {
+                    const uint64_t kd = kd0 + (uint64_t)(k_slot * (kTile >> 4));
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint64_t off = (uint64_t)((((ks >> 2) * kHalf) + (ks & 3) * 32) >> 4);
+                        mma_ss(tmem + col_s(x), qd[x] + off, kd + off, id_s, ks > 0 ? 1u : 0u);
+                    }
+                    commit(&sh.s_full[x]);
+                };
+                // O_x += P_x V; the tile's first PV of a part overwrites O_x, after
+                // the previous part's epilogue of that tile read it
+                auto issue_pv = [&](int x, int v_slot, bool first) -> bool {
+                    if (!mbar_wait(&sh.p_full[x], (uint32_t)(np[x] & 1), wait)) return false;
+                    ++np[x];
+                    if (first && nact[x] > 0 &&
+                        !mbar_wait(&sh.o_free[x], (uint32_t)((nact[x] - 1) & 1), wait))
+                        return false;
+                    fence_after();
+                    const uint64_t vd = vd0 + (uint64_t)(v_slot * (kTile >> 4));
+#pragma unroll
+                    for (int ks = 0; ks < kN / 16; ++ks)
+                        mma(tmem + col_o(x), tmem + col_s(x) + ks * 8,
+                            vd + (uint64_t)((ks * 2048) >> 4), id_pv, (ks > 0 || !first) ? 1u : 0u);
+                    return true;
+                };
+                while (ok && walk.next(A, u)) {
+                    const Tiles t = tiles_of(P, u);
+                    const int nA = t.steps[0], nB = t.steps[1], n = u.s1 - u.s0;
+                    if (*abort || !mbar_wait(&sh.q_full, (uint32_t)(nu & 1), wait) ||
+                        !mbar_wait(&sh.full[slot], ph, wait)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    // S(0) of both tiles
+                    if (nA > 0) issue_s(0, slot);
+                    if (nB > 0) issue_s(1, slot);
+                    commit(&sh.empty[slot]);
+                    if (n == 1) commit(&sh.q_empty);
+                    advance();
+                    for (int j = 0; j < n; ++j) {
+                        const int vslot = slot;
+                        if (!mbar_wait(&sh.full[vslot], ph, wait)) {
+                            ok = false;
+                            break;
+                        }
+                        if (!K8 && ragged(t, u.s0 + j)) {
+                            if (!mbar_wait(&sh.fixed[vslot], (fix_ph >> vslot) & 1u, wait)) {
+                                ok = false;
+                                break;
+                            }
+                            fix_ph ^= 1u << vslot;
+                        }
+                        advance();
+                        const bool next = j + 1 < n;
+                        const int kslot = slot;
+                        if (next && !mbar_wait(&sh.full[kslot], ph, wait)) {
+                            ok = false;
+                            break;
+                        }
+                        if (j < nA) {
+                            if (!issue_pv(0, vslot, j == 0)) {
+                                ok = false;
+                                break;
+                            }
+                            if (j + 1 == nA) commit(&sh.o_done[0]);
+                            else issue_s(0, kslot);
+                        }
+                        if (j < nB) {
+                            if (!issue_pv(1, vslot, j == 0)) {
+                                ok = false;
+                                break;
+                            }
+                            if (j + 1 == nB) commit(&sh.o_done[1]);
+                            commit(&sh.empty[vslot]);
+                            if (j + 1 < nB) issue_s(1, kslot);
+                        } else {
+                            commit(&sh.empty[vslot]);
+                        }
+                        if (next) {
+                            commit(&sh.empty[kslot]);
+                            if (j + 2 == n) commit(&sh.q_empty);
+                            advance();
+                        }
+                    }
+                    if (nA > 0) ++nact[0];
+                    if (nB > 0) ++nact[1];
+                    ++nu;
+                }
+                if (!ok) {
+                    raise_status(A.status, SPEC_DEV_TIMEOUT);
+                    *abort = 1;
+                }
+                // every MMA issued above has completed before TMEM is released
+                commit(&sh.drain);
+                if (!mbar_wait(&sh.drain, 0)) raise_status(A.status, SPEC_DEV_TIMEOUT);
+            }
+        } else if (!K8 && (warp == kFixWarp || warp == kFixWarp + 1)) {
+            // ------------------------- values that not every row sees, looked over
+            // (Both warps see every fill of the ring, and release it with the MMAs:
+            // a warp that skipped fills could take an earlier phase for its own.)
+            const int tid = threadIdx.x - kFixWarp * 32;
+            int slot = 0, nu = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            while (ok && walk.next(A, u)) {
+                const Tiles t = tiles_of(P, u);
+                int *bad = &sh.bad[nu++ % kBadRing][warp - kFixWarp];
+                bool fresh = true;
+                for (int i = 2 * u.s0; i < 2 * u.s1; ++i) {
+                    const int s = i >> 1;
+                    if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.full[slot], ph, wait)) {
+                        ok = false;
+                        break;
+                    }
+                    if ((i & 1) && ragged(t, s)) {
+                        if (fresh) {
+                            if (lane == 0) *bad = 0x7fffffff;
+                            __syncwarp();
+                            fresh = false;
+                        }
+                        uint8_t *v = ring + slot * kTile;
+                        const int r0 = max(0, t.seen0 - s * kN), r1 = t.lim - s * kN;
+                        for (int k = r0 * (NH * 8) + tid; k < kN * NH * 8; k += 64) {
+                            const int r = k / (NH * 8), c = k % (NH * 8);
+                            uint4 *p = reinterpret_cast<uint4 *>(v + (c / 8) * kHalf + r * 128 + (((c % 8) ^ (r & 7)) << 4));
+                            bool zero = r >= r1;
+                            if (!zero && odd8(*p)) {
+                                atomicMin(bad, s * kN + r);
+                                zero = true;
+                            }
+                            if (zero) *p = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.fixed[slot]);
+                    }
+                    if (lane == 0) mbar_arrive(&sh.empty[slot]);
+                    if (++slot == kSlots) {
+                        slot = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok && lane == 0) {
+                raise_status(A.status, SPEC_DEV_TIMEOUT);
+                *abort = 1;
+            }
+        } else if (K8 && warp >= kConvWarp) {
+            // ----------------------------------------- codes into bf16 tiles
+            constexpr int kStages = C::kStages > 0 ? C::kStages : 1;
+            const int tid = threadIdx.x - kConvWarp * 32;
+            int slot = 0, stage = 0, nu = 0;
+            uint32_t ph = 1, sph = 0;                    // parity of the slot's release; of the stage's fill
+            bool ok = true;
+            while (ok && walk.next(A, u)) {
+                const Tiles t = tiles_of(P, u);
+                int *bad = &sh.bad[nu++ % kBadRing][warp - kConvWarp];
+                bool fresh = true;
+                const int32_t *table = A.page_table + (size_t)u.b * A.max_pages;
+                // scales of the step's eight groups of 16 tokens: lane 2 i + x has
+                // group i's of K (x = 0) or V; loaded a step ahead
+                auto load_scale = [&](int s) -> float {
+                    const int tok = s * kN + (lane >> 1) * 16;
+                    if (lane >= 16 || s >= u.s1 || tok >= t.lim) return 1.f;
+                    const int id = __ldg(table + page_of(P, tok));
+                    if (id < 0 || id >= A.n_pages) return 1.f;
+                    return __ldg(A.scales + ((size_t)id * A.Hkv + u.h) * 2 + (lane & 1));
+                };
+                float next_scale = load_scale(u.s0);
+                for (int s = u.s0; s < u.s1 && ok; ++s) {
+                    const float my_scale = kv8_read_scale(next_scale);
+                    next_scale = load_scale(s + 1);
+                    if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.st_full[stage], sph, wait)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool rag = ragged(t, s);
+                    if (rag && fresh) {
+                        if (lane == 0) *bad = 0x7fffffff;
+                        __syncwarp();
+                        fresh = false;
+                    }
+                    const uint8_t *codes = stages + stage * C::kStage;
+                    for (int x = 0; x < 2; ++x) {
+                        if (!mbar_wait_warp(&sh.empty[slot], ph, wait)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *dst = ring + slot * kTile;
+                        constexpr int CPT = D / 16;      // 16-code vectors of a token
+                        constexpr int TPI = 128 / CPT;   // tokens a round (16 or 32)
+                        const int c = tid % CPT, tr = tid / CPT;
+#pragma unroll
+                        for (int i = 0; i < kN / TPI; ++i) {
+                            const int r = i * TPI + tr;
+                            const float scale = __shfl_sync(0xffffffffu, my_scale, (r >> 4) * 2 + x);
+                            const uint32_t sb = __float_as_uint(scale);
+                            const bool pow2 = (sb & 0x007fffffu) == 0u;  // (finite ones lie in 2^-60 .. 2^60)
+                            const uint32_t e2 = ((sb >> 23) + 56) << 7;  // bf16 2^(56 + e)
+                            const uint4 v = *reinterpret_cast<const uint4 *>(
+                                codes + (r >> 4) * (32 * D) + kv8_row(r & 15, x, D) + c * 16);
+                            uint4 lo, hi;
+                            widen16(v, scale, pow2, 0x5f805f80u, e2 | (e2 << 16), lo, hi);
+                            if (rag) {
+                                const int tok = s * kN + r;
+                                if (tok >= t.lim) {
+                                    lo = hi = make_uint4(0u, 0u, 0u, 0u);
+                                } else if (x == 1 && tok >= t.seen0 && (odd8(lo) || odd8(hi))) {
+                                    atomicMin(bad, tok);
+                                    lo = hi = make_uint4(0u, 0u, 0u, 0u);
+                                }
+                            }
+                            uint8_t *p = dst + (c / 4) * kHalf + r * 128;
+                            *reinterpret_cast<uint4 *>(p + (((2 * (c % 4)) ^ (r & 7)) << 4)) = lo;
+                            *reinterpret_cast<uint4 *>(p + (((2 * (c % 4) + 1) ^ (r & 7)) << 4)) = hi;
+                        }
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.full[slot]);
+                        if (++slot == kSlots) {
+                            slot = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(&sh.st_empty[stage]);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        sph ^= 1u;
+                    }
+                }
+            }
+            if (!ok && lane == 0) {
+                raise_status(A.status, SPEC_DEV_TIMEOUT);
+                *abort = 1;
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+        // ------------------------------------------------------ softmax
+        const int x = warp / kGroupWarps;               // query tile A (0) or B (1)
+        const int r = (warp % kGroupWarps) * 32 + lane; // row of the tile
+        const uint32_t lane_base = (uint32_t)((warp % kGroupWarps) * 32) << 16;
+        const uint32_t tS = tmem + lane_base + col_s(x), tO = tmem + lane_base + col_o(x);
+        const float sc = A.scale_log2;
+        const int rt = r / A.G, rg = r - rt * A.G;       // the row's token and query head
+        int ns = 0, nact = 0, nu = 0;      // S hand-offs taken; parts this tile took part in; parts
+        bool ok = true;
+        while (ok && walk.next(A, u)) {
+            const Tiles t = tiles_of(P, u);
+            const int unit = nu++;
+            if (t.nt[x] == 0) continue;
+            const bool row_ok = rt < t.nt[x];
+            const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+            const int seen = u.S + t.tok[x] + rt + 1;    // tokens this row sees
+            const int sure = u.S + t.tok[x] + 1;         // and the tile's first row
+            const bool whole = u.s0 == 0 && u.s1 == u.steps;
+            const size_t part = (size_t)chunk_slot(u) * A.ru + x * rows + r;
+            if (t.steps[x] == 0) {                       // (tile A is through: an empty part)
+                if (row_ok) A.part_ml[part] = make_float2(-INFINITY, 0.f);
+                continue;
+            }
+            float m_used = -INFINITY, l = 0.f;
+            for (int j = 0; j < t.steps[x]; ++j) {
+                if (__any_sync(0xffffffffu, *abort != 0) ||
+                    !mbar_wait_warp(&sh.s_full[x], (uint32_t)(ns & 1), wait)) {
+                    ok = false;
+                    break;
+                }
+                ++ns;
+                fence_after();
+                if (!warp_ok) {                          // (rows without a query: P is whatever is there)
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_full[x]);
+                    continue;
+                }
+                const int c0 = (u.s0 + j) * kN;
+                const bool masked = c0 + kN > sure;
+                // the S row: four TMEM loads in flight, one wait (each
+                // wait_ld ties its registers; the later ones return at once)
+                uint32_t v[kN / 32][32];
+#pragma unroll
+                for (int c = 0; c < kN / 32; ++c) ld32(tS + c * 32, v[c]);
+#pragma unroll
+                for (int c = 0; c < kN / 32; ++c) wait_ld(v[c]);
+                // hidden scores become -inf in place
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < kN / 32; ++c) {
+                        const int n = seen - c0 - c * 32;
+                        const uint32_t vm = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[c][e] = ((vm >> e) & 1u) ? v[c][e] : 0xff800000u;
+                    }
+                }
+                // the row maximum (three-input max, four chains)
+                float tmv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < kN / 32; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tmv[q] = max3(tmv[q], __uint_as_float(v[c][e + 2 * q]),
+                                          __uint_as_float(v[c][e + 2 * q + 1]));
+                const float traw = fmaxf(fmaxf(tmv[0], tmv[1]), fmaxf(tmv[2], tmv[3]));
+                const float tm = traw == -INFINITY ? -INFINITY : traw * sc;
+                const bool raise = tm > m_used + kRescale || (m_used == -INFINITY && tm != -INFINITY);
+                // (a sum that is NaN before any maximum stays so)
+                const float alpha =
+                    !raise ? 1.f : (m_used == -INFINITY) ? 1.f : fast_exp2(m_used - tm);
+                // O holds every earlier PV of this tile (issued before the S
+                // just waited for): rescale the rows that raised their max
+                // (TMEM loads and stores are warp-collective: the whole warp
+                // takes part, the other rows scaled by exactly 1)
+                const bool scale_o = raise && j > 0 && m_used != -INFINITY;
+                if (__any_sync(0xffffffffu, scale_o)) {
+                    const float a = scale_o ? alpha : 1.f;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        ld32(tO + c * 32, o);
+                        wait_ld(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                        st32(tO + c * 32, o);
+                    }
+                }
+                if (raise) {
+                    l *= alpha;
+                    m_used = tm;
+                }
+                const float mu = m_used == -INFINITY ? 0.f : m_used;
+                // P = exp2(s * scale - mu) (pairs: one f32x2 FMA, two ex2,
+                // one f32x2 add, one pack) over the first 64 columns of S
+                const uint64_t sc2 = pair(sc, sc), nmu2 = pair(-mu, -mu);
+                uint64_t rs2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < kN / 32; ++c) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float t0, t1;
+                        unpair(fma2(pair(__uint_as_float(v[c][2 * e]),
+                                         __uint_as_float(v[c][2 * e + 1])),
+                                    sc2, nmu2),
+                               t0, t1);
+                        const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                        rs2[e & 1] = add2(rs2[e & 1], pair(p0, p1));
+                        pw[e] = pack_bf16(p0, p1);
+                    }
+                    st16(tS + c * 16, pw);
+                }
+                float rs[4];
+                unpair(rs2[0], rs[0], rs[1]);
+                unpair(rs2[1], rs[2], rs[3]);
+                l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[x]);
+            }
+            if (!ok) break;
+            // epilogue: O / l (bf16) and the LSE of this row, or its part of them
+            if (!mbar_wait_warp(&sh.o_done[x], (uint32_t)(nact & 1), wait)) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            // a non-finite value among those looked over, which this row sees
+            bool odd = false;
+            if (ragged(t, u.s0 + t.steps[x] - 1)) {
+                const volatile int *bad = sh.bad[unit % kBadRing];
+                for (int w = 0; w < (K8 ? 4 : 2); ++w) odd = odd || seen > bad[w];
+            }
+            const float inv = odd ? __uint_as_float(0x7fffffffu) : whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            const long long row = u.first + t.tok[x] + rt, hq = (long long)u.h * A.G + rg;
+            if (warp_ok) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    ld32(tO + c * 32, v);
+                    wait_ld(v);
+                    if (!row_ok) continue;
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.o) +
+                                                               (row * A.Hq + hq) * D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            dst[e / 8] = make_uint4(
+                                pack_bf16(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv),
+                                pack_bf16(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv),
+                                pack_bf16(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv),
+                                pack_bf16(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv));
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(A.part_o + part * D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            dst[e / 4] = make_float4(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv,
+                                                     __uint_as_float(v[e + 2]) * inv,
+                                                     __uint_as_float(v[e + 3]) * inv);
+                    }
+                }
+                if (row_ok) {
+                    if (whole)
+                        A.lse[row * A.Hq + hq] = l == 0.f ? -INFINITY : l != l ? l : (m_used + log2f(l)) * kLn2;
+                    else
+                        A.part_ml[part] = make_float2(m_used, l);
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_free[x]);
+            ++nact;
+        }
+        if (!ok) {
+            if (lane == 0) raise_status(A.status, SPEC_DEV_TIMEOUT);
+            *abort = 1;
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == kMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols));
+}
+
+template <int D, bool K8>
+spec_status_t launch_tc(const ctc::Params &P, const CUtensorMap (&m)[3], int n_cta, cudaStream_t s) {
+    constexpr size_t smem = ctc::smem_bytes<D, K8>();
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    if (set_smem_limit(reinterpret_cast<const void *>(chunk_tc_kernel<D, K8>), smem) != SPEC_OK)
+        return SPEC_ERR_CUDA;
+    return launch(chunk_tc_kernel<D, K8>, dim3(n_cta), dim3(ctc::Cfg<D, K8>::kThreads), smem, s, P, m[0], m[1], m[2]);
+}
+
+}  // namespace
+
+ChunkPlan chunk_tc_plan(const ChunkParams &P, bool kv8) {
+    (void)kv8;
+    const int tb = ctc::kM / P.G;
+    return ChunkPlan{2 * tb * P.G, ctc::kN, 2 * ctc::kN, 2 * ctc::kN, num_sms()};
+}
+
+spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStream_t s) {
+    ctc::Params P{};
+    P.c = C;
+    P.tb = ctc::kM / C.G;
+    P.box = ctc::kN;
+    if (C.paged) {
+        int a = C.ps, b = ctc::kN;                       // the greatest common divisor
+        while (b) {
+            const int r = a % b;
+            a = b;
+            b = r;
+        }
+        P.box = a;
+        // floor(t / ps) = (t m) >> (31 + L), L = ceil(log2 ps), m = ceil(2^(31 + L) / ps),
+        // exact for t < 2^31
+        int L = 0;
+        while ((1ll << L) < C.ps) ++L;
+        P.ps_shift = 31 + L;
+        P.ps_mul = (uint32_t)(((1ull << (31 + L)) + C.ps - 1) / C.ps);
+    }
+    CUtensorMap m[3] = {};
+    const cuuint64_t d0[3] = {(cuuint64_t)C.d, (cuuint64_t)C.Hq, (cuuint64_t)C.n_tokens};
+    const cuuint64_t s0[2] = {(cuuint64_t)C.d * 2, (cuuint64_t)C.stride_q * 2};
+    const cuuint32_t b0[3] = {64u, (cuuint32_t)C.G, (cuuint32_t)P.tb};
+    if (!encode_bf16_map(&m[0], C.q, 3, d0, s0, b0)) return SPEC_ERR_CUDA;
+    if (!kv8) {
+        const cuuint64_t nh = C.d / 64;
+        cuuint64_t d1[3] = {(cuuint64_t)C.d, (cuuint64_t)C.capacity, (cuuint64_t)C.cache_heads};
+        cuuint64_t s1[2] = {(cuuint64_t)C.d * 2, (cuuint64_t)C.capacity * C.d * 2};
+        if (C.paged) {
+            d1[0] = 64;
+            d1[1] = C.ps;
+            d1[2] = (cuuint64_t)C.n_pages * C.Hkv * nh;
+            s1[0] = 128;
+            s1[1] = (cuuint64_t)C.ps * 128;
+        }
+        const cuuint32_t b1[3] = {64u, (cuuint32_t)P.box, 1u};
+        if (!encode_bf16_map(&m[1], C.kc, 3, d1, s1, b1) || !encode_bf16_map(&m[2], C.vc, 3, d1, s1, b1))
+            return SPEC_ERR_CUDA;
+    }
+    if (C.d == 128) return kv8 ? launch_tc<128, true>(P, m, n_cta, s) : launch_tc<128, false>(P, m, n_cta, s);
+    return kv8 ? launch_tc<64, true>(P, m, n_cta, s) : launch_tc<64, false>(P, m, n_cta, s);
+}
+
+}  // namespace sv
