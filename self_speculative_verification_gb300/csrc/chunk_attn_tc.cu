@@ -46,7 +46,7 @@ constexpr int kMmaWarp = 9;
 constexpr int kFixWarp = 10;             // bf16 cache: 10 and 11
 constexpr int kConvWarp = 12;            // 8-bit cache: 12 .. 15
 constexpr int kTmemCols = 512;
-constexpr int kBadRing = 8;
+constexpr int kParts = 8;                // parts announced ahead
 __host__ __device__ constexpr uint32_t col_o(int x) { return 256u * (uint32_t)x; }
 __host__ __device__ constexpr uint32_t col_s(int x) { return 256u * (uint32_t)x + 128u; }
 constexpr float kRescale = 8.f;          // log2 growth allowed before rescaling
@@ -79,7 +79,22 @@ struct Params {
     int ps_shift;
 };
 
+// A CTA's part of a unit, as the producer announces it: n steps of 128 keys
+// from s0 on, of which tiles A and B take n_t[0] and n_t[1] (the tile with rows
+// that see fewer tokens ends earlier).
+struct Part {
+    int n;                   // 0: no more parts
+    int s0;
+    int b, h;
+    int row;                 // packed row of the unit's first token
+    int pos;                 // its position: it sees pos + 1 tokens
+    int lim;                 // tokens that the unit's last one sees
+    int nt[2], n_t[2];       // tokens and steps of each tile
+    int slot;                // where a part that is not a whole unit goes; -1: whole
+};
+
 struct Shared {
+    uint64_t part_full[kParts], part_free[kParts];
     uint64_t q_full, q_empty;
     uint64_t full[kMaxSlots], empty[kMaxSlots], fixed[kMaxSlots];
     uint64_t st_full[kMaxStages], st_empty[kMaxStages];
@@ -87,7 +102,8 @@ struct Shared {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    int bad[kBadRing][4];    // by unit and looking warp: first token with a non-finite value
+    int bad[kParts][4];      // by part and looking warp: first token with a non-finite value
+    Part parts[kParts];
     ChunkShare share;
 };
 
@@ -97,32 +113,53 @@ constexpr size_t smem_bytes() {
     return (size_t)(2 + C::kSlots) * C::kTile + (size_t)C::kStages * C::kStage + sizeof(Shared) + 1024;
 }
 
-// A CTA's part of a unit, by query tiles.
-struct Tiles {
-    int tok[2];              // first token (within the request)
-    int nt[2];               // tokens
-    int steps[2];            // steps of the part that the tile takes
-    int seen0;               // tokens that the unit's first row sees
-    int lim;                 // tokens that its last row sees
-};
-
-__device__ __forceinline__ Tiles tiles_of(const Params &P, const ChunkPart &u) {
-    Tiles t;
-    t.tok[0] = u.j * 2 * P.tb;
-    t.tok[1] = t.tok[0] + P.tb;
+__device__ __forceinline__ Part part_of(const Params &P, const ChunkPart &u) {
+    Part t;
+    const int tok = u.j * 2 * P.tb;
+    t.n = u.s1 - u.s0;
+    t.s0 = u.s0;
+    t.b = u.b;
+    t.h = u.h;
+    t.row = u.first + tok;
+    t.pos = u.S + tok;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        t.nt[x] = max(0, min(P.tb, u.n - t.tok[x]));
-        const int end = (u.S + t.tok[x] + t.nt[x] + kN - 1) / kN;      // its last row's steps
-        t.steps[x] = t.nt[x] > 0 ? max(0, min(u.s1, end) - u.s0) : 0;
+        t.nt[x] = max(0, min(P.tb, u.n - tok - x * P.tb));
+        const int end = (t.pos + x * P.tb + t.nt[x] + kN - 1) / kN;    // its last row's steps
+        t.n_t[x] = t.nt[x] > 0 ? max(0, min(u.s1, end) - u.s0) : 0;
     }
-    t.seen0 = u.S + t.tok[0] + 1;
-    t.lim = u.S + t.tok[0] + t.nt[0] + t.nt[1];
+    t.lim = t.pos + t.nt[0] + t.nt[1];
+    t.slot = u.s0 == 0 && u.s1 == u.steps ? -1 : chunk_slot(u);
     return t;
 }
 
 // Whether step s holds tokens that some row of the unit does not see.
-__device__ __forceinline__ bool ragged(const Tiles &t, int s) { return (s + 1) * kN > t.seen0; }
+__device__ __forceinline__ bool ragged(const Part &t, int s) { return (s + 1) * kN > t.pos + 1; }
+
+// A reader's view of the announced parts.
+struct PartReader {
+    int i = 0;
+    uint32_t ph = 0;
+    // The next part (the whole warp, or one thread alone); false when there is
+    // none, *ok = false when the wait ran out.
+    template <bool kWarp>
+    __device__ __forceinline__ bool next(Shared &sh, Part &t, long long limit, bool *ok) {
+        if (!(kWarp ? mbar_wait_warp(&sh.part_full[i], ph, limit) : mbar_wait(&sh.part_full[i], ph, limit))) {
+            *ok = false;
+            return false;
+        }
+        t = sh.parts[i];
+        return t.n > 0;
+    }
+    // Lets go of the part (one lane of a reading warp).
+    __device__ __forceinline__ void release(Shared &sh) { mbar_arrive(&sh.part_free[i]); }
+    __device__ __forceinline__ void advance() {
+        if (++i == kParts) {
+            i = 0;
+            ph ^= 1u;
+        }
+    }
+};
 
 __device__ __forceinline__ int page_of(const Params &P, int t) {
     return (int)(((uint64_t)(uint32_t)t * P.ps_mul) >> P.ps_shift);
@@ -159,33 +196,29 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     return d;
 }
 
-// 16 codes times their scale as bf16.  `pow2`: the scale is 2^e, given as the
-// bf16 pairs 2^64 and 2^(56 + e); their products are exact.
-__device__ __forceinline__ void widen16(const uint4 &codes, float scale, bool pow2, uint32_t m1, uint32_t m2, uint4 &lo,
-                                        uint4 &hi) {
+// 16 codes times 2^e as bf16; m: the bf16 pair 2^(120 + e).  Exact.
+__device__ __forceinline__ void widen16(const uint4 &codes, uint32_t m, uint4 &lo, uint4 &hi) {
+    const uint2 a = widen4(codes.x), b = widen4(codes.y), c = widen4(codes.z), d = widen4(codes.w);
+    lo = make_uint4(mul2(a.x, m), mul2(a.y, m), mul2(b.x, m), mul2(b.y, m));
+    hi = make_uint4(mul2(c.x, m), mul2(c.y, m), mul2(d.x, m), mul2(d.y, m));
+}
+
+// The same with any scale, and NaN codes.
+__device__ __forceinline__ void widen16_any(const uint4 &codes, float scale, uint4 &lo, uint4 &hi) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint32_t nan = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
     uint32_t out[8];
-    if (pow2 && !(nan & 0x80808080u)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint2 x = widen4(w[i]);
-            out[2 * i] = mul2(mul2(x.x, m1), m2);
-            out[2 * i + 1] = mul2(mul2(x.y, m1), m2);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 a = from_e4m3x2(w[i] & 0xffffu), b = from_e4m3x2(w[i] >> 16);
-            out[2 * i] = pack_bf16(a.x * scale, a.y * scale);
-            out[2 * i + 1] = pack_bf16(b.x * scale, b.y * scale);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = from_e4m3x2(w[i] & 0xffffu), b = from_e4m3x2(w[i] >> 16);
+        out[2 * i] = pack_bf16(a.x * scale, a.y * scale);
+        out[2 * i + 1] = pack_bf16(b.x * scale, b.y * scale);
     }
     lo = make_uint4(out[0], out[1], out[2], out[3]);
     hi = make_uint4(out[4], out[5], out[6], out[7]);
 }
+
+// Whether a NaN code is among the four (0x7f of its low seven bits).
+__device__ __forceinline__ uint32_t nan4(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
 
 }  // namespace ctc
 
@@ -222,6 +255,10 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             mbar_init(&sh.o_done[x], 1);
             mbar_init(&sh.o_free[x], kGroupWarps);
         }
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(&sh.part_full[i], 1);
+            mbar_init(&sh.part_free[i], 8 + 1 + (K8 ? 4 : 2));       // softmax, MMA, and warps 10 / 12 on
+        }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(&sh.full[s], K8 ? 4 : 1);
             mbar_init(&sh.empty[s], K8 ? 1 : 3);
@@ -255,8 +292,6 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
     const uint32_t tmem = sh.tmem_base;
     volatile int *abort = &sh.abort;
     const long long wait = A.wait;
-    ChunkWalk walk(A, sh.share);
-    ChunkPart u;
 
     if (warp >= kProducerWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
@@ -270,9 +305,29 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             uint32_t ph = 1;                             // parity of its release
             long long ld = 0;                            // fills issued
             bool ok = true;
+            ChunkWalk walk(A, sh.share);
+            ChunkPart u;
+            int pi = 0;                                  // next place for a part, and the
+            uint32_t pph = 1;                            // parity of its release
+            auto announce = [&](const Part &t) -> bool {
+                if (!mbar_wait_warp(&sh.part_free[pi], pph, wait)) return false;
+                if (lane == 0) {
+                    sh.parts[pi] = t;
+                    mbar_arrive(&sh.part_full[pi]);
+                }
+                if (++pi == kParts) {
+                    pi = 0;
+                    pph ^= 1u;
+                }
+                return true;
+            };
             while (ok && walk.next(A, u)) {
-                const Tiles t = tiles_of(P, u);
-                const int tiles = t.steps[1] > 0 ? 2 : 1;
+                const Part t = part_of(P, u);
+                const int tiles = t.nt[1] > 0 ? 2 : 1;
+                if (__any_sync(0xffffffffu, *abort != 0) || !announce(t)) {
+                    ok = false;
+                    break;
+                }
                 if (!mbar_wait_warp(&sh.q_empty, (uint32_t)((nu & 1) ^ 1), wait)) {
                     ok = false;
                     break;
@@ -280,7 +335,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(tiles * NH * rows * 128));
                 __syncwarp();
                 if (lane < tiles * NH)
-                    tma_load_3d(qbuf + lane * kHalf, &mq, (lane % NH) * 64, u.h * A.G, u.first + t.tok[lane / NH],
+                    tma_load_3d(qbuf + lane * kHalf, &mq, (lane % NH) * 64, u.h * A.G, t.row + (lane / NH) * P.tb,
                                 &sh.q_full, pol_q);
                 ++nu;
                 const int32_t *table = A.paged ? A.page_table + (size_t)u.b * A.max_pages : nullptr;
@@ -342,6 +397,10 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         }
                     }
                 }
+            }
+            if (ok) {
+                Part none{};
+                ok = announce(none);
             }
             if (lane == 0) {
                 if (!ok) {
@@ -408,9 +467,12 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                             vd + (uint64_t)((ks * 2048) >> 4), id_pv, (ks > 0 || !first) ? 1u : 0u);
                     return true;
                 };
-                while (ok && walk.next(A, u)) {
-                    const Tiles t = tiles_of(P, u);
-                    const int nA = t.steps[0], nB = t.steps[1], n = u.s1 - u.s0;
+                PartReader reader;
+                Part t;
+                while (ok && reader.next<false>(sh, t, wait, &ok)) {
+                    reader.release(sh);
+                    reader.advance();
+                    const int nA = t.n_t[0], nB = t.n_t[1], n = t.n;
                     if (*abort || !mbar_wait(&sh.q_full, (uint32_t)(nu & 1), wait) ||
                         !mbar_wait(&sh.full[slot], ph, wait)) {
                         ok = false;
@@ -429,7 +491,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                             ok = false;
                             break;
                         }
-                        if (!K8 && ragged(t, u.s0 + j)) {
+                        if (!K8 && ragged(t, t.s0 + j)) {
                             if (!mbar_wait(&sh.fixed[vslot], (fix_ph >> vslot) & 1u, wait)) {
                                 ok = false;
                                 break;
@@ -439,18 +501,18 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         advance();
                         const bool next = j + 1 < n;
                         const int kslot = slot;
-                        if (next && !mbar_wait(&sh.full[kslot], ph, wait)) {
-                            ok = false;
-                            break;
-                        }
                         if (j < nA) {
                             if (!issue_pv(0, vslot, j == 0)) {
                                 ok = false;
                                 break;
                             }
                             if (j + 1 == nA) commit(&sh.o_done[0]);
-                            else issue_s(0, kslot);
                         }
+                        if (next && !mbar_wait(&sh.full[kslot], ph, wait)) {
+                            ok = false;
+                            break;
+                        }
+                        if (j + 1 < nA) issue_s(0, kslot);
                         if (j < nB) {
                             if (!issue_pv(1, vslot, j == 0)) {
                                 ok = false;
@@ -485,15 +547,16 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             // (Both warps see every fill of the ring, and release it with the MMAs:
             // a warp that skipped fills could take an earlier phase for its own.)
             const int tid = threadIdx.x - kFixWarp * 32;
-            int slot = 0, nu = 0;
+            int slot = 0;
             uint32_t ph = 0;
             bool ok = true;
-            while (ok && walk.next(A, u)) {
-                const Tiles t = tiles_of(P, u);
-                int *bad = &sh.bad[nu++ % kBadRing][warp - kFixWarp];
+            PartReader reader;
+            Part t;
+            while (ok && reader.next<true>(sh, t, wait, &ok)) {
+                int *bad = &sh.bad[reader.i][warp - kFixWarp];
                 bool fresh = true;
-                for (int i = 2 * u.s0; i < 2 * u.s1; ++i) {
-                    const int s = i >> 1;
+                for (int i = 0; i < 2 * t.n; ++i) {
+                    const int s = t.s0 + (i >> 1);
                     if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.full[slot], ph, wait)) {
                         ok = false;
                         break;
@@ -505,7 +568,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                             fresh = false;
                         }
                         uint8_t *v = ring + slot * kTile;
-                        const int r0 = max(0, t.seen0 - s * kN), r1 = t.lim - s * kN;
+                        const int r0 = max(0, t.pos + 1 - s * kN), r1 = t.lim - s * kN;
                         for (int k = r0 * (NH * 8) + tid; k < kN * NH * 8; k += 64) {
                             const int r = k / (NH * 8), c = k % (NH * 8);
                             uint4 *p = reinterpret_cast<uint4 *>(v + (c / 8) * kHalf + r * 128 + (((c % 8) ^ (r & 7)) << 4));
@@ -526,6 +589,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         ph ^= 1u;
                     }
                 }
+                if (lane == 0) reader.release(sh);
+                reader.advance();
             }
             if (!ok && lane == 0) {
                 raise_status(A.status, SPEC_DEV_TIMEOUT);
@@ -534,28 +599,47 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
         } else if (K8 && warp >= kConvWarp) {
             // ----------------------------------------- codes into bf16 tiles
             constexpr int kStages = C::kStages > 0 ? C::kStages : 1;
+            constexpr int CPT = D / 16;              // 16-code vectors of a token
+            constexpr int TPI = 128 / CPT;           // tokens a round (16 or 32)
+            constexpr int NI = kN / TPI;             // rounds
             const int tid = threadIdx.x - kConvWarp * 32;
-            int slot = 0, stage = 0, nu = 0;
-            uint32_t ph = 1, sph = 0;                    // parity of the slot's release; of the stage's fill
+            const int c = tid % CPT, tr = tid / CPT; // this thread's vector of tokens tr + i TPI
+            // its codes in a stage (of the keys), and where they go in a tile: two
+            // 16-byte chunks, which the lanes of a row's second half write in the
+            // other order, so that eight lanes meet all banks
+            const uint32_t from = (uint32_t)((tr >> 4) * (32 * D) + kv8_row(tr & 15, 0, D) + c * 16);
+            const uint32_t to = (uint32_t)((c / 4) * kHalf + tr * 128);
+            const uint32_t swap = c >= 4 ? 1u : 0u;
+            const uint32_t at0 = to + (((2 * (c % 4) + swap) ^ (tr & 7)) << 4);
+            const uint32_t at1 = to + (((2 * (c % 4) + 1 - swap) ^ (tr & 7)) << 4);
+            int slot = 0, stage = 0;
+            uint32_t ph = 1, sph = 0;                // parity of the slot's release; of the stage's fill
             bool ok = true;
-            while (ok && walk.next(A, u)) {
-                const Tiles t = tiles_of(P, u);
-                int *bad = &sh.bad[nu++ % kBadRing][warp - kConvWarp];
+            PartReader reader;
+            Part t;
+            while (ok && reader.next<true>(sh, t, wait, &ok)) {
+                int *bad = &sh.bad[reader.i][warp - kConvWarp];
                 bool fresh = true;
-                const int32_t *table = A.page_table + (size_t)u.b * A.max_pages;
+                const int32_t *table = A.page_table + (size_t)t.b * A.max_pages;
+                const int s1 = t.s0 + t.n;
                 // scales of the step's eight groups of 16 tokens: lane 2 i + x has
                 // group i's of K (x = 0) or V; loaded a step ahead
                 auto load_scale = [&](int s) -> float {
                     const int tok = s * kN + (lane >> 1) * 16;
-                    if (lane >= 16 || s >= u.s1 || tok >= t.lim) return 1.f;
+                    if (lane >= 16 || s >= s1 || tok >= t.lim) return 1.f;
                     const int id = __ldg(table + page_of(P, tok));
                     if (id < 0 || id >= A.n_pages) return 1.f;
-                    return __ldg(A.scales + ((size_t)id * A.Hkv + u.h) * 2 + (lane & 1));
+                    return __ldg(A.scales + ((size_t)id * A.Hkv + t.h) * 2 + (lane & 1));
                 };
-                float next_scale = load_scale(u.s0);
-                for (int s = u.s0; s < u.s1 && ok; ++s) {
+                float next_scale = load_scale(t.s0);
+                for (int s = t.s0; s < s1 && ok; ++s) {
                     const float my_scale = kv8_read_scale(next_scale);
                     next_scale = load_scale(s + 1);
+                    // 2^e, e <= 7: its codes' factor 2^(120 + e) is a bf16
+                    const uint32_t sb = __float_as_uint(my_scale);
+                    const bool plain = (sb & 0x007fffffu) == 0u && sb <= 0x43000000u;
+                    const uint32_t m = ((sb >> 23) + 120u) << 7, my_factor = m | (m << 16);
+                    const bool all_plain = __all_sync(0xffffffffu, plain);
                     if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.st_full[stage], sph, wait)) {
                         ok = false;
                         break;
@@ -566,39 +650,40 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         __syncwarp();
                         fresh = false;
                     }
-                    const uint8_t *codes = stages + stage * C::kStage;
+#pragma unroll 1
                     for (int x = 0; x < 2; ++x) {
+                        const uint8_t *codes = stages + stage * C::kStage + from + x * (8 * D);
+                        uint4 v[NI];
+                        uint32_t nan = 0;
+#pragma unroll
+                        for (int i = 0; i < NI; ++i) {
+                            v[i] = *reinterpret_cast<const uint4 *>(codes + i * (TPI * 2 * D));
+                            nan |= nan4(v[i].x) | nan4(v[i].y) | nan4(v[i].z) | nan4(v[i].w);
+                        }
+                        const bool fast = __all_sync(0xffffffffu, !(nan & 0x80808080u)) && all_plain && !rag;
                         if (!mbar_wait_warp(&sh.empty[slot], ph, wait)) {
                             ok = false;
                             break;
                         }
                         uint8_t *dst = ring + slot * kTile;
-                        constexpr int CPT = D / 16;      // 16-code vectors of a token
-                        constexpr int TPI = 128 / CPT;   // tokens a round (16 or 32)
-                        const int c = tid % CPT, tr = tid / CPT;
 #pragma unroll
-                        for (int i = 0; i < kN / TPI; ++i) {
-                            const int r = i * TPI + tr;
-                            const float scale = __shfl_sync(0xffffffffu, my_scale, (r >> 4) * 2 + x);
-                            const uint32_t sb = __float_as_uint(scale);
-                            const bool pow2 = (sb & 0x007fffffu) == 0u;  // (finite ones lie in 2^-60 .. 2^60)
-                            const uint32_t e2 = ((sb >> 23) + 56) << 7;  // bf16 2^(56 + e)
-                            const uint4 v = *reinterpret_cast<const uint4 *>(
-                                codes + (r >> 4) * (32 * D) + kv8_row(r & 15, x, D) + c * 16);
+                        for (int i = 0; i < NI; ++i) {
+                            const int group = ((i * TPI + tr) >> 4) * 2 + x;
                             uint4 lo, hi;
-                            widen16(v, scale, pow2, 0x5f805f80u, e2 | (e2 << 16), lo, hi);
-                            if (rag) {
-                                const int tok = s * kN + r;
+                            if (fast) {
+                                widen16(v[i], __shfl_sync(0xffffffffu, my_factor, group), lo, hi);
+                            } else {
+                                widen16_any(v[i], __shfl_sync(0xffffffffu, my_scale, group), lo, hi);
+                                const int tok = s * kN + i * TPI + tr;
                                 if (tok >= t.lim) {
                                     lo = hi = make_uint4(0u, 0u, 0u, 0u);
-                                } else if (x == 1 && tok >= t.seen0 && (odd8(lo) || odd8(hi))) {
+                                } else if (x == 1 && tok > t.pos && (odd8(lo) || odd8(hi))) {
                                     atomicMin(bad, tok);
                                     lo = hi = make_uint4(0u, 0u, 0u, 0u);
                                 }
                             }
-                            uint8_t *p = dst + (c / 4) * kHalf + r * 128;
-                            *reinterpret_cast<uint4 *>(p + (((2 * (c % 4)) ^ (r & 7)) << 4)) = lo;
-                            *reinterpret_cast<uint4 *>(p + (((2 * (c % 4) + 1) ^ (r & 7)) << 4)) = hi;
+                            *reinterpret_cast<uint4 *>(dst + at0 + i * (TPI * 128)) = swap ? hi : lo;
+                            *reinterpret_cast<uint4 *>(dst + at1 + i * (TPI * 128)) = swap ? lo : hi;
                         }
                         fence_async();
                         __syncwarp();
@@ -615,6 +700,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         sph ^= 1u;
                     }
                 }
+                if (lane == 0) reader.release(sh);
+                reader.advance();
             }
             if (!ok && lane == 0) {
                 raise_status(A.status, SPEC_DEV_TIMEOUT);
@@ -630,24 +717,25 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
         const uint32_t tS = tmem + lane_base + col_s(x), tO = tmem + lane_base + col_o(x);
         const float sc = A.scale_log2;
         const int rt = r / A.G, rg = r - rt * A.G;       // the row's token and query head
-        int ns = 0, nact = 0, nu = 0;      // S hand-offs taken; parts this tile took part in; parts
+        int ns = 0, nact = 0;      // S hand-offs taken; parts this tile took part in
         bool ok = true;
-        while (ok && walk.next(A, u)) {
-            const Tiles t = tiles_of(P, u);
-            const int unit = nu++;
-            if (t.nt[x] == 0) continue;
+        PartReader reader;
+        Part t;
+        while (ok && reader.next<true>(sh, t, wait, &ok)) {
             const bool row_ok = rt < t.nt[x];
-            const bool warp_ok = __any_sync(0xffffffffu, row_ok);
-            const int seen = u.S + t.tok[x] + rt + 1;    // tokens this row sees
-            const int sure = u.S + t.tok[x] + 1;         // and the tile's first row
-            const bool whole = u.s0 == 0 && u.s1 == u.steps;
-            const size_t part = (size_t)chunk_slot(u) * A.ru + x * rows + r;
-            if (t.steps[x] == 0) {                       // (tile A is through: an empty part)
-                if (row_ok) A.part_ml[part] = make_float2(-INFINITY, 0.f);
+            const int n = t.n_t[x];
+            if (n == 0) {                                // (no such tile, or tile A is through: an empty part)
+                if (row_ok) A.part_ml[(size_t)t.slot * A.ru + x * rows + r] = make_float2(-INFINITY, 0.f);
+                __syncwarp();
+                if (lane == 0) reader.release(sh);
+                reader.advance();
                 continue;
             }
+            const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+            const int sure = t.pos + x * P.tb + 1;       // tokens the tile's first row sees
+            const int seen = sure + rt;                  // and this row
             float m_used = -INFINITY, l = 0.f;
-            for (int j = 0; j < t.steps[x]; ++j) {
+            for (int j = 0; j < n; ++j) {
                 if (__any_sync(0xffffffffu, *abort != 0) ||
                     !mbar_wait_warp(&sh.s_full[x], (uint32_t)(ns & 1), wait)) {
                     ok = false;
@@ -661,7 +749,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     if (lane == 0) mbar_arrive(&sh.p_full[x]);
                     continue;
                 }
-                const int c0 = (u.s0 + j) * kN;
+                const int c0 = (t.s0 + j) * kN;
                 const bool masked = c0 + kN > sure;
                 // the S row: four TMEM loads in flight, one wait (each
                 // wait_ld ties its registers; the later ones return at once)
@@ -758,12 +846,14 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             fence_after();
             // a non-finite value among those looked over, which this row sees
             bool odd = false;
-            if (ragged(t, u.s0 + t.steps[x] - 1)) {
-                const volatile int *bad = sh.bad[unit % kBadRing];
+            if (ragged(t, t.s0 + n - 1)) {
+                const volatile int *bad = sh.bad[reader.i];
                 for (int w = 0; w < (K8 ? 4 : 2); ++w) odd = odd || seen > bad[w];
             }
+            const bool whole = t.slot < 0;
             const float inv = odd ? __uint_as_float(0x7fffffffu) : whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            const long long row = u.first + t.tok[x] + rt, hq = (long long)u.h * A.G + rg;
+            const size_t out = ((size_t)t.row + x * P.tb + rt) * A.Hq + (size_t)t.h * A.G + rg;
+            const size_t part = (size_t)(whole ? 0 : t.slot) * A.ru + x * rows + r;
             if (warp_ok) {
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
@@ -772,8 +862,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     wait_ld(v);
                     if (!row_ok) continue;
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.o) +
-                                                               (row * A.Hq + hq) * D + c * 32);
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.o) + out * D +
+                                                               c * 32);
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
                             dst[e / 8] = make_uint4(
@@ -792,14 +882,18 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 }
                 if (row_ok) {
                     if (whole)
-                        A.lse[row * A.Hq + hq] = l == 0.f ? -INFINITY : l != l ? l : (m_used + log2f(l)) * kLn2;
+                        A.lse[out] = l == 0.f ? -INFINITY : l != l ? l : (m_used + log2f(l)) * kLn2;
                     else
                         A.part_ml[part] = make_float2(m_used, l);
                 }
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.o_free[x]);
+            if (lane == 0) {
+                mbar_arrive(&sh.o_free[x]);
+                reader.release(sh);
+            }
+            reader.advance();
             ++nact;
         }
         if (!ok) {
