@@ -47,6 +47,9 @@ constexpr int kFixWarp = 10;             // bf16 cache: 10 and 11
 constexpr int kConvWarp = 12;            // 8-bit cache: 12 .. 15
 constexpr int kTmemCols = 512;
 constexpr int kParts = 8;                // parts announced ahead
+// Steps of a part that are copied before its queries: their slots (two a step) or
+// stages are free of it, so they come free without its queries.
+constexpr int kAhead = 2;
 __host__ __device__ constexpr uint32_t col_o(int x) { return 256u * (uint32_t)x; }
 __host__ __device__ constexpr uint32_t col_s(int x) { return 256u * (uint32_t)x + 128u; }
 constexpr float kRescale = 8.f;          // log2 growth allowed before rescaling
@@ -62,6 +65,7 @@ struct Cfg {
     static constexpr int kSlots = D == 128 ? (K8 ? 3 : 5) : 8;
     static constexpr int kStages = K8 ? (D == 128 ? 2 : 4) : 0;
     static constexpr int kStage = 2 * kN * D;            // codes of a step, K and V
+    static_assert(K8 ? kAhead <= kStages && kSlots >= 3 : 2 * kAhead < kSlots, "steps ahead of their queries");
     static constexpr int kWarps = K8 ? 16 : 12;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kLaunchRegs = K8 ? 128 : 168;
@@ -75,6 +79,7 @@ struct Params {
     ChunkParams c;
     int tb;                  // tokens of a query tile
     int box;                 // tokens of a tensor copy (paged: of one page)
+    bool wide_o;             // o is on a 32-byte boundary
     uint32_t ps_mul;         // t / ps = (t ps_mul) >> 31 + ps_shift, t < 2^30
     int ps_shift;
 };
@@ -194,6 +199,18 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
+}
+
+// 32 bytes to global memory, 16-byte aligned, or 32 (`wide`: one instruction).
+__device__ __forceinline__ void store32(void *p, const uint32_t *w, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 // 16 codes times 2^e as bf16; m: the bf16 pair 2^(120 + e).  Exact.
@@ -328,16 +345,26 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     ok = false;
                     break;
                 }
-                if (!mbar_wait_warp(&sh.q_empty, (uint32_t)((nu & 1) ^ 1), wait)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(tiles * NH * rows * 128));
-                __syncwarp();
-                if (lane < tiles * NH)
-                    tma_load_3d(qbuf + lane * kHalf, &mq, (lane % NH) * 64, u.h * A.G, t.row + (lane / NH) * P.tb,
-                                &sh.q_full, pol_q);
-                ++nu;
+                // The queries replace the part before's, so their copy waits for its
+                // last S; the first steps' K and V do not.
+                bool q_due = true;
+                auto load_q = [&](bool block) -> bool {
+                    const uint32_t parity = (uint32_t)((nu & 1) ^ 1);
+                    if (!q_due) return true;
+                    if (block) {
+                        if (!mbar_wait_warp(&sh.q_empty, parity, wait)) return false;
+                    } else if (!__all_sync(0xffffffffu, mbar_test_wait(&sh.q_empty, parity))) {
+                        return true;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(tiles * NH * rows * 128));
+                    __syncwarp();
+                    if (lane < tiles * NH)
+                        tma_load_3d(qbuf + lane * kHalf, &mq, (lane % NH) * 64, u.h * A.G, t.row + (lane / NH) * P.tb,
+                                    &sh.q_full, pol_q);
+                    ++nu;
+                    q_due = false;
+                    return true;
+                };
                 const int32_t *table = A.paged ? A.page_table + (size_t)u.b * A.max_pages : nullptr;
                 // the page of this lane's copy, loaded a step ahead of its use
                 const int at = K8 ? lane * 16 : bx * P.box;
@@ -357,6 +384,10 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     }
                     const int off = A.paged ? tok - page_of(P, tok) * A.ps : tok;
                     const uint32_t n_in = (uint32_t)__popc(__ballot_sync(0xffffffffu, in));
+                    if (!load_q(s == u.s0 + kAhead)) {
+                        ok = false;
+                        break;
+                    }
                     if constexpr (K8) {
                         if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.st_empty[slot], ph, wait)) {
                             ok = false;
@@ -397,6 +428,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         }
                     }
                 }
+                ok = ok && load_q(true);
             }
             if (ok) {
                 Part none{};
@@ -862,22 +894,19 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     wait_ld(v);
                     if (!row_ok) continue;
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(A.o) + out * D +
-                                                               c * 32);
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(A.o) + out * D + c * 32;
+                        uint32_t w[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            dst[e / 8] = make_uint4(
-                                pack_bf16(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv),
-                                pack_bf16(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv),
-                                pack_bf16(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv),
-                                pack_bf16(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv));
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = pack_bf16(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8) store32(dst + 2 * e, &w[e], P.wide_o);
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(A.part_o + part * D + c * 32);
+                        float *dst = A.part_o + part * D + c * 32;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            dst[e / 4] = make_float4(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv,
-                                                     __uint_as_float(v[e + 2]) * inv,
-                                                     __uint_as_float(v[e + 3]) * inv);
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * inv);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) store32(dst + e, &v[e], true);
                     }
                 }
                 if (row_ok) {
@@ -931,6 +960,7 @@ spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStr
     P.c = C;
     P.tb = ctc::kM / C.G;
     P.box = ctc::kN;
+    P.wide_o = reinterpret_cast<uintptr_t>(C.o) % 32 == 0;
     if (C.paged) {
         int a = C.ps, b = ctc::kN;                       // the greatest common divisor
         while (b) {
