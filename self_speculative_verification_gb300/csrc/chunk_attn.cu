@@ -263,10 +263,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(ChunkPara
     }
     __syncthreads();
     const int n = s_n;
+    const bool paired = chunk_paired(P, r);
     const long long r0 = (long long)c.z * P.ru;
-    const int nr = (int)min((long long)P.ru, (long long)r.n * P.G - r0);
     constexpr int E = D / 32;
-    for (int row = blockIdx.y * kMergeWarps + warp; row < nr; row += gridDim.y * kMergeWarps) {
+    for (int row = blockIdx.y * kMergeWarps + warp; row < P.ru; row += gridDim.y * kMergeWarps) {
+        // the row's packed row and head; the second tile of a pair is the other head
+        const int x = paired && 2 * row >= P.ru ? 1 : 0;
+        const long long p = paired ? row - x * (P.ru / 2) : r0 + row;
+        const int h = paired ? 2 * c.y + x : c.y;
+        if (p >= (long long)r.n * P.G || h >= P.Hkv) continue;
         // the largest maximum, a part a lane
         float top = -INFINITY;
         for (int k = lane; k < n; k += 32) top = fmaxf(top, P.part_ml[(size_t)s_slot[k] * P.ru + row].x);
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(ChunkPara
                 for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[v][e], acc[e]);
             }
         }
-        const long long p = r0 + row, tok = r.first + p / P.G, hq = (long long)c.y * P.G + p % P.G;
+        const long long tok = r.first + p / P.G, hq = (long long)h * P.G + p % P.G;
         T *o = static_cast<T *>(P.o) + (tok * P.Hq + hq) * D + lane * E;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if constexpr (sizeof(T) == 2) {
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(ChunkPara
 // ------------------------------------------------------------- host side
 
 ChunkPlan simt_plan() {
-    return ChunkPlan{kRows, kKeys, 2 * kKeys, 2 * kKeys, kSimtPerSm * num_sms()};
+    return ChunkPlan{kRows, 0, kKeys, 2 * kKeys, 2 * kKeys, kSimtPerSm * num_sms()};
 }
 
 ChunkPlan plan_of(const ChunkParams &P, int dtype, bool kv8) {
@@ -468,6 +473,7 @@ spec_status_t run_chunk(ChunkParams &P, int dtype, bool kv8, const void *q, long
     P.part_ml = reinterpret_cast<float2 *>(base + w.ml);
     P.records = reinterpret_cast<int4 *>(base + w.rec);
     P.ru = pl.ru;
+    P.tu = pl.tu;
     P.ks = pl.ks;
     P.fixed_cost = pl.fixed_cost;
     P.min_share = pl.min_share;

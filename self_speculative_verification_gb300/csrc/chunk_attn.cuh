@@ -7,7 +7,9 @@
 //
 // Unit: `ru` consecutive packed rows of one (request, KV head), cut along the
 // keys into steps of `ks` tokens up to the last one its last row sees.  Units
-// are numbered request by request, head by head, rows ascending.
+// are numbered request by request, head by head, rows ascending.  On the
+// tensor cores a unit is two query tiles; a request whose rows all fit one has
+// units of two heads instead, a tile each.
 //
 // Ranges: every unit has a cost in closed form -- a fixed one, and the tokens
 // its last row sees -- so the sum over any number of units is closed too, and
@@ -40,6 +42,7 @@ struct ChunkParams {
     int capacity;            // tokens per request
     long long cache_heads;   // contiguous: requests * heads of the cache
     int ru, ks;              // rows of a unit, keys of a step
+    int tu;                  // tokens of a unit (two tiles: ru / G), or 0: units end inside a token's rows
     int fixed_cost;          // of a unit, in keys
     int min_share;           // least cost (keys) worth a CTA
     float scale_log2;        // softmax scale * log2(e)
@@ -48,7 +51,7 @@ struct ChunkParams {
 
 // The tensor-core path: rows and CTAs of a call, its kernel's launch.
 struct ChunkPlan {
-    int ru, ks, fixed_cost, min_share, n_cta;
+    int ru, tu, ks, fixed_cost, min_share, n_cta;
 };
 ChunkPlan chunk_tc_plan(const ChunkParams &P, bool kv8);
 spec_status_t launch_chunk_tc(const ChunkParams &P, bool kv8, int n_cta, cudaStream_t s);
@@ -62,31 +65,36 @@ struct ChunkReq {
 };
 
 __device__ __forceinline__ ChunkReq chunk_request(const ChunkParams &P, int b, int *bits) {
-    ChunkReq r{__ldg(P.cu_new + b), 0, 0};
+    ChunkReq r{__ldg(P.cu_new + b), 0, __ldg(P.seq_len + b)};
     const int end = __ldg(P.cu_new + b + 1);
     if (r.first < 0 || end < r.first || end > P.n_tokens) {
         if (bits) *bits |= SPEC_DEV_BAD_INDEX;
-        return r;
-    }
-    if (end == r.first) return r;
-    r.S = __ldg(P.seq_len + b);
-    if (r.S < 0 || r.S > P.capacity - (end - r.first)) {
+    } else if (end == r.first) {
+    } else if (r.S < 0 || r.S > P.capacity - (end - r.first)) {
         if (bits) *bits |= SPEC_DEV_SEQ_OVERFLOW;
-        r.S = 0;
-        return r;
+    } else {
+        r.n = end - r.first;
     }
-    r.n = end - r.first;
     return r;
 }
 
+// Whether the request's units are pairs of heads, and how many heads or pairs.
+__device__ __forceinline__ bool chunk_paired(const ChunkParams &P, const ChunkReq &r) { return 2 * r.n <= P.tu; }
+__device__ __forceinline__ int chunk_heads(const ChunkParams &P, const ChunkReq &r) {
+    return chunk_paired(P, r) ? (P.Hkv + 1) / 2 : P.Hkv;
+}
+
 __device__ __forceinline__ int chunk_units(const ChunkParams &P, const ChunkReq &r) {
+    if (P.tu) return (int)(((uint32_t)r.n + P.tu - 1) / (uint32_t)P.tu);
     return (int)(((long long)r.n * P.G + P.ru - 1) / P.ru);
 }
 
-// Cost of a head's first j units (in keys * G): unit i costs G (fixed + S) +
-// (i + 1) ru.
+// Cost of a head's (a pair's) first j units (in keys * G): unit i costs G (fixed
+// + S) + (i + 1) ru; for a pair, whose steps are each head's own, the S counts
+// twice.
 __device__ __forceinline__ long long chunk_cost(const ChunkParams &P, const ChunkReq &r, long long j) {
-    return j * P.G * ((long long)P.fixed_cost + r.S) + P.ru * (j * (j + 1) / 2);
+    const long long S = chunk_paired(P, r) ? 2ll * r.S : r.S;
+    return j * P.G * (P.fixed_cost + S) + P.ru * (j * (j + 1) / 2);
 }
 
 // A place in the call's work: unit j of head h of request b, from step s on.
@@ -96,27 +104,39 @@ struct ChunkPos {
 
 // Steps of unit j: up to the last token its last row sees.
 __device__ __forceinline__ int chunk_steps(const ChunkParams &P, const ChunkReq &r, int j) {
-    const long long rows = (long long)r.n * P.G;
-    const long long last = min(rows, (long long)(j + 1) * P.ru) - 1;
-    return (int)((r.S + last / P.G + P.ks) / P.ks);      // (S + last / G + 1 tokens)
+    int last;                                            // that token, within the new ones
+    if (P.tu) {
+        last = (int)min((long long)r.n, (long long)(j + 1) * P.tu) - 1;
+    } else {
+        const long long rows = min((long long)r.n * P.G, (long long)(j + 1) * P.ru);
+        last = (int)((rows - 1) / P.G);
+    }
+    return (int)((uint32_t)(r.S + last + P.ks) / (uint32_t)P.ks);   // (S + last + 1 tokens)
 }
 
+// Where cost `at` of request b's lies.  Quotients and the root are taken in
+// fp32 and put right by comparisons: 64-bit divisions and fp64 cost the start
+// of a call microseconds.  (The same place comes out for the CTA that ends
+// there and for the one that begins.)
 __device__ __forceinline__ ChunkPos chunk_find(const ChunkParams &P, int b, const ChunkReq &r,
                                                long long at) {
     const int nu = chunk_units(P, r);
     const long long head = chunk_cost(P, r, nu);
-    ChunkPos p{b, (int)(at / head), 0, 0};
-    at %= head;
-    int lo = 0, hi = nu - 1;                              // the last j with cost(j) <= at
-    while (lo < hi) {
-        const int mid = lo + (hi - lo + 1) / 2;
-        if (chunk_cost(P, r, mid) <= at) lo = mid;
-        else hi = mid - 1;
-    }
-    p.j = lo;
-    const long long f = at - chunk_cost(P, r, lo), w = chunk_cost(P, r, lo + 1) - chunk_cost(P, r, lo);
-    p.s = (int)((double)f / (double)w * chunk_steps(P, r, lo));
-    p.s = min(p.s, chunk_steps(P, r, lo) - 1);
+    ChunkPos p{b, 0, 0, 0};
+    const int heads = chunk_heads(P, r);
+    p.h = min((int)(__ll2float_rn(at) / __ll2float_rn(head)), heads - 1);
+    while (p.h > 0 && p.h * head > at) --p.h;
+    while (p.h < heads - 1 && (p.h + 1) * head <= at) ++p.h;
+    at -= p.h * head;
+    // the last j with cost(j) <= at: cost(j) = (ru j^2 + (2 a + ru) j) / 2
+    const float a = __ll2float_rn(chunk_cost(P, r, 1)) - (float)P.ru, ru = (float)P.ru;
+    const float half = a / ru + 0.5f, x = __ll2float_rn(at) / ru;
+    p.j = min((int)(2.f * x / (half + sqrtf(half * half + 2.f * x))), nu - 1);
+    while (p.j > 0 && chunk_cost(P, r, p.j) > at) --p.j;
+    while (p.j < nu - 1 && chunk_cost(P, r, p.j + 1) <= at) ++p.j;
+    const long long f = at - chunk_cost(P, r, p.j), w = chunk_cost(P, r, p.j + 1) - chunk_cost(P, r, p.j);
+    const int steps = chunk_steps(P, r, p.j);
+    p.s = min((int)(__ll2float_rn(f) / __ll2float_rn(w) * (float)steps), steps - 1);
     return p;
 }
 
@@ -138,7 +158,7 @@ __device__ void chunk_share(const ChunkParams &P, ChunkShare &sh) {
     ChunkReq r{0, 0, 0};
     for (int b = b0; b < b1; ++b) {
         r = chunk_request(P, b, &bits);
-        mine += P.Hkv * chunk_cost(P, r, chunk_units(P, r));
+        mine += chunk_heads(P, r) * chunk_cost(P, r, chunk_units(P, r));
     }
     if (bits && blockIdx.x == 0) raise_status(P.status, bits);
     long long sum = mine;
@@ -156,17 +176,20 @@ __device__ void chunk_share(const ChunkParams &P, ChunkShare &sh) {
         total += x;
     }
     before += sum - mine;
-    long long n = total / ((long long)P.min_share * P.G);
-    n = n < 1 ? 1 : n > gridDim.x ? gridDim.x : n;
+    // n shares of `share` each, the last one with what fp32 left over (at most
+    // n 2^-23 of the total)
+    const float all = __ll2float_rn(total);
+    const int n = max(1, (int)fminf(all / ((float)P.min_share * (float)P.G), (float)gridDim.x));
+    const long long share = (long long)(all / (float)n);
     for (int e = 0; e < 2; ++e) {
-        const long long i = (long long)blockIdx.x + e;
+        const int i = (int)blockIdx.x + e;
         if (i >= n) break;
-        const long long at = total / n * i + total % n * i / n;
+        const long long at = share * i;
         if (at < before || at >= before + mine) continue;
         long long c = before;
         for (int b = b0; b < b1; ++b) {
             if (per > 1) r = chunk_request(P, b, nullptr);
-            const long long w = P.Hkv * chunk_cost(P, r, chunk_units(P, r));
+            const long long w = chunk_heads(P, r) * chunk_cost(P, r, chunk_units(P, r));
             if (at < c + w) {
                 (e ? sh.end : sh.begin) = chunk_find(P, b, r, at - c);
                 break;
@@ -188,6 +211,7 @@ struct ChunkPart {
     int first, S;            // request: its first packed token, tokens held before
     int n;                   // request: new tokens
     int steps, s0, s1;
+    bool paired;             // h: pair of heads 2 h, 2 h + 1
 };
 
 // Walks a CTA's share part by part.
@@ -220,6 +244,7 @@ struct ChunkWalk {
             u.first = r.first;
             u.S = r.S;
             u.n = r.n;
+            u.paired = chunk_paired(P, r);
             u.steps = chunk_steps(P, r, at.j);
             u.s0 = at.s;
             u.s1 = last ? end.s : u.steps;
@@ -229,7 +254,7 @@ struct ChunkWalk {
                 at.s = 0;
                 if (++at.j == nu) {
                     at.j = 0;
-                    if (++at.h == P.Hkv) {
+                    if (++at.h == chunk_heads(P, r)) {
                         at.h = 0;
                         ++at.b;
                         fresh = true;

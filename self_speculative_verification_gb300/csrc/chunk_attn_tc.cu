@@ -7,21 +7,23 @@
 //   persistent grid, one CTA per SM, takes equal shares of the call's cost, cut
 //   at 128-key steps (chunk_attn.cuh), so single tokens behind long histories
 //   and long prompts fill the GPU alike.
+//   A request whose rows fit one tile (single tokens among them) has units of two
+//   KV heads instead, a tile and a stream of K/V tiles each.
 // * Warps 0-3 run the softmax of tile A and 4-7 that of tile B, one row a
-//   thread; warp 8 copies the unit's queries and the cache's tiles, warp 9
-//   issues the MMAs from one thread.  The MMA thread interleaves the tiles --
-//   PV_A(j), S_A(j+1), PV_B(j), S_B(j+1) -- so the tensor core works on one
-//   while the other's softmax runs.
+//   thread; warp 8 copies the units' queries and the cache's tiles, warps 9 and
+//   10 issue the MMAs of tiles A and B from one thread each -- PV(j), S(j+1), PV
+//   (j+1), .. -- so that the tensor core works on one tile while the other's
+//   softmax, or its change of unit, runs.
 // * bf16 cache: K and V tiles come by tensor copies, one a page and 64 elements,
-//   into a ring of 128-byte-swizzled slots.  Warps 10 and 11 look through the
+//   into a ring of 128-byte-swizzled slots.  Warp 11 looks through the
 //   value tiles that not every row sees whole (the last ones of a unit): rows
 //   past the unit's last token become zeros, and non-finite values too, whose
 //   first place they note, for a hidden value's weight of zero would not keep
 //   it out of the sum.
 // * 8-bit cache: 16 tokens' codes, keys and values, are one run of memory, which
 //   a bulk copy brings into a stage; warps 12-15 turn them into the slots' bf16
-//   tiles (code * scale, exact for a power of two) and do what warps 10 and 11
-//   do on the way.
+//   tiles (code * scale, exact for a power of two) and do what warp 11 does
+//   on the way.
 // * Softmax and TMEM as in the prefill kernel: O (fp32) and S of a tile side by
 //   side, P (bf16) over the first half of S, the running maximum raised only
 //   when it grows by more than 2^8.
@@ -42,13 +44,13 @@ constexpr int kN = 128;                  // keys of a step
 constexpr int kHalf = 128 * 128;         // 128 rows x 64 bf16
 constexpr int kGroupWarps = 4;
 constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kFixWarp = 10;             // bf16 cache: 10 and 11
+constexpr int kMmaWarp = 9;              // and 10
+constexpr int kFixWarp = 11;             // bf16 cache
 constexpr int kConvWarp = 12;            // 8-bit cache: 12 .. 15
 constexpr int kTmemCols = 512;
 constexpr int kParts = 8;                // parts announced ahead
-// Steps of a part that are copied before its queries: their slots (two a step) or
-// stages are free of it, so they come free without its queries.
+// K/V pairs of a part that are copied before its queries: their slots (two each)
+// or stages are free of it, so they come free without its queries.
 constexpr int kAhead = 2;
 __host__ __device__ constexpr uint32_t col_o(int x) { return 256u * (uint32_t)x; }
 __host__ __device__ constexpr uint32_t col_s(int x) { return 256u * (uint32_t)x + 128u; }
@@ -78,36 +80,39 @@ struct Cfg {
 struct Params {
     ChunkParams c;
     int tb;                  // tokens of a query tile
+    uint32_t g_mul;          // r / G = (r g_mul) >> 16, r < 128
     int box;                 // tokens of a tensor copy (paged: of one page)
-    bool wide_o;             // o is on a 32-byte boundary
     uint32_t ps_mul;         // t / ps = (t ps_mul) >> 31 + ps_shift, t < 2^30
     int ps_shift;
 };
 
-// A CTA's part of a unit, as the producer announces it: n steps of 128 keys
-// from s0 on, of which tiles A and B take n_t[0] and n_t[1] (the tile with rows
-// that see fewer tokens ends earlier).
+// A CTA's part of a unit, as the producer announces it: n steps of 128 keys from
+// s0 on, of which tile x takes the first n_t[x] (tile A's rows may see fewer
+// tokens).  A step brings `sets` pairs of a K and a V tile: one for both query
+// tiles, or, in a unit of two heads, one for each.
 struct Part {
     int n;                   // 0: no more parts
     int s0;
-    int b, h;
-    int row;                 // packed row of the unit's first token
-    int pos;                 // its position: it sees pos + 1 tokens
+    int b, sets;
+    int h[2];                // KV head of each tile
+    int row[2];              // its first token's packed row
+    int pos[2];              // and position: it sees pos + 1 tokens
+    int nt[2], n_t[2];       // its tokens and steps
     int lim;                 // tokens that the unit's last one sees
-    int nt[2], n_t[2];       // tokens and steps of each tile
     int slot;                // where a part that is not a whole unit goes; -1: whole
 };
 
 struct Shared {
     uint64_t part_full[kParts], part_free[kParts];
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t full[kMaxSlots], empty[kMaxSlots], fixed[kMaxSlots];
     uint64_t st_full[kMaxStages], st_empty[kMaxStages];
-    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
-    uint64_t drain;
+    uint64_t s_full[2], p_full[2][2], o_done[2], o_free[2];      // p_full: by halves of the keys
+    uint64_t drain[2];
     uint32_t tmem_base;
+    uint32_t issued;         // fills of the ring begun
     int abort;
-    int bad[kParts][4];      // by part and looking warp: first token with a non-finite value
+    int bad[kParts][8];      // by part, looking warp and set: first token with a non-finite value
     Part parts[kParts];
     ChunkShare share;
 };
@@ -120,41 +125,45 @@ constexpr size_t smem_bytes() {
 
 __device__ __forceinline__ Part part_of(const Params &P, const ChunkPart &u) {
     Part t;
-    const int tok = u.j * 2 * P.tb;
+    const int tok = u.paired ? 0 : u.j * 2 * P.tb;
     t.n = u.s1 - u.s0;
     t.s0 = u.s0;
     t.b = u.b;
-    t.h = u.h;
-    t.row = u.first + tok;
-    t.pos = u.S + tok;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        t.nt[x] = max(0, min(P.tb, u.n - tok - x * P.tb));
-        const int end = (t.pos + x * P.tb + t.nt[x] + kN - 1) / kN;    // its last row's steps
+        const int tx = u.paired ? 0 : tok + x * P.tb;
+        t.h[x] = u.paired ? 2 * u.h + x : u.h;
+        t.row[x] = u.first + tx;
+        t.pos[x] = u.S + tx;
+        t.nt[x] = u.paired && t.h[x] >= P.c.Hkv ? 0 : max(0, min(P.tb, u.n - tx));
+        const int end = (t.pos[x] + t.nt[x] + kN - 1) / kN;            // its last row's steps
         t.n_t[x] = t.nt[x] > 0 ? max(0, min(u.s1, end) - u.s0) : 0;
     }
-    t.lim = t.pos + t.nt[0] + t.nt[1];
+    t.sets = u.paired && t.nt[1] > 0 ? 2 : 1;
+    t.lim = max(t.pos[0] + t.nt[0], t.nt[1] > 0 ? t.pos[1] + t.nt[1] : 0);
     t.slot = u.s0 == 0 && u.s1 == u.steps ? -1 : chunk_slot(u);
     return t;
 }
 
 // Whether step s holds tokens that some row of the unit does not see.
-__device__ __forceinline__ bool ragged(const Part &t, int s) { return (s + 1) * kN > t.pos + 1; }
+__device__ __forceinline__ bool ragged(const Part &t, int s) { return (s + 1) * kN > t.pos[0] + 1; }
+
+template <bool V> struct Bool { static constexpr bool value = V; };
 
 // A reader's view of the announced parts.
 struct PartReader {
     int i = 0;
     uint32_t ph = 0;
-    // The next part (the whole warp, or one thread alone); false when there is
-    // none, *ok = false when the wait ran out.
+    // Waits for the next part (the whole warp, or one thread alone), which is
+    // sh.parts[i] until it is let go of; false when there is none, *ok = false when
+    // the wait ran out.
     template <bool kWarp>
-    __device__ __forceinline__ bool next(Shared &sh, Part &t, long long limit, bool *ok) {
+    __device__ __forceinline__ bool next(Shared &sh, long long limit, bool *ok) {
         if (!(kWarp ? mbar_wait_warp(&sh.part_full[i], ph, limit) : mbar_wait(&sh.part_full[i], ph, limit))) {
             *ok = false;
             return false;
         }
-        t = sh.parts[i];
-        return t.n > 0;
+        return sh.parts[i].n > 0;
     }
     // Lets go of the part (one lane of a reading warp).
     __device__ __forceinline__ void release(Shared &sh) { mbar_arrive(&sh.part_free[i]); }
@@ -199,18 +208,6 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
-}
-
-// 32 bytes to global memory, 16-byte aligned, or 32 (`wide`: one instruction).
-__device__ __forceinline__ void store32(void *p, const uint32_t *w, bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    } else {
-        static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
 }
 
 // 16 codes times 2^e as bf16; m: the bf16 pair 2^(120 + e).  Exact.
@@ -264,29 +261,31 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                          : "memory");
     }
     if (threadIdx.x == 0) {
-        mbar_init(&sh.q_full, 1);
-        mbar_init(&sh.q_empty, 1);
         for (int x = 0; x < 2; ++x) {
+            mbar_init(&sh.q_full[x], 1);
+            mbar_init(&sh.q_empty[x], kGroupWarps);
             mbar_init(&sh.s_full[x], 1);
-            mbar_init(&sh.p_full[x], kGroupWarps);
+            mbar_init(&sh.p_full[x][0], kGroupWarps);
+            mbar_init(&sh.p_full[x][1], kGroupWarps);
             mbar_init(&sh.o_done[x], 1);
             mbar_init(&sh.o_free[x], kGroupWarps);
+            mbar_init(&sh.drain[x], 1);
         }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&sh.part_full[i], 1);
-            mbar_init(&sh.part_free[i], 8 + 1 + (K8 ? 4 : 2));       // softmax, MMA, and warps 10 / 12 on
+            mbar_init(&sh.part_free[i], 8 + 2 + (K8 ? 4 : 1));       // softmax, MMA, and warp 11 or 12 to 15
         }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(&sh.full[s], K8 ? 4 : 1);
-            mbar_init(&sh.empty[s], K8 ? 1 : 3);
-            mbar_init(&sh.fixed[s], 2);
+            mbar_init(&sh.empty[s], K8 ? 2 : 3);                     // MMA threads, warp 11
+            mbar_init(&sh.fixed[s], 1);
         }
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&sh.st_full[s], 1);
             mbar_init(&sh.st_empty[s], 4);
         }
-        mbar_init(&sh.drain, 1);
         sh.abort = 0;
+        sh.issued = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // the rows of the query tiles that hold no query (128 is not a multiple of G)
@@ -318,7 +317,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
             const int per = kN / P.box;                  // copies a tile, by tokens
             const int hh = lane % NH, bx = lane / NH;    // rows cache: this lane's copy
-            int slot = 0, nu = 0;                        // next slot (8 bits: stage); units
+            int slot = 0;                                // next slot (8 bits: stage)
+            int nq[2] = {0, 0};                          // queries copied, per tile
             uint32_t ph = 1;                             // parity of its release
             long long ld = 0;                            // fills issued
             bool ok = true;
@@ -340,29 +340,31 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             };
             while (ok && walk.next(A, u)) {
                 const Part t = part_of(P, u);
-                const int tiles = t.nt[1] > 0 ? 2 : 1;
                 if (__any_sync(0xffffffffu, *abort != 0) || !announce(t)) {
                     ok = false;
                     break;
                 }
-                // The queries replace the part before's, so their copy waits for its
-                // last S; the first steps' K and V do not.
-                bool q_due = true;
+                // A tile's queries replace those of its part before, whose results
+                // leave through their place, so their copy waits; the first steps'
+                // K and V do not.
+                uint32_t q_due = (t.n_t[0] > 0 ? 1u : 0u) | (t.n_t[1] > 0 ? 2u : 0u);
                 auto load_q = [&](bool block) -> bool {
-                    const uint32_t parity = (uint32_t)((nu & 1) ^ 1);
-                    if (!q_due) return true;
-                    if (block) {
-                        if (!mbar_wait_warp(&sh.q_empty, parity, wait)) return false;
-                    } else if (!__all_sync(0xffffffffu, mbar_test_wait(&sh.q_empty, parity))) {
-                        return true;
+                    for (int x = 0; x < 2; ++x) {
+                        if (!((q_due >> x) & 1u)) continue;
+                        const uint32_t parity = (uint32_t)((nq[x] & 1) ^ 1);
+                        if (block) {
+                            if (!mbar_wait_warp(&sh.q_empty[x], parity, wait)) return false;
+                        } else if (!__all_sync(0xffffffffu, mbar_test_wait(&sh.q_empty[x], parity))) {
+                            continue;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[x], (uint32_t)(NH * rows * 128));
+                        __syncwarp();
+                        if (lane < NH)
+                            tma_load_3d(qbuf + x * kTile + lane * kHalf, &mq, lane * 64, t.h[x] * A.G, t.row[x],
+                                        &sh.q_full[x], pol_q);
+                        ++nq[x];
+                        q_due &= ~(1u << x);
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(tiles * NH * rows * 128));
-                    __syncwarp();
-                    if (lane < tiles * NH)
-                        tma_load_3d(qbuf + lane * kHalf, &mq, (lane % NH) * 64, u.h * A.G, t.row + (lane / NH) * P.tb,
-                                    &sh.q_full, pol_q);
-                    ++nu;
-                    q_due = false;
                     return true;
                 };
                 const int32_t *table = A.paged ? A.page_table + (size_t)u.b * A.max_pages : nullptr;
@@ -373,7 +375,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     const int tok = s * kN + at;
                     return A.paged && mine && s < u.s1 && tok < t.lim ? __ldg(table + page_of(P, tok)) : -1;
                 };
-                int next_id = page_id(u.s0);
+                int next_id = page_id(u.s0), pairs = 0;
                 for (int s = u.s0; s < u.s1 && ok; ++s) {
                     const int id = next_id, tok = s * kN + at;
                     next_id = page_id(s + 1);
@@ -384,46 +386,54 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     }
                     const int off = A.paged ? tok - page_of(P, tok) * A.ps : tok;
                     const uint32_t n_in = (uint32_t)__popc(__ballot_sync(0xffffffffu, in));
-                    if (!load_q(s == u.s0 + kAhead)) {
-                        ok = false;
-                        break;
-                    }
-                    if constexpr (K8) {
-                        if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.st_empty[slot], ph, wait)) {
+                    for (int set = 0; set < t.sets && ok; ++set) {
+                        const int h = t.h[set];
+                        if (q_due && !load_q(pairs == kAhead)) {
                             ok = false;
                             break;
                         }
-                        if (lane == 0) mbar_arrive_expect_tx(&sh.st_full[slot], n_in * (32 * D));
-                        __syncwarp();
-                        if (in)
-                            bulk_load(stages + slot * C::kStage + lane * (32 * D),
-                                      static_cast<const uint8_t *>(A.kc) + kv8_block(id, u.h, A.Hkv, A.ps, D) +
-                                          (size_t)off * (2 * D),
-                                      32 * D, &sh.st_full[slot]);
-                        ++ld;
-                        if (++slot == C::kStages) {
-                            slot = 0;
-                            ph ^= 1u;
-                        }
-                    } else {
-                        for (int kv = 0; kv < 2; ++kv) {
-                            if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.empty[slot], ph, wait)) {
+                        ++pairs;
+                        if constexpr (K8) {
+                            if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.st_empty[slot], ph, wait)) {
                                 ok = false;
                                 break;
                             }
-                            if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], n_in * (uint32_t)(P.box * 128));
+                            if (lane == 0) mbar_arrive_expect_tx(&sh.st_full[slot], n_in * (32 * D));
                             __syncwarp();
-                            uint8_t *dst = ring + slot * kTile + hh * kHalf + bx * P.box * 128;
-                            if (in && A.paged)
-                                tma_load_3d(dst, kv ? &mv : &mk, 0, off, (id * A.Hkv + u.h) * NH + hh, &sh.full[slot],
-                                            pol_kv);
-                            else if (in)
-                                tma_load_3d(dst, kv ? &mv : &mk, hh * 64, tok, u.b * A.Hkv + u.h, &sh.full[slot],
-                                            pol_kv);
+                            if (in)
+                                bulk_load(stages + slot * C::kStage + lane * (32 * D),
+                                          static_cast<const uint8_t *>(A.kc) + kv8_block(id, h, A.Hkv, A.ps, D) +
+                                              (size_t)off * (2 * D),
+                                          32 * D, &sh.st_full[slot]);
                             ++ld;
-                            if (++slot == kSlots) {
+                            if (++slot == C::kStages) {
                                 slot = 0;
                                 ph ^= 1u;
+                            }
+                        } else {
+                            for (int kv = 0; kv < 2; ++kv) {
+                                if (__any_sync(0xffffffffu, *abort != 0) ||
+                                    !mbar_wait_warp(&sh.empty[slot], ph, wait)) {
+                                    ok = false;
+                                    break;
+                                }
+                                if (lane == 0) {
+                                    mbar_arrive_expect_tx(&sh.full[slot], n_in * (uint32_t)(P.box * 128));
+                                    *(volatile uint32_t *)&sh.issued = (uint32_t)ld + 1u;
+                                }
+                                __syncwarp();
+                                uint8_t *dst = ring + slot * kTile + hh * kHalf + bx * P.box * 128;
+                                if (in && A.paged)
+                                    tma_load_3d(dst, kv ? &mv : &mk, 0, off, (id * A.Hkv + h) * NH + hh,
+                                                &sh.full[slot], pol_kv);
+                                else if (in)
+                                    tma_load_3d(dst, kv ? &mv : &mk, hh * 64, tok, t.b * A.Hkv + h, &sh.full[slot],
+                                                pol_kv);
+                                ++ld;
+                                if (++slot == kSlots) {
+                                    slot = 0;
+                                    ph ^= 1u;
+                                }
                             }
                         }
                     }
@@ -448,174 +458,170 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         raise_status(A.status, SPEC_DEV_TIMEOUT);
                         break;
                     }
-                if (nu > 0 && !mbar_wait(&sh.q_full, (uint32_t)((nu - 1) & 1)))
-                    raise_status(A.status, SPEC_DEV_TIMEOUT);
+                for (int x = 0; x < 2; ++x)
+                    if (nq[x] > 0 && !mbar_wait(&sh.q_full[x], (uint32_t)((nq[x] - 1) & 1)))
+                        raise_status(A.status, SPEC_DEV_TIMEOUT);
             }
-        } else if (warp == kMmaWarp) {
-            // --------------------------------------------------- MMA issuer
+        } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+            // -------------------------------------------- MMA issuer of tile x
             if (lane == 0) {
+                const int x = warp - kMmaWarp;
                 const uint32_t id_s = idesc(kM, kN, false, false);
                 const uint32_t id_pv = idesc(kM, D, false, true);
-                int slot = 0;                            // ring slot of the next K / V tile
-                uint32_t ph = 0, fix_ph = 0;             // parity of its fill; of the fixes, a bit a slot
-                int nu = 0;                              // parts started
-                int np[2] = {0, 0};                      // P hand-offs taken, per tile
-                int nact[2] = {0, 0};                    // parts in which the tile took part
-                bool ok = true;
-                const uint64_t qd[2] = {smem_desc(smem_u32(qbuf), 16, 1024),
-                                        smem_desc(smem_u32(qbuf + kTile), 16, 1024)};
+                const uint32_t tO = tmem + col_o(x), tS = tmem + col_s(x);
+                const uint64_t qd = smem_desc(smem_u32(qbuf + x * kTile), 16, 1024);
                 // descriptors of slot 0 (K: K-major, V: MN-major); a slot is kTile
                 // further, i.e. kTile >> 4 in the address field
                 const uint64_t kd0 = smem_desc(smem_u32(ring), 16, 1024);
                 const uint64_t vd0 = smem_desc(smem_u32(ring), kHalf, 1024);
-                auto advance = [&]() {
-                    if (++slot == kSlots) {
-                        slot = 0;
-                        ph ^= 1u;
-                    }
-                };
-                auto issue_s = [&](int x, int k_slot) {
-                    const uint64_t kd = kd0 + (uint64_t)(k_slot * (kTile >> 4));
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint64_t off = (uint64_t)((((ks >> 2) * kHalf) + (ks & 3) * 32) >> 4);
-                        mma_ss(tmem + col_s(x), qd[x] + off, kd + off, id_s, ks > 0 ? 1u : 0u);
-                    }
-                    commit(&sh.s_full[x]);
-                };
-                // O_x += P_x V; the tile's first PV of a part overwrites O_x, after
-                // the previous part's epilogue of that tile read it
-                auto issue_pv = [&](int x, int v_slot, bool first) -> bool {
-                    if (!mbar_wait(&sh.p_full[x], (uint32_t)(np[x] & 1), wait)) return false;
-                    ++np[x];
-                    if (first && nact[x] > 0 &&
-                        !mbar_wait(&sh.o_free[x], (uint32_t)((nact[x] - 1) & 1), wait))
-                        return false;
-                    fence_after();
-                    const uint64_t vd = vd0 + (uint64_t)(v_slot * (kTile >> 4));
-#pragma unroll
-                    for (int ks = 0; ks < kN / 16; ++ks)
-                        mma(tmem + col_o(x), tmem + col_s(x) + ks * 8,
-                            vd + (uint64_t)((ks * 2048) >> 4), id_pv, (ks > 0 || !first) ? 1u : 0u);
-                    return true;
-                };
+                uint32_t base = 0;                       // fills of the ring before this part
+                uint32_t np = 0, nact = 0;               // P hand-offs taken; parts with this tile
+                bool ok = true;
                 PartReader reader;
-                Part t;
-                while (ok && reader.next<false>(sh, t, wait, &ok)) {
+                while (ok && reader.next<false>(sh, wait, &ok)) {
+                    const Part &t = sh.parts[reader.i];
+                    const int n = t.n_t[x], sets = t.sets, other = sets == 2 ? 0 : t.n_t[1 - x];
+                    const uint32_t fills = 2u * (uint32_t)(t.n * sets);
+                    const int sure = t.pos[0] + 1 - t.s0 * kN;       // tokens that every row sees, from s0 on
                     reader.release(sh);
                     reader.advance();
-                    const int nA = t.n_t[0], nB = t.n_t[1], n = t.n;
-                    if (*abort || !mbar_wait(&sh.q_full, (uint32_t)(nu & 1), wait) ||
-                        !mbar_wait(&sh.full[slot], ph, wait)) {
-                        ok = false;
-                        break;
+                    // fill of step j's K tile; its V tile is the next one
+                    auto fill = [&](int j) -> uint32_t {
+                        return base + 2u * (uint32_t)(j * sets + (sets == 2 ? x : 0));
+                    };
+                    // a slot is free once both threads have let go of it: each for
+                    // itself, and for the other where that one has no use for it
+                    auto release = [&](uint32_t slot, int j) {
+                        commit(&sh.empty[slot]);
+                        if (j >= other) mbar_arrive(&sh.empty[slot]);
+                    };
+                    auto issue_s = [&](int j) -> bool {
+                        const uint32_t f = fill(j), slot = f % kSlots;
+                        if (!mbar_wait(&sh.full[slot], (f / kSlots) & 1u, wait)) return false;
+                        fence_after();
+                        const uint64_t kd = kd0 + (uint64_t)(slot * (kTile >> 4));
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint64_t off = (uint64_t)((((ks >> 2) * kHalf) + (ks & 3) * 32) >> 4);
+                            mma_ss(tS, qd + off, kd + off, id_s, ks > 0 ? 1u : 0u);
+                        }
+                        commit(&sh.s_full[x]);
+                        release(slot, j);
+                        return true;
+                    };
+                    if (n > 0) {
+                        // (fills may have passed that this tile had no part in: only one
+                        // that has begun is told by its phase's parity)
+                        const long long since = clock64();
+                        while (*(volatile uint32_t *)&sh.issued <= fill(0) && clock64() - since < wait) {}
+                        if (*abort || *(volatile uint32_t *)&sh.issued <= fill(0) ||
+                            !mbar_wait(&sh.q_full[x], nact & 1u, wait) || !issue_s(0)) {
+                            ok = false;
+                            break;
+                        }
                     }
-                    fence_after();
-                    // S(0) of both tiles
-                    if (nA > 0) issue_s(0, slot);
-                    if (nB > 0) issue_s(1, slot);
-                    commit(&sh.empty[slot]);
-                    if (n == 1) commit(&sh.q_empty);
-                    advance();
                     for (int j = 0; j < n; ++j) {
-                        const int vslot = slot;
-                        if (!mbar_wait(&sh.full[vslot], ph, wait)) {
+                        // O += P V, by halves of the keys as P comes; the part's first
+                        // overwrites O, after the epilogue of the part before read it
+                        const uint32_t f = fill(j) + 1u, slot = f % kSlots;
+                        uint64_t *bar = !K8 && (j + 1) * kN > sure ? &sh.fixed[slot] : &sh.full[slot];
+                        if (!mbar_wait(bar, (f / kSlots) & 1u, wait) ||
+                            (j == 0 && nact > 0 && !mbar_wait(&sh.o_free[x], (nact - 1) & 1u, wait))) {
                             ok = false;
                             break;
                         }
-                        if (!K8 && ragged(t, t.s0 + j)) {
-                            if (!mbar_wait(&sh.fixed[vslot], (fix_ph >> vslot) & 1u, wait)) {
+                        const uint64_t vd = vd0 + (uint64_t)(slot * (kTile >> 4));
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (!mbar_wait(&sh.p_full[x][half], np & 1u, wait)) {
                                 ok = false;
                                 break;
                             }
-                            fix_ph ^= 1u << vslot;
+                            fence_after();
+#pragma unroll
+                            for (int ks = half * (kN / 32); ks < (half + 1) * (kN / 32); ++ks)
+                                mma(tO, tS + ks * 8, vd + (uint64_t)((ks * 2048) >> 4), id_pv,
+                                    (ks > 0 || j > 0) ? 1u : 0u);
                         }
-                        advance();
-                        const bool next = j + 1 < n;
-                        const int kslot = slot;
-                        if (j < nA) {
-                            if (!issue_pv(0, vslot, j == 0)) {
-                                ok = false;
-                                break;
-                            }
-                            if (j + 1 == nA) commit(&sh.o_done[0]);
-                        }
-                        if (next && !mbar_wait(&sh.full[kslot], ph, wait)) {
+                        if (!ok) break;
+                        ++np;
+                        if (j + 1 == n) commit(&sh.o_done[x]);
+                        release(slot, j);
+                        if (j + 1 < n && !issue_s(j + 1)) {
                             ok = false;
                             break;
-                        }
-                        if (j + 1 < nA) issue_s(0, kslot);
-                        if (j < nB) {
-                            if (!issue_pv(1, vslot, j == 0)) {
-                                ok = false;
-                                break;
-                            }
-                            if (j + 1 == nB) commit(&sh.o_done[1]);
-                            commit(&sh.empty[vslot]);
-                            if (j + 1 < nB) issue_s(1, kslot);
-                        } else {
-                            commit(&sh.empty[vslot]);
-                        }
-                        if (next) {
-                            commit(&sh.empty[kslot]);
-                            if (j + 2 == n) commit(&sh.q_empty);
-                            advance();
                         }
                     }
-                    if (nA > 0) ++nact[0];
-                    if (nB > 0) ++nact[1];
-                    ++nu;
+                    if (n > 0) ++nact;
+                    base += fills;
                 }
                 if (!ok) {
                     raise_status(A.status, SPEC_DEV_TIMEOUT);
                     *abort = 1;
                 }
                 // every MMA issued above has completed before TMEM is released
-                commit(&sh.drain);
-                if (!mbar_wait(&sh.drain, 0)) raise_status(A.status, SPEC_DEV_TIMEOUT);
+                commit(&sh.drain[x]);
+                if (!mbar_wait(&sh.drain[x], 0)) raise_status(A.status, SPEC_DEV_TIMEOUT);
             }
-        } else if (!K8 && (warp == kFixWarp || warp == kFixWarp + 1)) {
+        } else if (!K8 && warp == kFixWarp) {
             // ------------------------- values that not every row sees, looked over
-            // (Both warps see every fill of the ring, and release it with the MMAs:
-            // a warp that skipped fills could take an earlier phase for its own.)
-            const int tid = threadIdx.x - kFixWarp * 32;
+            // (The warp sees every fill of the ring, and releases it with the MMAs: one
+            // that skipped fills could take an earlier phase for its own.)
             int slot = 0;
             uint32_t ph = 0;
             bool ok = true;
             PartReader reader;
-            Part t;
-            while (ok && reader.next<true>(sh, t, wait, &ok)) {
-                int *bad = &sh.bad[reader.i][warp - kFixWarp];
+            while (ok && reader.next<true>(sh, wait, &ok)) {
+                const Part &t = sh.parts[reader.i];
+                int *bad = &sh.bad[reader.i][0];
                 bool fresh = true;
-                for (int i = 0; i < 2 * t.n; ++i) {
-                    const int s = t.s0 + (i >> 1);
+                const int per = 2 * t.sets;              // fills a step
+                for (int i = 0; i < per * t.n; ++i) {
+                    const int s = t.s0 + i / per;
                     if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.full[slot], ph, wait)) {
                         ok = false;
                         break;
                     }
                     if ((i & 1) && ragged(t, s)) {
                         if (fresh) {
-                            if (lane == 0) *bad = 0x7fffffff;
+                            if (lane < 2) bad[lane] = 0x7fffffff;
                             __syncwarp();
                             fresh = false;
                         }
+                        // (the tiles of a unit of two heads are noted apart)
+                        int *mine = bad + (t.sets == 2 ? (i >> 1) & 1 : 0);
                         uint8_t *v = ring + slot * kTile;
-                        const int r0 = max(0, t.pos + 1 - s * kN), r1 = t.lim - s * kN;
-                        for (int k = r0 * (NH * 8) + tid; k < kN * NH * 8; k += 64) {
+                        const int r0 = max(0, t.pos[0] + 1 - s * kN), r1 = t.lim - s * kN;
+                        auto at = [&](int k) {
                             const int r = k / (NH * 8), c = k % (NH * 8);
-                            uint4 *p = reinterpret_cast<uint4 *>(v + (c / 8) * kHalf + r * 128 + (((c % 8) ^ (r & 7)) << 4));
-                            bool zero = r >= r1;
-                            if (!zero && odd8(*p)) {
-                                atomicMin(bad, s * kN + r);
-                                zero = true;
+                            return reinterpret_cast<uint4 *>(v + (c / 8) * kHalf + r * 128 + (((c % 8) ^ (r & 7)) << 4));
+                        };
+                        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                        // eight vectors in flight; those that have one looked at again
+                        const int end = min(r1, kN) * (NH * 8);
+                        for (int k0 = r0 * (NH * 8) + lane; k0 < end; k0 += 32 * 8) {
+                            uint4 w[8];
+                            bool odd = false;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = k0 + 32 * e < end ? *at(k0 + 32 * e) : zero;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) odd = odd || odd8(w[e]);
+                            if (!odd) continue;
+                            for (int e = 0; e < 8; ++e) {
+                                const int k = k0 + 32 * e;
+                                if (k >= end || !odd8(*at(k))) continue;
+                                atomicMin(mine, s * kN + k / (NH * 8));
+                                *at(k) = zero;
                             }
-                            if (zero) *p = make_uint4(0u, 0u, 0u, 0u);
                         }
+                        for (int k = max(r1, 0) * (NH * 8) + lane; k < kN * NH * 8; k += 32) *at(k) = zero;
                         fence_async();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.fixed[slot]);
                     }
-                    if (lane == 0) mbar_arrive(&sh.empty[slot]);
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sh.fixed[slot]);
+                        mbar_arrive(&sh.empty[slot]);
+                    }
                     if (++slot == kSlots) {
                         slot = 0;
                         ph ^= 1u;
@@ -645,28 +651,30 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             const uint32_t at0 = to + (((2 * (c % 4) + swap) ^ (tr & 7)) << 4);
             const uint32_t at1 = to + (((2 * (c % 4) + 1 - swap) ^ (tr & 7)) << 4);
             int slot = 0, stage = 0;
+            uint32_t fills = 0;
             uint32_t ph = 1, sph = 0;                // parity of the slot's release; of the stage's fill
             bool ok = true;
             PartReader reader;
-            Part t;
-            while (ok && reader.next<true>(sh, t, wait, &ok)) {
-                int *bad = &sh.bad[reader.i][warp - kConvWarp];
+            while (ok && reader.next<true>(sh, wait, &ok)) {
+                const Part &t = sh.parts[reader.i];
+                int *bad = &sh.bad[reader.i][2 * (warp - kConvWarp)];
                 bool fresh = true;
                 const int32_t *table = A.page_table + (size_t)t.b * A.max_pages;
-                const int s1 = t.s0 + t.n;
                 // scales of the step's eight groups of 16 tokens: lane 2 i + x has
                 // group i's of K (x = 0) or V; loaded a step ahead
-                auto load_scale = [&](int s) -> float {
-                    const int tok = s * kN + (lane >> 1) * 16;
-                    if (lane >= 16 || s >= s1 || tok >= t.lim) return 1.f;
+                auto load_scale = [&](int i) -> float {
+                    const int s = t.s0 + i / t.sets, tok = s * kN + (lane >> 1) * 16;
+                    if (lane >= 16 || i >= t.n * t.sets || tok >= t.lim) return 1.f;
                     const int id = __ldg(table + page_of(P, tok));
                     if (id < 0 || id >= A.n_pages) return 1.f;
-                    return __ldg(A.scales + ((size_t)id * A.Hkv + t.h) * 2 + (lane & 1));
+                    return __ldg(A.scales + ((size_t)id * A.Hkv + t.h[i % t.sets]) * 2 + (lane & 1));
                 };
-                float next_scale = load_scale(t.s0);
-                for (int s = t.s0; s < s1 && ok; ++s) {
+                float next_scale = load_scale(0);
+                for (int i = 0; i < t.n * t.sets && ok; ++i) {
+                    const int s = t.s0 + i / t.sets;
+                    int *mine = bad + i % t.sets;
                     const float my_scale = kv8_read_scale(next_scale);
-                    next_scale = load_scale(s + 1);
+                    next_scale = load_scale(i + 1);
                     // 2^e, e <= 7: its codes' factor 2^(120 + e) is a bf16
                     const uint32_t sb = __float_as_uint(my_scale);
                     const bool plain = (sb & 0x007fffffu) == 0u && sb <= 0x43000000u;
@@ -678,7 +686,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     }
                     const bool rag = ragged(t, s);
                     if (rag && fresh) {
-                        if (lane == 0) *bad = 0x7fffffff;
+                        if (lane < 2) bad[lane] = 0x7fffffff;
                         __syncwarp();
                         fresh = false;
                     }
@@ -688,34 +696,42 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         uint4 v[NI];
                         uint32_t nan = 0;
 #pragma unroll
-                        for (int i = 0; i < NI; ++i) {
-                            v[i] = *reinterpret_cast<const uint4 *>(codes + i * (TPI * 2 * D));
-                            nan |= nan4(v[i].x) | nan4(v[i].y) | nan4(v[i].z) | nan4(v[i].w);
+                        for (int k = 0; k < NI; ++k) {
+                            v[k] = *reinterpret_cast<const uint4 *>(codes + k * (TPI * 2 * D));
+                            nan |= nan4(v[k].x) | nan4(v[k].y) | nan4(v[k].z) | nan4(v[k].w);
                         }
-                        const bool fast = __all_sync(0xffffffffu, !(nan & 0x80808080u)) && all_plain && !rag;
+                        const bool fast = __all_sync(0xffffffffu, !(nan & 0x80808080u)) && all_plain;
                         if (!mbar_wait_warp(&sh.empty[slot], ph, wait)) {
                             ok = false;
                             break;
                         }
+                        if (tid == 0) *(volatile uint32_t *)&sh.issued = ++fills;
                         uint8_t *dst = ring + slot * kTile;
+                        if (fast && !rag) {
 #pragma unroll
-                        for (int i = 0; i < NI; ++i) {
-                            const int group = ((i * TPI + tr) >> 4) * 2 + x;
-                            uint4 lo, hi;
-                            if (fast) {
-                                widen16(v[i], __shfl_sync(0xffffffffu, my_factor, group), lo, hi);
-                            } else {
-                                widen16_any(v[i], __shfl_sync(0xffffffffu, my_scale, group), lo, hi);
-                                const int tok = s * kN + i * TPI + tr;
+                            for (int k = 0; k < NI; ++k) {
+                                uint4 lo, hi;
+                                widen16(v[k], __shfl_sync(0xffffffffu, my_factor, ((k * TPI + tr) >> 4) * 2 + x), lo, hi);
+                                *reinterpret_cast<uint4 *>(dst + at0 + k * (TPI * 128)) = swap ? hi : lo;
+                                *reinterpret_cast<uint4 *>(dst + at1 + k * (TPI * 128)) = swap ? lo : hi;
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < NI; ++k) {
+                                const int group = ((k * TPI + tr) >> 4) * 2 + x;
+                                uint4 lo, hi;
+                                if (fast) widen16(v[k], __shfl_sync(0xffffffffu, my_factor, group), lo, hi);
+                                else widen16_any(v[k], __shfl_sync(0xffffffffu, my_scale, group), lo, hi);
+                                const int tok = s * kN + k * TPI + tr;
                                 if (tok >= t.lim) {
                                     lo = hi = make_uint4(0u, 0u, 0u, 0u);
-                                } else if (x == 1 && tok > t.pos && (odd8(lo) || odd8(hi))) {
-                                    atomicMin(bad, tok);
+                                } else if (x == 1 && tok > t.pos[0] && !fast && (odd8(lo) || odd8(hi))) {
+                                    atomicMin(mine, tok);
                                     lo = hi = make_uint4(0u, 0u, 0u, 0u);
                                 }
+                                *reinterpret_cast<uint4 *>(dst + at0 + k * (TPI * 128)) = swap ? hi : lo;
+                                *reinterpret_cast<uint4 *>(dst + at1 + k * (TPI * 128)) = swap ? lo : hi;
                             }
-                            *reinterpret_cast<uint4 *>(dst + at0 + i * (TPI * 128)) = swap ? hi : lo;
-                            *reinterpret_cast<uint4 *>(dst + at1 + i * (TPI * 128)) = swap ? lo : hi;
                         }
                         fence_async();
                         __syncwarp();
@@ -748,14 +764,14 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
         const uint32_t lane_base = (uint32_t)((warp % kGroupWarps) * 32) << 16;
         const uint32_t tS = tmem + lane_base + col_s(x), tO = tmem + lane_base + col_o(x);
         const float sc = A.scale_log2;
-        const int rt = r / A.G, rg = r - rt * A.G;       // the row's token and query head
+        const int rt = r / A.G;                          // the row's token
         int ns = 0, nact = 0;      // S hand-offs taken; parts this tile took part in
         bool ok = true;
         PartReader reader;
-        Part t;
-        while (ok && reader.next<true>(sh, t, wait, &ok)) {
+        while (ok && reader.next<true>(sh, wait, &ok)) {
+            const Part &t = sh.parts[reader.i];
             const bool row_ok = rt < t.nt[x];
-            const int n = t.n_t[x];
+            const int n = t.n_t[x], s0 = t.s0;
             if (n == 0) {                                // (no such tile, or tile A is through: an empty part)
                 if (row_ok) A.part_ml[(size_t)t.slot * A.ru + x * rows + r] = make_float2(-INFINITY, 0.f);
                 __syncwarp();
@@ -764,7 +780,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 continue;
             }
             const bool warp_ok = __any_sync(0xffffffffu, row_ok);
-            const int sure = t.pos + x * P.tb + 1;       // tokens the tile's first row sees
+            const int sure = t.pos[x] + 1;               // tokens the tile's first row sees
             const int seen = sure + rt;                  // and this row
             float m_used = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j) {
@@ -778,10 +794,13 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 if (!warp_ok) {                          // (rows without a query: P is whatever is there)
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.p_full[x]);
+                    if (lane == 0) {
+                        mbar_arrive(&sh.p_full[x][0]);
+                        mbar_arrive(&sh.p_full[x][1]);
+                    }
                     continue;
                 }
-                const int c0 = (t.s0 + j) * kN;
+                const int c0 = (s0 + j) * kN;
                 const bool masked = c0 + kN > sure;
                 // the S row: four TMEM loads in flight, one wait (each
                 // wait_ld ties its registers; the later ones return at once)
@@ -794,11 +813,10 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 if (masked) {
 #pragma unroll
                     for (int c = 0; c < kN / 32; ++c) {
-                        const int n = seen - c0 - c * 32;
-                        const uint32_t vm = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+                        const int ns = seen - c0 - c * 32;           // seen ones of these 32
+                        if (__all_sync(0xffffffffu, ns >= 32)) continue;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            v[c][e] = ((vm >> e) & 1u) ? v[c][e] : 0xff800000u;
+                        for (int e = 0; e < 32; ++e) v[c][e] = e < ns ? v[c][e] : 0xff800000u;
                     }
                 }
                 // the row maximum (three-input max, four chains)
@@ -859,6 +877,12 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         pw[e] = pack_bf16(p0, p1);
                     }
                     st16(tS + c * 16, pw);
+                    if (c == kN / 64 - 1) {              // the first half's MMAs may start
+                        wait_st();
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.p_full[x][0]);
+                    }
                 }
                 float rs[4];
                 unpair(rs2[0], rs[0], rs[1]);
@@ -867,7 +891,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[x]);
+                if (lane == 0) mbar_arrive(&sh.p_full[x][1]);
             }
             if (!ok) break;
             // epilogue: O / l (bf16) and the LSE of this row, or its part of them
@@ -879,48 +903,97 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             // a non-finite value among those looked over, which this row sees
             bool odd = false;
             if (ragged(t, t.s0 + n - 1)) {
-                const volatile int *bad = sh.bad[reader.i];
-                for (int w = 0; w < (K8 ? 4 : 2); ++w) odd = odd || seen > bad[w];
+                const volatile int *bad = sh.bad[reader.i] + (t.sets == 2 ? x : 0);
+                for (int w = 0; w < (K8 ? 4 : 1); ++w) odd = odd || seen > bad[2 * w];
             }
             const bool whole = t.slot < 0;
             const float inv = odd ? __uint_as_float(0x7fffffffu) : whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            const size_t out = ((size_t)t.row + x * P.tb + rt) * A.Hq + (size_t)t.h * A.G + rg;
-            const size_t part = (size_t)(whole ? 0 : t.slot) * A.ru + x * rows + r;
-            if (warp_ok) {
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t v[32];
-                    ld32(tO + c * 32, v);
-                    wait_ld(v);
-                    if (!row_ok) continue;
-                    if (whole) {
-                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(A.o) + out * D + c * 32;
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            w[e] = pack_bf16(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 8) store32(dst + 2 * e, &w[e], P.wide_o);
-                    } else {
-                        float *dst = A.part_o + part * D + c * 32;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * inv);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) store32(dst + e, &v[e], true);
-                    }
-                }
-                if (row_ok) {
-                    if (whole)
-                        A.lse[out] = l == 0.f ? -INFINITY : l != l ? l : (m_used + log2f(l)) * kLn2;
-                    else
-                        A.part_ml[part] = make_float2(m_used, l);
-                }
+            // A row's 2 D bytes -- all of it as bf16, or half of it as fp32 -- pass through
+            // the place of its query, 16-byte chunks swizzled, and leave as whole lines,
+            // two (D = 64: four) rows an instruction; what waits for the tile's O or
+            // the place goes on before the stores.
+            constexpr int RB = 2 * D, CH = RB / 16;      // bytes, chunks of a row
+            constexpr int RI = 32 / CH;                  // rows an instruction
+            uint8_t *stage = qbuf + x * kTile + (warp % kGroupWarps) * (32 * RB);
+            const int r0 = (warp % kGroupWarps) * 32, nr = min(32, t.nt[x] * A.G - r0);
+            // row r of the tile is row first + r + (its token) * skip of o (or of the parts)
+            const size_t first = whole ? (size_t)t.row[x] * A.Hq + (size_t)t.h[x] * A.G : (size_t)t.slot * A.ru + x * rows;
+            const uint32_t skip = whole ? (uint32_t)(A.Hq - A.G) : 0u;
+            if (row_ok) {
+                const size_t at = first + r + (size_t)rt * skip;
+                if (whole) A.lse[at] = l == 0.f ? -INFINITY : l != l ? l : (m_used + log2f(l)) * kLn2;
+                else A.part_ml[at] = make_float2(m_used, l);
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh.o_free[x]);
-                reader.release(sh);
+            auto let_go_of_o = [&]() {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.o_free[x]);
+            };
+            auto let_go_of_q = [&]() {
+                fence_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.q_empty[x]);
+                    reader.release(sh);
+                }
+            };
+            // N columns of O from column c0 on, as 16-byte chunks of bf16 or fp32
+            auto pass = [&](auto as_bf16, int c0, bool last) {
+                constexpr bool kBf16 = decltype(as_bf16)::value;
+                constexpr int N = kBf16 ? D : D / 2;
+                uint32_t v[N / 32][32];
+#pragma unroll
+                for (int c = 0; c < N / 32; ++c) ld32(tO + c0 + c * 32, v[c]);
+#pragma unroll
+                for (int c = 0; c < N / 32; ++c) wait_ld(v[c]);
+                if (last) let_go_of_o();
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    uint4 w;
+                    if constexpr (kBf16) {
+                        const uint32_t (&y)[32] = v[k / 4];
+                        const int e = 8 * (k % 4);
+                        w = make_uint4(pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
+                                       pack_bf16(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv),
+                                       pack_bf16(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv),
+                                       pack_bf16(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv));
+                    } else {
+                        const uint32_t (&y)[32] = v[k / 8];
+                        const int e = 4 * (k % 8);
+                        w = make_uint4(__float_as_uint(__uint_as_float(y[e]) * inv),
+                                       __float_as_uint(__uint_as_float(y[e + 1]) * inv),
+                                       __float_as_uint(__uint_as_float(y[e + 2]) * inv),
+                                       __float_as_uint(__uint_as_float(y[e + 3]) * inv));
+                    }
+                    *reinterpret_cast<uint4 *>(stage + lane * RB + ((k ^ (lane & 7)) << 4)) = w;
+                }
+                __syncwarp();
+                uint4 w[CH];
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    const int rr = k * RI + lane / CH;
+                    w[k] = *reinterpret_cast<const uint4 *>(stage + rr * RB + (((lane % CH) ^ (rr & 7)) << 4));
+                }
+                __syncwarp();
+                if (last) let_go_of_q();
+                uint8_t *dst = kBf16 ? static_cast<uint8_t *>(A.o) : reinterpret_cast<uint8_t *>(A.part_o) + c0 * 4;
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    const int rr = k * RI + lane / CH;
+                    if (rr >= nr) continue;
+                    const uint32_t tok = ((uint32_t)(r0 + rr) * P.g_mul) >> 16;
+                    const size_t at = first + (uint32_t)(r0 + rr) + (size_t)tok * skip;
+                    *reinterpret_cast<uint4 *>(dst + at * (kBf16 ? 2 * D : 4 * D) + (lane % CH) * 16) = w[k];
+                }
+            };
+            if (!warp_ok) {
+                let_go_of_o();
+                let_go_of_q();
+            } else if (whole) {
+                pass(Bool<true>{}, 0, true);
+            } else {
+                pass(Bool<false>{}, 0, false);
+                pass(Bool<false>{}, D / 2, true);
             }
             reader.advance();
             ++nact;
@@ -952,15 +1025,15 @@ spec_status_t launch_tc(const ctc::Params &P, const CUtensorMap (&m)[3], int n_c
 ChunkPlan chunk_tc_plan(const ChunkParams &P, bool kv8) {
     (void)kv8;
     const int tb = ctc::kM / P.G;
-    return ChunkPlan{2 * tb * P.G, ctc::kN, 2 * ctc::kN, 2 * ctc::kN, num_sms()};
+    return ChunkPlan{2 * tb * P.G, 2 * tb, ctc::kN, 2 * ctc::kN, 2 * ctc::kN, num_sms()};
 }
 
 spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStream_t s) {
     ctc::Params P{};
     P.c = C;
     P.tb = ctc::kM / C.G;
+    P.g_mul = (uint32_t)((65536 + C.G - 1) / C.G);
     P.box = ctc::kN;
-    P.wide_o = reinterpret_cast<uintptr_t>(C.o) % 32 == 0;
     if (C.paged) {
         int a = C.ps, b = ctc::kN;                       // the greatest common divisor
         while (b) {
