@@ -186,6 +186,13 @@ __device__ __forceinline__ bool odd8(const uint4 &v) {
     return ((((v.x & m) + one) | ((v.y & m) + one) | ((v.z & m) + one) | ((v.w & m) + one)) & 0x80008000u) != 0;
 }
 
+// a * 0 + c of two bf16
+__device__ __forceinline__ uint32_t times0(uint32_t a, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(0u), "r"(c));
+    return d;
+}
+
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // global -> shared bulk copy; both 16-byte aligned, bytes a multiple of 16
@@ -595,6 +602,9 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             // ------------------------- values that not every row sees, looked over
             // (The warp sees every fill of the ring, and releases it with the MMAs: one
             // that skipped fills could take an earlier phase for its own.)
+            // this lane's vector of rows 0 .. 3 and of rows 4 .. 7 of an eight
+            const uint32_t lo = (uint32_t)((lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
+            const uint32_t hi = (uint32_t)((4 + (lane >> 3)) * 128 + (((lane & 7) ^ (4 + (lane >> 3))) << 4));
             int slot = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -616,33 +626,41 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                             __syncwarp();
                             fresh = false;
                         }
-                        // (the tiles of a unit of two heads are noted apart)
-                        int *mine = bad + (t.sets == 2 ? (i >> 1) & 1 : 0);
                         uint8_t *v = ring + slot * kTile;
-                        const int r0 = max(0, t.pos[0] + 1 - s * kN), r1 = t.lim - s * kN;
-                        auto at = [&](int k) {
-                            const int r = k / (NH * 8), c = k % (NH * 8);
-                            return reinterpret_cast<uint4 *>(v + (c / 8) * kHalf + r * 128 + (((c % 8) ^ (r & 7)) << 4));
-                        };
+                        const int r0 = max(0, t.pos[0] + 1 - s * kN), r1 = max(0, min(kN, t.lim - s * kN));
                         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                        // eight vectors in flight; those that have one looked at again
-                        const int end = min(r1, kN) * (NH * 8);
-                        for (int k0 = r0 * (NH * 8) + lane; k0 < end; k0 += 32 * 8) {
-                            uint4 w[8];
-                            bool odd = false;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = k0 + 32 * e < end ? *at(k0 + 32 * e) : zero;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) odd = odd || odd8(w[e]);
-                            if (!odd) continue;
-                            for (int e = 0; e < 8; ++e) {
-                                const int k = k0 + 32 * e;
-                                if (k >= end || !odd8(*at(k))) continue;
-                                atomicMin(mine, s * kN + k / (NH * 8));
-                                *at(k) = zero;
+                        // past the last token: zeros
+                        for (int g = r1 >> 3; g < kN / 8; ++g) {
+                            for (int hh = 0; hh < NH; ++hh) {
+                                uint8_t *p = v + hh * kHalf + g * 1024;
+                                if (8 * g + (lane >> 3) >= r1) *reinterpret_cast<uint4 *>(p + lo) = zero;
+                                if (8 * g + 4 + (lane >> 3) >= r1) *reinterpret_cast<uint4 *>(p + hi) = zero;
                             }
                         }
-                        for (int k = max(r1, 0) * (NH * 8) + lane; k < kN * NH * 8; k += 32) *at(k) = zero;
+                        // x * 0 + sum is NaN from the first x on that is not finite
+                        uint32_t sum = 0u;
+#pragma unroll 4
+                        for (int g = r0 >> 3; 8 * g < r1; ++g)
+#pragma unroll
+                            for (int hh = 0; hh < NH; ++hh) {
+                                const uint8_t *p = v + hh * kHalf + g * 1024;
+                                const uint4 a = *reinterpret_cast<const uint4 *>(p + lo);
+                                const uint4 b = *reinterpret_cast<const uint4 *>(p + hi);
+                                sum = times0(a.x, times0(a.y, times0(a.z, times0(a.w, sum))));
+                                sum = times0(b.x, times0(b.y, times0(b.z, times0(b.w, sum))));
+                            }
+                        if (__any_sync(0xffffffffu, (sum & 0x7fff7fffu) != 0u)) {
+                            // (the tiles of a unit of two heads are noted apart)
+                            int *mine = bad + (t.sets == 2 ? (i >> 1) & 1 : 0);
+                            for (int r = r0; r < r1; ++r) {
+                                if (lane >= NH * 8) continue;
+                                uint4 *p = reinterpret_cast<uint4 *>(v + (lane >> 3) * kHalf + r * 128 +
+                                                                     (((lane & 7) ^ (r & 7)) << 4));
+                                if (!odd8(*p)) continue;
+                                atomicMin(mine, s * kN + r);
+                                *p = zero;
+                            }
+                        }
                         fence_async();
                     }
                     __syncwarp();
@@ -947,11 +965,6 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             // row r of the tile is row first + r + (its token) * skip of o (or of the parts)
             const size_t first = whole ? (size_t)t.row[x] * A.Hq + (size_t)t.h[x] * A.G : (size_t)t.slot * A.ru + x * rows;
             const uint32_t skip = whole ? (uint32_t)(A.Hq - A.G) : 0u;
-            if (row_ok) {
-                const size_t at = first + r + (size_t)rt * skip;
-                if (whole) A.lse[at] = l == 0.f ? -INFINITY : l != l ? l : (m_used + log2f(l)) * kLn2;
-                else A.part_ml[at] = make_float2(m_used, l);
-            }
             auto let_go_of_o = [&]() {
                 fence_before();
                 __syncwarp();
@@ -1022,6 +1035,11 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             } else {
                 pass(Bool<false>{}, 0, false);
                 pass(Bool<false>{}, D / 2, true);
+            }
+            if (row_ok) {
+                const size_t at = first + r + (size_t)rt * skip;
+                if (whole) A.lse[at] = l == 0.f ? -INFINITY : l != l ? l : (m_used + log2f(l)) * kLn2;
+                else A.part_ml[at] = make_float2(m_used, l);
             }
             reader.advance();
             ++nact;
