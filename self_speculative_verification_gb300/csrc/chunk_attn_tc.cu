@@ -498,6 +498,20 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     auto fill = [&](int j) -> uint32_t {
                         return base + 2u * (uint32_t)(j * sets + (sets == 2 ? x : 0));
                     };
+                    // Waits until the producer has begun fill f: from then on the parity of
+                    // the slot's phase tells f.  A tile that takes every fill needs that
+                    // only where a part begins (it may have had no part in the ones before);
+                    // one of a unit of two heads passes the other's fills by, whose copies
+                    // may come after later ones of its own.  (Widened codes come in order.)
+                    auto begun = [&](uint32_t f) -> bool {
+                        const long long since = clock64();
+                        while (*(volatile uint32_t *)&sh.issued <= f) {
+                            if (clock64() - since >= wait) return false;
+                            __nanosleep(20);
+                        }
+                        return true;
+                    };
+                    const bool passes = !K8 && sets == 2;
                     // a slot is free once both threads have let go of it: each for
                     // itself, and for the other where that one has no use for it
                     auto release = [&](uint32_t slot, int j) {
@@ -524,10 +538,12 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     };
                     auto issue_s = [&](int j, bool locked) -> bool {
                         const uint32_t f = fill(j), slot = f % kSlots;
-                        if (!mbar_test_wait(&sh.full[slot], (f / kSlots) & 1u)) {
+                        if ((passes && *(volatile uint32_t *)&sh.issued <= f) ||
+                            !mbar_test_wait(&sh.full[slot], (f / kSlots) & 1u)) {
                             if (locked) unlock();
                             locked = false;
-                            if (!mbar_wait(&sh.full[slot], (f / kSlots) & 1u, wait)) return false;
+                            if ((passes && !begun(f)) || !mbar_wait(&sh.full[slot], (f / kSlots) & 1u, wait))
+                                return false;
                         }
                         if (!locked && !lock()) return false;
                         fence_after();
@@ -543,11 +559,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         return true;
                     };
                     if (n > 0) {
-                        // (fills may have passed that this tile had no part in: only one
-                        // that has begun is told by its phase's parity)
-                        const long long since = clock64();
-                        while (*(volatile uint32_t *)&sh.issued <= fill(0) && clock64() - since < wait) {}
-                        if (*abort || *(volatile uint32_t *)&sh.issued <= fill(0) ||
+                        if (*abort || !begun(fill(0)) ||
                             !mbar_wait(&sh.q_full[x], nact & 1u, wait) || !issue_s(0, false)) {
                             ok = false;
                             break;
@@ -558,7 +570,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         // overwrites O, after the epilogue of the part before read it
                         const uint32_t f = fill(j) + 1u, slot = f % kSlots;
                         uint64_t *bar = !K8 && (j + 1) * kN > sure ? &sh.fixed[slot] : &sh.full[slot];
-                        if (!mbar_wait(bar, (f / kSlots) & 1u, wait) ||
+                        if ((passes && !begun(f)) || !mbar_wait(bar, (f / kSlots) & 1u, wait) ||
                             (j == 0 && nact > 0 && !mbar_wait(&sh.o_free[x], (nact - 1) & 1u, wait))) {
                             ok = false;
                             break;
@@ -638,7 +650,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                             }
                         }
                         // x * 0 + sum is NaN from the first x on that is not finite
-                        uint32_t sum = 0u;
+                        uint32_t sum[8] = {};
 #pragma unroll 4
                         for (int g = r0 >> 3; 8 * g < r1; ++g)
 #pragma unroll
@@ -646,10 +658,19 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                                 const uint8_t *p = v + hh * kHalf + g * 1024;
                                 const uint4 a = *reinterpret_cast<const uint4 *>(p + lo);
                                 const uint4 b = *reinterpret_cast<const uint4 *>(p + hi);
-                                sum = times0(a.x, times0(a.y, times0(a.z, times0(a.w, sum))));
-                                sum = times0(b.x, times0(b.y, times0(b.z, times0(b.w, sum))));
+                                sum[0] = times0(a.x, sum[0]);
+                                sum[1] = times0(a.y, sum[1]);
+                                sum[2] = times0(a.z, sum[2]);
+                                sum[3] = times0(a.w, sum[3]);
+                                sum[4] = times0(b.x, sum[4]);
+                                sum[5] = times0(b.y, sum[5]);
+                                sum[6] = times0(b.z, sum[6]);
+                                sum[7] = times0(b.w, sum[7]);
                             }
-                        if (__any_sync(0xffffffffu, (sum & 0x7fff7fffu) != 0u)) {
+                        uint32_t any = 0u;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) any |= sum[e] & 0x7fff7fffu;
+                        if (__any_sync(0xffffffffu, any != 0u)) {
                             // (the tiles of a unit of two heads are noted apart)
                             int *mine = bad + (t.sets == 2 ? (i >> 1) & 1 : 0);
                             for (int r = r0; r < r1; ++r) {
