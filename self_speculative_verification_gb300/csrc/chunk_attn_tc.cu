@@ -21,7 +21,7 @@
 //   first place they note, for a hidden value's weight of zero would not keep
 //   it out of the sum.
 // * 8-bit cache: 16 tokens' codes, keys and values, are one run of memory, which
-//   a bulk copy brings into a stage; warps 12-15 turn them into the slots' bf16
+//   a bulk copy brings into a stage; warps 12-19 turn them into the slots' bf16
 //   tiles (code * scale, exact for a power of two) and do what warp 11 does
 //   on the way.
 // * Softmax and TMEM as in the prefill kernel: O (fp32) and S of a tile side by
@@ -46,7 +46,8 @@ constexpr int kGroupWarps = 4;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;              // and 10
 constexpr int kFixWarp = 11;             // bf16 cache
-constexpr int kConvWarp = 12;            // 8-bit cache: 12 .. 15
+constexpr int kConvWarp = 12;            // 8-bit cache: 12 .. 19
+constexpr int kConvWarps = 8;
 constexpr int kTmemCols = 512;
 constexpr int kParts = 8;                // parts announced ahead
 // K/V pairs of a part that are copied before its queries: their slots (two each)
@@ -68,11 +69,11 @@ struct Cfg {
     static constexpr int kStages = K8 ? (D == 128 ? 2 : 4) : 0;
     static constexpr int kStage = 2 * kN * D;            // codes of a step, K and V
     static_assert(K8 ? kAhead <= kStages && kSlots >= 3 : 2 * kAhead < kSlots, "steps ahead of their queries");
-    static constexpr int kWarps = K8 ? 16 : 12;
+    static constexpr int kWarps = K8 ? 20 : 12;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kLaunchRegs = K8 ? 128 : 168;
-    static constexpr int kSoftmaxRegs = K8 ? 176 : 184;
-    static constexpr int kOtherRegs = K8 ? 80 : 128;
+    static constexpr int kLaunchRegs = K8 ? 96 : 168;
+    static constexpr int kSoftmaxRegs = K8 ? 128 : 184;
+    static constexpr int kOtherRegs = K8 ? 72 : 128;
     static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
                   "register split exceeds the launch allocation");
 };
@@ -113,7 +114,7 @@ struct Shared {
     uint32_t issued;         // fills of the ring begun
     int mma_busy;            // whether a tile's MMAs are being issued
     int abort;
-    int bad[kParts][8];      // by part, looking warp and set: first token with a non-finite value
+    int bad[kParts][2 * kConvWarps];     // by part, looking warp and set: first token with a non-finite value
     Part parts[kParts];
     ChunkShare share;
 };
@@ -281,16 +282,16 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
         }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&sh.part_full[i], 1);
-            mbar_init(&sh.part_free[i], 8 + 2 + (K8 ? 4 : 1));       // softmax, MMA, and warp 11 or 12 to 15
+            mbar_init(&sh.part_free[i], 8 + 2 + (K8 ? kConvWarps : 1));  // softmax, MMA, and warp 11 or 12 on
         }
         for (int s = 0; s < kSlots; ++s) {
-            mbar_init(&sh.full[s], K8 ? 4 : 1);
+            mbar_init(&sh.full[s], K8 ? kConvWarps : 1);
             mbar_init(&sh.empty[s], K8 ? 2 : 3);                     // MMA threads, warp 11
             mbar_init(&sh.fixed[s], 1);
         }
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&sh.st_full[s], 1);
-            mbar_init(&sh.st_empty[s], 4);
+            mbar_init(&sh.st_empty[s], kConvWarps);
         }
         sh.abort = 0;
         sh.issued = 0;
@@ -705,7 +706,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             // ----------------------------------------- codes into bf16 tiles
             constexpr int kStages = C::kStages > 0 ? C::kStages : 1;
             constexpr int CPT = D / 16;              // 16-code vectors of a token
-            constexpr int TPI = 128 / CPT;           // tokens a round (16 or 32)
+            constexpr int TPI = kConvWarps * 32 / CPT;   // tokens a round (32 or 64)
             constexpr int NI = kN / TPI;             // rounds
             const int tid = threadIdx.x - kConvWarp * 32;
             const int c = tid % CPT, tr = tid / CPT; // this thread's vector of tokens tr + i TPI
@@ -869,33 +870,46 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 }
                 const int c0 = (s0 + j) * kN;
                 const bool masked = c0 + kN > sure;
-                // the S row: four TMEM loads in flight, one wait (each
-                // wait_ld ties its registers; the later ones return at once)
-                uint32_t v[kN / 32][32];
-#pragma unroll
-                for (int c = 0; c < kN / 32; ++c) ld32(tS + c * 32, v[c]);
-#pragma unroll
-                for (int c = 0; c < kN / 32; ++c) wait_ld(v[c]);
-                // hidden scores become -inf in place
-                if (masked) {
-#pragma unroll
-                    for (int c = 0; c < kN / 32; ++c) {
-                        const int ns = seen - c0 - c * 32;           // seen ones of these 32
-                        if (__all_sync(0xffffffffu, ns >= 32)) continue;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[c][e] = e < ns ? v[c][e] : 0xff800000u;
-                    }
-                }
-                // the row maximum (three-input max, four chains)
+                // The S row: four TMEM loads in flight, one wait (each wait_ld ties its
+                // registers; the later ones return at once).  Beside eight widening
+                // warps there are registers for half of it: the other half is read
+                // again once the maximum is known.
+                constexpr int kHeld = K8 ? 2 : 4;        // 32-key parts of the row held
+                uint32_t v[kHeld][32];
                 float tmv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // hidden scores become -inf in place
+                auto mask = [&](uint32_t (&w)[32], int c) {
+                    const int n = seen - c0 - c * 32;                // seen ones of these 32
+                    if (__all_sync(0xffffffffu, n >= 32)) return;
 #pragma unroll
-                for (int c = 0; c < kN / 32; ++c)
+                    for (int e = 0; e < 32; ++e) w[e] = e < n ? w[e] : 0xff800000u;
+                };
+                // the row maximum (three-input max, four chains)
+                auto top = [&](const uint32_t (&w)[32]) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            tmv[q] = max3(tmv[q], __uint_as_float(v[c][e + 2 * q]),
-                                          __uint_as_float(v[c][e + 2 * q + 1]));
+                            tmv[q] = max3(tmv[q], __uint_as_float(w[e + 2 * q]), __uint_as_float(w[e + 2 * q + 1]));
+                };
+#pragma unroll
+                for (int c = 0; c < kHeld; ++c) ld32(tS + c * 32, v[c]);
+#pragma unroll
+                for (int c = 0; c < kHeld; ++c) wait_ld(v[c]);
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < kHeld; ++c) mask(v[c], c);
+                }
+#pragma unroll
+                for (int c = 0; c < kHeld; ++c) top(v[c]);
+#pragma unroll
+                for (int c = kHeld; c < kN / 32; ++c) {
+                    uint32_t w[32];
+                    ld32(tS + c * 32, w);
+                    wait_ld(w);
+                    if (masked) mask(w, c);
+                    top(w);
+                }
                 const float traw = fmaxf(fmaxf(tmv[0], tmv[1]), fmaxf(tmv[2], tmv[3]));
                 const float tm = traw == -INFINITY ? -INFINITY : traw * sc;
                 const bool raise = tm > m_used + kRescale || (m_used == -INFINITY && tm != -INFINITY);
@@ -932,12 +946,16 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
 #pragma unroll
                 for (int c = 0; c < kN / 32; ++c) {
                     uint32_t pw[16];
+                    uint32_t (&w)[32] = v[c % kHeld];
+                    if (c >= kHeld) {
+                        ld32(tS + c * 32, w);
+                        wait_ld(w);
+                        if (masked) mask(w, c);
+                    }
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float t0, t1;
-                        unpair(fma2(pair(__uint_as_float(v[c][2 * e]),
-                                         __uint_as_float(v[c][2 * e + 1])),
-                                    sc2, nmu2),
+                        unpair(fma2(pair(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1])), sc2, nmu2),
                                t0, t1);
                         const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
                         rs2[e & 1] = add2(rs2[e & 1], pair(p0, p1));
@@ -971,7 +989,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             bool odd = false;
             if (ragged(t, t.s0 + n - 1)) {
                 const volatile int *bad = sh.bad[reader.i] + (t.sets == 2 ? x : 0);
-                for (int w = 0; w < (K8 ? 4 : 1); ++w) odd = odd || seen > bad[2 * w];
+                for (int w = 0; w < (K8 ? kConvWarps : 1); ++w) odd = odd || seen > bad[2 * w];
             }
             const bool whole = t.slot < 0;
             const float inv = odd ? __uint_as_float(0x7fffffffu) : whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -1003,31 +1021,35 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             auto pass = [&](auto as_bf16, int c0, bool last) {
                 constexpr bool kBf16 = decltype(as_bf16)::value;
                 constexpr int N = kBf16 ? D : D / 2;
-                uint32_t v[N / 32][32];
+                constexpr int kCols = K8 && N > 64 ? 64 : N;         // read at a time
 #pragma unroll
-                for (int c = 0; c < N / 32; ++c) ld32(tO + c0 + c * 32, v[c]);
+                for (int n0 = 0; n0 < N; n0 += kCols) {
+                    uint32_t v[kCols / 32][32];
 #pragma unroll
-                for (int c = 0; c < N / 32; ++c) wait_ld(v[c]);
-                if (last) let_go_of_o();
+                    for (int c = 0; c < kCols / 32; ++c) ld32(tO + c0 + n0 + c * 32, v[c]);
 #pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    uint4 w;
-                    if constexpr (kBf16) {
-                        const uint32_t (&y)[32] = v[k / 4];
-                        const int e = 8 * (k % 4);
-                        w = make_uint4(pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
-                                       pack_bf16(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv),
-                                       pack_bf16(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv),
-                                       pack_bf16(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv));
-                    } else {
-                        const uint32_t (&y)[32] = v[k / 8];
-                        const int e = 4 * (k % 8);
-                        w = make_uint4(__float_as_uint(__uint_as_float(y[e]) * inv),
-                                       __float_as_uint(__uint_as_float(y[e + 1]) * inv),
-                                       __float_as_uint(__uint_as_float(y[e + 2]) * inv),
-                                       __float_as_uint(__uint_as_float(y[e + 3]) * inv));
+                    for (int c = 0; c < kCols / 32; ++c) wait_ld(v[c]);
+                    if (last && n0 + kCols == N) let_go_of_o();
+                    constexpr int kPer = kBf16 ? 4 : 8;              // chunks of 32 columns
+#pragma unroll
+                    for (int k = 0; k < kCols / 32 * kPer; ++k) {
+                        uint4 w;
+                        const uint32_t (&y)[32] = v[k / kPer];
+                        if constexpr (kBf16) {
+                            const int e = 8 * (k % 4);
+                            w = make_uint4(pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
+                                           pack_bf16(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv),
+                                           pack_bf16(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv),
+                                           pack_bf16(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv));
+                        } else {
+                            const int e = 4 * (k % 8);
+                            w = make_uint4(__float_as_uint(__uint_as_float(y[e]) * inv),
+                                           __float_as_uint(__uint_as_float(y[e + 1]) * inv),
+                                           __float_as_uint(__uint_as_float(y[e + 2]) * inv),
+                                           __float_as_uint(__uint_as_float(y[e + 3]) * inv));
+                        }
+                        *reinterpret_cast<uint4 *>(stage + lane * RB + (((n0 / 32 * kPer + k) ^ (lane & 7)) << 4)) = w;
                     }
-                    *reinterpret_cast<uint4 *>(stage + lane * RB + ((k ^ (lane & 7)) << 4)) = w;
                 }
                 __syncwarp();
                 uint4 w[CH];
@@ -1092,7 +1114,7 @@ spec_status_t launch_tc(const ctc::Params &P, const CUtensorMap (&m)[3], int n_c
 ChunkPlan chunk_tc_plan(const ChunkParams &P, bool kv8) {
     (void)kv8;
     const int tb = ctc::kM / P.G;
-    return ChunkPlan{2 * tb * P.G, 2 * tb, ctc::kN, 2 * ctc::kN, 2 * ctc::kN, num_sms()};
+    return ChunkPlan{2 * tb * P.G, 2 * tb, ctc::kN, 4 * ctc::kN, 2 * ctc::kN, num_sms()};
 }
 
 spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStream_t s) {
