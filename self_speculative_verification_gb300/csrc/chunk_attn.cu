@@ -30,30 +30,55 @@ struct ChunkSimtShared {
     ChunkShare share;
 };
 
-// Four elements of token t of (request b, head h): from element c on, of its
-// key (x = 0) or value (x = 1) row; zeros and SPEC_DEV_BAD_PAGE for a page id
-// outside the cache.
+// Where token t of (request b, head h) has its key and value rows, and an 8-bit
+// block's scales; null for a page id outside the cache (SPEC_DEV_BAD_PAGE),
+// whose tokens count as zeros.
+struct ChunkRow {
+    const uint8_t *k, *v;
+    float ks, vs;
+};
+
 template <int D, int kCache>
-__device__ __forceinline__ float4 chunk_load4(const ChunkParams &P, int b, int h, int t, int x, int c) {
+__device__ __forceinline__ ChunkRow chunk_row(const ChunkParams &P, int b, int h, int t) {
+    ChunkRow r{nullptr, nullptr, 1.f, 1.f};
+    const uint8_t *kc = static_cast<const uint8_t *>(P.kc), *vc = static_cast<const uint8_t *>(P.vc);
     if (kCache == kCacheRows && !P.paged) {
-        const float *p = static_cast<const float *>(x ? P.vc : P.kc) + (((size_t)b * P.Hkv + h) * P.capacity + t) * D + c;
-        return *reinterpret_cast<const float4 *>(p);
+        const size_t at = (((size_t)b * P.Hkv + h) * P.capacity + t) * D * 4;
+        r.k = kc + at;
+        r.v = vc + at;
+        return r;
     }
     const int page = __ldg(P.page_table + (size_t)b * P.max_pages + t / P.ps), off = t % P.ps;
     if (page < 0 || page >= P.n_pages) {
         raise_status(P.status, SPEC_DEV_BAD_PAGE);
-        return make_float4(0.f, 0.f, 0.f, 0.f);
+        return r;
     }
     if (kCache == kCache8) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(
-            static_cast<const uint8_t *>(P.kc) + kv8_block(page, h, P.Hkv, P.ps, D) + kv8_row(off, x, D) + c);
-        const float s = kv8_read_scale(P.scales[((size_t)page * P.Hkv + h) * 2 + x]);
-        const float2 lo = from_e4m3x2(w & 0xffffu), hi = from_e4m3x2(w >> 16);
-        return make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s);
+        const size_t at = kv8_block(page, h, P.Hkv, P.ps, D);
+        r.k = kc + at + kv8_row(off, 0, D);
+        r.v = kc + at + kv8_row(off, 1, D);
+        const float *s = P.scales + ((size_t)page * P.Hkv + h) * 2;
+        r.ks = kv8_read_scale(__ldg(s));
+        r.vs = kv8_read_scale(__ldg(s + 1));
+    } else {
+        const size_t at = (((size_t)page * P.Hkv + h) * (D / 64) * P.ps + off) * 256;
+        r.k = kc + at;
+        r.v = vc + at;
     }
-    const float *p = static_cast<const float *>(x ? P.vc : P.kc) +
-                 ((((size_t)page * P.Hkv + h) * (D / 64) + c / 64) * P.ps + off) * 64 + c % 64;
-    return *reinterpret_cast<const float4 *>(p);
+    return r;
+}
+
+// Elements c .. c + 3 of such a row.
+template <int D, int kCache>
+__device__ __forceinline__ float4 chunk_elems(const ChunkParams &P, const uint8_t *row, float scale, int c) {
+    if (kCache == kCache8) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(row + c));
+        const float2 lo = from_e4m3x2(w & 0xffffu), hi = from_e4m3x2(w >> 16);
+        return make_float4(lo.x * scale, lo.y * scale, hi.x * scale, hi.y * scale);
+    }
+    // (paged: the 64-element blocks of a head are a page's rows apart)
+    const size_t at = P.paged ? (size_t)(c / 64) * P.ps * 256 + (c % 64) * 4 : (size_t)c * 4;
+    return __ldg(reinterpret_cast<const float4 *>(row + at));
 }
 
 // The CUDA-core kernel, everything in fp32.  128 threads: thread (ty, tx) has
@@ -102,17 +127,35 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm) chunk_simt_kernel(Ch
             const int t0 = s * kKeys, nk = min(kKeys, last - t0);
             __syncthreads();
             bool odd = false;                            // a non-finite value among them
-            for (int i = tid; i < kKeys * (D / 4); i += kSimtThreads) {
-                const int t = i / (D / 4), c = (i % (D / 4)) * 4;
-                float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-                if (t < nk) {
-                    k = chunk_load4<D, kCache>(P, u.b, u.h, t0 + t, 0, c);
-                    v = chunk_load4<D, kCache>(P, u.b, u.h, t0 + t, 1, c);
-                    odd = odd || !(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY &&
-                                   fabsf(v.w) < INFINITY);
+            // a thread's vectors are of one column, every kStep-th token: their rows
+            // are found first, then all loads are in flight at once
+            constexpr int kStep = kSimtThreads / (D / 4), kBatch = 4;
+            const int c = (tid % (D / 4)) * 4, tr = tid / (D / 4);
+            for (int i0 = 0; i0 < kKeys; i0 += kStep * kBatch) {
+                ChunkRow row[kBatch];
+                float4 k[kBatch], v[kBatch];
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e) {
+                    const int t = i0 + e * kStep + tr;
+                    row[e] = ChunkRow{nullptr, nullptr, 1.f, 1.f};
+                    if (t < nk) row[e] = chunk_row<D, kCache>(P, u.b, u.h, t0 + t);
                 }
-                *reinterpret_cast<float4 *>(&sh.k[t][c]) = k;
-                *reinterpret_cast<float4 *>(&sh.v[t][c]) = v;
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e) {
+                    k[e] = v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (row[e].k) {
+                        k[e] = chunk_elems<D, kCache>(P, row[e].k, row[e].ks, c);
+                        v[e] = chunk_elems<D, kCache>(P, row[e].v, row[e].vs, c);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e) {
+                    const int t = i0 + e * kStep + tr;
+                    odd = odd || !(fabsf(v[e].x) < INFINITY && fabsf(v[e].y) < INFINITY && fabsf(v[e].z) < INFINITY &&
+                                   fabsf(v[e].w) < INFINITY);
+                    *reinterpret_cast<float4 *>(&sh.k[t][c]) = k[e];
+                    *reinterpret_cast<float4 *>(&sh.v[t][c]) = v[e];
+                }
             }
             odd = __syncthreads_or(odd);
             float x[4][4] = {};

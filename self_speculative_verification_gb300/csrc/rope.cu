@@ -14,8 +14,7 @@
 namespace sv {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 16;      // most tokens of a CTA
+constexpr int kRopeTokens = 4;       // most tokens of a CTA
 constexpr int kMaxPairs = 128;       // rot_dim <= 256
 
 struct RopeParams {
@@ -34,23 +33,25 @@ struct RopeParams {
 
 enum { kPairs = 0, kHalves = 1, kHalvesScalar = 2 };
 
+// Threads of a CTA: at least a head's parts (by vectors 64 at most, by elements
+// 255).  Small CTAs of few tokens: 128 threads and 4 tokens take 118 us for 36 K
+// tokens of 40 heads of 128 (680 MB, 5.8 TB/s), 256 and 16 take 127.
+__host__ __device__ constexpr int rope_threads(int layout) { return layout == kHalvesScalar ? 256 : 128; }
+
 template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
 
-// The position of packed token i; false for a row that is left as it is.
-__device__ __forceinline__ bool rope_position(const RopeParams &P, int i, long long *pos) {
+// The position of packed token i, which no request before b0 holds; false for a
+// row that is left as it is.
+__device__ __forceinline__ bool rope_position(const RopeParams &P, int i, int b0, long long *pos) {
     if (P.positions) {
         *pos = P.positions[i];
         return *pos >= 0;
     }
-    int lo = 0, hi = P.B;                    // the last b with cu_new[b] <= i
-    while (lo < hi) {
-        const int mid = lo + (hi - lo + 1) / 2;
-        if (__ldg(P.cu_new + mid) <= i) lo = mid;
-        else hi = mid - 1;
-    }
-    const int first = __ldg(P.cu_new + lo);
-    if (lo == P.B || i < first || i >= __ldg(P.cu_new + lo + 1)) return false;
-    const int S = __ldg(P.seq_len + lo);
+    int b = b0;
+    while (b < P.B && __ldg(P.cu_new + b + 1) <= i) ++b;
+    if (b >= P.B) return false;
+    const int first = __ldg(P.cu_new + b), S = __ldg(P.seq_len + b);
+    if (i < first) return false;
     if (S < 0) {
         raise_status(P.status, SPEC_DEV_SEQ_OVERFLOW);
         return false;
@@ -65,8 +66,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 template <typename T>
-__device__ __forceinline__ void load_vec(const T *p, float (&x)[kVec<T>]) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+__device__ __forceinline__ void unpack_vec(const uint4 &v, float (&x)[kVec<T>]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -98,9 +98,10 @@ __device__ __forceinline__ void rotate(float &x, float &y, float2 cs) {
 
 // Part `it` of one head: src -> dst.
 //   kPairs         vector it of the head, pairs (2i, 2i + 1)
-//   kHalves        vectors it and it + rot / 2 of the rotated part, pairs
-//                  (i, i + rot / 2); behind them the rest, a vector a part
-//   kHalvesScalar  the same by elements (rot / 2 not a multiple of a vector)
+//   kHalvesScalar  elements it and it + rot / 2 of the rotated part; behind them
+//                  the rest, an element a part
+// (kHalves, where rot / 2 is a multiple of a vector: the same by vectors, in the
+// kernel.)
 template <typename T, int kLayout>
 __device__ __forceinline__ void rope_item(const RopeParams &P, const T *src, T *dst, int it,
                                           const float2 *cs, bool keep) {
@@ -126,20 +127,6 @@ __device__ __forceinline__ void rope_item(const RopeParams &P, const T *src, T *
             }
         }
         *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if constexpr (kLayout == kHalves) {
-        if (it < half / V) {
-            const int c = it * V;
-            float x[V], y[V];
-            load_vec(src + c, x);
-            load_vec(src + c + half, y);
-#pragma unroll
-            for (int e = 0; e < V; ++e) rotate(x[e], y[e], cs[c + e]);
-            store_vec(dst + c, x);
-            store_vec(dst + c + half, y);
-        } else if (!keep) {
-            const int c = P.rot + (it - half / V) * V;
-            *reinterpret_cast<uint4 *>(dst + c) = *reinterpret_cast<const uint4 *>(src + c);
-        }
     } else {
         if (it < half) {
             float x = load_f(src + it), y = load_f(src + it + half);
@@ -153,26 +140,32 @@ __device__ __forceinline__ void rope_item(const RopeParams &P, const T *src, T *
 }
 
 template <typename T, int kLayout>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(rope_threads(kLayout)) rope_kernel(const __grid_constant__ RopeParams P) {
+    constexpr int kThreads = rope_threads(kLayout);
     pdl_wait();
     __shared__ long long s_pos[kRopeTokens];
     __shared__ bool s_in[kRopeTokens];
     __shared__ float2 s_cs[kRopeTokens][kMaxPairs];
     const int tid = threadIdx.x, base = blockIdx.x * P.tpc, nt = min(P.tpc, P.n - base);
+    // the requests that end before this CTA's tokens, counted by all threads at once
+    int b0 = 0;
+    if (!P.positions)
+        for (int b = 0; b < P.B; b += kThreads)
+            b0 += __syncthreads_count(b + tid < P.B && __ldg(P.cu_new + b + tid + 1) <= base);
     if (tid < nt) {
         long long pos = 0;
-        s_in[tid] = rope_position(P, base + tid, &pos);
+        s_in[tid] = rope_position(P, base + tid, b0, &pos);
         s_pos[tid] = pos;
     }
     if (blockIdx.x == 0 && !P.positions) {
         bool bad = tid == 0 && P.cu_new[0] < 0;
-        for (int b = tid; b < P.B; b += kRopeThreads)
+        for (int b = tid; b < P.B; b += kThreads)
             bad = bad || P.cu_new[b + 1] < P.cu_new[b] || P.cu_new[b + 1] > P.n;
         if (bad) raise_status(P.status, SPEC_DEV_BAD_INDEX);
     }
     __syncthreads();
     const int half = P.rot / 2;
-    for (int f = tid; f < nt * half; f += kRopeThreads) {
+    for (int f = tid; f < nt * half; f += kThreads) {
         const int t = f / half, i = f - t * half;
         const float x = __ll2float_rn((long long)((uint64_t)s_pos[t] * P.turn[i])) * 0x1p-63f;
         float s, c;
@@ -180,18 +173,55 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         s_cs[t][i] = make_float2(c * P.attention, s * P.attention);
     }
     __syncthreads();
-    const int slots = kRopeThreads / P.items;            // rows at a time
+    const int slots = kThreads / P.items;            // rows at a time
     const int slot = tid / P.items, it = tid - slot * P.items;
     if (slot >= slots) return;
-    for (int row = slot; row < nt * P.H; row += slots) {
+    auto find = [&](int row, const T *&src, T *&dst, const float2 *&cs, bool &keep) -> bool {
+        if (row >= nt * P.H) return false;
         const int t = row / P.H, h = row - t * P.H;
-        if (!s_in[t]) continue;
+        if (!s_in[t]) return false;
         const long long i = base + t;
         const bool key = h >= P.Hq;
         const int hh = key ? h - P.Hq : h;
-        const T *src = static_cast<const T *>(key ? P.k : P.q) + i * (key ? P.sk : P.sq) + (long long)hh * P.d;
-        T *dst = static_cast<T *>(key ? P.k_out : P.q_out) + i * (key ? P.sko : P.sqo) + (long long)hh * P.d;
-        rope_item<T, kLayout>(P, src, dst, it, s_cs[t], key ? P.keep_k : P.keep_q);
+        src = static_cast<const T *>(key ? P.k : P.q) + i * (key ? P.sk : P.sq) + (long long)hh * P.d;
+        dst = static_cast<T *>(key ? P.k_out : P.q_out) + i * (key ? P.sko : P.sqo) + (long long)hh * P.d;
+        cs = s_cs[t];
+        keep = key ? P.keep_k : P.keep_q;
+        return true;
+    };
+    if constexpr (kLayout == kHalves) {
+        constexpr int V = kVec<T>;
+        const int half = P.rot / 2, c = it * V;
+        const bool turns = c < half;
+        const int second = turns ? c + half : half + c;  // (behind: the vector that is copied)
+        for (int row = slot; row < nt * P.H; row += slots) {
+            const T *src;
+            T *dst;
+            const float2 *cs;
+            bool keep;
+            if (!find(row, src, dst, cs, keep) || (!turns && keep)) continue;
+            const uint4 b = *reinterpret_cast<const uint4 *>(src + second);
+            if (!turns) {
+                *reinterpret_cast<uint4 *>(dst + second) = b;
+                continue;
+            }
+            float x[V], y[V];
+            unpack_vec<T>(*reinterpret_cast<const uint4 *>(src + c), x);
+            unpack_vec<T>(b, y);
+#pragma unroll
+            for (int e = 0; e < V; ++e) rotate(x[e], y[e], cs[c + e]);
+            store_vec(dst + c, x);
+            store_vec(dst + second, y);
+        }
+    } else {
+#pragma unroll 2
+        for (int row = slot; row < nt * P.H; row += slots) {
+            const T *src;
+            T *dst;
+            const float2 *cs;
+            bool keep;
+            if (find(row, src, dst, cs, keep)) rope_item<T, kLayout>(P, src, dst, it, cs, keep);
+        }
     }
 }
 
@@ -306,12 +336,13 @@ extern "C" spec_status_t spec_rope(const spec_rope_desc *desc, const double *fre
     }
     P.status = status_ptr();
     if (!P.status) return SPEC_ERR_CUDA;
-    // tokens of a CTA: up to 16, fewer while the GPU has room for more CTAs
+    // tokens of a CTA: up to 4, fewer while the GPU has room for more CTAs
     P.tpc = kRopeTokens;
     while (P.tpc > 1 && ceil_div(n, P.tpc) < 4 * num_sms()) P.tpc /= 2;
-    const dim3 grid((unsigned)ceil_div(n, P.tpc)), block(kRopeThreads);
+    const dim3 grid((unsigned)ceil_div(n, P.tpc));
     const int layout = desc->layout == SPEC_ROPE_PAIRS ? kPairs : rot / 2 % per == 0 ? kHalves : kHalvesScalar;
     P.items = layout == kPairs ? d / per : layout == kHalves ? rot / 2 / per + (d - rot) / per : d - rot / 2;
+    const dim3 block(rope_threads(layout));
     cudaStream_t s = as_stream(stream);
     spec_status_t st;
 #define SV_ROPE(T)                                                                        \
