@@ -728,21 +728,26 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 int *bad = &sh.bad[reader.i][2 * (warp - kConvWarp)];
                 bool fresh = true;
                 const int32_t *table = A.page_table + (size_t)t.b * A.max_pages;
-                // scales of the step's eight groups of 16 tokens: lane 2 i + x has
-                // group i's of K (x = 0) or V; loaded a step ahead
-                auto load_scale = [&](int i) -> float {
-                    const int s = t.s0 + i / t.sets, tok = s * kN + (lane >> 1) * 16;
-                    if (lane >= 16 || i >= t.n * t.sets || tok >= t.lim) return 1.f;
-                    const int id = __ldg(table + page_of(P, tok));
-                    if (id < 0 || id >= A.n_pages) return 1.f;
-                    return __ldg(A.scales + ((size_t)id * A.Hkv + t.h[i % t.sets]) * 2 + (lane & 1));
+                const int two = t.sets - 1, n_pairs = t.n << two;    // K/V pairs
+                // scales of a pair's eight groups of 16 tokens: lane 2 g + x has group
+                // g's of K (x = 0) or V.  Loaded a pair ahead, their pages' ids two: a
+                // warp waits where it first needs a value
+                auto load_id = [&](int i) -> int {
+                    const int tok = (t.s0 + (i >> two)) * kN + (lane >> 1) * 16;
+                    return lane < 16 && i < n_pairs && tok < t.lim ? __ldg(table + page_of(P, tok)) : -1;
                 };
-                float next_scale = load_scale(0);
-                for (int i = 0; i < t.n * t.sets && ok; ++i) {
-                    const int s = t.s0 + i / t.sets;
-                    int *mine = bad + i % t.sets;
+                auto load_scale = [&](int i, int id) -> float {
+                    if (id < 0 || id >= A.n_pages) return 1.f;
+                    return __ldg(A.scales + ((size_t)id * A.Hkv + t.h[i & two]) * 2 + (lane & 1));
+                };
+                float next_scale = load_scale(0, load_id(0));
+                int next_id = load_id(1);
+                for (int i = 0; i < n_pairs && ok; ++i) {
+                    const int s = t.s0 + (i >> two);
+                    int *mine = bad + (i & two);
                     const float my_scale = kv8_read_scale(next_scale);
-                    next_scale = load_scale(i + 1);
+                    next_scale = load_scale(i + 1, next_id);
+                    next_id = load_id(i + 2);
                     // 2^e, e <= 7: its codes' factor 2^(120 + e) is a bf16
                     const uint32_t sb = __float_as_uint(my_scale);
                     const bool plain = (sb & 0x007fffffu) == 0u && sb <= 0x43000000u;
@@ -769,6 +774,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                             nan |= nan4(v[k].x) | nan4(v[k].y) | nan4(v[k].z) | nan4(v[k].w);
                         }
                         const bool fast = __all_sync(0xffffffffu, !(nan & 0x80808080u)) && all_plain;
+                        if (x == 1 && lane == 0) mbar_arrive(&sh.st_empty[stage]);
                         if (!mbar_wait_warp(&sh.empty[slot], ph, wait)) {
                             ok = false;
                             break;
@@ -810,7 +816,6 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         }
                     }
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive(&sh.st_empty[stage]);
                     if (++stage == kStages) {
                         stage = 0;
                         sph ^= 1u;
