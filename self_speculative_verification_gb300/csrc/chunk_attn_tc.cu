@@ -108,7 +108,7 @@ struct Shared {
     uint64_t q_full[2], q_empty[2];
     uint64_t full[kMaxSlots], empty[kMaxSlots], fixed[kMaxSlots];
     uint64_t st_full[kMaxStages], st_empty[kMaxStages];
-    uint64_t s_full[2], p_full[2][2], o_done[2], o_free[2];      // p_full: by halves of the keys
+    uint64_t s_full[2], p_full[2][2], o_done[2], o_free[2], o_ready[2];      // p_full: by halves of the keys
     uint64_t drain[2];
     uint32_t tmem_base;
     uint32_t issued;         // fills of the ring begun
@@ -205,6 +205,19 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
+// shared -> global tensor copy, and the wait until this thread's have read their
+// source
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit_and_wait_read() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 // Four e4m3 codes as bf16 times 2^-120: sign, and exponent and mantissa in the
 // low bits of bf16's (subnormal codes become subnormal).  NaN codes are not
 // told apart.
@@ -248,7 +261,8 @@ __device__ __forceinline__ uint32_t nan4(uint32_t w) { return (w & 0x7f7f7f7fu) 
 template <int D, bool K8>
 __global__ void __launch_bounds__(ctc::Cfg<D, K8>::kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ CUtensorMap mq,
-                const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+                const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv) {
     using namespace ctc;
     using namespace tc5;
     using C = Cfg<D, K8>;
@@ -264,8 +278,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == kProducerWarp * 32) {
-        const CUtensorMap *maps[3] = {&mq, &mk, &mv};
-        for (int i = 0; i < (K8 ? 1 : 3); ++i)
+        const CUtensorMap *maps[4] = {&mq, &mo, &mk, &mv};
+        for (int i = 0; i < (K8 ? 2 : 4); ++i)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i]))
                          : "memory");
     }
@@ -278,6 +292,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             mbar_init(&sh.p_full[x][1], kGroupWarps);
             mbar_init(&sh.o_done[x], 1);
             mbar_init(&sh.o_free[x], kGroupWarps);
+            mbar_init(&sh.o_ready[x], kGroupWarps);
             mbar_init(&sh.drain[x], 1);
         }
         for (int i = 0; i < kParts; ++i) {
@@ -839,6 +854,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
         const float sc = A.scale_log2;
         const int rt = r / A.G;                          // the row's token
         int ns = 0, nact = 0;      // S hand-offs taken; parts this tile took part in
+        uint32_t n_full = 0;       // and those whose results were copied as a tile
         bool ok = true;
         PartReader reader;
         while (ok && reader.next<true>(sh, wait, &ok)) {
@@ -1023,8 +1039,9 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 }
             };
             // N columns of O from column c0 on, as 16-byte chunks of bf16 or fp32
-            auto pass = [&](auto as_bf16, int c0, bool last) {
-                constexpr bool kBf16 = decltype(as_bf16)::value;
+            // (kFull: a whole query tile, laid out as its queries were)
+            auto pass = [&](auto as_bf16, auto as_tile, int c0, bool last) {
+                constexpr bool kBf16 = decltype(as_bf16)::value, kFull = decltype(as_tile)::value;
                 constexpr int N = kBf16 ? D : D / 2;
                 constexpr int kCols = K8 && N > 64 ? 64 : N;         // read at a time
 #pragma unroll
@@ -1053,9 +1070,15 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                                            __float_as_uint(__uint_as_float(y[e + 2]) * inv),
                                            __float_as_uint(__uint_as_float(y[e + 3]) * inv));
                         }
-                        *reinterpret_cast<uint4 *>(stage + lane * RB + (((n0 / 32 * kPer + k) ^ (lane & 7)) << 4)) = w;
+                        const int at = n0 / 32 * kPer + k;
+                        if constexpr (kFull)
+                            *reinterpret_cast<uint4 *>(qbuf + x * kTile + (at / 8) * kHalf + r * 128 +
+                                                       (((at % 8) ^ (r & 7)) << 4)) = w;
+                        else
+                            *reinterpret_cast<uint4 *>(stage + lane * RB + ((at ^ (lane & 7)) << 4)) = w;
                     }
                 }
+                if constexpr (kFull) return;
                 __syncwarp();
                 uint4 w[CH];
 #pragma unroll
@@ -1075,14 +1098,38 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     *reinterpret_cast<uint4 *>(dst + at * (kBf16 ? 2 * D : 4 * D) + (lane % CH) * 16) = w[k];
                 }
             };
-            if (!warp_ok) {
+            if (whole && t.nt[x] == P.tb) {
+                // all of the tile's tokens: one warp has them copied once the four have
+                // written them (a warp's own stores wait behind the MMAs' reads of
+                // shared memory: 5 K cycles a tile)
+                if (warp_ok) pass(Bool<true>{}, Bool<true>{}, 0, true);
+                else let_go_of_o();
+                fence_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.o_ready[x]);
+                    if (warp % kGroupWarps == 0) {
+                        if (mbar_wait(&sh.o_ready[x], n_full & 1u, wait)) {
+                            for (int hh = 0; hh < NH; ++hh)
+                                tma_store_3d(&mo, qbuf + x * kTile + hh * kHalf, hh * 64, t.h[x] * A.G, t.row[x]);
+                            bulk_commit_and_wait_read();
+                        } else {
+                            ok = false;
+                        }
+                    }
+                    mbar_arrive(&sh.q_empty[x]);
+                    reader.release(sh);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                ++n_full;
+            } else if (!warp_ok) {
                 let_go_of_o();
                 let_go_of_q();
             } else if (whole) {
-                pass(Bool<true>{}, 0, true);
+                pass(Bool<true>{}, Bool<false>{}, 0, true);
             } else {
-                pass(Bool<false>{}, 0, false);
-                pass(Bool<false>{}, D / 2, true);
+                pass(Bool<false>{}, Bool<false>{}, 0, false);
+                pass(Bool<false>{}, Bool<false>{}, D / 2, true);
             }
             if (row_ok) {
                 const size_t at = first + r + (size_t)rt * skip;
@@ -1106,12 +1153,13 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
 }
 
 template <int D, bool K8>
-spec_status_t launch_tc(const ctc::Params &P, const CUtensorMap (&m)[3], int n_cta, cudaStream_t s) {
+spec_status_t launch_tc(const ctc::Params &P, const CUtensorMap (&m)[4], int n_cta, cudaStream_t s) {
     constexpr size_t smem = ctc::smem_bytes<D, K8>();
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     if (set_smem_limit(reinterpret_cast<const void *>(chunk_tc_kernel<D, K8>), smem) != SPEC_OK)
         return SPEC_ERR_CUDA;
-    return launch(chunk_tc_kernel<D, K8>, dim3(n_cta), dim3(ctc::Cfg<D, K8>::kThreads), smem, s, P, m[0], m[1], m[2]);
+    return launch(chunk_tc_kernel<D, K8>, dim3(n_cta), dim3(ctc::Cfg<D, K8>::kThreads), smem, s, P, m[0], m[1], m[2],
+                  m[3]);
 }
 
 }  // namespace
@@ -1143,11 +1191,13 @@ spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStr
         P.ps_shift = 31 + L;
         P.ps_mul = (uint32_t)(((1ull << (31 + L)) + C.ps - 1) / C.ps);
     }
-    CUtensorMap m[3] = {};
+    CUtensorMap m[4] = {};
     const cuuint64_t d0[3] = {(cuuint64_t)C.d, (cuuint64_t)C.Hq, (cuuint64_t)C.n_tokens};
     const cuuint64_t s0[2] = {(cuuint64_t)C.d * 2, (cuuint64_t)C.stride_q * 2};
     const cuuint32_t b0[3] = {64u, (cuuint32_t)C.G, (cuuint32_t)P.tb};
-    if (!encode_bf16_map(&m[0], C.q, 3, d0, s0, b0)) return SPEC_ERR_CUDA;
+    const cuuint64_t so[2] = {(cuuint64_t)C.d * 2, (cuuint64_t)C.Hq * C.d * 2};
+    if (!encode_bf16_map(&m[0], C.q, 3, d0, s0, b0) || !encode_bf16_map(&m[1], C.o, 3, d0, so, b0))
+        return SPEC_ERR_CUDA;
     if (!kv8) {
         const cuuint64_t nh = C.d / 64;
         cuuint64_t d1[3] = {(cuuint64_t)C.d, (cuuint64_t)C.capacity, (cuuint64_t)C.cache_heads};
@@ -1160,7 +1210,7 @@ spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStr
             s1[1] = (cuuint64_t)C.ps * 128;
         }
         const cuuint32_t b1[3] = {64u, (cuuint32_t)P.box, 1u};
-        if (!encode_bf16_map(&m[1], C.kc, 3, d1, s1, b1) || !encode_bf16_map(&m[2], C.vc, 3, d1, s1, b1))
+        if (!encode_bf16_map(&m[2], C.kc, 3, d1, s1, b1) || !encode_bf16_map(&m[3], C.vc, 3, d1, s1, b1))
             return SPEC_ERR_CUDA;
     }
     if (C.d == 128) return kv8 ? launch_tc<128, true>(P, m, n_cta, s) : launch_tc<128, false>(P, m, n_cta, s);
