@@ -593,8 +593,15 @@ def _packed_rows(t, cache, n, name, dev):
     return _rows(t, n, cache.n_kv_heads, cache.head_dim, name, dev)
 
 
-def _rows(t, n, H, d, name, dev):
+def _rows(t, n, H, d, name, dev, dtype=None):
     """Pointer and row stride of [n][H][d] rows that may lie in wider rows."""
+    try:
+        if t.get_device() == dev and t.shape == (n, H, d) and (dtype is None or t.dtype is dtype):
+            s = t.stride()
+            if s[2] == 1 and (H == 1 or s[1] == d):
+                return t.data_ptr(), s[0] if n > 1 else H * d
+    except AttributeError:          # not a tensor
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
@@ -603,6 +610,8 @@ def _rows(t, n, H, d, name, dev):
         raise ValueError(f"{name} must be {[n, H, d]}, got {list(t.shape)}")
     if n and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
         raise ValueError(f"{name}: a token's heads must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr(), t.stride(0) if n > 1 else H * d
 
 
@@ -710,14 +719,11 @@ def spec_rope(desc: RopeDesc, freqs, q, q_out, k=None, k_out=None, positions=Non
     if not isinstance(freqs, ctypes.Array) or freqs._type_ is not c_double:
         freqs = (c_double * half)(*(float(f) for f in freqs))
     dt = torch.bfloat16 if desc.dtype == SPEC_BF16 else torch.float32
-    ptrs = []
-    for name, t, H in (("q", q, Hq), ("q_out", q_out, Hq), ("k", k, Hk), ("k_out", k_out, Hk)):
-        if H == 0:
-            ptrs += [None, 0]
-            continue
-        ptrs += _rows(t, n, H, d, name, dev)
-        if t.dtype != dt:
-            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    none = (None, 0)
+    pq, sq = _rows(q, n, Hq, d, "q", dev, dt) if Hq else none
+    pqo, sqo = _rows(q_out, n, Hq, d, "q_out", dev, dt) if Hq else none
+    pk, sk = _rows(k, n, Hk, d, "k", dev, dt) if Hk else none
+    pko, sko = _rows(k_out, n, Hk, d, "k_out", dev, dt) if Hk else none
     i32, B = torch.int32, 0
     if positions is not None:
         pos, sl, cu = _on(positions, i32, (n,), "positions", dev), None, None
@@ -725,7 +731,8 @@ def spec_rope(desc: RopeDesc, freqs, q, q_out, k=None, k_out=None, positions=Non
         sl = _on(seq_len, i32, None, "seq_len", dev)
         B, pos = seq_len.numel(), None
         cu = _on(cu_new, i32, (B + 1,), "cu_new", dev)
-    _check("spec_rope", load_library().spec_rope(ctypes.byref(desc), freqs, *ptrs, pos, B, sl, cu, st))
+    _check("spec_rope", load_library().spec_rope(ctypes.byref(desc), freqs, pq, sq, pqo, sqo, pk, sk, pko, sko,
+                                                 pos, B, sl, cu, st))
 
 
 def kv_append(cache: KvDesc, k, v, slot_map, stream=None):
@@ -757,9 +764,7 @@ def _chunk(fn, desc, q, cache, seq_len, cu_new, o, lse, workspace, stream):
     _cache_on(cache, dev)
     B, n, Hq, d = desc.batch, desc.n_tokens, desc.n_q_heads, desc.head_dim
     dt = torch.bfloat16 if desc.dtype == SPEC_BF16 else torch.float32
-    pq, sq = _rows(q, n, Hq, d, "q", dev)
-    if q.dtype != dt:
-        raise TypeError(f"q must be {dt}, got {q.dtype}")
+    pq, sq = _rows(q, n, Hq, d, "q", dev, dt)
     _check(fn, getattr(load_library(), fn)(
         ctypes.byref(desc), pq, sq, ctypes.byref(cache), _on(seq_len, torch.int32, (B,), "seq_len", dev),
         _on(cu_new, torch.int32, (B + 1,), "cu_new", dev), _on(o, dt, (n, Hq, d), "o", dev),

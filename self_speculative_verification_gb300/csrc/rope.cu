@@ -332,7 +332,7 @@ extern "C" spec_status_t spec_rope(const spec_rope_desc *desc, const double *fre
     for (int i = 0; i < rot / 2; ++i) {
         const double t = freqs[i] / (2.0 * M_PI);
         const double f = t - floor(t);       // (a tiny negative one gives 1)
-        P.turn[i] = f < 1.0 ? (uint64_t)ldexp(f, 64) : 0u;
+        P.turn[i] = f < 1.0 ? (uint64_t)(f * 0x1p64) : 0u;
     }
     P.status = status_ptr();
     if (!P.status) return SPEC_ERR_CUDA;
