@@ -248,8 +248,10 @@ def kv_desc_contiguous(k: torch.Tensor, v: torch.Tensor) -> KvDesc:
         raise ValueError("k and v must be [B][Hkv][max_seq][d]")
     _ptr(k, name="k"), _ptr(v, k.dtype, "v")
     B, Hkv, S, d = k.shape
-    return KvDesc(SPEC_KV_CONTIGUOUS, spec_dtype(k), Hkv, d, k.data_ptr(), v.data_ptr(),
+    desc = KvDesc(SPEC_KV_CONTIGUOUS, spec_dtype(k), Hkv, d, k.data_ptr(), v.data_ptr(),
                   B, S, 0, 0, 0, None)
+    desc.device = k.get_device()
+    return desc
 
 
 def kv_desc_paged(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor) -> KvDesc:
@@ -261,8 +263,10 @@ def kv_desc_paged(k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor) ->
     P, Hkv, nblk, ps, _ = k.shape
     d = nblk * 64
     B, maxp = page_table.shape
-    return KvDesc(SPEC_KV_PAGED, spec_dtype(k), Hkv, d, k.data_ptr(), v.data_ptr(),
+    desc = KvDesc(SPEC_KV_PAGED, spec_dtype(k), Hkv, d, k.data_ptr(), v.data_ptr(),
                   B, 0, P, ps, maxp, page_table.data_ptr())
+    desc.device = k.get_device()
+    return desc
 
 
 def attn_desc(batch, n_rows, n_q_heads, n_kv_heads, head_dim, dtype, n_soft=0,
@@ -739,6 +743,7 @@ def kv_append(cache: KvDesc, k, v, slot_map, stream=None):
     """Packed new tokens k, v [n][Hkv][d] (rows may be part of wider ones) into
     the slots of slot_map int64 [n] (negative: not written) of a cache of rows."""
     st, dev = _cur(stream)
+    _cache_on(cache, dev)
     n = slot_map.numel()
     pk, sk = _packed_rows(k, cache, n, "k", dev)
     pv, sv = _packed_rows(v, cache, n, "v", dev)

@@ -344,3 +344,19 @@ def test_refusals_of_rope_and_append():
         with pytest.raises(err):
             bn.kv_append(c, *args)
     assert bn.spec_get_status() == 0
+
+
+def test_a_cache_of_another_device_is_refused():
+    x = torch.zeros(2, 2, 16, 64, device="cuda")
+    p = torch.zeros(2, 2, 1, 16, 64, device="cuda")
+    rows, slots = torch.zeros(6, 2, 64, device="cuda"), torch.zeros(6, dtype=torch.int64, device="cuda")
+    o, lse, ws = torch.zeros_like(rows), torch.zeros(6, 2, device="cuda"), torch.zeros(1 << 20, device="cuda")
+    d = bn.chunk_desc(1, 6, 2, 2, 64, bn.SPEC_F32)
+    for cache in (bn.kv_desc_contiguous(x, x.clone()), bn.kv_desc_paged(p, p.clone(), i32(1, 2))):
+        assert cache.device == torch.cuda.current_device()
+        cache.device += 1
+        with pytest.raises(ValueError):
+            bn.kv_append(cache, rows, rows, slots)
+        with pytest.raises(ValueError):
+            bn.spec_chunk_attn(d, rows, cache, i32(1), i32(2), o, lse, ws)
+    assert bn.spec_get_status() == 0
