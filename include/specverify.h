@@ -985,10 +985,9 @@ spec_status_t spec_chunk_attn_kv8(const spec_chunk_desc *desc, const void *q,
 
 /*
  * spec_set_wait_limit -- limit, in SM clock cycles, of the internal pipeline
- * waits of the kernels launched from now on (verify attention over either
- * cache, prefill attention, and the bulk row stream of the vocabulary
- * reduction),
- * process-wide.  The pages have no counterpart: this is the
+ * waits of the kernels launched from now on (verify and chunk attention over
+ * either cache, prefill attention, and the bulk row stream of the vocabulary
+ * reduction), process-wide.  The pages have no counterpart: this is the
  * library's guard against a hang.  A wait that runs out sets
  * SPEC_DEV_TIMEOUT; the kernel then stops issuing work, waits (with the
  * default limit) for its own copies and tensor-core operations, frees its

@@ -1,5 +1,10 @@
 // Tensor-core chunk attention (bf16 rows), over a bf16 cache or one in 8 bits.
 //
+// For each row, running over the keys once: S = q K^T (tcgen05, fp32), P = exp2(S
+// scale log2(e) - m), l += sum P in fp32, O += P V (tcgen05, fp32) with P rounded
+// to bf16, as the MMA wants it beside bf16 values (half a step, 2^-8 of a weight);
+// o = O / l, lse = (m + log2 l) ln 2.
+//
 // Design (GB300, tcgen05):
 // * A unit is 2 TB consecutive new tokens of one (request, KV head), TB =
 //   128 / G: two query tiles A and B of up to 128 packed rows (row t G + g:
@@ -27,9 +32,29 @@
 // * Softmax and TMEM as in the prefill kernel: O (fp32) and S of a tile side by
 //   side, P (bf16) over the first half of S, the running maximum raised only
 //   when it grows by more than 2^8.
+// * A tile's whole rows leave by tensor copies through the place of its queries;
+//   the last tokens' and a part's fp32 rows as whole lines by their warps.
 // * Every wait is bounded; on expiry the kernel sets SPEC_DEV_TIMEOUT, stops
 //   issuing work, waits (bounded) for its own copies and MMAs, frees its TMEM
 //   and returns.
+//
+// What it measures, and what bounds it (heads of 128, the merging launch included):
+// * Three chunks of 1.5 - 2 K tokens behind 45 - 66 K, 32 heads over 8: 3.7 - 3.95
+//   ms, 1240 - 1320 TFLOP/s.  The MMAs of a 128-key step of both tiles take 2.08 K
+//   cycles of 3.1 K: a tile's chain of softmax, PV and next S is longer than the
+//   other's MMAs, and the clock gives way to the power limit.
+// * Whole prompts, 12.9 K tokens of 32 heads: 378 us (960 TFLOP/s): a unit's start,
+//   its last (masked) steps with their value check and its results, against 2 to 32
+//   steps.
+// * 39 single tokens and 9 chunks up to 512, behind 0.6 - 4 K: 226 us, of 79 for
+//   the bytes and 75 for the products: single tokens' tiles hold G rows of 128, and
+//   a CTA streams for them or computes for the others, not both.  48 single tokens
+//   behind 4 K, pages of 64: 135 us, 88 % of a copy's rate; 154 in pages of 16.
+// * 8 bits: 5.0 ms and 349 us on the first and third: the codes' widening (two
+//   tiles of 16 K elements a step, 8 warps) shares issue slots and shared memory
+//   with the softmax.  MMAs on the codes themselves would need none, but queries
+//   as two e4m3 values and P as three of e5m2, 2.5 products at twice the rate in
+//   the place of one, and the splitting of P in the softmax's chain.
 #include "chunk_attn.cuh"
 #include "kv8_common.cuh"
 #include "ptx_sm103.cuh"

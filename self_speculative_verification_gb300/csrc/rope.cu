@@ -7,8 +7,8 @@
 // fraction's own (2^-53 of it, or 2^-65), at any position; the remainder
 // becomes a float, and sin and cos of pi times it are taken in fp32.
 //
-// Bound by memory: 36 K tokens of 40 heads of 128 (bf16, halves; 680 MB) take 118
-// us, 5.8 TB/s, 85 % of a copy's rate; 4 K tokens of 10 heads of 64 in fp32 (31 MB)
+// Bound by memory: 33 K tokens of 40 heads of 128 (bf16, halves; 680 MB) take 118
+// us, 5.8 TB/s, 85 % of a copy's rate; 6 K tokens of 10 heads of 64 in fp32 (31 MB)
 // 7.0; a block of 128 rows of 64 heads 3.4, its launch and three dependent reads.
 #include <math.h>
 
@@ -38,7 +38,7 @@ struct RopeParams {
 enum { kPairs = 0, kHalves = 1, kHalvesScalar = 2 };
 
 // Threads of a CTA: at least a head's parts (by vectors 64 at most, by elements
-// 255).  Small CTAs of few tokens: 128 threads and 4 tokens take 118 us for 36 K
+// 255).  Small CTAs of few tokens: 128 threads and 4 tokens take 118 us for 33 K
 // tokens of 40 heads of 128 (680 MB, 5.8 TB/s), 256 and 16 take 127.
 __host__ __device__ constexpr int rope_threads(int layout) { return layout == kHalvesScalar ? 256 : 128; }
 
