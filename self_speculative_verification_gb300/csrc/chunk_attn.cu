@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm) chunk_simt_kernel(Ch
             bool odd = false;                            // a non-finite value among them
             // a thread's vectors are of one column, every kStep-th token: their rows
             // are found first, then all loads are in flight at once
-            constexpr int kStep = kSimtThreads / (D / 4), kBatch = 4;
+            constexpr int kStep = kSimtThreads / (D / 4), kBatch = 8;
             const int c = (tid % (D / 4)) * 4, tr = tid / (D / 4);
             for (int i0 = 0; i0 < kKeys; i0 += kStep * kBatch) {
                 ChunkRow row[kBatch];
@@ -161,7 +161,9 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm) chunk_simt_kernel(Ch
                     *reinterpret_cast<float4 *>(&sh.v[t][c]) = v[e];
                 }
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             odd = __syncthreads_or(odd);
+            if (tid / 32 * 8 >= nr) continue;            // (a warp's eight rows: none)
             float x[4][4] = {};
 #pragma unroll 4
             for (int c = 0; c < D; c += 4) {
@@ -271,114 +273,178 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm) chunk_simt_kernel(Ch
 }
 
 constexpr int kMergeWarps = 8;
+// rows of a warp, and parts of them, in flight (64 registers: 2 x 3 of D = 128; a
+// unit of the fp32 kernel has more parts, its steps being shorter)
+template <typename T> constexpr int kMergeRows = sizeof(T) == 2 ? 2 : 1;
+template <typename T> constexpr int kMergeParts = sizeof(T) == 2 ? 3 : 4;
 
 // Merges the parts of the unit that is first cut where CTA blockIdx.x + 1
-// begins; a warp a row, in the parts' order.
+// begins, in the parts' order; no read depends on more
+// than the records, since the call's end waits for them (four rows of a warp after
+// each other, each behind three more reads: mixed batch 226 -> 222 us, whole prompts
+// 380 -> 372, the smallest calls 20.6 -> 17.4).
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(ChunkParams P, int n_cta) {
+__global__ void __launch_bounds__(kMergeWarps * 32, 4) chunk_merge_kernel(ChunkParams P, int n_cta) {
     pdl_wait();
+    constexpr int R = kMergeRows<T>, U = kMergeParts<T>, E = D / 32;      // E: elements of a lane
     const int i = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int4 c = P.records[i];
-    if (c.x >= P.B || c.w == 0) return;
-    const int4 a = P.records[i - 1];
-    if (a.x == c.x && a.y == c.y && a.z == c.z && a.w > 0) return;     // cut earlier
-    const ChunkReq r = chunk_request(P, c.x, nullptr);
-    const int steps = chunk_steps(P, r, c.z);
     __shared__ int s_slot[1024];
+    __shared__ int4 s_at, s_unit;
     __shared__ int s_n;
     // the unit's parts: the one that begins it, then every CTA's that begins
     // inside it and has a step of it
     if (warp == 0) {
-        if (lane == 0) s_slot[0] = 2 * (i - 1) + 1;
-        int n = 1;
-        for (int k0 = i; k0 < n_cta; k0 += 32) {
-            const int k = k0 + lane;
-            const int4 x = k < n_cta ? P.records[k] : make_int4(P.B, 0, 0, 0);
-            const bool in = x.x == c.x && x.y == c.y && x.z == c.z && x.w > 0;
-            bool some = false;
-            if (in) {
-                const int4 y = P.records[k + 1];
-                const int end = y.x == c.x && y.y == c.y && y.z == c.z ? y.w : steps;
-                some = x.w < end;
+        const ChunkRecord x = P.records[min(i - 1 + lane, n_cta)];
+        int4 c, m;
+        c.x = __shfl_sync(0xffffffffu, x.at.x, 1);
+        c.y = __shfl_sync(0xffffffffu, x.at.y, 1);
+        c.z = __shfl_sync(0xffffffffu, x.at.z, 1);
+        c.w = __shfl_sync(0xffffffffu, x.at.w, 1);
+        m.x = __shfl_sync(0xffffffffu, x.unit.x, 1);
+        m.y = __shfl_sync(0xffffffffu, x.unit.y, 1);
+        m.z = __shfl_sync(0xffffffffu, x.unit.z, 1);
+        const bool in = x.at.x == c.x && x.at.y == c.y && x.at.z == c.z && x.at.w > 0;
+        unsigned inside = __ballot_sync(0xffffffffu, in);
+        int n = 0;
+        if (c.x < P.B && c.w > 0 && !(inside & 1u)) {    // (else no unit, or one that is cut earlier)
+            n = 1;
+            // CTA i - 1 + lane has steps of the unit up to where the next one begins
+            const int next = __shfl_down_sync(0xffffffffu, x.at.w, 1);
+            const bool on = (inside >> min(lane + 1, 31)) & 1u;
+            const bool some = lane > 0 && lane < 31 && in && i - 1 + lane < n_cta && x.at.w < (on ? next : m.z);
+            unsigned w = __ballot_sync(0xffffffffu, some);
+            if (lane == 0) s_slot[0] = 2 * (i - 1) + 1;
+            if (some) s_slot[n + __popc(w & ((1u << lane) - 1u))] = 2 * (i - 1 + lane);
+            n += __popc(w);
+            // (more than 30)
+            for (int k0 = i + 30; (inside >> 31) && k0 < n_cta; k0 += 31) {
+                const int k = min(k0 + lane, n_cta);
+                const int4 y = P.records[k].at;
+                const bool in2 = k < n_cta && y.x == c.x && y.y == c.y && y.z == c.z && y.w > 0;
+                inside = __ballot_sync(0xffffffffu, in2);
+                const int next2 = __shfl_down_sync(0xffffffffu, y.w, 1);
+                const bool on2 = (inside >> min(lane + 1, 31)) & 1u;
+                const bool some2 = lane < 31 && in2 && y.w < (on2 ? next2 : m.z);
+                w = __ballot_sync(0xffffffffu, some2);
+                if (some2) s_slot[n + __popc(w & ((1u << lane) - 1u))] = 2 * k;
+                n += __popc(w);
             }
-            const unsigned m = __ballot_sync(0xffffffffu, some);
-            if (some) s_slot[n + __popc(m & ((1u << lane) - 1u))] = 2 * k;
-            n += __popc(m);
-            if (!__all_sync(0xffffffffu, in)) break;
         }
-        if (lane == 0) s_n = n;
+        if (lane == 0) {
+            s_n = n;
+            s_at = c;
+            s_unit = m;
+        }
     }
     __syncthreads();
     const int n = s_n;
+    if (n == 0) return;
+    const int4 c = s_at, unit = s_unit;
+    const ChunkReq r{unit.x, unit.y, 0};
     const bool paired = chunk_paired(P, r);
     const long long r0 = (long long)c.z * P.ru;
-    constexpr int E = D / 32;
-    for (int row = blockIdx.y * kMergeWarps + warp; row < P.ru; row += gridDim.y * kMergeWarps) {
-        // the row's packed row and head; the second tile of a pair is the other head
-        const int x = paired && 2 * row >= P.ru ? 1 : 0;
-        const long long p = paired ? row - x * (P.ru / 2) : r0 + row;
-        const int h = paired ? 2 * c.y + x : c.y;
-        if (p >= (long long)r.n * P.G || h >= P.Hkv) continue;
-        // the largest maximum, a part a lane
-        float top = -INFINITY;
-        for (int k = lane; k < n; k += 32) top = fmaxf(top, P.part_ml[(size_t)s_slot[k] * P.ru + row].x);
-        top = warp_max(top);
-        float l = 0.f, acc[E] = {};
-        constexpr int U = 4;                             // parts in flight
-        for (int k0 = 0; k0 < n; k0 += U) {
-            float2 ml[U];
-            float x[U][E];
+    for (int row0 = (blockIdx.y * kMergeWarps + warp) * R; row0 < P.ru; row0 += gridDim.y * kMergeWarps * R) {
+        // each row's place in o (in heads), or -1; the second tile of a pair is the
+        // other head
+        long long to[R];
 #pragma unroll
-            for (int v = 0; v < U; ++v) {
-                ml[v] = make_float2(-INFINITY, 0.f);
-                if (k0 + v >= n) continue;
-                const size_t at = (size_t)s_slot[k0 + v] * P.ru + row;
-                ml[v] = P.part_ml[at];
-                const float *o = P.part_o + at * D + lane * E;
-                if constexpr (E == 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(o);
-                    x[v][0] = f.x; x[v][1] = f.y; x[v][2] = f.z; x[v][3] = f.w;
-                } else {
-                    const float2 f = *reinterpret_cast<const float2 *>(o);
-                    x[v][0] = f.x; x[v][1] = f.y;
+        for (int q = 0; q < R; ++q) {
+            const int row = row0 + q;
+            const int x = paired && 2 * row >= P.ru ? 1 : 0;
+            const long long p = paired ? row - x * (P.ru / 2) : r0 + row;
+            const int h = paired ? 2 * c.y + x : c.y;
+            to[q] = -1;
+            if (row < P.ru && p < (long long)r.n * P.G && h < P.Hkv)
+                to[q] = (r.first + p / P.G) * P.Hq + (long long)h * P.G + p % P.G;
+        }
+        float2 ml[R][U];
+        float x[R][U][E];
+        auto load = [&](int k0) {
+#pragma unroll
+            for (int v = 0; v < U; ++v)
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    ml[q][v] = make_float2(-INFINITY, 0.f);
+                    if (k0 + v >= n || to[q] < 0) continue;
+                    const size_t at = (size_t)s_slot[k0 + v] * P.ru + row0 + q;
+                    ml[q][v] = P.part_ml[at];
+                    const float *o = P.part_o + at * D + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(o);
+                        x[q][v][0] = f.x; x[q][v][1] = f.y; x[q][v][2] = f.z; x[q][v][3] = f.w;
+                    } else {
+                        const float2 f = *reinterpret_cast<const float2 *>(o);
+                        x[q][v][0] = f.x; x[q][v][1] = f.y;
+                    }
                 }
-            }
+        };
+        load(0);
+        // the largest maximum, a part a lane
+        float top[R], l[R], acc[R][E];
 #pragma unroll
-            for (int v = 0; v < U; ++v) {
-                // (a part without weight may hold nothing; one of NaN has its
-                // maximum from the other scores, or none)
-                if (ml[v].y == 0.f) continue;
-                const float w = ml[v].x == -INFINITY ? 1.f : exp2f(ml[v].x - top);
-                l = fmaf(w, ml[v].y, l);
+        for (int q = 0; q < R; ++q) {
+            top[q] = -INFINITY;
+            l[q] = 0.f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[v][e], acc[e]);
-            }
+            for (int e = 0; e < E; ++e) acc[q][e] = 0.f;
         }
-        const long long tok = r.first + p / P.G, hq = (long long)h * P.G + p % P.G;
-        T *o = static_cast<T *>(P.o) + (tok * P.Hq + hq) * D + lane * E;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if constexpr (sizeof(T) == 2) {
-            uint32_t w[E / 2];
+        if (n <= U) {
 #pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-                w[e] = *reinterpret_cast<const uint32_t *>(&h);
-            }
-            if constexpr (E == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t *>(o) = w[0];
+            for (int q = 0; q < R; ++q)
+#pragma unroll
+                for (int v = 0; v < U; ++v) top[q] = fmaxf(top[q], ml[q][v].x);
         } else {
+            for (int k = lane; k < n; k += 32)
 #pragma unroll
-            for (int e = 0; e < E; ++e) store_f(o + e, acc[e] * inv);
+                for (int q = 0; q < R; ++q)
+                    if (to[q] >= 0) top[q] = fmaxf(top[q], P.part_ml[(size_t)s_slot[k] * P.ru + row0 + q].x);
+#pragma unroll
+            for (int q = 0; q < R; ++q) top[q] = warp_max(top[q]);
         }
-        if (lane == 0)
-            P.lse[tok * P.Hq + hq] = l == 0.f ? -INFINITY : l != l ? l : (top + log2f(l)) * kLn2;
+        for (int k0 = 0; k0 < n; k0 += U) {
+            if (k0 > 0) load(k0);
+#pragma unroll
+            for (int v = 0; v < U; ++v)
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    // (a part without weight may hold nothing; one of NaN has its
+                    // maximum from the other scores, or none)
+                    if (ml[q][v].y == 0.f) continue;
+                    const float w = ml[q][v].x == -INFINITY ? 1.f : exp2f(ml[q][v].x - top[q]);
+                    l[q] = fmaf(w, ml[q][v].y, l[q]);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[q][e] = fmaf(w, x[q][v][e], acc[q][e]);
+                }
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            if (to[q] < 0) continue;
+            T *o = static_cast<T *>(P.o) + to[q] * D + lane * E;
+            const float inv = l[q] == 0.f ? 0.f : 1.f / l[q];
+            if constexpr (sizeof(T) == 2) {
+                uint32_t w[E / 2];
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[q][2 * e] * inv, acc[q][2 * e + 1] * inv);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                if constexpr (E == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+                else *reinterpret_cast<uint32_t *>(o) = w[0];
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) store_f(o + e, acc[q][e] * inv);
+            }
+            if (lane == 0)
+                P.lse[to[q]] = l[q] == 0.f ? -INFINITY : l[q] != l[q] ? l[q] : (top[q] + log2f(l[q])) * kLn2;
+        }
     }
 }
 
 // ------------------------------------------------------------- host side
 
 ChunkPlan simt_plan() {
-    return ChunkPlan{kRows, 0, kKeys, 2 * kKeys, 2 * kKeys, kSimtPerSm * num_sms()};
+    // (a step is worth a CTA: the smallest calls 21 -> 17 us)
+    return ChunkPlan{kRows, 0, kKeys, 2 * kKeys, kKeys, kSimtPerSm * num_sms()};
 }
 
 ChunkPlan plan_of(const ChunkParams &P, int dtype, bool kv8) {
@@ -396,7 +462,7 @@ ChunkSpace space_of(const ChunkPlan &pl, int d) {
     const size_t rows = 2 * (size_t)pl.n_cta * pl.ru;
     w.ml = round256(rows * d * sizeof(float));
     w.rec = w.ml + round256(rows * sizeof(float2));
-    w.bytes = w.rec + round256((size_t)(pl.n_cta + 1) * sizeof(int4));
+    w.bytes = w.rec + round256((size_t)(pl.n_cta + 1) * sizeof(ChunkRecord));
     return w;
 }
 
@@ -486,6 +552,12 @@ spec_status_t launch_simt(const ChunkParams &P, int n_cta, cudaStream_t s) {
     return launch(f, dim3(n_cta), dim3(kSimtThreads), smem, s, P);
 }
 
+template <typename T, int D>
+spec_status_t launch_merge(const ChunkParams &P, int n_cta, cudaStream_t s) {
+    const dim3 grid(n_cta - 1, ceil_div(P.ru, kMergeRows<T> * kMergeWarps));
+    return launch(chunk_merge_kernel<T, D>, grid, dim3(kMergeWarps * 32), 0, s, P, n_cta);
+}
+
 spec_status_t run_chunk(ChunkParams &P, int dtype, bool kv8, const void *q, long long stride_q,
                         const int32_t *seq_len, const int32_t *cu_new, void *o, float *lse,
                         void *workspace, size_t workspace_bytes, void *stream) {
@@ -518,7 +590,7 @@ spec_status_t run_chunk(ChunkParams &P, int dtype, bool kv8, const void *q, long
     uint8_t *base = static_cast<uint8_t *>(workspace);
     P.part_o = reinterpret_cast<float *>(base + w.o);
     P.part_ml = reinterpret_cast<float2 *>(base + w.ml);
-    P.records = reinterpret_cast<int4 *>(base + w.rec);
+    P.records = reinterpret_cast<ChunkRecord *>(base + w.rec);
     P.ru = pl.ru;
     P.tu = pl.tu;
     P.ks = pl.ks;
@@ -531,13 +603,10 @@ spec_status_t run_chunk(ChunkParams &P, int dtype, bool kv8, const void *q, long
     if (dtype == SPEC_BF16) st = launch_chunk_tc(P, kv8, pl.n_cta, s);
     else st = kv8 ? launch_simt<kCache8>(P, pl.n_cta, s) : launch_simt<kCacheRows>(P, pl.n_cta, s);
     if (st != SPEC_OK) return st;
-    const dim3 grid(pl.n_cta - 1, ceil_div(pl.ru, 4 * kMergeWarps)), block(kMergeWarps * 32);
     if (dtype == SPEC_BF16)
-        st = P.d == 128 ? launch(chunk_merge_kernel<__nv_bfloat16, 128>, grid, block, 0, s, P, pl.n_cta)
-                        : launch(chunk_merge_kernel<__nv_bfloat16, 64>, grid, block, 0, s, P, pl.n_cta);
+        st = P.d == 128 ? launch_merge<__nv_bfloat16, 128>(P, pl.n_cta, s) : launch_merge<__nv_bfloat16, 64>(P, pl.n_cta, s);
     else
-        st = P.d == 128 ? launch(chunk_merge_kernel<float, 128>, grid, block, 0, s, P, pl.n_cta)
-                        : launch(chunk_merge_kernel<float, 64>, grid, block, 0, s, P, pl.n_cta);
+        st = P.d == 128 ? launch_merge<float, 128>(P, pl.n_cta, s) : launch_merge<float, 64>(P, pl.n_cta, s);
     if (st != SPEC_OK) return st;
     return launch_status();
 }

@@ -25,6 +25,12 @@
 
 namespace sv {
 
+// Where a CTA's share begins (ChunkPos; a request past the last: nowhere), and of
+// that unit its request's first packed token, new tokens, and its steps.
+struct ChunkRecord {
+    int4 at, unit;
+};
+
 struct ChunkParams {
     const void *q;
     long long stride_q;      // elements between two tokens' rows of q
@@ -35,7 +41,7 @@ struct ChunkParams {
     float *lse;
     float *part_o;           // [2 n_cta][ru][d]
     float2 *part_ml;         // [2 n_cta][ru] (log2 domain)
-    int4 *records;           // [n_cta + 1] where each CTA's share begins
+    ChunkRecord *records;    // [n_cta + 1]
     int *status;
     int B, n_tokens, Hq, Hkv, G, d;
     int paged, ps, max_pages, n_pages;
@@ -200,8 +206,14 @@ __device__ void chunk_share(const ChunkParams &P, ChunkShare &sh) {
     __syncthreads();
     if (tid == 0) {
         const ChunkPos p = sh.begin;
-        P.records[blockIdx.x] = make_int4(p.b, p.h, p.j, p.s);
-        if (blockIdx.x == gridDim.x - 1) P.records[gridDim.x] = make_int4(P.B, 0, 0, 0);
+        ChunkRecord c{make_int4(p.b, p.h, p.j, p.s), make_int4(0, 0, 0, 0)};
+        if (p.s > 0) {                                   // (what the merging kernel asks for)
+            const ChunkReq q = chunk_request(P, p.b, nullptr);
+            c.unit = make_int4(q.first, q.n, chunk_steps(P, q, p.j), 0);
+        }
+        P.records[blockIdx.x] = c;
+        if (blockIdx.x == gridDim.x - 1)
+            P.records[gridDim.x] = ChunkRecord{make_int4(P.B, 0, 0, 0), make_int4(0, 0, 0, 0)};
     }
 }
 
