@@ -927,18 +927,29 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 constexpr int kHeld = K8 ? 2 : 4;        // 32-key parts of the row held
                 uint32_t v[kHeld][32];
                 float tmv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                // hidden scores become -inf in place
-                // Parts of which no row of the warp sees any: their weights are left out.
-                // (With the row held whole the branch costs the main path more than
-                // it saves: whole prompts 379 -> 408 us.)
+                // Hidden scores become -inf where they lie: a few rolled instructions, so
+                // that all steps run the same unrolled ones below (masked there, whole
+                // prompts take 370 us instead of 359, and the 8-bit mixed batch 347
+                // instead of 310; a copy of them for such steps alone 427 and 332).
+                // hidden: parts of which no row of the warp sees any, whose weights are
+                // left out beside the widening warps (elsewhere the branch costs more:
+                // prompts 383 us).
                 uint32_t hidden = 0u;
-                auto mask = [&](uint32_t (&w)[32], int c) {
-                    const int n = seen - c0 - c * 32;                // seen ones of these 32
-                    if (__all_sync(0xffffffffu, n >= 32)) return;
-                    if (K8 && __all_sync(0xffffffffu, n <= 0)) hidden |= 1u << c;
+                if (masked) {
+#pragma unroll 1
+                    for (int c = 0; c < kN / 32; ++c) {
+                        const int n = seen - c0 - c * 32;            // seen ones of these 32
+                        if (__all_sync(0xffffffffu, n >= 32)) continue;
+                        if (K8 && __all_sync(0xffffffffu, n <= 0)) hidden |= 1u << c;
+                        uint32_t w[32];
+                        ld32(tS + c * 32, w);
+                        wait_ld(w);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) w[e] = e < n ? w[e] : 0xff800000u;
-                };
+                        for (int e = 0; e < 32; ++e) w[e] = e < n ? w[e] : 0xff800000u;
+                        st32(tS + c * 32, w);
+                    }
+                    wait_st();
+                }
                 // the row maximum (three-input max, four chains)
                 auto top = [&](const uint32_t (&w)[32]) {
 #pragma unroll
@@ -951,10 +962,6 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 for (int c = 0; c < kHeld; ++c) ld32(tS + c * 32, v[c]);
 #pragma unroll
                 for (int c = 0; c < kHeld; ++c) wait_ld(v[c]);
-                if (masked) {
-#pragma unroll
-                    for (int c = 0; c < kHeld; ++c) mask(v[c], c);
-                }
 #pragma unroll
                 for (int c = 0; c < kHeld; ++c) top(v[c]);
 #pragma unroll
@@ -962,7 +969,6 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     uint32_t w[32];
                     ld32(tS + c * 32, w);
                     wait_ld(w);
-                    if (masked) mask(w, c);
                     top(w);
                 }
                 const float traw = fmaxf(fmaxf(tmv[0], tmv[1]), fmaxf(tmv[2], tmv[3]));
@@ -1009,7 +1015,6 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         if (c >= kHeld) {
                             ld32(tS + c * 32, w);
                             wait_ld(w);
-                            if (masked) mask(w, c);
                         }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
