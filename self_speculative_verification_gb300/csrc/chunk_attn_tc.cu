@@ -1087,28 +1087,24 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             auto pass = [&](auto as_bf16, auto as_tile, int c0, bool last) {
                 constexpr bool kBf16 = decltype(as_bf16)::value, kFull = decltype(as_tile)::value;
                 constexpr int N = kBf16 ? D : D / 2;
-                constexpr int kCols = K8 && N > 64 ? 64 : N;         // read at a time
+                constexpr int kPer = kBf16 ? 4 : 8;                  // chunks of 32 columns
+#pragma unroll 1
+                for (int n0 = 0; n0 < N; n0 += 32) {
+                    uint32_t y[32];
+                    ld32(tO + c0 + n0, y);
+                    wait_ld(y);
+                    if (last && n0 + 32 == N) let_go_of_o();
 #pragma unroll
-                for (int n0 = 0; n0 < N; n0 += kCols) {
-                    uint32_t v[kCols / 32][32];
-#pragma unroll
-                    for (int c = 0; c < kCols / 32; ++c) ld32(tO + c0 + n0 + c * 32, v[c]);
-#pragma unroll
-                    for (int c = 0; c < kCols / 32; ++c) wait_ld(v[c]);
-                    if (last && n0 + kCols == N) let_go_of_o();
-                    constexpr int kPer = kBf16 ? 4 : 8;              // chunks of 32 columns
-#pragma unroll
-                    for (int k = 0; k < kCols / 32 * kPer; ++k) {
+                    for (int k = 0; k < kPer; ++k) {
                         uint4 w;
-                        const uint32_t (&y)[32] = v[k / kPer];
                         if constexpr (kBf16) {
-                            const int e = 8 * (k % 4);
+                            const int e = 8 * k;
                             w = make_uint4(pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
                                            pack_bf16(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv),
                                            pack_bf16(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv),
                                            pack_bf16(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv));
                         } else {
-                            const int e = 4 * (k % 8);
+                            const int e = 4 * k;
                             w = make_uint4(__float_as_uint(__uint_as_float(y[e]) * inv),
                                            __float_as_uint(__uint_as_float(y[e + 1]) * inv),
                                            __float_as_uint(__uint_as_float(y[e + 2]) * inv),
@@ -1172,8 +1168,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             } else if (whole) {
                 pass(Bool<true>{}, Bool<false>{}, 0, true);
             } else {
-                pass(Bool<false>{}, Bool<false>{}, 0, false);
-                pass(Bool<false>{}, Bool<false>{}, D / 2, true);
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += D / 2) pass(Bool<false>{}, Bool<false>{}, c0, c0 > 0);
             }
             if (row_ok) {
                 const size_t at = first + r + (size_t)rt * skip;
