@@ -1120,22 +1120,26 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 }
                 if constexpr (kFull) return;
                 __syncwarp();
-                uint4 w[CH];
-#pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    const int rr = k * RI + lane / CH;
-                    w[k] = *reinterpret_cast<const uint4 *>(stage + rr * RB + (((lane % CH) ^ (rr & 7)) << 4));
-                }
-                __syncwarp();
-                if (last) let_go_of_q();
                 uint8_t *dst = kBf16 ? static_cast<uint8_t *>(A.o) : reinterpret_cast<uint8_t *>(A.part_o) + c0 * 4;
+                constexpr int kAtOnce = 8;
+#pragma unroll 1
+                for (int k0 = 0; k0 < CH; k0 += kAtOnce) {
+                    uint4 w[kAtOnce];
 #pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    const int rr = k * RI + lane / CH;
-                    if (rr >= nr) continue;
-                    const uint32_t tok = ((uint32_t)(r0 + rr) * P.g_mul) >> 16;
-                    const size_t at = first + (uint32_t)(r0 + rr) + (size_t)tok * skip;
-                    *reinterpret_cast<uint4 *>(dst + at * (kBf16 ? 2 * D : 4 * D) + (lane % CH) * 16) = w[k];
+                    for (int k = 0; k < kAtOnce; ++k) {
+                        const int rr = (k0 + k) * RI + lane / CH;
+                        w[k] = *reinterpret_cast<const uint4 *>(stage + rr * RB + (((lane % CH) ^ (rr & 7)) << 4));
+                    }
+                    __syncwarp();
+                    if (last && k0 + kAtOnce == CH) let_go_of_q();
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) {
+                        const int rr = (k0 + k) * RI + lane / CH;
+                        if (rr >= nr) continue;
+                        const uint32_t tok = ((uint32_t)(r0 + rr) * P.g_mul) >> 16;
+                        const size_t at = first + (uint32_t)(r0 + rr) + (size_t)tok * skip;
+                        *reinterpret_cast<uint4 *>(dst + at * (kBf16 ? 2 * D : 4 * D) + (lane % CH) * 16) = w[k];
+                    }
                 }
             };
             if (whole && t.nt[x] == P.tb) {
@@ -1207,7 +1211,7 @@ spec_status_t launch_tc(const ctc::Params &P, const CUtensorMap (&m)[4], int n_c
 ChunkPlan chunk_tc_plan(const ChunkParams &P, bool kv8) {
     (void)kv8;
     const int tb = ctc::kM / P.G;
-    return ChunkPlan{2 * tb * P.G, 2 * tb, ctc::kN, 4 * ctc::kN, 2 * ctc::kN, num_sms()};
+    return ChunkPlan{2 * tb * P.G, 2 * tb, ctc::kN, 3 * ctc::kN, 2 * ctc::kN, num_sms()};
 }
 
 spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStream_t s) {
