@@ -85,7 +85,7 @@ __device__ __forceinline__ float4 chunk_elems(const ChunkParams &P, const uint8_
 // 128 threads: thread (ty, tx) has the scores of rows 4 ty .. + 3 and keys tx + 16
 // i, and the outputs of the same rows and dimensions 4 tx + 64 i .. + 3, so that a
 // 16-byte read of shared memory feeds eight FMAs and more.  Long calls are bound by
-// those; the smallest (two chunks of 8 tokens behind 200: 21 us with the merging launch)
+// those; the smallest (two chunks of 8 tokens behind 200: 14 us with the merging launch)
 // by a few steps' chains -- page id, loads, products -- after the share of the
 // work is found.
 template <int D, int kCache>

@@ -19,8 +19,8 @@
 //   10 issue the MMAs of tiles A and B from one thread each -- PV(j), S(j+1), PV
 //   (j+1), .. -- so that the tensor core works on one tile while the other's
 //   softmax, or its change of unit, runs.
-// * bf16 cache: K and V tiles come by tensor copies, one a page and 64 elements,
-//   into a ring of 128-byte-swizzled slots.  Warp 11 looks through the
+// * bf16 cache: K and V tiles come by tensor copies, one a page (contiguous, or D =
+//   64: one a tile or page and 64 elements), into a ring of 128-byte-swizzled slots.  Warp 11 looks through the
 //   value tiles that not every row sees whole (the last ones of a unit): rows
 //   past the unit's last token become zeros, and non-finite values too, whose
 //   first place they note, for a hidden value's weight of zero would not keep
@@ -43,14 +43,15 @@
 //   ms, 1240 - 1320 TFLOP/s.  The MMAs of a 128-key step of both tiles take 2.08 K
 //   cycles of 3.1 K: a tile's chain of softmax, PV and next S is longer than the
 //   other's MMAs, and the clock gives way to the power limit.
-// * Whole prompts, 12.9 K tokens of 32 heads: 378 us (960 TFLOP/s): a unit's start,
+// * Whole prompts, 12.9 K tokens of 32 heads: 345 us (1050 TFLOP/s): a unit's start,
 //   its last (masked) steps with their value check and its results, against 2 to 32
-//   steps.
-// * 39 single tokens and 9 chunks up to 512, behind 0.6 - 4 K: 226 us, of 79 for
-//   the bytes and 75 for the products: single tokens' tiles hold G rows of 128, and
-//   a CTA streams for them or computes for the others, not both.  48 single tokens
-//   behind 4 K, pages of 64: 135 us, 88 % of a copy's rate; 154 in pages of 16.
-// * 8 bits: 5.0 ms and 349 us on the first and third: the codes' widening (two
+//   steps, and the merging launch (11).  What runs once a unit or less is kept in
+//   rolled loops: unrolled it has to be fetched each time, beside the steps' code.
+// * 39 single tokens and 9 chunks up to 512, behind 0.6 - 4 K: 213 us, of 79 for
+//   the bytes and 75 for the products: a unit of two heads takes four slots of the
+//   ring a step, which leaves one to load ahead, and holds G rows of 128 in a tile.
+//   48 single tokens behind 4 K: 133 us, 89 % of a copy's rate, in pages of any size.
+// * 8 bits: 4.9 ms and 304 us on the first and third: the codes' widening (two
 //   tiles of 16 K elements a step, 8 warps) shares issue slots and shared memory
 //   with the softmax.  MMAs on the codes themselves would need none, but queries
 //   as two e4m3 values and P as three of e5m2, 2.5 products at twice the rate in
@@ -283,7 +284,12 @@ __device__ __forceinline__ uint32_t nan4(uint32_t w) { return (w & 0x7f7f7f7fu) 
 
 }  // namespace ctc
 
-template <int D, bool K8>
+// kJoint (pages of the bf16 cache, D = 128): the K and V tiles' 64-element halves
+// lie side by side, eight tokens of the one, then of the other, so that a page
+// comes in one copy; a copy costs the producer its issue, whatever its size (48
+// single tokens behind 4 K in pages of 16: 152 -> 136 us).  half_at, group_at: bytes
+// between the halves, and between groups of eight tokens.
+template <int D, bool K8, bool kJoint>
 __global__ void __launch_bounds__(ctc::Cfg<D, K8>::kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ CUtensorMap mq,
                 const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mk,
@@ -301,6 +307,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
     Shared &sh = *reinterpret_cast<Shared *>(stages + C::kStages * C::kStage);
     const ChunkParams &A = P.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    constexpr uint32_t half_at = kJoint ? 1024u : (uint32_t)kHalf, group_at = kJoint ? 2048u : 1024u;
 
     if (threadIdx.x == kProducerWarp * 32) {
         const CUtensorMap *maps[4] = {&mq, &mo, &mk, &mv};
@@ -370,7 +378,9 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             // 3.71 ms)
             const uint64_t pol = policy_evict_first();
             const int per = kN / P.box;                  // copies a tile, by tokens
-            const int hh = lane % NH, bx = lane / NH;    // rows cache: this lane's copy
+            // rows cache: this lane's copy
+            const int hh = kJoint ? 0 : lane % NH, bx = kJoint ? lane : lane / NH;
+            const uint32_t copy_bytes = (uint32_t)P.box * (kJoint ? 256u : 128u);
             int slot = 0;                                // next slot (8 bits: stage)
             int nq[2] = {0, 0};                          // queries copied, per tile
             uint32_t ph = 1;                             // parity of its release
@@ -472,12 +482,15 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                                     break;
                                 }
                                 if (lane == 0) {
-                                    mbar_arrive_expect_tx(&sh.full[slot], n_in * (uint32_t)(P.box * 128));
+                                    mbar_arrive_expect_tx(&sh.full[slot], n_in * copy_bytes);
                                     *(volatile uint32_t *)&sh.issued = (uint32_t)ld + 1u;
                                 }
                                 __syncwarp();
-                                uint8_t *dst = ring + slot * kTile + hh * kHalf + bx * P.box * 128;
-                                if (in && A.paged)
+                                uint8_t *dst = ring + slot * kTile + hh * kHalf + bx * copy_bytes;
+                                if (in && kJoint)
+                                    tma_load_5d(dst, kv ? &mv : &mk, 0, 0, 0, off >> 3, id * A.Hkv + h,
+                                                &sh.full[slot], pol);
+                                else if (in && A.paged)
                                     tma_load_3d(dst, kv ? &mv : &mk, 0, off, (id * A.Hkv + h) * NH + hh,
                                                 &sh.full[slot], pol);
                                 else if (in)
@@ -526,8 +539,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 const uint64_t qd = smem_desc(smem_u32(qbuf + x * kTile), 16, 1024);
                 // descriptors of slot 0 (K: K-major, V: MN-major); a slot is kTile
                 // further, i.e. kTile >> 4 in the address field
-                const uint64_t kd0 = smem_desc(smem_u32(ring), 16, 1024);
-                const uint64_t vd0 = smem_desc(smem_u32(ring), kHalf, 1024);
+                const uint64_t kd0 = smem_desc(smem_u32(ring), 16, group_at);
+                const uint64_t vd0 = smem_desc(smem_u32(ring), half_at, group_at);
                 uint32_t base = 0;                       // fills of the ring before this part
                 uint32_t np = 0, nact = 0;               // P hand-offs taken; parts with this tile
                 bool ok = true;
@@ -595,8 +608,9 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         const uint64_t kd = kd0 + (uint64_t)(slot * (kTile >> 4));
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint64_t off = (uint64_t)((((ks >> 2) * kHalf) + (ks & 3) * 32) >> 4);
-                            mma_ss(tS, qd + off, kd + off, id_s, ks > 0 ? 1u : 0u);
+                            const uint64_t q_off = (uint64_t)((((ks >> 2) * kHalf) + (ks & 3) * 32) >> 4);
+                            const uint64_t k_off = (uint64_t)(((ks >> 2) * half_at + (ks & 3) * 32) >> 4);
+                            mma_ss(tS, qd + q_off, kd + k_off, id_s, ks > 0 ? 1u : 0u);
                             if (ks == 3) unlock();           // (the queue holds that many)
                         }
                         commit(&sh.s_full[x]);
@@ -630,7 +644,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                             fence_after();
 #pragma unroll
                             for (int ks = half * (kN / 32); ks < (half + 1) * (kN / 32); ++ks)
-                                mma(tO, tS + ks * 8, vd + (uint64_t)((ks * 2048) >> 4), id_pv,
+                                mma(tO, tS + ks * 8, vd + (uint64_t)((ks * 2 * group_at) >> 4), id_pv,
                                     (ks > 0 || j > 0) ? 1u : 0u);
                         }
                         if (!ok) break;
@@ -689,7 +703,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         // past the last token: zeros
                         for (int g = r1 >> 3; g < kN / 8; ++g) {
                             for (int hh = 0; hh < NH; ++hh) {
-                                uint8_t *p = v + hh * kHalf + g * 1024;
+                                uint8_t *p = v + hh * half_at + g * group_at;
                                 if (8 * g + (lane >> 3) >= r1) *reinterpret_cast<uint4 *>(p + lo) = zero;
                                 if (8 * g + 4 + (lane >> 3) >= r1) *reinterpret_cast<uint4 *>(p + hi) = zero;
                             }
@@ -700,7 +714,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         for (int g = r0 >> 3; 8 * g < r1; ++g)
 #pragma unroll
                             for (int hh = 0; hh < NH; ++hh) {
-                                const uint8_t *p = v + hh * kHalf + g * 1024;
+                                const uint8_t *p = v + hh * half_at + g * group_at;
                                 const uint4 a = *reinterpret_cast<const uint4 *>(p + lo);
                                 const uint4 b = *reinterpret_cast<const uint4 *>(p + hi);
                                 sum[0] = times0(a.x, sum[0]);
@@ -720,7 +734,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                             int *mine = bad + (t.sets == 2 ? (i >> 1) & 1 : 0);
                             for (int r = r0; r < r1; ++r) {
                                 if (lane >= NH * 8) continue;
-                                uint4 *p = reinterpret_cast<uint4 *>(v + (lane >> 3) * kHalf + r * 128 +
+                                uint4 *p = reinterpret_cast<uint4 *>(v + (lane >> 3) * half_at + (r >> 3) * group_at + (r & 7) * 128 +
                                                                      (((lane & 7) ^ (r & 7)) << 4));
                                 if (!odd8(*p)) continue;
                                 atomicMin(mine, s * kN + r);
@@ -1196,13 +1210,13 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                      "r"(kTmemCols));
 }
 
-template <int D, bool K8>
+template <int D, bool K8, bool kJoint>
 spec_status_t launch_tc(const ctc::Params &P, const CUtensorMap (&m)[4], int n_cta, cudaStream_t s) {
     constexpr size_t smem = ctc::smem_bytes<D, K8>();
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    if (set_smem_limit(reinterpret_cast<const void *>(chunk_tc_kernel<D, K8>), smem) != SPEC_OK)
+    if (set_smem_limit(reinterpret_cast<const void *>(chunk_tc_kernel<D, K8, kJoint>), smem) != SPEC_OK)
         return SPEC_ERR_CUDA;
-    return launch(chunk_tc_kernel<D, K8>, dim3(n_cta), dim3(ctc::Cfg<D, K8>::kThreads), smem, s, P, m[0], m[1], m[2],
+    return launch(chunk_tc_kernel<D, K8, kJoint>, dim3(n_cta), dim3(ctc::Cfg<D, K8>::kThreads), smem, s, P, m[0], m[1], m[2],
                   m[3]);
 }
 
@@ -1235,6 +1249,7 @@ spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStr
         P.ps_shift = 31 + L;
         P.ps_mul = (uint32_t)(((1ull << (31 + L)) + C.ps - 1) / C.ps);
     }
+    const bool joint = !kv8 && C.paged && C.d == 128;
     CUtensorMap m[4] = {};
     const cuuint64_t d0[3] = {(cuuint64_t)C.d, (cuuint64_t)C.Hq, (cuuint64_t)C.n_tokens};
     const cuuint64_t s0[2] = {(cuuint64_t)C.d * 2, (cuuint64_t)C.stride_q * 2};
@@ -1254,11 +1269,20 @@ spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStr
             s1[1] = (cuuint64_t)C.ps * 128;
         }
         const cuuint32_t b1[3] = {64u, (cuuint32_t)P.box, 1u};
-        if (!encode_bf16_map(&m[2], C.kc, 3, d1, s1, b1) || !encode_bf16_map(&m[3], C.vc, 3, d1, s1, b1))
-            return SPEC_ERR_CUDA;
+        // pages of two halves: eight tokens of the one, of the other, and so on
+        const cuuint64_t d2[5] = {64u, 8u, nh, (cuuint64_t)C.ps / 8, (cuuint64_t)C.n_pages * C.Hkv};
+        const cuuint64_t s2[4] = {128u, (cuuint64_t)C.ps * 128, 1024u, (cuuint64_t)C.ps * 128 * nh};
+        const cuuint32_t b2[5] = {64u, 8u, (cuuint32_t)nh, (cuuint32_t)P.box / 8, 1u};
+        for (int kv = 0; kv < 2; ++kv) {
+            const void *base = kv ? C.vc : C.kc;
+            if (!(joint ? encode_bf16_map(&m[2 + kv], base, 5, d2, s2, b2)
+                        : encode_bf16_map(&m[2 + kv], base, 3, d1, s1, b1)))
+                return SPEC_ERR_CUDA;
+        }
     }
-    if (C.d == 128) return kv8 ? launch_tc<128, true>(P, m, n_cta, s) : launch_tc<128, false>(P, m, n_cta, s);
-    return kv8 ? launch_tc<64, true>(P, m, n_cta, s) : launch_tc<64, false>(P, m, n_cta, s);
+    if (C.d == 64) return kv8 ? launch_tc<64, true, false>(P, m, n_cta, s) : launch_tc<64, false, false>(P, m, n_cta, s);
+    if (kv8) return launch_tc<128, true, false>(P, m, n_cta, s);
+    return joint ? launch_tc<128, false, true>(P, m, n_cta, s) : launch_tc<128, false, false>(P, m, n_cta, s);
 }
 
 }  // namespace sv
