@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) chunk_merge_kernel(ChunkP
 
 ChunkPlan simt_plan() {
     // (a step is worth a CTA: the smallest calls 21 -> 17 us)
-    return ChunkPlan{kRows, 0, kKeys, 2 * kKeys, kKeys, kSimtPerSm * num_sms()};
+    return ChunkPlan{kRows, 0, kKeys, 2 * kKeys, 8, kKeys, kSimtPerSm * num_sms()};
 }
 
 ChunkPlan plan_of(const ChunkParams &P, int dtype, bool kv8) {
@@ -595,6 +595,7 @@ spec_status_t run_chunk(ChunkParams &P, int dtype, bool kv8, const void *q, long
     P.tu = pl.tu;
     P.ks = pl.ks;
     P.fixed_cost = pl.fixed_cost;
+    P.pair_cost = pl.pair_cost;
     P.min_share = pl.min_share;
     P.wait = wait_limit();
     P.status = status_ptr();

@@ -50,6 +50,7 @@ struct ChunkParams {
     int ru, ks;              // rows of a unit, keys of a step
     int tu;                  // tokens of a unit (two tiles: ru / G), or 0: units end inside a token's rows
     int fixed_cost;          // of a unit, in keys
+    int pair_cost;           // of a key behind a pair of heads, in eighths
     int min_share;           // least cost (keys) worth a CTA
     float scale_log2;        // softmax scale * log2(e)
     long long wait;          // limit of every pipeline wait, in SM cycles
@@ -57,7 +58,7 @@ struct ChunkParams {
 
 // The tensor-core path: rows and CTAs of a call, its kernel's launch.
 struct ChunkPlan {
-    int ru, tu, ks, fixed_cost, min_share, n_cta;
+    int ru, tu, ks, fixed_cost, pair_cost, min_share, n_cta;
 };
 ChunkPlan chunk_tc_plan(const ChunkParams &P, bool kv8);
 spec_status_t launch_chunk_tc(const ChunkParams &P, bool kv8, int n_cta, cudaStream_t s);
@@ -97,9 +98,9 @@ __device__ __forceinline__ int chunk_units(const ChunkParams &P, const ChunkReq 
 
 // Cost of a head's (a pair's) first j units (in keys * G): unit i costs G (fixed
 // + S) + (i + 1) ru; for a pair, whose steps are each head's own, the S counts
-// twice.
+// pair_cost / 8 times.
 __device__ __forceinline__ long long chunk_cost(const ChunkParams &P, const ChunkReq &r, long long j) {
-    const long long S = chunk_paired(P, r) ? 2ll * r.S : r.S;
+    const long long S = chunk_paired(P, r) ? (long long)r.S * P.pair_cost >> 3 : r.S;
     return j * P.G * (P.fixed_cost + S) + P.ru * (j * (j + 1) / 2);
 }
 

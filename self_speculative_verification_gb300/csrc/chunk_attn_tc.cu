@@ -47,11 +47,11 @@
 //   its last (masked) steps with their value check and its results, against 2 to 32
 //   steps, and the merging launch (11).  What runs once a unit or less is kept in
 //   rolled loops: unrolled it has to be fetched each time, beside the steps' code.
-// * 39 single tokens and 9 chunks up to 512, behind 0.6 - 4 K: 213 us, of 79 for
+// * 39 single tokens and 9 chunks up to 512, behind 0.6 - 4 K: 191 us, of 79 for
 //   the bytes and 75 for the products: a unit of two heads takes four slots of the
 //   ring a step, which leaves one to load ahead, and holds G rows of 128 in a tile.
 //   48 single tokens behind 4 K: 133 us, 89 % of a copy's rate, in pages of any size.
-// * 8 bits: 4.9 ms and 304 us on the first and third: the codes' widening (two
+// * 8 bits: 4.9 ms and 285 us on the first and third: the codes' widening (two
 //   tiles of 16 K elements a step, 8 warps) shares issue slots and shared memory
 //   with the softmax.  MMAs on the codes themselves would need none, but queries
 //   as two e4m3 values and P as three of e5m2, 2.5 products at twice the rate in
@@ -1223,9 +1223,14 @@ spec_status_t launch_tc(const ctc::Params &P, const CUtensorMap (&m)[4], int n_c
 }  // namespace
 
 ChunkPlan chunk_tc_plan(const ChunkParams &P, bool kv8) {
-    (void)kv8;
     const int tb = ctc::kM / P.G;
-    return ChunkPlan{2 * tb * P.G, 2 * tb, ctc::kN, 3 * ctc::kN, 2 * ctc::kN, num_sms()};
+    // What a key costs a unit of two heads, against one of a single head's two tiles:
+    // 39 single tokens and 9 chunks, by eighths 8 / 9 / 10 / 11 / 12 / 16: 213 / 202 /
+    // 191 / 195 / 198 / 213 us; 8 bits, 10 / 12 / 13 / 14 / 16: 322 / 297 / 285 / 290 /
+    // 303.  A unit's start counts as three steps (2 / 3 / 4 / 6: whole prompts 345 /
+    // 347 / 350 / 365, mixed 219 / 213 / 212 / 224 at 16 eighths).
+    const int pair_cost = kv8 ? 13 : 10;
+    return ChunkPlan{2 * tb * P.G, 2 * tb, ctc::kN, 3 * ctc::kN, pair_cost, 2 * ctc::kN, num_sms()};
 }
 
 spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStream_t s) {
