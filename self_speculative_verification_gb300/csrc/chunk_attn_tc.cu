@@ -1230,7 +1230,7 @@ ChunkPlan chunk_tc_plan(const ChunkParams &P, bool kv8) {
     // 303.  A unit's start counts as three steps (2 / 3 / 4 / 6: whole prompts 345 /
     // 347 / 350 / 365, mixed 219 / 213 / 212 / 224 at 16 eighths).
     const int pair_cost = kv8 ? 13 : 10;
-    return ChunkPlan{2 * tb * P.G, 2 * tb, ctc::kN, 3 * ctc::kN, pair_cost, 2 * ctc::kN, num_sms()};
+    return ChunkPlan{2 * tb * P.G, 2 * tb, ctc::kN, 3 * ctc::kN, pair_cost, ctc::kN, num_sms()};
 }
 
 spec_status_t launch_chunk_tc(const ChunkParams &C, bool kv8, int n_cta, cudaStream_t s) {
