@@ -20,11 +20,11 @@
 //   (j+1), .. -- so that the tensor core works on one tile while the other's
 //   softmax, or its change of unit, runs.
 // * bf16 cache: K and V tiles come by tensor copies, one a page (contiguous, or D =
-//   64: one a tile or page and 64 elements), into a ring of 128-byte-swizzled slots.  Warp 11 looks through the
-//   value tiles that not every row sees whole (the last ones of a unit): rows
-//   past the unit's last token become zeros, and non-finite values too, whose
-//   first place they note, for a hidden value's weight of zero would not keep
-//   it out of the sum.
+//   64: one a tile or page and 64 elements), into a ring of 128-byte-swizzled
+//   slots.  Warp 11 looks through the value tiles that not every row sees whole
+//   (the last ones of a unit): rows past the unit's last token become zeros, and
+//   non-finite values too, whose first place they note, for a hidden value's
+//   weight of zero would not keep it out of the sum.
 // * 8-bit cache: 16 tokens' codes, keys and values, are one run of memory, which
 //   a bulk copy brings into a stage; warps 12-19 turn them into the slots' bf16
 //   tiles (code * scale, exact for a power of two) and do what warp 11 does
@@ -48,9 +48,9 @@
 //   steps, and the merging launch (11).  What runs once a unit or less is kept in
 //   rolled loops: unrolled it has to be fetched each time, beside the steps' code.
 // * 39 single tokens and 9 chunks up to 512, behind 0.6 - 4 K: 191 us, of 79 for
-//   the bytes and 75 for the products: a unit of two heads takes four slots of the
-//   ring a step, which leaves one to load ahead, and holds G rows of 128 in a tile.
-//   48 single tokens behind 4 K: 133 us, 89 % of a copy's rate, in pages of any size.
+//   the bytes and 75 for the products: a CTA streams for single tokens, G rows of
+//   128 in a tile, or computes for the others, not both.  48 single tokens behind
+//   4 K: 133 us, 89 % of a copy's rate, in pages of any size.
 // * 8 bits: 4.9 ms and 285 us on the first and third: the codes' widening (two
 //   tiles of 16 K elements a step, 8 warps) shares issue slots and shared memory
 //   with the softmax.  MMAs on the codes themselves would need none, but queries
