@@ -215,3 +215,11 @@ def test_many_requests(kind, dtype):
 def test_one_long_row_over_all_ctas(kind, dtype):
     """A single token behind a long history: its keys are shared out."""
     run(Chunk(13, kind, dtype, 128, 4, 1, (1, 2), (40000, 9), ps=64)).check()
+
+
+@pytest.mark.parametrize("kind", ["paged", "kv8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ps", [80, 128, 256])
+def test_long_pages(kind, dtype, ps):
+    """Pages as long as a step or longer, and of a size that does not divide it."""
+    run(Chunk(14, kind, dtype, 128, 6, 3, (70, 1, 9, 200), (300, 511, 0, 57), ps=ps)).check()
