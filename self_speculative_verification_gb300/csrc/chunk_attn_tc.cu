@@ -43,7 +43,7 @@
 //   ms, 1240 - 1320 TFLOP/s.  The MMAs of a 128-key step of both tiles take 2.08 K
 //   cycles of 3.1 K: a tile's chain of softmax, PV and next S is longer than the
 //   other's MMAs, and the clock gives way to the power limit.
-// * Whole prompts, 12.9 K tokens of 32 heads: 345 us (1050 TFLOP/s): a unit's start,
+// * Whole prompts, 12.9 K tokens of 32 heads: 343 us (1057 TFLOP/s): a unit's start,
 //   its last (masked) steps with their value check and its results, against 2 to 32
 //   steps, and the merging launch (11).  What runs once a unit or less is kept in
 //   rolled loops: unrolled it has to be fetched each time, beside the steps' code.
@@ -611,7 +611,9 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                             const uint64_t q_off = (uint64_t)((((ks >> 2) * kHalf) + (ks & 3) * 32) >> 4);
                             const uint64_t k_off = (uint64_t)(((ks >> 2) * half_at + (ks & 3) * 32) >> 4);
                             mma_ss(tS, qd + q_off, kd + k_off, id_s, ks > 0 ? 1u : 0u);
-                            if (ks == 3) unlock();           // (the queue holds that many)
+                            // (a little ahead, as the queue holds some: after 2 / 4 / 6 / 8 of
+                            // 8, whole prompts 358 / 347 / 342 / 347 us)
+                            if (ks == (D == 128 ? 5 : 3)) unlock();
                         }
                         commit(&sh.s_full[x]);
                         release(slot, j);
