@@ -109,7 +109,7 @@ struct Params {
     int tb;                  // tokens of a query tile
     uint32_t g_mul;          // r / G = (r g_mul) >> 16, r < 128
     int box;                 // tokens of a tensor copy (paged: of one page)
-    uint32_t ps_mul;         // t / ps = (t ps_mul) >> 31 + ps_shift, t < 2^30
+    uint32_t ps_mul;         // t / ps = (t ps_mul) >> ps_shift, t < 2^31
     int ps_shift;
 };
 
