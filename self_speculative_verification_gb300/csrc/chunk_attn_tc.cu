@@ -98,8 +98,8 @@ struct Cfg {
     static constexpr int kWarps = K8 ? 20 : 12;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kLaunchRegs = K8 ? 96 : 168;
-    static constexpr int kSoftmaxRegs = K8 ? 128 : 184;
-    static constexpr int kOtherRegs = K8 ? 72 : 128;
+    static constexpr int kSoftmaxRegs = K8 ? 136 : 184;
+    static constexpr int kOtherRegs = K8 ? 64 : 128;
     static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
                   "register split exceeds the launch allocation");
 };
