@@ -975,7 +975,8 @@ spec_status_t spec_chunk_attn_kv8_workspace_size(const spec_chunk_desc *desc,
  * o have desc->dtype.  For bf16 rows an element counts as code * scale rounded
  * to bf16, which is exact for the powers of two that the writers give.  A row
  * that sees a block whose key scale is NaN gets o = lse = NaN, one whose value
- * scale is NaN o = NaN.
+ * scale is NaN o = NaN.  (A batch of single tokens alone goes faster through
+ * spec_verify_attn_kv8 with one row, before its commit.)
  */
 spec_status_t spec_chunk_attn_kv8(const spec_chunk_desc *desc, const void *q,
                                   long long row_stride_q, const spec_kv8_desc *cache,
