@@ -57,6 +57,7 @@
 //   as two e4m3 values and P as three of e5m2, 2.5 products at twice the rate in
 //   the place of one, and the splitting of P in the softmax's chain.
 #include "chunk_attn.cuh"
+#include "chunk_ring.cuh"
 #include "kv8_common.cuh"
 #include "ptx_sm103.cuh"
 
@@ -221,6 +222,16 @@ __device__ __forceinline__ uint32_t times0(uint32_t a, uint32_t c) {
 }
 
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// A word of shared memory that one thread counts up and others look at.
+__device__ __forceinline__ void store_release(uint32_t *p, uint32_t x) {
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(x) : "memory");
+}
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t *p) {
+    uint32_t x;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(x) : "r"(smem_u32(p)) : "memory");
+    return x;
+}
 
 // global -> shared bulk copy; both 16-byte aligned, bytes a multiple of 16
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -483,7 +494,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                                 }
                                 if (lane == 0) {
                                     mbar_arrive_expect_tx(&sh.full[slot], n_in * copy_bytes);
-                                    *(volatile uint32_t *)&sh.issued = (uint32_t)ld + 1u;
+                                    store_release(&sh.issued, (uint32_t)ld + 1u);
                                 }
                                 __syncwarp();
                                 uint8_t *dst = ring + slot * kTile + hh * kHalf + bx * copy_bytes;
@@ -542,6 +553,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 const uint64_t kd0 = smem_desc(smem_u32(ring), 16, group_at);
                 const uint64_t vd0 = smem_desc(smem_u32(ring), half_at, group_at);
                 uint32_t base = 0;                       // fills of the ring before this part
+                uint32_t known = 0;                      // and how many are known to have begun
                 uint32_t np = 0, nact = 0;               // P hand-offs taken; parts with this tile
                 bool ok = true;
                 PartReader reader;
@@ -556,20 +568,23 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     auto fill = [&](int j) -> uint32_t {
                         return base + 2u * (uint32_t)(j * sets + (sets == 2 ? x : 0));
                     };
-                    // Waits until the producer has begun fill f: from then on the parity of
-                    // the slot's phase tells f.  A tile that takes every fill needs that
-                    // only where a part begins (it may have had no part in the ones before);
-                    // one of a unit of two heads passes the other's fills by, whose copies
-                    // may come after later ones of its own.  (Widened codes come in order.)
+                    // A slot's phase tells fill f by its parity alone, once the fill before it
+                    // in the slot has landed: until then the phase two back has the same
+                    // parity, and the old tile would pass for the new one.  The producer
+                    // begins f when that fill has been let go of by all, so what is known to
+                    // have begun may be waited for, on `full` or `fixed` (chunk_ring.cuh).
+                    auto begun_now = [&](uint32_t f) -> bool {
+                        if (known <= f) known = load_acquire(&sh.issued);
+                        return known > f;
+                    };
                     auto begun = [&](uint32_t f) -> bool {
                         const long long since = clock64();
-                        while (*(volatile uint32_t *)&sh.issued <= f) {
+                        while (!begun_now(f)) {
                             if (clock64() - since >= wait) return false;
                             __nanosleep(20);
                         }
                         return true;
                     };
-                    const bool passes = !K8 && sets == 2;
                     // a slot is free once both threads have let go of it: each for
                     // itself, and for the other where that one has no use for it
                     auto release = [&](uint32_t slot, int j) {
@@ -596,11 +611,11 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     };
                     auto issue_s = [&](int j, bool locked) -> bool {
                         const uint32_t f = fill(j), slot = f % kSlots;
-                        if ((passes && *(volatile uint32_t *)&sh.issued <= f) ||
-                            !mbar_test_wait(&sh.full[slot], (f / kSlots) & 1u)) {
+                        const bool ask = chunk_ring_asks(K8, j == 0);
+                        if ((ask && !begun_now(f)) || !mbar_test_wait(&sh.full[slot], (f / kSlots) & 1u)) {
                             if (locked) unlock();
                             locked = false;
-                            if ((passes && !begun(f)) || !mbar_wait(&sh.full[slot], (f / kSlots) & 1u, wait))
+                            if ((ask && !begun(f)) || !mbar_wait(&sh.full[slot], (f / kSlots) & 1u, wait))
                                 return false;
                         }
                         if (!locked && !lock()) return false;
@@ -620,8 +635,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         return true;
                     };
                     if (n > 0) {
-                        if (*abort || !begun(fill(0)) ||
-                            !mbar_wait(&sh.q_full[x], nact & 1u, wait) || !issue_s(0, false)) {
+                        if (*abort || !begun(fill(0)) || !mbar_wait(&sh.q_full[x], nact & 1u, wait) ||
+                            !issue_s(0, false)) {
                             ok = false;
                             break;
                         }
@@ -631,7 +646,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         // overwrites O, after the epilogue of the part before read it
                         const uint32_t f = fill(j) + 1u, slot = f % kSlots;
                         uint64_t *bar = !K8 && (j + 1) * kN > sure ? &sh.fixed[slot] : &sh.full[slot];
-                        if ((passes && !begun(f)) || !mbar_wait(bar, (f / kSlots) & 1u, wait) ||
+                        if ((chunk_ring_asks(K8, false) && !begun(f)) || !mbar_wait(bar, (f / kSlots) & 1u, wait) ||
                             (j == 0 && nact > 0 && !mbar_wait(&sh.o_free[x], (nact - 1) & 1u, wait))) {
                             ok = false;
                             break;
@@ -839,7 +854,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                             ok = false;
                             break;
                         }
-                        if (tid == 0) *(volatile uint32_t *)&sh.issued = ++fills;
+                        if (tid == 0) store_release(&sh.issued, ++fills);
                         uint8_t *dst = ring + slot * kTile;
                         if (fast && !rag) {
 #pragma unroll
