@@ -194,8 +194,13 @@ struct PartReader {
         }
         return sh.parts[i].n > 0;
     }
-    // Lets go of the part (one lane of a reading warp).
-    __device__ __forceinline__ void release(Shared &sh) { mbar_arrive(&sh.part_free[i]); }
+    // Lets go of the part (the whole warp, or one thread alone), which the producer
+    // may then overwrite: a warp's lanes have all read what they need of it first.
+    template <bool kWarp>
+    __device__ __forceinline__ void release(Shared &sh) {
+        if (kWarp) __syncwarp();
+        if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&sh.part_free[i]);
+    }
     __device__ __forceinline__ void advance() {
         if (++i == kParts) {
             i = 0;
@@ -562,7 +567,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                     const int n = t.n_t[x], sets = t.sets, other = sets == 2 ? 0 : t.n_t[1 - x];
                     const uint32_t fills = 2u * (uint32_t)(t.n * sets);
                     const int sure = t.pos[0] + 1 - t.s0 * kN;       // tokens that every row sees, from s0 on
-                    reader.release(sh);
+                    reader.release<false>(sh);
                     reader.advance();
                     // fill of step j's K tile; its V tile is the next one
                     auto fill = [&](int j) -> uint32_t {
@@ -701,9 +706,9 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                 const Part &t = sh.parts[reader.i];
                 int *bad = &sh.bad[reader.i][0];
                 bool fresh = true;
-                const int per = 2 * t.sets;              // fills a step
-                for (int i = 0; i < per * t.n; ++i) {
-                    const int s = t.s0 + i / per;
+                const int per = 2 * t.sets, n = per * t.n, s0 = t.s0;    // fills a step, of the part
+                for (int i = 0; i < n; ++i) {
+                    const int s = s0 + i / per;
                     if (__any_sync(0xffffffffu, *abort != 0) || !mbar_wait_warp(&sh.full[slot], ph, wait)) {
                         ok = false;
                         break;
@@ -770,7 +775,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         ph ^= 1u;
                     }
                 }
-                if (lane == 0) reader.release(sh);
+                reader.release<true>(sh);
                 reader.advance();
             }
             if (!ok && lane == 0) {
@@ -896,7 +901,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         sph ^= 1u;
                     }
                 }
-                if (lane == 0) reader.release(sh);
+                reader.release<true>(sh);
                 reader.advance();
             }
             if (!ok && lane == 0) {
@@ -923,8 +928,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             const int n = t.n_t[x], s0 = t.s0;
             if (n == 0) {                                // (no such tile, or tile A is through: an empty part)
                 if (row_ok) A.part_ml[(size_t)t.slot * A.ru + x * rows + r] = make_float2(-INFINITY, 0.f);
-                __syncwarp();
-                if (lane == 0) reader.release(sh);
+                reader.release<true>(sh);
                 reader.advance();
                 continue;
             }
@@ -1108,10 +1112,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             auto let_go_of_q = [&]() {
                 fence_async();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sh.q_empty[x]);
-                    reader.release(sh);
-                }
+                if (lane == 0) mbar_arrive(&sh.q_empty[x]);
+                reader.release<true>(sh);
             };
             // N columns of O from column c0 on, as 16-byte chunks of bf16 or fp32
             // (kFull: a whole query tile, laid out as its queries were)
@@ -1193,8 +1195,8 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
                         }
                     }
                     mbar_arrive(&sh.q_empty[x]);
-                    reader.release(sh);
                 }
+                reader.release<true>(sh);
                 ok = __all_sync(0xffffffffu, ok);
                 ++n_full;
             } else if (!warp_ok) {
