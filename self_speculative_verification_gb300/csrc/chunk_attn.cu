@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) chunk_merge_kernel(ChunkP
             for (int v = 0; v < U; ++v)
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
-                    ml[q][v] = make_float2(-INFINITY, 0.f);
+                    ml[q][v] = make_float2(-INFINITY, kUnwritten);
                     if (k0 + v >= n || to[q] < 0) continue;
                     const size_t at = (size_t)s_slot[k0 + v] * P.ru + row0 + q;
                     ml[q][v] = P.part_ml[at];
@@ -407,9 +407,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) chunk_merge_kernel(ChunkP
             for (int v = 0; v < U; ++v)
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
-                    // (a part without weight may hold nothing; one of NaN has its
-                    // maximum from the other scores, or none)
-                    if (ml[q][v].y == 0.f) continue;
+                    // (one whose scores are all -inf has no weight and an output of 0, or
+                    // NaN from a value; one of NaN has its maximum from the other scores,
+                    // or none)
+                    if (ml[q][v].y == kUnwritten) continue;
                     const float w = ml[q][v].x == -INFINITY ? 1.f : exp2f(ml[q][v].x - top[q]);
                     l[q] = fmaf(w, ml[q][v].y, l[q]);
 #pragma unroll

@@ -65,6 +65,9 @@ spec_status_t launch_chunk_tc(const ChunkParams &P, bool kv8, int n_cta, cudaStr
 
 namespace {
 
+// The sum of a part whose row has no output in part_o.
+constexpr float kUnwritten = -1.f;
+
 // A request's new tokens: n of them, packed from row `first` on, S held
 // before; n = 0 for one without any, or with lengths out of range.
 struct ChunkReq {

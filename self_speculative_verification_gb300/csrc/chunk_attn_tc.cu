@@ -927,7 +927,7 @@ chunk_tc_kernel(const __grid_constant__ ctc::Params P, const __grid_constant__ C
             const bool row_ok = rt < t.nt[x];
             const int n = t.n_t[x], s0 = t.s0;
             if (n == 0) {                                // (no such tile, or tile A is through: an empty part)
-                if (row_ok) A.part_ml[(size_t)t.slot * A.ru + x * rows + r] = make_float2(-INFINITY, 0.f);
+                if (row_ok) A.part_ml[(size_t)t.slot * A.ru + x * rows + r] = make_float2(-INFINITY, kUnwritten);
                 reader.release<true>(sh);
                 reader.advance();
                 continue;
