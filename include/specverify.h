@@ -879,7 +879,7 @@ spec_status_t spec_rope_freqs(int rot_dim, double base, int scaling, double fact
  *
  * Pair i of a head, (x, y), becomes attention * (x cos t - y sin t, y cos t + x
  * sin t), t = position * freqs[i]; elements from rot_dim on are copied.  The
- * angle is held to 2^-24 of a half turn at any position (a frequency to 2^-53
+ * angle is held to 2^-24 of a half turn at any position (a frequency to 2^-52
  * of itself), products and sums are fp32, rounded once to dtype.  What a call
  * writes must not meet anything else that it reads or writes
  * (SPEC_ERR_INVALID_ARG; rows of unlike strides are told apart by the spans of
