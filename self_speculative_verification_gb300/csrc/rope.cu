@@ -251,17 +251,6 @@ bool rows_meet(const void *pa, long long sa, long long wa, const void *pb, long 
     return at < wa || at + wb > sa;
 }
 
-// Whether n rows of w bytes from r on, s bytes apart, meet the block of len bytes
-// at p: the row that the block's first byte follows, or the one after it, has to
-// reach into it.
-bool block_meets(const void *pr, long long s, long long w, int n, const void *p, long long len) {
-    const uintptr_t r = reinterpret_cast<uintptr_t>(pr), b = reinterpret_cast<uintptr_t>(p), e = b + (uintptr_t)len;
-    if (b >= r + (uintptr_t)((n - 1) * s + w) || r >= e) return false;
-    if (b < r) return true;
-    const uintptr_t row = r + (b - r) / (uintptr_t)s * (uintptr_t)s;
-    return b < row + (uintptr_t)w || e > row + (uintptr_t)s;
-}
-
 }  // namespace
 }  // namespace sv
 
@@ -322,15 +311,9 @@ extern "C" spec_status_t spec_rope(const spec_rope_desc *desc, const double *fre
     struct Rows { const void *p; long long s, w; };
     const Rows in[2] = {{q, row_stride_q * es, wq * es}, {k, row_stride_k * es, wk * es}};
     const Rows out[2] = {{q_out, row_stride_q_out * es, wq * es}, {k_out, row_stride_k_out * es, wk * es}};
-    struct Block { const void *p; long long len; };
-    const Block where[3] = {{positions, 4ll * n},
-                            {positions ? nullptr : seq_len, 4ll * batch},
-                            {positions ? nullptr : cu_new, 4 * (batch + 1ll)}};
     bool keep[2] = {false, false};
     for (int x = 0; x < 2; ++x) {
         if (in[x].w == 0) continue;
-        for (const Block &b : where)
-            if (b.p && block_meets(out[x].p, out[x].s, out[x].w, n, b.p, b.len)) return SPEC_ERR_INVALID_ARG;
         keep[x] = in[x].p == out[x].p && in[x].s == out[x].s;
         for (int y = 0; y < 2; ++y) {
             if (in[y].w == 0) continue;
