@@ -881,9 +881,10 @@ spec_status_t spec_rope_freqs(int rot_dim, double base, int scaling, double fact
  * sin t), t = position * freqs[i]; elements from rot_dim on are copied.  The
  * angle is held to 2^-24 of a half turn at any position (a frequency to 2^-52
  * of itself), products and sums are fp32, rounded once to dtype.  What a call
- * writes must not meet anything else that it reads or writes
- * (SPEC_ERR_INVALID_ARG; rows of unlike strides are told apart by the spans of
- * memory that they reach over).  A cu_new that decreases or leaves [0,
+ * writes must not meet anything else that it reads or writes.  Of queries and
+ * keys this is checked (SPEC_ERR_INVALID_ARG; rows of unlike strides are told
+ * apart by the spans of memory that they reach over); positions, seq_len and
+ * cu_new are the caller's to keep apart.  A cu_new that decreases or leaves [0,
  * n_tokens] sets SPEC_DEV_BAD_INDEX (which rows are turned is then
  * unspecified), a negative seq_len SPEC_DEV_SEQ_OVERFLOW (its rows are left as
  * they are).  One launch.
