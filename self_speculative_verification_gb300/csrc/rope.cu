@@ -299,6 +299,14 @@ extern "C" spec_status_t spec_rope(const spec_rope_desc *desc, const double *fre
     if (row_stride_q < wq || row_stride_q_out < wq || row_stride_k < wk || row_stride_k_out < wk)
         return SPEC_ERR_INVALID_ARG;
     if (n == 0 || Hq + Hk == 0) return SPEC_OK;
+    // (the stride of a single row is not used; of more, all rows' bytes are counted
+    // in 64 bits)
+    for (long long *s : {&row_stride_q, &row_stride_q_out})
+        if (n == 1) *s = wq;
+        else if (Hq && *s > (1ll << 59) / n) return SPEC_ERR_INVALID_ARG;
+    for (long long *s : {&row_stride_k, &row_stride_k_out})
+        if (n == 1) *s = wk;
+        else if (Hk && *s > (1ll << 59) / n) return SPEC_ERR_INVALID_ARG;
     if ((Hq && (!q || !q_out)) || (Hk && (!k || !k_out))) return SPEC_ERR_INVALID_ARG;
     if (!positions && (!seq_len || !cu_new || batch == 0)) return SPEC_ERR_INVALID_ARG;
     const int es = desc->dtype == SPEC_BF16 ? 2 : 4, per = 16 / es;
