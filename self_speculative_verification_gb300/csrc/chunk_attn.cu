@@ -161,7 +161,6 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm) chunk_simt_kernel(Ch
                     *reinterpret_cast<float4 *>(&sh.v[t][c]) = v[e];
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
             odd = __syncthreads_or(odd);
             if (tid / 32 * 8 >= nr) continue;            // (a warp's eight rows: none)
             float x[4][4] = {};

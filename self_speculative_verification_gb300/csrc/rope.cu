@@ -15,6 +15,7 @@
 
 #include "common.cuh"
 #include "kv8.cuh"
+#include "ptx_sm103.cuh"
 
 namespace sv {
 namespace {
@@ -73,11 +74,6 @@ __device__ __forceinline__ bool rope_position(const RopeParams &P, int i, int b0
     return true;
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 template <typename T>
 __device__ __forceinline__ void unpack_vec(const uint4 &v, float (&x)[kVec<T>]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -97,7 +93,7 @@ __device__ __forceinline__ void store_vec(T *p, const float (&x)[kVec<T>]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 2) w[i] = pack2(x[2 * i], x[2 * i + 1]);
+        if constexpr (sizeof(T) == 2) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
         else w[i] = __float_as_uint(x[i]);
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -133,7 +129,7 @@ __device__ __forceinline__ void rope_item(const RopeParams &P, const T *src, T *
             else x = make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
             rotate(x.x, x.y, cs[e / 2 * parts + it]);
             if constexpr (sizeof(T) == 2) {
-                w[e / 2] = pack2(x.x, x.y);
+                w[e / 2] = pack_bf16(x.x, x.y);
             } else {
                 w[e] = __float_as_uint(x.x);
                 w[e + 1] = __float_as_uint(x.y);
