@@ -38,12 +38,14 @@
 //   issuing work, waits (bounded) for its own copies and MMAs, frees its TMEM
 //   and returns.
 //
-// What it measures, and what bounds it (heads of 128, the merging launch included):
-// * Three chunks of 1.5 - 2 K tokens behind 45 - 66 K, 32 heads over 8: 3.7 - 3.95
-//   ms, 1240 - 1320 TFLOP/s.  The MMAs of a 128-key step of both tiles take 2.08 K
+// What it measures, and what bounds it (heads of 128, the merging launch included;
+// a graph's passes over one input -- of calls one by one, on inputs that change, the
+// first three take 4.0 ms, 372 and 203 us, 1230, 976 and 700 TFLOP/s):
+// * Three chunks of 1.5 - 2 K tokens behind 45 - 66 K, 32 heads over 8: 3.8 - 3.9
+//   ms, 1250 - 1290 TFLOP/s.  The MMAs of a 128-key step of both tiles take 2.08 K
 //   cycles of 3.1 K: a tile's chain of softmax, PV and next S is longer than the
 //   other's MMAs, and the clock gives way to the power limit.
-// * Whole prompts, 12.9 K tokens of 32 heads: 343 us (1057 TFLOP/s): a unit's start,
+// * Whole prompts, 12.9 K tokens of 32 heads: 346 us (1050 TFLOP/s): a unit's start,
 //   its last (masked) steps with their value check and its results, against 2 to 32
 //   steps, and the merging launch (11).  What runs once a unit or less is kept in
 //   rolled loops: unrolled it has to be fetched each time, beside the steps' code.
@@ -51,7 +53,7 @@
 //   the bytes and 75 for the products: a CTA streams for single tokens, G rows of
 //   128 in a tile, or computes for the others, not both.  48 single tokens behind
 //   4 K: 133 us, 89 % of a copy's rate, in pages of any size.
-// * 8 bits: 4.9 ms and 285 us on the first and third: the codes' widening (two
+// * 8 bits: 4.9 ms and 290 us on the first and third: the codes' widening (two
 //   tiles of 16 K elements a step, 8 warps) shares issue slots and shared memory
 //   with the softmax.  MMAs on the codes themselves would need none, but queries
 //   as two e4m3 values and P as three of e5m2, 2.5 products at twice the rate in
@@ -303,7 +305,7 @@ __device__ __forceinline__ uint32_t nan4(uint32_t w) { return (w & 0x7f7f7f7fu) 
 // kJoint (pages of the bf16 cache, D = 128): the K and V tiles' 64-element halves
 // lie side by side, eight tokens of the one, then of the other, so that a page
 // comes in one copy; a copy costs the producer its issue, whatever its size (48
-// single tokens behind 4 K in pages of 16: 152 -> 136 us).  half_at, group_at: bytes
+// single tokens behind 4 K in pages of 16: 152 -> 133 us).  half_at, group_at: bytes
 // between the halves, and between groups of eight tokens.
 template <int D, bool K8, bool kJoint>
 __global__ void __launch_bounds__(ctc::Cfg<D, K8>::kThreads, 1)
